@@ -1,0 +1,459 @@
+// attention_rows.cu -- attention of few query rows over a long cache (sm_103a).
+//
+// The query rows of one key/value head (query tokens times its group of query
+// heads) are cut into tiles of 16 or 32 rows; a tile's slots are cut into
+// splits, one CTA each, so that a single token still uses the whole GPU.  Each
+// of a CTA's four warps walks its own slot tiles with its own running maximum
+// m, sum l and output o:
+//     s = q k^T, m' = max(m, s), p = exp(s - m'), l = l exp(m - m') + sum p,
+//     o = o exp(m - m') + p v,
+// and the partial (m, l, o) are joined by the same rule: over the warps in
+// shared memory, over the splits by the CTA that finishes last, always in the
+// same order.  Every key and value is read once: HBM bounds it.  A warp keeps
+// a private ring of slot tiles filled by cp.async, so nothing in the loop
+// waits for another warp.
+#include <algorithm>
+#include <cstdint>
+
+#include "attention.cuh"
+
+namespace splitzip {
+namespace {
+
+constexpr int kWarpsRows = 4;
+constexpr int kStagesRows = 3;
+constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
+
+struct RowsParams {
+    splitzip_attention_args a;
+    uint32_t group, rows, row_tiles, splits;
+    uint32_t* counters;
+    float* partials;
+};
+
+template <int D, bool kF8, int MT>
+struct RowsShape {
+    static constexpr int kElem = kF8 ? 1 : 2;
+    static constexpr int kRow = D * kElem;             // bytes of a key
+    static constexpr int kSlots = kTileBytes / kRow;   // slots per warp tile
+    static constexpr int kTileRows = 16 * MT;
+    static constexpr int kRing = kWarpsRows * kStagesRows * 2 * kTileBytes;
+    static constexpr int kQ = kTileRows * D * 2;
+    static constexpr int kSmem = kRing + kQ;
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile of rows of kRow bytes; the
+// chunks of eight consecutive rows at one c fall into eight different banks
+// groups, as ldmatrix reads them.
+template <int kRow>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+    if (kRow >= 128) return r * kRow + ((c ^ (r & 7u)) << 4);
+    return r * kRow + ((c ^ ((r >> 1) & 3u)) << 4);  // two rows to 128 bytes
+}
+
+template <int D, bool kF8, int MT>
+__global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_constant__ RowsParams p) {
+    using S = RowsShape<D, kF8, MT>;
+    constexpr int NT = S::kSlots / 8;    // n-tiles of the scores
+    constexpr int KS = D / 16;           // k-steps of the scores
+    constexpr int PS = S::kSlots / 16;   // k-steps of the output
+    constexpr int OT = D / 8;            // n-tiles of the output
+    constexpr int kChunks = S::kRow / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_scale[S::kTileRows];
+    __shared__ float s_m[kWarpsRows][S::kTileRows], s_l[kWarpsRows][S::kTileRows];
+    __shared__ uint32_t s_last;
+    const splitzip_attention_args& a = p.a;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t unit = blockIdx.x / p.splits;
+    const uint32_t split = blockIdx.x - unit * p.splits;
+    const uint32_t bh = unit / p.row_tiles, rt = unit - bh * p.row_tiles;
+    const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+    const Mask mask(a, b);
+    const uint32_t r0 = rt * S::kTileRows, r1 = min(r0 + S::kTileRows, p.rows);
+    const int32_t p0 = mask.first + (int32_t)(r0 / p.group), p1 = mask.first + (int32_t)((r1 - 1) / p.group);
+    const SlotTiles tiles(mask, p0, p1, S::kSlots);
+    const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
+    const uint32_t j1 = (uint32_t)((uint64_t)tiles.count * (split + 1) / p.splits);
+
+    uint8_t* ring = smem + warp * (kStagesRows * 2 * kTileBytes);
+    uint8_t* qs = smem + S::kRing;
+    const uint8_t* kbase = static_cast<const uint8_t*>(a.k.data) + (b * a.k.stride_b + h * a.k.stride_h) * S::kElem;
+    const uint8_t* vbase = static_cast<const uint8_t*>(a.v.data) + (b * a.v.stride_b + h * a.v.stride_h) * S::kElem;
+    // Slots past the last one in use are loaded as copies of it and masked.
+    auto load = [&](uint32_t j, uint32_t stage) {
+        if (j < j1) {
+            const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
+            uint8_t* dk = ring + stage * (2 * kTileBytes);
+#pragma unroll
+            for (int i = 0; i < kTileBytes / 512; i++) {
+                const uint32_t at = i * 32 + lane, r = at / kChunks, c = at % kChunks;
+                const int64_t slot = min(s0 + (int32_t)r, mask.n - 1);
+                cp_async16(dk + chunk_at<S::kRow>(r, c), kbase + slot * a.k.stride_t * S::kElem + 16 * c);
+                cp_async16(dk + kTileBytes + chunk_at<S::kRow>(r, c), vbase + slot * a.v.stride_t * S::kElem + 16 * c);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStagesRows - 1; i++) load(j0 + warp + i * kWarpsRows, i);
+
+    // Queries: one warp per row, as FP16 of the scaled row for E5M2.
+    for (uint32_t r = warp; r < S::kTileRows; r += kWarpsRows) {
+        const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
+        constexpr int V = D / 32;  // values per lane: 2 or 4
+        uint32_t v[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) v[i] = 0;
+        if (row < r1) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                static_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.stride_b + (int64_t)t * a.q.stride_t +
+                (h * p.group + g) * a.q.stride_h);
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) v[i] = src[lane * (V / 2) + i];
+        }
+        float power = 1.0f;
+        if (kF8) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < V / 2; i++) top = max(top, max(v[i] & 0x7FFFu, v[i] >> 16 & 0x7FFFu));
+            power = row_power(__reduce_max_sync(0xFFFFFFFFu, top));
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) {
+            uint32_t d = lane * V + 2 * i, w = v[i];
+            if (kF8) {
+                w = pack2<true>(__uint_as_float(v[i] << 16) * power, __uint_as_float(v[i] & 0xFFFF0000u) * power);
+                d = (d & ~15u) + e5m2_place(d & 15u);
+            }
+            *reinterpret_cast<uint32_t*>(qs + chunk_at<2 * D>(r, d / 8) + 2 * (d % 8)) = w;
+        }
+        if (lane == 0) s_scale[r] = a.scale * kLog2e / power;
+    }
+    __syncthreads();
+
+    // This thread's rows: 16 i + lane / 4 and that + 8.
+    int32_t pos[MT][2];
+    float scale[MT][2], m[MT][2], l[MT][2], o[MT][OT][4];
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            const uint32_t r = 16 * i + 8 * x + lane / 4;
+            pos[i][x] = r0 + r < r1 ? mask.pos((r0 + r) / p.group) : -1;
+            scale[i][x] = s_scale[r];
+            m[i][x] = -INFINITY;
+            l[i][x] = 0.0f;
+        }
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int j = 0; j < OT; j++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) o[i][j][x] = 0.0f;
+
+    const uint32_t qaddr = smem_addr(qs);
+    bool odd = false;  // a value of a partly visible tile was infinite or NaN
+    uint32_t stage = 0;
+    for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
+        cp_async_wait<kStagesRows - 2>();
+        __syncwarp();
+        load(j + (kStagesRows - 1) * kWarpsRows, stage == 0 ? kStagesRows - 1 : stage - 1);
+        const uint32_t ks = smem_addr(ring + stage * (2 * kTileBytes)), vs = ks + kTileBytes;
+        stage = stage == kStagesRows - 1 ? 0 : stage + 1;
+        const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
+        const bool whole = p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kSlots - 1);
+
+        float sc[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) sc[i][n][x] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            uint32_t q[MT][4];
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+                ldmatrix4(q[i], qaddr + chunk_at<2 * D>(16 * i + (lane & 15), 2 * k + (lane >> 4)));
+            if (kF8) {
+#pragma unroll
+                for (int n = 0; n < NT; n += 4) {
+                    uint32_t r[4];
+                    ldmatrix4(r, ks + chunk_at<S::kRow>(8 * n + lane, k));
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int i = 0; i < MT; i++) mma16816<true>(sc[i][n + x], q[i], e5m2_01(r[x]), e5m2_23(r[x]));
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t r[4];
+                    ldmatrix4(r, ks + chunk_at<S::kRow>(8 * n + 8 * (lane >> 4) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int i = 0; i < MT; i++) {
+                        mma16816<false>(sc[i][n], q[i], r[0], r[1]);
+                        mma16816<false>(sc[i][n + 1], q[i], r[2], r[3]);
+                    }
+                }
+            }
+        }
+        uint32_t pr[MT][PS][4];
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            float top[2] = {m[i][0], m[i][1]};
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    float v = sc[i][n][x] * scale[i][x >> 1];
+                    if (!whole && !mask.sees(pos[i][x >> 1], s0 + 8 * n + 2 * (int32_t)(lane & 3) + (x & 1))) v = -INFINITY;
+                    sc[i][n][x] = v;
+                    top[x >> 1] = fmaxf(top[x >> 1], v);
+                }
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
+            }
+            const bool same = top[0] == m[i][0] && top[1] == m[i][1];
+            const float use[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
+            if (!__all_sync(0xFFFFFFFFu, same)) {
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    const float f = exp2_approx(m[i][x] - use[x]);
+                    l[i][x] *= f;
+#pragma unroll
+                    for (int n = 0; n < OT; n++) {
+                        o[i][n][2 * x] *= f;
+                        o[i][n][2 * x + 1] *= f;
+                    }
+                    m[i][x] = top[x];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                float e[4];
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    e[x] = exp2_approx(sc[i][n][x] - use[x >> 1]);
+                    l[i][x >> 1] += e[x];
+                }
+                // p in 16 bits for the product: a relative error of up to 2^-8 (BF16) or
+                // 2^-11 (FP16) of each term, independent from term to term.
+                pr[i][n >> 1][2 * (n & 1)] = pack2<kF8>(e[0], e[1]);
+                pr[i][n >> 1][2 * (n & 1) + 1] = pack2<kF8>(e[2], e[3]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < PS; k++) {
+#pragma unroll
+            for (int n = 0; n < OT; n += kF8 ? 4 : 2) {
+                uint32_t r[4];
+                ldmatrix4_trans(r, vs + chunk_at<S::kRow>(16 * k + 8 * ((lane >> 3) & 1) + (lane & 7),
+                                                          n / 2 * S::kElem + (lane >> 4)));
+                uint32_t v[kF8 ? 8 : 4];
+                if (kF8) {
+#pragma unroll
+                    for (int x = 0; x < 4; x += 2) {
+                        v[2 * x] = e5m2_02(r[x]);
+                        v[2 * x + 1] = e5m2_02(r[x + 1]);
+                        v[2 * x + 2] = e5m2_13(r[x]);
+                        v[2 * x + 3] = e5m2_13(r[x + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; x++) v[x] = r[x];
+                }
+                if (!whole) {  // 0 x infinity is not 0: keep such values out of the product
+#pragma unroll
+                    for (int x = 0; x < (kF8 ? 8 : 4); x++) {
+                        const uint32_t f = finite_or_zero<kF8>(v[x]);
+                        odd |= f != v[x];
+                        v[x] = f;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < (kF8 ? 4 : 2); x++)
+#pragma unroll
+                    for (int i = 0; i < MT; i++) mma16816<kF8>(o[i][n + x], pr[i][k], v[2 * x], v[2 * x + 1]);
+            }
+        }
+    }
+    cp_async_wait<0>();
+    // Column of o[..][n][x] in the head.
+    auto column = [&](int n, int x) {
+        return kF8 ? 16 * (n / 2) + 4 * (int)(lane & 3) + 2 * (x & 1) + (n & 1) : 8 * n + 2 * (int)(lane & 3) + (x & 1);
+    };
+    if (__any_sync(0xFFFFFFFFu, odd)) {
+        // The infinite and NaN values of partly visible tiles go to the rows that
+        // see them: whatever their (positive) weight, the sum takes their value.
+        for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
+            const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
+            if (p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kSlots - 1)) continue;
+            for (int32_t s = s0; s < min(s0 + S::kSlots, mask.n); s++)
+#pragma unroll
+                for (int n = 0; n < OT; n++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const uint8_t* at = vbase + s * a.v.stride_t * S::kElem + column(n, x) * S::kElem;
+                        const float v = kF8 ? __half2float(__ushort_as_half((unsigned short)(*at << 8)))
+                                            : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
+                        if (isfinite(v)) continue;
+#pragma unroll
+                        for (int i = 0; i < MT; i++)
+#pragma unroll
+                            for (int y = 0; y < 2; y++)
+                                if (mask.sees(pos[i][y], s)) o[i][n][2 * y + x] += v;
+                    }
+        }
+    }
+
+    // Join the warps: everything into shared memory (over the ring), then each
+    // thread a share of the columns.
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            l[i][x] += __shfl_xor_sync(0xFFFFFFFFu, l[i][x], 1);
+            l[i][x] += __shfl_xor_sync(0xFFFFFFFFu, l[i][x], 2);
+            if ((lane & 3) == 0) {
+                s_m[warp][16 * i + 8 * x + lane / 4] = m[i][x];
+                s_l[warp][16 * i + 8 * x + lane / 4] = l[i][x];
+            }
+        }
+    __syncthreads();  // every warp is done with its ring
+    float* os = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < MT; i++)
+#pragma unroll
+        for (int n = 0; n < OT; n++)
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                os[(warp * S::kTileRows + 16 * i + 8 * (x >> 1) + lane / 4) * D + column(n, x)] = o[i][n][x];
+    __syncthreads();
+
+    auto store_row = [&](uint32_t r, uint32_t c, float v, float mm, float ll) {
+        const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
+        const uint32_t hq = h * p.group + g;
+        const bool sees = mask.first + (int32_t)t >= 0;  // its own position, then
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)t * a.out.stride_t +
+                             hq * a.out.stride_h;
+        out[c] = __float2bfloat16(sees ? v / ll : 0.0f);
+        if (c == 0 && a.lse)
+            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    };
+    const uint32_t nrows = r1 - r0;
+    float* part = p.partials + (uint64_t)blockIdx.x * (S::kTileRows * (D + 2));
+    for (uint32_t at = tid; at < nrows * D; at += 32 * kWarpsRows) {
+        const uint32_t r = at / D, c = at % D;
+        float mm = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarpsRows; w++) mm = fmaxf(mm, s_m[w][r]);
+        const float use = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarpsRows; w++) {
+            const float f = exp2_approx(s_m[w][r] - use);
+            ll = fmaf(f, s_l[w][r], ll);
+            v = fmaf(f, os[(w * S::kTileRows + r) * D + c], v);
+        }
+        if (p.splits == 1) {
+            store_row(r, c, v, mm, ll);
+        } else {
+            __stcg(part + r * D + c, v);
+            if (c == 0) {
+                __stcg(part + S::kTileRows * D + r, mm);
+                __stcg(part + S::kTileRows * (D + 1) + r, ll);
+            }
+        }
+    }
+    if (p.splits == 1) return;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        s_last = atomicAdd(p.counters + unit, 1u) == p.splits - 1;
+        if (s_last) p.counters[unit] = 0;  // ready for the next call
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const float* all = p.partials + (uint64_t)unit * p.splits * (S::kTileRows * (D + 2));
+    constexpr uint32_t kStep = S::kTileRows * (D + 2);
+    for (uint32_t at = tid; at < nrows * D; at += 32 * kWarpsRows) {
+        const uint32_t r = at / D, c = at % D;
+        float mm = -INFINITY;
+        for (uint32_t i = 0; i < p.splits; i++) mm = fmaxf(mm, __ldcg(all + i * kStep + S::kTileRows * D + r));
+        const float use = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f, v = 0.0f;
+        for (uint32_t i = 0; i < p.splits; i++) {
+            const float* q = all + i * kStep;
+            const float f = exp2_approx(__ldcg(q + S::kTileRows * D + r) - use);
+            ll = fmaf(f, __ldcg(q + S::kTileRows * (D + 1) + r), ll);
+            v = fmaf(f, __ldcg(q + r * D + c), v);
+        }
+        store_row(r, c, v, mm, ll);
+    }
+}
+
+template <int D, bool kF8, int MT>
+cudaError_t launch(const RowsParams& p, uint32_t ctas, cudaStream_t s) {
+    using S = RowsShape<D, kF8, MT>;
+    Wave w;
+    const cudaError_t e = launch_wave<rows_kernel<D, kF8, MT>>(32 * kWarpsRows, S::kSmem, w);
+    if (e != cudaSuccess) return e;
+    rows_kernel<D, kF8, MT><<<ctas, 32 * kWarpsRows, S::kSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, bool kF8>
+cudaError_t launch_tile(const RowsParams& p, uint32_t tile_rows, uint32_t ctas, cudaStream_t s) {
+    return tile_rows == 16 ? launch<D, kF8, 1>(p, ctas, s) : launch<D, kF8, 2>(p, ctas, s);
+}
+
+}  // namespace
+
+bool attention_plan(const splitzip_attention_args& a, AttentionPlan& p) {
+    const uint32_t group = a.q_heads / a.kv_heads;
+    p.rows = a.q_tokens * group;
+    p.tile_rows = p.rows <= 16 ? 16 : 32;
+    p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+    const uint64_t units = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
+    const uint32_t slots = kTileBytes / (a.head_dim * (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 1 : 2));
+    // The slots a row tile can see at most.
+    uint64_t most = a.kv_tokens;
+    if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
+    // Two CTAs on every SM if each split still has two tiles for each warp.
+    uint64_t splits = 2 * kSms / units;
+    splits = std::min(splits, most / (2 * kWarpsRows * slots));
+    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
+    if (units * p.splits > 0x7FFFFFFFull) return false;
+    // The counters have a place of their own whatever the sizes: they are zero
+    // between calls, while the partials hold what the last call left there.
+    static_assert(4 * kSms <= 1024, "two or more splits: at most kSms row tiles");
+    p.counters_off = 0;
+    p.partials_off = 1024;
+    p.bytes = 1024 + (p.splits > 1 ? units * p.splits * p.tile_rows * (a.head_dim + 2) * 4 : 0);
+    return true;
+}
+
+cudaError_t launch_attention(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
+                             cudaStream_t s) {
+    RowsParams p;
+    p.a = a;
+    p.group = a.q_heads / a.kv_heads;
+    p.rows = plan.rows;
+    p.row_tiles = plan.row_tiles;
+    p.splits = plan.splits;
+    p.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + plan.counters_off);
+    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.partials_off);
+    const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
+    const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
+    if (a.head_dim == 64)
+        return f8 ? launch_tile<64, true>(p, plan.tile_rows, ctas, s) : launch_tile<64, false>(p, plan.tile_rows, ctas, s);
+    return f8 ? launch_tile<128, true>(p, plan.tile_rows, ctas, s) : launch_tile<128, false>(p, plan.tile_rows, ctas, s);
+}
+
+}  // namespace splitzip

@@ -1,0 +1,30 @@
+// serving.h -- launch arguments and launchers of the operators around the KV
+// cache (internal; the public interface is include/splitzip_serving.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/splitzip_serving.h"
+
+namespace splitzip {
+
+cudaError_t launch_norm_rope(const splitzip_norm_rope_args& a, cudaStream_t s);
+
+// How a call's query rows (query token, query head of one key/value head) are
+// cut into row tiles and each tile's slots into splits.
+struct AttentionPlan {
+    uint32_t rows;       // q_tokens * group, of one key/value head
+    uint32_t row_tiles;  // of tile_rows rows
+    uint32_t tile_rows;
+    uint32_t splits;     // parts of one row tile's slots, joined at the end
+    size_t counters_off, partials_off, bytes;  // workspace
+};
+bool attention_plan(const splitzip_attention_args& a, AttentionPlan& p);
+cudaError_t launch_attention(const splitzip_attention_args& a, const AttentionPlan& p,
+                             void* workspace, cudaStream_t s);
+cudaError_t launch_attention_weights(const splitzip_attention_args& a, const float* weights_in,
+                                     float* weights_out, cudaStream_t s);
+cudaError_t launch_evict(const splitzip_evict_args& a, cudaStream_t s);
+
+}  // namespace splitzip

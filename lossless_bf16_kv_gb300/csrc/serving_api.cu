@@ -1,0 +1,107 @@
+// serving_api.cu -- the extern "C" entry points of include/splitzip_serving.h:
+// host-side argument checks and status mapping.
+#include <cmath>
+#include <cstdint>
+
+#include "serving.h"
+#include "trace.h"
+
+using namespace splitzip;
+
+namespace {
+
+inline splitzip_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SPLITZIP_OK : SPLITZIP_ERR_CUDA; }
+
+inline uint32_t elem_bytes(uint32_t format) { return format == SPLITZIP_FORMAT_E5M2 ? 1 : 2; }
+inline bool format_ok(uint32_t format) { return format == SPLITZIP_FORMAT_BF16 || format == SPLITZIP_FORMAT_E5M2; }
+inline bool dim_ok(uint32_t d) { return d == 64 || d == 128; }
+inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bool view_ok(const splitzip_view& v, uint32_t elem, bool batch = true) {
+    const int64_t unit = 16 / elem;
+    const auto ok = [unit](int64_t s) { return s >= 0 && s % unit == 0; };
+    return v.data && aligned(v.data, 16) && (!batch || ok(v.stride_b)) && ok(v.stride_t) && ok(v.stride_h);
+}
+
+constexpr uint64_t kMax31 = 0x7FFFFFFFull;
+
+bool sizes_ok(const splitzip_attention_args& a) {
+    if (!dim_ok(a.head_dim) || !format_ok(a.cache_format)) return false;
+    if (!a.batch || !a.q_tokens || !a.kv_tokens || !a.kv_heads || !a.q_heads) return false;
+    if (a.q_heads % a.kv_heads || a.q_heads / a.kv_heads > SPLITZIP_MAX_GROUP) return false;
+    return (uint64_t)a.q_tokens * (a.q_heads / a.kv_heads) <= kMax31 && a.kv_tokens <= kMax31 &&
+           (uint64_t)a.batch * a.kv_heads <= kMax31;
+}
+
+}  // namespace
+
+extern "C" {
+
+splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args* a, splitzip_stream_t s) {
+    TraceRange trace("splitzip_qk_norm_rope");
+    if (!a || !dim_ok(a->head_dim) || !format_ok(a->cache_format) || !a->q_heads || !a->kv_heads)
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (a->rot_dim % 8 || a->rot_dim > a->head_dim || !(a->eps >= 0.0f)) return SPLITZIP_ERR_INVALID_ARG;
+    if ((uint64_t)a->q_heads + 2ull * a->kv_heads > kMax31 ||
+        (uint64_t)a->n * ((uint64_t)a->q_heads + 2ull * a->kv_heads) > kMax31)
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->n) return SPLITZIP_OK;
+    if (a->rot_dim && (!a->positions || !a->table)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->slots || !aligned(a->slots, 8) || !aligned(a->positions, 4) || !aligned(a->table, 16) ||
+        !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))
+        return SPLITZIP_ERR_INVALID_ARG;
+    const uint32_t e = elem_bytes(a->cache_format);
+    if (!view_ok(a->q, 2, false) || !view_ok(a->k, 2, false) || !view_ok(a->v, 2, false) ||
+        !view_ok(a->q_out, 2, false) || !view_ok(a->k_cache, e, false) || !view_ok(a->v_cache, e, false))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_norm_rope(*a, (cudaStream_t)s));
+}
+
+size_t splitzip_attention_workspace_bytes(const splitzip_attention_args* a) {
+    AttentionPlan p;
+    return a && sizes_ok(*a) && attention_plan(*a, p) ? p.bytes : 0;
+}
+
+splitzip_status splitzip_attention(const splitzip_attention_args* a, void* workspace, size_t workspace_bytes,
+                                   splitzip_stream_t s) {
+    TraceRange trace("splitzip_attention");
+    AttentionPlan p;
+    if (!a || !sizes_ok(*a) || !attention_plan(*a, p)) return SPLITZIP_ERR_INVALID_ARG;
+    const uint32_t e = elem_bytes(a->cache_format);
+    if (!view_ok(a->q, 2) || !view_ok(a->k, e) || !view_ok(a->v, e) || !view_ok(a->out, 2))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_attention(*a, p, workspace, (cudaStream_t)s));
+}
+
+splitzip_status splitzip_attention_weights(const splitzip_attention_args* a, const float* weights_in,
+                                           float* weights_out, splitzip_stream_t s) {
+    TraceRange trace("splitzip_attention_weights");
+    if (!a || !sizes_ok(*a) || !weights_out || !a->lse) return SPLITZIP_ERR_INVALID_ARG;
+    if ((uint64_t)a->batch * a->kv_heads * ((a->kv_tokens + 127ull) / 128) > kMax31) return SPLITZIP_ERR_INVALID_ARG;
+    if (!view_ok(a->q, 2) || !view_ok(a->k, elem_bytes(a->cache_format))) return SPLITZIP_ERR_INVALID_ARG;
+    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4) ||
+        !std::isfinite(a->scale))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_attention_weights(*a, weights_in, weights_out, (cudaStream_t)s));
+}
+
+splitzip_status splitzip_evict(const splitzip_evict_args* a, splitzip_stream_t s) {
+    TraceRange trace("splitzip_evict");
+    if (!a || !dim_ok(a->head_dim) || !format_ok(a->cache_format)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->batch || a->batch > 65535 || !a->kv_tokens || !a->kv_heads || !a->budget) return SPLITZIP_ERR_INVALID_ARG;
+    if (a->kv_tokens > kMax31 || a->budget > kMax31 || (uint64_t)a->batch * a->kv_heads > kMax31 ||
+        (uint64_t)a->budget * a->kv_heads > kMax31 * 16)
+        return SPLITZIP_ERR_INVALID_ARG;
+    if ((uint64_t)a->keep_first + a->keep_last > a->budget) return SPLITZIP_ERR_INVALID_ARG;
+    const uint32_t e = elem_bytes(a->cache_format);
+    if (!view_ok(a->k, e) || !view_ok(a->v, e) || !view_ok(a->k_out, e) || !view_ok(a->v_out, e))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->weights || !a->index || !aligned(a->weights, 4) || !aligned(a->index, 4) || !aligned(a->weights_out, 4) ||
+        !aligned(a->lens, 4) || !aligned(a->lens_out, 4))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_evict(*a, (cudaStream_t)s));
+}
+
+}  // extern "C"
