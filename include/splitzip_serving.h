@@ -131,6 +131,12 @@ size_t splitzip_attention_workspace_bytes(const splitzip_attention_args *args);
 splitzip_status splitzip_attention(const splitzip_attention_args *args, void *workspace,
                                    size_t workspace_bytes, splitzip_stream_t s);
 
+/* Synchronise s and report on the calls of splitzip_attention that ran on this
+ * workspace since the last report: SPLITZIP_OK, or SPLITZIP_ERR_TIMEOUT if a
+ * bounded wait inside a kernel gave up (its rows of out and lse are NaN).  The
+ * workspace stays usable. */
+splitzip_status splitzip_attention_status(void *workspace, splitzip_stream_t s);
+
 /* weights_out[b][h][t] = weights_in[b][h][t] + the sum over the queries i and
  * the query heads of key/value head h that see slot t of
  * exp(scale q.k - lse): the softmax weight the slot got from them.  A sum's

@@ -415,7 +415,7 @@ cudaError_t launch_tile(const RowsParams& p, uint32_t tile_rows, uint32_t ctas, 
 
 }  // namespace
 
-bool attention_plan(const splitzip_attention_args& a, AttentionPlan& p) {
+bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     const uint32_t group = a.q_heads / a.kv_heads;
     p.rows = a.q_tokens * group;
     p.tile_rows = p.rows <= 16 ? 16 : 32;
@@ -430,16 +430,12 @@ bool attention_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     splits = std::min(splits, most / (2 * kWarpsRows * slots));
     p.splits = (uint32_t)(splits < 1 ? 1 : splits);
     if (units * p.splits > 0x7FFFFFFFull) return false;
-    // The counters have a place of their own whatever the sizes: they are zero
-    // between calls, while the partials hold what the last call left there.
-    static_assert(4 * kSms <= 1024, "two or more splits: at most kSms row tiles");
-    p.counters_off = 0;
-    p.partials_off = 1024;
-    p.bytes = 1024 + (p.splits > 1 ? units * p.splits * p.tile_rows * (a.head_dim + 2) * 4 : 0);
+    static_assert(4 * kSms <= kAttentionStatus, "two or more splits: at most kSms row tiles");
+    p.bytes = kAttentionHeader + (p.splits > 1 ? units * p.splits * p.tile_rows * (a.head_dim + 2) * 4 : 0);
     return true;
 }
 
-cudaError_t launch_attention(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
+cudaError_t launch_attention_rows(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
                              cudaStream_t s) {
     RowsParams p;
     p.a = a;
@@ -447,8 +443,8 @@ cudaError_t launch_attention(const splitzip_attention_args& a, const AttentionPl
     p.rows = plan.rows;
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
-    p.counters = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + plan.counters_off);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.partials_off);
+    p.counters = reinterpret_cast<uint32_t*>(workspace);
+    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
     const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
     if (a.head_dim == 64)

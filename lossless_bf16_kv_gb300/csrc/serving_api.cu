@@ -33,6 +33,15 @@ bool sizes_ok(const splitzip_attention_args& a) {
            (uint64_t)a.batch * a.kv_heads <= kMax31;
 }
 
+// Tiles of 256 query rows on the tensor cores from 33 rows on (more than the
+// other kernel's largest tile), where the views allow it.
+bool plans(const splitzip_attention_args& a, AttentionPlan& rows, AttentionPlan& tiles) {
+    return attention_rows_plan(a, rows) && attention_tiles_plan(a, tiles);
+}
+size_t bytes_of(const AttentionPlan& rows, const AttentionPlan& tiles) {
+    return rows.bytes > tiles.bytes ? rows.bytes : tiles.bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -58,21 +67,36 @@ splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args* a, splitzip
 }
 
 size_t splitzip_attention_workspace_bytes(const splitzip_attention_args* a) {
-    AttentionPlan p;
-    return a && sizes_ok(*a) && attention_plan(*a, p) ? p.bytes : 0;
+    AttentionPlan rows, tiles;
+    return a && sizes_ok(*a) && plans(*a, rows, tiles) ? bytes_of(rows, tiles) : 0;
 }
 
 splitzip_status splitzip_attention(const splitzip_attention_args* a, void* workspace, size_t workspace_bytes,
                                    splitzip_stream_t s) {
     TraceRange trace("splitzip_attention");
-    AttentionPlan p;
-    if (!a || !sizes_ok(*a) || !attention_plan(*a, p)) return SPLITZIP_ERR_INVALID_ARG;
+    AttentionPlan rows, tiles;
+    if (!a || !sizes_ok(*a) || !plans(*a, rows, tiles)) return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
     if (!view_ok(a->q, 2) || !view_ok(a->k, e) || !view_ok(a->v, e) || !view_ok(a->out, 2))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
-    return from_cuda(launch_attention(*a, p, workspace, (cudaStream_t)s));
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < bytes_of(rows, tiles))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (rows.rows > 32 && attention_tiles_usable(*a))
+        return from_cuda(launch_attention_tiles(*a, tiles, workspace, (cudaStream_t)s));
+    return from_cuda(launch_attention_rows(*a, rows, workspace, (cudaStream_t)s));
+}
+
+splitzip_status splitzip_attention_status(void* workspace, splitzip_stream_t s) {
+    TraceRange trace("splitzip_attention_status");
+    if (!workspace || !aligned(workspace, 16)) return SPLITZIP_ERR_INVALID_ARG;
+    uint32_t* status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
+    uint32_t bits = 0;
+    cudaError_t e = cudaMemcpyAsync(&bits, status, sizeof(bits), cudaMemcpyDeviceToHost, (cudaStream_t)s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)s);
+    if (e == cudaSuccess && bits) e = cudaMemsetAsync(status, 0, sizeof(bits), (cudaStream_t)s);
+    if (e != cudaSuccess) return SPLITZIP_ERR_CUDA;
+    return bits ? SPLITZIP_ERR_TIMEOUT : SPLITZIP_OK;
 }
 
 splitzip_status splitzip_attention_weights(const splitzip_attention_args* a, const float* weights_in,

@@ -68,6 +68,7 @@ def library() -> ctypes.CDLL:
             "splitzip_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(NormRopeArgs), _vp]),
             "splitzip_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttentionArgs)]),
             "splitzip_attention": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), _vp, ctypes.c_size_t, _vp]),
+            "splitzip_attention_status": (ctypes.c_int, [_vp, _vp]),
             "splitzip_attention_weights": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), _vp, _vp, _vp]),
             "splitzip_evict": (ctypes.c_int, [ctypes.POINTER(EvictArgs), _vp]),
         }
@@ -234,6 +235,12 @@ def splitzip_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                       _array(lens, torch.int32, (b,), "lens"), *sizes, dim ** -0.5 if scale is None else scale)
     _check(library().splitzip_attention(ctypes.byref(a), _array(workspace, torch.uint8, None, "workspace"),
                                         workspace.numel(), _stream_of(stream)), "splitzip_attention")
+
+
+def splitzip_attention_status(workspace: torch.Tensor, stream=None) -> int:
+    """Status of the attention calls on this workspace since the last report
+    (OK or ERR_TIMEOUT); synchronises the stream."""
+    return int(library().splitzip_attention_status(_array(workspace, torch.uint8, None, "workspace"), _stream_of(stream)))
 
 
 def splitzip_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, weights_out: torch.Tensor,

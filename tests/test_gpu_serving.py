@@ -193,6 +193,7 @@ def test_attention_workspace_is_reused_across_sizes_and_streams(tq):
     for o in outs[1:]:
         for x, y in zip(o, outs[0]):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert serving.splitzip_attention_status(ws) == sz.OK
     o, l, tol, ltol = ref.attention(big_q, big_kv[:, 0], big_kv[:, 1], lens_of([6000]), 0, 0, 128 ** -0.5)
     close(outs[0][0][0], o, tol)
     o, l, tol, ltol = ref.attention(small_q, small_kv[:, 0], small_kv[:, 1], lens_of([900] * 3), 200, 2, 64 ** -0.5)

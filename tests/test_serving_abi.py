@@ -28,7 +28,7 @@ def lib():
 def test_library_exports_and_binds_every_declared_function(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(splitzip_\w+)\s*\(", text)))
-    assert len(names) == 5
+    assert len(names) == 6
     for name in names:
         assert getattr(lib, name).argtypes is not None, name
 
@@ -88,6 +88,8 @@ def test_attention_refuses_its_workspace(lib):
         assert lib.splitzip_attention(ctypes.byref(a), ws, n, None) == sz.ERR_INVALID_ARG
     assert lib.splitzip_attention(None, FAKE, need, None) == sz.ERR_INVALID_ARG
     assert lib.splitzip_attention_workspace_bytes(None) == 0
+    for ws in (None, FAKE + 8):
+        assert lib.splitzip_attention_status(ws, None) == sz.ERR_INVALID_ARG
 
 
 def test_attention_weights_refuses_its_buffers(lib):
