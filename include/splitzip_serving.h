@@ -39,10 +39,11 @@
 extern "C" {
 #endif
 
-/* A strided view [batch, tokens, heads, head_dim]: `data` and all strides
- * (counted in elements) multiples of 16 bytes, strides not negative, the
- * head_dim values of a row contiguous.  A dimension of length 1 may have any
- * such stride.  stride_b is ignored where a call takes no batch. */
+/* A strided view [batch, tokens, heads, head_dim]: the head_dim values of a row
+ * contiguous, `data` and all strides (counted in elements) multiples of 16
+ * bytes, strides positive and below 2^38; stride_b of an input may be 0 (one
+ * sequence shared by the batch).  Strides of dimensions of length 1 are not
+ * looked at, nor stride_b where a call takes no batch. */
 typedef struct splitzip_view {
     void *data;
     int64_t stride_b, stride_t, stride_h;

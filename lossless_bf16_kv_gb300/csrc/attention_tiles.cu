@@ -25,6 +25,7 @@
 
 #include "attention.cuh"
 #include "tcgen.cuh"
+#include "tensor_map.h"
 
 namespace splitzip {
 namespace {
@@ -47,7 +48,7 @@ struct TilesParams {
     CUtensorMap qmap, kmap, vmap;
     uint32_t group, tokens;   // query tokens per tile: 128 / group
     uint32_t row_ctas, splits;
-    uint32_t one_k_head, one_v_head, one_q_batch, one_k_batch, one_v_batch;  // a stride of 0: coordinate 0
+    uint32_t one_q, one_k, one_v;  // the batch is one sequence: coordinate 0
     uint32_t* counters;
     uint32_t* status;
     float* partials;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < D / 64; i++)
                     tma_load4(qs + t * S::kQ + i * (kTileM * 128), &p.qmap, 64 * i, (int32_t)(h * p.group),
-                              (int32_t)(t0 + t * p.tokens), p.one_q_batch ? 0 : (int32_t)b, &bars.q_full);
+                              (int32_t)(t0 + t * p.tokens), p.one_q ? 0 : (int32_t)b, &bars.q_full);
             uint32_t i = 0;
             for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
                 if (i >= S::kStages && !mbar_wait_bounded(&bars.empty[st], ph ^ 1, err)) break;
@@ -152,8 +153,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
 #pragma unroll
                 for (int x = 0; x < D / 64; x++)
                     tma_load4(ring + st * S::kKV + x * (kBN * 128), v ? &p.vmap : &p.kmap, 64 * x, slot0(i >> 1),
-                              (v ? p.one_v_head : p.one_k_head) ? 0 : (int32_t)h,
-                              (v ? p.one_v_batch : p.one_k_batch) ? 0 : (int32_t)b, &bars.full[st]);
+                              (int32_t)h, (v ? p.one_v : p.one_k) ? 0 : (int32_t)b, &bars.full[st]);
                 if (++st == S::kStages) st = 0, ph ^= 1;
             }
             // Every load has landed before this CTA may end, also where a wait gave up.
@@ -449,41 +449,6 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     if (warp == 8) tmem_free512(tmem);
 }
 
-// A [batch, tokens, heads, D] view as a tensor map of boxes of 64 values, `heads`
-// heads and `tokens` tokens.  Dimensions of length 1 or stride 0 become length 1
-// with some valid stride; `one_*` say where the coordinate has to be 0 then.
-bool make_map(CUtensorMap& map, const splitzip_view& v, uint32_t dim, uint32_t heads, uint32_t tokens, uint32_t batch,
-              uint32_t box_heads, uint32_t box_tokens, bool heads_first, uint32_t* one_head, uint32_t* one_batch) {
-    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static Encode encode = [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<Encode>(fn);
-    }();
-    if (!encode) return false;
-    const auto fix = [&](uint64_t& n, uint64_t& stride, uint32_t* one) {
-        if (one) *one = n > 1 && stride == 0;
-        if (n == 1 || stride == 0) n = 1, stride = 2 * dim;
-    };
-    uint64_t nh = heads, nt = tokens, nb = batch;
-    uint64_t sh = 2 * (uint64_t)v.stride_h, st = 2 * (uint64_t)v.stride_t, sb = 2 * (uint64_t)v.stride_b;
-    fix(nh, sh, one_head);
-    fix(nt, st, nullptr);
-    fix(nb, sb, one_batch);
-    const cuuint64_t sizes[4] = {dim, heads_first ? nh : nt, heads_first ? nt : nh, nb};
-    const cuuint64_t strides[3] = {heads_first ? sh : st, heads_first ? st : sh, sb};
-    const cuuint32_t box[4] = {64, heads_first ? box_heads : box_tokens, heads_first ? box_tokens : box_heads, 1};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.data, sizes, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
     Wave w;
@@ -514,14 +479,7 @@ bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p) {
 }
 
 bool attention_tiles_usable(const splitzip_attention_args& a) {
-    // The softmax takes maxima before scaling (a positive scale); a tensor map
-    // has no token stride of 0 and strides below 2^40 bytes.
-    const auto fits = [](const splitzip_view& v, uint32_t tokens) {
-        const int64_t most = (1ll << 39) - 16;
-        return (tokens == 1 || v.stride_t != 0) && v.stride_b < most && v.stride_t < most && v.stride_h < most;
-    };
-    return a.scale > 0.0f && a.cache_format == SPLITZIP_FORMAT_BF16 && fits(a.q, a.q_tokens) &&
-           (a.q_heads == 1 || a.q.stride_h != 0) && fits(a.k, a.kv_tokens) && fits(a.v, a.kv_tokens);
+    return a.scale > 0.0f && a.cache_format == SPLITZIP_FORMAT_BF16;  // maxima are taken before scaling
 }
 
 cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
@@ -536,11 +494,9 @@ cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const Atten
     p.counters = reinterpret_cast<uint32_t*>(ws);
     p.status = reinterpret_cast<uint32_t*>(ws + kAttentionStatus);
     p.partials = reinterpret_cast<float*>(ws + kAttentionHeader);
-    uint32_t one_q_head;
-    if (!make_map(p.qmap, a.q, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &one_q_head,
-                  &p.one_q_batch) ||
-        !make_map(p.kmap, a.k, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_k_head, &p.one_k_batch) ||
-        !make_map(p.vmap, a.v, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_v_head, &p.one_v_batch))
+    if (!make_map(p.qmap, a.q, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q) ||
+        !make_map(p.kmap, a.k, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_k) ||
+        !make_map(p.vmap, a.v, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_v))
         return cudaErrorInvalidValue;
     const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
     return a.head_dim == 64 ? launch<64>(p, ctas, s) : launch<128>(p, ctas, s);

@@ -17,10 +17,12 @@ inline bool format_ok(uint32_t format) { return format == SPLITZIP_FORMAT_BF16 |
 inline bool dim_ok(uint32_t d) { return d == 64 || d == 128; }
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-bool view_ok(const splitzip_view& v, uint32_t elem, bool batch = true) {
-    const int64_t unit = 16 / elem;
-    const auto ok = [unit](int64_t s) { return s >= 0 && s % unit == 0; };
-    return v.data && aligned(v.data, 16) && (!batch || ok(v.stride_b)) && ok(v.stride_t) && ok(v.stride_h);
+// A view of nb x nt x nh rows.  Strides of dimensions of length 1 are not
+// looked at; only a batch stride may be 0 (one sequence shared by the batch).
+bool view_ok(const splitzip_view& v, uint32_t elem, uint32_t nb, uint32_t nt, uint32_t nh) {
+    const int64_t unit = 16 / elem, most = 1ll << 38;
+    const auto ok = [=](uint32_t n, int64_t s, int64_t least) { return n <= 1 || (s >= least && s < most && s % unit == 0); };
+    return v.data && aligned(v.data, 16) && ok(nb, v.stride_b, 0) && ok(nt, v.stride_t, 1) && ok(nh, v.stride_h, 1);
 }
 
 constexpr uint64_t kMax31 = 0x7FFFFFFFull;
@@ -34,7 +36,7 @@ bool sizes_ok(const splitzip_attention_args& a) {
 }
 
 // Tiles of 256 query rows on the tensor cores from 33 rows on (more than the
-// other kernel's largest tile), where the views allow it.
+// other kernel's largest tile), for the cases that kernel takes.
 bool plans(const splitzip_attention_args& a, AttentionPlan& rows, AttentionPlan& tiles) {
     return attention_rows_plan(a, rows) && attention_tiles_plan(a, tiles);
 }
@@ -60,8 +62,10 @@ splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args* a, splitzip
         !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16))
         return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
-    if (!view_ok(a->q, 2, false) || !view_ok(a->k, 2, false) || !view_ok(a->v, 2, false) ||
-        !view_ok(a->q_out, 2, false) || !view_ok(a->k_cache, e, false) || !view_ok(a->v_cache, e, false))
+    const uint32_t rows = a->cache_rows > kMax31 ? (uint32_t)kMax31 : (uint32_t)a->cache_rows;
+    if (!view_ok(a->q, 2, 1, a->n, a->q_heads) || !view_ok(a->k, 2, 1, a->n, a->kv_heads) ||
+        !view_ok(a->v, 2, 1, a->n, a->kv_heads) || !view_ok(a->q_out, 2, 1, a->n, a->q_heads) ||
+        !view_ok(a->k_cache, e, 1, rows, a->kv_heads) || !view_ok(a->v_cache, e, 1, rows, a->kv_heads))
         return SPLITZIP_ERR_INVALID_ARG;
     return from_cuda(launch_norm_rope(*a, (cudaStream_t)s));
 }
@@ -77,7 +81,8 @@ splitzip_status splitzip_attention(const splitzip_attention_args* a, void* works
     AttentionPlan rows, tiles;
     if (!a || !sizes_ok(*a) || !plans(*a, rows, tiles)) return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
-    if (!view_ok(a->q, 2) || !view_ok(a->k, e) || !view_ok(a->v, e) || !view_ok(a->out, 2))
+    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) || !view_ok(a->out, 2, a->batch, a->q_tokens, a->q_heads) ||
+        !view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < bytes_of(rows, tiles))
@@ -104,7 +109,9 @@ splitzip_status splitzip_attention_weights(const splitzip_attention_args* a, con
     TraceRange trace("splitzip_attention_weights");
     if (!a || !sizes_ok(*a) || !weights_out || !a->lse) return SPLITZIP_ERR_INVALID_ARG;
     if ((uint64_t)a->batch * a->kv_heads * ((a->kv_tokens + 127ull) / 128) > kMax31) return SPLITZIP_ERR_INVALID_ARG;
-    if (!view_ok(a->q, 2) || !view_ok(a->k, elem_bytes(a->cache_format))) return SPLITZIP_ERR_INVALID_ARG;
+    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) ||
+        !view_ok(a->k, elem_bytes(a->cache_format), a->batch, a->kv_tokens, a->kv_heads))
+        return SPLITZIP_ERR_INVALID_ARG;
     if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4) ||
         !std::isfinite(a->scale))
         return SPLITZIP_ERR_INVALID_ARG;
@@ -120,7 +127,8 @@ splitzip_status splitzip_evict(const splitzip_evict_args* a, splitzip_stream_t s
         return SPLITZIP_ERR_INVALID_ARG;
     if ((uint64_t)a->keep_first + a->keep_last > a->budget) return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
-    if (!view_ok(a->k, e) || !view_ok(a->v, e) || !view_ok(a->k_out, e) || !view_ok(a->v_out, e))
+    if (!view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads) ||
+        !view_ok(a->k_out, e, a->batch, a->budget, a->kv_heads) || !view_ok(a->v_out, e, a->batch, a->budget, a->kv_heads))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!a->weights || !a->index || !aligned(a->weights, 4) || !aligned(a->index, 4) || !aligned(a->weights_out, 4) ||
         !aligned(a->lens, 4) || !aligned(a->lens_out, 4))

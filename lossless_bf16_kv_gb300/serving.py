@@ -16,6 +16,7 @@ kv_heads, head_dim].
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -55,6 +56,15 @@ class EvictArgs(ctypes.Structure):
                 ("budget", _u32), ("keep_first", _u32), ("keep_last", _u32), ("cache_format", _u32)]
 
 
+# The structures above as packed bytes (native layout, as the C compiler lays
+# them out): a call packs its arguments in one step, which costs a fraction of
+# filling a ctypes structure field by field.
+_VIEW = "P3q"
+_NORM_ROPE = struct.Struct("@" + 3 * _VIEW + "5P" + 3 * _VIEW + "2Q7If")
+_ATTENTION = struct.Struct("@" + 4 * _VIEW + "2P9If")
+_EVICT = struct.Struct("@" + 4 * _VIEW + "5P8I")
+_NO_VIEW = (0, 0, 0, 0)
+
 _lib = None
 
 
@@ -65,12 +75,12 @@ def library() -> ctypes.CDLL:
     if _lib is None:
         lib = _sz.library()
         sig = {
-            "splitzip_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(NormRopeArgs), _vp]),
-            "splitzip_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(AttentionArgs)]),
-            "splitzip_attention": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), _vp, ctypes.c_size_t, _vp]),
+            "splitzip_qk_norm_rope": (ctypes.c_int, [_vp, _vp]),
+            "splitzip_attention_workspace_bytes": (ctypes.c_size_t, [_vp]),
+            "splitzip_attention": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp]),
             "splitzip_attention_status": (ctypes.c_int, [_vp, _vp]),
-            "splitzip_attention_weights": (ctypes.c_int, [ctypes.POINTER(AttentionArgs), _vp, _vp, _vp]),
-            "splitzip_evict": (ctypes.c_int, [ctypes.POINTER(EvictArgs), _vp]),
+            "splitzip_attention_weights": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
+            "splitzip_evict": (ctypes.c_int, [_vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -88,28 +98,46 @@ def _check(status: int, what: str):
         raise SplitZipError(status, what)
 
 
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
+
+
 def _stream_of(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
-def _view(t: torch.Tensor, shape: tuple, what: str) -> tuple:
+def _view4(t: torch.Tensor, shape, what: str) -> tuple:
     """(pointer, stride_b, stride_t, stride_h) of a [batch, tokens, heads, dim] view."""
     if t.shape != shape:
-        _bad(f"{what} has shape {tuple(t.shape)}, {shape} needed")
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    st = t.stride()
-    if st[-1] != 1:
+    sb, st, sh, one = t.stride()
+    if one != 1:
         _bad(f"{what}: the values of a row must be contiguous")
-    return (t.data_ptr(), *st[:-1]) if len(st) == 4 else (t.data_ptr(), 0, *st[:-1])
+    return t.data_ptr(), sb, st, sh
 
 
-def _array(t: torch.Tensor | None, dtype, shape: tuple | None, what: str):
-    """Pointer of a contiguous array of this type and shape, or None."""
+def _view3(t: torch.Tensor, shape, what: str) -> tuple:
+    """(pointer, 0, stride_t, stride_h) of a [tokens, heads, dim] view."""
+    if t.shape != shape:
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    st, sh, one = t.stride()
+    if one != 1:
+        _bad(f"{what}: the values of a row must be contiguous")
+    return t.data_ptr(), 0, st, sh
+
+
+def _array(t: torch.Tensor | None, dtype, shape: tuple | None, what: str) -> int:
+    """Pointer of a contiguous array of this type and shape, or 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype != dtype:
         _bad(f"{what} is {t.dtype}, {dtype} needed")
     if shape is not None and t.shape != shape:
@@ -180,14 +208,15 @@ def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
         rot = table.shape[1]
         if positions is None:
             _bad("a rotation needs positions")
-    a = NormRopeArgs(_view(q, (n, hq, dim), "q"), _view(k, (n, hk, dim), "k"), _view(v, (n, hk, dim), "v"),
-                     _array(q_weight, torch.bfloat16, (dim,), "q_weight"),
-                     _array(k_weight, torch.bfloat16, (dim,), "k_weight"),
-                     _array(positions, torch.int32, (n,), "positions"),
-                     _array(table, torch.float32, None, "table"), _array(slots, torch.int64, (n,), "slots"),
-                     _view(q_out, (n, hq, dim), "q_out"), (kp, 0, kst, ksh), (vp, 0, vst, vsh),
-                     table.shape[0] if rot else 0, min(krows, vrows), n, hq, hk, dim, rot, fmt, interleaved, eps)
-    _check(library().splitzip_qk_norm_rope(ctypes.byref(a), _stream_of(stream)), "splitzip_qk_norm_rope")
+    kshape = (n, hk, dim)
+    a = _NORM_ROPE.pack(*_view3(q, q.shape, "q"), *_view3(k, kshape, "k"), *_view3(v, kshape, "v"),
+                        _array(q_weight, torch.bfloat16, (dim,), "q_weight"),
+                        _array(k_weight, torch.bfloat16, (dim,), "k_weight"),
+                        _array(positions, torch.int32, (n,), "positions"),
+                        _array(table, torch.float32, None, "table"), _array(slots, torch.int64, (n,), "slots"),
+                        *_view3(q_out, q.shape, "q_out"), kp, 0, kst, ksh, vp, 0, vst, vsh,
+                        table.shape[0] if rot else 0, min(krows, vrows), n, hq, hk, dim, rot, fmt, bool(interleaved), eps)
+    _check((_lib or library()).splitzip_qk_norm_rope(a, _stream_of(stream)), "splitzip_qk_norm_rope")
 
 
 # ------------------------------------------------------------- attention
@@ -203,8 +232,9 @@ def _sizes(q_shape, k_shape, fmt: int, window: int, sinks: int):
 
 def splitzip_attention_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, window: int = 0, sinks: int = 0) -> int:
     """Workspace bytes of splitzip_attention at these sizes (0: refused)."""
-    a = AttentionArgs((), (), (), (), None, None, *_sizes(q.shape, k_cache.shape, _format(k_cache), window, sinks), 1.0)
-    return int(library().splitzip_attention_workspace_bytes(ctypes.byref(a)))
+    a = _ATTENTION.pack(*_NO_VIEW, *_NO_VIEW, *_NO_VIEW, *_NO_VIEW, 0, 0,
+                        *_sizes(q.shape, k_cache.shape, _format(k_cache), window, sinks), 1.0)
+    return int(library().splitzip_attention_workspace_bytes(a))
 
 
 def alloc_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, window: int = 0, sinks: int = 0) -> torch.Tensor:
@@ -230,11 +260,11 @@ def splitzip_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     _bf16(out, "out")
     if ks[0] != b or ks[3] != dim:
         _bad("q's batch and dims must be the caches'")
-    a = AttentionArgs(_view(q, qs, "q"), _view(k_cache, ks, "k_cache"), _view(v_cache, ks, "v_cache"),
-                      _view(out, qs, "out"), _array(lse, torch.float32, (b, hq, tq), "lse"),
-                      _array(lens, torch.int32, (b,), "lens"), *sizes, dim ** -0.5 if scale is None else scale)
-    _check(library().splitzip_attention(ctypes.byref(a), _array(workspace, torch.uint8, None, "workspace"),
-                                        workspace.numel(), _stream_of(stream)), "splitzip_attention")
+    a = _ATTENTION.pack(*_view4(q, qs, "q"), *_view4(k_cache, ks, "k_cache"), *_view4(v_cache, ks, "v_cache"),
+                        *_view4(out, qs, "out"), _array(lse, torch.float32, (b, hq, tq), "lse"),
+                        _array(lens, torch.int32, (b,), "lens"), *sizes, dim ** -0.5 if scale is None else scale)
+    _check((_lib or library()).splitzip_attention(a, _array(workspace, torch.uint8, None, "workspace"),
+                                                  workspace.numel(), _stream_of(stream)), "splitzip_attention")
 
 
 def splitzip_attention_status(workspace: torch.Tensor, stream=None) -> int:
@@ -258,11 +288,11 @@ def splitzip_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torc
         _bad("q's batch and dims must be the cache's")
     if lse is None or weights_out is None:
         _bad("lse and weights_out are needed")
-    a = AttentionArgs(_view(q, qs, "q"), _view(k_cache, ks, "k_cache"), (), (),
-                      _array(lse, torch.float32, (b, hq, tq), "lse"), _array(lens, torch.int32, (b,), "lens"),
-                      *sizes, dim ** -0.5 if scale is None else scale)
-    _check(library().splitzip_attention_weights(
-        ctypes.byref(a), _array(weights_in, torch.float32, (b, hk, tk), "weights_in"),
+    a = _ATTENTION.pack(*_view4(q, qs, "q"), *_view4(k_cache, ks, "k_cache"), *_NO_VIEW, *_NO_VIEW,
+                        _array(lse, torch.float32, (b, hq, tq), "lse"), _array(lens, torch.int32, (b,), "lens"),
+                        *sizes, dim ** -0.5 if scale is None else scale)
+    _check((_lib or library()).splitzip_attention_weights(
+        a, _array(weights_in, torch.float32, (b, hk, tk), "weights_in"),
         _array(weights_out, torch.float32, (b, hk, tk), "weights_out"), _stream_of(stream)),
         "splitzip_attention_weights")
 
@@ -286,9 +316,9 @@ def splitzip_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.
         _bad("keep_first and keep_last are not negative")
     b, t, h, dim = ks
     budget = os[1]
-    a = EvictArgs(_view(k_cache, ks, "k_cache"), _view(v_cache, ks, "v_cache"), _view(k_out, os, "k_out"),
-                  _view(v_out, os, "v_out"), _array(weights, torch.float32, (b, h, t), "weights"),
-                  _array(lens, torch.int32, (b,), "lens"), _array(index, torch.int32, (b, h, budget), "index"),
-                  _array(weights_out, torch.float32, (b, h, budget), "weights_out"),
-                  _array(lens_out, torch.int32, (b,), "lens_out"), b, t, h, dim, budget, keep_first, keep_last, fmt)
-    _check(library().splitzip_evict(ctypes.byref(a), _stream_of(stream)), "splitzip_evict")
+    a = _EVICT.pack(*_view4(k_cache, ks, "k_cache"), *_view4(v_cache, ks, "v_cache"), *_view4(k_out, os, "k_out"),
+                    *_view4(v_out, os, "v_out"), _array(weights, torch.float32, (b, h, t), "weights"),
+                    _array(lens, torch.int32, (b,), "lens"), _array(index, torch.int32, (b, h, budget), "index"),
+                    _array(weights_out, torch.float32, (b, h, budget), "weights_out"),
+                    _array(lens_out, torch.int32, (b,), "lens_out"), b, t, h, dim, budget, keep_first, keep_last, fmt)
+    _check((_lib or library()).splitzip_evict(a, _stream_of(stream)), "splitzip_evict")

@@ -51,6 +51,8 @@ def test_structures_have_the_c_layout(tmp_path):
         want.append(ctypes.sizeof(cls))
         want += [getattr(cls, f).offset for f, _ in cls._fields_]
     assert got == want
+    assert [x.size for x in (serving._NORM_ROPE, serving._ATTENTION, serving._EVICT)] == \
+        [ctypes.sizeof(x) for x in (serving.NormRopeArgs, serving.AttentionArgs, serving.EvictArgs)]
 
 
 FAKE = 1 << 20   # aligned, never dereferenced: every call below is refused
