@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     auto whole_cta = [&](int32_t s0) { return p0 >= 0 && mask.all(p0, p1, s0, s0 + kBN - 1); };
     volatile uint32_t* err = &bars.err;
 
-    if (warp == 8) tmem_alloc512(&bars.tmem);
+    if (warp == 8) tmem_alloc<512>(&bars.tmem);
     if (tid == 0) {
         for (int i = 0; i < S::kStages; i++) {
             mbar_init(&bars.full[i], 1);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     }
     __syncthreads();
     tcgen_fence_after();
-    if (warp == 8) tmem_free512(tmem);
+    if (warp == 8) tmem_free<512>(tmem);
 }
 
 template <int D>
