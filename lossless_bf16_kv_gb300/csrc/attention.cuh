@@ -64,6 +64,31 @@ struct SlotTiles {
     __device__ __forceinline__ uint32_t tile(uint32_t j) const { return j < head ? j : j - head + from; }
 };
 
+// ----------------------------------------------------- thread-block cluster
+
+// All threads of the cluster; shared-memory writes before it are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 32-bit (4 x 32-bit) value at this CTA's shared address, of the cluster's CTA `rank`.
+__device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // ------------------------------------------------- warp matrix products
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {

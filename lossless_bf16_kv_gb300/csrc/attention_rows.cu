@@ -8,10 +8,11 @@
 //     s = q k^T, m' = max(m, s), p = exp(s - m'), l = l exp(m - m') + sum p,
 //     o = o exp(m - m') + p v,
 // and the partial (m, l, o) are joined by the same rule: over the warps in
-// shared memory, over the splits by the CTA that finishes last, always in the
-// same order.  Every key and value is read once: HBM bounds it.  A warp keeps
-// a private ring of slot tiles filled by cp.async, so nothing in the loop
-// waits for another warp.
+// shared memory, over up to eight splits through the shared memory of their
+// thread-block cluster, over more than that by the CTA that finishes last,
+// always in the same order.  Every key and value is read once: HBM bounds it.
+// A warp keeps a private ring of slot tiles filled by cp.async, so nothing in
+// the loop waits for another warp.
 #include <algorithm>
 #include <cstdint>
 
@@ -26,7 +27,7 @@ constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
 
 struct RowsParams {
     splitzip_attention_args a;
-    uint32_t group, rows, row_tiles, splits;
+    uint32_t group, rows, row_tiles, splits, cluster;  // splits: a multiple of the cluster size
     uint32_t* counters;
     float* partials;
 };
@@ -51,6 +52,10 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
     return r * kRow + ((c ^ ((r >> 1) & 3u)) << 4);  // two rows to 128 bytes
 }
 
+__device__ __forceinline__ void add_scaled(float4& v, float f, float4 x) {
+    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+}
+
 template <int D, bool kF8, int MT>
 __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_constant__ RowsParams p) {
     using S = RowsShape<D, kF8, MT>;
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
     constexpr int kChunks = S::kRow / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_scale[S::kTileRows];
-    __shared__ float s_m[kWarpsRows][S::kTileRows], s_l[kWarpsRows][S::kTileRows];
+    __shared__ float s_m[kWarpsRows][S::kTileRows], s_l[kWarpsRows][S::kTileRows], s_mm[S::kTileRows], s_ll[S::kTileRows];
     __shared__ uint32_t s_last;
     const splitzip_attention_args& a = p.a;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -335,42 +340,84 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
                 os[(warp * S::kTileRows + 16 * i + 8 * (x >> 1) + lane / 4) * D + column(n, x)] = o[i][n][x];
     __syncthreads();
 
-    auto store_row = [&](uint32_t r, uint32_t c, float v, float mm, float ll) {
-        const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
-        const uint32_t hq = h * p.group + g;
-        const bool sees = mask.first + (int32_t)t >= 0;  // its own position, then
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)t * a.out.stride_t +
-                             hq * a.out.stride_h;
-        out[c] = __float2bfloat16(sees ? v / ll : 0.0f);
-        if (c == 0 && a.lse)
-            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-    };
     const uint32_t nrows = r1 - r0;
-    float* part = p.partials + (uint64_t)blockIdx.x * (S::kTileRows * (D + 2));
-    for (uint32_t at = tid; at < nrows * D; at += 32 * kWarpsRows) {
-        const uint32_t r = at / D, c = at % D;
+    for (uint32_t at = tid; at < nrows * (D / 4); at += 32 * kWarpsRows) {
+        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
         float mm = s_m[0][r];
 #pragma unroll
         for (int w = 1; w < kWarpsRows; w++) mm = fmaxf(mm, s_m[w][r]);
         const float use = mm == -INFINITY ? 0.0f : mm;
-        float ll = 0.0f, v = 0.0f;
+        float ll = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarpsRows; w++) {
             const float f = exp2_approx(s_m[w][r] - use);
             ll = fmaf(f, s_l[w][r], ll);
-            v = fmaf(f, os[(w * S::kTileRows + r) * D + c], v);
+            add_scaled(v, f, *reinterpret_cast<const float4*>(os + (w * S::kTileRows + r) * D + c));
         }
-        if (p.splits == 1) {
-            store_row(r, c, v, mm, ll);
-        } else {
-            __stcg(part + r * D + c, v);
-            if (c == 0) {
-                __stcg(part + S::kTileRows * D + r, mm);
-                __stcg(part + S::kTileRows * (D + 1) + r, ll);
-            }
+        *reinterpret_cast<float4*>(os + r * D + c) = v;  // over the first warp's, which only this thread reads
+        if (c == 0) {
+            s_mm[r] = mm;
+            s_ll[r] = ll;
         }
     }
-    if (p.splits == 1) return;
+
+    // Join the cluster: each of its CTAs a share of the outputs.
+    const uint32_t cluster = p.cluster, rank = split % cluster, groups = p.splits / cluster;
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+    auto store = [&](uint32_t r, uint32_t c, float4 v, float mm, float ll) {
+        const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
+        const uint32_t hq = h * p.group + g;
+        const bool sees = mask.first + (int32_t)t >= 0;  // its own position, then
+        const float inv = 1.0f / ll;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)t * a.out.stride_t +
+                             hq * a.out.stride_h;
+        *reinterpret_cast<uint2*>(out + c) =
+            sees ? make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+        if (c == 0 && a.lse)
+            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    };
+    constexpr uint32_t kPart = S::kTileRows * (D + 4);  // floats of a partial result: rows of o, m, l
+    const uint32_t group = split / cluster;
+    float* all = p.partials + (uint64_t)unit * groups * kPart;
+    for (uint32_t at = rank * 32 * kWarpsRows + tid; at < nrows * (D / 4); at += cluster * 32 * kWarpsRows) {
+        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
+        float m8[8], l8[8];
+        float4 v8[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            m8[i] = -INFINITY;
+            l8[i] = 0.0f;
+            v8[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < (int)cluster) {
+                m8[i] = cluster_ld(smem_addr(&s_mm[r]), i);
+                l8[i] = cluster_ld(smem_addr(&s_ll[r]), i);
+                v8[i] = cluster_ld4(smem_addr(os + r * D + c), i);
+            }
+        }
+        float mm = m8[0];
+#pragma unroll
+        for (int i = 1; i < 8; i++) mm = fmaxf(mm, m8[i]);
+        const float use = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float f = exp2_approx(m8[i] - use);
+            ll = fmaf(f, l8[i], ll);
+            add_scaled(v, f, v8[i]);
+        }
+        if (groups == 1) {
+            store(r, c, v, mm, ll);
+        } else {
+            float* q = all + group * kPart + r * (D + 4);
+            __stcg(reinterpret_cast<float4*>(q + c), v);
+            if (c == 0) __stcg(reinterpret_cast<float2*>(q + D), make_float2(mm, ll));
+        }
+    }
+    if (cluster > 1) cluster_sync();  // this CTA's shared memory has been read
+    if (groups == 1) return;
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -380,21 +427,23 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    const float* all = p.partials + (uint64_t)unit * p.splits * (S::kTileRows * (D + 2));
-    constexpr uint32_t kStep = S::kTileRows * (D + 2);
-    for (uint32_t at = tid; at < nrows * D; at += 32 * kWarpsRows) {
-        const uint32_t r = at / D, c = at % D;
-        float mm = -INFINITY;
-        for (uint32_t i = 0; i < p.splits; i++) mm = fmaxf(mm, __ldcg(all + i * kStep + S::kTileRows * D + r));
-        const float use = mm == -INFINITY ? 0.0f : mm;
-        float ll = 0.0f, v = 0.0f;
-        for (uint32_t i = 0; i < p.splits; i++) {
-            const float* q = all + i * kStep;
-            const float f = exp2_approx(__ldcg(q + S::kTileRows * D + r) - use);
-            ll = fmaf(f, __ldcg(q + S::kTileRows * (D + 1) + r), ll);
-            v = fmaf(f, __ldcg(q + r * D + c), v);
+    for (uint32_t at = tid; at < nrows * (D / 4); at += 32 * kWarpsRows) {
+        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
+        const float* q = all + r * (D + 4);
+        float mm = -INFINITY, ll = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (uint32_t i = 0; i < groups; i++) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + i * kPart + D));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + i * kPart + c));
+            const float top = fmaxf(mm, ml.x), use = top == -INFINITY ? 0.0f : top;
+            const float f = exp2_approx(mm - use), g = exp2_approx(ml.x - use);
+            ll = fmaf(f, ll, g * ml.y);
+            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            add_scaled(v, g, x);
+            mm = top;
         }
-        store_row(r, c, v, mm, ll);
+        store(r, c, v, mm, ll);
     }
 }
 
@@ -404,8 +453,18 @@ cudaError_t launch(const RowsParams& p, uint32_t ctas, cudaStream_t s) {
     Wave w;
     const cudaError_t e = launch_wave<rows_kernel<D, kF8, MT>>(32 * kWarpsRows, S::kSmem, w);
     if (e != cudaSuccess) return e;
-    rows_kernel<D, kF8, MT><<<ctas, 32 * kWarpsRows, S::kSmem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * kWarpsRows);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rows_kernel<D, kF8, MT>, p);
 }
 
 template <int D, bool kF8>
@@ -425,13 +484,17 @@ bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     // The slots a row tile can see at most.
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
-    // Two CTAs on every SM if each split still has two tiles for each warp.
-    uint64_t splits = 2 * kSms / units;
-    splits = std::min(splits, most / (2 * kWarpsRows * slots));
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
+    // Enough CTAs for two on every SM while each split still has two tiles for
+    // each warp; and up to four times as many, so that sequences of different
+    // lengths even out, while it has eight.
+    const uint64_t fill = std::min(2 * kSms / units, most / (2 * kWarpsRows * slots));
+    const uint64_t even = std::min(8 * kSms / units, most / (8 * kWarpsRows * slots));
+    const uint64_t splits = std::max(fill, even);
+    // Up to eight splits are one cluster, more are clusters of eight.
+    p.splits = (uint32_t)(splits < 1 ? 1 : splits > 8 ? splits / 8 * 8 : splits);
     if (units * p.splits > 0x7FFFFFFFull) return false;
-    static_assert(4 * kSms <= kAttentionStatus, "two or more splits: at most kSms row tiles");
-    p.bytes = kAttentionHeader + (p.splits > 1 ? units * p.splits * p.tile_rows * (a.head_dim + 2) * 4 : 0);
+    static_assert(4 * kSms <= kAttentionStatus, "more than eight splits: fewer than kSms row tiles");
+    p.bytes = kAttentionHeader + (p.splits > 8 ? units * (p.splits / 8) * p.tile_rows * (a.head_dim + 4) * 4 : 0);
     return true;
 }
 
@@ -443,6 +506,7 @@ cudaError_t launch_attention_rows(const splitzip_attention_args& a, const Attent
     p.rows = plan.rows;
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
+    p.cluster = std::min(plan.splits, 8u);
     p.counters = reinterpret_cast<uint32_t*>(workspace);
     p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
     const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
