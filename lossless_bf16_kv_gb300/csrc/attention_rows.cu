@@ -22,7 +22,8 @@ namespace splitzip {
 namespace {
 
 constexpr int kWarpsRows = 4;
-constexpr int kStagesRows = 3;
+constexpr int kStagesRows = 2;
+constexpr uint32_t kCtasPerSm = 3;  // of 16-row tiles, by registers and shared memory
 constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
 
 struct RowsParams {
@@ -57,7 +58,7 @@ __device__ __forceinline__ void add_scaled(float4& v, float f, float4 x) {
 }
 
 template <int D, bool kF8, int MT>
-__global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) rows_kernel(const __grid_constant__ RowsParams p) {
     using S = RowsShape<D, kF8, MT>;
     constexpr int NT = S::kSlots / 8;    // n-tiles of the scores
     constexpr int KS = D / 16;           // k-steps of the scores
@@ -85,17 +86,32 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
     uint8_t* qs = smem + S::kRing;
     const uint8_t* kbase = static_cast<const uint8_t*>(a.k.data) + (b * a.k.stride_b + h * a.k.stride_h) * S::kElem;
     const uint8_t* vbase = static_cast<const uint8_t*>(a.v.data) + (b * a.v.stride_b + h * a.v.stride_h) * S::kElem;
-    // Slots past the last one in use are loaded as copies of it and masked.
+    // A lane copies one 16-byte chunk of every kStep-th row of a tile.  Slots past
+    // the last one in use are loaded as copies of it and masked.
+    constexpr int kStep = 32 / kChunks, kCopies = S::kSlots / kStep;
+    const uint32_t lr = lane / kChunks, lc = lane % kChunks;
+    const int64_t kstride = a.k.stride_t * S::kElem, vstride = a.v.stride_t * S::kElem;
+    const uint8_t *klane = kbase + 16 * lc, *vlane = vbase + 16 * lc;
     auto load = [&](uint32_t j, uint32_t stage) {
         if (j < j1) {
             const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
             uint8_t* dk = ring + stage * (2 * kTileBytes);
+            if (s0 + S::kSlots <= mask.n) {
+                const uint8_t *k = klane + (s0 + (int64_t)lr) * kstride, *v = vlane + (s0 + (int64_t)lr) * vstride;
 #pragma unroll
-            for (int i = 0; i < kTileBytes / 512; i++) {
-                const uint32_t at = i * 32 + lane, r = at / kChunks, c = at % kChunks;
-                const int64_t slot = min(s0 + (int32_t)r, mask.n - 1);
-                cp_async16(dk + chunk_at<S::kRow>(r, c), kbase + slot * a.k.stride_t * S::kElem + 16 * c);
-                cp_async16(dk + kTileBytes + chunk_at<S::kRow>(r, c), vbase + slot * a.v.stride_t * S::kElem + 16 * c);
+                for (int i = 0; i < kCopies; i++) {
+                    cp_async16(dk + chunk_at<S::kRow>(i * kStep + lr, lc), k);
+                    cp_async16(dk + kTileBytes + chunk_at<S::kRow>(i * kStep + lr, lc), v);
+                    k += kStep * kstride;
+                    v += kStep * vstride;
+                }
+            } else {
+                for (int i = 0; i < kCopies; i++) {
+                    const uint32_t r = i * kStep + lr;
+                    const int64_t slot = min(s0 + (int32_t)r, mask.n - 1);
+                    cp_async16(dk + chunk_at<S::kRow>(r, lc), klane + slot * kstride);
+                    cp_async16(dk + kTileBytes + chunk_at<S::kRow>(r, lc), vlane + slot * vstride);
+                }
             }
         }
         cp_async_commit();
@@ -158,6 +174,10 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
             for (int x = 0; x < 4; x++) o[i][j][x] = 0.0f;
 
     const uint32_t qaddr = smem_addr(qs);
+    uint32_t qf[KS][4];  // one row tile: its query fragments stay in registers
+    if (MT == 1)
+#pragma unroll
+        for (int k = 0; k < KS; k++) ldmatrix4(qf[k], qaddr + chunk_at<2 * D>(lane & 15, 2 * k + (lane >> 4)));
     bool odd = false;  // a value of a partly visible tile was infinite or NaN
     uint32_t stage = 0;
     for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
@@ -180,8 +200,13 @@ __global__ void __launch_bounds__(32 * kWarpsRows) rows_kernel(const __grid_cons
         for (int k = 0; k < KS; k++) {
             uint32_t q[MT][4];
 #pragma unroll
-            for (int i = 0; i < MT; i++)
-                ldmatrix4(q[i], qaddr + chunk_at<2 * D>(16 * i + (lane & 15), 2 * k + (lane >> 4)));
+            for (int i = 0; i < MT; i++) {
+                if (MT == 1)
+#pragma unroll
+                    for (int x = 0; x < 4; x++) q[i][x] = qf[k][x];
+                else
+                    ldmatrix4(q[i], qaddr + chunk_at<2 * D>(16 * i + (lane & 15), 2 * k + (lane >> 4)));
+            }
             if (kF8) {
 #pragma unroll
                 for (int n = 0; n < NT; n += 4) {
@@ -484,16 +509,23 @@ bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     // The slots a row tile can see at most.
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
-    // Enough CTAs for two on every SM while each split still has two tiles for
-    // each warp; and up to four times as many, so that sequences of different
-    // lengths even out, while it has eight.
-    const uint64_t fill = std::min(2 * kSms / units, most / (2 * kWarpsRows * slots));
-    const uint64_t even = std::min(8 * kSms / units, most / (8 * kWarpsRows * slots));
-    const uint64_t splits = std::max(fill, even);
-    // Up to eight splits are one cluster, more are clusters of eight.
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits > 8 ? splits / 8 * 8 : splits);
+    // The splits with the least time, taken as waves of CTAs times the tiles of
+    // each warp in a split plus kSplitCost tiles for a CTA's start and join, of
+    // those that leave each warp two tiles.  Up to eight splits are one cluster,
+    // more are clusters of eight.
+    constexpr uint64_t kSplitCost = 2;
+    const uint64_t wave = (p.tile_rows == 16 ? kCtasPerSm : 2) * kSms, tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
+    uint64_t best = ~0ull;
+    p.splits = 1;
+    for (uint64_t n = 1; n == 1 || (n * 2 <= tiles && units * n <= 16 * wave && (n <= 8 || units <= kSms)); n += n < 8 ? 1 : 8) {
+        const uint64_t time = (units * n + wave - 1) / wave * ((tiles + n - 1) / n + kSplitCost);
+        if (time < best) {
+            best = time;
+            p.splits = (uint32_t)n;
+        }
+    }
     if (units * p.splits > 0x7FFFFFFFull) return false;
-    static_assert(4 * kSms <= kAttentionStatus, "more than eight splits: fewer than kSms row tiles");
+    static_assert(4 * kSms <= kAttentionStatus, "splits in several clusters are counted by row tile");
     p.bytes = kAttentionHeader + (p.splits > 8 ? units * (p.splits / 8) * p.tile_rows * (a.head_dim + 4) * 4 : 0);
     return true;
 }
