@@ -13,9 +13,15 @@
 // 2 x 512 cycles at head_dim 128, the 128 x 128 exponentials 512.
 //
 // Roles: warps 0-3 and 4-7 softmax (one thread per row, so row statistics need
-// no exchange), 8 issues the products, 9 the TMA loads of a ring of key and
-// value tiles, 10 and 11 keep infinities and NaN of partly visible tiles out of
-// the second product (0 x infinity is not 0).
+// no exchange), 8 issues the products, 9 the TMA loads, 10 and 11 keep
+// infinities and NaN of partly visible tiles out of the second product (0 x
+// infinity is not 0) and, for an E5M2 cache, widen its tiles to FP16 (exact: an
+// E5M2 value is the upper byte of the FP16 value it stands for).  The queries
+// are then FP16 too, each row scaled by a power of two.
+//
+// What the roles share sits in shared memory and is read from there: a softmax
+// thread's 168 to 216 registers hold a row of scores and little else, and a
+// value spilled there costs hundreds of cycles in every step.
 //
 // The running maximum is only raised when a row's maximum grows by more than
 // 2^8 (in which case O and l are rescaled by the softmax warps, after the
@@ -35,12 +41,17 @@ constexpr int kTileM = 128;    // query rows per tile
 constexpr int kThreadsTiles = 384;
 constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
 
-template <int D>
+template <int D, bool kF8>
 struct TilesShape {
-    static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile
+    static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
+    static constexpr int kRaw = kBN * D;         // bytes of one in E5M2
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
-    static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr int kSmem = 2 * kQ + kStages * kKV + 1024;
+    static constexpr int kStages = D == 128 ? (kF8 ? 3 : 5) : (kF8 ? 4 : 8);
+    static constexpr int kRaws = kF8 ? 3 : 0;
+    static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
+    static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * kRaw;
+    static constexpr int kSmem = kUsed + 1024;
+    static_assert(kUsed >= 2 * kTileM * kRowFloats * 4, "partial results take the place of the tiles");
 };
 
 struct TilesParams {
@@ -49,413 +60,616 @@ struct TilesParams {
     uint32_t group, tokens;   // query tokens per tile: 128 / group
     uint32_t row_ctas, splits;
     uint32_t one_q, one_k, one_v;  // the batch is one sequence: coordinate 0
-    uint32_t* counters;
     uint32_t* status;
-    float* partials;
 };
 
-struct TilesBars {
-    uint64_t full[8], empty[8], ok[8];  // ring stage: loaded, free again, values fit for the product
+struct TilesShared {
+    uint64_t full[8], empty[8];  // ring stage: tile there in 16 bits, free again
+    uint64_t ok[8];              // step i mod 8: its values are fit for the product
+    uint64_t raw_full[3], raw_empty[3];  // E5M2 tiles
     uint64_t q_full;
-    uint64_t s_full[2], p_full[2], o_full[2], drained;
-    uint32_t tmem, err, odd, last;
+    uint64_t s_full[2], p_full[2][2], o_full[2], drained;  // of the query tiles; P by halves of the slots
+    uint32_t tmem, err, odd;
+    // This CTA's work: sequence, head, first query token; the first slot of step
+    // 0, the step that jumps from the sinks to the window and to where.
+    uint32_t b, h, t0, steps;
+    int32_t s0, jump_at, jump_to;
+    int32_t n, first, sinks, p0, p1;
+    uint32_t window;
 };
 
-// Bits of the slots s0 .. s0 + 31 that a query at `pos` sees.
-__device__ __forceinline__ uint32_t seen_bits(const Mask& m, int32_t pos, int32_t s0) {
-    const int32_t hi = min(pos - s0, 31);  // slots s0 + j with j <= hi, and
-    if (hi < 0) return 0u;                 // j >= lo (window) or j <= sk (sinks)
-    const uint32_t upto = 0xFFFFFFFFu >> (31 - hi);
-    const int64_t lo = (int64_t)pos - (int64_t)m.window + 1 - s0;
-    const uint32_t in_window = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << (uint32_t)lo;
-    const int32_t sk = min(m.sinks - 1 - s0, 31);
-    const uint32_t sink = sk < 0 ? 0u : 0xFFFFFFFFu >> (31 - sk);
-    return upto & (in_window | sink);
+// The first slot of each step in turn.
+struct StepSlots {
+    int32_t s0, at, to, i;
+    __device__ __forceinline__ explicit StepSlots(const volatile TilesShared& sh)
+        : s0(sh.s0), at(sh.jump_at), to(sh.jump_to), i(0) {}
+    __device__ __forceinline__ void next() { s0 = ++i == at ? to : s0 + kBN; }
+};
+// The tiles of slots that every query of [p0, p1] sees, from the tile's first slot.
+struct WholeTiles {
+    int32_t upto, after, sinks;
+    __device__ __forceinline__ WholeTiles(const volatile TilesShared& sh, int32_t p0, int32_t p1) {
+        upto = p0 - (kBN - 1);
+        const int64_t back = (int64_t)p1 - (int64_t)sh.window;
+        after = back < -1 ? -1 : (int32_t)back;
+        sinks = sh.sinks - kBN;
+    }
+    __device__ __forceinline__ bool operator()(int32_t s0) const { return s0 <= upto && (s0 > after || s0 <= sinks); }
+};
+
+// Bits of the slots s0 .. s0 + 31 that a query sees: those from `lo` (the start
+// of its window) to `pos`, and the first `sinks`.
+__device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t lo, int32_t sinks, int32_t s0) {
+    const int32_t hi = pos - s0, l = lo - s0, k = sinks - s0;
+    const uint32_t upto = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : ~(0xFFFFFFFEu << hi);
+    const uint32_t from = l <= 0 ? 0xFFFFFFFFu : l > 31 ? 0u : 0xFFFFFFFFu << l;
+    const uint32_t sink = k <= 0 ? 0u : k > 31 ? 0xFFFFFFFFu : ~(0xFFFFFFFFu << k);
+    return upto & (from | sink);
 }
 
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
-    using S = TilesShape<D>;
-    constexpr uint32_t kShapeS = mma_shape(kHalf, kBN, false), kShapeO = mma_shape(kHalf, D, true);
-    constexpr uint32_t kColO = 256;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ TilesBars bars;
-    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* qs = smem;                 // two tiles, each D / 64 blocks of 128 rows of 128 bytes
-    uint8_t* ring = smem + 2 * S::kQ;   // kStages tiles, each D / 64 blocks of 128 slots of 128 bytes
-    const splitzip_attention_args& a = p.a;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// ------------------------------------------------------------------ roles
 
-    // The last row tiles see the most slots: they go first.
-    uint32_t unit = blockIdx.x / p.splits;
-    const uint32_t split = blockIdx.x - unit * p.splits;
-    const uint32_t rc = p.row_ctas - 1 - unit % p.row_ctas, bh = unit / p.row_ctas;
-    const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
-    const Mask mask(a, b);
-    const uint32_t t0 = rc * 2 * p.tokens, t1 = min(t0 + 2 * p.tokens, a.q_tokens);
-    const int32_t p0 = mask.first + (int32_t)t0, p1 = mask.first + (int32_t)t1 - 1;
-    const SlotTiles tiles(mask, p0, p1, kBN);
-    const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
-    const uint32_t steps = (uint32_t)((uint64_t)tiles.count * (split + 1) / p.splits) - j0;
-    auto slot0 = [&](uint32_t i) { return (int32_t)(tiles.tile(j0 + i) * kBN); };
-    auto whole_cta = [&](int32_t s0) { return p0 >= 0 && mask.all(p0, p1, s0, s0 + kBN - 1); };
-    volatile uint32_t* err = &bars.err;
-
-    if (warp == 8) tmem_alloc<512>(&bars.tmem);
-    if (tid == 0) {
-        for (int i = 0; i < S::kStages; i++) {
-            mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
-        }
-        for (int i = 0; i < 8; i++) mbar_init(&bars.ok[i], 2);  // of step i mod 8: fewer are in the ring
-        mbar_init(&bars.q_full, 1);
-        for (int i = 0; i < 2; i++) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.o_full[i], 1);
-        }
-        mbar_init(&bars.drained, 1);
-        bars.err = bars.odd = 0;
-        fence_mbar_init();
-    }
-    // Rows of a tile that hold no query (128 is not a multiple of every group).
-    if (tid < 256) {
-        const uint32_t r = tid & 127;
-        if (r >= p.tokens * p.group)
+template <int D, bool kF8>
+__device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw) {
+    using S = TilesShape<D, kF8>;
+    volatile uint32_t* err = &sh.err;
+    const int32_t b = (int32_t)sh.b, h = (int32_t)sh.h;
+    const uint32_t steps = sh.steps;
+    if (!kF8) {
+        mbar_arrive_expect_tx(&sh.q_full, 2 * p.tokens * p.group * D * 2);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
 #pragma unroll
             for (int i = 0; i < D / 64; i++)
-#pragma unroll
-                for (int c = 0; c < 8; c++)
-                    *reinterpret_cast<uint4*>(qs + (tid >> 7) * S::kQ + i * (kTileM * 128) + r * 128 + 16 * c) = make_uint4(0, 0, 0, 0);
-        fence_async_proxy();
+                tma_load4(qs + t * S::kQ + i * (kTileM * 128), &p.qmap, 64 * i, h * (int32_t)p.group,
+                          (int32_t)(sh.t0 + t * p.tokens), p.one_q ? 0 : b, &sh.q_full);
     }
-    tcgen_fence_before();
-    __syncthreads();
-    tcgen_fence_after();
-    const uint32_t tmem = bars.tmem;
+    constexpr int kN = kF8 ? S::kRaws : S::kStages;
+    uint64_t* full = kF8 ? sh.raw_full : sh.full;
+    uint64_t* empty = kF8 ? sh.raw_empty : sh.empty;
+    StepSlots slots(sh);
+    uint32_t i = 0;
+    for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
+        if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, err)) break;
+        const bool v = i & 1;
+        const int32_t bb = (v ? p.one_v : p.one_k) ? 0 : b;
+        mbar_arrive_expect_tx(&full[st], kF8 ? S::kRaw : S::kKV);
+        if (kF8) {
+            tma_load4(raw + st * S::kRaw, v ? &p.vmap : &p.kmap, 0, slots.s0, h, bb, &full[st]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < D / 64; x++)
+                tma_load4(ring + st * S::kKV + x * (kBN * 128), v ? &p.vmap : &p.kmap, 64 * x, slots.s0, h, bb, &full[st]);
+        }
+        if (v) slots.next();
+        if (++st == kN) st = 0, ph ^= 1;
+    }
+    // Every load has landed before this CTA may end, also where a wait gave up.
+    uint32_t late = 0;
+    if (!kF8) mbar_wait_bounded(&sh.q_full, 0, &late);
+    for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded(&full[x % kN], (x / kN) & 1, &late);
+}
 
-    if (warp >= 8) {
-        regs_dec<72>();
-        if (warp == 9 && lane == 0 && steps) {  // TMA
-            const uint32_t rows = p.tokens * p.group;
-            mbar_arrive_expect_tx(&bars.q_full, 2 * rows * D * 2);
+template <int D, bool kF8>
+__device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, const uint8_t* qs, const uint8_t* ring) {
+    using S = TilesShape<D, kF8>;
+    constexpr uint32_t kShapeS = mma_shape(kF8, kBN, false), kShapeO = mma_shape(kF8, D, true);
+    volatile uint32_t* err = &sh.err;
+    const bool leader = elect_one();
+    const uint32_t steps = sh.steps;
+    const uint32_t qd = desc_rows(smem_addr(qs)), kd = desc_rows(smem_addr(ring)), vd = desc_columns(smem_addr(ring), kBN * 128);
+    // S of query tile t from the keys in ring stage st.
+    auto issue_s = [&](uint32_t t, uint32_t st) {
+        if (leader) {
+            const uint32_t qa = qd + t * (S::kQ >> 4), ka = kd + st * (S::kKV >> 4);
 #pragma unroll
-            for (int t = 0; t < 2; t++)
-#pragma unroll
-                for (int i = 0; i < D / 64; i++)
-                    tma_load4(qs + t * S::kQ + i * (kTileM * 128), &p.qmap, 64 * i, (int32_t)(h * p.group),
-                              (int32_t)(t0 + t * p.tokens), p.one_q ? 0 : (int32_t)b, &bars.q_full);
-            uint32_t i = 0;
-            for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
-                if (i >= S::kStages && !mbar_wait_bounded(&bars.empty[st], ph ^ 1, err)) break;
-                const bool v = i & 1;
-                mbar_arrive_expect_tx(&bars.full[st], S::kKV);
-#pragma unroll
-                for (int x = 0; x < D / 64; x++)
-                    tma_load4(ring + st * S::kKV + x * (kBN * 128), v ? &p.vmap : &p.kmap, 64 * x, slot0(i >> 1),
-                              (int32_t)h, (v ? p.one_v : p.one_k) ? 0 : (int32_t)b, &bars.full[st]);
-                if (++st == S::kStages) st = 0, ph ^= 1;
+            for (int k = 0; k < D / 16; k++) {
+                const uint32_t at = (k >> 2) * (kBN * 128) + (k & 3) * 32;
+                mma_ss(tmem + t * kBN, desc(qa, at), desc(ka, at), kShapeS, k > 0);
             }
-            // Every load has landed before this CTA may end, also where a wait gave up.
-            uint32_t late = 0;
-            mbar_wait_bounded(&bars.q_full, 0, &late);
-            for (uint32_t x = i > S::kStages ? i - S::kStages : 0; x < i; x++)
-                mbar_wait_bounded(&bars.full[x % S::kStages], (x / S::kStages) & 1, &late);
-        } else if (warp == 8 && lane == 0 && steps) {  // matrix products
-            const uint32_t qa = smem_addr(qs), ra = smem_addr(ring);
-            auto issue_s = [&](uint32_t t, uint32_t st) {
+            mma_commit(&sh.s_full[t]);
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+        if (leader) mma_commit(bar);
+        __syncwarp();
+    };
+    uint32_t st = 0, ph = 0;
+    auto next = [&]() {
+        if (++st == S::kStages) st = 0, ph ^= 1;
+    };
+    bool go = mbar_wait_bounded(&sh.q_full, 0, err) && mbar_wait_bounded(&sh.full[0], 0, err);
+    if (go) {
+        tcgen_fence_after();
+        issue_s(0, 0);
+        issue_s(1, 0);
+        commit(&sh.empty[0]);
+        next();
+    }
+    for (uint32_t i = 0; go && i < steps; i++) {
+        const uint32_t vst = st;
+        go = mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) && mbar_wait_bounded(&sh.full[st], ph, err);
+        if (!go) break;
+        next();
+        const bool more = i + 1 < steps;
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint32_t at = (k >> 2) * (kBN * 128) + (k & 3) * 32;
-                    mma_ss(tmem + t * kBN, desc_rows(qa + t * S::kQ + at), desc_rows(ra + st * S::kKV + at), kShapeS, k > 0);
-                }
-                mma_commit(&bars.s_full[t]);
-            };
-            uint32_t st = 0, ph = 0;
-            auto next = [&]() {
-                if (++st == S::kStages) st = 0, ph ^= 1;
-            };
-            bool go = mbar_wait_bounded(&bars.q_full, 0, err) && mbar_wait_bounded(&bars.full[0], 0, err);
-            if (go) {
+        for (uint32_t t = 0; t < 2; t++) {
+            // The first half of the slots' P is ready while the second is still being made.
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                if (go) go = mbar_wait_bounded(&sh.p_full[t][half], i & 1, err);
                 tcgen_fence_after();
-                issue_s(0, 0);
-                issue_s(1, 0);
-                mma_commit(&bars.empty[0]);
-                next();
-            }
-            for (uint32_t i = 0; go && i < steps; i++) {
-                const uint32_t vst = st;
-                if (!mbar_wait_bounded(&bars.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&bars.full[st], ph, err)) break;
-                next();
-                const bool more = i + 1 < steps;
-                for (uint32_t t = 0; t < 2; t++) {
-                    if (!mbar_wait_bounded(&bars.p_full[t], i & 1, err)) {
-                        go = false;
-                        break;
-                    }
-                    tcgen_fence_after();
+                if (go && leader) {
+                    const uint32_t va = vd + vst * (S::kKV >> 4);
 #pragma unroll
-                    for (int k = 0; k < kBN / 16; k++)
-                        mma_ts(tmem + kColO + t * D, tmem + t * kBN + 8 * k,
-                               desc_columns(ra + vst * S::kKV + k * 2048, kBN * 128), kShapeO, i > 0 || k > 0);
-                    if (!more) {
-                        mma_commit(&bars.o_full[t]);
-                    } else {
-                        if (t == 0 && !mbar_wait_bounded(&bars.full[st], ph, err)) {
-                            go = false;
-                            break;
-                        }
-                        issue_s(t, st);
-                    }
+                    for (int k = half * kBN / 32; k < (half + 1) * kBN / 32; k++)
+                        mma_ts(tmem + 256 + t * D, tmem + t * kBN + 8 * k, desc(va, k * 2048), kShapeO, i > 0 || k > 0);
                 }
-                if (!go) break;
-                mma_commit(&bars.empty[vst]);
-                if (more) {
-                    mma_commit(&bars.empty[st]);
-                    next();
-                }
+                __syncwarp();
             }
-            uint32_t late = 0;
-            mma_commit(&bars.drained);
-            mbar_wait_bounded(&bars.drained, 0, &late);
-        } else if (warp >= 10) {
-            // Values of partly visible tiles: infinities and NaN become 0 here and are
-            // added to the rows that see them at the end.
-            for (uint32_t i = 0; i < steps; i++) {
-                const uint32_t n = 2 * i + 1, st = n % S::kStages, ph = (n / S::kStages) & 1;
-                if (!mbar_wait_bounded(&bars.full[st], ph, err)) break;
-                if (!whole_cta(slot0(i))) {
-                    bool found = false;
-                    uint4* tile = reinterpret_cast<uint4*>(ring + st * S::kKV);
-                    for (uint32_t x = tid - 320; x < S::kKV / 16; x += 64) {
-                        uint4 v = tile[x];
-                        const uint4 f = make_uint4(finite_or_zero<kHalf>(v.x), finite_or_zero<kHalf>(v.y), finite_or_zero<kHalf>(v.z),
-                                                   finite_or_zero<kHalf>(v.w));
-                        if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                            tile[x] = f;
-                            found = true;
-                        }
-                    }
-                    if (found) {
-                        bars.odd = 1;
-                        fence_async_proxy();
-                    }
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(&bars.ok[i & 7]);
+            if (!go) break;
+            if (!more) {
+                commit(&sh.o_full[t]);
+            } else {
+                if (t == 0) go = mbar_wait_bounded(&sh.full[st], ph, err);
+                tcgen_fence_after();
+                if (go) issue_s(t, st);
             }
         }
-    } else {
-        regs_inc<216>();
-        const uint32_t t = warp >> 2, r = tid & 127;
-        const uint32_t tok = t0 + t * p.tokens + r / p.group, g = r % p.group;
-        const bool valid = r < p.tokens * p.group && tok < a.q_tokens;
-        const int32_t pos = valid ? mask.pos(tok) : -1;
-        // Positions of this tile, for whole tiles of slots.
-        const uint32_t ta = t0 + t * p.tokens, tb = min(ta + p.tokens, a.q_tokens);
-        const int32_t q0 = mask.first + (int32_t)ta, q1 = mask.first + (int32_t)tb - 1;
-        const float scale = a.scale * kLog2e;
-        const uint32_t lanes = ((warp & 3) * 32) << 16;
-        const uint32_t sa = tmem + lanes + t * kBN, oa = tmem + lanes + kColO + t * D;
-        float m = -INFINITY, l = 0.0f;
-        bool go = true;
-        for (uint32_t i = 0; i < steps; i++) {
-            if (!mbar_wait_bounded(&bars.s_full[t], i & 1, err)) {
-                go = false;
-                break;
+        if (!go) break;
+        commit(&sh.empty[vst]);
+        if (more) {
+            commit(&sh.empty[st]);
+            next();
+        }
+    }
+    uint32_t late = 0;
+    __syncwarp();
+    commit(&sh.drained);
+    mbar_wait_bounded(&sh.drained, 0, &late);
+}
+
+// Values of partly visible tiles: infinities and NaN become 0 here and are added
+// to the rows that see them at the end.  E5M2 tiles are widened on the way.
+template <int D, bool kF8>
+__device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, const uint8_t* raw, uint32_t thread) {
+    using S = TilesShape<D, kF8>;
+    volatile uint32_t* err = &sh.err;
+    const uint32_t lane = thread & 31, steps = sh.steps;
+    StepSlots slots(sh);
+    const WholeTiles whole(sh, sh.p0, sh.p1);
+    if constexpr (kF8) {
+        uint32_t st = 0, ph = 0, rs = 0, rph = 0;
+        for (uint32_t n = 0; n < 2 * steps; n++) {
+            if (!mbar_wait_bounded(&sh.raw_full[rs], rph, err)) break;
+            if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], ph ^ 1, err)) break;
+            const bool part = (n & 1) && (sh.p0 < 0 || !whole(slots.s0));
+            bool found = false;
+            // 16 bytes of a row become two adjacent 16-byte chunks of the swizzled row.
+#pragma unroll 4
+            for (uint32_t x = thread; x < S::kRaw / 16; x += 64) {
+                const uint32_t r = x / (D / 16), c = x % (D / 16);
+                const uint4 v = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + 16 * x);
+                uint4 lo = make_uint4(e5m2_01(v.x), e5m2_23(v.x), e5m2_01(v.y), e5m2_23(v.y));
+                uint4 hi = make_uint4(e5m2_01(v.z), e5m2_23(v.z), e5m2_01(v.w), e5m2_23(v.w));
+                if (part) {
+                    const uint4 l = lo, u = hi;
+                    lo = make_uint4(finite_or_zero<true>(l.x), finite_or_zero<true>(l.y), finite_or_zero<true>(l.z), finite_or_zero<true>(l.w));
+                    hi = make_uint4(finite_or_zero<true>(u.x), finite_or_zero<true>(u.y), finite_or_zero<true>(u.z), finite_or_zero<true>(u.w));
+                    found |= l.x != lo.x || l.y != lo.y || l.z != lo.z || l.w != lo.w || u.x != hi.x || u.y != hi.y || u.z != hi.z || u.w != hi.w;
+                }
+                uint8_t* row = ring + st * S::kKV + (c >> 2) * (kBN * 128) + r * 128;
+                const uint32_t c0 = 2 * (c & 3);
+                *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
             }
-            tcgen_fence_after();
-            uint32_t s[4][32];
+            if (found) sh.odd = 1;
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.raw_empty[rs]);
+                mbar_arrive(&sh.full[st]);
+                if (n & 1) mbar_arrive(&sh.ok[(n >> 1) & 7]);
+            }
+            if (n & 1) slots.next();
+            if (++st == S::kStages) st = 0, ph ^= 1;
+            if (++rs == S::kRaws) rs = 0, rph ^= 1;
+        }
+    } else {
+        for (uint32_t i = 0; i < steps; i++, slots.next()) {
+            const uint32_t n = 2 * i + 1, st = n % S::kStages, ph = (n / S::kStages) & 1;
+            if (!mbar_wait_bounded(&sh.full[st], ph, err)) break;
+            if (sh.p0 < 0 || !whole(slots.s0)) {
+                bool found = false;
+                uint4* tile = reinterpret_cast<uint4*>(ring + st * S::kKV);
+#pragma unroll 4
+                for (uint32_t x = thread; x < S::kKV / 16; x += 64) {
+                    const uint4 v = tile[x];
+                    const uint4 f = make_uint4(finite_or_zero<false>(v.x), finite_or_zero<false>(v.y), finite_or_zero<false>(v.z),
+                                               finite_or_zero<false>(v.w));
+                    if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
+                        tile[x] = f;
+                        found = true;
+                    }
+                }
+                if (found) {
+                    sh.odd = 1;
+                    fence_async_proxy();
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&sh.ok[i & 7]);
+        }
+    }
+}
+
+// The rows' softmax.  Returns false where a wait gave up.
+template <int D, bool kF8>
+__device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t lane,
+                                             int32_t pos, float scale, float& m, float& l) {
+    volatile uint32_t* err = &sh.err;
+    const uint32_t sa = tmem + t * kBN, oa = tmem + 256 + t * D, steps = sh.steps;
+    StepSlots slots(sh);
+    // Positions of this tile's rows; none are whole if the tile has no queries.
+    const uint32_t ta = sh.t0 + t * p.tokens, tb = min(ta + p.tokens, p.a.q_tokens);
+    const int32_t q0 = sh.first + (int32_t)ta;
+    WholeTiles whole(sh, q0, sh.first + (int32_t)tb - 1);
+    if (ta >= p.a.q_tokens || q0 < 0) whole.upto = -1;
+    const int32_t sinks = sh.sinks;
+    const int64_t back = (int64_t)pos - (int64_t)sh.window + 1;
+    const int32_t lo = back < 0 ? 0 : (int32_t)back;
+    m = -INFINITY;
+    l = 0.0f;
+    for (uint32_t i = 0; i < steps; i++, slots.next()) {
+        if (!mbar_wait_bounded(&sh.s_full[t], i & 1, err)) return false;
+        tcgen_fence_after();
+        uint32_t s[4][32];
+        tmem_ld32(s[0], sa);
+        tmem_ld32(s[1], sa + 32);
+        const bool part = !whole(slots.s0);
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 4; c++) tmem_ld32(s[c], sa + 32 * c);
+        for (int half = 0; half < 2; half++) {
             tmem_wait_ld();
-            const int32_t s0 = slot0(i);
-            if (!(ta < a.q_tokens && q0 >= 0 && mask.all(q0, q1, s0, s0 + kBN - 1))) {
+            tmem_loaded(s[2 * half]);
+            tmem_loaded(s[2 * half + 1]);
+            if (half == 0) {  // on their way while the first half is looked at
+                tmem_ld32(s[2], sa + 64);
+                tmem_ld32(s[3], sa + 96);
+            }
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    const uint32_t seen = seen_bits(mask, pos, s0 + 32 * c);
+            for (int c = 2 * half; c < 2 * half + 2; c++) {
+                if (part) {
+                    const uint32_t seen = seen_bits(pos, lo, sinks, slots.s0 + 32 * c);
 #pragma unroll
                     for (int x = 0; x < 32; x++)
                         if (!(seen >> x & 1u)) s[c][x] = 0xFF800000u;
                 }
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 4; c++)
 #pragma unroll
                 for (int x = 0; x < 32; x += 2)
                     top[(x >> 1) & 3] = fmaxf(fmaxf(top[(x >> 1) & 3], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
-            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-            const bool raise = now > m + kLazy;  // from -inf too
-            if (__any_sync(0xFFFFFFFFu, raise)) {
-                const float f = raise ? exp2_approx(m - now) : 1.0f;
-                if (raise) m = now;
-                l *= f;
-                if (i) {
-                    const uint64_t ff = pair(f, f);
-#pragma unroll
-                    for (int c = 0; c < D / 32; c++) {
-                        uint32_t o[32];
-                        tmem_ld32(o, oa + 32 * c);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            float u, v;
-                            unpair(mul2(pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), ff), u, v);
-                            o[x] = __float_as_uint(u);
-                            o[x + 1] = __float_as_uint(v);
-                        }
-                        tmem_st32(oa + 32 * c, o);
-                    }
-                }
             }
-            const float use = m == -INFINITY ? 0.0f : m;
-            const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-                uint32_t w[32];
-#pragma unroll
-                for (int x = 0; x < 64; x += 2) {
-                    const uint32_t(&sx)[32] = s[c + (x >> 5)];
-                    float u, v;
-                    unpair(fma2(pair(__uint_as_float(sx[x & 31]), __uint_as_float(sx[(x & 31) + 1])), sc, neg), u, v);
-                    u = exp2_approx(u);
-                    v = exp2_approx(v);
-                    sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(u, v));
-                    // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
-                    w[x >> 1] = pack2<kHalf>(u, v);
-                }
-                tmem_st32(sa + 16 * c, w);
-            }
-            float u, v, u2, v2;
-            unpair(sum[0], u, v);
-            unpair(sum[1], u2, v2);
-            l += (u + v) + (u2 + v2);
-            tmem_wait_st();
-            tcgen_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_full[t]);
         }
-        if (steps && go) go = mbar_wait_bounded(&bars.o_full[t], 0, err);
-        tcgen_fence_after();
+        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        const bool raise = now > m + kLazy;  // from -inf too
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+            const float f = raise ? exp2_approx(m - now) : 1.0f;
+            if (raise) m = now;
+            l *= f;
+            if (i) {
+                const uint64_t ff = pair(f, f);
+#pragma unroll
+                for (int c = 0; c < D / 16; c++) {
+                    uint32_t o[16];
+                    tmem_ld16(o, oa + 16 * c);
+                    tmem_wait_ld();
+                    tmem_loaded(o);
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        float u, v;
+                        unpair(mul2(pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), ff), u, v);
+                        o[x] = __float_as_uint(u);
+                        o[x + 1] = __float_as_uint(v);
+                    }
+                    tmem_st16(oa + 16 * c, o);
+                }
+            }
+        }
+        const float use = m == -INFINITY ? 0.0f : m;
+        const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            uint32_t w[16];
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+                float u, v;
+                unpair(fma2(pair(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc, neg), u, v);
+                u = exp2_approx(u);
+                v = exp2_approx(v);
+                sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(u, v));
+                // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
+                w[x >> 1] = pack2<kF8>(u, v);
+            }
+            tmem_st16(sa + 16 * c, w);
+            if (c & 1) {
+                tmem_wait_st();
+                tcgen_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[t][c >> 1]);
+            }
+        }
+        float u, v, u2, v2;
+        unpair(sum[0], u, v);
+        unpair(sum[1], u2, v2);
+        l += (u + v) + (u2 + v2);
+    }
+    // Both tiles' products are done: a CTA's partial results take the tiles' place.
+    const bool go = steps == 0 || (mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
+    tcgen_fence_after();
+    return go;
+}
+
+// Columns 32 c .. 32 c + 31 of this row of O.
+template <int D, bool kF8>
+__device__ __forceinline__ void read_output(const TilesParams& p, const TilesShared& sh, uint32_t oa, int32_t pos, int c, float (&o)[32]) {
+    constexpr int kElem = kF8 ? 1 : 2;
+    const uint32_t steps = sh.steps;
+    uint32_t w[32];
+    __syncwarp();
+    if (steps) {
+        tmem_ld32(w, oa + 32 * c);
+        tmem_wait_ld();
+        tmem_loaded(w);
+    }
+#pragma unroll
+    for (int x = 0; x < 32; x++) o[x] = steps ? __uint_as_float(w[x]) : 0.0f;
+    if (*reinterpret_cast<const volatile uint32_t*>(&sh.odd)) {
+        // The infinite and NaN values of partly visible tiles go to the rows that
+        // see them: whatever their (positive) weight, the sum takes their value.
+        const WholeTiles whole(sh, sh.p0, sh.p1);
+        const int32_t n = sh.n, sinks = sh.sinks;
+        const uint32_t window = sh.window;
+        const uint8_t* vbase = static_cast<const uint8_t*>(p.a.v.data) + ((int64_t)sh.b * p.a.v.stride_b + (int64_t)sh.h * p.a.v.stride_h + 32 * c) * kElem;
+        StepSlots slots(sh);
+        for (uint32_t i = 0; i < steps; i++, slots.next()) {
+            if (sh.p0 >= 0 && whole(slots.s0)) continue;
+            for (int32_t s = slots.s0; s < min(slots.s0 + kBN, n); s++) {
+                if (!((uint32_t)(pos - s) < window || (s < sinks && s <= pos))) continue;
+                const uint8_t* row = vbase + s * p.a.v.stride_t * kElem;
+#pragma unroll
+                for (int x = 0; x < 32; x++) {
+                    const float v = kF8 ? __half2float(__ushort_as_half((unsigned short)(row[x] << 8)))
+                                        : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[x]);
+                    if (!isfinite(v)) o[x] += v;
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
+    using S = TilesShape<D, kF8>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ TilesShared sh;
+    uint8_t* qs = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* ring = qs + 2 * S::kQ;             // tiles of D / 64 blocks of 128 rows of 128 bytes, as qs
+    uint8_t* raw = ring + S::kStages * S::kKV;  // E5M2 tiles as they are
+    const uint32_t warp = threadIdx.x >> 5;
+
+    if (warp == 8) tmem_alloc<512>(&sh.tmem);
+    if (threadIdx.x == 0) {
+        const splitzip_attention_args& a = p.a;
+        // The last row tiles see the most slots: they go first.
+        const uint32_t unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
+        const uint32_t heads = a.batch * a.kv_heads, rc = p.row_ctas - 1 - unit / heads, bh = unit % heads;
+        const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+        const Mask mask(a, b);
+        const uint32_t t0 = rc * 2 * p.tokens, t1 = min(t0 + 2 * p.tokens, a.q_tokens);
+        sh.p0 = mask.first + (int32_t)t0;
+        sh.p1 = mask.first + (int32_t)t1 - 1;
+        const SlotTiles tiles(mask, sh.p0, sh.p1, kBN);
+        const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
+        sh.b = b;
+        sh.h = h;
+        sh.t0 = t0;
+        sh.steps = (uint32_t)((uint64_t)tiles.count * (split + 1) / p.splits) - j0;
+        sh.s0 = (int32_t)(tiles.tile(j0) * kBN);
+        sh.jump_at = j0 < tiles.head ? (int32_t)(tiles.head - j0) : -1;
+        sh.jump_to = (int32_t)(tiles.from * kBN);
+        sh.n = mask.n;
+        sh.first = mask.first;
+        sh.sinks = mask.sinks;
+        sh.window = mask.window;
+        for (int i = 0; i < 8; i++) {
+            mbar_init(&sh.full[i], kF8 ? 2 : 1);
+            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.ok[i], 2);
+        }
+        for (int i = 0; i < 3; i++) {
+            mbar_init(&sh.raw_full[i], 1);
+            mbar_init(&sh.raw_empty[i], 2);
+        }
+        mbar_init(&sh.q_full, kF8 ? 256 : 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i][0], 4);
+            mbar_init(&sh.p_full[i][1], 4);
+            mbar_init(&sh.o_full[i], 1);
+        }
+        mbar_init(&sh.drained, 1);
+        sh.err = sh.odd = 0;
+        fence_mbar_init();
+    }
+    if (!kF8 && threadIdx.x < 256) {
+        // Rows of a tile that hold no query (128 is not a multiple of every group).
+        const uint32_t r = threadIdx.x & 127;
+        if (r >= p.tokens * p.group) {
+#pragma unroll
+            for (int i = 0; i < D / 8; i++)
+                *reinterpret_cast<uint4*>(qs + (threadIdx.x >> 7) * S::kQ + (i >> 3) * (kTileM * 128) + r * 128 + 16 * (i & 7)) =
+                    make_uint4(0, 0, 0, 0);
+            fence_async_proxy();
+        }
+    }
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp >= 8) {
+        regs_dec<72>();
+        if (sh.steps) {
+            if (warp == 8) issue_products<D, kF8>(sh, tmem, qs, ring);
+            else if (warp >= 10) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - 320);
+            else if ((threadIdx.x & 31) == 0) load_tiles<D, kF8>(p, sh, qs, ring, raw);
+        }
         __syncwarp();
-        const bool sees = pos >= 0;
-        const uint32_t hq = h * p.group + g;
-        const bool alone = p.splits == 1;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)tok * a.out.stride_t +
-                             hq * a.out.stride_h;
-        float* part = p.partials + ((uint64_t)blockIdx.x * 256 + t * 128 + r) * (D + 4);
-        const bool odd = *reinterpret_cast<volatile uint32_t*>(&bars.odd);
-        const uint8_t* vbase = static_cast<const uint8_t*>(a.v.data) + (b * a.v.stride_b + h * a.v.stride_h) * 2;
-        const float inv = !go ? __int_as_float(0x7FC00000) : 1.0f / l;  // a wait that gave up: NaN
-#pragma unroll 1
-        for (int c = 0; c < D / 32; c++) {
-            uint32_t o[32];
-            __syncwarp();
-            if (steps) {
-                tmem_ld32(o, oa + 32 * c);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int x = 0; x < 32; x++) o[x] = 0;
-            }
-            if (odd) {
-                for (uint32_t i = 0; i < steps; i++) {
-                    const int32_t s0 = slot0(i);
-                    if (whole_cta(s0)) continue;
-                    for (int32_t s = s0; s < min(s0 + kBN, mask.n); s++) {
-                        if (!mask.sees(pos, s)) continue;
-                        const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(vbase + s * a.v.stride_t * 2) + 32 * c;
-#pragma unroll
-                        for (int x = 0; x < 32; x++) {
-                            const float v = __bfloat162float(row[x]);
-                            if (!isfinite(v)) o[x] = __float_as_uint(__uint_as_float(o[x]) + v);
-                        }
-                    }
-                }
-            }
-            if (valid && alone) {
-#pragma unroll
-                for (int x = 0; x < 32; x += 8) {
-                    uint4 w;
-                    uint32_t* ww = &w.x;
-#pragma unroll
-                    for (int y = 0; y < 4; y++)
-                        ww[y] = sees ? pack2<false>(__uint_as_float(o[x + 2 * y]) * inv, __uint_as_float(o[x + 2 * y + 1]) * inv) : 0u;
-                    *reinterpret_cast<uint4*>(out + 32 * c + x) = w;
-                }
-            } else if (valid) {
-#pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                    __stcg(reinterpret_cast<float4*>(part + 32 * c + x),
-                           make_float4(__uint_as_float(o[x]), __uint_as_float(o[x + 1]), __uint_as_float(o[x + 2]),
-                                       __uint_as_float(o[x + 3])));
-            }
+        if (p.splits > 1) {  // with the softmax warps below
+            cluster_sync();
+            cluster_sync();
         }
-        if (valid) {
-            if (!go) l = __int_as_float(0x7FC00000);
-            if (!alone)
-                __stcg(reinterpret_cast<float4*>(part + D), make_float4(m, l, 0.0f, 0.0f));
-            else if (a.lse)
-                a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + tok] = sees ? (m + log2f(l)) * kLn2 : -INFINITY;
+    } else {
+        regs_inc<216>();
+        const uint32_t t = warp >> 2, r = threadIdx.x & 127, lane = threadIdx.x & 31;
+        float m, l;
+        bool go;
+        {
+            const uint32_t tok = sh.t0 + t * p.tokens + r / p.group, g = r % p.group;
+            const bool valid = r < p.tokens * p.group && tok < p.a.q_tokens;
+            const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
+            float scale = p.a.scale * kLog2e;
+            if (kF8) {
+                // This thread's query row: FP16 of the row scaled by a power of two.
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const __nv_bfloat16*>(p.a.q.data) + (int64_t)sh.b * p.a.q.stride_b + (int64_t)tok * p.a.q.stride_t +
+                    (int64_t)(sh.h * p.group + g) * p.a.q.stride_h);
+                uint4 v[D / 8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; i++) {
+                    v[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int x = 0; x < 4; x++) top = max(top, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
+                }
+                const float power = row_power(top);
+                scale /= power;
+#pragma unroll
+                for (int i = 0; i < D / 8; i++) {
+                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+                        w[x] = pack2<true>(__uint_as_float(w[x] << 16) * power, __uint_as_float(w[x] & 0xFFFF0000u) * power);
+                    *reinterpret_cast<uint4*>(qs + t * S::kQ + (i >> 3) * (kTileM * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_async_proxy();
+                mbar_arrive(&sh.q_full);
+            }
+            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, lane, pos, scale, m, l);
+        }
+        if (threadIdx.x == 0 && !go) atomicOr(p.status, kStatusTimeout);
+        if (!go) l = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
+
+        // Derived again rather than kept through the loop.
+        const uint32_t rr = opaque(threadIdx.x) & 127;
+        const uint32_t tok = sh.t0 + t * p.tokens + rr / p.group, g = rr % p.group, hq = sh.h * p.group + g;
+        const bool valid = rr < p.tokens * p.group && tok < p.a.q_tokens;
+        const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
+        const uint32_t oa = tmem + (((warp & 3) * 32) << 16) + 256 + t * D;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out.data) + (int64_t)sh.b * p.a.out.stride_b +
+                             (int64_t)tok * p.a.out.stride_t + (int64_t)hq * p.a.out.stride_h;
+        float* lse = p.a.lse ? p.a.lse + ((uint64_t)sh.b * p.a.q_heads + hq) * p.a.q_tokens + tok : nullptr;
+        if (p.splits == 1) {
+            const float inv = 1.0f / l;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; c++) {
+                float o[32];
+                read_output<D, kF8>(p, sh, oa, pos, c, o);
+                if (valid) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8)
+                        *reinterpret_cast<uint4*>(out + 32 * c + x) =
+                            pos < 0 ? make_uint4(0, 0, 0, 0)
+                                    : make_uint4(pack2<false>(o[x] * inv, o[x + 1] * inv), pack2<false>(o[x + 2] * inv, o[x + 3] * inv),
+                                                 pack2<false>(o[x + 4] * inv, o[x + 5] * inv), pack2<false>(o[x + 6] * inv, o[x + 7] * inv));
+                }
+            }
+            if (valid && lse) *lse = pos < 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+            // Join the cluster's splits: every CTA leaves its rows in shared memory and
+            // joins a share of them, in the order of the splits.
+            float* rows = reinterpret_cast<float*>(qs);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; c++) {
+                float o[32];
+                read_output<D, kF8>(p, sh, oa, pos, c, o);
+                float4* to = reinterpret_cast<float4*>(rows + (t * kTileM + rr) * S::kRowFloats + 32 * c);
+#pragma unroll
+                for (int x = 0; x < 32; x += 4) to[x >> 2] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            }
+            rows[(t * kTileM + rr) * S::kRowFloats + D] = m;
+            rows[(t * kTileM + rr) * S::kRowFloats + D + 1] = l;
+            __syncwarp();
+            cluster_sync();
+            constexpr uint32_t kLanes = D / 4;  // threads to a row
+            const uint32_t rank = blockIdx.x % p.splits, c = 4 * (threadIdx.x % kLanes);
+            for (uint32_t x = threadIdx.x / kLanes * p.splits + rank; x < 2 * kTileM; x += 256 / kLanes * p.splits) {
+                const uint32_t xr = x & 127, xt = sh.t0 + (x >> 7) * p.tokens + xr / p.group, xh = sh.h * p.group + xr % p.group;
+                if (xr >= p.tokens * p.group || xt >= p.a.q_tokens) continue;
+                const uint32_t at = smem_addr(rows + x * S::kRowFloats);
+                float mm = -INFINITY, ll = 0.0f;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (uint32_t i = 0; i < p.splits; i++) {
+                    const float mi = cluster_ld(at + 4 * D, i), li = cluster_ld(at + 4 * D + 4, i);
+                    const float4 y = cluster_ld4(at + 4 * c, i);
+                    const float top = fmaxf(mm, mi), base = top == -INFINITY ? 0.0f : top;
+                    const float f = exp2_approx(mm - base), gi = exp2_approx(mi - base);
+                    ll = fmaf(ll, f, li * gi);
+                    v = make_float4(fmaf(v.x, f, y.x * gi), fmaf(v.y, f, y.y * gi), fmaf(v.z, f, y.z * gi), fmaf(v.w, f, y.w * gi));
+                    mm = top;
+                }
+                const bool sees = sh.first + (int32_t)xt >= 0;
+                const float inv = 1.0f / ll;
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.a.out.data) + (int64_t)sh.b * p.a.out.stride_b +
+                                    (int64_t)xt * p.a.out.stride_t + (int64_t)xh * p.a.out.stride_h;
+                *reinterpret_cast<uint2*>(to + c) =
+                    sees ? make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+                if (c == 0 && p.a.lse)
+                    p.a.lse[((uint64_t)sh.b * p.a.q_heads + xh) * p.a.q_tokens + xt] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            }
+            __syncwarp();
+            cluster_sync();  // this CTA's rows have been read
         }
         tcgen_fence_before();
-        if (tid == 0 && !go) atomicOr(p.status, kStatusTimeout);
-        if (p.splits > 1) {
-            // Join the splits: the CTA that comes last, in the order of the splits.
-            __threadfence();
-            named_sync(1, 256);
-            if (tid == 0) {
-                bars.last = atomicAdd(p.counters + unit, 1u) == p.splits - 1;
-                if (bars.last) p.counters[unit] = 0;  // ready for the next call
-            }
-            named_sync(1, 256);
-            if (bars.last) {
-                __threadfence();
-            constexpr uint32_t kLanes = D / 4;  // threads to a row
-            const float* all = p.partials + (uint64_t)unit * p.splits * 256 * (D + 4);
-            for (uint32_t r = tid / kLanes; r < 256; r += 256 / kLanes) {
-                const uint32_t rr = r & 127, rtok = t0 + (r >> 7) * p.tokens + rr / p.group, rg = rr % p.group;
-                if (rr >= p.tokens * p.group || rtok >= a.q_tokens) continue;
-                const uint32_t c = 4 * (tid % kLanes);
-                float mm = -INFINITY;
-                for (uint32_t i = 0; i < p.splits; i++) mm = fmaxf(mm, __ldcg(all + ((uint64_t)i * 256 + r) * (D + 4) + D));
-                const float base = mm == -INFINITY ? 0.0f : mm;
-                float ll = 0.0f;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (uint32_t i = 0; i < p.splits; i++) {
-                    const float* q = all + ((uint64_t)i * 256 + r) * (D + 4);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + D));
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(q + c));
-                    const float f = exp2_approx(ml.x - base);
-                    ll = fmaf(f, ml.y, ll);
-                    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-                }
-                const bool seen = mask.pos(rtok) >= 0;
-                const float rl = 1.0f / ll;
-                const uint32_t rh = h * p.group + rg;
-                __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)rtok * a.out.stride_t +
-                                     rh * a.out.stride_h;
-                const uint2 w = make_uint2(pack2<false>(o.x * rl, o.y * rl), pack2<false>(o.z * rl, o.w * rl));
-                *reinterpret_cast<uint2*>(row + c) = seen ? w : make_uint2(0, 0);
-                if (c == 0 && a.lse) a.lse[((uint64_t)b * a.q_heads + rh) * a.q_tokens + rtok] = seen ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-            }
-            }
-        }
     }
     __syncthreads();
     tcgen_fence_after();
     if (warp == 8) tmem_free<512>(tmem);
 }
 
-template <int D>
+template <int D, bool kF8>
 cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
+    constexpr int kSmem = TilesShape<D, kF8>::kSmem;
     Wave w;
-    const cudaError_t e = launch_wave<tiles_kernel<D, false>>(kThreadsTiles, TilesShape<D>::kSmem, w);
+    const cudaError_t e = launch_wave<tiles_kernel<D, kF8>>(kThreadsTiles, kSmem, w);
     if (e != cudaSuccess) return e;
-    tiles_kernel<D, false><<<ctas, kThreadsTiles, TilesShape<D>::kSmem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreadsTiles);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kF8>, p);
 }
 
 }  // namespace
@@ -470,16 +684,24 @@ bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     uint64_t most = (a.kv_tokens + kBN - 1) / kBN;
     if (a.window)
         most = std::min(most, ((uint64_t)a.window + 2 * tokens + kBN - 1) / kBN + 1 + ((uint64_t)a.sinks + kBN - 1) / kBN);
-    // Fill the GPU with one CTA per SM if each split still has four steps.
-    const uint64_t splits = std::min((uint64_t)kSms / units, most / 4);
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
-    if (units * p.splits > 0x7FFFFFFFull) return false;
-    p.bytes = kAttentionHeader + (p.splits > 1 ? units * p.splits * 256 * (a.head_dim + 4) * 4 : 0);
-    return true;
+    // The splits (one cluster) with the least time, as waves of one CTA per SM times
+    // the steps of a split plus kSplitCost steps for a CTA's start, join and end.
+    constexpr uint64_t kSplitCost = 4;
+    uint64_t best = ~0ull;
+    p.splits = 1;
+    for (uint64_t n = 1; n <= 8 && (n == 1 || 2 * n <= most); n++) {
+        const uint64_t time = (units * n + kSms - 1) / kSms * ((most + n - 1) / n + kSplitCost);
+        if (time < best) {
+            best = time;
+            p.splits = (uint32_t)n;
+        }
+    }
+    p.bytes = kAttentionHeader;
+    return units * p.splits <= 0x7FFFFFFFull;
 }
 
 bool attention_tiles_usable(const splitzip_attention_args& a) {
-    return a.scale > 0.0f && a.cache_format == SPLITZIP_FORMAT_BF16;  // maxima are taken before scaling
+    return a.scale > 0.0f;  // maxima are taken before scaling
 }
 
 cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
@@ -490,16 +712,16 @@ cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const Atten
     p.tokens = kTileM / p.group;
     p.row_ctas = plan.row_tiles;
     p.splits = plan.splits;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.counters = reinterpret_cast<uint32_t*>(ws);
-    p.status = reinterpret_cast<uint32_t*>(ws + kAttentionStatus);
-    p.partials = reinterpret_cast<float*>(ws + kAttentionHeader);
-    if (!make_map(p.qmap, a.q, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q) ||
-        !make_map(p.kmap, a.k, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_k) ||
-        !make_map(p.vmap, a.v, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_v))
+    p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
+    const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
+    p.one_q = 1;
+    if ((!f8 && !make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q)) ||
+        !make_map(p.kmap, a.k, f8 ? 1 : 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_k) ||
+        !make_map(p.vmap, a.v, f8 ? 1 : 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_v))
         return cudaErrorInvalidValue;
     const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
-    return a.head_dim == 64 ? launch<64>(p, ctas, s) : launch<128>(p, ctas, s);
+    if (a.head_dim == 64) return f8 ? launch<64, true>(p, ctas, s) : launch<64, false>(p, ctas, s);
+    return f8 ? launch<128, true>(p, ctas, s) : launch<128, false>(p, ctas, s);
 }
 
 }  // namespace splitzip

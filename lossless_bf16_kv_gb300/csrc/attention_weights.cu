@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(kThreadsWeights, 2) weights_kernel(const __gri
                 mbar_wait_bounded(&sh.q_full[x % kQStages], (x / kQStages) & 1, &late);
         }
     } else if (warp == 8) {
-        if (lane == 0 && steps) {  // matrix products
-            const uint32_t ka = smem_addr(ks), qa = smem_addr(ring);
+        if (steps) {  // matrix products: the whole warp waits, one lane issues
+            const bool leader = elect_one();
+            const uint32_t ka = desc_rows(smem_addr(ks)), qa = desc_rows(smem_addr(ring));
             bool go = kF8 || mbar_wait_bounded(&sh.k_full, 0, err);
             for (uint32_t i = 0; go && i < steps; i++) {
                 const uint32_t st = i % kQStages, x = i & 1;
@@ -164,16 +165,20 @@ __global__ void __launch_bounds__(kThreadsWeights, 2) weights_kernel(const __gri
                 // As many columns as the tile has rows, in steps of 16.
                 const uint32_t shape = mma_shape(false, (rows_of(i) + 15) & ~15u, false);
                 tcgen_fence_after();
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint32_t at = (k >> 2) * (kSlotTile * 128) + (k & 3) * 32;
-                    mma_ss(tmem + x * kRowTile, desc_rows(ka + at), desc_rows(qa + st * S::kTile + at), shape, k > 0);
+                    for (int k = 0; k < D / 16; k++) {
+                        const uint32_t at = (k >> 2) * (kSlotTile * 128) + (k & 3) * 32;
+                        mma_ss(tmem + x * kRowTile, desc(ka, at), desc(qa + st * (S::kTile >> 4), at), shape, k > 0);
+                    }
+                    mma_commit(&sh.s_full[x]);
+                    mma_commit(&sh.q_empty[st]);
                 }
-                mma_commit(&sh.s_full[x]);
-                mma_commit(&sh.q_empty[st]);
+                __syncwarp();  // no lane falls a phase behind
             }
             uint32_t late = 0;
-            mma_commit(&sh.drained);
+            __syncwarp();
+            if (leader) mma_commit(&sh.drained);
             mbar_wait_bounded(&sh.drained, 0, &late);
         }
     } else if (warp >= 10) {
@@ -218,6 +223,8 @@ __global__ void __launch_bounds__(kThreadsWeights, 2) weights_kernel(const __gri
             tmem_ld32(s[1], sa + x * kRowTile + 32);
             const bool whole = i >= whole_lo && i < whole_hi;
             tmem_wait_ld();
+            tmem_loaded(s[0]);
+            tmem_loaded(s[1]);
             uint64_t part[2] = {0, 0};
 #pragma unroll
             for (int c = 0; c < 2; c++) {
@@ -291,9 +298,9 @@ cudaError_t launch_attention_weights(const splitzip_attention_args& a, const flo
     p.tokens = kRowTile / p.group;
     p.slot_ctas = (a.kv_tokens + kSlotTile - 1) / kSlotTile;
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
-    if (!make_map(p.qmap, a.q, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q))
+    if (!make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q))
         return cudaErrorInvalidValue;
-    if (!f8 && !make_map(p.kmap, a.k, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kSlotTile, false, &p.one_k))
+    if (!f8 && !make_map(p.kmap, a.k, 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kSlotTile, false, &p.one_k))
         return cudaErrorInvalidValue;
     const uint32_t ctas = a.batch * a.kv_heads * p.slot_ctas;
     if (a.head_dim == 64) return f8 ? launch<64, true>(p, ctas, s) : launch<64, false>(p, ctas, s);

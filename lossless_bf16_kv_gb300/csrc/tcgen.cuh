@@ -56,6 +56,13 @@ __device__ __forceinline__ void tmem_free(uint32_t addr) {
 __device__ __forceinline__ void tcgen_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tcgen_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Loaded registers hold their values only after the wait: arithmetic on them
+// must not be moved before it.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of this warp's 32 lanes: register i = column i of the lane.
@@ -70,32 +77,48 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
-        "%29,%30,%31};" ::"r"(r[0]),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
         : "memory");
 }
 
 // ------------------------------------------------------ matrix products
 
-// Shared-memory operand of 16-bit values in 128-byte swizzled rows (1024-byte
-// aligned blocks of 8 rows).  Contraction-major (a row holds 64 contraction
-// values): groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operands of 16-bit values in 128-byte swizzled rows (1024-byte
+// aligned blocks of 8 rows).  A descriptor has 14 bits of an address within the
+// CTA's shared memory, in 16 bytes (in a cluster an address has the CTA's rank
+// above bit 18: it must not reach the fields above), so one `bytes` further on
+// differs in its low word alone.
+//
+// Contraction-major (a row holds 64 contraction values): groups of 8 rows 1024
+// bytes apart.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc(uint32_t low, uint32_t bytes) {
+    return (uint64_t)kDescHigh << 32 | (low + (bytes >> 4));
 }
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 // The other way round (a row is one contraction index and holds 64 output
 // columns): groups of 8 contraction indices 1024 bytes apart, blocks of 64
 // columns `block` bytes apart.
-__device__ __forceinline__ uint64_t desc_columns(uint32_t addr, uint32_t block) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
+__device__ __forceinline__ uint32_t desc_columns(uint32_t addr, uint32_t block) {
+    return ((addr & 0x3FFFFu) >> 4) | ((block >> 4) << 16);
+}
+
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 // kind::f16 with 32-bit sums: operand type (BF16 or FP16, both the same), M =
 // 128, N, and whether the second operand is stored columns-first.
@@ -133,8 +156,9 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {  // the compiler cannot tell where the value is from
+    asm volatile("" : "+r"(v));
+    return v;
 }
 // Shared-memory writes of this thread become visible to tensor cores and TMA.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
