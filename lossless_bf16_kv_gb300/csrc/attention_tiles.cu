@@ -10,18 +10,21 @@
 // where the second product takes it as its first operand.  The two tiles
 // alternate: while one tile's warps do its softmax, the tensor cores run the
 // other's O += P V and next S = Q K^T.  Per tile and step the two products take
-// 2 x 512 cycles at head_dim 128, the 128 x 128 exponentials 512.
+// 2 x 512 cycles at head_dim 128, the 128 x 128 exponentials 512; a tile's next
+// S has to wait for its P (which lies over S), so the softmax's latency must
+// stay near the 1024 cycles of the other tile's products.  Hence two threads to
+// a row, 64 slots each, that exchange their maxima through shared memory.
 //
-// Roles: warps 0-3 and 4-7 softmax (one thread per row, so row statistics need
-// no exchange), 8 issues the products, 9 the TMA loads, 10 and 11 keep
-// infinities and NaN of partly visible tiles out of the second product (0 x
-// infinity is not 0) and, for an E5M2 cache, widen its tiles to FP16 (exact: an
-// E5M2 value is the upper byte of the FP16 value it stands for).  The queries
-// are then FP16 too, each row scaled by a power of two.
+// Roles: warps 0-15 softmax (four per tile and half of the slots), 16 issues
+// the products, 17 the TMA loads, 18 and 19 keep infinities and NaN of partly
+// visible tiles out of the second product (0 x infinity is not 0) and, for an
+// E5M2 cache, widen its tiles to FP16 (exact: an E5M2 value is the upper byte of
+// the FP16 value it stands for).  The queries are then FP16 too, each row scaled
+// by a power of two.
 //
 // What the roles share sits in shared memory and is read from there: a softmax
-// thread's 168 to 216 registers hold a row of scores and little else, and a
-// value spilled there costs hundreds of cycles in every step.
+// thread's 104 registers hold 64 scores and little else, and a value spilled
+// there costs hundreds of cycles in every step.
 //
 // The running maximum is only raised when a row's maximum grows by more than
 // 2^8 (in which case O and l are rescaled by the softmax warps, after the
@@ -38,7 +41,7 @@ namespace {
 
 constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
-constexpr int kThreadsTiles = 384;
+constexpr int kThreadsTiles = 640, kSoftmax = 512;
 constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
 
 template <int D, bool kF8>
@@ -50,7 +53,6 @@ struct TilesShape {
     static constexpr int kRaws = kF8 ? 3 : 0;
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
     static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * kRaw;
-    static constexpr int kSmem = kUsed + 1024;
     static_assert(kUsed >= 2 * kTileM * kRowFloats * 4, "partial results take the place of the tiles");
 };
 
@@ -68,7 +70,7 @@ struct TilesShared {
     uint64_t ok[8];              // step i mod 8: its values are fit for the product
     uint64_t raw_full[3], raw_empty[3];  // E5M2 tiles
     uint64_t q_full;
-    uint64_t s_full[2], p_full[2][2], o_full[2], drained;  // of the query tiles; P by halves of the slots
+    uint64_t s_full[2], p_full[2], o_full[2], drained;  // of the query tiles
     uint32_t tmem, err, odd;
     // This CTA's work: sequence, head, first query token; the first slot of step
     // 0, the step that jumps from the sinks to the window and to where.
@@ -76,6 +78,10 @@ struct TilesShared {
     int32_t s0, jump_at, jump_to;
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
+    int32_t upto[2], after[2], whole_sinks;  // WholeTiles of the query tiles
+    // Exchanged by the two threads of a row.  A step's S is only there once every
+    // warp of the tile has handed over the last step's P, so one value does.
+    float row[2][2][kTileM];
 };
 
 // The first slot of each step in turn.
@@ -158,75 +164,75 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
     const bool leader = elect_one();
     const uint32_t steps = sh.steps;
     const uint32_t qd = desc_rows(smem_addr(qs)), kd = desc_rows(smem_addr(ring)), vd = desc_columns(smem_addr(ring), kBN * 128);
-    // S of query tile t from the keys in ring stage st.
+    // One lane issues, in straight runs: S of query tile t from the keys in stage
+    // st, and O += P V with the values in stage st.
     auto issue_s = [&](uint32_t t, uint32_t st) {
-        if (leader) {
-            const uint32_t qa = qd + t * (S::kQ >> 4), ka = kd + st * (S::kKV >> 4);
+        const uint32_t qa = qd + t * (S::kQ >> 4), ka = kd + st * (S::kKV >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-                const uint32_t at = (k >> 2) * (kBN * 128) + (k & 3) * 32;
-                mma_ss(tmem + t * kBN, desc(qa, at), desc(ka, at), kShapeS, k > 0);
-            }
-            mma_commit(&sh.s_full[t]);
+        for (int k = 0; k < D / 16; k++) {
+            const uint32_t at = (k >> 2) * (kBN * 128) + (k & 3) * 32;
+            mma_ss(tmem + t * kBN, desc(qa, at), desc(ka, at), kShapeS, k > 0);
         }
-        __syncwarp();
+        mma_commit(&sh.s_full[t]);
     };
-    auto commit = [&](uint64_t* bar) {
-        if (leader) mma_commit(bar);
-        __syncwarp();
+    auto issue_o = [&](uint32_t t, uint32_t st, bool add) {
+        const uint32_t va = vd + st * (S::kKV >> 4);
+        mma_ts(tmem + 256 + t * D, tmem + t * kBN, desc(va, 0), kShapeO, add);
+#pragma unroll
+        for (int k = 1; k < kBN / 16; k++) mma_ts(tmem + 256 + t * D, tmem + t * kBN + 8 * k, desc(va, k * 2048), kShapeO, true);
     };
     uint32_t st = 0, ph = 0;
     auto next = [&]() {
         if (++st == S::kStages) st = 0, ph ^= 1;
     };
-    bool go = mbar_wait_bounded(&sh.q_full, 0, err) && mbar_wait_bounded(&sh.full[0], 0, err);
-    if (go) {
+    const auto run = [&]() {
+        if (!mbar_wait_bounded(&sh.q_full, 0, err) || !mbar_wait_bounded(&sh.full[0], 0, err)) return;
         tcgen_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
-        commit(&sh.empty[0]);
+        if (leader) {
+            issue_s(0, 0);
+            issue_s(1, 0);
+            mma_commit(&sh.empty[0]);
+        }
         next();
-    }
-    for (uint32_t i = 0; go && i < steps; i++) {
-        const uint32_t vst = st;
-        go = mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) && mbar_wait_bounded(&sh.full[st], ph, err);
-        if (!go) break;
-        next();
-        const bool more = i + 1 < steps;
+        for (uint32_t i = 0; i + 1 < steps; i++) {
+            const uint32_t vst = st, vph = ph;
+            next();
+            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err) ||
+                !mbar_wait_bounded(&sh.full[st], ph, err))
+                return;
 #pragma unroll
-        for (uint32_t t = 0; t < 2; t++) {
-            // The first half of the slots' P is ready while the second is still being made.
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                if (go) go = mbar_wait_bounded(&sh.p_full[t][half], i & 1, err);
+            for (uint32_t t = 0; t < 2; t++) {
+                if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
                 tcgen_fence_after();
-                if (go && leader) {
-                    const uint32_t va = vd + vst * (S::kKV >> 4);
-#pragma unroll
-                    for (int k = half * kBN / 32; k < (half + 1) * kBN / 32; k++)
-                        mma_ts(tmem + 256 + t * D, tmem + t * kBN + 8 * k, desc(va, k * 2048), kShapeO, i > 0 || k > 0);
+                if (leader) {
+                    issue_o(t, vst, i > 0);
+                    issue_s(t, st);
+                    if (t) {
+                        mma_commit(&sh.empty[vst]);
+                        mma_commit(&sh.empty[st]);
+                    }
                 }
                 __syncwarp();
             }
-            if (!go) break;
-            if (!more) {
-                commit(&sh.o_full[t]);
-            } else {
-                if (t == 0) go = mbar_wait_bounded(&sh.full[st], ph, err);
-                tcgen_fence_after();
-                if (go) issue_s(t, st);
-            }
-        }
-        if (!go) break;
-        commit(&sh.empty[vst]);
-        if (more) {
-            commit(&sh.empty[st]);
             next();
         }
-    }
+        const uint32_t i = steps - 1;
+        if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[st], ph, err)) return;
+#pragma unroll
+        for (uint32_t t = 0; t < 2; t++) {
+            if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
+            tcgen_fence_after();
+            if (leader) {
+                issue_o(t, st, i > 0);
+                mma_commit(&sh.o_full[t]);
+            }
+            __syncwarp();
+        }
+    };
+    run();
     uint32_t late = 0;
     __syncwarp();
-    commit(&sh.drained);
+    if (leader) mma_commit(&sh.drained);
     mbar_wait_bounded(&sh.drained, 0, &late);
 }
 
@@ -304,75 +310,69 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
     }
 }
 
-// The rows' softmax.  Returns false where a wait gave up.
+// The rows' softmax, slots 64 half .. 64 half + 63 of each step.  l is this
+// half's sum.  Returns false where a wait gave up.
 template <int D, bool kF8>
-__device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t lane,
-                                             int32_t pos, float scale, float& m, float& l) {
+__device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
+                                             uint32_t r, int32_t pos, float scale, float& m, float& l) {
     volatile uint32_t* err = &sh.err;
-    const uint32_t sa = tmem + t * kBN, oa = tmem + 256 + t * D, steps = sh.steps;
-    StepSlots slots(sh);
-    // Positions of this tile's rows; none are whole if the tile has no queries.
-    const uint32_t ta = sh.t0 + t * p.tokens, tb = min(ta + p.tokens, p.a.q_tokens);
-    const int32_t q0 = sh.first + (int32_t)ta;
-    WholeTiles whole(sh, q0, sh.first + (int32_t)tb - 1);
-    if (ta >= p.a.q_tokens || q0 < 0) whole.upto = -1;
-    const int32_t sinks = sh.sinks;
-    const int64_t back = (int64_t)pos - (int64_t)sh.window + 1;
-    const int32_t lo = back < 0 ? 0 : (int32_t)back;
+    const uint32_t sa = tmem + t * kBN, oa = tmem + 256 + t * D + half * (D / 2);
+    // What a step needs only a moment is read again from shared memory, as volatile.
+    const volatile TilesShared& now_sh = sh;
+    int32_t s0 = sh.s0;
     m = -INFINITY;
     l = 0.0f;
-    for (uint32_t i = 0; i < steps; i++, slots.next()) {
-        if (!mbar_wait_bounded(&sh.s_full[t], i & 1, err)) return false;
+    for (uint32_t i = 0; i < now_sh.steps; i++) {
+        const bool ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err);
         tcgen_fence_after();
-        uint32_t s[4][32];
-        tmem_ld32(s[0], sa);
-        tmem_ld32(s[1], sa + 32);
-        const bool part = !whole(slots.s0);
+        uint32_t s[2][32];
+        tmem_ld32(s[0], sa + 64 * half);
+        tmem_ld32(s[1], sa + 64 * half + 32);
+        const bool part = !(s0 <= now_sh.upto[t] && (s0 > now_sh.after[t] || s0 <= now_sh.whole_sinks));
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_wait_ld();
+        tmem_loaded(s[0]);
+        tmem_loaded(s[1]);
 #pragma unroll
-        for (int half = 0; half < 2; half++) {
-            tmem_wait_ld();
-            tmem_loaded(s[2 * half]);
-            tmem_loaded(s[2 * half + 1]);
-            if (half == 0) {  // on their way while the first half is looked at
-                tmem_ld32(s[2], sa + 64);
-                tmem_ld32(s[3], sa + 96);
+        for (int c = 0; c < 2; c++) {
+            if (part) {
+                const int64_t back = (int64_t)pos - (int64_t)now_sh.window + 1;
+                const uint32_t seen = seen_bits(pos, back < 0 ? 0 : (int32_t)back, now_sh.sinks, s0 + 64 * (int32_t)half + 32 * c);
+#pragma unroll
+                for (int x = 0; x < 32; x++)
+                    if (!(seen >> x & 1u)) s[c][x] = 0xFF800000u;
             }
 #pragma unroll
-            for (int c = 2 * half; c < 2 * half + 2; c++) {
-                if (part) {
-                    const uint32_t seen = seen_bits(pos, lo, sinks, slots.s0 + 32 * c);
-#pragma unroll
-                    for (int x = 0; x < 32; x++)
-                        if (!(seen >> x & 1u)) s[c][x] = 0xFF800000u;
-                }
-#pragma unroll
-                for (int x = 0; x < 32; x += 2)
-                    top[(x >> 1) & 3] = fmaxf(fmaxf(top[(x >> 1) & 3], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
-            }
+            for (int x = 0; x < 32; x += 2)
+                top[(x >> 1) & 3] = fmaxf(fmaxf(top[(x >> 1) & 3], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
         }
-        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        sh.row[t][half][r] = own;
+        // All 256 threads of the tile also have their scores in registers after
+        // this, so P may go over S.  Where one's wait gave up, all return.
+        if (named_any(1 + t, 256, !ready)) return false;
+        const float now = fmaxf(own, sh.row[t][half ^ 1][r]);
         const bool raise = now > m + kLazy;  // from -inf too
         if (__any_sync(0xFFFFFFFFu, raise)) {
             const float f = raise ? exp2_approx(m - now) : 1.0f;
             if (raise) m = now;
             l *= f;
-            if (i) {
+            if (i) {  // this half's columns of O
                 const uint64_t ff = pair(f, f);
 #pragma unroll
                 for (int c = 0; c < D / 16; c++) {
-                    uint32_t o[16];
-                    tmem_ld16(o, oa + 16 * c);
+                    uint32_t o[8];
+                    tmem_ld8(o, oa + 8 * c);
                     tmem_wait_ld();
                     tmem_loaded(o);
 #pragma unroll
-                    for (int x = 0; x < 16; x += 2) {
+                    for (int x = 0; x < 8; x += 2) {
                         float u, v;
                         unpair(mul2(pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), ff), u, v);
                         o[x] = __float_as_uint(u);
                         o[x + 1] = __float_as_uint(v);
                     }
-                    tmem_st16(oa + 16 * c, o);
+                    tmem_st8(oa + 8 * c, o);
                 }
             }
         }
@@ -380,7 +380,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
+        for (int c = 0; c < 2; c++) {
             uint32_t w[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
@@ -392,21 +392,20 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                 // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
                 w[x >> 1] = pack2<kF8>(u, v);
             }
-            tmem_st16(sa + 16 * c, w);
-            if (c & 1) {
-                tmem_wait_st();
-                tcgen_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[t][c >> 1]);
-            }
+            tmem_st16(sa + 32 * half + 16 * c, w);
         }
         float u, v, u2, v2;
         unpair(sum[0], u, v);
         unpair(sum[1], u2, v2);
         l += (u + v) + (u2 + v2);
+        tmem_wait_st();
+        tcgen_fence_before();
+        __syncwarp();
+        if ((r & 31) == 0) mbar_arrive(&sh.p_full[t]);
+        s0 = (int32_t)i + 1 == now_sh.jump_at ? now_sh.jump_to : s0 + kBN;
     }
     // Both tiles' products are done: a CTA's partial results take the tiles' place.
-    const bool go = steps == 0 || (mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
+    const bool go = sh.steps == 0 || (mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
     tcgen_fence_after();
     return go;
 }
@@ -452,14 +451,13 @@ __device__ __forceinline__ void read_output(const TilesParams& p, const TilesSha
 template <int D, bool kF8>
 __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
     using S = TilesShape<D, kF8>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ TilesShared sh;
-    uint8_t* qs = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t qs[];
+    TilesShared& sh = *reinterpret_cast<TilesShared*>(qs + S::kUsed);
     uint8_t* ring = qs + 2 * S::kQ;             // tiles of D / 64 blocks of 128 rows of 128 bytes, as qs
     uint8_t* raw = ring + S::kStages * S::kKV;  // E5M2 tiles as they are
     const uint32_t warp = threadIdx.x >> 5;
 
-    if (warp == 8) tmem_alloc<512>(&sh.tmem);
+    if (warp == 16) tmem_alloc<512>(&sh.tmem);
     if (threadIdx.x == 0) {
         const splitzip_attention_args& a = p.a;
         // The last row tiles see the most slots: they go first.
@@ -483,6 +481,14 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         sh.first = mask.first;
         sh.sinks = mask.sinks;
         sh.window = mask.window;
+        for (int t = 0; t < 2; t++) {
+            // No tile of slots is whole for a tile without queries.
+            const uint32_t ta = t0 + t * p.tokens, tb = min(ta + p.tokens, a.q_tokens);
+            const WholeTiles whole(sh, mask.first + (int32_t)ta, mask.first + (int32_t)tb - 1);
+            sh.upto[t] = ta < a.q_tokens ? whole.upto : -1;
+            sh.after[t] = whole.after;
+            sh.whole_sinks = whole.sinks;
+        }
         for (int i = 0; i < 8; i++) {
             mbar_init(&sh.full[i], kF8 ? 2 : 1);
             mbar_init(&sh.empty[i], 1);
@@ -492,11 +498,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_empty[i], 2);
         }
-        mbar_init(&sh.q_full, kF8 ? 256 : 1);
+        mbar_init(&sh.q_full, kF8 ? kSoftmax : 1);
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i][0], 4);
-            mbar_init(&sh.p_full[i][1], 4);
+            mbar_init(&sh.p_full[i], 8);
             mbar_init(&sh.o_full[i], 1);
         }
         mbar_init(&sh.drained, 1);
@@ -519,11 +524,11 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     tcgen_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    if (warp >= 8) {
-        regs_dec<72>();
+    if (warp >= 16) {
+        regs_dec<64>();
         if (sh.steps) {
-            if (warp == 8) issue_products<D, kF8>(sh, tmem, qs, ring);
-            else if (warp >= 10) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - 320);
+            if (warp == 16) issue_products<D, kF8>(sh, tmem, qs, ring);
+            else if (warp >= 18) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - 576);
             else if ((threadIdx.x & 31) == 0) load_tiles<D, kF8>(p, sh, qs, ring, raw);
         }
         __syncwarp();
@@ -532,8 +537,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             cluster_sync();
         }
     } else {
-        regs_inc<216>();
-        const uint32_t t = warp >> 2, r = threadIdx.x & 127, lane = threadIdx.x & 31;
+        regs_inc<104>();
+        const uint32_t t = (warp >> 2) & 1, half = warp >> 3, r = threadIdx.x & 127;
         float m, l;
         bool go;
         {
@@ -542,35 +547,43 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
             float scale = p.a.scale * kLog2e;
             if (kF8) {
-                // This thread's query row: FP16 of the row scaled by a power of two.
+                // This thread's half of its query row: FP16 of the row scaled by a power of two.
                 const uint4* src = reinterpret_cast<const uint4*>(
                     static_cast<const __nv_bfloat16*>(p.a.q.data) + (int64_t)sh.b * p.a.q.stride_b + (int64_t)tok * p.a.q.stride_t +
-                    (int64_t)(sh.h * p.group + g) * p.a.q.stride_h);
-                uint4 v[D / 8];
+                    (int64_t)(sh.h * p.group + g) * p.a.q.stride_h) + half * (D / 16);
+                uint4 v[D / 16];
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < D / 8; i++) {
+                for (int i = 0; i < D / 16; i++) {
                     v[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                     for (int x = 0; x < 4; x++) top = max(top, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
                 }
-                const float power = row_power(top);
+                sh.row[t][half][r] = __uint_as_float(top);
+                named_sync(1 + t, 256);
+                const float power = row_power(max(top, __float_as_uint(sh.row[t][half ^ 1][r])));
                 scale /= power;
 #pragma unroll
-                for (int i = 0; i < D / 8; i++) {
+                for (int i = 0; i < D / 16; i++) {
                     uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                     for (int x = 0; x < 4; x++)
                         w[x] = pack2<true>(__uint_as_float(w[x] << 16) * power, __uint_as_float(w[x] & 0xFFFF0000u) * power);
-                    *reinterpret_cast<uint4*>(qs + t * S::kQ + (i >> 3) * (kTileM * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+                    const uint32_t c = half * (D / 16) + i;  // 16-byte chunk of the row
+                    *reinterpret_cast<uint4*>(qs + t * S::kQ + (c >> 3) * (kTileM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_async_proxy();
                 mbar_arrive(&sh.q_full);
             }
-            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, lane, pos, scale, m, l);
+            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pos, scale, m, l);
         }
+        // The row's sum, of both halves in the same order.
+        __syncwarp();
+        sh.row[t][half][r] = l;
+        named_sync(1 + t, 256);
+        l = sh.row[t][0][r] + sh.row[t][1][r];
         if (threadIdx.x == 0 && !go) atomicOr(p.status, kStatusTimeout);
         if (!go) l = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
 
@@ -586,7 +599,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         if (p.splits == 1) {
             const float inv = 1.0f / l;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; c++) {
+            for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
                 float o[32];
                 read_output<D, kF8>(p, sh, oa, pos, c, o);
                 if (valid) {
@@ -598,26 +611,28 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
                                                  pack2<false>(o[x + 4] * inv, o[x + 5] * inv), pack2<false>(o[x + 6] * inv, o[x + 7] * inv));
                 }
             }
-            if (valid && lse) *lse = pos < 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (valid && lse && half == 0) *lse = pos < 0 ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
             // Join the cluster's splits: every CTA leaves its rows in shared memory and
             // joins a share of them, in the order of the splits.
             float* rows = reinterpret_cast<float*>(qs);
 #pragma unroll 1
-            for (int c = 0; c < D / 32; c++) {
+            for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
                 float o[32];
                 read_output<D, kF8>(p, sh, oa, pos, c, o);
                 float4* to = reinterpret_cast<float4*>(rows + (t * kTileM + rr) * S::kRowFloats + 32 * c);
 #pragma unroll
                 for (int x = 0; x < 32; x += 4) to[x >> 2] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
             }
-            rows[(t * kTileM + rr) * S::kRowFloats + D] = m;
-            rows[(t * kTileM + rr) * S::kRowFloats + D + 1] = l;
+            if (half == 0) {
+                rows[(t * kTileM + rr) * S::kRowFloats + D] = m;
+                rows[(t * kTileM + rr) * S::kRowFloats + D + 1] = l;
+            }
             __syncwarp();
             cluster_sync();
             constexpr uint32_t kLanes = D / 4;  // threads to a row
             const uint32_t rank = blockIdx.x % p.splits, c = 4 * (threadIdx.x % kLanes);
-            for (uint32_t x = threadIdx.x / kLanes * p.splits + rank; x < 2 * kTileM; x += 256 / kLanes * p.splits) {
+            for (uint32_t x = threadIdx.x / kLanes * p.splits + rank; x < 2 * kTileM; x += kSoftmax / kLanes * p.splits) {
                 const uint32_t xr = x & 127, xt = sh.t0 + (x >> 7) * p.tokens + xr / p.group, xh = sh.h * p.group + xr % p.group;
                 if (xr >= p.tokens * p.group || xt >= p.a.q_tokens) continue;
                 const uint32_t at = smem_addr(rows + x * S::kRowFloats);
@@ -649,12 +664,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     }
     __syncthreads();
     tcgen_fence_after();
-    if (warp == 8) tmem_free<512>(tmem);
+    if (warp == 16) tmem_free<512>(tmem);
 }
 
 template <int D, bool kF8>
 cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
-    constexpr int kSmem = TilesShape<D, kF8>::kSmem;
+    constexpr int kSmem = TilesShape<D, kF8>::kUsed + (int)sizeof(TilesShared);
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
     Wave w;
     const cudaError_t e = launch_wave<tiles_kernel<D, kF8>>(kThreadsTiles, kSmem, w);
     if (e != cudaSuccess) return e;
