@@ -15,6 +15,11 @@
 // stay near the 1024 cycles of the other tile's products.  Hence two threads to
 // a row, 64 slots each, that exchange their maxima through shared memory.
 //
+// At head_dim 64 there is room for P beside S and O: S of the next step is made
+// as soon as the softmax warps have this step's in registers, and they never
+// wait for a product (the step is then bound by the exponentials, 1024 cycles,
+// as much as by the products).
+//
 // Roles: warps 0-15 softmax (four per tile and half of the slots), 16 issues
 // the products, 17 the TMA loads, 18 and 19 keep infinities and NaN of partly
 // visible tiles out of the second product (0 x infinity is not 0) and, for an
@@ -42,6 +47,7 @@ namespace {
 constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
 constexpr int kThreadsTiles = 640, kSoftmax = 512;
+constexpr int kPart = 16;        // scores turned into P at a time
 constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
 
 template <int D, bool kF8>
@@ -52,7 +58,11 @@ struct TilesShape {
     static constexpr int kStages = D == 128 ? (kF8 ? 3 : 5) : (kF8 ? 4 : 8);
     static constexpr int kRaws = kF8 ? 3 : 0;
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
-    static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * kRaw;
+    // Tensor memory: S of the query tiles from column 0, O, and P over S or apart.
+    static constexpr bool kApart = D == 64;
+    static constexpr uint32_t kColO = 2 * kBN, kColP = kApart ? kColO + 2 * D : 0, kStepP = kApart ? kBN / 2 : kBN;
+    static constexpr int kTiles = 2 * kQ + kStages * kKV + kRaws * kRaw;
+    static constexpr int kUsed = kTiles + (kApart ? 2048 : 0);  // and a second exchange of the rows
     static_assert(kUsed >= 2 * kTileM * kRowFloats * 4, "partial results take the place of the tiles");
 };
 
@@ -71,6 +81,7 @@ struct TilesShared {
     uint64_t raw_full[3], raw_empty[3];  // E5M2 tiles
     uint64_t q_full;
     uint64_t s_full[2], p_full[2], o_full[2], drained;  // of the query tiles
+    uint64_t s_free[2], o_done[2];  // P apart: S is in registers, a step's O is there
     uint32_t tmem, err, odd;
     // This CTA's work: sequence, head, first query token; the first slot of step
     // 0, the step that jumps from the sinks to the window and to where.
@@ -79,8 +90,9 @@ struct TilesShared {
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
     int32_t upto[2], after[2], whole_sinks;  // WholeTiles of the query tiles
-    // Exchanged by the two threads of a row.  A step's S is only there once every
-    // warp of the tile has handed over the last step's P, so one value does.
+    // Exchanged by the two threads of a row.  With P over S a step's S is only there
+    // once every warp of the tile has handed over the last step's P, so one value
+    // does; with P apart the steps take turns with a second array.
     float row[2][2][kTileM];
 };
 
@@ -177,9 +189,10 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
     };
     auto issue_o = [&](uint32_t t, uint32_t st, bool add) {
         const uint32_t va = vd + st * (S::kKV >> 4);
-        mma_ts(tmem + 256 + t * D, tmem + t * kBN, desc(va, 0), kShapeO, add);
+        const uint32_t o = tmem + S::kColO + t * D, pa = tmem + S::kColP + t * S::kStepP;
+        mma_ts(o, pa, desc(va, 0), kShapeO, add);
 #pragma unroll
-        for (int k = 1; k < kBN / 16; k++) mma_ts(tmem + 256 + t * D, tmem + t * kBN + 8 * k, desc(va, k * 2048), kShapeO, true);
+        for (int k = 1; k < kBN / 16; k++) mma_ts(o, pa + 8 * k, desc(va, k * 2048), kShapeO, true);
     };
     uint32_t st = 0, ph = 0;
     auto next = [&]() {
@@ -197,19 +210,35 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
         for (uint32_t i = 0; i + 1 < steps; i++) {
             const uint32_t vst = st, vph = ph;
             next();
-            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err) ||
-                !mbar_wait_bounded(&sh.full[st], ph, err))
-                return;
+            if (!mbar_wait_bounded(&sh.full[st], ph, err)) return;
+            if constexpr (S::kApart) {
+#pragma unroll
+                for (uint32_t t = 0; t < 2; t++) {
+                    if (!mbar_wait_bounded(&sh.s_free[t], i & 1, err)) return;
+                    tcgen_fence_after();
+                    if (leader) {
+                        issue_s(t, st);
+                        if (t) mma_commit(&sh.empty[st]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err)) return;
 #pragma unroll
             for (uint32_t t = 0; t < 2; t++) {
                 if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
                 tcgen_fence_after();
                 if (leader) {
                     issue_o(t, vst, i > 0);
-                    issue_s(t, st);
-                    if (t) {
-                        mma_commit(&sh.empty[vst]);
-                        mma_commit(&sh.empty[st]);
+                    if constexpr (S::kApart) {
+                        mma_commit(&sh.o_done[t]);
+                        if (t) mma_commit(&sh.empty[vst]);
+                    } else {
+                        issue_s(t, st);
+                        if (t) {
+                            mma_commit(&sh.empty[vst]);
+                            mma_commit(&sh.empty[st]);
+                        }
                     }
                 }
                 __syncwarp();
@@ -314,25 +343,33 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
 // half's sum.  Returns false where a wait gave up.
 template <int D, bool kF8>
 __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
-                                             uint32_t r, int32_t pos, float scale, float& m, float& l) {
+                                             uint32_t r, uint32_t pair_bar, float* row2, int32_t pos, float scale, float& m, float& l) {
     volatile uint32_t* err = &sh.err;
-    const uint32_t sa = tmem + t * kBN, oa = tmem + 256 + t * D + half * (D / 2);
+    using S = TilesShape<D, kF8>;
+    const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + 32 * half;
     // What a step needs only a moment is read again from shared memory, as volatile.
     const volatile TilesShared& now_sh = sh;
     int32_t s0 = sh.s0;
     m = -INFINITY;
     l = 0.0f;
+    bool ready = true;
     for (uint32_t i = 0; i < now_sh.steps; i++) {
-        const bool ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err);
+        ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err) && ready;
         tcgen_fence_after();
         uint32_t s[2][32];
         tmem_ld32(s[0], sa + 64 * half);
         tmem_ld32(s[1], sa + 64 * half + 32);
-        const bool part = !(s0 <= now_sh.upto[t] && (s0 > now_sh.after[t] || s0 <= now_sh.whole_sinks));
+        const int32_t upto = now_sh.upto[t], after = now_sh.after[t], whole_sinks = now_sh.whole_sinks;
+        const bool part = !((s0 <= upto) & ((s0 > after) | (s0 <= whole_sinks)));
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         tmem_wait_ld();
         tmem_loaded(s[0]);
         tmem_loaded(s[1]);
+        if constexpr (S::kApart) {
+            tcgen_fence_before();
+            __syncwarp();
+            if ((r & 31) == 0) mbar_arrive(&sh.s_free[t]);
+        }
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             if (part) {
@@ -344,14 +381,20 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
             }
 #pragma unroll
             for (int x = 0; x < 32; x += 2)
-                top[(x >> 1) & 3] = fmaxf(fmaxf(top[(x >> 1) & 3], __uint_as_float(s[c][x])), __uint_as_float(s[c][x + 1]));
+                top[(x >> 1) & 3] = max3(top[(x >> 1) & 3], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
         }
         const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-        sh.row[t][half][r] = own;
-        // All 256 threads of the tile also have their scores in registers after
-        // this, so P may go over S.  Where one's wait gave up, all return.
-        if (named_any(1 + t, 256, !ready)) return false;
-        const float now = fmaxf(own, sh.row[t][half ^ 1][r]);
+        float* row = S::kApart && (i & 1) ? row2 : &sh.row[0][0][0];
+        row[(2 * t + half) * kTileM + r] = own;
+        // The two warps of these rows also have their scores in registers after this,
+        // so P may go over S.  Where one's wait gave up, both return.
+        if (named_any(pair_bar, 64, !ready)) return false;
+        if constexpr (S::kApart) {  // the last step's product is done with P and O
+            if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, err);
+            tcgen_fence_after();
+            __syncwarp();
+        }
+        const float now = fmaxf(own, row[(2 * t + (half ^ 1)) * kTileM + r]);
         const bool raise = now > m + kLazy;  // from -inf too
         if (__any_sync(0xFFFFFFFFu, raise)) {
             const float f = raise ? exp2_approx(m - now) : 1.0f;
@@ -372,7 +415,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                         o[x] = __float_as_uint(u);
                         o[x + 1] = __float_as_uint(v);
                     }
-                    tmem_st8(oa + 8 * c, o);
+                    tmem_st<8>(oa + 8 * c, o);
                 }
             }
         }
@@ -380,19 +423,20 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-            uint32_t w[16];
+        for (int c = 0; c < 64 / kPart; c++) {
+            uint32_t w[kPart / 2];
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) {
+            for (int x = 0; x < kPart; x += 2) {
+                const int y = kPart * c + x;
                 float u, v;
-                unpair(fma2(pair(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc, neg), u, v);
+                unpair(fma2(pair(__uint_as_float(s[y >> 5][y & 31]), __uint_as_float(s[y >> 5][(y & 31) + 1])), sc, neg), u, v);
                 u = exp2_approx(u);
                 v = exp2_approx(v);
                 sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(u, v));
                 // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
                 w[x >> 1] = pack2<kF8>(u, v);
             }
-            tmem_st16(sa + 32 * half + 16 * c, w);
+            tmem_st<kPart / 2>(pa + kPart / 2 * c, w);
         }
         float u, v, u2, v2;
         unpair(sum[0], u, v);
@@ -405,7 +449,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         s0 = (int32_t)i + 1 == now_sh.jump_at ? now_sh.jump_to : s0 + kBN;
     }
     // Both tiles' products are done: a CTA's partial results take the tiles' place.
-    const bool go = sh.steps == 0 || (mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
+    const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
     tcgen_fence_after();
     return go;
 }
@@ -503,6 +547,8 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 8);
             mbar_init(&sh.o_full[i], 1);
+            mbar_init(&sh.s_free[i], 8);
+            mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.drained, 1);
         sh.err = sh.odd = 0;
@@ -539,6 +585,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     } else {
         regs_inc<104>();
         const uint32_t t = (warp >> 2) & 1, half = warp >> 3, r = threadIdx.x & 127;
+        const uint32_t pair_bar = 1 + (warp & 7);  // of the two warps of the same rows
         float m, l;
         bool go;
         {
@@ -561,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
                     for (int x = 0; x < 4; x++) top = max(top, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
                 }
                 sh.row[t][half][r] = __uint_as_float(top);
-                named_sync(1 + t, 256);
+                named_sync(pair_bar, 64);
                 const float power = row_power(max(top, __float_as_uint(sh.row[t][half ^ 1][r])));
                 scale /= power;
 #pragma unroll
@@ -577,12 +624,12 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
                 fence_async_proxy();
                 mbar_arrive(&sh.q_full);
             }
-            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pos, scale, m, l);
+            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pair_bar, reinterpret_cast<float*>(qs + S::kTiles), pos, scale, m, l);
         }
         // The row's sum, of both halves in the same order.
         __syncwarp();
         sh.row[t][half][r] = l;
-        named_sync(1 + t, 256);
+        named_sync(pair_bar, 64);
         l = sh.row[t][0][r] + sh.row[t][1][r];
         if (threadIdx.x == 0 && !go) atomicOr(p.status, kStatusTimeout);
         if (!go) l = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
@@ -592,7 +639,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
         const uint32_t tok = sh.t0 + t * p.tokens + rr / p.group, g = rr % p.group, hq = sh.h * p.group + g;
         const bool valid = rr < p.tokens * p.group && tok < p.a.q_tokens;
         const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
-        const uint32_t oa = tmem + (((warp & 3) * 32) << 16) + 256 + t * D;
+        const uint32_t oa = tmem + (((warp & 3) * 32) << 16) + S::kColO + t * D;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out.data) + (int64_t)sh.b * p.a.out.stride_b +
                              (int64_t)tok * p.a.out.stride_t + (int64_t)hq * p.a.out.stride_h;
         float* lse = p.a.lse ? p.a.lse + ((uint64_t)sh.b * p.a.q_heads + hq) * p.a.q_tokens + tok : nullptr;

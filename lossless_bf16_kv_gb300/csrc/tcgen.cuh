@@ -95,6 +95,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16, "columns");
+    if constexpr (N == 8) tmem_st8(addr, r);
+    else tmem_st16(addr, r);
+}
+
 // ------------------------------------------------------ matrix products
 
 // Shared-memory operands of 16-bit values in 128-byte swizzled rows (1024-byte
@@ -186,6 +193,13 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The largest of three, NaN only if all are.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // ------------------------------------------------- packed 32-bit pairs
