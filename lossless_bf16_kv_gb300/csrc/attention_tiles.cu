@@ -21,11 +21,12 @@
 // as much as by the products).
 //
 // Roles: warps 0-15 softmax (four per tile and half of the slots), 16 issues
-// the products, 17 the TMA loads, 18 and 19 keep infinities and NaN of partly
-// visible tiles out of the second product (0 x infinity is not 0) and, for an
-// E5M2 cache, widen its tiles to FP16 (exact: an E5M2 value is the upper byte of
-// the FP16 value it stands for).  The queries are then FP16 too, each row scaled
-// by a power of two.
+// the products of both tiles (from two warps they interleave and both tiles wait
+// for both: 734 against 879 us at 16k), 17 the TMA loads; the rest keep
+// infinities and NaN of partly visible tiles out of the second product (0 x
+// infinity is not 0) and, for an E5M2 cache, widen its tiles to FP16 (exact: an
+// E5M2 value is the upper byte of the FP16 value it stands for).  The queries
+// are then FP16 too, each row scaled by a power of two.
 //
 // What the roles share sits in shared memory and is read from there: a softmax
 // thread's 104 registers hold 64 scores and little else, and a value spilled
@@ -46,7 +47,7 @@ namespace {
 
 constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
-constexpr int kThreadsTiles = 640, kSoftmax = 512;
+constexpr int kSoftmax = 512;  // threads
 constexpr int kPart = 16;        // scores turned into P at a time
 constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
 
@@ -57,6 +58,12 @@ struct TilesShape {
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
     static constexpr int kStages = D == 128 ? (kF8 ? 3 : 5) : (kF8 ? 4 : 8);
     static constexpr int kRaws = kF8 ? 3 : 0;
+    // Threads: softmax, a warp for the products, one for the loads, and those that
+    // tend the values; registers of a softmax thread and of another.
+    static constexpr int kTend = kF8 ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
+    static constexpr int kRegs = kF8 ? 96 : 104, kOtherRegs = kF8 ? 48 : 64;
+    static_assert(kThreads % 128 == 0 && kSoftmax * kRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8),
+                  "register shares add up to what the CTA is launched with");
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
     // Tensor memory: S of the query tiles from column 0, O, and P over S or apart.
     static constexpr bool kApart = D == 64;
@@ -283,7 +290,7 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
             bool found = false;
             // 16 bytes of a row become two adjacent 16-byte chunks of the swizzled row.
 #pragma unroll 4
-            for (uint32_t x = thread; x < S::kRaw / 16; x += 64) {
+            for (uint32_t x = thread; x < S::kRaw / 16; x += 32 * S::kTend) {
                 const uint32_t r = x / (D / 16), c = x % (D / 16);
                 const uint4 v = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + 16 * x);
                 uint4 lo = make_uint4(e5m2_01(v.x), e5m2_23(v.x), e5m2_01(v.y), e5m2_23(v.y));
@@ -319,7 +326,7 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
                 bool found = false;
                 uint4* tile = reinterpret_cast<uint4*>(ring + st * S::kKV);
 #pragma unroll 4
-                for (uint32_t x = thread; x < S::kKV / 16; x += 64) {
+                for (uint32_t x = thread; x < S::kKV / 16; x += 32 * S::kTend) {
                     const uint4 v = tile[x];
                     const uint4 f = make_uint4(finite_or_zero<false>(v.x), finite_or_zero<false>(v.y), finite_or_zero<false>(v.z),
                                                finite_or_zero<false>(v.w));
@@ -352,15 +359,17 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
     int32_t s0 = sh.s0;
     m = -INFINITY;
     l = 0.0f;
-    bool ready = true;
-    for (uint32_t i = 0; i < now_sh.steps; i++) {
+    bool ready = true, more = now_sh.steps != 0;
+    for (uint32_t i = 0; more; i++) {
         ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err) && ready;
         tcgen_fence_after();
         uint32_t s[2][32];
         tmem_ld32(s[0], sa + 64 * half);
         tmem_ld32(s[1], sa + 64 * half + 32);
         const int32_t upto = now_sh.upto[t], after = now_sh.after[t], whole_sinks = now_sh.whole_sinks;
+        const int32_t jump_at = now_sh.jump_at, jump_to = now_sh.jump_to;
         const bool part = !((s0 <= upto) & ((s0 > after) | (s0 <= whole_sinks)));
+        more = i + 1 < now_sh.steps;
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         tmem_wait_ld();
         tmem_loaded(s[0]);
@@ -383,6 +392,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
             for (int x = 0; x < 32; x += 2)
                 top[(x >> 1) & 3] = max3(top[(x >> 1) & 3], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
         }
+        s0 = (int32_t)i + 1 == jump_at ? jump_to : s0 + kBN;
         const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
         float* row = S::kApart && (i & 1) ? row2 : &sh.row[0][0][0];
         row[(2 * t + half) * kTileM + r] = own;
@@ -446,7 +456,6 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         tcgen_fence_before();
         __syncwarp();
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[t]);
-        s0 = (int32_t)i + 1 == now_sh.jump_at ? now_sh.jump_to : s0 + kBN;
     }
     // Both tiles' products are done: a CTA's partial results take the tiles' place.
     const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
@@ -493,7 +502,7 @@ __device__ __forceinline__ void read_output(const TilesParams& p, const TilesSha
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
+__global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
     using S = TilesShape<D, kF8>;
     extern __shared__ __align__(1024) uint8_t qs[];
     TilesShared& sh = *reinterpret_cast<TilesShared*>(qs + S::kUsed);
@@ -534,13 +543,13 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             sh.whole_sinks = whole.sinks;
         }
         for (int i = 0; i < 8; i++) {
-            mbar_init(&sh.full[i], kF8 ? 2 : 1);
+            mbar_init(&sh.full[i], kF8 ? S::kTend : 1);
             mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.ok[i], 2);
+            mbar_init(&sh.ok[i], S::kTend);
         }
         for (int i = 0; i < 3; i++) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], 2);
+            mbar_init(&sh.raw_empty[i], S::kTend);
         }
         mbar_init(&sh.q_full, kF8 ? kSoftmax : 1);
         for (int i = 0; i < 2; i++) {
@@ -571,10 +580,10 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
     const uint32_t tmem = sh.tmem;
 
     if (warp >= 16) {
-        regs_dec<64>();
+        regs_dec<S::kOtherRegs>();
         if (sh.steps) {
             if (warp == 16) issue_products<D, kF8>(sh, tmem, qs, ring);
-            else if (warp >= 18) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - 576);
+            else if (warp > 17) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - (kSoftmax + 64));
             else if ((threadIdx.x & 31) == 0) load_tiles<D, kF8>(p, sh, qs, ring, raw);
         }
         __syncwarp();
@@ -583,7 +592,7 @@ __global__ void __launch_bounds__(kThreadsTiles, 1) tiles_kernel(const __grid_co
             cluster_sync();
         }
     } else {
-        regs_inc<104>();
+        regs_inc<S::kRegs>();
         const uint32_t t = (warp >> 2) & 1, half = warp >> 3, r = threadIdx.x & 127;
         const uint32_t pair_bar = 1 + (warp & 7);  // of the two warps of the same rows
         float m, l;
@@ -719,7 +728,7 @@ cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
     constexpr int kSmem = TilesShape<D, kF8>::kUsed + (int)sizeof(TilesShared);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     Wave w;
-    const cudaError_t e = launch_wave<tiles_kernel<D, kF8>>(kThreadsTiles, kSmem, w);
+    const cudaError_t e = launch_wave<tiles_kernel<D, kF8>>(TilesShape<D, kF8>::kThreads, kSmem, w);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -727,7 +736,7 @@ cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreadsTiles);
+    cfg.blockDim = dim3(TilesShape<D, kF8>::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = &attr;
