@@ -218,9 +218,10 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
             const uint32_t vst = st, vph = ph;
             next();
             if (!mbar_wait_bounded(&sh.full[st], ph, err)) return;
-            if constexpr (S::kApart) {
+            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err)) return;
 #pragma unroll
-                for (uint32_t t = 0; t < 2; t++) {
+            for (uint32_t t = 0; t < 2; t++) {
+                if constexpr (S::kApart) {
                     if (!mbar_wait_bounded(&sh.s_free[t], i & 1, err)) return;
                     tcgen_fence_after();
                     if (leader) {
@@ -229,10 +230,6 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
                     }
                     __syncwarp();
                 }
-            }
-            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err)) return;
-#pragma unroll
-            for (uint32_t t = 0; t < 2; t++) {
                 if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
                 tcgen_fence_after();
                 if (leader) {
