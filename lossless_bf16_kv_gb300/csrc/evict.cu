@@ -11,7 +11,7 @@
 // The keys are read once and stay in shared memory where they fit (rows of up
 // to 51200 slots): 512 rows of 16384 took 91 us reading the weights again from
 // L2 in each of four passes of eight bits, with a CTA barrier every 1024 slots
-// of the last pass; now every warp ranks a contiguous range of its own.
+// of the last pass; now every thread ranks a short run of its own.
 //
 // Gather: kept rows are copied in order.  HBM bounds it: at 64 x 8 rows, 2048
 // of 16384 slots of 128 BF16 values kept, 1.07 GB in 154 us (6.6 TB/s, 97% of a
@@ -56,6 +56,17 @@ __device__ __forceinline__ uint32_t before_warp(uint32_t v, uint32_t warp, uint3
     return __shfl_sync(0xFFFFFFFFu, x - own, warp);
 }
 
+// Exclusive sums over the threads of each thread's value.
+__device__ __forceinline__ uint32_t before_thread(uint32_t v, uint32_t lane, uint32_t warp, uint32_t* all) {
+    uint32_t incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    return before_warp(__shfl_sync(0xFFFFFFFFu, incl, 31), warp, all) + incl - v;
+}
+
 template <bool kInShared>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ splitzip_evict_args a) {
     __shared__ SelectShared sh;
@@ -82,10 +93,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     }
     const uint32_t lo = a.keep_first, hi = n - a.keep_last;  // the slots to choose from
     uint32_t want = a.budget - a.keep_first - a.keep_last;   // how many of them, < hi - lo
-    uint32_t least = 0xFFFFFFFFu;                            // smallest key kept; none yet
+    uint32_t least = 0;                                      // the smallest key kept
     auto key = [&](uint32_t i) { return kInShared ? keys[i] : weight_key(w[i]); };
-    if (kInShared) {
-#pragma unroll 8
+    if (kInShared && !want) {
         for (uint32_t i = tid; i < n; i += kSelectThreads) keys[i] = weight_key(w[i]);
     }
     if (want) {
@@ -95,28 +105,31 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             for (uint32_t i = tid; i < kBins; i += kSelectThreads) sh.hist[i] = 0;
             __syncthreads();
-            for (uint32_t i = lo + tid; i < hi; i += kSelectThreads) {
-                const uint32_t k = key(i);
-                if (pass == 0 || k >> (shift + bits) == prefix) {
-                    // Many weights may share one digit (slots never attended): lanes with
-                    // the first lane's digit count together.
-                    const uint32_t active = __activemask(), d = (k >> shift) & ((1u << bits) - 1u);
-                    const uint32_t first = __ffs(active) - 1, same = __ballot_sync(active, d == __shfl_sync(active, d, first));
-                    if (lane == first) atomicAdd(&sh.hist[d], __popc(same));
-                    else if (!(same >> lane & 1u)) atomicAdd(&sh.hist[d], 1u);
+            if (pass == 0) {
+                // The weight 0 is common (slots never attended) and counted apart.
+                constexpr uint32_t kZero = 0x80000000u;
+                uint32_t zeros = 0;
+#pragma unroll 8
+                for (uint32_t i = tid; i < n; i += kSelectThreads) {
+                    const uint32_t k = weight_key(w[i]);
+                    if (kInShared) keys[i] = k;
+                    if (i < lo || i >= hi) continue;
+                    if (k == kZero) zeros++;
+                    else atomicAdd(&sh.hist[k >> shift], 1u);
+                }
+                zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
+                if (lane == 0 && zeros) atomicAdd(&sh.hist[kZero >> shift], zeros);
+            } else {
+#pragma unroll 4
+                for (uint32_t i = lo + tid; i < hi; i += kSelectThreads) {
+                    const uint32_t k = key(i);
+                    if (k >> (shift + bits) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
                 }
             }
             __syncthreads();
             // Thread t holds digits kBins - 1 - 2 t and the one below.
             const uint32_t d0 = kBins - 1 - 2 * tid, c0 = sh.hist[d0], c1 = sh.hist[d0 - 1];
-            uint32_t incl = c0 + c1;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                if (lane >= d) incl += y;
-            }
-            const uint32_t total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-            const uint32_t before = before_warp(total, warp, sh.warp[0]) + incl - (c0 + c1);
+            const uint32_t before = before_thread(c0 + c1, lane, warp, sh.warp[0]);
             if (before < want && want <= before + c0 + c1) {
                 const bool upper = want <= before + c0;
                 sh.digit = upper ? d0 : d0 - 1;
@@ -128,34 +141,40 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         }
         least = prefix;
     }
-    // Each warp ranks a contiguous range of slots: how many before it are kept for
-    // good, and how many have the smallest kept key (the first `want` of those are
-    // kept, so a slot's place depends on how many came before).
+    // Each thread ranks a short run of slots: how many before it are kept for good,
+    // and how many have the smallest kept key (the first `want` of those are kept, so
+    // a slot's place depends on how many came before).  Slots that are always kept
+    // get a key above every weight's.  Runs of odd length: no bank conflicts.
+    constexpr uint32_t kAlways = 0xFFFFFFFFu;
     __syncthreads();
-    const uint32_t span = (n + kSelectThreads - 1) / kSelectThreads * 32, from = min(warp * span, n), to = min(from + span, n);
-    uint32_t sure = 0, equal = 0;
-    for (uint32_t base = from; base < to; base += 32) {
-        const uint32_t i = base + lane, k = i < to ? key(i) : 0u;
-        const bool choice = i >= lo && i < hi;
-        sure += __popc(__ballot_sync(0xFFFFFFFFu, i < to && (!choice || k > least)));
-        equal += __popc(__ballot_sync(0xFFFFFFFFu, i < to && choice && k == least));
+    if (kInShared) {
+        for (uint32_t i = tid; i < lo; i += kSelectThreads) keys[i] = kAlways;
+        for (uint32_t i = hi + tid; i < n; i += kSelectThreads) keys[i] = kAlways;
+        __syncthreads();
     }
-    sure = before_warp(sure, warp, sh.warp[0]);
-    equal = before_warp(equal, warp, sh.warp[1]);
-    const uint32_t below = (1u << lane) - 1u;
-    for (uint32_t base = from; base < to; base += 32) {
-        const uint32_t i = base + lane, k = i < to ? key(i) : 0u;
-        const bool choice = i >= lo && i < hi;
-        const bool in = i < to && (!choice || k > least), eq = i < to && choice && k == least;
-        const uint32_t ins = __ballot_sync(0xFFFFFFFFu, in), eqs = __ballot_sync(0xFFFFFFFFu, eq);
-        const uint32_t eq_at = equal + __popc(eqs & below);
-        if (in || (eq && eq_at < want)) {
-            const uint32_t at = sure + __popc(ins & below) + min(eq_at, want);
+    // The keys kept for good are those from `sure_key` on.
+    const uint32_t sure_key = a.budget == a.keep_first + a.keep_last ? kAlways : least + 1;
+    auto rank_key = [&](uint32_t i) { return kInShared ? keys[i] : i < lo || i >= hi ? kAlways : weight_key(w[i]); };
+    const uint32_t run = ((n + kSelectThreads - 1) / kSelectThreads) | 1u, from = min(tid * run, n), to = min(from + run, n);
+    uint32_t sure = 0, equal = 0;
+    for (uint32_t i = from; i < to; i++) {
+        const uint32_t k = rank_key(i);
+        sure += k >= sure_key;
+        equal += k == least;
+    }
+    if (want == 0) equal = 0;
+    sure = before_thread(sure, lane, warp, sh.warp[0]);
+    equal = before_thread(equal, lane, warp, sh.warp[1]);
+    for (uint32_t i = from; i < to; i++) {
+        const uint32_t k = rank_key(i);
+        const bool eq = k == least;
+        if (k >= sure_key || (eq && equal < want)) {
+            const uint32_t at = sure + min(equal, want);
             index[at] = (int32_t)i;
             if (w_out) w_out[at] = w[i];
         }
-        sure += __popc(ins);
-        equal += __popc(eqs);
+        sure += k >= sure_key;
+        equal += eq;
     }
 }
 
