@@ -145,7 +145,8 @@ splitzip_status splitzip_attention_status(void *workspace, splitzip_stream_t s);
  * may be any of its queries (with lens and q_tokens placing them);
  * q.k of a masked slot is not looked at.  Both float[batch][kv_heads][kv_tokens];
  * weights_in may be weights_out, or NULL for zeros.  Slots past a sequence's
- * length get weights_in.  Needs no workspace; v and out are ignored. */
+ * length get weights_in.  Needs no workspace; v and out are ignored.  If a bounded wait
+ * inside the kernel gives up, the weights it had not finished are NaN. */
 splitzip_status splitzip_attention_weights(const splitzip_attention_args *args,
                                            const float *weights_in, float *weights_out,
                                            splitzip_stream_t s);

@@ -25,6 +25,7 @@
 // keys to BF16 (exact).
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "tcgen.cuh"
@@ -62,11 +63,19 @@ struct WeightsShape {
 // One item: its slots s_lo .. s_hi of key/value head h of sequence b (bh counts
 // both), the query tiles i0 .. i0 + steps - 1 that can see them; from the first of
 // these tiles on, how many query tokens there are (last) and which of them is at
-// the position of s_lo (behind, may be negative).
+// the position of s_lo (behind, may be negative); the tiles all of whose tokens
+// see all of the slots, whole_lo .. whole_hi - 1.
 constexpr uint32_t kNoItem = 0xFFFFFFFFu;  // bh of the end of the list
 struct Item {
     uint32_t b, h, bh, i0, steps;
     int32_t s_lo, s_hi, last, behind, sinks;
+    uint32_t whole_lo, whole_hi;
+    // The query tokens that see slot s_lo + r, from the first tile on: [see_from, see_end).
+    __device__ __forceinline__ int32_t see_from(uint32_t r) const { return min(max(behind + (int32_t)r, 0), last); }
+    __device__ __forceinline__ int32_t see_end(const WeightsParams& p, uint32_t r) const {
+        const int64_t end = (int64_t)behind + (int32_t)r + p.window;
+        return s_lo + (int32_t)r < sinks || end >= last ? last : max((int32_t)end, 0);
+    }
 };
 
 struct WeightsShared {
@@ -144,6 +153,10 @@ __device__ __forceinline__ void plan_items(const WeightsParams& p, WeightsShared
                     w.steps = quotient(p.by_tokens, (uint32_t)t_hi + p.tokens - 1) - w.i0;
                     w.last = (int32_t)(a.q_tokens - w.i0 * p.tokens);
                     w.behind = (int32_t)((int64_t)w.s_lo - mask.first - (int64_t)w.i0 * p.tokens);
+                    w.whole_lo = quotient(p.by_tokens, (uint32_t)max(w.behind + kSlotTile - 1, 0) + p.tokens - 1);
+                    // The first slot that is no sink is the first to leave the window.
+                    const uint32_t r = (uint32_t)min(max(w.sinks - w.s_lo, 0), kSlotTile - 1);
+                    w.whole_hi = quotient(p.by_tokens, (uint32_t)w.see_end(p, r));
                 }
             }
         }
@@ -329,6 +342,16 @@ __device__ __forceinline__ void widen_keys(const WeightsParams& p, WeightsShared
     }
 }
 
+// NaN for the items from this CTA's round on.
+__device__ __forceinline__ void give_up(const WeightsParams& p, uint32_t round, uint32_t g, uint32_t r) {
+    const uint32_t heads = p.a.batch * p.a.kv_heads;
+    for (; g == 0 && (uint64_t)round * gridDim.x < p.items; round++) {
+        const uint64_t at = (uint64_t)round * gridDim.x + (round & 1u ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const uint64_t sc = at / heads, slot = sc * kSlotTile + r;
+        if (at < p.items && slot < p.a.kv_tokens) p.out[(at - sc * heads) * p.a.kv_tokens + slot] = __int_as_float(0x7FC00000);
+    }
+}
+
 // Group of warps g: columns 64 (g & 1) .. of the query tiles n with (n & 1) = g >> 1.
 __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared& sh, uint32_t tmem, uint32_t g, uint32_t r) {
     volatile uint32_t* err = &sh.err;
@@ -337,67 +360,77 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
     const uint64_t scale2 = pair(scale, scale);
     const int32_t group = (int32_t)p.group, tokens = (int32_t)p.tokens;
     const bool full = p.tokens * p.group >= c0 + 64;  // all of these columns are in use
-    uint32_t n = 0, parity = 0;
-    Items list(sh);
-    for (; list.next<true>(); parity ^= 1) {
-        const Item& w = list.w;
-        const int32_t slot = w.s_lo + (int32_t)r;
-        // Query tokens that see this slot, [see_lo, see_hi) from the first tile on, and
-        // the tiles all of whose tokens see all of this warp's slots.
-        const int32_t behind = w.behind + (int32_t)r, see_lo = min(max(behind, 0), w.last);
-        const int64_t behind_window = (int64_t)behind + p.window;
-        const int32_t see_hi = slot < w.sinks || behind_window >= w.last ? w.last : max((int32_t)behind_window, 0);
-        const uint32_t whole_lo = quotient(p.by_tokens, __reduce_max_sync(0xFFFFFFFFu, (uint32_t)see_lo) + p.tokens - 1);
-        const uint32_t whole_hi = quotient(p.by_tokens, __reduce_min_sync(0xFFFFFFFFu, (uint32_t)see_hi));
-        const uint64_t to = (uint64_t)w.bh * p.a.kv_tokens + (uint32_t)slot;
-        const float before = g == 0 && p.in && slot <= w.s_hi ? p.in[to] : 0.0f;
+    uint32_t n = 0, at = 0;
+    for (;; at++) {
+        // The item's record is read where it lies, and given back at the item's end.
+        // Where a wait for one gave up, all return at the barrier below.
+        const uint32_t rec = at % kItems;
+        const bool ok = mbar_wait_bounded(&sh.item_full[rec], (at / kItems) & 1, err);
+        const Item& w = sh.item[rec];
+        if (!ok || w.bh == kNoItem) {
+            if (named_any(1, kSum, !ok)) give_up(p, at, g, r);
+            return;
+        }
+        const uint32_t steps = w.steps, whole_lo = w.whole_lo, whole_hi = w.whole_hi, parity = at & 1;
+        const bool mine = g == 0 && w.s_lo + (int32_t)r <= w.s_hi;
+        const uint64_t to = (uint64_t)w.bh * p.a.kv_tokens + (uint32_t)w.s_lo + r;
+        const float before = mine && p.in ? p.in[to] : 0.0f;
         float sum = 0.0f;
         uint32_t i = (n ^ (g >> 1)) & 1;  // the first of this group's tiles
         n += i;
-        for (; i < w.steps; i += 2, n += 2) {
+        for (; i < steps; i += 2, n += 2) {
             const uint32_t x = n & 3, mx = n % kMetas;
             if (!mbar_wait_bounded(&sh.meta_full[mx], (n / kMetas) & 1, err) || !mbar_wait_bounded(&sh.s_full[x], (n >> 2) & 1, err)) {
                 sum = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
                 continue;
             }
             tcgen_fence_after();
-            uint32_t s[2][32];
             __syncwarp();
-            tmem_ld32(s[0], tmem + x * kRowTile + c0);
-            tmem_ld32(s[1], tmem + x * kRowTile + c0 + 32);
+            const uint32_t sa = tmem + x * kRowTile + c0;
+            uint32_t s[2][16];  // sixteen columns, and the next sixteen on their way
+            tmem_ld16(s[0], sa);
             const bool whole = i >= whole_lo && i < whole_hi;
-            tmem_wait_ld();
-            tmem_loaded(s[0]);
-            tmem_loaded(s[1]);
-            tcgen_fence_before();
-            __syncwarp();
-            if ((r & 31) == 0) mbar_arrive(&sh.s_free[x]);
             uint64_t part[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                if (!whole || (!full && p.tokens * p.group < c0 + 32 * c + 32)) {
-                    // This tile's columns that the slot takes part in.
-                    const int32_t t0 = (int32_t)i * tokens, col = (int32_t)c0 + 32 * c;
-                    const int32_t l = max(0, min(tokens, see_lo - t0)) * group - col, u = max(0, min(tokens, see_hi - t0)) * group - col;
-                    const uint32_t from = l <= 0 ? 0xFFFFFFFFu : l > 31 ? 0u : 0xFFFFFFFFu << l;
-                    const uint32_t below = u <= 0 ? 0u : u > 31 ? 0xFFFFFFFFu : ~(0xFFFFFFFFu << u);
-                    const uint32_t in = from & below;
-#pragma unroll
-                    for (int y = 0; y < 32; y++) {
-                        const float e = exp2_approx(fmaf(__uint_as_float(s[c][y]), scale, sh.lse[mx][c0 + 32 * c + y]));
-                        part[y & 1] = add2(part[y & 1], pair(in >> y & 1u ? e : 0.0f, 0.0f));
-                    }
+            for (int c = 0; c < 4; c++) {
+                uint32_t(&v)[16] = s[c & 1];
+                tmem_wait_ld();
+                tmem_loaded(v);
+                if (c < 3) {
+                    tmem_ld16(s[(c + 1) & 1], sa + 16 * (c + 1));
                 } else {
+                    tcgen_fence_before();
+                    __syncwarp();
+                    if ((r & 31) == 0) mbar_arrive(&sh.s_free[x]);
+                }
+                const auto add = [&](auto masked, uint32_t in) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4) {
-                        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&sh.lse[mx][c0 + 32 * c + y]);
+                    for (int y = 0; y < 16; y += 4) {
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&sh.lse[mx][c0 + 16 * c + y]);
 #pragma unroll
                         for (int z = 0; z < 4; z += 2) {
-                            float u, v;
-                            unpair(fma2(pair(__uint_as_float(s[c][y + z]), __uint_as_float(s[c][y + z + 1])), scale2, z ? l.y : l.x), u, v);
-                            part[z >> 1] = add2(part[z >> 1], pair(exp2_approx(u), exp2_approx(v)));
+                            float e, f;
+                            unpair(fma2(pair(__uint_as_float(v[y + z]), __uint_as_float(v[y + z + 1])), scale2, z ? l.y : l.x), e, f);
+                            e = exp2_approx(e);
+                            f = exp2_approx(f);
+                            if (masked) {
+                                e = in >> (y + z) & 1u ? e : 0.0f;
+                                f = in >> (y + z + 1) & 1u ? f : 0.0f;
+                            }
+                            part[z >> 1] = add2(part[z >> 1], pair(e, f));
                         }
                     }
+                };
+                if (whole && (full || p.tokens * p.group >= c0 + 16 * c + 16)) {
+                    add(std::false_type(), 0u);
+                } else {
+                    // This tile's columns that the slot takes part in.
+                    const int32_t t0 = (int32_t)i * tokens, col = (int32_t)c0 + 16 * c;
+                    const int32_t l = max(0, min(tokens, w.see_from(r) - t0)) * group - col;
+                    const int32_t u = max(0, min(tokens, w.see_end(p, r) - t0)) * group - col;
+                    const uint32_t from = l <= 0 ? 0xFFFFFFFFu : l > 31 ? 0u : 0xFFFFFFFFu << l;
+                    const uint32_t below = u <= 0 ? 0u : u > 31 ? 0xFFFFFFFFu : ~(0xFFFFFFFFu << u);
+                    if (__any_sync(0xFFFFFFFFu, from & below & 0xFFFFu)) add(std::true_type(), from & below);
                 }
             }
             float u, v, u2, v2;
@@ -407,14 +440,16 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
             __syncwarp();
             if ((r & 31) == 0) mbar_arrive(&sh.meta_free[mx]);
         }
-        n += w.steps - i;  // to the next item's first tile
+        n += steps - i;  // to the next item's first tile
         sh.part[parity][g][r] = sum;
-        named_sync(1, kSum);
-        if (g == 0 && slot <= w.s_hi) {
-            p.out[to] = before + ((sum + sh.part[parity][1][r]) + (sh.part[parity][2][r] + sh.part[parity][3][r]));
+        __syncwarp();
+        if ((r & 31) == 0) mbar_arrive(&sh.item_free[rec]);
+        if (named_any(1, kSum, false)) {
+            give_up(p, at, g, r);
+            return;
         }
+        if (mine) p.out[to] = before + ((sum + sh.part[parity][1][r]) + (sh.part[parity][2][r] + sh.part[parity][3][r]));
     }
-    tcgen_fence_before();
 }
 
 template <int D, bool kF8>
@@ -464,6 +499,7 @@ __global__ void __launch_bounds__(WeightsShape<D, kF8>::kThreads, 1) weights_ker
     if (warp < 16) {
         regs_inc<S::kRegs>();
         sum_items(p, sh, tmem + (((warp & 3) * 32) << 16), warp >> 2, tid & 127);
+        tcgen_fence_before();
     } else {
         regs_dec<S::kOtherRegs>();
         if (warp == 16) issue_items<D, kF8>(p, sh, tmem, ks, ring);
