@@ -66,6 +66,9 @@ _EVICT = struct.Struct("@" + 4 * _VIEW + "5P8I")
 _NO_VIEW = (0, 0, 0, 0)
 
 _lib = None
+_fn_norm_rope = _fn_attention = _fn_weights = _fn_evict = None
+_B16, _F8, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float8_e5m2, torch.float32, torch.int32, torch.int64,
+                                    torch.uint8)
 
 
 def library() -> ctypes.CDLL:
@@ -86,6 +89,9 @@ def library() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
+        global _fn_norm_rope, _fn_attention, _fn_weights, _fn_evict
+        _fn_norm_rope, _fn_attention = lib.splitzip_qk_norm_rope, lib.splitzip_attention
+        _fn_weights, _fn_evict = lib.splitzip_attention_weights, lib.splitzip_evict
     return _lib
 
 
@@ -110,41 +116,29 @@ def _stream_of(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _view4(t: torch.Tensor, shape, what: str) -> tuple:
-    """(pointer, stride_b, stride_t, stride_h) of a [batch, tokens, heads, dim] view."""
-    if t.shape != shape:
+# A call on small tensors costs less than looking at its arguments, so each
+# function checks them in one expression; only where that fails are they gone
+# through one by one, to say which is wrong.
+
+def _check_view(t: torch.Tensor, shape, what: str):
+    if tuple(t.shape) != tuple(shape):
         _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    sb, st, sh, one = t.stride()
-    if one != 1:
+    if t.stride()[-1] != 1:
         _bad(f"{what}: the values of a row must be contiguous")
-    return t.data_ptr(), sb, st, sh
 
 
-def _view3(t: torch.Tensor, shape, what: str) -> tuple:
-    """(pointer, 0, stride_t, stride_h) of a [tokens, heads, dim] view."""
-    if t.shape != shape:
-        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    st, sh, one = t.stride()
-    if one != 1:
-        _bad(f"{what}: the values of a row must be contiguous")
-    return t.data_ptr(), 0, st, sh
-
-
-def _array(t: torch.Tensor | None, dtype, shape: tuple | None, what: str) -> int:
-    """Pointer of a contiguous array of this type and shape, or 0 for None."""
+def _check_array(t: torch.Tensor | None, dtype, shape: tuple | None, what: str):
+    """A contiguous array of this type and shape, or None."""
     if t is None:
-        return 0
+        return
     if t.dtype != dtype:
         _bad(f"{what} is {t.dtype}, {dtype} needed")
-    if shape is not None and t.shape != shape:
-        _bad(f"{what} has shape {tuple(t.shape)}, {shape} needed")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor")
-    return t.data_ptr()
 
 
 def _bf16(t: torch.Tensor, what: str):
@@ -164,22 +158,49 @@ def _format(k: torch.Tensor, v: torch.Tensor | None = None) -> int:
 # --------------------------------------------------- norm, rotation, cache
 
 def _cache_rows(t: torch.Tensor, what: str) -> tuple:
-    """(rows, pointer, stride_t, stride_h) of a cache addressed by row: [rows,
-    heads, dim], or [batch, tokens, heads, dim] whose batch stride is a whole
-    number of token strides (row = b * stride_b // stride_t + token)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
+    """(rows, stride_t, stride_h) of a cache addressed by row: [rows, heads,
+    dim], or [batch, tokens, heads, dim] whose batch stride is a whole number of
+    token strides (row = b * stride_b // stride_t + token)."""
     shape, st = t.shape, t.stride()
     if st[-1] != 1:
         _bad(f"{what}: the values of a row must be contiguous")
     if len(shape) == 3:
-        return shape[0], t.data_ptr(), st[0], st[1]
+        return shape[0], st[0], st[1]
     if len(shape) != 4:
         _bad(f"{what} is [rows, heads, dim] or [batch, tokens, heads, dim]")
     if shape[0] > 1 and (st[1] == 0 or st[0] % st[1]):
         _bad(f"{what}: the batch stride must be a multiple of the token stride")
     rows = (shape[0] - 1) * (st[0] // st[1]) + shape[1] if shape[0] > 1 else shape[0] * shape[1]
-    return rows, t.data_ptr(), st[1], st[2]
+    return rows, st[1], st[2]
+
+
+def _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache):
+    for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
+        _bf16(t, what)
+        if t.dim() != 3:
+            _bad(f"{what} is [tokens, heads, dim]")
+    _format(k_cache, v_cache)
+    n, _, dim = q.shape
+    hk = k.shape[1]
+    _check_view(q, q.shape, "q")
+    _check_view(k, (n, hk, dim), "k")
+    _check_view(v, (n, hk, dim), "v")
+    _check_view(q_out, q.shape, "q_out")
+    for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
+        if tuple(t.shape[-2:]) != (hk, dim):
+            _bad("the caches' heads and dims must be those of k")
+    _check_array(q_weight, _B16, (dim,), "q_weight")
+    _check_array(k_weight, _B16, (dim,), "k_weight")
+    if slots is None:
+        _bad("slots are needed")
+    _check_array(slots, _I64, (n,), "slots")
+    _check_array(positions, _I32, (n,), "positions")
+    _check_array(table, _F32, None, "table")
+    if table is not None and (table.dim() != 2 or positions is None):
+        _bad("a rotation needs a table [positions, rot_dim] and positions")
+    _bad("these arguments are not accepted")
 
 
 def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight, k_weight, positions, table,
@@ -192,31 +213,40 @@ def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     (cosines, then sines) or None for no rotation; positions int32 [n].
     slots: int64 [n]; a cache [batch, tokens, heads, dim] is addressed by
     b * stride_b // stride_t + token.  q_out may be q."""
-    n, hq, dim = q.shape
-    hk = k.shape[1]
-    for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
-        _bf16(t, what)
-    fmt = _format(k_cache, v_cache)
-    krows, kp, kst, ksh = _cache_rows(k_cache, "k_cache")
-    vrows, vp, vst, vsh = _cache_rows(v_cache, "v_cache")
-    if k_cache.shape[-2:] != (hk, dim) or v_cache.shape[-2:] != (hk, dim):
-        _bad("the caches' heads and dims must be those of k")
-    rot = 0
-    if table is not None:
-        if table.dim() != 2:
-            _bad("table is [positions, rot_dim]")
-        rot = table.shape[1]
-        if positions is None:
-            _bad("a rotation needs positions")
-    kshape = (n, hk, dim)
-    a = _NORM_ROPE.pack(*_view3(q, q.shape, "q"), *_view3(k, kshape, "k"), *_view3(v, kshape, "v"),
-                        _array(q_weight, torch.bfloat16, (dim,), "q_weight"),
-                        _array(k_weight, torch.bfloat16, (dim,), "k_weight"),
-                        _array(positions, torch.int32, (n,), "positions"),
-                        _array(table, torch.float32, None, "table"), _array(slots, torch.int64, (n,), "slots"),
-                        *_view3(q_out, q.shape, "q_out"), kp, 0, kst, ksh, vp, 0, vst, vsh,
-                        table.shape[0] if rot else 0, min(krows, vrows), n, hq, hk, dim, rot, fmt, bool(interleaved), eps)
-    _check((_lib or library()).splitzip_qk_norm_rope(a, _stream_of(stream)), "splitzip_qk_norm_rope")
+    qs, ks, kind = q.shape, k.shape, k_cache.dtype
+    qst, kst, vst, ost = q.stride(), k.stride(), v.stride(), q_out.stride()
+    cs, rot = k_cache.shape, 0
+    ok = (len(qs) == 3 and len(ks) == 3 and qs[0] == ks[0] and qs[2] == ks[2] and v.shape == ks and q_out.shape == qs
+          and q.dtype is _B16 and k.dtype is _B16 and v.dtype is _B16 and q_out.dtype is _B16
+          and (kind is _B16 or kind is _F8) and v_cache.dtype is kind
+          and qst[2] == 1 and kst[2] == 1 and vst[2] == 1 and ost[2] == 1
+          and cs[-2:] == ks[1:] and v_cache.shape[-2:] == ks[1:]
+          and slots is not None and slots.dtype is _I64 and slots.shape == qs[:1] and slots.is_contiguous()
+          and q.is_cuda and k.is_cuda and v.is_cuda and q_out.is_cuda and k_cache.is_cuda and v_cache.is_cuda
+          and slots.is_cuda)
+    for w in (q_weight, k_weight):
+        ok = ok and (w is None or (w.dtype is _B16 and w.shape == qs[2:] and w.is_contiguous() and w.is_cuda))
+    if ok and table is not None:
+        ts = table.shape
+        ok = (len(ts) == 2 and table.dtype is _F32 and table.is_contiguous() and table.is_cuda
+              and positions is not None and positions.dtype is _I32 and positions.shape == qs[:1]
+              and positions.is_contiguous() and positions.is_cuda)
+        rot = ts[1] if ok else 0
+    if not ok:
+        _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache)
+    krows, kct, kch = _cache_rows(k_cache, "k_cache")
+    vrows, vct, vch = _cache_rows(v_cache, "v_cache")
+    a = _NORM_ROPE.pack(q.data_ptr(), 0, qst[0], qst[1], k.data_ptr(), 0, kst[0], kst[1], v.data_ptr(), 0, vst[0], vst[1],
+                        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+                        positions.data_ptr() if rot else 0, table.data_ptr() if rot else 0, slots.data_ptr(),
+                        q_out.data_ptr(), 0, ost[0], ost[1], k_cache.data_ptr(), 0, kct, kch, v_cache.data_ptr(), 0, vct, vch,
+                        ts[0] if rot else 0, krows if krows < vrows else vrows, *qs[:2], *ks[1:], rot, _FORMAT[kind],
+                        1 if interleaved else 0, eps)
+    if _fn_norm_rope is None:
+        library()
+    status = _fn_norm_rope(a, _stream_of(stream))
+    if status:
+        _check(status, "splitzip_qk_norm_rope")
 
 
 # ------------------------------------------------------------- attention
@@ -227,7 +257,7 @@ def _sizes(q_shape, k_shape, fmt: int, window: int, sinks: int):
     if window < 0 or sinks < 0:
         _bad("window and sinks are not negative")
     return (q_shape[0], q_shape[1], k_shape[1], q_shape[2], k_shape[2], q_shape[3],
-            min(window, 0x80000000), min(sinks, 0x80000000), fmt)
+            min(window, _MOST), min(sinks, _MOST), fmt)
 
 
 def splitzip_attention_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, window: int = 0, sinks: int = 0) -> int:
@@ -245,6 +275,40 @@ def alloc_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, window: in
     return torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
 
 
+_MOST = 0x80000000   # a longer window is unlimited too
+
+
+def _check_attention(q, k_cache, v_cache, out, workspace, lens, lse, window, sinks):
+    fmt = _format(k_cache, v_cache)
+    b, tq, _, hq, _, dim = _sizes(q.shape, k_cache.shape, fmt, window, sinks)[:6]
+    _bf16(q, "q")
+    _bf16(out, "out")
+    if k_cache.shape[0] != b or k_cache.shape[3] != dim:
+        _bad("q's batch and dims must be the caches'")
+    for t, like, what in ((q, q, "q"), (k_cache, k_cache, "k_cache"), (v_cache, k_cache, "v_cache"), (out, q, "out")):
+        _check_view(t, like.shape, what)
+    _check_array(workspace, _U8, None, "workspace")
+    _check_array(lens, _I32, (b,), "lens")
+    _check_array(lse, _F32, (b, hq, tq), "lse")
+    _bad("these arguments are not accepted")
+
+
+def _check_weights(q, k_cache, lse, weights_out, lens, weights_in, window, sinks):
+    b, tq, tk, hq, hk, dim = _sizes(q.shape, k_cache.shape, _format(k_cache), window, sinks)[:6]
+    _bf16(q, "q")
+    if k_cache.shape[0] != b or k_cache.shape[3] != dim:
+        _bad("q's batch and dims must be the cache's")
+    if lse is None or weights_out is None:
+        _bad("lse and weights_out are needed")
+    _check_view(q, q.shape, "q")
+    _check_view(k_cache, k_cache.shape, "k_cache")
+    _check_array(lse, _F32, (b, hq, tq), "lse")
+    _check_array(lens, _I32, (b,), "lens")
+    _check_array(weights_in, _F32, (b, hk, tk), "weights_in")
+    _check_array(weights_out, _F32, (b, hk, tk), "weights_out")
+    _bad("these arguments are not accepted")
+
+
 def splitzip_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, out: torch.Tensor,
                        workspace: torch.Tensor, lens: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                        window: int = 0, sinks: int = 0, scale: float | None = None, stream=None):
@@ -252,25 +316,35 @@ def splitzip_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     [batch, kv_tokens, kv_heads, dim]; asynchronous.  The queries are the last
     q_tokens of lens[b] (int32; None: kv_tokens) tokens.  lse: float32 [batch,
     q_heads, q_tokens] or None.  scale: None for dim ** -0.5."""
-    qs, ks = q.shape, k_cache.shape
-    fmt = _format(k_cache, v_cache)
-    sizes = _sizes(qs, ks, fmt, window, sinks)
-    b, tq, tk, hq, hk, dim = sizes[:6]
-    _bf16(q, "q")
-    _bf16(out, "out")
-    if ks[0] != b or ks[3] != dim:
-        _bad("q's batch and dims must be the caches'")
-    a = _ATTENTION.pack(*_view4(q, qs, "q"), *_view4(k_cache, ks, "k_cache"), *_view4(v_cache, ks, "v_cache"),
-                        *_view4(out, qs, "out"), _array(lse, torch.float32, (b, hq, tq), "lse"),
-                        _array(lens, torch.int32, (b,), "lens"), *sizes, dim ** -0.5 if scale is None else scale)
-    _check((_lib or library()).splitzip_attention(a, _array(workspace, torch.uint8, None, "workspace"),
-                                                  workspace.numel(), _stream_of(stream)), "splitzip_attention")
+    qs, ks, kind = q.shape, k_cache.shape, k_cache.dtype
+    qst, kst, vst, ost = q.stride(), k_cache.stride(), v_cache.stride(), out.stride()
+    ok = (len(qs) == 4 and len(ks) == 4 and qs[0] == ks[0] and qs[3] == ks[3] and v_cache.shape == ks and out.shape == qs
+          and q.dtype is _B16 and out.dtype is _B16 and (kind is _B16 or kind is _F8) and v_cache.dtype is kind
+          and qst[3] == 1 and kst[3] == 1 and vst[3] == 1 and ost[3] == 1 and window >= 0 and sinks >= 0
+          and q.is_cuda and k_cache.is_cuda and v_cache.is_cuda and out.is_cuda
+          and workspace.dtype is _U8 and workspace.is_contiguous() and workspace.is_cuda
+          and (lens is None or (lens.dtype is _I32 and lens.shape == qs[:1] and lens.is_contiguous() and lens.is_cuda))
+          and (lse is None or (lse.dtype is _F32 and lse.shape == (qs[0], qs[2], qs[1]) and lse.is_contiguous()
+                               and lse.is_cuda)))
+    if not ok:
+        _check_attention(q, k_cache, v_cache, out, workspace, lens, lse, window, sinks)
+    a = _ATTENTION.pack(q.data_ptr(), *qst[:3], k_cache.data_ptr(), *kst[:3], v_cache.data_ptr(), *vst[:3],
+                        out.data_ptr(), *ost[:3], 0 if lse is None else lse.data_ptr(),
+                        0 if lens is None else lens.data_ptr(), qs[0], qs[1], ks[1], qs[2], ks[2], qs[3],
+                        window if window < _MOST else _MOST, sinks if sinks < _MOST else _MOST, _FORMAT[kind],
+                        qs[3] ** -0.5 if scale is None else scale)
+    if _fn_attention is None:
+        library()
+    status = _fn_attention(a, workspace.data_ptr(), workspace.numel(), _stream_of(stream))
+    if status:
+        _check(status, "splitzip_attention")
 
 
 def splitzip_attention_status(workspace: torch.Tensor, stream=None) -> int:
     """Status of the attention calls on this workspace since the last report
     (OK or ERR_TIMEOUT); synchronises the stream."""
-    return int(library().splitzip_attention_status(_array(workspace, torch.uint8, None, "workspace"), _stream_of(stream)))
+    _check_array(workspace, _U8, None, "workspace")
+    return int(library().splitzip_attention_status(workspace.data_ptr(), _stream_of(stream)))
 
 
 def splitzip_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, weights_out: torch.Tensor,
@@ -280,21 +354,30 @@ def splitzip_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torc
     weight each slot gets from q's rows, whose lse splitzip_attention returned;
     asynchronous.  To weigh the tokens by the last queries only, pass those
     queries and their lse."""
-    qs, ks = q.shape, k_cache.shape
-    sizes = _sizes(qs, ks, _format(k_cache), window, sinks)
-    b, tq, tk, hq, hk, dim = sizes[:6]
-    _bf16(q, "q")
-    if ks[0] != b or ks[3] != dim:
-        _bad("q's batch and dims must be the cache's")
-    if lse is None or weights_out is None:
-        _bad("lse and weights_out are needed")
-    a = _ATTENTION.pack(*_view4(q, qs, "q"), *_view4(k_cache, ks, "k_cache"), *_NO_VIEW, *_NO_VIEW,
-                        _array(lse, torch.float32, (b, hq, tq), "lse"), _array(lens, torch.int32, (b,), "lens"),
-                        *sizes, dim ** -0.5 if scale is None else scale)
-    _check((_lib or library()).splitzip_attention_weights(
-        a, _array(weights_in, torch.float32, (b, hk, tk), "weights_in"),
-        _array(weights_out, torch.float32, (b, hk, tk), "weights_out"), _stream_of(stream)),
-        "splitzip_attention_weights")
+    qs, ks, kind = q.shape, k_cache.shape, k_cache.dtype
+    qst, kst = q.stride(), k_cache.stride()
+    ok = (len(qs) == 4 and len(ks) == 4 and qs[0] == ks[0] and qs[3] == ks[3] and q.dtype is _B16
+          and (kind is _B16 or kind is _F8) and qst[3] == 1 and kst[3] == 1 and window >= 0 and sinks >= 0
+          and q.is_cuda and k_cache.is_cuda and lse is not None and lse.dtype is _F32
+          and lse.shape == (qs[0], qs[2], qs[1]) and lse.is_contiguous() and lse.is_cuda)
+    if ok:
+        ws = (ks[0], ks[2], ks[1])
+        ok = (weights_out is not None and weights_out.dtype is _F32 and weights_out.shape == ws
+              and weights_out.is_contiguous() and weights_out.is_cuda
+              and (weights_in is None or weights_in is weights_out or (
+                  weights_in.dtype is _F32 and weights_in.shape == ws and weights_in.is_contiguous() and weights_in.is_cuda))
+              and (lens is None or (lens.dtype is _I32 and lens.shape == qs[:1] and lens.is_contiguous() and lens.is_cuda)))
+    if not ok:
+        _check_weights(q, k_cache, lse, weights_out, lens, weights_in, window, sinks)
+    a = _ATTENTION.pack(q.data_ptr(), *qst[:3], k_cache.data_ptr(), *kst[:3], *_NO_VIEW, *_NO_VIEW, lse.data_ptr(),
+                        0 if lens is None else lens.data_ptr(), qs[0], qs[1], ks[1], qs[2], ks[2], qs[3],
+                        window if window < _MOST else _MOST, sinks if sinks < _MOST else _MOST, _FORMAT[kind],
+                        qs[3] ** -0.5 if scale is None else scale)
+    if _fn_weights is None:
+        library()
+    status = _fn_weights(a, 0 if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(), _stream_of(stream))
+    if status:
+        _check(status, "splitzip_attention_weights")
 
 
 # -------------------------------------------------------------- eviction
@@ -306,19 +389,51 @@ def splitzip_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.
     """Keep, per sequence and head, the first keep_first, the last keep_last and
     the most attended slots, k_out.shape[1] in all; index [batch, kv_heads,
     budget] int32 receives the old slots, in order; asynchronous."""
-    ks, os = k_cache.shape, k_out.shape
-    fmt = _format(k_cache, v_cache)
-    if _format(k_out, v_out) != fmt:
+    ks, os, kind = k_cache.shape, k_out.shape, k_cache.dtype
+    kst, vst, kot, vot = k_cache.stride(), v_cache.stride(), k_out.stride(), v_out.stride()
+    ok = (len(ks) == 4 and len(os) == 4 and os[0] == ks[0] and os[2:] == ks[2:] and v_cache.shape == ks and v_out.shape == os
+          and (kind is _B16 or kind is _F8) and v_cache.dtype is kind and k_out.dtype is kind and v_out.dtype is kind
+          and kst[3] == 1 and vst[3] == 1 and kot[3] == 1 and vot[3] == 1 and keep_first >= 0 and keep_last >= 0
+          and k_cache.is_cuda and v_cache.is_cuda and k_out.is_cuda and v_out.is_cuda)
+    if ok:
+        b, t, h, dim = ks
+        budget = os[1]
+        kept = (b, h, budget)
+        ok = (weights.dtype is _F32 and weights.shape == (b, h, t) and weights.is_contiguous() and weights.is_cuda
+              and index.dtype is _I32 and index.shape == kept and index.is_contiguous() and index.is_cuda
+              and (weights_out is None or (weights_out.dtype is _F32 and weights_out.shape == kept
+                                           and weights_out.is_contiguous() and weights_out.is_cuda))
+              and (lens is None or (lens.dtype is _I32 and lens.shape == ks[:1] and lens.is_contiguous() and lens.is_cuda))
+              and (lens_out is None or (lens_out.dtype is _I32 and lens_out.shape == ks[:1] and lens_out.is_contiguous()
+                                        and lens_out.is_cuda)))
+    if not ok:
+        _check_evict(k_cache, v_cache, weights, k_out, v_out, index, lens, weights_out, lens_out, keep_first, keep_last)
+    a = _EVICT.pack(k_cache.data_ptr(), *kst[:3], v_cache.data_ptr(), *vst[:3], k_out.data_ptr(), *kot[:3],
+                    v_out.data_ptr(), *vot[:3], weights.data_ptr(), 0 if lens is None else lens.data_ptr(), index.data_ptr(),
+                    0 if weights_out is None else weights_out.data_ptr(), 0 if lens_out is None else lens_out.data_ptr(),
+                    b, t, h, dim, budget, keep_first if keep_first < _MOST else _MOST,
+                    keep_last if keep_last < _MOST else _MOST, _FORMAT[kind])
+    if _fn_evict is None:
+        library()
+    status = _fn_evict(a, _stream_of(stream))
+    if status:
+        _check(status, "splitzip_evict")
+
+
+def _check_evict(k_cache, v_cache, weights, k_out, v_out, index, lens, weights_out, lens_out, keep_first, keep_last):
+    if _format(k_out, v_out) != _format(k_cache, v_cache):
         _bad("the outputs must have the cache's type")
+    ks, os = tuple(k_cache.shape), tuple(k_out.shape)
     if len(ks) != 4 or len(os) != 4 or (os[0], *os[2:]) != (ks[0], *ks[2:]):
         _bad("the outputs must be [batch, budget, kv_heads, dim] of the cache")
     if keep_first < 0 or keep_last < 0:
         _bad("keep_first and keep_last are not negative")
-    b, t, h, dim = ks
-    budget = os[1]
-    a = _EVICT.pack(*_view4(k_cache, ks, "k_cache"), *_view4(v_cache, ks, "v_cache"), *_view4(k_out, os, "k_out"),
-                    *_view4(v_out, os, "v_out"), _array(weights, torch.float32, (b, h, t), "weights"),
-                    _array(lens, torch.int32, (b,), "lens"), _array(index, torch.int32, (b, h, budget), "index"),
-                    _array(weights_out, torch.float32, (b, h, budget), "weights_out"),
-                    _array(lens_out, torch.int32, (b,), "lens_out"), b, t, h, dim, budget, keep_first, keep_last, fmt)
-    _check((_lib or library()).splitzip_evict(a, _stream_of(stream)), "splitzip_evict")
+    for x, shape, what in ((k_cache, ks, "k_cache"), (v_cache, ks, "v_cache"), (k_out, os, "k_out"), (v_out, os, "v_out")):
+        _check_view(x, shape, what)
+    b, t, h, _ = ks
+    _check_array(weights, _F32, (b, h, t), "weights")
+    _check_array(index, _I32, (b, h, os[1]), "index")
+    _check_array(weights_out, _F32, (b, h, os[1]), "weights_out")
+    _check_array(lens, _I32, (b,), "lens")
+    _check_array(lens_out, _I32, (b,), "lens_out")
+    _bad("these arguments are not accepted")
