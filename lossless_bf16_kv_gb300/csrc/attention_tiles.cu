@@ -56,8 +56,8 @@ struct TilesShape {
     static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
     static constexpr int kRaw = kBN * D;         // bytes of one in E5M2
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
-    static constexpr int kStages = D == 128 ? (kF8 ? 3 : 5) : (kF8 ? 4 : 8);
-    static constexpr int kRaws = kF8 ? 3 : 0;
+    static constexpr int kStages = D == 128 ? (kF8 ? 4 : 5) : (kF8 ? 6 : 8);
+    static constexpr int kRaws = kF8 ? 2 : 0;
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
     static constexpr int kTend = kF8 ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
@@ -279,15 +279,17 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
     StepSlots slots(sh);
     const WholeTiles whole(sh, sh.p0, sh.p1);
     if constexpr (kF8) {
-        uint32_t st = 0, ph = 0, rs = 0, rph = 0;
-        for (uint32_t n = 0; n < 2 * steps; n++) {
-            if (!mbar_wait_bounded(&sh.raw_full[rs], rph, err)) break;
-            if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], ph ^ 1, err)) break;
-            const bool part = (n & 1) && (sh.p0 < 0 || !whole(slots.s0));
+        // Half of the warps widen the keys, half the values.
+        const uint32_t mine = thread >= 16 * S::kTend, in_half = thread - mine * 16 * S::kTend;
+        for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
+            const uint32_t rs = n % S::kRaws, st = n % S::kStages;
+            if (!mbar_wait_bounded(&sh.raw_full[rs], (n / S::kRaws) & 1, err)) break;
+            if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, err)) break;
+            const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
             bool found = false;
             // 16 bytes of a row become two adjacent 16-byte chunks of the swizzled row.
 #pragma unroll 4
-            for (uint32_t x = thread; x < S::kRaw / 16; x += 32 * S::kTend) {
+            for (uint32_t x = in_half; x < S::kRaw / 16; x += 16 * S::kTend) {
                 const uint32_t r = x / (D / 16), c = x % (D / 16);
                 const uint4 v = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + 16 * x);
                 uint4 lo = make_uint4(e5m2_01(v.x), e5m2_23(v.x), e5m2_01(v.y), e5m2_23(v.y));
@@ -298,10 +300,12 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
                     hi = make_uint4(finite_or_zero<true>(u.x), finite_or_zero<true>(u.y), finite_or_zero<true>(u.z), finite_or_zero<true>(u.w));
                     found |= l.x != lo.x || l.y != lo.y || l.z != lo.z || l.w != lo.w || u.x != hi.x || u.y != hi.y || u.z != hi.z || u.w != hi.w;
                 }
+                // Rows of the second block of 64 values store their upper half first, so that
+                // the eight lanes of a row hit different banks.
                 uint8_t* row = ring + st * S::kKV + (c >> 2) * (kBN * 128) + r * 128;
-                const uint32_t c0 = 2 * (c & 3);
-                *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = hi;
+                const uint32_t c0 = 2 * (c & 3), second = c >> 2;
+                *reinterpret_cast<uint4*>(row + (((c0 + second) ^ (r & 7)) << 4)) = second ? hi : lo;
+                *reinterpret_cast<uint4*>(row + (((c0 + 1 - second) ^ (r & 7)) << 4)) = second ? lo : hi;
             }
             if (found) sh.odd = 1;
             fence_async_proxy();
@@ -309,11 +313,8 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
             if (lane == 0) {
                 mbar_arrive(&sh.raw_empty[rs]);
                 mbar_arrive(&sh.full[st]);
-                if (n & 1) mbar_arrive(&sh.ok[(n >> 1) & 7]);
+                if (mine) mbar_arrive(&sh.ok[(n >> 1) & 7]);
             }
-            if (n & 1) slots.next();
-            if (++st == S::kStages) st = 0, ph ^= 1;
-            if (++rs == S::kRaws) rs = 0, rph ^= 1;
         }
     } else {
         for (uint32_t i = 0; i < steps; i++, slots.next()) {
@@ -540,13 +541,13 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
             sh.whole_sinks = whole.sinks;
         }
         for (int i = 0; i < 8; i++) {
-            mbar_init(&sh.full[i], kF8 ? S::kTend : 1);
+            mbar_init(&sh.full[i], kF8 ? S::kTend / 2 : 1);
             mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.ok[i], S::kTend);
+            mbar_init(&sh.ok[i], kF8 ? S::kTend / 2 : S::kTend);
         }
         for (int i = 0; i < 3; i++) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], S::kTend);
+            mbar_init(&sh.raw_empty[i], S::kTend / 2);
         }
         mbar_init(&sh.q_full, kF8 ? kSoftmax : 1);
         for (int i = 0; i < 2; i++) {
