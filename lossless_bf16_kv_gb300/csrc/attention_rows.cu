@@ -509,21 +509,17 @@ bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     // The slots a row tile can see at most.
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
-    // The splits with the least time, taken as waves of CTAs times the tiles of
-    // each warp in a split plus kSplitCost tiles for a CTA's start and join, of
-    // those that leave each warp two tiles.  Up to eight splits are one cluster,
-    // more are clusters of eight.
-    constexpr uint64_t kSplitCost = 2;
-    const uint64_t wave = (p.tile_rows == 16 ? kCtasPerSm : 2) * kSms, tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
-    uint64_t best = ~0ull;
-    p.splits = 1;
-    for (uint64_t n = 1; n == 1 || (n * 2 <= tiles && units * n <= 16 * wave && (n <= 8 || units <= kSms)); n += n < 8 ? 1 : 8) {
-        const uint64_t time = (units * n + wave - 1) / wave * ((tiles + n - 1) / n + kSplitCost);
-        if (time < best) {
-            best = time;
-            p.splits = (uint32_t)n;
-        }
-    }
+    // As many splits as fill the GPU with CTAs at once, of which each warp has at
+    // least two tiles.  Three 16-row CTAs fit an SM and two 32-row ones, but clusters
+    // do not fill every SM: at 64 units of 8192 slots 6 splits (384 CTAs) take 44 us, 7
+    // (448) 59, 3 50; at 128 units of 16384 slots 3 take 154, 4 191, 6 158; 32-row tiles
+    // there take 175 with 2 (256 CTAs) and 243 with 3.  Up to eight splits are one
+    // cluster, more are clusters of eight, and fewer CTAs do then: 8 units of 131072
+    // slots take 88 us with 32 and with 40 splits, 115 with 56.
+    const uint64_t fill = p.tile_rows == 16 ? 384 : 256, tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
+    uint64_t splits = std::min(fill / units, tiles / 2);
+    if (splits > 8) splits = std::max((uint64_t)8, std::min(splits, 320 / units) / 8 * 8);
+    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
     if (units * p.splits > 0x7FFFFFFFull) return false;
     static_assert(4 * kSms <= kAttentionStatus, "splits in several clusters are counted by row tile");
     p.bytes = kAttentionHeader + (p.splits > 8 ? units * (p.splits / 8) * p.tile_rows * (a.head_dim + 4) * 4 : 0);
