@@ -126,6 +126,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+template <bool kHalf>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 
 // --------------------------------------------------------- E5M2 operands
 //

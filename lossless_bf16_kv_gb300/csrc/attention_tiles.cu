@@ -68,8 +68,8 @@ struct TilesShape {
     // Tensor memory: S of the query tiles from column 0, O, and P over S or apart.
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColO = 2 * kBN, kColP = kApart ? kColO + 2 * D : 0, kStepP = kApart ? kBN / 2 : kBN;
-    static constexpr int kTiles = 2 * kQ + kStages * kKV + kRaws * kRaw;
-    static constexpr int kUsed = kTiles + (kApart ? 2048 : 0);  // and a second exchange of the rows
+    static constexpr uint32_t kHalfP = kApart ? kBN / 4 : kBN / 2;  // over S, each half of P over its own scores
+    static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * kRaw;
     static_assert(kUsed >= 2 * kTileM * kRowFloats * 4, "partial results take the place of the tiles");
 };
 
@@ -199,7 +199,7 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
         const uint32_t o = tmem + S::kColO + t * D, pa = tmem + S::kColP + t * S::kStepP;
         mma_ts(o, pa, desc(va, 0), kShapeO, add);
 #pragma unroll
-        for (int k = 1; k < kBN / 16; k++) mma_ts(o, pa + 8 * k, desc(va, k * 2048), kShapeO, true);
+        for (int k = 1; k < kBN / 16; k++) mma_ts(o, pa + (k >> 2) * S::kHalfP + (k & 3) * 8, desc(va, k * 2048), kShapeO, true);
     };
     uint32_t st = 0, ph = 0;
     auto next = [&]() {
@@ -348,10 +348,10 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
 // half's sum.  Returns false where a wait gave up.
 template <int D, bool kF8>
 __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
-                                             uint32_t r, uint32_t pair_bar, float* row2, int32_t pos, float scale, float& m, float& l) {
+                                             uint32_t r, uint32_t pair_bar, int32_t pos, float scale, float& m, float& l) {
     volatile uint32_t* err = &sh.err;
     using S = TilesShape<D, kF8>;
-    const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + 32 * half;
+    const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + half * S::kHalfP;
     // What a step needs only a moment is read again from shared memory, as volatile.
     const volatile TilesShared& now_sh = sh;
     int32_t s0 = sh.s0;
@@ -392,42 +392,15 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         }
         s0 = (int32_t)i + 1 == jump_at ? jump_to : s0 + kBN;
         const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-        float* row = S::kApart && (i & 1) ? row2 : &sh.row[0][0][0];
-        row[(2 * t + half) * kTileM + r] = own;
-        // The two warps of these rows also have their scores in registers after this,
-        // so P may go over S.  Where one's wait gave up, both return.
-        if (named_any(pair_bar, 64, !ready)) return false;
-        if constexpr (S::kApart) {  // the last step's product is done with P and O
-            if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, err);
+        if constexpr (S::kApart) {  // the last step's product is done with P
+            if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, err) && ready;
             tcgen_fence_after();
             __syncwarp();
         }
-        const float now = fmaxf(own, row[(2 * t + (half ^ 1)) * kTileM + r]);
-        const bool raise = now > m + kLazy;  // from -inf too
-        if (__any_sync(0xFFFFFFFFu, raise)) {
-            const float f = raise ? exp2_approx(m - now) : 1.0f;
-            if (raise) m = now;
-            l *= f;
-            if (i) {  // this half's columns of O
-                const uint64_t ff = pair(f, f);
-#pragma unroll
-                for (int c = 0; c < D / 16; c++) {
-                    uint32_t o[8];
-                    tmem_ld8(o, oa + 8 * c);
-                    tmem_wait_ld();
-                    tmem_loaded(o);
-#pragma unroll
-                    for (int x = 0; x < 8; x += 2) {
-                        float u, v;
-                        unpair(mul2(pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), ff), u, v);
-                        o[x] = __float_as_uint(u);
-                        o[x + 1] = __float_as_uint(v);
-                    }
-                    tmem_st<8>(oa + 8 * c, o);
-                }
-            }
-        }
-        const float use = m == -INFINITY ? 0.0f : m;
+        // P of this half by the maximum that it would choose; an integer, so that P can
+        // be brought to another one without a second rounding.
+        const float mine = own > m + kLazy ? ceilf(own) : m;  // from -inf too
+        const float use = mine == -INFINITY ? 0.0f : mine;
         const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -449,8 +422,54 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         float u, v, u2, v2;
         unpair(sum[0], u, v);
         unpair(sum[1], u2, v2);
-        l += (u + v) + (u2 + v2);
+        float add = (u + v) + (u2 + v2);
         tmem_wait_st();
+        // In the first step and rarely after it one of the rows of these two warps has a
+        // new maximum, and they settle on one.  Where one's wait gave up, both return.
+        if (named_any(pair_bar, 64, mine != m || !ready)) {
+            sh.row[t][half][r] = mine;
+            if (named_any(pair_bar, 64, !ready)) return false;
+            const float now = fmaxf(mine, sh.row[t][half ^ 1][r]);
+            const float f = m == now ? 1.0f : exp2_approx(m - now), g = mine == now ? 1.0f : exp2_approx(mine - now);
+            m = now;
+            l *= f;
+            add *= g;
+            if (i) {  // this half's columns of O
+                const uint64_t ff = pair(f, f);
+#pragma unroll
+                for (int c = 0; c < D / 16; c++) {
+                    uint32_t o[8];
+                    tmem_ld8(o, oa + 8 * c);
+                    tmem_wait_ld();
+                    tmem_loaded(o);
+#pragma unroll
+                    for (int x = 0; x < 8; x += 2) {
+                        float u, v;
+                        unpair(mul2(pair(__uint_as_float(o[x]), __uint_as_float(o[x + 1])), ff), u, v);
+                        o[x] = __float_as_uint(u);
+                        o[x + 1] = __float_as_uint(v);
+                    }
+                    tmem_st<8>(oa + 8 * c, o);
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, mine != now)) {
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t w[8];
+                    tmem_ld8(w, pa + 8 * c);
+                    tmem_wait_ld();
+                    tmem_loaded(w);
+#pragma unroll
+                    for (int x = 0; x < 8; x++) {
+                        const float2 y = unpack2<kF8>(w[x]);
+                        w[x] = pack2<kF8>(y.x * g, y.y * g);
+                    }
+                    tmem_st<8>(pa + 8 * c, w);
+                }
+            }
+            tmem_wait_st();
+        }
+        l += add;
         tcgen_fence_before();
         __syncwarp();
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[t]);
@@ -631,7 +650,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
                 fence_async_proxy();
                 mbar_arrive(&sh.q_full);
             }
-            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pair_bar, reinterpret_cast<float*>(qs + S::kTiles), pos, scale, m, l);
+            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pair_bar, pos, scale, m, l);
         }
         // The row's sum, of both halves in the same order.
         __syncwarp();
