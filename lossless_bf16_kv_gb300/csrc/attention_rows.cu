@@ -509,17 +509,25 @@ bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     // The slots a row tile can see at most.
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
-    // As many splits as fill the GPU with CTAs at once, of which each warp has at
-    // least two tiles.  Three 16-row CTAs fit an SM and two 32-row ones, but clusters
-    // do not fill every SM: at 64 units of 8192 slots 6 splits (384 CTAs) take 44 us, 7
-    // (448) 59, 3 50; at 128 units of 16384 slots 3 take 154, 4 191, 6 158; 32-row tiles
-    // there take 175 with 2 (256 CTAs) and 243 with 3.  Up to eight splits are one
-    // cluster, more are clusters of eight, and fewer CTAs do then: 8 units of 131072
-    // slots take 88 us with 32 and with 40 splits, 115 with 56.
-    const uint64_t fill = p.tile_rows == 16 ? 384 : 256, tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
-    uint64_t splits = std::min(fill / units, tiles / 2);
-    if (splits > 8) splits = std::max((uint64_t)8, std::min(splits, 320 / units) / 8 * 8);
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits);
+    // As many splits as run at once, of which each warp has a tile of slots (512 slots of
+    // 8 units: 5.8 us with 8 splits, 6.6 with 4).  Three 16-row CTAs fit an SM, but a
+    // cluster lies within one of the GPU's groups of SMs, and fewer of the large ones run
+    // at once (as cudaOccupancyMaxActiveClusters has it): 64 units of 8192 slots take 44 us
+    // in 6 splits, 59 in 7, 50 in 3; 128 units of 16384 slots 154 in 3, 191 in 4, 158 in 6.
+    // Of 32-row CTAs two fit, and 256 are few enough for all sizes: 128 units of 16384
+    // slots take 175 us in 2 splits and 243 in 3.
+    static constexpr uint64_t kAtOnce[9] = {0, 3 * kSms, 228, 148, 110, 87, 74, 59, 51};
+    const uint64_t tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
+    uint64_t splits = 8;
+    while (splits > 1 && (splits > tiles || units > (p.tile_rows == 16 ? kAtOnce[splits] : 256 / splits))) splits--;
+    // Up to eight splits are one cluster.  More are clusters of eight, of which the last
+    // one joins all: that costs as much as a few tiles, more with more to join.  8 units,
+    // 16-row tiles: 4096 slots of 64 take 7.5 us with 8 splits and 8.6 with 32, 8192 of
+    // 128 16.6 and 12.2 (13.0 with 40); 32-row tiles: 4096 of 128 18.2 and 22.3, 12000
+    // 33.9 and 27.7; 131072 slots of 128 take 88 us with 32 splits, 115 with 56.
+    const uint64_t more = std::min(256 / units, tiles) / 8 * 8, join = p.tile_rows * a.head_dim > 2048 ? 10 : 4;
+    if (more > 8 && tiles / more + join < tiles / 8) splits = more;
+    p.splits = (uint32_t)splits;
     if (units * p.splits > 0x7FFFFFFFull) return false;
     static_assert(4 * kSms <= kAttentionStatus, "splits in several clusters are counted by row tile");
     p.bytes = kAttentionHeader + (p.splits > 8 ? units * (p.splits / 8) * p.tile_rows * (a.head_dim + 4) * 4 : 0);
