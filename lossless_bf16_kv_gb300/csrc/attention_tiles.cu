@@ -773,13 +773,16 @@ bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     uint64_t most = (a.kv_tokens + kBN - 1) / kBN;
     if (a.window)
         most = std::min(most, ((uint64_t)a.window + 2 * tokens + kBN - 1) / kBN + 1 + ((uint64_t)a.sinks + kBN - 1) / kBN);
-    // The splits (one cluster) with the least time, as waves of one CTA per SM times
-    // the steps of a split plus kSplitCost steps for a CTA's start, join and end.
-    constexpr uint64_t kSplitCost = 4;
+    // The splits (one cluster) with the least time, as waves of clusters times the steps
+    // of a split plus kSplitCost steps for a CTA's start, join and end.  A cluster lies
+    // within one of the GPU's groups of SMs, so fewer of the large ones run at once (as
+    // cudaOccupancyMaxActiveClusters has it): 16 units of 2048 slots of 64 take 20.6 us
+    // in 8 splits, two waves, and 11.7 in 6.
+    constexpr uint64_t kSplitCost = 4, kAtOnce[9] = {0, kSms, 76, 46, 36, 28, 23, 15, 15};
     uint64_t best = ~0ull;
     p.splits = 1;
     for (uint64_t n = 1; n <= 8 && (n == 1 || 2 * n <= most); n++) {
-        const uint64_t time = (units * n + kSms - 1) / kSms * ((most + n - 1) / n + kSplitCost);
+        const uint64_t time = (units + kAtOnce[n] - 1) / kAtOnce[n] * ((most + n - 1) / n + kSplitCost);
         if (time < best) {
             best = time;
             p.splits = (uint32_t)n;
