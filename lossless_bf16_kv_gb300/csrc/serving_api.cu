@@ -35,8 +35,16 @@ bool sizes_ok(const splitzip_attention_args& a) {
            (uint64_t)a.batch * a.kv_heads <= kMax31;
 }
 
-// Tiles of 256 query rows on the tensor cores from 33 rows on (more than the
-// other kernel's largest tile), for the cases that kernel takes.
+// Tiles of 256 query rows on the tensor cores from 33 rows of a key/value head on
+// (the other kernel's largest tile, past which it reads the cache twice), from 65 on
+// for an E5M2 cache, which that kernel widens at less cost; only for scales that
+// kernel takes.  128 units of 16384 slots, head_dim 128, in us, this kernel and the
+// other: BF16 32 rows 217 and 176, 40 rows 217 and 320; E5M2 64 rows 300 and 276, 96
+// rows 302 and 443.  16 units of 2048: BF16 40 rows 13.5 and 17.2, E5M2 64 rows 17.5
+// and 16.3, 96 rows 17.9 and 19.5.
+bool on_tiles(const splitzip_attention_args& a, const AttentionPlan& rows) {
+    return rows.rows > (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 64u : 32u) && attention_tiles_usable(a);
+}
 bool plans(const splitzip_attention_args& a, AttentionPlan& rows, AttentionPlan& tiles) {
     return attention_rows_plan(a, rows) && attention_tiles_plan(a, tiles);
 }
@@ -87,7 +95,7 @@ splitzip_status splitzip_attention(const splitzip_attention_args* a, void* works
     if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < bytes_of(rows, tiles))
         return SPLITZIP_ERR_INVALID_ARG;
-    if (rows.rows > 32 && attention_tiles_usable(*a))
+    if (on_tiles(*a, rows))
         return from_cuda(launch_attention_tiles(*a, tiles, workspace, (cudaStream_t)s));
     return from_cuda(launch_attention_rows(*a, rows, workspace, (cudaStream_t)s));
 }
