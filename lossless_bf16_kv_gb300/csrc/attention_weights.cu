@@ -380,33 +380,33 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
         n += i;
         for (; i < steps; i += 2, n += 2) {
             const uint32_t x = n & 3, mx = n % kMetas;
-            if (!mbar_wait_bounded(&sh.meta_full[mx], (n / kMetas) & 1, err) || !mbar_wait_bounded(&sh.s_full[x], (n >> 2) & 1, err)) {
+            const uint32_t m_at = (n / kMetas) & 1, s_at = (n >> 2) & 1;
+            const bool m_there = mbar_try_wait(&sh.meta_full[mx], m_at), s_there = mbar_try_wait(&sh.s_full[x], s_at);  // mostly both
+            const bool there = (m_there & s_there) || (mbar_wait_bounded(&sh.meta_full[mx], m_at, err) && mbar_wait_bounded(&sh.s_full[x], s_at, err));
+            if (!__all_sync(0xFFFFFFFFu, there)) {
                 sum = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
                 continue;
             }
             tcgen_fence_after();
-            __syncwarp();
             const uint32_t sa = tmem + x * kRowTile + c0;
-            uint32_t s[2][16];  // sixteen columns, and the next sixteen on their way
-            tmem_ld16(s[0], sa);
+            uint32_t s[2][32];
+            tmem_ld32(s[0], sa);
+            tmem_ld32(s[1], sa + 32);
             const bool whole = i >= whole_lo && i < whole_hi;
             uint64_t part[2] = {0, 0};
+            tmem_wait_ld();
+            tmem_loaded(s[0]);
+            tmem_loaded(s[1]);
+            tcgen_fence_before();
+            __syncwarp();
+            if ((r & 31) == 0) mbar_arrive(&sh.s_free[x]);
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t(&v)[16] = s[c & 1];
-                tmem_wait_ld();
-                tmem_loaded(v);
-                if (c < 3) {
-                    tmem_ld16(s[(c + 1) & 1], sa + 16 * (c + 1));
-                } else {
-                    tcgen_fence_before();
-                    __syncwarp();
-                    if ((r & 31) == 0) mbar_arrive(&sh.s_free[x]);
-                }
+            for (int c = 0; c < 2; c++) {
+                uint32_t(&v)[32] = s[c];
                 const auto add = [&](auto masked, uint32_t in) {
 #pragma unroll
-                    for (int y = 0; y < 16; y += 4) {
-                        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&sh.lse[mx][c0 + 16 * c + y]);
+                    for (int y = 0; y < 32; y += 4) {
+                        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(&sh.lse[mx][c0 + 32 * c + y]);
 #pragma unroll
                         for (int z = 0; z < 4; z += 2) {
                             float e, f;
@@ -421,16 +421,16 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
                         }
                     }
                 };
-                if (whole && (full || p.tokens * p.group >= c0 + 16 * c + 16)) {
+                if (whole && (full || p.tokens * p.group >= c0 + 32 * c + 32)) {
                     add(std::false_type(), 0u);
                 } else {
                     // This tile's columns that the slot takes part in.
-                    const int32_t t0 = (int32_t)i * tokens, col = (int32_t)c0 + 16 * c;
+                    const int32_t t0 = (int32_t)i * tokens, col = (int32_t)c0 + 32 * c;
                     const int32_t l = max(0, min(tokens, w.see_from(r) - t0)) * group - col;
                     const int32_t u = max(0, min(tokens, w.see_end(p, r) - t0)) * group - col;
                     const uint32_t from = l <= 0 ? 0xFFFFFFFFu : l > 31 ? 0u : 0xFFFFFFFFu << l;
                     const uint32_t below = u <= 0 ? 0u : u > 31 ? 0xFFFFFFFFu : ~(0xFFFFFFFFu << u);
-                    if (__any_sync(0xFFFFFFFFu, from & below & 0xFFFFu)) add(std::true_type(), from & below);
+                    if (__any_sync(0xFFFFFFFFu, from & below)) add(std::true_type(), from & below);
                 }
             }
             float u, v, u2, v2;
