@@ -13,6 +13,14 @@
 // always in the same order.  Every key and value is read once: HBM bounds it.
 // A warp keeps a private ring of slot tiles filled by cp.async, so nothing in
 // the loop waits for another warp.
+//
+// The products are mma.sync: with one token of a group of four to eight heads
+// most rows of a 128-row tensor-memory tile would be padding, and at 16 rows the
+// tensor units are 16% busy here.  16 sequences of 16384 tokens, 8 heads of 128
+// for 32 query heads: 153 us in BF16 (7.0 TB/s, above a copy's 6.8: nothing is
+// written), 87 us in E5M2 (6.2 TB/s, next to the widening).  One sequence: 16.8
+// and 13.8 us, of which 5.6 are what a call of 128 slots takes, its chain of
+// loads, products and joins.
 #include <algorithm>
 #include <cstdint>
 
