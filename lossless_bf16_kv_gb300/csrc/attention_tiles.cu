@@ -25,6 +25,11 @@
 // in BF16, 500 in E5M2; head_dim 64 273 (1.0) and 338.  16384 tokens in a window
 // of 4096 with sinks, head_dim 128: 731-735 us (1.31).
 //
+// Where one tile holds all rows, both tiles of a CTA are that one (twins): each
+// takes every other tile of slots, and they are joined like splits.  64 rows over
+// 128 caches of 16384 slots: head_dim 128 161 us, 6.7 TB/s (217 with the second
+// tile empty), head_dim 64 92 (172).
+//
 // Roles: warps 0-15 softmax (four per tile and half of the slots), 16 issues
 // the products of both tiles (from two warps they interleave and both tiles wait
 // for both: 734 against 879 us at 16k), 17 the TMA loads; the rest keep
@@ -46,6 +51,7 @@
 // cost 285 us where this takes 273.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "tcgen.cuh"
@@ -106,10 +112,7 @@ struct TilesShared {
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
     int32_t upto[2], after[2], whole_sinks;  // WholeTiles of the query tiles
-    // Exchanged by the two threads of a row.  With P over S a step's S is only there
-    // once every warp of the tile has handed over the last step's P, so one value
-    // does; with P apart the steps take turns with a second array.
-    float row[2][2][kTileM];
+    float row[2][2][kTileM];  // exchanged by the two threads of a row
 };
 
 // The first slot of each step in turn.
@@ -143,7 +146,7 @@ __device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t lo, int32_t s
 
 // ------------------------------------------------------------------ roles
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw) {
     using S = TilesShape<D, kF8>;
     volatile uint32_t* err = &sh.err;
@@ -156,7 +159,7 @@ __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh
 #pragma unroll
             for (int i = 0; i < D / 64; i++)
                 tma_load4(qs + t * S::kQ + i * (kTileM * 128), &p.qmap, 64 * i, h * (int32_t)p.group,
-                          (int32_t)(sh.t0 + t * p.tokens), p.one_q ? 0 : b, &sh.q_full);
+                          (int32_t)(sh.t0 + (kTwin ? 0 : t * p.tokens)), p.one_q ? 0 : b, &sh.q_full);
     }
     constexpr int kN = kF8 ? S::kRaws : S::kStages;
     uint64_t* full = kF8 ? sh.raw_full : sh.full;
@@ -184,7 +187,7 @@ __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh
     for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded(&full[x % kN], (x / kN) & 1, &late);
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, const uint8_t* qs, const uint8_t* ring) {
     using S = TilesShape<D, kF8>;
     constexpr uint32_t kShapeS = mma_shape(kF8, kBN, false), kShapeO = mma_shape(kF8, D, true);
@@ -209,6 +212,49 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
         mma_ts(o, pa, desc(va, 0), kShapeO, add);
 #pragma unroll
         for (int k = 1; k < kBN / 16; k++) mma_ts(o, pa + (k >> 2) * S::kHalfP + (k & 3) * 8, desc(va, k * 2048), kShapeO, true);
+    };
+    // Twins: slot tile j is tile j & 1's.  Its next keys are four stages on at most.
+    static_assert(S::kStages >= 4, "the ring reaches from a slot tile's values to the next but one's keys");
+    const auto run_twins = [&]() {
+        const auto at = [](uint32_t n) { return n % S::kStages; };
+        const auto loaded = [&](uint32_t n) { return mbar_wait_bounded(&sh.full[at(n)], (n / S::kStages) & 1, err); };
+        if (!mbar_wait_bounded(&sh.q_full, 0, err)) return;
+        for (uint32_t j = 0; j < min(steps, 2u); j++) {
+            if (!loaded(2 * j)) return;
+            tcgen_fence_after();
+            if (leader) {
+                issue_s(j, at(2 * j));
+                mma_commit(&sh.empty[at(2 * j)]);
+            }
+            __syncwarp();
+        }
+        for (uint32_t j = 0; j < steps; j++) {
+            const uint32_t t = j & 1, vst = at(2 * j + 1), kst = at(2 * j + 4), turn = (j >> 1) & 1;
+            const bool more = j + 2 < steps;
+            const auto next_s = [&]() {
+                if (!loaded(2 * j + 4)) return false;
+                tcgen_fence_after();
+                if (leader) {
+                    issue_s(t, kst);
+                    mma_commit(&sh.empty[kst]);
+                }
+                __syncwarp();
+                return true;
+            };
+            if (!mbar_wait_bounded(&sh.ok[j & 7], (j >> 3) & 1, err) || !loaded(2 * j + 1)) return;
+            if (S::kApart && more && !(mbar_wait_bounded(&sh.s_free[t], turn, err) && next_s())) return;
+            if (!mbar_wait_bounded(&sh.p_full[t], turn, err)) return;
+            tcgen_fence_after();
+            if (leader) {
+                issue_o(t, vst, j > 1);
+                mma_commit(&sh.empty[vst]);
+                if (S::kApart && more) mma_commit(&sh.o_done[t]);
+                if (!more) mma_commit(&sh.o_full[t]);
+                if (steps == 1) mma_commit(&sh.o_full[1]);
+            }
+            __syncwarp();
+            if (!S::kApart && more && !next_s()) return;
+        }
     };
     uint32_t st = 0, ph = 0;
     auto next = [&]() {
@@ -271,7 +317,8 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
             __syncwarp();
         }
     };
-    run();
+    if constexpr (kTwin) run_twins();
+    else run();
     uint32_t late = 0;
     __syncwarp();
     if (leader) mma_commit(&sh.drained);
@@ -355,7 +402,7 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
 
 // The rows' softmax, slots 64 half .. 64 half + 63 of each step.  l is this
 // half's sum.  Returns false where a wait gave up.
-template <int D, bool kF8>
+template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
                                              uint32_t r, uint32_t pair_bar, int32_t pos, float scale, float& m, float& l) {
     volatile uint32_t* err = &sh.err;
@@ -363,10 +410,14 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
     const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + half * S::kHalfP;
     // What a step needs only a moment is read again from shared memory, as volatile.
     const volatile TilesShared& now_sh = sh;
+    constexpr uint32_t kStride = kTwin ? 2 : 1;  // from this tile's slot tile to its next
+    uint32_t j = 0;
     int32_t s0 = sh.s0;
+    const auto advance = [&](int32_t at, int32_t to) { s0 = (int32_t)++j == at ? to : s0 + kBN; };
+    if (kTwin && t) advance(sh.jump_at, sh.jump_to);
     m = -INFINITY;
     l = 0.0f;
-    bool ready = true, more = now_sh.steps != 0;
+    bool ready = true, more = j < now_sh.steps;
     for (uint32_t i = 0; more; i++) {
         ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err) && ready;
         tcgen_fence_after();
@@ -376,7 +427,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         const int32_t upto = now_sh.upto[t], after = now_sh.after[t], whole_sinks = now_sh.whole_sinks;
         const int32_t jump_at = now_sh.jump_at, jump_to = now_sh.jump_to;
         const bool part = !((s0 <= upto) & ((s0 > after) | (s0 <= whole_sinks)));
-        more = i + 1 < now_sh.steps;
+        more = j + kStride < now_sh.steps;
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         tmem_wait_ld();
         tmem_loaded(s[0]);
@@ -399,7 +450,8 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
             for (int x = 0; x < 32; x += 2)
                 top[(x >> 1) & 3] = max3(top[(x >> 1) & 3], __uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1]));
         }
-        s0 = (int32_t)i + 1 == jump_at ? jump_to : s0 + kBN;
+        advance(jump_at, jump_to);
+        if (kTwin) advance(jump_at, jump_to);
         const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
         if constexpr (S::kApart) {  // the last step's product is done with P
             if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, err) && ready;
@@ -484,25 +536,27 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[t]);
     }
     // Both tiles' products are done: a CTA's partial results take the tiles' place.
-    const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[t], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
+    const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[0], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
     tcgen_fence_after();
     return go;
 }
 
 // Columns 32 c .. 32 c + 31 of this row of O.
-template <int D, bool kF8>
-__device__ __forceinline__ void read_output(const TilesParams& p, const TilesShared& sh, uint32_t oa, int32_t pos, int c, float (&o)[32]) {
+template <int D, bool kF8, bool kTwin>
+__device__ __forceinline__ void read_output(const TilesParams& p, const TilesShared& sh, uint32_t oa, uint32_t t, int32_t pos, int c,
+                                            float (&o)[32]) {
     constexpr int kElem = kF8 ? 1 : 2;
     const uint32_t steps = sh.steps;
+    const bool any = kTwin ? steps > t : steps != 0;
     uint32_t w[32];
     __syncwarp();
-    if (steps) {
+    if (any) {
         tmem_ld32(w, oa + 32 * c);
         tmem_wait_ld();
         tmem_loaded(w);
     }
 #pragma unroll
-    for (int x = 0; x < 32; x++) o[x] = steps ? __uint_as_float(w[x]) : 0.0f;
+    for (int x = 0; x < 32; x++) o[x] = any ? __uint_as_float(w[x]) : 0.0f;
     if (*reinterpret_cast<const volatile uint32_t*>(&sh.odd)) {
         // The infinite and NaN values of partly visible tiles go to the rows that
         // see them: whatever their (positive) weight, the sum takes their value.
@@ -512,7 +566,7 @@ __device__ __forceinline__ void read_output(const TilesParams& p, const TilesSha
         const uint8_t* vbase = static_cast<const uint8_t*>(p.a.v.data) + ((int64_t)sh.b * p.a.v.stride_b + (int64_t)sh.h * p.a.v.stride_h + 32 * c) * kElem;
         StepSlots slots(sh);
         for (uint32_t i = 0; i < steps; i++, slots.next()) {
-            if (sh.p0 >= 0 && whole(slots.s0)) continue;
+            if ((kTwin && (i & 1) != t) || (sh.p0 >= 0 && whole(slots.s0))) continue;
             for (int32_t s = slots.s0; s < min(slots.s0 + kBN, n); s++) {
                 if (!((uint32_t)(pos - s) < window || (s < sinks && s <= pos))) continue;
                 const uint8_t* row = vbase + s * p.a.v.stride_t * kElem;
@@ -527,7 +581,7 @@ __device__ __forceinline__ void read_output(const TilesParams& p, const TilesSha
     }
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kTwin>
 __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(const __grid_constant__ TilesParams p) {
     using S = TilesShape<D, kF8>;
     extern __shared__ __align__(1024) uint8_t qs[];
@@ -562,7 +616,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
         sh.window = mask.window;
         for (int t = 0; t < 2; t++) {
             // No tile of slots is whole for a tile without queries.
-            const uint32_t ta = t0 + t * p.tokens, tb = min(ta + p.tokens, a.q_tokens);
+            const uint32_t ta = t0 + (kTwin ? 0 : t * p.tokens), tb = min(ta + p.tokens, a.q_tokens);
             const WholeTiles whole(sh, mask.first + (int32_t)ta, mask.first + (int32_t)tb - 1);
             sh.upto[t] = ta < a.q_tokens ? whole.upto : -1;
             sh.after[t] = whole.after;
@@ -608,12 +662,12 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
     if (warp >= 16) {
         regs_dec<S::kOtherRegs>();
         if (sh.steps) {
-            if (warp == 16) issue_products<D, kF8>(sh, tmem, qs, ring);
+            if (warp == 16) issue_products<D, kF8, kTwin>(sh, tmem, qs, ring);
             else if (warp > 17) tend_values<D, kF8>(sh, ring, raw, threadIdx.x - (kSoftmax + 64));
-            else if ((threadIdx.x & 31) == 0) load_tiles<D, kF8>(p, sh, qs, ring, raw);
+            else if ((threadIdx.x & 31) == 0) load_tiles<D, kF8, kTwin>(p, sh, qs, ring, raw);
         }
         __syncwarp();
-        if (p.splits > 1) {  // with the softmax warps below
+        if (kTwin || p.splits > 1) {  // with the softmax warps below
             cluster_sync();
             cluster_sync();
         }
@@ -624,7 +678,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
         float m, l;
         bool go;
         {
-            const uint32_t tok = sh.t0 + t * p.tokens + r / p.group, g = r % p.group;
+            const uint32_t tok = sh.t0 + (kTwin ? 0 : t * p.tokens) + r / p.group, g = r % p.group;
             const bool valid = r < p.tokens * p.group && tok < p.a.q_tokens;
             const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
             float scale = p.a.scale * kLog2e;
@@ -659,7 +713,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
                 fence_async_proxy();
                 mbar_arrive(&sh.q_full);
             }
-            go = softmax_rows<D, kF8>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pair_bar, pos, scale, m, l);
+            go = softmax_rows<D, kF8, kTwin>(p, sh, tmem + (((warp & 3) * 32) << 16), t, half, r, pair_bar, pos, scale, m, l);
         }
         // The row's sum, of both halves in the same order.
         __syncwarp();
@@ -671,19 +725,19 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
 
         // Derived again rather than kept through the loop.
         const uint32_t rr = opaque(threadIdx.x) & 127;
-        const uint32_t tok = sh.t0 + t * p.tokens + rr / p.group, g = rr % p.group, hq = sh.h * p.group + g;
+        const uint32_t tok = sh.t0 + (kTwin ? 0 : t * p.tokens) + rr / p.group, g = rr % p.group, hq = sh.h * p.group + g;
         const bool valid = rr < p.tokens * p.group && tok < p.a.q_tokens;
         const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
         const uint32_t oa = tmem + (((warp & 3) * 32) << 16) + S::kColO + t * D;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out.data) + (int64_t)sh.b * p.a.out.stride_b +
                              (int64_t)tok * p.a.out.stride_t + (int64_t)hq * p.a.out.stride_h;
         float* lse = p.a.lse ? p.a.lse + ((uint64_t)sh.b * p.a.q_heads + hq) * p.a.q_tokens + tok : nullptr;
-        if (p.splits == 1) {
+        if (!kTwin && p.splits == 1) {
             const float inv = 1.0f / l;
 #pragma unroll 1
             for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
                 float o[32];
-                read_output<D, kF8>(p, sh, oa, pos, c, o);
+                read_output<D, kF8, kTwin>(p, sh, oa, t, pos, c, o);
                 if (valid) {
 #pragma unroll
                     for (int x = 0; x < 32; x += 8)
@@ -701,7 +755,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
 #pragma unroll 1
             for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
                 float o[32];
-                read_output<D, kF8>(p, sh, oa, pos, c, o);
+                read_output<D, kF8, kTwin>(p, sh, oa, t, pos, c, o);
                 float4* to = reinterpret_cast<float4*>(rows + (t * kTileM + rr) * S::kRowFloats + 32 * c);
 #pragma unroll
                 for (int x = 0; x < 32; x += 4) to[x >> 2] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
@@ -714,16 +768,17 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
             cluster_sync();
             constexpr uint32_t kLanes = D / 4;  // threads to a row
             const uint32_t rank = blockIdx.x % p.splits, c = 4 * (threadIdx.x % kLanes);
-            for (uint32_t x = threadIdx.x / kLanes * p.splits + rank; x < 2 * kTileM; x += kSoftmax / kLanes * p.splits) {
+            for (uint32_t x = threadIdx.x / kLanes * p.splits + rank; x < (kTwin ? 1 : 2) * kTileM; x += kSoftmax / kLanes * p.splits) {
                 const uint32_t xr = x & 127, xt = sh.t0 + (x >> 7) * p.tokens + xr / p.group, xh = sh.h * p.group + xr % p.group;
                 if (xr >= p.tokens * p.group || xt >= p.a.q_tokens) continue;
                 const uint32_t at = smem_addr(rows + x * S::kRowFloats);
                 float mm = -INFINITY, ll = 0.0f;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-                for (uint32_t i = 0; i < p.splits; i++) {
-                    const float mi = cluster_ld(at + 4 * D, i), li = cluster_ld(at + 4 * D + 4, i);
-                    const float4 y = cluster_ld4(at + 4 * c, i);
+                for (uint32_t i = 0; i < p.splits * (kTwin ? 2 : 1); i++) {
+                    const uint32_t from = kTwin ? i >> 1 : i, row = kTwin ? at + (i & 1) * (kTileM * S::kRowFloats * 4) : at;
+                    const float mi = cluster_ld(row + 4 * D, from), li = cluster_ld(row + 4 * D + 4, from);
+                    const float4 y = cluster_ld4(row + 4 * c, from);
                     const float top = fmaxf(mm, mi), base = top == -INFINITY ? 0.0f : top;
                     const float f = exp2_approx(mm - base), gi = exp2_approx(mi - base);
                     ll = fmaf(ll, f, li * gi);
@@ -749,12 +804,12 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
     if (warp == 16) tmem_free<512>(tmem);
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, bool kTwin>
 cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
     constexpr int kSmem = TilesShape<D, kF8>::kUsed + (int)sizeof(TilesShared);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     Wave w;
-    const cudaError_t e = launch_wave<tiles_kernel<D, kF8>>(TilesShape<D, kF8>::kThreads, kSmem, w);
+    const cudaError_t e = launch_wave<tiles_kernel<D, kF8, kTwin>>(TilesShape<D, kF8>::kThreads, kSmem, w);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -767,17 +822,22 @@ cudaError_t launch(const TilesParams& p, uint32_t ctas, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kF8>, p);
+    return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kF8, kTwin>, p);
 }
 
 }  // namespace
+
+// All rows in one tile, and slots for two: both tiles of a CTA hold the rows and take every other slot tile.
+inline bool is_twin(const splitzip_attention_args& a) {
+    return a.q_tokens <= kTileM / (a.q_heads / a.kv_heads) && a.kv_tokens > kBN;
+}
 
 bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     const uint32_t group = a.q_heads / a.kv_heads, tokens = kTileM / group;
     p.rows = a.q_tokens * group;
     p.tile_rows = 2 * tokens * group;
     p.row_tiles = (a.q_tokens + 2 * tokens - 1) / (2 * tokens);
-    const uint64_t units = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
+    const uint64_t units = (uint64_t)a.batch * a.kv_heads * p.row_tiles, at_once = is_twin(a) ? 2 : 1;
     // The tiles of slots a CTA's rows can see at most.
     uint64_t most = (a.kv_tokens + kBN - 1) / kBN;
     if (a.window)
@@ -791,7 +851,7 @@ bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     uint64_t best = ~0ull;
     p.splits = 1;
     for (uint64_t n = 1; n <= 8 && (n == 1 || 2 * n <= most); n++) {
-        const uint64_t time = (units + kAtOnce[n] - 1) / kAtOnce[n] * ((most + n - 1) / n + kSplitCost);
+        const uint64_t time = (units + kAtOnce[n] - 1) / kAtOnce[n] * (((most + n - 1) / n + at_once - 1) / at_once + kSplitCost);
         if (time < best) {
             best = time;
             p.splits = (uint32_t)n;
@@ -821,8 +881,12 @@ cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const Atten
         !make_map(p.vmap, a.v, f8 ? 1 : 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kBN, false, &p.one_v))
         return cudaErrorInvalidValue;
     const uint32_t ctas = a.batch * a.kv_heads * plan.row_tiles * plan.splits;
-    if (a.head_dim == 64) return f8 ? launch<64, true>(p, ctas, s) : launch<64, false>(p, ctas, s);
-    return f8 ? launch<128, true>(p, ctas, s) : launch<128, false>(p, ctas, s);
+    const auto go = [&](auto twin) {
+        constexpr bool kTwin = decltype(twin)::value;
+        if (a.head_dim == 64) return f8 ? launch<64, true, kTwin>(p, ctas, s) : launch<64, false, kTwin>(p, ctas, s);
+        return f8 ? launch<128, true, kTwin>(p, ctas, s) : launch<128, false, kTwin>(p, ctas, s);
+    };
+    return is_twin(a) ? go(std::true_type()) : go(std::false_type());
 }
 
 }  // namespace splitzip

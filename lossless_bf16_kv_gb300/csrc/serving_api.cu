@@ -35,15 +35,16 @@ bool sizes_ok(const splitzip_attention_args& a) {
            (uint64_t)a.batch * a.kv_heads <= kMax31;
 }
 
-// Tiles of 256 query rows on the tensor cores from 33 rows of a key/value head on
-// (the other kernel's largest tile, past which it reads the cache twice), from 65 on
-// for an E5M2 cache, which that kernel widens at less cost; only for scales that
-// kernel takes.  128 units of 16384 slots, head_dim 128, in us, this kernel and the
-// other: BF16 32 rows 217 and 176, 40 rows 217 and 320; E5M2 64 rows 300 and 276, 96
-// rows 302 and 443.  16 units of 2048: BF16 40 rows 13.5 and 17.2, E5M2 64 rows 17.5
-// and 16.3, 96 rows 17.9 and 19.5.
+// Tiles of 128 query rows on the tensor cores from 17 rows of a key/value head on
+// (the other kernel's smaller tile), from 65 on for an E5M2 cache, which that kernel
+// widens at less cost; only for scales that kernel takes.  In us, this kernel and the
+// other, head_dim 128: 128 units of 16384 slots, BF16 16 rows 158 and 157, 32 rows 159
+// and 175, 64 rows 161 and 321; E5M2 32 rows 262 and 148, 64 rows 265 and 276, 128
+// rows 269 and 545.  16 units of 2048: BF16 16 rows 12.9 and 11.4, 32 rows 13.3 and
+// 16.5; E5M2 64 rows 18.8 and 16.0, 128 rows 22.3 and 20.5.  512 units of 1024: BF16
+// 32 rows 76.5 and 75.5, 64 rows 81 and 142.
 bool on_tiles(const splitzip_attention_args& a, const AttentionPlan& rows) {
-    return rows.rows > (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 64u : 32u) && attention_tiles_usable(a);
+    return rows.rows > (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 64u : 16u) && attention_tiles_usable(a);
 }
 bool plans(const splitzip_attention_args& a, AttentionPlan& rows, AttentionPlan& tiles) {
     return attention_rows_plan(a, rows) && attention_tiles_plan(a, tiles);

@@ -127,6 +127,40 @@ def test_attention_ignores_what_it_does_not_see(tq, bad, fmt):
     check_attention(q, kv, lens, window, sinks)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (130, 0), (300, 130), (64, 4), (1, 0)])
+@pytest.mark.parametrize("shape", [(1, 3, 129, 24, 3, 64), (2, 1, 255, 64, 1, 128), (1, 16, 257, 16, 2, 64), (2, 42, 700, 6, 2, 128),
+                                   (1, 100, 1000, 2, 2, 64), (3, 9, 641, 8, 1, 128), (1, 4, 5000, 40, 2, 64), (1, 128, 384, 3, 3, 128)])
+def test_attention_of_up_to_128_rows(shape, window, sinks, fmt):
+    """17 to 128 query rows of a key/value head, an odd or even number of tiles of
+    128 slots, a first or second one that only some rows see."""
+    q, kv = make(*shape, fmt=fmt, seed=shape[2] + window)
+    check_attention(q, kv, None, window, sinks)
+    b, tq, tk = shape[:3]
+    lens = lens_of([min(tk, tq + 100 * i + 3) for i in range(b)])
+    kv[0, :, int(lens[0]):] = float("nan")
+    check_attention(q, kv, lens, window, sinks)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+@pytest.mark.parametrize("rows", [3, 20, 70, 300])
+def test_attention_negative_and_zero_scale_of_many_rows(rows, scale):
+    q, kv = make(1, rows, 600, 2, 2, 128, seed=rows)
+    check_attention(q, kv, None, 200, 3, scale=scale)
+
+
+@pytest.mark.parametrize("rows,tokens", [(64, 300), (64, 1000), (300, 700)])
+def test_attention_maxima_that_rise(rows, tokens):
+    """Keys that grow with the slot: every tile of slots raises the maximum, in one
+    half of its slots or in both; and ones that fall, of which none after the first does."""
+    q, kv = make(1, rows, tokens, 2, 2, 128, seed=tokens)
+    grow = torch.linspace(0.1, 60.0, tokens, device=DEV)
+    for size in (grow, grow.flip(0), torch.where(torch.arange(tokens, device=DEV) % 128 < 64, grow, 0.1)):
+        k = kv.clone()
+        k[:, 0] = (kv[:, 0].float() * size[:, None, None]).bfloat16()
+        check_attention(q, k, None, scale=0.05)
+
+
 @pytest.mark.parametrize("tq", [1, 200])
 def test_attention_visible_nan_and_infinity_stay(tq):
     q, kv = make(1, tq, 500, 4, 2, 128, seed=3)
