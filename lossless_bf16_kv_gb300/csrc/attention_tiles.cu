@@ -63,7 +63,7 @@ namespace {
 constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
 constexpr int kSoftmax = 512;  // threads
-constexpr int kPart = 16;        // scores turned into P at a time
+constexpr int kPart = 16;      // scores turned into P at a time: eight words
 constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
 
 template <int D, bool kF8>
@@ -466,7 +466,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 64 / kPart; c++) {
-            uint32_t w[kPart / 2];
+            uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < kPart; x += 2) {
                 const int y = kPart * c + x;
@@ -478,7 +478,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                 // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
                 w[x >> 1] = pack2<kF8>(u, v);
             }
-            tmem_st<kPart / 2>(pa + kPart / 2 * c, w);
+            tmem_st8(pa + 8 * c, w);
         }
         float u, v, u2, v2;
         unpair(sum[0], u, v);
@@ -510,7 +510,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                         o[x] = __float_as_uint(u);
                         o[x + 1] = __float_as_uint(v);
                     }
-                    tmem_st<8>(oa + 8 * c, o);
+                    tmem_st8(oa + 8 * c, o);
                 }
             }
             if (__any_sync(0xFFFFFFFFu, mine != now)) {
@@ -525,7 +525,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                         const float2 y = unpack2<kF8>(w[x]);
                         w[x] = pack2<kF8>(y.x * g, y.y * g);
                     }
-                    tmem_st<8>(pa + 8 * c, w);
+                    tmem_st8(pa + 8 * c, w);
                 }
             }
             tmem_wait_st();
