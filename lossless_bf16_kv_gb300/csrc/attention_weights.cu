@@ -20,10 +20,10 @@
 //
 // What bounds it is the latency of its roles: a group of warps takes about 1900
 // cycles for a query tile, which with two groups is 950 each, and the warp that
-// issues the products about as many to wait, issue and commit them in turn, where
-// the products and the exponentials take 512 each.  Two prompts of 3000 tokens,
-// 32 heads of 128 over 8: 74 us (0.76 PFLOP/s over the visible pairs); the last
-// 64 tokens over 16384: 14.6-15.1 us (keys at 2.3 TB/s).  Keys in tensor memory
+// issues the products not much less to issue and commit them in turn, where the
+// products and the exponentials take 512 each.  Two prompts of 3000 tokens, 32
+// heads of 128 over 8: 72.5 us (0.78 PFLOP/s over the visible pairs); the last 64
+// tokens over 16384: 14.6-15.3 us (keys at 2.3 TB/s).  Keys in tensor memory
 // as the first operand gave 71 and 16 us, with a third fewer accumulators.
 //
 // Roles: warps 0-15 sum (0-7 the even, 8-15 the odd query tiles, four warps to
@@ -227,41 +227,53 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
         mbar_wait_bounded(&sh.q_full[x % kQStages], (x / kQStages) & 1, &late);
 }
 
-// The whole warp waits, one lane issues.
+// The whole warp takes the items, one lane issues.
 template <int D, bool kF8>
 __device__ __forceinline__ void issue_items(const WeightsParams& p, WeightsShared& sh, uint32_t tmem, const uint8_t* ks, const uint8_t* ring) {
     using S = WeightsShape<D, kF8>;
     volatile uint32_t* err = &sh.err;
     const bool leader = elect_one();
     const uint32_t kd = desc_rows(smem_addr(ks)), qd = desc_rows(smem_addr(ring));
-    uint32_t it = 0, n = 0;
-    bool go = true;
+    const uint32_t leader_lane = __ffs(__ballot_sync(0xFFFFFFFFu, leader)) - 1;
+    // As many columns as a tile has rows, in steps of 16; here, of all but an item's last.
+    const uint32_t most = mma_shape(false, (p.tokens * p.group + 15) & ~15u, false);
+    uint32_t it = 0, n = 0, st = 0, turn = 0;  // item, tile, query stage and its phase
+    bool go = true, ready = false;             // ready: the next tile's queries and accumulator are
     Items list(sh);
     while (go && list.next()) {
         const Item& w = list.w;
         const uint32_t kst = it % kKStages;
         go = mbar_wait_bounded(&sh.k_full[kst], (it / kKStages) & 1, err);
-        for (uint32_t i = 0; go && i < w.steps; i++, n++) {
-            const uint32_t st = n % kQStages, x = n & 3;
-            go = mbar_wait_bounded(&sh.q_full[st], (n / kQStages) & 1, err) &&
-                 (n < 4 || mbar_wait_bounded(&sh.s_free[x], ((n >> 2) - 1) & 1, err));
-            if (!go) break;
-            // As many columns as the tile has rows, in steps of 16.
-            const uint32_t shape = mma_shape(false, (tile_rows(p, w, i) + 15) & ~15u, false);
-            tcgen_fence_after();
-            if (leader) {
-                const uint32_t ka = kd + kst * (S::kTile >> 4), qa = qd + st * (S::kTile >> 4);
+        tcgen_fence_after();
+        if (leader) {
+            const uint32_t ka = kd + kst * (S::kTile >> 4);
+            for (uint32_t i = 0; go && i < w.steps; i++, n++) {
+                const uint32_t x = n & 3;
+                go = ready || (mbar_wait_bounded(&sh.q_full[st], turn, err) &&
+                               (n < 4 || mbar_wait_bounded(&sh.s_free[x], ((n >> 2) - 1) & 1, err)));
+                if (!go) break;
+                const uint32_t shape = i + 1 < w.steps ? most : mma_shape(false, (tile_rows(p, w, i) + 15) & ~15u, false);
+                const uint32_t qa = qd + st * (S::kTile >> 4);
+                tcgen_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; k++) {
                     const uint32_t off = (k >> 2) * (kSlotTile * 128) + (k & 3) * 32;
                     mma_ss(tmem + x * kRowTile, desc(ka, off), desc(qa, off), shape, k > 0);
+                    if (k == D / 32 - 1) {  // a look ahead while these run: 72.5 us at 2 x 3000, 74.2 without
+                        const uint32_t m = n + 1;
+                        const bool wraps = st + 1 == kQStages;
+                        const bool q = mbar_test(&sh.q_full[wraps ? 0 : st + 1], wraps ? turn ^ 1 : turn);
+                        const bool f = m < 4 || mbar_test(&sh.s_free[m & 3], ((m >> 2) - 1) & 1);
+                        ready = q & f;
+                    }
                 }
                 mma_commit(&sh.s_full[x]);
                 mma_commit(&sh.q_empty[st]);
                 if (i + 1 == w.steps) mma_commit(&sh.k_empty[kst]);
+                if (++st == kQStages) st = 0, turn ^= 1;
             }
-            __syncwarp();  // no lane falls a phase behind
         }
+        go = __shfl_sync(0xFFFFFFFFu, (int)go, leader_lane) != 0;
         it++;
     }
     uint32_t late = 0;
