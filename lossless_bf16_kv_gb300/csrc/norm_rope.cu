@@ -14,7 +14,7 @@
 // heads of one kind (queries, keys or values) of one token, so addresses,
 // weights and the token's table row are found once for them.  Runs of eight
 // (16-byte loads) leave half as many instructions, which limited runs of four:
-// 16384 tokens of 48 heads of 128 take 77 us (5.3 TB/s, 79% of a copy's rate)
+// 16384 tokens of 48 heads of 128 take 75 us (5.5 TB/s, 81% of a copy's rate)
 // against 88; runs of four remain for a rot_dim that is not a multiple of sixteen.
 #include <cstdint>
 
@@ -95,7 +95,7 @@ struct NormRopeParams {
 };
 
 template <int D, int kRun, int kRows, bool kF8>
-__global__ void __launch_bounds__(kThreadsRope, 6) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreadsRope, kRun == 8 && kRows == 4 ? 5 : 6) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr uint32_t kLanes = D / (2 * kRun);
     const splitzip_norm_rope_args& a = p.a;
     const uint32_t lane = threadIdx.x % kLanes;
@@ -129,18 +129,18 @@ __global__ void __launch_bounds__(kThreadsRope, 6) norm_rope_kernel(const __grid
     if (active && !q) slot = a.slots[tok];
     // The factors of kRun pairs: of the first run's values with the second's, or,
     // interleaved, half of them in each run.
-    float c[kRun], s[kRun];
+    alignas(16) float c[kRun], s[kRun];
     if (turns && active) {
         const int32_t pos = a.positions[tok];
         if (pos >= 0 && (uint64_t)pos < a.table_rows) {
             const float* t = a.table + (uint64_t)pos * a.rot_dim;
             const uint32_t f0 = a.interleaved ? u0 / 2 : u0, f1 = a.interleaved ? u1 / 2 : u0 + kRun / 2;
+            const float* at[4] = {t + f0, t + f1, t + a.rot_dim / 2 + f0, t + a.rot_dim / 2 + f1};
 #pragma unroll
-            for (int i = 0; i < kRun / 2; i += 2) {
-                *reinterpret_cast<float2*>(c + i) = *reinterpret_cast<const float2*>(t + f0 + i);
-                *reinterpret_cast<float2*>(c + kRun / 2 + i) = *reinterpret_cast<const float2*>(t + f1 + i);
-                *reinterpret_cast<float2*>(s + i) = *reinterpret_cast<const float2*>(t + a.rot_dim / 2 + f0 + i);
-                *reinterpret_cast<float2*>(s + kRun / 2 + i) = *reinterpret_cast<const float2*>(t + a.rot_dim / 2 + f1 + i);
+            for (int x = 0; x < 4; x++) {
+                float* to = (x < 2 ? c : s) + (x & 1) * (kRun / 2);
+                if constexpr (kRun == 8) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(at[x]);
+                else *reinterpret_cast<float2*>(to) = *reinterpret_cast<const float2*>(at[x]);
             }
         } else {
 #pragma unroll
@@ -224,11 +224,13 @@ template <int D, bool kF8>
 cudaError_t launch_dim(NormRopeParams& p, cudaStream_t s) {
     // Runs of eight where the rotated values are whole pairs of them.
     const bool eight = p.a.rot_dim % 16 == 0;
-    // One row per group of lanes where the rows do not fill the GPU anyway
-    // (fewer than 8 warps' worth per SM), two (or four of half the lanes' size) where they do.
-    const uint64_t rows = (uint64_t)p.a.n * (p.a.q_heads + 2 * p.a.kv_heads);
-    const bool few = rows * (D / 16) < kSms * 256;
-    if (eight) return few ? launch<D, 8, 1, kF8>(p, s) : launch<D, 8, 2, kF8>(p, s);
+    // One row per group of lanes where the rows do not fill the GPU anyway (fewer than 8
+    // warps' worth per SM), two (or four of half the lanes' size) where they do, and four
+    // where they fill it many times: 48 heads of 128 of 16384 tokens take 70 us with four
+    // and 74 with two, of 1024 tokens 7.3 and 6.4.
+    const uint64_t rows = (uint64_t)p.a.n * (p.a.q_heads + 2 * p.a.kv_heads), lanes = rows * (D / 16);
+    const bool few = lanes < kSms * 256, many = lanes >= kSms * 256 * 16;
+    if (eight) return few ? launch<D, 8, 1, kF8>(p, s) : many ? launch<D, 8, 4, kF8>(p, s) : launch<D, 8, 2, kF8>(p, s);
     return few ? launch<D, 4, 1, kF8>(p, s) : launch<D, 4, 4, kF8>(p, s);
 }
 

@@ -350,6 +350,14 @@ def test_norm_rope(n, hq, hk, d, rot, interleaved, fmt):
     assert bool((kv.float()[:, rest] == 7.0).all())
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n,hq,hk,d,rot", [(2601, 30, 5, 128, 128), (3001, 23, 1, 128, 16), (5003, 30, 7, 64, 32), (2001, 6, 2, 128, 48)])
+def test_norm_rope_of_many_tokens(n, hq, hk, d, rot, interleaved, fmt):
+    """Heads that are not a whole number of what a group of lanes takes."""
+    test_norm_rope(n, hq, hk, d, rot, interleaved, fmt)
+
+
 def test_norm_rope_batched_cache_dropped_slots_in_place_and_no_weights():
     b, t, hq, hk, d = 3, 40, 4, 2, 64
     g = gen(2)
