@@ -12,7 +12,7 @@
 // to 51200 slots): 512 rows of 16384 took 91 us reading the weights again from
 // L2 in each of four passes of eight bits, with a CTA barrier every 1024 slots
 // of the last pass; they take 49 us now that every thread ranks a short run of
-// its own (0.7 TB/s: barriers and shared-memory atomics bound it).
+// its own (0.7 TB/s: two CTAs to an SM, which wait for loads and barriers in turn).
 //
 // Gather: kept rows are copied in order.  HBM bounds it: at 64 x 8 rows, 2048
 // of 16384 slots of 128 BF16 values kept, 1.07 GB in 154 us (6.6 TB/s, 97% of a
