@@ -22,6 +22,7 @@
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "lane_groups.h"
 #include "serving.h"
 
 namespace splitzip {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kThreadsRope, kRun == 8 && kRows == 4 ? 5 : 6)
     constexpr uint32_t kLanes = D / (2 * kRun);
     const splitzip_norm_rope_args& a = p.a;
     const uint32_t lane = threadIdx.x % kLanes;
-    const uint32_t item = (blockIdx.x * kThreadsRope + threadIdx.x) / kLanes;
+    const uint32_t item = lane_group(blockIdx.x, threadIdx.x, kThreadsRope, kLanes);
     if (__all_sync(0xFFFFFFFFu, item >= p.items)) return;
     const bool active = item < p.items;
     const uint32_t tok = active ? item / p.parts : 0, part = active ? item - tok * p.parts : 0;
