@@ -70,9 +70,14 @@ typedef struct splitzip_view {
  *   table          float[table_rows][rot_dim], 16-byte aligned
  *   slots          int64[n]: the cache row, counted in stride_t steps from
  *                  `data`, each used once; a token whose slot is outside
- *                  [0, cache_rows) writes its queries only
+ *                  [0, cache_rows), or in a gap of the cache, writes its
+ *                  queries only
  *   q_out          BF16 [n, q_heads, head_dim]; may be q itself
  *   k_cache, v_cache  rows [cache_rows, kv_heads, head_dim] of cache_format
+ *   cache_step, cache_tokens  0, or the caches hold sequences with gaps between
+ *                  them: sequence b's token t is row b * cache_step + t, and
+ *                  rows from cache_tokens on to the next sequence's first are
+ *                  no part of the caches; cache_rows is then at most 2^32
  * head_dim 64 or 128; rot_dim a multiple of 8 up to head_dim, or 0;
  * n * (q_heads + 2 kv_heads) < 2^31.  One launch; n = 0 enqueues nothing. */
 typedef struct splitzip_norm_rope_args {
@@ -87,6 +92,7 @@ typedef struct splitzip_norm_rope_args {
     uint32_t cache_format; /* SPLITZIP_FORMAT_BF16 or SPLITZIP_FORMAT_E5M2 */
     uint32_t interleaved;
     float eps; /* >= 0 */
+    uint32_t cache_step, cache_tokens;
 } splitzip_norm_rope_args;
 
 splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args *args, splitzip_stream_t s);

@@ -155,7 +155,9 @@ __global__ void __launch_bounds__(kThreadsRope, kRun == 8 && kRows == 4 ? 5 : 6)
         w1 = load_run<kRun>(static_cast<const __nv_bfloat16*>(weight) + u1);
     }
     const splitzip_view& cache = k ? a.k_cache : a.v_cache;
-    const bool store = !q && slot >= 0 && (uint64_t)slot < a.cache_rows;
+    // A row between two sequences of the cache is someone else's memory.
+    const bool store = !q && slot >= 0 && (uint64_t)slot < a.cache_rows &&
+                       (!a.cache_step || (uint32_t)slot % a.cache_step < a.cache_tokens);
     const int64_t at = q ? (int64_t)tok * a.q_out.stride_t + h0 * a.q_out.stride_h : slot * cache.stride_t + h0 * cache.stride_h;
     const int64_t step = q ? a.q_out.stride_h : cache.stride_h;
     uint8_t* dst = static_cast<uint8_t*>(q ? a.q_out.data : cache.data) + at * (q || !kF8 ? 2 : 1);

@@ -65,6 +65,7 @@ splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args* a, splitzip
     if ((uint64_t)a->q_heads + 2ull * a->kv_heads > kMax31 ||
         (uint64_t)a->n * ((uint64_t)a->q_heads + 2ull * a->kv_heads) > kMax31)
         return SPLITZIP_ERR_INVALID_ARG;
+    if (a->cache_step && (a->cache_tokens > a->cache_step || a->cache_rows > 1ull << 32)) return SPLITZIP_ERR_INVALID_ARG;
     if (!a->n) return SPLITZIP_OK;
     if (a->rot_dim && (!a->positions || !a->table)) return SPLITZIP_ERR_INVALID_ARG;
     if (!a->slots || !aligned(a->slots, 8) || !aligned(a->positions, 4) || !aligned(a->table, 16) ||

@@ -39,7 +39,8 @@ class NormRopeArgs(ctypes.Structure):
                 ("q_out", View), ("k_cache", View), ("v_cache", View),
                 ("table_rows", _u64), ("cache_rows", _u64),
                 ("n", _u32), ("q_heads", _u32), ("kv_heads", _u32), ("head_dim", _u32),
-                ("rot_dim", _u32), ("cache_format", _u32), ("interleaved", _u32), ("eps", _f32)]
+                ("rot_dim", _u32), ("cache_format", _u32), ("interleaved", _u32), ("eps", _f32),
+                ("cache_step", _u32), ("cache_tokens", _u32)]
 
 
 class AttentionArgs(ctypes.Structure):
@@ -60,7 +61,7 @@ class EvictArgs(ctypes.Structure):
 # them out): a call packs its arguments in one step, which costs a fraction of
 # filling a ctypes structure field by field.
 _VIEW = "P3q"
-_NORM_ROPE = struct.Struct("@" + 3 * _VIEW + "5P" + 3 * _VIEW + "2Q7If")
+_NORM_ROPE = struct.Struct("@" + 3 * _VIEW + "5P" + 3 * _VIEW + "2Q7If2I")
 _ATTENTION = struct.Struct("@" + 4 * _VIEW + "2P9If")
 _EVICT = struct.Struct("@" + 4 * _VIEW + "5P8I")
 _NO_VIEW = (0, 0, 0, 0)
@@ -158,20 +159,23 @@ def _format(k: torch.Tensor, v: torch.Tensor | None = None) -> int:
 # --------------------------------------------------- norm, rotation, cache
 
 def _cache_rows(t: torch.Tensor, what: str) -> tuple:
-    """(rows, stride_t, stride_h) of a cache addressed by row: [rows, heads,
+    """(rows, stride_t, stride_h, step) of a cache addressed by row: [rows, heads,
     dim], or [batch, tokens, heads, dim] whose batch stride is a whole number of
-    token strides (row = b * stride_b // stride_t + token)."""
+    token strides (row = b * stride_b // stride_t + token).  step is that number
+    where it leaves gaps between the sequences, else 0."""
     shape, st = t.shape, t.stride()
     if st[-1] != 1:
         _bad(f"{what}: the values of a row must be contiguous")
     if len(shape) == 3:
-        return shape[0], st[0], st[1]
+        return shape[0], st[0], st[1], 0
     if len(shape) != 4:
         _bad(f"{what} is [rows, heads, dim] or [batch, tokens, heads, dim]")
     if shape[0] > 1 and (st[1] == 0 or st[0] % st[1]):
         _bad(f"{what}: the batch stride must be a multiple of the token stride")
-    rows = (shape[0] - 1) * (st[0] // st[1]) + shape[1] if shape[0] > 1 else shape[0] * shape[1]
-    return rows, st[1], st[2]
+    if shape[0] <= 1:
+        return shape[0] * shape[1], st[1], st[2], 0
+    step = st[0] // st[1]
+    return (shape[0] - 1) * step + shape[1], st[1], st[2], step if step > shape[1] else 0
 
 
 def _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache):
@@ -212,7 +216,8 @@ def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     q_weight, k_weight: BF16 [dim] or None.  table: float32 [positions, rot_dim]
     (cosines, then sines) or None for no rotation; positions int32 [n].
     slots: int64 [n]; a cache [batch, tokens, heads, dim] is addressed by
-    b * stride_b // stride_t + token.  q_out may be q."""
+    b * stride_b // stride_t + token; a slot that is no row of the cache is
+    dropped, one between two sequences too.  q_out may be q."""
     qs, ks, kind = q.shape, k.shape, k_cache.dtype
     qst, kst, vst, ost = q.stride(), k.stride(), v.stride(), q_out.stride()
     cs, rot = k_cache.shape, 0
@@ -234,14 +239,14 @@ def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
         rot = ts[1] if ok else 0
     if not ok:
         _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache)
-    krows, kct, kch = _cache_rows(k_cache, "k_cache")
-    vrows, vct, vch = _cache_rows(v_cache, "v_cache")
+    krows, kct, kch, step = _cache_rows(k_cache, "k_cache")
+    vrows, vct, vch, _ = _cache_rows(v_cache, "v_cache")
     a = _NORM_ROPE.pack(q.data_ptr(), 0, qst[0], qst[1], k.data_ptr(), 0, kst[0], kst[1], v.data_ptr(), 0, vst[0], vst[1],
                         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
                         positions.data_ptr() if rot else 0, table.data_ptr() if rot else 0, slots.data_ptr(),
                         q_out.data_ptr(), 0, ost[0], ost[1], k_cache.data_ptr(), 0, kct, kch, v_cache.data_ptr(), 0, vct, vch,
                         ts[0] if rot else 0, krows if krows < vrows else vrows, *qs[:2], *ks[1:], rot, _FORMAT[kind],
-                        1 if interleaved else 0, eps)
+                        1 if interleaved else 0, eps, step, cs[1] if step else 0)
     if _fn_norm_rope is None:
         library()
     status = _fn_norm_rope(a, _stream_of(stream))

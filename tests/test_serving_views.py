@@ -1,0 +1,37 @@
+"""Views that the operators around the KV cache accept and refuse, on the CPU: a
+refused call enqueues nothing, so it needs no GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from lossless_bf16_kv_gb300 import _build, serving
+from lossless_bf16_kv_gb300 import splitzip as sz
+
+FAKE = 1 << 20   # aligned, never dereferenced: every call below is refused
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build_library()
+    return serving.library()
+
+
+def test_cache_rows_between_sequences():
+    kv = torch.empty((3, 2, 40, 2, 64), dtype=torch.bfloat16)
+    assert serving._cache_rows(kv[:, 0], "k") == (200, 128, 64, 80)          # the values lie between
+    assert serving._cache_rows(kv[:1, 0], "k") == (40, 128, 64, 0)           # one sequence
+    assert serving._cache_rows(kv[0], "k") == (80, 128, 64, 0)               # sequences without gaps
+    assert serving._cache_rows(kv[0, 0], "k") == (40, 128, 64, 0)
+    heads_first = torch.empty((3, 2, 40, 64), dtype=torch.bfloat16).transpose(1, 2)
+    assert serving._cache_rows(heads_first, "k") == (200, 64, 2560, 80)
+
+
+@pytest.mark.parametrize("kw", [dict(cache_step=40, cache_tokens=41), dict(cache_step=40, cache_tokens=40, cache_rows=(1 << 32) + 1)])
+def test_norm_rope_refuses_sequences_that_do_not_fit(lib, kw):
+    view = (FAKE, 0, 1024, 128)
+    a = serving.NormRopeArgs(view, view, view, None, None, FAKE, FAKE, FAKE, view, view, view, 10, 10, 5, 8, 2, 128, 128,
+                             0, 0, 1e-6)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    assert lib.splitzip_qk_norm_rope(ctypes.byref(a), None) == sz.ERR_INVALID_ARG
