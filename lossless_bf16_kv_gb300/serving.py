@@ -178,6 +178,18 @@ def _cache_rows(t: torch.Tensor, what: str) -> tuple:
     return (shape[0] - 1) * step + shape[1], st[1], st[2], step if step > shape[1] else 0
 
 
+def _check_same_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, kstep: int, vstep: int):
+    """One slot addresses both caches: it must be the same sequence's same token in both."""
+    ks, vs, kst, vst = k_cache.shape, v_cache.shape, k_cache.stride(), v_cache.stride()
+    if len(ks) == 4 and len(vs) == 4 and ks[0] > 1 and vs[0] > 1:
+        if ks != vs:
+            _bad(f"batched caches must have one shape, not {tuple(ks)} and {tuple(vs)}")
+        if kst[0] * vst[1] != vst[0] * kst[1]:
+            _bad("the caches' sequences must be the same number of tokens apart")
+    elif kstep or vstep:
+        _bad("a cache with gaps between its sequences needs the other one like it")
+
+
 def _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache):
     for t, what in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
         _bf16(t, what)
@@ -240,7 +252,9 @@ def splitzip_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     if not ok:
         _check_norm_rope(q, k, v, q_weight, k_weight, positions, table, slots, q_out, k_cache, v_cache)
     krows, kct, kch, step = _cache_rows(k_cache, "k_cache")
-    vrows, vct, vch, _ = _cache_rows(v_cache, "v_cache")
+    vrows, vct, vch, vstep = _cache_rows(v_cache, "v_cache")
+    if len(cs) == 4 or len(v_cache.shape) == 4:
+        _check_same_rows(k_cache, v_cache, step, vstep)
     a = _NORM_ROPE.pack(q.data_ptr(), 0, qst[0], qst[1], k.data_ptr(), 0, kst[0], kst[1], v.data_ptr(), 0, vst[0], vst[1],
                         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
                         positions.data_ptr() if rot else 0, table.data_ptr() if rot else 0, slots.data_ptr(),

@@ -35,3 +35,27 @@ def test_norm_rope_refuses_sequences_that_do_not_fit(lib, kw):
     for k, v in kw.items():
         setattr(a, k, v)
     assert lib.splitzip_qk_norm_rope(ctypes.byref(a), None) == sz.ERR_INVALID_ARG
+
+
+def test_norm_rope_refuses_caches_that_a_slot_addresses_differently(monkeypatch):
+    """The binding's own check, in front of the library (which is never reached: the
+    tensors are on the CPU and only said to be elsewhere)."""
+    bf = lambda *shape: torch.empty(shape, dtype=torch.bfloat16)  # noqa: E731
+    whole = bf(2, 40, 2, 64)
+    pairs = [(whole, bf(2, 48, 2, 64)[:, :40]), (bf(2, 48, 2, 64)[:, :40], whole),      # 40 and 48 tokens apart
+             (whole, bf(4, 20, 2, 64)), (bf(2, 2, 40, 2, 64)[:, 0], bf(2, 2, 40, 2, 64)[:, 0, :39]),
+             (bf(2, 48, 2, 64)[:, :40], bf(88, 2, 64)), (bf(88, 2, 64), bf(2, 48, 2, 64)[:, :40])]
+    fine = [(whole, bf(2, 40, 2, 64)), (whole, bf(80, 2, 64)), (bf(2, 2, 40, 2, 64)[:, 0], bf(2, 2, 40, 2, 64)[:, 1]),
+            (bf(2, 2, 40, 64).transpose(1, 2), bf(2, 80, 2, 64)[:, :40]), (bf(1, 40, 2, 64), bf(50, 2, 64))]
+    reached = []
+    monkeypatch.setattr(serving, "_fn_norm_rope", lambda a, s: reached.append(a) or 0)
+    monkeypatch.setattr(serving, "_stream_of", lambda s: 0)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    x, y, slots = bf(3, 4, 64), bf(3, 2, 64), torch.arange(3)
+    for i, (k, v) in enumerate(pairs):
+        with pytest.raises(sz.SplitZipError) as err:
+            serving.splitzip_qk_norm_rope(x, y, y, None, None, None, None, slots, x, k, v)
+        assert err.value.status == sz.ERR_INVALID_ARG and not reached, i
+    for k, v in fine:
+        serving.splitzip_qk_norm_rope(x, y, y, None, None, None, None, slots, x, k, v)
+    assert len(reached) == len(fine)
