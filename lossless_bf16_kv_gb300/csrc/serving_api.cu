@@ -18,11 +18,12 @@ inline bool dim_ok(uint32_t d) { return d == 64 || d == 128; }
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // A view of nb x nt x nh rows.  Strides of dimensions of length 1 are not
-// looked at; only a batch stride may be 0 (one sequence shared by the batch).
-bool view_ok(const splitzip_view& v, uint32_t elem, uint32_t nb, uint32_t nt, uint32_t nh) {
+// looked at; only an input's batch stride may be 0 (one sequence shared by the
+// batch: as an output, all of it would be written to the same rows).
+bool view_ok(const splitzip_view& v, uint32_t elem, uint32_t nb, uint32_t nt, uint32_t nh, bool output = false) {
     const int64_t unit = 16 / elem, most = 1ll << 38;
     const auto ok = [=](uint32_t n, int64_t s, int64_t least) { return n <= 1 || (s >= least && s < most && s % unit == 0); };
-    return v.data && aligned(v.data, 16) && ok(nb, v.stride_b, 0) && ok(nt, v.stride_t, 1) && ok(nh, v.stride_h, 1);
+    return v.data && aligned(v.data, 16) && ok(nb, v.stride_b, output ? 1 : 0) && ok(nt, v.stride_t, 1) && ok(nh, v.stride_h, 1);
 }
 
 constexpr uint64_t kMax31 = 0x7FFFFFFFull;
@@ -91,7 +92,7 @@ splitzip_status splitzip_attention(const splitzip_attention_args* a, void* works
     AttentionPlan rows, tiles;
     if (!a || !sizes_ok(*a) || !plans(*a, rows, tiles)) return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
-    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) || !view_ok(a->out, 2, a->batch, a->q_tokens, a->q_heads) ||
+    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) || !view_ok(a->out, 2, a->batch, a->q_tokens, a->q_heads, true) ||
         !view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
@@ -138,7 +139,8 @@ splitzip_status splitzip_evict(const splitzip_evict_args* a, splitzip_stream_t s
     if ((uint64_t)a->keep_first + a->keep_last > a->budget) return SPLITZIP_ERR_INVALID_ARG;
     const uint32_t e = elem_bytes(a->cache_format);
     if (!view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads) ||
-        !view_ok(a->k_out, e, a->batch, a->budget, a->kv_heads) || !view_ok(a->v_out, e, a->batch, a->budget, a->kv_heads))
+        !view_ok(a->k_out, e, a->batch, a->budget, a->kv_heads, true) ||
+        !view_ok(a->v_out, e, a->batch, a->budget, a->kv_heads, true))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!a->weights || !a->index || !aligned(a->weights, 4) || !aligned(a->index, 4) || !aligned(a->weights_out, 4) ||
         !aligned(a->lens, 4) || !aligned(a->lens_out, 4))

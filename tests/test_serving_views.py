@@ -59,3 +59,16 @@ def test_norm_rope_refuses_caches_that_a_slot_addresses_differently(monkeypatch)
     for k, v in fine:
         serving.splitzip_qk_norm_rope(x, y, y, None, None, None, None, slots, x, k, v)
     assert len(reached) == len(fine)
+
+
+def test_outputs_are_not_shared_by_a_batch(lib):
+    """A batch stride of 0 is one sequence for the whole batch: an input's only."""
+    view, shared = (FAKE, 1 << 16, 1 << 10, 128), (FAKE, 0, 1 << 10, 128)
+    a = serving.AttentionArgs(view, view, view, shared, None, None, 2, 3, 64, 8, 2, 128, 0, 0, 0, 1.0)
+    need = lib.splitzip_attention_workspace_bytes(ctypes.byref(a))
+    assert need and lib.splitzip_attention(ctypes.byref(a), FAKE, need, None) == sz.ERR_INVALID_ARG
+    for kw in (dict(k_out=shared), dict(v_out=shared)):
+        a = serving.EvictArgs(view, view, view, view, FAKE, None, FAKE, None, None, 2, 64, 2, 128, 8, 2, 2, 0)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        assert lib.splitzip_evict(ctypes.byref(a), None) == sz.ERR_INVALID_ARG
