@@ -110,8 +110,8 @@ splitzip_status splitzip_qk_norm_rope(const splitzip_norm_rope_args *args, split
  *   q     BF16 [batch, q_tokens, q_heads, head_dim]
  *   k, v  [batch, kv_tokens, kv_heads, head_dim] of cache_format
  * head_dim 64 or 128; q_heads a multiple of kv_heads, at most
- * SPLITZIP_MAX_GROUP times it.  q_tokens * (q_heads / kv_heads), kv_tokens
- * and batch * kv_heads < 2^31. */
+ * SPLITZIP_MAX_GROUP times it.  q_tokens * (q_heads / kv_heads) and kv_tokens
+ * at most 2^31 - 256, batch * kv_heads < 2^31. */
 typedef struct splitzip_attention_args {
     splitzip_view q, k, v;
     splitzip_view out;   /* BF16 like q (attention only) */

@@ -27,12 +27,15 @@ bool view_ok(const splitzip_view& v, uint32_t elem, uint32_t nb, uint32_t nt, ui
 }
 
 constexpr uint64_t kMax31 = 0x7FFFFFFFull;
+// Slots and query rows of the attention calls: their kernels look up to two tiles
+// of 128 past the last one in signed 32-bit numbers.
+constexpr uint64_t kMostTokens = (1ull << 31) - 256;
 
 bool sizes_ok(const splitzip_attention_args& a) {
     if (!dim_ok(a.head_dim) || !format_ok(a.cache_format)) return false;
     if (!a.batch || !a.q_tokens || !a.kv_tokens || !a.kv_heads || !a.q_heads) return false;
     if (a.q_heads % a.kv_heads || a.q_heads / a.kv_heads > SPLITZIP_MAX_GROUP) return false;
-    return (uint64_t)a.q_tokens * (a.q_heads / a.kv_heads) <= kMax31 && a.kv_tokens <= kMax31 &&
+    return (uint64_t)a.q_tokens * (a.q_heads / a.kv_heads) <= kMostTokens && a.kv_tokens <= kMostTokens &&
            (uint64_t)a.batch * a.kv_heads <= kMax31;
 }
 

@@ -72,3 +72,20 @@ def test_outputs_are_not_shared_by_a_batch(lib):
         for k, v in kw.items():
             setattr(a, k, v)
         assert lib.splitzip_evict(ctypes.byref(a), None) == sz.ERR_INVALID_ARG
+
+
+def test_attention_refuses_tokens_whose_tiles_pass_32_bits(lib):
+    """From 2^31 - 255 slots on the end of the last tile of slots is no signed 32-bit
+    number: the few-row kernel took such a tile for one inside the cache, and read
+    past it."""
+    view, inv = (FAKE, 0, 128, 1 << 20), sz.ERR_INVALID_ARG
+    for kw in (dict(kv_tokens=(1 << 31) - 1), dict(kv_tokens=(1 << 31) - 255), dict(q_tokens=(1 << 31) - 255),
+               dict(q_tokens=(1 << 30) - 127, q_heads=2)):
+        a = serving.AttentionArgs(view, view, view, view, FAKE, None, 1, 1, 64, 1, 1, 64, 0, 0, 1, 1.0)
+        for k, v in kw.items():
+            setattr(a, k, v)
+        assert lib.splitzip_attention_workspace_bytes(ctypes.byref(a)) == 0
+        assert lib.splitzip_attention(ctypes.byref(a), FAKE, 1 << 40, None) == inv
+        assert lib.splitzip_attention_weights(ctypes.byref(a), None, FAKE, None) == inv
+        a.kv_tokens, a.q_tokens = min(a.kv_tokens, (1 << 31) - 256), min(a.q_tokens, ((1 << 31) - 256) // a.q_heads)
+        assert lib.splitzip_attention_workspace_bytes(ctypes.byref(a)) > 0
