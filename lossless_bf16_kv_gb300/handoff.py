@@ -122,13 +122,14 @@ def send(s: Shape, kv: torch.Tensor):
 
 
 def decode(m: Layers, thinned: torch.Tensor):
-    """Attention outputs [steps, layers, q_heads, dim] of the new tokens over the thinned cache and themselves."""
+    """Attention outputs [steps, layers, q_heads, dim] of the new tokens over the thinned cache and themselves,
+    their queries likewise, and the cache with the new tokens appended."""
     s, dev = m.s, m.device
     kv = torch.empty((s.layers, 2, s.budget + s.steps, s.kv_heads, s.dim), dtype=thinned.dtype, device=dev)
     kv[:, :, :s.budget] = thinned
-    q = torch.empty((1, 1, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
-    outs = torch.empty((s.steps, s.layers, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
-    workspace = serving.alloc_attention_workspace(q, kv[:1, 0])
+    queries = torch.empty((s.steps, s.layers, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
+    outs = torch.empty_like(queries)
+    workspace = serving.alloc_attention_workspace(queries[:1, :1], kv[:1, 0])
     lens = torch.full((1,), s.budget, dtype=torch.int32, device=dev)
     for step in range(s.steps):
         position = torch.full((1,), s.tokens + step, dtype=torch.int32, device=dev)   # in the whole text
@@ -138,11 +139,11 @@ def decode(m: Layers, thinned: torch.Tensor):
         for layer in range(s.layers):
             qr, kr, vr = m.project(layer, x)
             k, v = kv[layer:layer + 1, 0], kv[layer:layer + 1, 1]
-            out = outs[step, layer][None, None]
+            q, out = queries[step:step + 1, layer:layer + 1], outs[step:step + 1, layer:layer + 1]   # [1, 1, q_heads, dim]
             serving.splitzip_qk_norm_rope(qr, kr, vr, m.norm[layer][0], m.norm[layer][1], position, m.table, slot, q[0], k, v)
             serving.splitzip_attention(q, k, v, out, workspace, lens=lens)
-            x = m.mix(layer, x, out[0, 0][None])
-    return outs
+            x = m.mix(layer, x, out[0])
+    return outs, queries, kv
 
 
 def run(s: Shape, device="cuda") -> dict:
@@ -150,10 +151,10 @@ def run(s: Shape, device="cuda") -> dict:
     kv, weights = prefill(m)
     small, index = thin(s, kv, weights)
     payload, nbytes, there = send(s, small)
-    outs = decode(m, there)
+    outs, queries, decoded = decode(m, there)
     torch.cuda.synchronize()
     return {"kv": kv, "weights": weights, "small": small, "index": index, "there": there, "outs": outs,
-            "payload_bytes": nbytes, "layers": m}
+            "queries": queries, "decoded": decoded, "payload_bytes": nbytes, "layers": m}
 
 
 def main(argv=None) -> int:
