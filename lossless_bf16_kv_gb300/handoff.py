@@ -34,7 +34,7 @@ class Shape:
     dim: int = 128
     window: int = 1024
     sinks: int = 4
-    budget: int = 512      # cached tokens a layer and head keeps
+    budget: int = 512      # cached tokens a layer and head keeps at most
     observe: int = 64      # last queries whose attention decides
     steps: int = 8         # tokens decoded
     fmt: str = "bf16"
@@ -43,6 +43,11 @@ class Shape:
     @property
     def dtype(self) -> torch.dtype:
         return torch.bfloat16 if self.fmt == "bf16" else torch.float8_e5m2
+
+    @property
+    def kept(self) -> int:
+        """Cached tokens a layer and head keeps: a prompt shorter than the budget keeps all of its own."""
+        return min(self.budget, self.tokens)
 
 
 class Layers:
@@ -100,11 +105,11 @@ def prefill(m: Layers):
 
 
 def thin(s: Shape, kv: torch.Tensor, weights: torch.Tensor):
-    """(thinned cache, kept slots [layers, kv_heads, budget]): all layers in one call, as its batch."""
-    small = torch.empty((s.layers, 2, s.budget, s.kv_heads, s.dim), dtype=kv.dtype, device=kv.device)
-    index = torch.empty((s.layers, s.kv_heads, s.budget), dtype=torch.int32, device=kv.device)
-    serving.splitzip_evict(kv[:, 0], kv[:, 1], weights, small[:, 0], small[:, 1], index, keep_first=min(s.sinks, s.budget),
-                           keep_last=min(s.observe, s.budget - min(s.sinks, s.budget)))
+    """(thinned cache, kept slots [layers, kv_heads, kept]): all layers in one call, as its batch."""
+    small = torch.empty((s.layers, 2, s.kept, s.kv_heads, s.dim), dtype=kv.dtype, device=kv.device)
+    index = torch.empty((s.layers, s.kv_heads, s.kept), dtype=torch.int32, device=kv.device)
+    serving.splitzip_evict(kv[:, 0], kv[:, 1], weights, small[:, 0], small[:, 1], index, keep_first=min(s.sinks, s.kept),
+                           keep_last=min(s.observe, s.kept - min(s.sinks, s.kept)))
     return small, index
 
 
@@ -125,15 +130,15 @@ def decode(m: Layers, thinned: torch.Tensor):
     """Attention outputs [steps, layers, q_heads, dim] of the new tokens over the thinned cache and themselves,
     their queries likewise, and the cache with the new tokens appended."""
     s, dev = m.s, m.device
-    kv = torch.empty((s.layers, 2, s.budget + s.steps, s.kv_heads, s.dim), dtype=thinned.dtype, device=dev)
-    kv[:, :, :s.budget] = thinned
+    kv = torch.empty((s.layers, 2, s.kept + s.steps, s.kv_heads, s.dim), dtype=thinned.dtype, device=dev)
+    kv[:, :, :s.kept] = thinned
     queries = torch.empty((s.steps, s.layers, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
     outs = torch.empty_like(queries)
     workspace = serving.alloc_attention_workspace(queries[:1, :1], kv[:1, 0])
-    lens = torch.full((1,), s.budget, dtype=torch.int32, device=dev)
+    lens = torch.full((1,), s.kept, dtype=torch.int32, device=dev)
     for step in range(s.steps):
         position = torch.full((1,), s.tokens + step, dtype=torch.int32, device=dev)   # in the whole text
-        slot = torch.full((1,), s.budget + step, dtype=torch.int64, device=dev)       # in the thinned cache
+        slot = torch.full((1,), s.kept + step, dtype=torch.int64, device=dev)       # in the thinned cache
         lens += 1
         x = m.new[step:step + 1]
         for layer in range(s.layers):
@@ -166,7 +171,7 @@ def main(argv=None) -> int:
     bits = torch.int16 if s.fmt == "bf16" else torch.uint8
     same = torch.equal(r["small"].view(bits), r["there"].view(bits))
     whole, thinned = (t.numel() * t.element_size() for t in (r["kv"], r["small"]))
-    print(f"{s.layers} layers, {s.tokens} tokens: cache {whole / 1e6:.1f} MB, thinned to {s.budget} tokens {thinned / 1e6:.1f} MB, "
+    print(f"{s.layers} layers, {s.tokens} tokens: cache {whole / 1e6:.1f} MB, thinned to {s.kept} tokens {thinned / 1e6:.1f} MB, "
           f"sent {r['payload_bytes'] / 1e6:.1f} MB ({whole / r['payload_bytes']:.2f}x less than the cache)")
     print(f"arrived bit for bit: {same}; {s.steps} tokens decoded, outputs finite: {bool(torch.isfinite(r['outs']).all())}")
     return 0 if same else 1

@@ -47,3 +47,12 @@ def test_decode_over_a_thinned_cache(fmt, heads, dim):
     ensure_library()
     check_decode(handoff.Shape(layers=2, tokens=300, q_heads=heads[0], kv_heads=heads[1], dim=dim, window=120, sinks=4,
                                budget=70, observe=16, steps=3, fmt=fmt, seed=3), 70)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+@pytest.mark.parametrize("tokens,budget", [(50, 128), (5, 6), (40, 40)])
+def test_decode_after_a_prompt_shorter_than_the_budget(tokens, budget, fmt):
+    """Only the prompt's tokens are there to attend to, however many would be kept."""
+    ensure_library()
+    check_decode(handoff.Shape(layers=2, tokens=tokens, q_heads=8, kv_heads=2, dim=64, window=32, sinks=4, budget=budget,
+                               observe=16, steps=2, fmt=fmt, seed=4), tokens)
