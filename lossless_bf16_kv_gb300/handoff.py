@@ -91,14 +91,14 @@ def prefill(m: Layers):
     q = torch.empty((1, s.tokens, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
     out, lse = torch.empty_like(q), torch.empty((1, s.q_heads, s.tokens), device=dev)
     workspace = serving.alloc_attention_workspace(q, kv[:1, 0], s.window, s.sinks)
-    last = min(s.observe, s.tokens)
+    watch = s.tokens - min(s.observe, s.tokens)     # the first of the last queries
     x = m.prompt
     for layer in range(s.layers):
         qr, kr, vr = m.project(layer, x)
         k, v = kv[layer:layer + 1, 0], kv[layer:layer + 1, 1]
         serving.splitzip_qk_norm_rope(qr, kr, vr, m.norm[layer][0], m.norm[layer][1], positions, m.table, slots, q[0], k, v)
         serving.splitzip_attention(q, k, v, out, workspace, lse=lse, window=s.window, sinks=s.sinks)
-        serving.splitzip_attention_weights(q[:, -last:], k, lse[:, :, -last:].contiguous(), weights[layer:layer + 1],
+        serving.splitzip_attention_weights(q[:, watch:], k, lse[:, :, watch:].contiguous(), weights[layer:layer + 1],
                                            window=s.window, sinks=s.sinks)
         x = m.mix(layer, x, out[0])
     return kv, weights

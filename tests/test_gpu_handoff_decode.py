@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from lossless_bf16_kv_gb300 import handoff
+from lossless_bf16_kv_gb300 import splitzip as sz
 from tests import serving_ref as ref
 from tests.gpu_helpers import ensure_library
 from tests.test_gpu_serving import close
@@ -56,3 +57,10 @@ def test_decode_after_a_prompt_shorter_than_the_budget(tokens, budget, fmt):
     ensure_library()
     check_decode(handoff.Shape(layers=2, tokens=tokens, q_heads=8, kv_heads=2, dim=64, window=32, sinks=4, budget=budget,
                                observe=16, steps=2, fmt=fmt, seed=4), tokens)
+
+
+def test_no_query_to_weigh_by_is_refused():
+    """With none to observe, none decides; not all of the prompt's."""
+    ensure_library()
+    with pytest.raises(sz.SplitZipError):
+        handoff.run(handoff.Shape(layers=1, tokens=30, q_heads=2, kv_heads=1, dim=64, budget=10, observe=0, steps=1))
