@@ -359,10 +359,15 @@ def splitzip_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         _check(status, "splitzip_attention")
 
 
+_HEADER = 1024   # bytes that every workspace begins with: counters, then the status in the last word
+
+
 def splitzip_attention_status(workspace: torch.Tensor, stream=None) -> int:
     """Status of the attention calls on this workspace since the last report
     (OK or ERR_TIMEOUT); synchronises the stream."""
     _check_array(workspace, _U8, None, "workspace")
+    if workspace.numel() < _HEADER:
+        _bad(f"a workspace of {workspace.numel()} bytes is none of splitzip_attention's")
     return int(library().splitzip_attention_status(workspace.data_ptr(), _stream_of(stream)))
 
 

@@ -89,3 +89,20 @@ def test_attention_refuses_tokens_whose_tiles_pass_32_bits(lib):
         assert lib.splitzip_attention_weights(ctypes.byref(a), None, FAKE, None) == inv
         a.kv_tokens, a.q_tokens = min(a.kv_tokens, (1 << 31) - 256), min(a.q_tokens, ((1 << 31) - 256) // a.q_heads)
         assert lib.splitzip_attention_workspace_bytes(ctypes.byref(a)) > 0
+
+
+def test_status_refuses_what_is_no_workspace(lib, monkeypatch):
+    """The status is a word of the workspace's header: a shorter tensor has none, and
+    the word behind it is someone else's."""
+    q = torch.empty((1, 1, 1, 64), dtype=torch.bfloat16)
+    least = serving.splitzip_attention_workspace_bytes(q, q)
+    assert least == serving._HEADER
+    reached = []
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(serving, "_stream_of", lambda s: 0)
+    monkeypatch.setattr(lib, "splitzip_attention_status", lambda w, s: reached.append(w) or 0)
+    for n in (0, 16, least - 1):
+        with pytest.raises(sz.SplitZipError) as err:
+            serving.splitzip_attention_status(torch.zeros(n, dtype=torch.uint8))
+        assert err.value.status == sz.ERR_INVALID_ARG and not reached
+    assert serving.splitzip_attention_status(torch.zeros(least, dtype=torch.uint8)) == 0 and len(reached) == 1
