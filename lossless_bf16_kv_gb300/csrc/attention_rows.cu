@@ -33,6 +33,12 @@ constexpr int kWarpsRows = 4;
 constexpr int kStagesRows = 2;
 constexpr uint32_t kCtasPerSm = 3;  // of 16-row tiles, by registers and shared memory
 constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
+// log2 of p at a row's maximum: m is that much less than the maximum.  FP16 holds p in
+// full from 2^-14 to 2^16, so with 2^15 on top terms down to 2^-29 of a row's largest
+// keep all bits and those below 2^-40 vanish.  With 1 on top those below 2^-25 do,
+// and 2^17 slots of them are 2^-8 of the sum.
+template <bool kF8>
+constexpr float kLift = kF8 ? 15.0f : 0.0f;
 
 struct RowsParams {
     splitzip_attention_args a;
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
         uint32_t pr[MT][PS][4];
 #pragma unroll
         for (int i = 0; i < MT; i++) {
-            float top[2] = {m[i][0], m[i][1]};
+            float top[2] = {m[i][0] + kLift<kF8>, m[i][1] + kLift<kF8>};
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -256,6 +262,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
                 top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
                 top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
             }
+            top[0] -= kLift<kF8>, top[1] -= kLift<kF8>;
             const bool same = top[0] == m[i][0] && top[1] == m[i][1];
             const float use[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
             if (!__all_sync(0xFFFFFFFFu, same)) {
@@ -280,7 +287,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
                     l[i][x >> 1] += e[x];
                 }
                 // p in 16 bits for the product: a relative error of up to 2^-8 (BF16) or
-                // 2^-11 (FP16) of each term, independent from term to term.
+                // 2^-11 (FP16, down to 2^-29 of the row's largest) of each term,
+                // independent from term to term.
                 pr[i][n >> 1][2 * (n & 1)] = pack2<kF8>(e[0], e[1]);
                 pr[i][n >> 1][2 * (n & 1) + 1] = pack2<kF8>(e[2], e[3]);
             }

@@ -46,6 +46,12 @@
 // The running maximum is only raised when a row's maximum grows by more than
 // 2^8 (in which case O and l are rescaled by the softmax warps, after the
 // product that wrote O): P stays below 2^8, and the quotient O / l is the same.
+// For an E5M2 cache P is FP16, which has fewer exponents: there it is up to 2^9 at
+// a maximum just taken and 2^15.9 before the next, so that terms down to 2^-22 of a
+// row's largest keep all bits and those below 2^-33 vanish (with 1 and 2^8 those
+// below 2^-25 did, and 2^17 slots of them are 2^-8 of the sum).  Giving the growth
+// less room costs steps that settle: 2^11 and 2^4 made 16384 tokens in a window
+// behind sinks 1016 us, where 2^9 and 2^6.9 take 938, as 1 and 2^8 did.
 // Each half of a row starts with the maximum that it would choose by itself, and
 // the two settle after their exponentials: an exchange before them in every step
 // cost 285 us where this takes 273.
@@ -64,7 +70,11 @@ constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
 constexpr int kSoftmax = 512;  // threads
 constexpr int kPart = 16;      // scores turned into P at a time: eight words
-constexpr float kLazy = 8.0f;  // log2 of how far P may exceed 1
+// log2 of P at a maximum just taken, and of how far a P may exceed that.
+template <bool kF8>
+constexpr float kLift = kF8 ? 9.0f : 0.0f;
+template <bool kF8>
+constexpr float kLazy = kF8 ? 6.9f : 8.0f;
 
 template <int D, bool kF8>
 struct TilesShape {
@@ -460,7 +470,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         }
         // P of this half by the maximum that it would choose; an integer, so that P can
         // be brought to another one without a second rounding.
-        const float mine = own > m + kLazy ? ceilf(own) : m;  // from -inf too
+        const float mine = own > m + (kLift<kF8> + kLazy<kF8>) ? ceilf(own) - kLift<kF8> : m;  // from -inf too
         const float use = mine == -INFINITY ? 0.0f : mine;
         const uint64_t sc = pair(scale, scale), neg = pair(-use, -use);
         uint64_t sum[2] = {0, 0};
@@ -475,7 +485,8 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
                 u = exp2_approx(u);
                 v = exp2_approx(v);
                 sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(u, v));
-                // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16) of each term.
+                // P in 16 bits: an error of up to 2^-8 (BF16) or 2^-11 (FP16, down to 2^-22 of
+                // the row's largest) of each term.
                 w[x >> 1] = pack2<kF8>(u, v);
             }
             tmem_st8(pa + 8 * c, w);
