@@ -132,9 +132,10 @@ typedef struct splitzip_attention_args {
 size_t splitzip_attention_workspace_bytes(const splitzip_attention_args *args);
 
 /* out = softmax(scale q k^T over the visible slots) v, and lse = log(sum
- * exp(scale q k^T)) (natural logarithm).  A query that sees nothing gets out =
- * 0 and lse = -inf.  Scores, the softmax statistics and sums are held in 32
- * bits.  workspace: 16-byte aligned, workspace_bytes of it. */
+ * exp(scale q k^T)) (natural logarithm).  A query that sees nothing, or scores
+ * of -infinity alone, gets out = 0 and lse = -inf, and gives no weight below.
+ * Scores, the softmax statistics and sums are held in 32 bits.  workspace:
+ * 16-byte aligned, workspace_bytes of it. */
 splitzip_status splitzip_attention(const splitzip_attention_args *args, void *workspace,
                                    size_t workspace_bytes, splitzip_stream_t s);
 

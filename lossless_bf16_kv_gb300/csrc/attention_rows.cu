@@ -410,14 +410,14 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
     auto store = [&](uint32_t r, uint32_t c, float4 v, float mm, float ll) {
         const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
         const uint32_t hq = h * p.group + g;
-        const bool sees = mask.first + (int32_t)t >= 0;  // its own position, then
+        const bool none = ll == 0.0f;  // nothing seen, or scores of -infinity alone
         const float inv = 1.0f / ll;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)t * a.out.stride_t +
                              hq * a.out.stride_h;
         *reinterpret_cast<uint2*>(out + c) =
-            sees ? make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+            none ? make_uint2(0, 0) : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
         if (c == 0 && a.lse)
-            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
     constexpr uint32_t kPart = S::kTileRows * (D + 4);  // floats of a partial result: rows of o, m, l
     const uint32_t group = split / cluster;

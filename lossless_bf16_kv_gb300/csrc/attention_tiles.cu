@@ -745,6 +745,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
         float* lse = p.a.lse ? p.a.lse + ((uint64_t)sh.b * p.a.q_heads + hq) * p.a.q_tokens + tok : nullptr;
         if (!kTwin && p.splits == 1) {
             const float inv = 1.0f / l;
+            const bool none = l == 0.0f;  // nothing seen, or scores of -infinity alone
 #pragma unroll 1
             for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
                 float o[32];
@@ -753,12 +754,12 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
 #pragma unroll
                     for (int x = 0; x < 32; x += 8)
                         *reinterpret_cast<uint4*>(out + 32 * c + x) =
-                            pos < 0 ? make_uint4(0, 0, 0, 0)
-                                    : make_uint4(pack2<false>(o[x] * inv, o[x + 1] * inv), pack2<false>(o[x + 2] * inv, o[x + 3] * inv),
-                                                 pack2<false>(o[x + 4] * inv, o[x + 5] * inv), pack2<false>(o[x + 6] * inv, o[x + 7] * inv));
+                            none ? make_uint4(0, 0, 0, 0)
+                                 : make_uint4(pack2<false>(o[x] * inv, o[x + 1] * inv), pack2<false>(o[x + 2] * inv, o[x + 3] * inv),
+                                              pack2<false>(o[x + 4] * inv, o[x + 5] * inv), pack2<false>(o[x + 6] * inv, o[x + 7] * inv));
                 }
             }
-            if (valid && lse && half == 0) *lse = pos < 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (valid && lse && half == 0) *lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
             // Join the cluster's splits: every CTA leaves its rows in shared memory and
             // joins a share of them, in the order of the splits.
@@ -796,14 +797,14 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
                     v = make_float4(fmaf(v.x, f, y.x * gi), fmaf(v.y, f, y.y * gi), fmaf(v.z, f, y.z * gi), fmaf(v.w, f, y.w * gi));
                     mm = top;
                 }
-                const bool sees = sh.first + (int32_t)xt >= 0;
+                const bool none = ll == 0.0f;
                 const float inv = 1.0f / ll;
                 __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.a.out.data) + (int64_t)sh.b * p.a.out.stride_b +
                                     (int64_t)xt * p.a.out.stride_t + (int64_t)xh * p.a.out.stride_h;
                 *reinterpret_cast<uint2*>(to + c) =
-                    sees ? make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv)) : make_uint2(0, 0);
+                    none ? make_uint2(0, 0) : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
                 if (c == 0 && p.a.lse)
-                    p.a.lse[((uint64_t)sh.b * p.a.q_heads + xh) * p.a.q_tokens + xt] = sees ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                    p.a.lse[((uint64_t)sh.b * p.a.q_heads + xh) * p.a.q_tokens + xt] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
             }
             __syncwarp();
             cluster_sync();  // this CTA's rows have been read

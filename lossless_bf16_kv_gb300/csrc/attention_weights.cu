@@ -300,7 +300,11 @@ __device__ __forceinline__ void bring_lse(const WeightsParams& p, WeightsShared&
         const uint32_t of = n - held, x = of % kMetas, use = of / kMetas;
         if (use && !mbar_wait_bounded(&sh.meta_free[x], (use - 1) & 1, err)) return false;
 #pragma unroll
-        for (int y = 0; y < 4; y++) sh.lse[x][32 * y + lane] = (held == 2 ? value[0][y] : value[1][y]) * -kLog2e;
+        for (int y = 0; y < 4; y++) {
+            // -infinity: the query has no score above it, and gives no weight.
+            const float v = held == 2 ? value[0][y] : value[1][y];
+            sh.lse[x][32 * y + lane] = v == -INFINITY ? 0.0f : v * -kLog2e;
+        }
         held--;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.meta_full[x]);
