@@ -8,27 +8,30 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "wait_time.h"
 
 namespace splitzip {
 
 // ------------------------------------------------------- bounded waits
 //
-// A wait gives up after kWaitLimitNs, or as soon as another wait of the CTA
-// has (then *err is set); the caller drains and returns.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// A wait gives up after kWaitLimit (units of 2^10 ns: two seconds) of the program's
+// own time on the GPU, or as soon as another wait of the CTA has (then *err is set);
+// the caller drains and returns.
+constexpr uint32_t kWaitLimit = 2000000000u >> 10;
 
-__device__ __forceinline__ uint64_t clock_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+__device__ __forceinline__ uint32_t clock_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
 }
 __device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* err) {
-    const uint64_t t0 = clock_ns();
+    WaitTime time(clock_ns());
     while (true) {
         for (int i = 0; i < 32; i++)
             if (mbar_try_wait(bar, parity)) return true;
         if (*err) return false;
-        if (clock_ns() - t0 > kWaitLimitNs) {
+        time.round(clock_ns());
+        if (time.waited > kWaitLimit) {
             *err = 1u;
             return false;
         }
