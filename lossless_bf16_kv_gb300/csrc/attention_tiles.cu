@@ -105,6 +105,7 @@ struct TilesParams {
     uint32_t row_ctas, splits;
     uint32_t one_q, one_k, one_v;  // the batch is one sequence: coordinate 0
     uint32_t* status;
+    uint32_t wait_limit;
 };
 
 struct TilesShared {
@@ -114,7 +115,8 @@ struct TilesShared {
     uint64_t q_full;
     uint64_t s_full[2], p_full[2], o_full[2], drained;  // of the query tiles
     uint64_t s_free[2], o_done[2];  // P apart: S is in registers, a step's O is there
-    uint32_t tmem, err, odd;
+    WaitLimit wait;
+    uint32_t tmem, odd;
     // This CTA's work: sequence, head, first query token; the first slot of step
     // 0, the step that jumps from the sinks to the window and to where.
     uint32_t b, h, t0, steps;
@@ -159,7 +161,7 @@ __device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t lo, int32_t s
 template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw) {
     using S = TilesShape<D, kF8>;
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const int32_t b = (int32_t)sh.b, h = (int32_t)sh.h;
     const uint32_t steps = sh.steps;
     if (!kF8) {
@@ -177,7 +179,7 @@ __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh
     StepSlots slots(sh);
     uint32_t i = 0;
     for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
-        if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, err)) break;
+        if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
         const bool v = i & 1;
         const int32_t bb = (v ? p.one_v : p.one_k) ? 0 : b;
         mbar_arrive_expect_tx(&full[st], kF8 ? S::kRaw : S::kKV);
@@ -192,16 +194,15 @@ __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh
         if (++st == kN) st = 0, ph ^= 1;
     }
     // Every load has landed before this CTA may end, also where a wait gave up.
-    uint32_t late = 0;
-    if (!kF8) mbar_wait_bounded(&sh.q_full, 0, &late);
-    for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded(&full[x % kN], (x / kN) & 1, &late);
+    if (!kF8) mbar_wait_bounded<true>(&sh.q_full, 0, wait);
+    for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded<true>(&full[x % kN], (x / kN) & 1, wait);
 }
 
 template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, const uint8_t* qs, const uint8_t* ring) {
     using S = TilesShape<D, kF8>;
     constexpr uint32_t kShapeS = mma_shape(kF8, kBN, false), kShapeO = mma_shape(kF8, D, true);
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const bool leader = elect_one();
     const uint32_t steps = sh.steps;
     const uint32_t qd = desc_rows(smem_addr(qs)), kd = desc_rows(smem_addr(ring)), vd = desc_columns(smem_addr(ring), kBN * 128);
@@ -227,8 +228,8 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
     static_assert(S::kStages >= 4, "the ring reaches from a slot tile's values to the next but one's keys");
     const auto run_twins = [&]() {
         const auto at = [](uint32_t n) { return n % S::kStages; };
-        const auto loaded = [&](uint32_t n) { return mbar_wait_bounded(&sh.full[at(n)], (n / S::kStages) & 1, err); };
-        if (!mbar_wait_bounded(&sh.q_full, 0, err)) return;
+        const auto loaded = [&](uint32_t n) { return mbar_wait_bounded(&sh.full[at(n)], (n / S::kStages) & 1, wait); };
+        if (!mbar_wait_bounded(&sh.q_full, 0, wait)) return;
         for (uint32_t j = 0; j < min(steps, 2u); j++) {
             if (!loaded(2 * j)) return;
             tcgen_fence_after();
@@ -251,9 +252,9 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
                 __syncwarp();
                 return true;
             };
-            if (!mbar_wait_bounded(&sh.ok[j & 7], (j >> 3) & 1, err) || !loaded(2 * j + 1)) return;
-            if (S::kApart && more && !(mbar_wait_bounded(&sh.s_free[t], turn, err) && next_s())) return;
-            if (!mbar_wait_bounded(&sh.p_full[t], turn, err)) return;
+            if (!mbar_wait_bounded(&sh.ok[j & 7], (j >> 3) & 1, wait) || !loaded(2 * j + 1)) return;
+            if (S::kApart && more && !(mbar_wait_bounded(&sh.s_free[t], turn, wait) && next_s())) return;
+            if (!mbar_wait_bounded(&sh.p_full[t], turn, wait)) return;
             tcgen_fence_after();
             if (leader) {
                 issue_o(t, vst, j > 1);
@@ -271,7 +272,7 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
         if (++st == S::kStages) st = 0, ph ^= 1;
     };
     const auto run = [&]() {
-        if (!mbar_wait_bounded(&sh.q_full, 0, err) || !mbar_wait_bounded(&sh.full[0], 0, err)) return;
+        if (!mbar_wait_bounded(&sh.q_full, 0, wait) || !mbar_wait_bounded(&sh.full[0], 0, wait)) return;
         tcgen_fence_after();
         if (leader) {
             issue_s(0, 0);
@@ -282,12 +283,12 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
         for (uint32_t i = 0; i + 1 < steps; i++) {
             const uint32_t vst = st, vph = ph;
             next();
-            if (!mbar_wait_bounded(&sh.full[st], ph, err)) return;
-            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[vst], vph, err)) return;
+            if (!mbar_wait_bounded(&sh.full[st], ph, wait)) return;
+            if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, wait) || !mbar_wait_bounded(&sh.full[vst], vph, wait)) return;
 #pragma unroll
             for (uint32_t t = 0; t < 2; t++) {
                 if constexpr (S::kApart) {
-                    if (!mbar_wait_bounded(&sh.s_free[t], i & 1, err)) return;
+                    if (!mbar_wait_bounded(&sh.s_free[t], i & 1, wait)) return;
                     tcgen_fence_after();
                     if (leader) {
                         issue_s(t, st);
@@ -295,7 +296,7 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
                     }
                     __syncwarp();
                 }
-                if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
+                if (!mbar_wait_bounded(&sh.p_full[t], i & 1, wait)) return;
                 tcgen_fence_after();
                 if (leader) {
                     issue_o(t, vst, i > 0);
@@ -315,10 +316,10 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
             next();
         }
         const uint32_t i = steps - 1;
-        if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, err) || !mbar_wait_bounded(&sh.full[st], ph, err)) return;
+        if (!mbar_wait_bounded(&sh.ok[i & 7], (i >> 3) & 1, wait) || !mbar_wait_bounded(&sh.full[st], ph, wait)) return;
 #pragma unroll
         for (uint32_t t = 0; t < 2; t++) {
-            if (!mbar_wait_bounded(&sh.p_full[t], i & 1, err)) return;
+            if (!mbar_wait_bounded(&sh.p_full[t], i & 1, wait)) return;
             tcgen_fence_after();
             if (leader) {
                 issue_o(t, st, i > 0);
@@ -329,10 +330,9 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
     };
     if constexpr (kTwin) run_twins();
     else run();
-    uint32_t late = 0;
     __syncwarp();
     if (leader) mma_commit(&sh.drained);
-    mbar_wait_bounded(&sh.drained, 0, &late);
+    mbar_wait_bounded<true>(&sh.drained, 0, wait);
 }
 
 // Values of partly visible tiles: infinities and NaN become 0 here and are added
@@ -340,7 +340,7 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
 template <int D, bool kF8>
 __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, const uint8_t* raw, uint32_t thread) {
     using S = TilesShape<D, kF8>;
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const uint32_t lane = thread & 31, steps = sh.steps;
     StepSlots slots(sh);
     const WholeTiles whole(sh, sh.p0, sh.p1);
@@ -349,8 +349,8 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
         const uint32_t mine = thread >= 16 * S::kTend, in_half = thread - mine * 16 * S::kTend;
         for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
             const uint32_t rs = n % S::kRaws, st = n % S::kStages;
-            if (!mbar_wait_bounded(&sh.raw_full[rs], (n / S::kRaws) & 1, err)) break;
-            if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, err)) break;
+            if (!mbar_wait_bounded(&sh.raw_full[rs], (n / S::kRaws) & 1, wait)) break;
+            if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, wait)) break;
             const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
             bool found = false;
             // 16 bytes of a row become two adjacent 16-byte chunks of the swizzled row.
@@ -385,7 +385,7 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
     } else {
         for (uint32_t i = 0; i < steps; i++, slots.next()) {
             const uint32_t n = 2 * i + 1, st = n % S::kStages, ph = (n / S::kStages) & 1;
-            if (!mbar_wait_bounded(&sh.full[st], ph, err)) break;
+            if (!mbar_wait_bounded(&sh.full[st], ph, wait)) break;
             if (sh.p0 < 0 || !whole(slots.s0)) {
                 bool found = false;
                 uint4* tile = reinterpret_cast<uint4*>(ring + st * S::kKV);
@@ -415,7 +415,7 @@ __device__ __forceinline__ void tend_values(TilesShared& sh, uint8_t* ring, cons
 template <int D, bool kF8, bool kTwin>
 __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
                                              uint32_t r, uint32_t pair_bar, int32_t pos, float scale, float& m, float& l) {
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     using S = TilesShape<D, kF8>;
     const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + half * S::kHalfP;
     // What a step needs only a moment is read again from shared memory, as volatile.
@@ -429,7 +429,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
     l = 0.0f;
     bool ready = true, more = j < now_sh.steps;
     for (uint32_t i = 0; more; i++) {
-        ready = mbar_wait_bounded(&sh.s_full[t], i & 1, err) && ready;
+        ready = mbar_wait_bounded(&sh.s_full[t], i & 1, wait) && ready;
         tcgen_fence_after();
         uint32_t s[2][32];
         tmem_ld32(s[0], sa + 64 * half);
@@ -464,7 +464,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         if (kTwin) advance(jump_at, jump_to);
         const float own = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
         if constexpr (S::kApart) {  // the last step's product is done with P
-            if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, err) && ready;
+            if (i) ready = mbar_wait_bounded(&sh.o_done[t], (i - 1) & 1, wait) && ready;
             tcgen_fence_after();
             __syncwarp();
         }
@@ -547,7 +547,7 @@ __device__ __forceinline__ bool softmax_rows(const TilesParams& p, TilesShared& 
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[t]);
     }
     // Both tiles' products are done: a CTA's partial results take the tiles' place.
-    const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[0], 0, err) && mbar_wait_bounded(&sh.o_full[1], 0, err));
+    const bool go = sh.steps == 0 || (ready && mbar_wait_bounded(&sh.o_full[0], 0, wait) && mbar_wait_bounded(&sh.o_full[1], 0, wait));
     tcgen_fence_after();
     return go;
 }
@@ -651,7 +651,8 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
             mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.drained, 1);
-        sh.err = sh.odd = 0;
+        sh.wait.given_up = sh.odd = 0;
+        sh.wait.limit = p.wait_limit;
         fence_mbar_init();
     }
     if (!kF8 && threadIdx.x < 256) {
@@ -886,6 +887,7 @@ cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const Atten
     p.row_ctas = plan.row_tiles;
     p.splits = plan.splits;
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
+    p.wait_limit = wait_limit(0);  // a few steps at most
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
     p.one_q = 1;
     if ((!f8 && !make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q)) ||

@@ -56,6 +56,7 @@ struct WeightsParams {
     ChunkDiv by_heads, by_kv_heads, by_tokens;  // divisions by batch * kv_heads, kv_heads, tokens
     uint32_t window;         // at most 2^31: unlimited
     uint32_t one_q, one_k;   // the batch is one sequence: coordinate 0
+    uint32_t wait_limit;
 };
 
 template <int D, bool kF8>
@@ -94,7 +95,8 @@ struct WeightsShared {
     uint64_t s_full[4], s_free[4];
     uint64_t meta_full[kMetas], meta_free[kMetas];
     uint64_t drained;
-    uint32_t tmem, err;
+    WaitLimit wait;
+    uint32_t tmem;
     alignas(16) float lse[kMetas][kRowTile];  // times -log2(e)
     float part[2][4][kSlotTile];              // sums of the four groups of warps, by item
 };
@@ -111,7 +113,7 @@ struct Items {
     __device__ __forceinline__ bool next() {
         while (true) {
             const uint32_t x = at % kItems;
-            if (!mbar_wait_bounded(&sh.item_full[x], (at / kItems) & 1, &sh.err)) return false;
+            if (!mbar_wait_bounded(&sh.item_full[x], (at / kItems) & 1, &sh.wait)) return false;
             w = sh.item[x];
             __syncwarp();
             if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.item_free[x]);
@@ -168,7 +170,7 @@ __device__ __forceinline__ void plan_items(const WeightsParams& p, WeightsShared
                 }
             }
         }
-        if (use && !mbar_wait_bounded(&sh.item_free[x], (use - 1) & 1, &sh.err)) return;
+        if (use && !mbar_wait_bounded(&sh.item_free[x], (use - 1) & 1, &sh.wait)) return;
         sh.item[x] = w;
         mbar_arrive(&sh.item_full[x]);
         if (w.bh == kNoItem) return;
@@ -186,7 +188,7 @@ template <int D, bool kF8>
 __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared& sh, uint8_t* ks, uint8_t* ring, uint8_t* raw) {
     using S = WeightsShape<D, kF8>;
     constexpr uint32_t kN = kF8 ? kRaws : kKStages;
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     uint64_t* k_full = kF8 ? sh.raw_full : sh.k_full;
     uint64_t* k_empty = kF8 ? sh.raw_empty : sh.k_empty;
     uint32_t it = 0, n = 0;
@@ -196,7 +198,7 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
     while (go && list.next()) {
         const Item& w = list.w;
         const uint32_t ks_at = it % kN, use = it / kN;
-        if (use && !mbar_wait_bounded(&k_empty[ks_at], (use - 1) & 1, err)) break;
+        if (use && !mbar_wait_bounded(&k_empty[ks_at], (use - 1) & 1, wait)) break;
         if (leader) mbar_arrive_expect_tx(&k_full[ks_at], kF8 ? S::kRaw : S::kTile);
         if (kF8) {
             if (leader) tma_load4(raw + ks_at * S::kRaw, &p.kmap, 0, w.s_lo, (int32_t)w.h, p.one_k ? 0 : (int32_t)w.b, &k_full[ks_at]);
@@ -209,7 +211,7 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
         it++;
         for (uint32_t i = 0; i < w.steps; i++, n++) {
             const uint32_t st = n % kQStages, quse = n / kQStages;
-            if (quse && !(go = mbar_wait_bounded(&sh.q_empty[st], (quse - 1) & 1, err))) break;
+            if (quse && !(go = mbar_wait_bounded(&sh.q_empty[st], (quse - 1) & 1, wait))) break;
             if (leader) {
                 mbar_arrive_expect_tx(&sh.q_full[st], p.tokens * p.group * D * 2);
 #pragma unroll
@@ -221,17 +223,16 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
         }
     }
     // Every load has landed before this CTA may end, also where a wait gave up.
-    uint32_t late = 0;
-    for (uint32_t x = it > kN ? it - kN : 0; x < it; x++) mbar_wait_bounded(&k_full[x % kN], (x / kN) & 1, &late);
+    for (uint32_t x = it > kN ? it - kN : 0; x < it; x++) mbar_wait_bounded<true>(&k_full[x % kN], (x / kN) & 1, wait);
     for (uint32_t x = n > kQStages ? n - kQStages : 0; x < n; x++)
-        mbar_wait_bounded(&sh.q_full[x % kQStages], (x / kQStages) & 1, &late);
+        mbar_wait_bounded<true>(&sh.q_full[x % kQStages], (x / kQStages) & 1, wait);
 }
 
 // The whole warp takes the items, one lane issues.
 template <int D, bool kF8>
 __device__ __forceinline__ void issue_items(const WeightsParams& p, WeightsShared& sh, uint32_t tmem, const uint8_t* ks, const uint8_t* ring) {
     using S = WeightsShape<D, kF8>;
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const bool leader = elect_one();
     const uint32_t kd = desc_rows(smem_addr(ks)), qd = desc_rows(smem_addr(ring));
     const uint32_t leader_lane = __ffs(__ballot_sync(0xFFFFFFFFu, leader)) - 1;
@@ -243,14 +244,14 @@ __device__ __forceinline__ void issue_items(const WeightsParams& p, WeightsShare
     while (go && list.next()) {
         const Item& w = list.w;
         const uint32_t kst = it % kKStages;
-        go = mbar_wait_bounded(&sh.k_full[kst], (it / kKStages) & 1, err);
+        go = mbar_wait_bounded(&sh.k_full[kst], (it / kKStages) & 1, wait);
         tcgen_fence_after();
         if (leader) {
             const uint32_t ka = kd + kst * (S::kTile >> 4);
             for (uint32_t i = 0; go && i < w.steps; i++, n++) {
                 const uint32_t x = n & 3;
-                go = ready || (mbar_wait_bounded(&sh.q_full[st], turn, err) &&
-                               (n < 4 || mbar_wait_bounded(&sh.s_free[x], ((n >> 2) - 1) & 1, err)));
+                go = ready || (mbar_wait_bounded(&sh.q_full[st], turn, wait) &&
+                               (n < 4 || mbar_wait_bounded(&sh.s_free[x], ((n >> 2) - 1) & 1, wait)));
                 if (!go) break;
                 const uint32_t shape = i + 1 < w.steps ? most : mma_shape(false, (tile_rows(p, w, i) + 15) & ~15u, false);
                 const uint32_t qa = qd + st * (S::kTile >> 4);
@@ -276,15 +277,14 @@ __device__ __forceinline__ void issue_items(const WeightsParams& p, WeightsShare
         go = __shfl_sync(0xFFFFFFFFu, (int)go, leader_lane) != 0;
         it++;
     }
-    uint32_t late = 0;
     __syncwarp();
     if (leader) mma_commit(&sh.drained);
-    mbar_wait_bounded(&sh.drained, 0, &late);
+    mbar_wait_bounded<true>(&sh.drained, 0, wait);
 }
 
 // One warp; two tiles' values are on their way while an earlier one's are handed over.
 __device__ __forceinline__ void bring_lse(const WeightsParams& p, WeightsShared& sh) {
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const uint32_t lane = threadIdx.x & 31;
     uint32_t place[4];  // of this lane's four rows: token in the tile
     uint64_t head[4];   // and the start of the query head's values
@@ -298,7 +298,7 @@ __device__ __forceinline__ void bring_lse(const WeightsParams& p, WeightsShared&
     uint32_t n = 0, held = 0;  // value[2 - held ..] are the tiles n - held ..
     auto hand_over = [&]() {   // the oldest tile held
         const uint32_t of = n - held, x = of % kMetas, use = of / kMetas;
-        if (use && !mbar_wait_bounded(&sh.meta_free[x], (use - 1) & 1, err)) return false;
+        if (use && !mbar_wait_bounded(&sh.meta_free[x], (use - 1) & 1, wait)) return false;
 #pragma unroll
         for (int y = 0; y < 4; y++) {
             // -infinity: the query has no score above it, and gives no weight.
@@ -338,13 +338,13 @@ __device__ __forceinline__ void bring_lse(const WeightsParams& p, WeightsShared&
 template <int D>
 __device__ __forceinline__ void widen_keys(const WeightsParams& p, WeightsShared& sh, uint8_t* ks, const uint8_t* raw, uint32_t thread) {
     using S = WeightsShape<D, true>;
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     uint32_t it = 0;
     Items list(sh);
     while (list.next()) {
         const uint32_t rs = it % kRaws, st = it % kKStages;
-        if (!mbar_wait_bounded(&sh.raw_full[rs], (it / kRaws) & 1, err)) return;
-        if (it >= kKStages && !mbar_wait_bounded(&sh.k_empty[st], (it / kKStages - 1) & 1, err)) return;
+        if (!mbar_wait_bounded(&sh.raw_full[rs], (it / kRaws) & 1, wait)) return;
+        if (it >= kKStages && !mbar_wait_bounded(&sh.k_empty[st], (it / kKStages - 1) & 1, wait)) return;
         // 16 bytes of a row become two adjacent 16-byte chunks of the swizzled row.
 #pragma unroll 2
         for (uint32_t x = thread; x < kSlotTile * (D / 16); x += 128) {
@@ -378,7 +378,7 @@ __device__ __forceinline__ void give_up(const WeightsParams& p, uint32_t round, 
 
 // Group of warps g: columns 64 (g & 1) .. of the query tiles n with (n & 1) = g >> 1.
 __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared& sh, uint32_t tmem, uint32_t g, uint32_t r) {
-    volatile uint32_t* err = &sh.err;
+    volatile WaitLimit* wait = &sh.wait;
     const uint32_t c0 = (g & 1) * 64;
     const float scale = p.a.scale * kLog2e;
     const uint64_t scale2 = pair(scale, scale);
@@ -389,7 +389,7 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
         // The item's record is read where it lies, and given back at the item's end.
         // Where a wait for one gave up, all return at the barrier below.
         const uint32_t rec = at % kItems;
-        const bool ok = mbar_wait_bounded(&sh.item_full[rec], (at / kItems) & 1, err);
+        const bool ok = mbar_wait_bounded(&sh.item_full[rec], (at / kItems) & 1, wait);
         const Item& w = sh.item[rec];
         if (!ok || w.bh == kNoItem) {
             if (named_any(1, kSum, !ok)) give_up(p, at, g, r);
@@ -406,7 +406,7 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
             const uint32_t x = n & 3, mx = n % kMetas;
             const uint32_t m_at = (n / kMetas) & 1, s_at = (n >> 2) & 1;
             const bool m_there = mbar_try_wait(&sh.meta_full[mx], m_at), s_there = mbar_try_wait(&sh.s_full[x], s_at);  // mostly both
-            const bool there = (m_there & s_there) || (mbar_wait_bounded(&sh.meta_full[mx], m_at, err) && mbar_wait_bounded(&sh.s_full[x], s_at, err));
+            const bool there = (m_there & s_there) || (mbar_wait_bounded(&sh.meta_full[mx], m_at, wait) && mbar_wait_bounded(&sh.s_full[x], s_at, wait));
             if (!__all_sync(0xFFFFFFFFu, there)) {
                 sum = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
                 continue;
@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(WeightsShape<D, kF8>::kThreads, 1) weights_ker
             mbar_init(&sh.item_free[i], S::kThreads / 32 - 1);  // every warp but the one that plans
         }
         mbar_init(&sh.drained, 1);
-        sh.err = 0;
+        sh.wait.given_up = 0;
+        sh.wait.limit = p.wait_limit;
         fence_mbar_init();
     }
     tcgen_fence_before();
@@ -564,6 +565,7 @@ cudaError_t launch_attention_weights(const splitzip_attention_args& a, const flo
     p.by_kv_heads = make_chunk_div(a.kv_heads);
     p.by_tokens = make_chunk_div(p.tokens);
     p.window = a.window ? std::min(a.window, 0x80000000u) : 0x80000000u;
+    p.wait_limit = wait_limit((a.q_tokens + p.tokens - 1) / p.tokens);  // of one item
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
     if (!make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q) ||
         !make_map(p.kmap, a.k, f8 ? 1 : 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kSlotTile, false, &p.one_k))

@@ -17,6 +17,10 @@ namespace splitzip {
 // as long as that was: no round counts for more than this (2^24 ns).
 constexpr uint32_t kMostRound = 1u << 14;
 
+// What a wait may last: two seconds, and for each tile of work that the longest wait
+// of a launch has to sit out 16 us, many times what one takes.  In units of 2^10 ns.
+SPLITZIP_HOST_DEVICE constexpr uint32_t wait_limit(uint32_t tiles) { return (2000000000u >> 10) + 16u * tiles; }
+
 // Counts in units of 2^10 ns, from the lower 32 bits of a clock in ns.
 struct WaitTime {
     uint32_t last, waited;

@@ -46,3 +46,28 @@ def test_time_away_from_the_gpu_does_not_count(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+LIMITS = r"""
+#include <cstdio>
+#include "wait_time.h"
+int main() {
+    // 2^31 - 256 query rows are at most 2^24 tiles of 128, or of 2 x 64; a tile takes about 1 us.
+    for (uint64_t tiles = 0; tiles <= 1ull << 24; tiles += 4099) {
+        const uint64_t ns = (uint64_t)splitzip::wait_limit((uint32_t)tiles) << 10;
+        if (ns < 1999999000ull + 10000 * tiles || ns > 2000000000ull + 20000 * tiles)
+            return std::printf("%llu tiles: %llu ns\n", (unsigned long long)tiles, (unsigned long long)ns), 1;
+    }
+    return 0;
+}
+"""
+
+
+def test_limit_covers_the_longest_valid_wait(tmp_path):
+    """A wait of the weights kernel lasts as long as one item: of the most query rows
+    that a call may have, 17 seconds."""
+    src, exe = tmp_path / "limit.cpp", tmp_path / "limit"
+    src.write_text(LIMITS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", f"-I{CSRC}", str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
