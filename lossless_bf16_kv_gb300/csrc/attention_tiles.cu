@@ -694,7 +694,9 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
             const bool valid = r < p.tokens * p.group && tok < p.a.q_tokens;
             const int32_t pos = valid ? max(-1, sh.first + (int32_t)tok) : -1;
             float scale = p.a.scale * kLog2e;
-            if (kF8) {
+            // Only where there are steps: the products, which wait for all queries, keep this
+            // apart from the partial results that take the queries' place.
+            if (kF8 && sh.steps) {
                 // This thread's half of its query row: FP16 of the row scaled by a power of two.
                 const uint4* src = reinterpret_cast<const uint4*>(
                     static_cast<const __nv_bfloat16*>(p.a.q.data) + (int64_t)sh.b * p.a.q.stride_b + (int64_t)tok * p.a.q.stride_t +
