@@ -106,6 +106,7 @@ struct TilesParams {
     uint32_t one_q, one_k, one_v;  // the batch is one sequence: coordinate 0
     uint32_t* status;
     uint32_t wait_limit;
+    uint32_t test_cta, test_tile;  // a copy that a test has left out
 };
 
 struct TilesShared {
@@ -177,13 +178,15 @@ __device__ __forceinline__ void load_tiles(const TilesParams& p, TilesShared& sh
     uint64_t* full = kF8 ? sh.raw_full : sh.full;
     uint64_t* empty = kF8 ? sh.raw_empty : sh.empty;
     StepSlots slots(sh);
+    const uint32_t left_out = blockIdx.x == p.test_cta ? p.test_tile : 0xFFFFFFFFu;
     uint32_t i = 0;
     for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
         if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
         const bool v = i & 1;
         const int32_t bb = (v ? p.one_v : p.one_k) ? 0 : b;
         mbar_arrive_expect_tx(&full[st], kF8 ? S::kRaw : S::kKV);
-        if (kF8) {
+        if (i == left_out) {
+        } else if (kF8) {
             tma_load4(raw + st * S::kRaw, v ? &p.vmap : &p.kmap, 0, slots.s0, h, bb, &full[st]);
         } else {
 #pragma unroll
@@ -279,6 +282,7 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
             issue_s(1, 0);
             mma_commit(&sh.empty[0]);
         }
+        __syncwarp();
         next();
         for (uint32_t i = 0; i + 1 < steps; i++) {
             const uint32_t vst = st, vph = ph;
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(TilesShape<D, kF8>::kThreads, 1) tiles_kernel(
         sh.row[t][half][r] = l;
         named_sync(pair_bar, 64);
         l = sh.row[t][0][r] + sh.row[t][1][r];
-        if (threadIdx.x == 0 && !go) atomicOr(p.status, kStatusTimeout);
+        if ((threadIdx.x & 31) == 0 && !go) atomicOr(p.status, kStatusTimeout);
         if (!go) l = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
 
         // Derived again rather than kept through the loop.
@@ -881,7 +885,7 @@ bool attention_tiles_usable(const splitzip_attention_args& a) {
 }
 
 cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const AttentionPlan& plan, void* workspace,
-                                   cudaStream_t s) {
+                                   const WaitTest& test, cudaStream_t s) {
     TilesParams p;
     p.a = a;
     p.group = a.q_heads / a.kv_heads;
@@ -889,7 +893,9 @@ cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const Atten
     p.row_ctas = plan.row_tiles;
     p.splits = plan.splits;
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
-    p.wait_limit = wait_limit(0);  // a few steps at most
+    p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a few steps at most
+    p.test_cta = test.cta;
+    p.test_tile = test.tile;
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
     p.one_q = 1;
     if ((!f8 && !make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q)) ||

@@ -57,6 +57,7 @@ struct WeightsParams {
     uint32_t window;         // at most 2^31: unlimited
     uint32_t one_q, one_k;   // the batch is one sequence: coordinate 0
     uint32_t wait_limit;
+    uint32_t test_cta, test_tile;  // a copy that a test has left out
 };
 
 template <int D, bool kF8>
@@ -194,13 +195,15 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
     uint32_t it = 0, n = 0;
     bool go = true;
     const bool leader = elect_one();
+    const uint32_t left_out = blockIdx.x == p.test_cta ? p.test_tile : 0xFFFFFFFFu;
     Items list(sh);
     while (go && list.next()) {
         const Item& w = list.w;
         const uint32_t ks_at = it % kN, use = it / kN;
         if (use && !mbar_wait_bounded(&k_empty[ks_at], (use - 1) & 1, wait)) break;
         if (leader) mbar_arrive_expect_tx(&k_full[ks_at], kF8 ? S::kRaw : S::kTile);
-        if (kF8) {
+        if (it + n == left_out) {
+        } else if (kF8) {
             if (leader) tma_load4(raw + ks_at * S::kRaw, &p.kmap, 0, w.s_lo, (int32_t)w.h, p.one_k ? 0 : (int32_t)w.b, &k_full[ks_at]);
         } else if (leader) {
 #pragma unroll
@@ -215,7 +218,7 @@ __device__ __forceinline__ void load_items(const WeightsParams& p, WeightsShared
             if (leader) {
                 mbar_arrive_expect_tx(&sh.q_full[st], p.tokens * p.group * D * 2);
 #pragma unroll
-                for (int x = 0; x < D / 64; x++)
+                for (int x = 0; x < D / 64 && it + n != left_out; x++)
                     tma_load4(ring + st * S::kTile + x * (kRowTile * 128), &p.qmap, 64 * x, (int32_t)(w.h * p.group),
                               (int32_t)((w.i0 + i) * p.tokens), p.one_q ? 0 : (int32_t)w.b, &sh.q_full[st]);
             }
@@ -553,7 +556,7 @@ cudaError_t launch(const WeightsParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attention_weights(const splitzip_attention_args& a, const float* weights_in, float* weights_out,
-                                     cudaStream_t s) {
+                                     const WaitTest& test, cudaStream_t s) {
     WeightsParams p;
     p.a = a;
     p.in = weights_in;
@@ -565,7 +568,9 @@ cudaError_t launch_attention_weights(const splitzip_attention_args& a, const flo
     p.by_kv_heads = make_chunk_div(a.kv_heads);
     p.by_tokens = make_chunk_div(p.tokens);
     p.window = a.window ? std::min(a.window, 0x80000000u) : 0x80000000u;
-    p.wait_limit = wait_limit((a.q_tokens + p.tokens - 1) / p.tokens);  // of one item
+    p.wait_limit = test.limit ? test.limit : wait_limit((a.q_tokens + p.tokens - 1) / p.tokens);  // a wait lasts an item at most
+    p.test_cta = test.cta;
+    p.test_tile = test.tile;
     const bool f8 = a.cache_format == SPLITZIP_FORMAT_E5M2;
     if (!make_map(p.qmap, a.q, 2, a.head_dim, a.q_heads, a.q_tokens, a.batch, p.group, p.tokens, true, &p.one_q) ||
         !make_map(p.kmap, a.k, f8 ? 1 : 2, a.head_dim, a.kv_heads, a.kv_tokens, a.batch, 1, kSlotTile, false, &p.one_k))

@@ -32,10 +32,15 @@ bool attention_tiles_plan(const splitzip_attention_args& a, AttentionPlan& p);
 bool attention_tiles_usable(const splitzip_attention_args& a);
 cudaError_t launch_attention_rows(const splitzip_attention_args& a, const AttentionPlan& p,
                                   void* workspace, cudaStream_t s);
+// A CTA whose tile-th copy is left out, and the limit of the waits (0: as it is
+// otherwise), for tests of what happens then.
+struct WaitTest {
+    uint32_t limit = 0, cta = 0xFFFFFFFFu, tile = 0xFFFFFFFFu;
+};
 cudaError_t launch_attention_tiles(const splitzip_attention_args& a, const AttentionPlan& p,
-                                   void* workspace, cudaStream_t s);
+                                   void* workspace, const WaitTest& test, cudaStream_t s);
 cudaError_t launch_attention_weights(const splitzip_attention_args& a, const float* weights_in,
-                                     float* weights_out, cudaStream_t s);
+                                     float* weights_out, const WaitTest& test, cudaStream_t s);
 cudaError_t launch_evict(const splitzip_evict_args& a, cudaStream_t s);
 
 }  // namespace splitzip

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "../../include/splitzip_serving_testing.h"
 #include "serving.h"
 #include "trace.h"
 
@@ -57,6 +58,45 @@ size_t bytes_of(const AttentionPlan& rows, const AttentionPlan& tiles) {
     return rows.bytes > tiles.bytes ? rows.bytes : tiles.bytes;
 }
 
+// Both calls, as users make them and (test) with a copy left out.
+splitzip_status attention(const splitzip_attention_args* a, void* workspace, size_t workspace_bytes,
+                          splitzip_stream_t s, const WaitTest* test) {
+    AttentionPlan rows, tiles;
+    if (!a || !sizes_ok(*a) || !plans(*a, rows, tiles)) return SPLITZIP_ERR_INVALID_ARG;
+    const uint32_t e = elem_bytes(a->cache_format);
+    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) || !view_ok(a->out, 2, a->batch, a->q_tokens, a->q_heads, true) ||
+        !view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < bytes_of(rows, tiles))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (on_tiles(*a, rows))
+        return from_cuda(launch_attention_tiles(*a, tiles, workspace, test ? *test : WaitTest(), (cudaStream_t)s));
+    if (test) return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_attention_rows(*a, rows, workspace, (cudaStream_t)s));
+}
+
+splitzip_status attention_weights(const splitzip_attention_args* a, const float* weights_in, float* weights_out,
+                                  splitzip_stream_t s, const WaitTest& test) {
+    if (!a || !sizes_ok(*a) || !weights_out || !a->lse) return SPLITZIP_ERR_INVALID_ARG;
+    if ((uint64_t)a->batch * a->kv_heads * ((a->kv_tokens + 127ull) / 128) > kMax31) return SPLITZIP_ERR_INVALID_ARG;
+    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) ||
+        !view_ok(a->k, elem_bytes(a->cache_format), a->batch, a->kv_tokens, a->kv_heads))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4) ||
+        !std::isfinite(a->scale))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_attention_weights(*a, weights_in, weights_out, test, (cudaStream_t)s));
+}
+
+bool wait_test(const splitzip_wait_test_opts* opts, WaitTest& test) {
+    if (!opts || opts->wait_ms > 2000) return false;
+    test.limit = opts->wait_ms * 1000000u >> 10;
+    test.cta = opts->cta;
+    test.tile = opts->tile;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -92,18 +132,13 @@ size_t splitzip_attention_workspace_bytes(const splitzip_attention_args* a) {
 splitzip_status splitzip_attention(const splitzip_attention_args* a, void* workspace, size_t workspace_bytes,
                                    splitzip_stream_t s) {
     TraceRange trace("splitzip_attention");
-    AttentionPlan rows, tiles;
-    if (!a || !sizes_ok(*a) || !plans(*a, rows, tiles)) return SPLITZIP_ERR_INVALID_ARG;
-    const uint32_t e = elem_bytes(a->cache_format);
-    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) || !view_ok(a->out, 2, a->batch, a->q_tokens, a->q_heads, true) ||
-        !view_ok(a->k, e, a->batch, a->kv_tokens, a->kv_heads) || !view_ok(a->v, e, a->batch, a->kv_tokens, a->kv_heads))
-        return SPLITZIP_ERR_INVALID_ARG;
-    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !std::isfinite(a->scale)) return SPLITZIP_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < bytes_of(rows, tiles))
-        return SPLITZIP_ERR_INVALID_ARG;
-    if (on_tiles(*a, rows))
-        return from_cuda(launch_attention_tiles(*a, tiles, workspace, (cudaStream_t)s));
-    return from_cuda(launch_attention_rows(*a, rows, workspace, (cudaStream_t)s));
+    return attention(a, workspace, workspace_bytes, s, nullptr);
+}
+
+splitzip_status splitzip_attention_test(const splitzip_attention_args* a, void* workspace, size_t workspace_bytes,
+                                        splitzip_stream_t s, const splitzip_wait_test_opts* opts) {
+    WaitTest test;
+    return wait_test(opts, test) ? attention(a, workspace, workspace_bytes, s, &test) : SPLITZIP_ERR_INVALID_ARG;
 }
 
 splitzip_status splitzip_attention_status(void* workspace, splitzip_stream_t s) {
@@ -121,15 +156,14 @@ splitzip_status splitzip_attention_status(void* workspace, splitzip_stream_t s) 
 splitzip_status splitzip_attention_weights(const splitzip_attention_args* a, const float* weights_in,
                                            float* weights_out, splitzip_stream_t s) {
     TraceRange trace("splitzip_attention_weights");
-    if (!a || !sizes_ok(*a) || !weights_out || !a->lse) return SPLITZIP_ERR_INVALID_ARG;
-    if ((uint64_t)a->batch * a->kv_heads * ((a->kv_tokens + 127ull) / 128) > kMax31) return SPLITZIP_ERR_INVALID_ARG;
-    if (!view_ok(a->q, 2, a->batch, a->q_tokens, a->q_heads) ||
-        !view_ok(a->k, elem_bytes(a->cache_format), a->batch, a->kv_tokens, a->kv_heads))
-        return SPLITZIP_ERR_INVALID_ARG;
-    if (!aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(weights_in, 4) || !aligned(weights_out, 4) ||
-        !std::isfinite(a->scale))
-        return SPLITZIP_ERR_INVALID_ARG;
-    return from_cuda(launch_attention_weights(*a, weights_in, weights_out, (cudaStream_t)s));
+    return attention_weights(a, weights_in, weights_out, s, WaitTest());
+}
+
+splitzip_status splitzip_attention_weights_test(const splitzip_attention_args* a, const float* weights_in,
+                                                float* weights_out, splitzip_stream_t s,
+                                                const splitzip_wait_test_opts* opts) {
+    WaitTest test;
+    return wait_test(opts, test) ? attention_weights(a, weights_in, weights_out, s, test) : SPLITZIP_ERR_INVALID_ARG;
 }
 
 splitzip_status splitzip_evict(const splitzip_evict_args* a, splitzip_stream_t s) {

@@ -16,7 +16,9 @@ namespace splitzip {
 //
 // A wait gives up after `limit` (wait_limit) of the program's own time on the GPU,
 // or as soon as another wait of the CTA has; the caller drains and returns.  A wait
-// for what is in flight when others have given up (kLate) lasts its own time.
+// for what is in flight when others have given up (kLate) lasts its own time.  The
+// lanes of a warp wait together, on one barrier and by one clock, and so go on or
+// give up together.
 struct WaitLimit {
     uint32_t given_up, limit;
 };

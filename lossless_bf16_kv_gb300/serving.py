@@ -57,6 +57,11 @@ class EvictArgs(ctypes.Structure):
                 ("budget", _u32), ("keep_first", _u32), ("keep_last", _u32), ("cache_format", _u32)]
 
 
+class WaitTestOpts(ctypes.Structure):
+    """Test controls (include/splitzip_serving_testing.h)."""
+    _fields_ = [("wait_ms", _u32), ("cta", _u32), ("tile", _u32)]
+
+
 # The structures above as packed bytes (native layout, as the C compiler lays
 # them out): a call packs its arguments in one step, which costs a fraction of
 # filling a ctypes structure field by field.
@@ -85,6 +90,8 @@ def library() -> ctypes.CDLL:
             "splitzip_attention_status": (ctypes.c_int, [_vp, _vp]),
             "splitzip_attention_weights": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
             "splitzip_evict": (ctypes.c_int, [_vp, _vp]),
+            "splitzip_attention_test": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp, _vp]),
+            "splitzip_attention_weights_test": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
