@@ -403,6 +403,7 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
         const uint64_t to = (uint64_t)w.bh * p.a.kv_tokens + (uint32_t)w.s_lo + r;
         const float before = mine && p.in ? p.in[to] : 0.0f;
         float sum = 0.0f;
+        bool gave_up = false;
         uint32_t i = (n ^ (g >> 1)) & 1;  // the first of this group's tiles
         n += i;
         for (; i < steps; i += 2, n += 2) {
@@ -411,8 +412,8 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
             const bool m_there = mbar_try_wait(&sh.meta_full[mx], m_at), s_there = mbar_try_wait(&sh.s_full[x], s_at);  // mostly both
             const bool there = (m_there & s_there) || (mbar_wait_bounded(&sh.meta_full[mx], m_at, wait) && mbar_wait_bounded(&sh.s_full[x], s_at, wait));
             if (!__all_sync(0xFFFFFFFFu, there)) {
-                sum = __int_as_float(0x7FC00000);  // a wait that gave up: NaN
-                continue;
+                gave_up = true;
+                break;
             }
             tcgen_fence_after();
             const uint32_t sa = tmem + x * kRowTile + c0;
@@ -471,7 +472,9 @@ __device__ __forceinline__ void sum_items(const WeightsParams& p, WeightsShared&
         sh.part[parity][g][r] = sum;
         __syncwarp();
         if ((r & 31) == 0) mbar_arrive(&sh.item_free[rec]);
-        if (named_any(1, kSum, false)) {
+        // After a wait that gave up the barriers' phases say nothing any more: this item and
+        // those after it are NaN.
+        if (named_any(1, kSum, gave_up)) {
             give_up(p, at, g, r);
             return;
         }

@@ -9,9 +9,8 @@ import torch
 
 from lossless_bf16_kv_gb300 import serving
 from lossless_bf16_kv_gb300 import splitzip as sz
-from tests import serving_ref as ref
 from tests.gpu_helpers import ensure_library
-from tests.test_gpu_serving import attend, close, lens_of, make
+from tests.test_gpu_serving import attend, make
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -83,3 +82,53 @@ def test_attention_without_waits_is_refused(lib):
     a = arguments(q, kv, torch.empty_like(q), torch.empty((1, 8, 1), device=DEV))
     assert lib.splitzip_attention_test(ctypes.byref(a), ws.data_ptr(), ws.numel(), None, opts(0, 0)) == sz.ERR_INVALID_ARG
     assert lib.splitzip_attention_test(ctypes.byref(a), ws.data_ptr(), ws.numel(), None, None) == sz.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tq,cta,tile", [(600, 0, 0), (600, 3, 1), (600, 7, 9), (600, 50, 14), (600, 50, 22), (600, 151, 30),
+                                         (600, 20, 37), (30, 0, 0), (30, 9, 1), (30, 40, 3), (30, 41, 4), (100, 40, 3), (100, 77, 5)])
+def test_weights_give_up(lib, tq, cta, tile, dim, fmt):
+    """NaN for the item of 128 slots that the tile belongs to and for those after it that
+    the CTA had left; the others are right, to the bit."""
+    b, tk, hq, hk = 8, 2500, 16, 8
+    q, kv = make(b, tq, tk, hq, hk, dim, fmt=fmt, seed=tile)
+    _, lse = attend(q, kv, None)
+    before = torch.rand((b, hk, tk), device=DEV)
+    good, got = torch.empty_like(before), torch.zeros_like(before)
+    a = arguments(q, kv, None, lse)
+    call = lambda o, w: lib.splitzip_attention_weights_test(ctypes.byref(a), before.data_ptr(), w.data_ptr(), None, o)  # noqa: E731
+    torch.cuda.synchronize()
+    assert call(opts(NONE, NONE), good) == sz.OK
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles, heads = -(-tk // 128), b * hk
+    assert tiles * heads > 3 * ctas
+    mine = [at for i in range(-(-tiles * heads // ctas)) if (at := i * ctas + (ctas - 1 - cta if i % 2 else cta)) < tiles * heads]
+    for _ in range(3):
+        got.zero_()
+        torch.cuda.synchronize()
+        assert call(opts(cta, tile), got) == sz.OK
+        torch.cuda.synchronize()
+        lost = torch.isnan(got)
+        state = []
+        for at in mine:
+            sc, bh = divmod(at, heads)
+            part = lost[bh // hk, bh % hk, sc * 128:(sc + 1) * 128]
+            assert bool(part.all()) or not bool(part.any())
+            state.append(bool(part.any()))
+        assert any(state) and state == sorted(state), state            # from one item on
+        assert int(lost.sum()) == sum(min(128, tk - at // heads * 128) for at, s in zip(mine, state) if s)
+        assert torch.equal(got[~lost], good[~lost])
+    # How many tiles come before the lost item: none of them was the one left out.
+    seen = 0
+    for at, s in zip(mine, state):
+        s_lo, first = at // heads * 128, tk - tq
+        t_lo = max(0, s_lo - first)
+        i0 = t_lo // 64
+        count = 1 + (-(-tq // 64) - i0) if t_lo < tq else 0
+        if s:
+            assert seen <= tile < seen + count
+            break
+        seen += count
+    assert call(opts(NONE, NONE), got) == sz.OK
+    assert torch.equal(got, good)
