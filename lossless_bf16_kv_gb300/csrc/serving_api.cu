@@ -41,15 +41,24 @@ bool sizes_ok(const splitzip_attention_args& a) {
 }
 
 // Tiles of 128 query rows on the tensor cores from 17 rows of a key/value head on
-// (the other kernel's smaller tile), from 65 on for an E5M2 cache, which that kernel
-// widens at less cost; only for scales that kernel takes.  In us, this kernel and the
-// other, head_dim 128: 128 units of 16384 slots, BF16 16 rows 158 and 157, 32 rows 159
-// and 175, 64 rows 161 and 321; E5M2 32 rows 262 and 148, 64 rows 265 and 276, 128
-// rows 269 and 545.  16 units of 2048: BF16 16 rows 12.9 and 11.4, 32 rows 13.3 and
-// 16.5; E5M2 64 rows 18.8 and 16.0, 128 rows 22.3 and 20.5.  512 units of 1024: BF16
-// 32 rows 76.5 and 75.5, 64 rows 81 and 142.
+// (the other kernel's smaller tile), and only for scales that kernel takes.  E5M2
+// caches, which the other kernel widens at less cost, from 65 rows on, and from 33 on
+// at head_dim 128 with enough units (sequences times key/value heads) to fill the GPU:
+// there the other kernel walks each cache twice.  In us, this kernel and the other:
+//   BF16, head_dim 128, 128 units of 16384 slots: 16 rows 159 and 157, 24 161 and 172,
+//     64 163 and 320; 16 units of 2048: 16 rows 11.7 and 11.2, 24 13.0 and 15.5; 512
+//     units of 1024: 24 rows 76 and 70, 40 79 and 123.
+//   E5M2, head_dim 128, 40 rows: 128 units of 16384 265 and 278, 512 of 1024 103 and
+//     110, 24 of 8192 33 and 40; 16 of 8192 30 and 29, 16 of 2048 17.4 and 15.5.
+//   E5M2, head_dim 64, 64 rows: 128 units of 16384 194 and 170, 32 of 16384 45 and 53,
+//     16 of 2048 13.4 and 12.7; 128 rows: 196 and 331, 48 and 92, 15.3 and 15.3.
+// Neither side holds for one or two units and a long cache, of which a cluster of
+// eight is all that this kernel makes: 2 units of 60000 slots, head_dim 128, 64 rows,
+// BF16 56 and 43.
 bool on_tiles(const splitzip_attention_args& a, const AttentionPlan& rows) {
-    return rows.rows > (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 64u : 16u) && attention_tiles_usable(a);
+    uint32_t most = 16;  // rows of the other kernel
+    if (a.cache_format == SPLITZIP_FORMAT_E5M2) most = a.head_dim == 128 && (uint64_t)a.batch * a.kv_heads > 16 ? 32 : 64;
+    return rows.rows > most && attention_tiles_usable(a);
 }
 bool plans(const splitzip_attention_args& a, AttentionPlan& rows, AttentionPlan& tiles) {
     return attention_rows_plan(a, rows) && attention_tiles_plan(a, tiles);

@@ -6,6 +6,7 @@ import re
 import subprocess
 
 import pytest
+import torch
 
 from lossless_bf16_kv_gb300 import _build, serving
 from lossless_bf16_kv_gb300 import splitzip as sz
@@ -50,3 +51,19 @@ def test_refusals(lib):
         assert lib.splitzip_attention_test(ctypes.byref(args), FAKE, 1 << 40, None, o) == inv
     for args, o in ((a, None), (a, ctypes.byref(long)), (bad, ctypes.byref(fine))):
         assert lib.splitzip_attention_weights_test(ctypes.byref(args), None, FAKE, None, o) == inv
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call would run; here it ends at the missing GPU")
+@pytest.mark.parametrize("fmt,dim,units,rows,tiles", [
+    (0, 128, 128, 16, False), (0, 128, 128, 24, True), (0, 64, 16, 24, True),
+    (1, 128, 128, 32, False), (1, 128, 128, 40, True), (1, 128, 24, 64, True), (1, 128, 512, 40, True),      # 265 us against 278
+    (1, 128, 16, 64, False), (1, 64, 128, 64, False), (1, 64, 16, 64, False), (1, 64, 128, 128, True), (1, 128, 16, 72, True)])
+def test_kernel_by_rows_and_units(lib, fmt, dim, units, rows, tiles):
+    """Which of the two attention kernels takes a call, on both sides of the rule's
+    limits: the test entry refuses the one without waits."""
+    view = (FAKE, 1 << 24, 1 << 10, 128)
+    a = serving.AttentionArgs(view, view, view, view, FAKE, None, units, 1, 2048, rows, 1, dim, 0, 0, fmt, 1.0)
+    if rows > 64:
+        a.q_tokens, a.q_heads = rows // 8, 8
+    got = lib.splitzip_attention_test(ctypes.byref(a), FAKE, 1 << 40, None, ctypes.byref(serving.WaitTestOpts(10, 0, 0)))
+    assert got == (sz.ERR_CUDA if tiles else sz.ERR_INVALID_ARG)
