@@ -138,9 +138,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 // keys and values enter FP16 matrix products exactly, by a byte permute.
 // Queries are BF16: each row is scaled by a power of two that brings its
 // largest magnitude into [1, 2), which FP16 then holds with all 8 significant
-// bits down to 2^-17 of the largest (smaller ones are rounded to 2^-24 times
-// the row's scale, below the rounding of a 32-bit sum over the row).  The
-// power goes back into the score's scale.
+// bits down to 2^-17 of the largest; smaller ones are off by up to 2^-25 of it.  A
+// score is then off by up to 2^-25 max|q| sum|k|.  Where the keys' channels are
+// alike that is below the rounding of a 32-bit sum over the row; it is not where
+// the row's small queries meet keys far larger than the others (E5M2 keys may:
+// a query of 2^-20 of the largest enters with 5 bits).  The power goes back into
+// the score's scale.
 
 // Position in a 16-value run of the matrix product's contraction index of the
 // run's value d, such that a lane's four consecutive bytes (4 q .. 4 q + 3)

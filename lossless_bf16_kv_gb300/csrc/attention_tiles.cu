@@ -21,9 +21,9 @@
 // as soon as the softmax warps have this step's in registers, and their chain of
 // about 2500 cycles a step does not wait for it.
 //
-// 8192 causal tokens, 32 heads over 8: head_dim 128 371 us (1.48 PFLOP/s visible)
-// in BF16, 500 in E5M2; head_dim 64 273 (1.0) and 338.  16384 tokens in a window
-// of 4096 with sinks, head_dim 128: 731-735 us (1.31).
+// 8192 causal tokens, 32 heads over 8: head_dim 128 368 us (1.49 PFLOP/s visible)
+// in BF16, 500 in E5M2; head_dim 64 271 (1.0) and 329.  16384 tokens in a window
+// of 4096 with sinks, head_dim 128: 733-740 us (1.31), 940 in E5M2.
 //
 // Where one tile holds all rows, both tiles of a CTA are that one (twins): each
 // takes every other tile of slots, and they are joined like splits.  64 rows over
@@ -40,8 +40,10 @@
 // it.  The queries are then FP16 too, each row scaled by a power of two.
 //
 // What the roles share sits in shared memory and is read from there: a softmax
-// thread's 104 registers hold 64 scores and little else, and a value spilled
-// there costs hundreds of cycles in every step.
+// thread's 104 registers (96 for E5M2) hold 64 scores and little else, and a value
+// spilled in its loop costs hundreds of cycles in every step.  The compiler still
+// spills 20 to 24 bytes a thread in the E5M2 kernels of head_dim 128, and 8 in the
+// BF16 one of shared rows at 64.
 //
 // The running maximum is only raised when a row's maximum grows by more than
 // 2^8 (in which case O and l are rescaled by the softmax warps, after the

@@ -14,8 +14,11 @@
 // heads of one kind (queries, keys or values) of one token, so addresses,
 // weights and the token's table row are found once for them.  Runs of eight
 // (16-byte loads) leave half as many instructions, which limited runs of four:
-// 16384 tokens of 48 heads of 128 take 75 us (5.5 TB/s, 81% of a copy's rate)
-// against 88; runs of four remain for a rot_dim that is not a multiple of sixteen.
+// 16384 tokens of 48 heads of 128 take 74-75 us (5.5 TB/s, 81% of a copy's rate)
+// against 88, and 76 into an E5M2 cache; runs of four remain for a rot_dim that is
+// not a multiple of sixteen.  With two and four rows into BF16 caches the compiler
+// spills 20 and 44 bytes a thread; one CTA less to an SM spills nothing and is slower
+// (the 16384 tokens 75 us where this takes 69, with their cache in one piece).
 #include <cstdint>
 
 #include <cuda_bf16.h>
