@@ -35,6 +35,9 @@ struct Mask {
         window = a.window ? min(a.window, 0x80000000u) : 0x80000000u;
         sinks = (int32_t)min(a.sinks, 0x7FFFFFFFu);
     }
+    // n slots, the last `count` of which are the queries.
+    __device__ __forceinline__ Mask(int32_t n, int32_t count, uint32_t window, uint32_t sinks)
+        : n(n), first(n - count), window(window ? min(window, 0x80000000u) : 0x80000000u), sinks((int32_t)min(sinks, 0x7FFFFFFFu)) {}
     // Position of query token t; every negative one as -1.
     __device__ __forceinline__ int32_t pos(uint32_t t) const { return max(-1, first + (int32_t)t); }
     // p - s is taken modulo 2^32: for s > p it is at least 2^31.
@@ -155,6 +158,20 @@ __device__ __forceinline__ uint32_t e5m2_01(uint32_t r) { return prmt(r, 0u, 0x1
 __device__ __forceinline__ uint32_t e5m2_23(uint32_t r) { return prmt(r, 0u, 0x3424u); }
 __device__ __forceinline__ uint32_t e5m2_02(uint32_t r) { return prmt(r, 0u, 0x2404u); }
 __device__ __forceinline__ uint32_t e5m2_13(uint32_t r) { return prmt(r, 0u, 0x3414u); }
+
+// Four E5M2 bytes, to nearest even.  The conversion instruction saturates; a
+// value of at least 61440, half way from the largest finite value (57344) to
+// the next step (65536), rounds to infinity instead.  NaN stays NaN.
+__device__ __forceinline__ uint32_t pack4_e5m2(const float* f) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    uint32_t w = (uint32_t)lo | ((uint32_t)hi << 16);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        if (fabsf(f[i]) >= 61440.0f) w = (w & ~(0x7Fu << (8 * i))) | (0x7Cu << (8 * i));
+    return w;
+}
 
 // 2^-e for the largest magnitude's bits of a row of BF16 values (e its
 // exponent; 2^-127 for a row with infinities or NaN); 1 for a row of zeros and

@@ -24,21 +24,10 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "attention.cuh"
+#include "attention_rows.cuh"
 
 namespace splitzip {
 namespace {
-
-constexpr int kWarpsRows = 4;
-constexpr int kStagesRows = 2;
-constexpr uint32_t kCtasPerSm = 3;  // of 16-row tiles, by registers and shared memory
-constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
-// log2 of p at a row's maximum: m is that much less than the maximum.  FP16 holds p in
-// full from 2^-14 to 2^16, so with 2^15 on top terms down to 2^-29 of a row's largest
-// keep all bits and those below 2^-40 vanish.  With 1 on top those below 2^-25 do,
-// and 2^17 slots of them are 2^-8 of the sum.
-template <bool kF8>
-constexpr float kLift = kF8 ? 15.0f : 0.0f;
 
 struct RowsParams {
     splitzip_attention_args a;
@@ -58,19 +47,6 @@ struct RowsShape {
     static constexpr int kSmem = kRing + kQ;
 };
 
-// Byte offset of 16-byte chunk c of row r in a tile of rows of kRow bytes; the
-// chunks of eight consecutive rows at one c fall into eight different banks
-// groups, as ldmatrix reads them.
-template <int kRow>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
-    if (kRow >= 128) return r * kRow + ((c ^ (r & 7u)) << 4);
-    return r * kRow + ((c ^ ((r >> 1) & 3u)) << 4);  // two rows to 128 bytes
-}
-
-__device__ __forceinline__ void add_scaled(float4& v, float f, float4 x) {
-    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-}
-
 template <int D, bool kF8, int MT>
 __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) rows_kernel(const __grid_constant__ RowsParams p) {
     using S = RowsShape<D, kF8, MT>;
@@ -81,8 +57,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
     constexpr int kChunks = S::kRow / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_scale[S::kTileRows];
-    __shared__ float s_m[kWarpsRows][S::kTileRows], s_l[kWarpsRows][S::kTileRows], s_mm[S::kTileRows], s_ll[S::kTileRows];
-    __shared__ uint32_t s_last;
+    __shared__ RowsShared<S::kTileRows> sh;
     const splitzip_attention_args& a = p.a;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t unit = blockIdx.x / p.splits;
@@ -366,8 +341,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
             l[i][x] += __shfl_xor_sync(0xFFFFFFFFu, l[i][x], 1);
             l[i][x] += __shfl_xor_sync(0xFFFFFFFFu, l[i][x], 2);
             if ((lane & 3) == 0) {
-                s_m[warp][16 * i + 8 * x + lane / 4] = m[i][x];
-                s_l[warp][16 * i + 8 * x + lane / 4] = l[i][x];
+                sh.m[warp][16 * i + 8 * x + lane / 4] = m[i][x];
+                sh.l[warp][16 * i + 8 * x + lane / 4] = l[i][x];
             }
         }
     __syncthreads();  // every warp is done with its ring
@@ -382,31 +357,6 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
     __syncthreads();
 
     const uint32_t nrows = r1 - r0;
-    for (uint32_t at = tid; at < nrows * (D / 4); at += 32 * kWarpsRows) {
-        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
-        float mm = s_m[0][r];
-#pragma unroll
-        for (int w = 1; w < kWarpsRows; w++) mm = fmaxf(mm, s_m[w][r]);
-        const float use = mm == -INFINITY ? 0.0f : mm;
-        float ll = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kWarpsRows; w++) {
-            const float f = exp2_approx(s_m[w][r] - use);
-            ll = fmaf(f, s_l[w][r], ll);
-            add_scaled(v, f, *reinterpret_cast<const float4*>(os + (w * S::kTileRows + r) * D + c));
-        }
-        *reinterpret_cast<float4*>(os + r * D + c) = v;  // over the first warp's, which only this thread reads
-        if (c == 0) {
-            s_mm[r] = mm;
-            s_ll[r] = ll;
-        }
-    }
-
-    // Join the cluster: each of its CTAs a share of the outputs.
-    const uint32_t cluster = p.cluster, rank = split % cluster, groups = p.splits / cluster;
-    if (cluster > 1) cluster_sync();
-    else __syncthreads();
     auto store = [&](uint32_t r, uint32_t c, float4 v, float mm, float ll) {
         const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
         const uint32_t hq = h * p.group + g;
@@ -419,73 +369,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
         if (c == 0 && a.lse)
             a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
-    constexpr uint32_t kPart = S::kTileRows * (D + 4);  // floats of a partial result: rows of o, m, l
-    const uint32_t group = split / cluster;
-    float* all = p.partials + (uint64_t)unit * groups * kPart;
-    for (uint32_t at = rank * 32 * kWarpsRows + tid; at < nrows * (D / 4); at += cluster * 32 * kWarpsRows) {
-        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
-        float m8[8], l8[8];
-        float4 v8[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            m8[i] = -INFINITY;
-            l8[i] = 0.0f;
-            v8[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < (int)cluster) {
-                m8[i] = cluster_ld(smem_addr(&s_mm[r]), i);
-                l8[i] = cluster_ld(smem_addr(&s_ll[r]), i);
-                v8[i] = cluster_ld4(smem_addr(os + r * D + c), i);
-            }
-        }
-        float mm = m8[0];
-#pragma unroll
-        for (int i = 1; i < 8; i++) mm = fmaxf(mm, m8[i]);
-        const float use = mm == -INFINITY ? 0.0f : mm;
-        float ll = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float f = exp2_approx(m8[i] - use);
-            ll = fmaf(f, l8[i], ll);
-            add_scaled(v, f, v8[i]);
-        }
-        if (groups == 1) {
-            store(r, c, v, mm, ll);
-        } else {
-            float* q = all + group * kPart + r * (D + 4);
-            __stcg(reinterpret_cast<float4*>(q + c), v);
-            if (c == 0) __stcg(reinterpret_cast<float2*>(q + D), make_float2(mm, ll));
-        }
-    }
-    if (cluster > 1) cluster_sync();  // this CTA's shared memory has been read
-    if (groups == 1) return;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        s_last = atomicAdd(p.counters + unit, 1u) == p.splits - 1;
-        if (s_last) p.counters[unit] = 0;  // ready for the next call
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    for (uint32_t at = tid; at < nrows * (D / 4); at += 32 * kWarpsRows) {
-        const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
-        const float* q = all + r * (D + 4);
-        float mm = -INFINITY, ll = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (uint32_t i = 0; i < groups; i++) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + i * kPart + D));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(q + i * kPart + c));
-            const float top = fmaxf(mm, ml.x), use = top == -INFINITY ? 0.0f : top;
-            const float f = exp2_approx(mm - use), g = exp2_approx(ml.x - use);
-            ll = fmaf(f, ll, g * ml.y);
-            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            add_scaled(v, g, x);
-            mm = top;
-        }
-        store(r, c, v, mm, ll);
-    }
+    join_rows<D, S::kTileRows>(os, sh, unit, split, p.splits, p.cluster, nrows, p.counters, p.partials, store);
 }
 
 template <int D, bool kF8, int MT>
@@ -515,16 +399,7 @@ cudaError_t launch_tile(const RowsParams& p, uint32_t tile_rows, uint32_t ctas, 
 
 }  // namespace
 
-bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
-    const uint32_t group = a.q_heads / a.kv_heads;
-    p.rows = a.q_tokens * group;
-    p.tile_rows = p.rows <= 16 ? 16 : 32;
-    p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
-    const uint64_t units = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
-    const uint32_t slots = kTileBytes / (a.head_dim * (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 1 : 2));
-    // The slots a row tile can see at most.
-    uint64_t most = a.kv_tokens;
-    if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
+uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, uint32_t tile_rows, uint32_t head_dim) {
     // As many splits as run at once, of which each warp has a tile of slots (512 slots of
     // 8 units: 5.8 us with 8 splits, 6.6 with 4).  Three 16-row CTAs fit an SM, but a
     // cluster lies within one of the GPU's groups of SMs, and fewer of the large ones run
@@ -535,18 +410,35 @@ bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
     static constexpr uint64_t kAtOnce[9] = {0, 3 * kSms, 228, 148, 110, 87, 74, 59, 51};
     const uint64_t tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
     uint64_t splits = 8;
-    while (splits > 1 && (splits > tiles || units > (p.tile_rows == 16 ? kAtOnce[splits] : 256 / splits))) splits--;
+    while (splits > 1 && (splits > tiles || units > (tile_rows == 16 ? kAtOnce[splits] : 256 / splits))) splits--;
     // Up to eight splits are one cluster.  More are clusters of eight, of which the last
     // one joins all: that costs as much as a few tiles, more with more to join.  8 units,
     // 16-row tiles: 4096 slots of 64 take 7.5 us with 8 splits and 8.6 with 32, 8192 of
     // 128 16.6 and 12.2 (13.0 with 40); 32-row tiles: 4096 of 128 18.2 and 22.3, 12000
     // 33.9 and 27.7; 131072 slots of 128 take 88 us with 32 splits, 115 with 56.
-    const uint64_t more = std::min(256 / units, tiles) / 8 * 8, join = p.tile_rows * a.head_dim > 2048 ? 10 : 4;
+    const uint64_t more = std::min(256 / units, tiles) / 8 * 8, join = tile_rows * head_dim > 2048 ? 10 : 4;
     if (more > 8 && tiles / more + join < tiles / 8) splits = more;
-    p.splits = (uint32_t)splits;
-    if (units * p.splits > 0x7FFFFFFFull) return false;
+    return (uint32_t)splits;
+}
+
+size_t attention_rows_bytes(uint64_t units, uint32_t splits, uint32_t tile_rows, uint32_t head_dim) {
     static_assert(4 * kSms <= kAttentionStatus, "splits in several clusters are counted by row tile");
-    p.bytes = kAttentionHeader + (p.splits > 8 ? units * (p.splits / 8) * p.tile_rows * (a.head_dim + 4) * 4 : 0);
+    return kAttentionHeader + (splits > 8 ? units * (splits / 8) * tile_rows * (head_dim + 4) * 4 : 0);
+}
+
+bool attention_rows_plan(const splitzip_attention_args& a, AttentionPlan& p) {
+    const uint32_t group = a.q_heads / a.kv_heads;
+    p.rows = a.q_tokens * group;
+    p.tile_rows = p.rows <= 16 ? 16 : 32;
+    p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+    const uint64_t units = (uint64_t)a.batch * a.kv_heads * p.row_tiles;
+    const uint32_t slots = kTileBytes / (a.head_dim * (a.cache_format == SPLITZIP_FORMAT_E5M2 ? 1 : 2));
+    // The slots a row tile can see at most.
+    uint64_t most = a.kv_tokens;
+    if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (p.tile_rows + group - 1) / group + 2 * slots);
+    p.splits = attention_rows_splits(units, most, slots, p.tile_rows, a.head_dim);
+    if (units * p.splits > 0x7FFFFFFFull) return false;
+    p.bytes = attention_rows_bytes(units, p.splits, p.tile_rows, a.head_dim);
     return true;
 }
 

@@ -71,19 +71,6 @@ __device__ __forceinline__ Run<kRun> pack_bf16(const float (&f)[kRun]) {
     }
     return r;
 }
-// Four E5M2 bytes, to nearest even.  The conversion instruction saturates; a
-// value of at least 61440, half way from the largest finite value (57344) to
-// the next step (65536), rounds to infinity instead.  NaN stays NaN.
-__device__ __forceinline__ uint32_t pack4_e5m2(const float* f) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
-    uint32_t w = (uint32_t)lo | ((uint32_t)hi << 16);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (fabsf(f[i]) >= 61440.0f) w = (w & ~(0x7Fu << (8 * i))) | (0x7Cu << (8 * i));
-    return w;
-}
 template <int kRun>
 __device__ __forceinline__ void store_e5m2(uint8_t* p, const float (&f)[kRun]) {
     if constexpr (kRun == 8) st_stream8(p, make_uint2(pack4_e5m2(f), pack4_e5m2(f + 4)));

@@ -1,0 +1,276 @@
+// pages.cu -- rows into and out of the pages of a cache (sm_103a): the store that
+// quantises new keys and values, and the load that widens them back.
+//
+// A block of head_dim / 4 values x becomes codes c = rne(x 2^-k) with k the smallest
+// power for which the largest |x| 2^-k does not round past the largest code.  That
+// largest |x| is an 8-bit significand 1.f times 2^E, so k = E - 6 for INT8, or E - 5
+// where 1.f is 255/128 (127.5 rounds to 128); and k = E - 2 for E2M1, or E - 1 from
+// 1.75 on (7 rounds past 6).  x 2^-k is exact in 32 bits: one rounding in all, and
+// no division.
+//
+// Both move each byte once, so HBM bounds them.  A row is shared by head_dim / 8
+// lanes of eight values (16 bytes of BF16); a group of lanes takes kRows tokens of one
+// head, and the groups of a CTA neighbouring tokens, whose rows are neighbours in
+// a page that lies head by head (E2M1 rows of head_dim 64 are 32 bytes).
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "pages.cuh"
+
+namespace splitzip {
+namespace {
+
+constexpr int kThreadsPages = 256, kRows = 4;
+// Tokens of a CTA.
+template <int D>
+constexpr uint32_t kTokens = kThreadsPages / (D / 8) * kRows;
+
+// What both kernels' CTAs take: one of keys and values, a sequence (0 for the
+// store), a head, and kTokens tokens from `first` on.
+struct Part {
+    uint32_t b, h, first;
+    bool v;
+};
+template <int D>
+__device__ __forceinline__ Part part_of(uint32_t block, uint32_t heads, uint32_t token_ctas) {
+    const uint32_t x = block / token_ctas, y = x / heads;
+    return {y >> 1, x - y * heads, (block - x * token_ctas) * kTokens<D>, (y & 1) != 0};
+}
+
+// The largest magnitude's BF16 bits over the lanes of a block (`lanes` neighbours).
+template <int kLanes>
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+#pragma unroll
+    for (int i = 1; i < kLanes; i *= 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
+    return m;
+}
+
+// The block's power from its largest magnitude's BF16 bits, and its exponent byte.
+template <int kFmt>
+__device__ __forceinline__ int block_power(uint32_t top, uint32_t& e) {
+    constexpr int kAway = kFmt == kInt8 ? 6 : 2, kLow = kFmt == kInt8 ? -24 : -23, kHigh = kFmt == kInt8 ? 9 : 13;
+    constexpr uint32_t kNext = kFmt == kInt8 ? 127 : 96;  // fraction bits from where the next power is taken
+    const int k = min(max((int)(top >> 7) - 127 - kAway + ((top & 127u) >= kNext ? 1 : 0), kLow), kHigh);
+    e = top >= 0x7F80u ? 255u : top == 0u ? 0u : (uint32_t)(k + 127);
+    return k;
+}
+__device__ __forceinline__ uint32_t to_int8x4(const float* z) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = (uint32_t)__float2int_rn(fminf(fmaxf(z[i], -127.0f), 127.0f));
+    return prmt(prmt(r[0], r[1], 0x0040), prmt(r[2], r[3], 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* z) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]), "f"(z[4]), "f"(z[5]), "f"(z[6]), "f"(z[7]));
+    return r;
+}
+
+struct StoreParams {
+    splitzip_pages_store_args a;
+    uint32_t token_ctas, page_shift;
+};
+
+template <int D, int kFmt>
+__global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_constant__ StoreParams p) {
+    constexpr uint32_t kLanes = D / 8, kGroups = kThreadsPages / kLanes;
+    const splitzip_pages_store_args& a = p.a;
+    const Part part = part_of<D>(blockIdx.x, a.pool.kv_heads, p.token_ctas);
+    const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const splitzip_view& in = part.v ? a.v : a.k;
+    const splitzip_page_rows& out = part.v ? a.pool.v : a.pool.k;
+    const uint64_t slots = (uint64_t)a.pool.pages << p.page_shift;
+    const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * (part.h * in.stride_h) + 16 * lane;
+    uint4 x[kRows];
+    int64_t slot[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const uint32_t t = part.first + r * kGroups + group;
+        x[r] = make_uint4(0, 0, 0, 0);
+        slot[r] = -1;
+        if (t < a.n) {
+            x[r] = ld_stream16(src + 2 * ((int64_t)t * in.stride_t));
+            slot[r] = a.slots[t];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const bool there = slot[r] >= 0 && (uint64_t)slot[r] < slots;
+        const int64_t page = slot[r] >> p.page_shift, at = slot[r] & (a.pool.page_tokens - 1);
+        const int64_t row = page * out.stride_p + at * out.stride_t + part.h * out.stride_h;
+        uint8_t* to = static_cast<uint8_t*>(out.data);
+        const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        if constexpr (kFmt == kBf16) {
+            if (there) *reinterpret_cast<uint4*>(to + 2 * row + 16 * lane) = x[r];
+        } else {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+            if constexpr (kFmt == kE5m2) {
+                if (there) *reinterpret_cast<uint2*>(to + row + 8 * lane) = make_uint2(pack4_e5m2(f), pack4_e5m2(f + 4));
+            } else {
+                uint32_t top = 0, e;
+#pragma unroll
+                for (int i = 0; i < 4; i++) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+                top = block_max<kLanes / 4>(top);
+                const int k = block_power<kFmt>(top, e);
+                // A block that holds an infinity or a NaN gets codes 0.
+                const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] = e == 255u ? 0.0f : f[i] * inv;
+                // The four exponent bytes, gathered over the row's lanes.
+                e <<= 8 * (lane / (kLanes / 4));
+#pragma unroll
+                for (uint32_t i = kLanes / 4; i < kLanes; i *= 2) e |= __shfl_xor_sync(0xFFFFFFFFu, e, i);
+                if (there) {
+                    if constexpr (kFmt == kInt8) *reinterpret_cast<uint2*>(to + row + 8 * lane) = make_uint2(to_int8x4(f), to_int8x4(f + 4));
+                    else *reinterpret_cast<uint32_t*>(to + row + 4 * lane) = to_e2m1x8(f);
+                    if (lane == 0)
+                        *reinterpret_cast<uint32_t*>(out.exponents + page * out.exp_stride_p + at * out.exp_stride_t +
+                                                     part.h * out.exp_stride_h) = e;
+                }
+            }
+        }
+    }
+}
+
+struct LoadParams {
+    splitzip_pages_load_args a;
+    uint32_t token_ctas, page_shift;
+};
+
+// kCopy: E5M2 rows as they are.
+template <int D, int kFmt, bool kCopy>
+__global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_constant__ LoadParams p) {
+    constexpr uint32_t kLanes = D / 8, kGroups = kThreadsPages / kLanes;
+    const splitzip_pages_load_args& a = p.a;
+    const Part part = part_of<D>(blockIdx.x, a.pool.kv_heads, p.token_ctas);
+    const int32_t len = a.lens ? a.lens[part.b] : (int32_t)a.tokens;
+    const uint32_t n = len < 0 ? 0u : min((uint32_t)len, a.tokens);
+    if (part.first >= n) return;
+    const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const splitzip_page_rows& in = part.v ? a.pool.v : a.pool.k;
+    const splitzip_view& out = part.v ? a.v_out : a.k_out;
+    const int32_t* table = a.table + (uint64_t)part.b * a.table_width;
+    const uint8_t* src = static_cast<const uint8_t*>(in.data) + kRowBytes<D, kFmt> / kLanes * lane;
+    uint32_t page[kRows], e[kRows];
+    uint4 x[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const uint32_t t = part.first + r * kGroups + group;
+        page[r] = t < n ? (uint32_t)table[t >> p.page_shift] : 0xFFFFFFFFu;
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const uint32_t at = (part.first + r * kGroups + group) & (a.pool.page_tokens - 1);
+        x[r] = make_uint4(0, 0, 0, 0);
+        e[r] = 0;
+        if (page[r] < a.pool.pages) {
+            const int64_t row = page[r] * in.stride_p + at * in.stride_t + part.h * in.stride_h;
+            if constexpr (kFmt == kBf16) {
+                x[r] = ld_stream16(src + 2 * row);
+            } else if constexpr (kFmt == kE2m1) {
+                x[r].x = ld_stream4(src + row);
+            } else {
+                const uint2 y = ld_stream8(src + row);
+                x[r].x = y.x, x[r].y = y.y;
+            }
+            if constexpr (kQuantised<kFmt>)
+                e[r] = in.exponents[page[r] * in.exp_stride_p + at * in.exp_stride_t + part.h * in.exp_stride_h + lane / (kLanes / 4)];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        const uint32_t t = part.first + r * kGroups + group;
+        if (t >= n) continue;
+        const bool bad = page[r] >= a.pool.pages;
+        const int64_t row = part.b * out.stride_b + (int64_t)t * out.stride_t + part.h * out.stride_h;
+        if constexpr (kCopy) {
+            st_stream8(static_cast<uint8_t*>(out.data) + row + 8 * lane, bad ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : make_uint2(x[r].x, x[r].y));
+            continue;
+        }
+        uint32_t h[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        if constexpr (kFmt == kE5m2) {
+            const uint32_t w[4] = {e5m2_01(x[r].x), e5m2_23(x[r].x), e5m2_01(x[r].y), e5m2_23(x[r].y)};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 f = unpack2<true>(w[i]);
+                h[i] = pack2<false>(f.x, f.y);
+            }
+        } else if constexpr (kQuantised<kFmt>) {
+            uint32_t w[4];
+            if constexpr (kFmt == kInt8) {
+                const uint32_t lo = int8_bias(x[r].x), hi = int8_bias(x[r].y);
+                w[0] = int8_pair<kInt8_01>(lo), w[1] = int8_pair<kInt8_23>(lo), w[2] = int8_pair<kInt8_01>(hi), w[3] = int8_pair<kInt8_23>(hi);
+            } else {
+                e2m1_pairs(w, x[r].x);
+            }
+            const float scale = block_scale(e[r]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 f = unpack2<true>(w[i]);
+                h[i] = pack2<false>(f.x * scale, f.y * scale);
+            }
+        }
+        if (bad) h[0] = h[1] = h[2] = h[3] = 0x7FC07FC0u;
+        st_stream16(static_cast<uint8_t*>(out.data) + 2 * row + 16 * lane, make_uint4(h[0], h[1], h[2], h[3]));
+    }
+}
+
+inline uint32_t log2_of(uint32_t x) {
+    uint32_t n = 0;
+    while (x >>= 1) n++;
+    return n;
+}
+
+template <int D>
+cudaError_t store(const splitzip_pages_store_args& a, cudaStream_t s) {
+    const uint32_t token_ctas = (uint32_t)(((uint64_t)a.n + kTokens<D> - 1) / kTokens<D>);
+    const StoreParams p{a, token_ctas, log2_of(a.pool.page_tokens)};
+    const uint32_t ctas = token_ctas * a.pool.kv_heads * 2;
+    switch (a.pool.format) {
+        case kBf16: store_kernel<D, kBf16><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kE5m2: store_kernel<D, kE5m2><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kInt8: store_kernel<D, kInt8><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        default: store_kernel<D, kE2m1><<<ctas, kThreadsPages, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t load(const splitzip_pages_load_args& a, cudaStream_t s) {
+    const uint32_t token_ctas = (a.tokens + kTokens<D> - 1) / kTokens<D>;
+    const LoadParams p{a, token_ctas, log2_of(a.pool.page_tokens)};
+    const uint32_t ctas = token_ctas * a.pool.kv_heads * 2 * a.batch;
+    switch (a.pool.format) {
+        case kBf16: load_kernel<D, kBf16, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kE5m2:
+            if (a.out_format == kE5m2) load_kernel<D, kE5m2, true><<<ctas, kThreadsPages, 0, s>>>(p);
+            else load_kernel<D, kE5m2, false><<<ctas, kThreadsPages, 0, s>>>(p);
+            break;
+        case kInt8: load_kernel<D, kInt8, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        default: load_kernel<D, kE2m1, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_pages_store(const splitzip_pages_store_args& a, cudaStream_t s) {
+    return a.pool.head_dim == 64 ? store<64>(a, s) : store<128>(a, s);
+}
+cudaError_t launch_pages_load(const splitzip_pages_load_args& a, cudaStream_t s) {
+    return a.pool.head_dim == 64 ? load<64>(a, s) : load<128>(a, s);
+}
+
+}  // namespace splitzip

@@ -1,0 +1,63 @@
+// pages.cuh -- rows of a paged cache (sm_103a): their formats, where they lie, and
+// the widening of quantised codes to FP16.
+#pragma once
+
+#include <cstdint>
+
+#include "attention.cuh"
+#include "pages.h"
+
+namespace splitzip {
+
+enum Format : int { kBf16 = SPLITZIP_FORMAT_BF16, kE5m2 = SPLITZIP_FORMAT_E5M2, kInt8 = SPLITZIP_FORMAT_INT8, kE2m1 = SPLITZIP_FORMAT_E2M1 };
+
+template <int kFmt>
+constexpr bool kQuantised = kFmt == kInt8 || kFmt == kE2m1;
+// Bytes of a row's codes.
+template <int D, int kFmt>
+constexpr int kRowBytes = kFmt == kBf16 ? 2 * D : kFmt == kE2m1 ? D / 2 : D;
+
+// One sequence of a batch: its new tokens' first row, their number (0: left out),
+// its length.
+struct Sequence {
+    int32_t row, count, n;
+    __device__ __forceinline__ Sequence(const splitzip_paged_attention_args& a, uint32_t b) {
+        const int32_t from = a.q_start[b], to = a.q_start[b + 1], len = a.lens[b];
+        const bool ok = from >= 0 && to >= from && (uint32_t)to <= a.tokens && (uint32_t)(to - from) <= a.max_q_tokens;
+        row = from;
+        count = ok ? to - from : 0;
+        n = len < 0 ? 0 : min(len, (int32_t)a.kv_tokens);
+    }
+};
+
+// 2^(e - 127) for an exponent byte: 0 for 0, NaN for 255.
+__device__ __forceinline__ float block_scale(uint32_t e) {
+    const uint32_t bits = e << 23;
+    return __uint_as_float(e == 255u ? bits | 0x400000u : bits);
+}
+
+// FP16 pairs of codes, exact.  INT8: two bytes of r, as 1024 + (b + 128) less 1152
+// (1024 to 2047 have a step of 1 in FP16, so the byte is the lower half of the value).
+template <int kSelect>
+__device__ __forceinline__ uint32_t int8_pair(uint32_t biased) {
+    const uint32_t w = prmt(biased, 0x64646464u, kSelect);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t int8_bias(uint32_t r) { return r ^ 0x80808080u; }
+constexpr int kInt8_01 = 0x4140, kInt8_23 = 0x4342, kInt8_02 = 0x4240, kInt8_13 = 0x4341;
+// E2M1: the two halves of each byte of r (the lower half first).
+__device__ __forceinline__ void e2m1_pairs(uint32_t (&h)[4], uint32_t r) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(r));
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+}  // namespace splitzip

@@ -1,0 +1,88 @@
+// pages_api.cu -- the extern "C" entry points of include/splitzip_pages.h:
+// host-side argument checks and status mapping.
+#include <cmath>
+#include <cstdint>
+
+#include "api_checks.h"
+#include "pages.h"
+#include "trace.h"
+
+using namespace splitzip;
+
+namespace {
+
+bool quantised(uint32_t format) { return format == SPLITZIP_FORMAT_INT8 || format == SPLITZIP_FORMAT_E2M1; }
+
+bool pool_sizes_ok(const splitzip_pool& p) {
+    return dim_ok(p.head_dim) && p.format <= SPLITZIP_FORMAT_E2M1 && p.pages && p.pages <= kMax31 && p.kv_heads &&
+           p.page_tokens >= 16 && p.page_tokens <= 65536 && (p.page_tokens & (p.page_tokens - 1)) == 0;
+}
+// Strides of dimensions of length 1 are not looked at.
+bool rows_ok(const splitzip_page_rows& r, const splitzip_pool& p) {
+    const int64_t unit = p.format == SPLITZIP_FORMAT_BF16 ? 8 : 16, most = 1ll << 38;
+    const auto ok = [=](uint32_t n, int64_t s, int64_t of) { return n <= 1 || (s > 0 && s < most && s % of == 0); };
+    if (!r.data || !aligned(r.data, 16) || !ok(p.pages, r.stride_p, unit) || !ok(p.page_tokens, r.stride_t, unit) ||
+        !ok(p.kv_heads, r.stride_h, unit))
+        return false;
+    return !quantised(p.format) || (r.exponents && aligned(r.exponents, 4) && ok(p.pages, r.exp_stride_p, 4) &&
+                                    ok(p.page_tokens, r.exp_stride_t, 4) && ok(p.kv_heads, r.exp_stride_h, 4));
+}
+bool pool_ok(const splitzip_pool& p) { return pool_sizes_ok(p) && rows_ok(p.k, p) && rows_ok(p.v, p); }
+
+bool sizes_ok(const splitzip_paged_attention_args& a) {
+    if (!pool_sizes_ok(a.pool) || !a.batch || !a.tokens || !a.max_q_tokens || !a.kv_tokens || !a.q_heads) return false;
+    const uint32_t hk = a.pool.kv_heads;
+    if (a.q_heads % hk || a.q_heads / hk > SPLITZIP_MAX_GROUP || a.max_q_tokens > a.tokens) return false;
+    return (uint64_t)a.tokens * (a.q_heads / hk) <= kMostTokens && a.kv_tokens <= kMostTokens &&
+           a.kv_tokens <= (uint64_t)a.table_width * a.pool.page_tokens && (uint64_t)a.batch * hk <= kMax31 &&
+           (uint64_t)a.batch * hk * a.tokens <= kMax31;
+}
+
+}  // namespace
+
+extern "C" {
+
+splitzip_status splitzip_pages_store(const splitzip_pages_store_args* a, splitzip_stream_t s) {
+    TraceRange trace("splitzip_pages_store");
+    if (!a || !pool_sizes_ok(a->pool) || (uint64_t)a->n * a->pool.kv_heads > kMax31) return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->n) return SPLITZIP_OK;
+    if (!pool_ok(a->pool) || !view_ok(a->k, 2, 1, a->n, a->pool.kv_heads) || !view_ok(a->v, 2, 1, a->n, a->pool.kv_heads) ||
+        !a->slots || !aligned(a->slots, 8))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_pages_store(*a, (cudaStream_t)s));
+}
+
+splitzip_status splitzip_pages_load(const splitzip_pages_load_args* a, splitzip_stream_t s) {
+    TraceRange trace("splitzip_pages_load");
+    if (!a || !pool_ok(a->pool) || !a->batch || !a->tokens || a->tokens > kMostTokens) return SPLITZIP_ERR_INVALID_ARG;
+    const uint32_t e = a->out_format == SPLITZIP_FORMAT_E5M2 ? 1 : 2;
+    if (a->out_format != SPLITZIP_FORMAT_BF16 && (e == 2 || a->pool.format != SPLITZIP_FORMAT_E5M2)) return SPLITZIP_ERR_INVALID_ARG;
+    if (a->tokens > (uint64_t)a->table_width * a->pool.page_tokens || (uint64_t)a->batch * a->pool.kv_heads > kMax31 ||
+        2ull * a->batch * a->pool.kv_heads > kMax31 / ((a->tokens + 31) / 32))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->table || !aligned(a->table, 4) || !aligned(a->lens, 4) ||
+        !view_ok(a->k_out, e, a->batch, a->tokens, a->pool.kv_heads, true) ||
+        !view_ok(a->v_out, e, a->batch, a->tokens, a->pool.kv_heads, true))
+        return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_pages_load(*a, (cudaStream_t)s));
+}
+
+size_t splitzip_paged_attention_workspace_bytes(const splitzip_paged_attention_args* a) {
+    PagedPlan rows;
+    return a && sizes_ok(*a) && paged_rows_plan(*a, rows) ? rows.bytes : 0;
+}
+
+splitzip_status splitzip_paged_attention(const splitzip_paged_attention_args* a, void* workspace, size_t workspace_bytes,
+                                         splitzip_stream_t s) {
+    TraceRange trace("splitzip_paged_attention");
+    PagedPlan rows;
+    if (!a || !sizes_ok(*a) || !paged_rows_plan(*a, rows) || !pool_ok(a->pool)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!view_ok(a->q, 2, 1, a->tokens, a->q_heads) || !view_ok(a->out, 2, 1, a->tokens, a->q_heads, true)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->table || !a->q_start || !a->lens || !aligned(a->table, 4) || !aligned(a->q_start, 4) || !aligned(a->lens, 4) ||
+        !aligned(a->lse, 4) || !std::isfinite(a->scale) || !(a->scale > 0.0f))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < rows.bytes) return SPLITZIP_ERR_INVALID_ARG;
+    return from_cuda(launch_paged_rows(*a, rows, workspace, (cudaStream_t)s));
+}
+
+}  // extern "C"

@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/splitzip_serving_testing.h"
+#include "api_checks.h"
 #include "serving.h"
 #include "trace.h"
 
@@ -11,26 +12,8 @@ using namespace splitzip;
 
 namespace {
 
-inline splitzip_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SPLITZIP_OK : SPLITZIP_ERR_CUDA; }
-
 inline uint32_t elem_bytes(uint32_t format) { return format == SPLITZIP_FORMAT_E5M2 ? 1 : 2; }
 inline bool format_ok(uint32_t format) { return format == SPLITZIP_FORMAT_BF16 || format == SPLITZIP_FORMAT_E5M2; }
-inline bool dim_ok(uint32_t d) { return d == 64 || d == 128; }
-inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// A view of nb x nt x nh rows.  Strides of dimensions of length 1 are not
-// looked at; only an input's batch stride may be 0 (one sequence shared by the
-// batch: as an output, all of it would be written to the same rows).
-bool view_ok(const splitzip_view& v, uint32_t elem, uint32_t nb, uint32_t nt, uint32_t nh, bool output = false) {
-    const int64_t unit = 16 / elem, most = 1ll << 38;
-    const auto ok = [=](uint32_t n, int64_t s, int64_t least) { return n <= 1 || (s >= least && s < most && s % unit == 0); };
-    return v.data && aligned(v.data, 16) && ok(nb, v.stride_b, output ? 1 : 0) && ok(nt, v.stride_t, 1) && ok(nh, v.stride_h, 1);
-}
-
-constexpr uint64_t kMax31 = 0x7FFFFFFFull;
-// Slots and query rows of the attention calls: their kernels look up to two tiles
-// of 128 past the last one in signed 32-bit numbers.
-constexpr uint64_t kMostTokens = (1ull << 31) - 256;
 
 bool sizes_ok(const splitzip_attention_args& a) {
     if (!dim_ok(a.head_dim) || !format_ok(a.cache_format)) return false;
