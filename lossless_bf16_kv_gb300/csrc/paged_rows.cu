@@ -31,6 +31,7 @@ namespace {
 struct PagedRowsParams {
     splitzip_paged_attention_args a;
     uint32_t group, page_shift, row_tiles, splits, cluster;
+    uint32_t rows_upto;  // only sequences with no more query rows than this
     uint32_t* counters;
     float* partials;
 };
@@ -60,24 +61,6 @@ __device__ __forceinline__ uint32_t place(uint32_t d) {
     return (d & ~15u) + e5m2_place(d & 15u);
 }
 
-// The FP16 power of block b, twice, of a slot's four.
-__device__ __forceinline__ uint32_t twice(uint2 powers, uint32_t b) {
-    return prmt(b & 2 ? powers.y : powers.x, 0u, b & 1 ? 0x3232u : 0x1010u);
-}
-
-// One value of a row as the products have it, for the rare ones that are not finite.
-template <int D, int kFmt>
-__device__ __forceinline__ float page_value(const uint8_t* row, const uint8_t* exps, uint32_t d) {
-    if (kFmt == kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
-    if (kFmt == kE5m2) return __half2float(__ushort_as_half((unsigned short)(row[d] << 8)));
-    uint32_t w[4];
-    if (kFmt == kInt8) w[0] = int8_pair<kInt8_01>(int8_bias(row[d]));
-    else e2m1_pairs(w, row[d / 2]);
-    const uint32_t f = pack2<true>(block_scale(exps[d / (D / 4)]), 0.0f);
-    const float2 v = unpack2<true>(mul_half2(kFmt == kE2m1 && (d & 1) ? w[0] >> 16 : w[0], f));
-    return v.x;
-}
-
 template <int D, int kFmt>
 __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
     using S = PagedShape<D, kFmt>;
@@ -100,7 +83,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
     const Sequence seq(a, b);
     const uint32_t rows = (uint32_t)seq.count * p.group;
     const uint32_t r0 = rt * kTileRows, r1 = min(r0 + kTileRows, rows);
-    if (r0 >= rows) return;  // with all of its cluster
+    if (r0 >= rows || rows > p.rows_upto) return;  // with all of its cluster
     const Mask mask(seq.n, seq.count, a.window, a.sinks);
     const int32_t p0 = mask.first + (int32_t)(r0 / p.group), p1 = mask.first + (int32_t)((r1 - 1) / p.group);
     const SlotTiles tiles(mask, p0, p1, S::kSlots);
@@ -503,9 +486,9 @@ cudaError_t launch_format(const PagedRowsParams& p, uint32_t ctas, cudaStream_t 
 
 }  // namespace
 
-bool paged_rows_plan(const splitzip_paged_attention_args& a, PagedPlan& p) {
+bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p) {
     const uint32_t group = a.q_heads / a.pool.kv_heads, d = a.pool.head_dim;
-    p.row_tiles = (uint32_t)(((uint64_t)a.max_q_tokens * group + 15) / 16);
+    p.row_tiles = (uint32_t)((std::min<uint64_t>((uint64_t)a.max_q_tokens * group, rows_upto) + 15) / 16);
     const uint64_t units = (uint64_t)a.batch * a.pool.kv_heads * p.row_tiles;
     const uint32_t slots = (a.pool.format == kBf16 ? 2048 : 4096) / d;
     uint64_t most = a.kv_tokens;
@@ -515,12 +498,14 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, PagedPlan& p) {
     return units * p.splits <= 0x7FFFFFFFull;
 }
 
-cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, const PagedPlan& plan, void* workspace, cudaStream_t s) {
+cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
+                              cudaStream_t s) {
     PagedRowsParams p;
     p.a = a;
     p.group = a.q_heads / a.pool.kv_heads;
     p.page_shift = 0;
     while ((1u << p.page_shift) < a.pool.page_tokens) p.page_shift++;
+    p.rows_upto = rows_upto;
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
     p.cluster = std::min(plan.splits, 8u);

@@ -1,0 +1,123 @@
+// paged_tiles.cuh -- attention of many query rows over pages (sm_103a): where the
+// work and the rows of attention_tiles.cuh lie when the queries are packed and the
+// cache is in pages.
+//
+// A CTA's row tiles belong to one sequence.  How many a batch has is on the device,
+// so the grid is as large as it can be, each CTA counts the sequences' row tiles up
+// to its own, and those past the last one leave.
+//
+// A tile of 128 slots is loaded page by page, one TMA box of up to 128 rows each,
+// by as many lanes of the loading warp.  Quantised codes are widened to FP16 in
+// shared memory as E5M2 ones are; their exponent bytes come by plain loads.
+#pragma once
+
+#include "attention_tiles.cuh"
+
+namespace splitzip {
+
+struct PagedTilesParams {
+    splitzip_paged_attention_args a;
+    CUtensorMap qmap, kmap, vmap;
+    uint32_t group, tokens;    // query tokens per tile: 128 / group
+    uint32_t splits;
+    uint32_t box, boxes;       // slots to a TMA box, and boxes to a tile
+    uint32_t page_shift;
+    uint32_t rows_from;        // only sequences with more query rows than this
+    uint32_t* status;
+    uint32_t wait_limit;
+
+    static constexpr bool kPaged = true;
+    // Row-tile CTAs of a sequence.
+    template <bool kTwin>
+    __device__ __forceinline__ uint32_t ctas_of(uint32_t b) const {
+        if (b >= a.batch) return 0;
+        const uint32_t count = (uint32_t)sequence_count(a, a.q_start[b], a.q_start[b + 1]), per = kTwin ? tokens : 2 * tokens;
+        return count * group > rows_from ? (count + per - 1) / per : 0;
+    }
+    // This CTA's part of the work: one warp.  count stays 0 where there is none.  The last
+    // sequence's last tiles, which see the most of its slots, go first.
+    template <bool kTwin>
+    __device__ __forceinline__ void place(TilesShared& sh, uint32_t lane) const {
+        const uint32_t unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
+        const uint32_t h = unit % a.pool.kv_heads, at = unit / a.pool.kv_heads;
+        uint32_t total = 0;
+        for (uint32_t b = 0; b < a.batch; b += 32) total += __reduce_add_sync(0xFFFFFFFFu, ctas_of<kTwin>(b + lane));
+        if (lane == 0) sh.count = 0;
+        if (at >= total) return;
+        uint32_t left = total - 1 - at;  // row tiles before this one
+        for (uint32_t b = 0; b < a.batch; b += 32) {
+            const uint32_t mine = ctas_of<kTwin>(b + lane);
+            uint32_t upto = mine;
+#pragma unroll
+            for (int i = 1; i < 32; i *= 2) {
+                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, i);
+                if (lane >= (uint32_t)i) upto += x;
+            }
+            const uint32_t found = __ballot_sync(0xFFFFFFFFu, left < upto);
+            if (!found) {
+                left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+                continue;
+            }
+            if (lane == (uint32_t)__ffs(found) - 1) {
+                const Sequence seq(a, b + lane);
+                sh.b = b + lane;
+                sh.h = h;
+                sh.first_row = seq.row;
+                sh.count = seq.count;
+                set_work<kTwin>(sh, Mask(seq.n, seq.count, a.window, a.sinks), (left - (upto - mine)) * (kTwin ? tokens : 2 * tokens),
+                                (uint32_t)seq.count, tokens, split, splits);
+            }
+            return;
+        }
+    }
+    // Where query token tok and query head hq of this CTA's sequence lie.
+    __device__ __forceinline__ uint32_t queries(const TilesShared& sh) const { return (uint32_t)sh.count; }
+    __device__ __forceinline__ const __nv_bfloat16* query(const TilesShared& sh, uint32_t tok, uint32_t hq) const {
+        return static_cast<const __nv_bfloat16*>(a.q.data) + (int64_t)(sh.first_row + tok) * a.q.stride_t + (int64_t)hq * a.q.stride_h;
+    }
+    __device__ __forceinline__ __nv_bfloat16* out(const TilesShared& sh, uint32_t tok, uint32_t hq) const {
+        return static_cast<__nv_bfloat16*>(a.out.data) + (int64_t)(sh.first_row + tok) * a.out.stride_t + (int64_t)hq * a.out.stride_h;
+    }
+    __device__ __forceinline__ float* lse(const TilesShared& sh, uint32_t tok, uint32_t hq) const {
+        return a.lse + (uint64_t)hq * a.tokens + sh.first_row + tok;
+    }
+    // Whether a query of this CTA may see one of the slots s .. s + run - 1.
+    __device__ __forceinline__ bool run_seen(const volatile TilesShared& sh, int32_t s, uint32_t run) const {
+        return s <= sh.p1 && ((int64_t)s + run > (int64_t)sh.p0 - (int64_t)sh.window + 1 || s < sh.sinks);
+    }
+    __device__ __forceinline__ uint32_t page(const volatile TilesShared& sh, int32_t s) const {
+        return (uint32_t)a.table[(uint64_t)sh.b * a.table_width + ((uint32_t)s >> page_shift)];
+    }
+    // The rows of this CTA's values by slot; none where the page is outside the pool.
+    struct Row {
+        const uint8_t *data, *exponents;
+    };
+    template <int kElem>
+    __device__ __forceinline__ auto values(const TilesShared& sh) const {
+        return [&sh, this](int32_t s) {
+            const splitzip_page_rows& v = a.pool.v;
+            const uint32_t x = page(sh, s);
+            if (x >= a.pool.pages) return Row{nullptr, nullptr};
+            const int64_t at = (uint32_t)s & (a.pool.page_tokens - 1);
+            return Row{static_cast<const uint8_t*>(v.data) + (x * v.stride_p + at * v.stride_t + (int64_t)sh.h * v.stride_h) * kElem,
+                       v.exponents + x * v.exp_stride_p + at * v.exp_stride_t + (int64_t)sh.h * v.exp_stride_h};
+        };
+    }
+};
+
+template <int D, bool kTwin>
+cudaError_t launch_paged_format(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s) {
+    switch (p.a.pool.format) {
+        case kBf16: return launch_tiles<D, kBf16, kTwin>(p, ctas, s);
+        case kE5m2: return launch_tiles<D, kE5m2, kTwin>(p, ctas, s);
+        case kInt8: return launch_tiles<D, kInt8, kTwin>(p, ctas, s);
+        default: return launch_tiles<D, kE2m1, kTwin>(p, ctas, s);
+    }
+}
+// One for each head_dim and kind of tile, compiled side by side.
+cudaError_t launch_paged_64(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
+cudaError_t launch_paged_64_twin(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
+cudaError_t launch_paged_128(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
+cudaError_t launch_paged_128_twin(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
+
+}  // namespace splitzip

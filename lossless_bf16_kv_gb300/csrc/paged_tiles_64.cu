@@ -1,0 +1,8 @@
+// paged_tiles_64.cu -- the kernels of paged_tiles.cuh for head_dim 64 (sm_103a).
+#include "paged_tiles.cuh"
+
+namespace splitzip {
+
+cudaError_t launch_paged_64(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s) { return launch_paged_format<64, false>(p, ctas, s); }
+
+}  // namespace splitzip

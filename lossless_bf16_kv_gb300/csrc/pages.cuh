@@ -12,10 +12,17 @@ namespace splitzip {
 enum Format : int { kBf16 = SPLITZIP_FORMAT_BF16, kE5m2 = SPLITZIP_FORMAT_E5M2, kInt8 = SPLITZIP_FORMAT_INT8, kE2m1 = SPLITZIP_FORMAT_E2M1 };
 
 template <int kFmt>
+constexpr bool kWide = kFmt != kBf16;  // operands are FP16, widened from the cache's bytes
+template <int kFmt>
 constexpr bool kQuantised = kFmt == kInt8 || kFmt == kE2m1;
 // Bytes of a row's codes.
 template <int D, int kFmt>
 constexpr int kRowBytes = kFmt == kBf16 ? 2 * D : kFmt == kE2m1 ? D / 2 : D;
+
+// New tokens of a sequence whose rows are from .. to - 1; 0 where that is no range to be taken.
+__device__ __forceinline__ int32_t sequence_count(const splitzip_paged_attention_args& a, int32_t from, int32_t to) {
+    return from >= 0 && to >= from && (uint32_t)to <= a.tokens && (uint32_t)(to - from) <= a.max_q_tokens ? to - from : 0;
+}
 
 // One sequence of a batch: its new tokens' first row, their number (0: left out),
 // its length.
@@ -23,9 +30,8 @@ struct Sequence {
     int32_t row, count, n;
     __device__ __forceinline__ Sequence(const splitzip_paged_attention_args& a, uint32_t b) {
         const int32_t from = a.q_start[b], to = a.q_start[b + 1], len = a.lens[b];
-        const bool ok = from >= 0 && to >= from && (uint32_t)to <= a.tokens && (uint32_t)(to - from) <= a.max_q_tokens;
         row = from;
-        count = ok ? to - from : 0;
+        count = sequence_count(a, from, to);
         n = len < 0 ? 0 : min(len, (int32_t)a.kv_tokens);
     }
 };
@@ -58,6 +64,24 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t (&h)[4], uint32_t r) {
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The FP16 power of block b, twice, of a slot's four.
+__device__ __forceinline__ uint32_t twice(uint2 powers, uint32_t b) {
+    return prmt(b & 2 ? powers.y : powers.x, 0u, b & 1 ? 0x3232u : 0x1010u);
+}
+
+// One value of a row as the products have it, for the rare ones that are not finite.
+template <int D, int kFmt>
+__device__ __forceinline__ float page_value(const uint8_t* row, const uint8_t* exps, uint32_t d) {
+    if (kFmt == kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
+    if (kFmt == kE5m2) return __half2float(__ushort_as_half((unsigned short)(row[d] << 8)));
+    uint32_t w[4];
+    if (kFmt == kInt8) w[0] = int8_pair<kInt8_01>(int8_bias(row[d]));
+    else e2m1_pairs(w, row[d / 2]);
+    const uint32_t f = pack2<true>(block_scale(exps[d / (D / 4)]), 0.0f);
+    const float2 v = unpack2<true>(mul_half2(kFmt == kE2m1 && (d & 1) ? w[0] >> 16 : w[0], f));
+    return v.x;
 }
 
 }  // namespace splitzip

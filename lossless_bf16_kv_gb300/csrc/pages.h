@@ -13,12 +13,20 @@ namespace splitzip {
 cudaError_t launch_pages_store(const splitzip_pages_store_args& a, cudaStream_t s);
 cudaError_t launch_pages_load(const splitzip_pages_load_args& a, cudaStream_t s);
 
-// Sequences by how many query rows (new tokens times heads of a group) they bring.
+// Sequences of few query rows (new tokens times the heads of a group; paged_rows.cu)
+// and of many (paged_tiles.cu).  A plan depends on the sizes alone; it is false where
+// they do not fit a launch.
 struct PagedPlan {
-    uint32_t row_tiles, splits;
-    size_t bytes;  // of workspace
+    uint32_t row_tiles;  // of a sequence (few rows), or at most of the batch (many)
+    uint32_t splits;
+    size_t bytes;        // of workspace
 };
-bool paged_rows_plan(const splitzip_paged_attention_args& a, PagedPlan& p);
-cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, const PagedPlan& p, void* workspace, cudaStream_t s);
+// Sequences of up to rows_upto query rows, and of more than rows_from.
+bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p);
+bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from, PagedPlan& p);
+cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& p, void* workspace,
+                              cudaStream_t s);
+cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, const PagedPlan& p, void* workspace,
+                               cudaStream_t s);
 
 }  // namespace splitzip

@@ -38,6 +38,28 @@ bool sizes_ok(const splitzip_paged_attention_args& a) {
            (uint64_t)a.batch * hk * a.tokens <= kMax31;
 }
 
+// Which kernel takes a sequence: tiles of 128 query rows on the tensor cores from 17
+// rows of a key/value head on.  With one sequence that may have as many, they take it
+// whatever it has.
+struct Plans {
+    bool rows, tiles;
+    uint32_t border;  // the most rows of the few-row kernel
+    PagedPlan few, many;
+    size_t bytes;
+};
+bool plan(const splitzip_paged_attention_args& a, Plans& p) {
+    constexpr uint32_t kFewRows = 16;
+    p.tiles = (uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads) > kFewRows;
+    p.rows = !p.tiles || a.batch > 1;
+    p.border = p.rows ? kFewRows : 0;
+    p.bytes = 0;
+    if (p.rows && !paged_rows_plan(a, p.border, p.few)) return false;
+    if (p.tiles && !paged_tiles_plan(a, p.border, p.many)) return false;
+    if (p.rows) p.bytes = p.few.bytes;
+    if (p.tiles && p.many.bytes > p.bytes) p.bytes = p.many.bytes;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -68,21 +90,25 @@ splitzip_status splitzip_pages_load(const splitzip_pages_load_args* a, splitzip_
 }
 
 size_t splitzip_paged_attention_workspace_bytes(const splitzip_paged_attention_args* a) {
-    PagedPlan rows;
-    return a && sizes_ok(*a) && paged_rows_plan(*a, rows) ? rows.bytes : 0;
+    Plans p;
+    return a && sizes_ok(*a) && plan(*a, p) ? p.bytes : 0;
 }
 
 splitzip_status splitzip_paged_attention(const splitzip_paged_attention_args* a, void* workspace, size_t workspace_bytes,
                                          splitzip_stream_t s) {
     TraceRange trace("splitzip_paged_attention");
-    PagedPlan rows;
-    if (!a || !sizes_ok(*a) || !paged_rows_plan(*a, rows) || !pool_ok(a->pool)) return SPLITZIP_ERR_INVALID_ARG;
+    Plans p;
+    if (!a || !sizes_ok(*a) || !plan(*a, p) || !pool_ok(a->pool)) return SPLITZIP_ERR_INVALID_ARG;
     if (!view_ok(a->q, 2, 1, a->tokens, a->q_heads) || !view_ok(a->out, 2, 1, a->tokens, a->q_heads, true)) return SPLITZIP_ERR_INVALID_ARG;
     if (!a->table || !a->q_start || !a->lens || !aligned(a->table, 4) || !aligned(a->q_start, 4) || !aligned(a->lens, 4) ||
         !aligned(a->lse, 4) || !std::isfinite(a->scale) || !(a->scale > 0.0f))
         return SPLITZIP_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < rows.bytes) return SPLITZIP_ERR_INVALID_ARG;
-    return from_cuda(launch_paged_rows(*a, rows, workspace, (cudaStream_t)s));
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
+    if (p.tiles) {
+        const cudaError_t e = launch_paged_tiles(*a, p.border, p.many, workspace, (cudaStream_t)s);
+        if (e != cudaSuccess || !p.rows) return from_cuda(e);
+    }
+    return from_cuda(launch_paged_rows(*a, p.border, p.few, workspace, (cudaStream_t)s));
 }
 
 }  // extern "C"
