@@ -1,11 +1,16 @@
 // paged_rows.cu -- attention of few query rows over pages (sm_103a).
 //
-// The kernel of attention_rows.cu for a paged cache: the query rows of one sequence
-// and key/value head (its new tokens times the group's query heads) in tiles of 16,
-// a tile's slots in splits, one CTA each, each of its four warps with its own slot
-// tiles, running maximum, sum and output, joined at the end in a fixed order.
-// Every key and value is read once: HBM bounds it, next to the widening of
-// quantised codes.
+// The query rows of one sequence and key/value head (its new tokens times the group's
+// query heads) in tiles of 8 or 16, a tile's slots in splits, one CTA each, each of
+// its four warps with its own slot tiles, running maximum, sum and output as in
+// attention_rows.cu, joined at the end in a fixed order.  Every key and value is
+// read once: HBM bounds it, next to the widening of quantised codes.
+//
+// The products are transposed: S^T = K Q^T and O^T += V^T P^T, with slots, then a
+// head's values as the 16 rows of an m16n8k16 product and the query rows as its 8
+// columns.  One token of a group of up to eight heads fills those: half the products,
+// exponentials and registers that 16 rows take.  P^T comes out of S^T by a
+// transposition of 8 x 8 blocks between registers (movmatrix).
 //
 // Pages hold at least 16 slots, and a warp's tiles 32 or 64 (16 of BF16 at head_dim
 // 128), so a tile is a few runs of 16 slots of one page each.  The lanes hold the
@@ -46,7 +51,6 @@ struct PagedShape {
     static constexpr int kStage = 2 * (kTile + kExps);
     static constexpr int kScales = kQuantised<kFmt> ? 16 * kSlots : 0;  // of the powers as FP16, keys' and values'
     static constexpr int kRing = kWarpsRows * (kStages * kStage + kScales);
-    static constexpr int kSmem = kRing + 16 * D * 2;
     static_assert(kRing >= kWarpsRows * 16 * D * 4, "partial results take the place of the ring");
 };
 
@@ -61,15 +65,21 @@ __device__ __forceinline__ uint32_t place(uint32_t d) {
     return (d & ~15u) + e5m2_place(d & 15u);
 }
 
-template <int D, int kFmt>
+// The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// NB: blocks of 8 query rows.
+template <int D, int kFmt, int NB>
 __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
     using S = PagedShape<D, kFmt>;
-    constexpr bool kHalf = kFmt != kBf16;  // operands FP16, else BF16
-    constexpr int kTileRows = 16;
-    constexpr int NT = S::kSlots / 8;    // n-tiles of the scores
-    constexpr int KS = D / 16;           // k-steps of the scores
-    constexpr int PS = S::kSlots / 16;   // k-steps of the output, and runs of one page each
-    constexpr int OT = D / 8;            // n-tiles of the output
+    constexpr bool kHalf = kWide<kFmt>;  // operands FP16, else BF16
+    constexpr int kTileRows = 8 * NB;
+    constexpr int KS = D / 16;           // steps of the scores, and 16-value blocks of the output
+    constexpr int PS = S::kSlots / 16;   // 16-slot blocks of the scores, steps of the output, runs of one page each
     constexpr int kChunks = S::kRow / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_scale[kTileRows];
@@ -129,12 +139,24 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
                 const uint8_t* k = kbase + page * pool.k.stride_p * kElem + 16 * lc;
                 const uint8_t* v = vbase + page * pool.v.stride_p * kElem + 16 * lc;
                 const int32_t first = s0 + 16 * i;
+                if (full) {
+                    const uint32_t at = ((uint32_t)first & in_page) + lr;
+                    k += at * kst;
+                    v += at * vst;
 #pragma unroll
-                for (int x = 0; x < 16 / kStep; x++) {
-                    const int32_t s = first + x * kStep + (int32_t)lr;
-                    const uint32_t at = (uint32_t)(full ? s : min(s, mask.n - 1)) & in_page;
-                    cp_async16(dk + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), k + at * kst);
-                    cp_async16(dk + S::kTile + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), v + at * vst);
+                    for (int x = 0; x < 16 / kStep; x++) {
+                        cp_async16(dk + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), k);
+                        cp_async16(dk + S::kTile + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), v);
+                        k += kStep * kst;
+                        v += kStep * vst;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int x = 0; x < 16 / kStep; x++) {
+                        const uint32_t at = (uint32_t)min(first + x * kStep + (int32_t)lr, mask.n - 1) & in_page;
+                        cp_async16(dk + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), k + at * kst);
+                        cp_async16(dk + S::kTile + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), v + at * vst);
+                    }
                 }
             }
             if constexpr (kQuantised<kFmt>) {
@@ -193,26 +215,36 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
     }
     __syncthreads();
 
-    // This thread's rows: lane / 4 and that + 8.
-    int32_t pos[2];
-    float scale[2], m[2], l[2], o[OT][4];
+    // This thread's query rows: 8 y + 2 (lane & 3) and the next.  m is the same for all
+    // lanes that share a row, l each lane's own part.
+    int32_t pos[NB][2];
+    float scale[NB][2], m[NB][2], l[NB][2], o[KS][NB][4];
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-        const uint32_t r = 8 * x + lane / 4;
-        pos[x] = r0 + r < r1 ? mask.pos((r0 + r) / p.group) : -1;
-        scale[x] = s_scale[r];
-        m[x] = -INFINITY;
-        l[x] = 0.0f;
-    }
+    for (int y = 0; y < NB; y++)
 #pragma unroll
-    for (int j = 0; j < OT; j++)
+        for (int x = 0; x < 2; x++) {
+            const uint32_t r = 8 * y + 2 * (lane & 3) + x;
+            pos[y][x] = r0 + r < r1 ? mask.pos((r0 + r) / p.group) : -1;
+            scale[y][x] = s_scale[r];
+            m[y][x] = -INFINITY;
+            l[y][x] = 0.0f;
+        }
 #pragma unroll
-        for (int x = 0; x < 4; x++) o[j][x] = 0.0f;
+    for (int k = 0; k < KS; k++)
+#pragma unroll
+        for (int y = 0; y < NB; y++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) o[k][y][x] = 0.0f;
 
-    const uint32_t qaddr = smem_addr(qs);
-    uint32_t qf[KS][4];
+    uint32_t qf[KS][NB][2];  // the queries' fragments stay in registers
 #pragma unroll
-    for (int k = 0; k < KS; k++) ldmatrix4(qf[k], qaddr + chunk_at<2 * D>(lane & 15, 2 * k + (lane >> 4)));
+    for (int k = 0; k < KS; k += 2)
+#pragma unroll
+        for (int y = 0; y < NB; y++) {
+            uint32_t r[4];
+            ldmatrix4(r, smem_addr(qs) + chunk_at<2 * D>(8 * y + (lane & 7), 2 * k + (lane >> 3)));
+            qf[k][y][0] = r[0], qf[k][y][1] = r[1], qf[k + 1][y][0] = r[2], qf[k + 1][y][1] = r[3];
+        }
     bool odd = false;  // a value of a partly visible tile was infinite or NaN
     uint32_t stage = 0;
     for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
@@ -244,157 +276,190 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             }
             __syncwarp();
         }
-        float sc[NT][4];
-        uint2 kpow[kQuantised<kFmt> ? NT : 1];
+        // Scores of slots 16 i + lane / 4 and that + 8 (x >> 1) for this thread's rows (x & 1).
+        float sc[PS][NB][4];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
+        for (int i = 0; i < PS; i++) {
 #pragma unroll
-            for (int x = 0; x < 4; x++) sc[n][x] = 0.0f;
-            if constexpr (kQuantised<kFmt>) kpow[n] = *reinterpret_cast<const uint2*>(scales + 8 * (8 * n + lane / 4));
-        }
-        if constexpr (kFmt == kBf16) {
+            for (int y = 0; y < NB; y++)
 #pragma unroll
-            for (int k = 0; k < KS; k++)
+                for (int x = 0; x < 4; x++) sc[i][y][x] = 0.0f;
+            const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                const uint32_t f[4] = {a0, a1, a2, a3};
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
+                for (int y = 0; y < NB; y++) mma16816<kHalf>(sc[i][y], f, qf[k][y][0], qf[k][y][1]);
+            };
+            if constexpr (kFmt == kBf16) {
+#pragma unroll
+                for (int k = 0; k < KS; k++) {
                     uint32_t r[4];
-                    ldmatrix4(r, ks + chunk_at<S::kRow>(8 * n + 8 * (lane >> 4) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
-                    mma16816<false>(sc[n], qf[k], r[0], r[1]);
-                    mma16816<false>(sc[n + 1], qf[k], r[2], r[3]);
+                    ldmatrix4(r, ks + chunk_at<S::kRow>(16 * i + (lane & 15), 2 * k + (lane >> 4)));
+                    product(k, r[0], r[1], r[2], r[3]);
                 }
-        } else {
+            } else {
+                uint2 power[2];  // of the two slots
+                if constexpr (kQuantised<kFmt>)
 #pragma unroll
-            for (int c = 0; c < kChunks; c++)  // 16 bytes of each key: one step, or two of E2M1
+                    for (int x = 0; x < 2; x++) power[x] = *reinterpret_cast<const uint2*>(scales + 8 * (16 * i + 8 * x + lane / 4));
 #pragma unroll
-                for (int n = 0; n < NT; n += 4) {
-                    uint32_t r[4];
-                    ldmatrix4(r, ks + chunk_at<S::kRow>(8 * n + lane, c));
+                for (int c = 0; c < kChunks; c += 2) {
+                    uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block
+                    ldmatrix4(r, ks + chunk_at<S::kRow>(16 * i + (lane & 15), c + (lane >> 4)));
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                        if constexpr (kFmt == kE5m2) {
-                            mma16816<true>(sc[n + x], qf[c], e5m2_01(r[x]), e5m2_23(r[x]));
-                        } else if constexpr (kFmt == kInt8) {
-                            const uint32_t f = twice(kpow[n + x], c * 16 / (D / 4)), w = int8_bias(r[x]);
-                            mma16816<true>(sc[n + x], qf[c], mul_half2(int8_pair<kInt8_01>(w), f), mul_half2(int8_pair<kInt8_23>(w), f));
+                    for (int u = 0; u < 2; u++) {
+                        uint32_t w[2][4];
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            const uint32_t v = r[2 * u + x];
+                            if constexpr (kFmt == kE5m2) {
+                                w[x][0] = e5m2_01(v), w[x][1] = e5m2_23(v);
+                            } else if constexpr (kFmt == kInt8) {
+                                const uint32_t f = twice(power[x], (c + u) * 16 / (D / 4)), z = int8_bias(v);
+                                w[x][0] = mul_half2(int8_pair<kInt8_01>(z), f), w[x][1] = mul_half2(int8_pair<kInt8_23>(z), f);
+                            } else {
+                                // A lane's eight values are one block's: its half of the 32, or all of them.
+                                const uint32_t f = D == 128 ? twice(power[x], c + u)
+                                                            : prmt(u ? power[x].y : power[x].x, 0u, lane & 2 ? 0x3232u : 0x1010u);
+                                e2m1_pairs(w[x], v);
+#pragma unroll
+                                for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
+                            }
+                        }
+                        if constexpr (kFmt == kE2m1) {
+                            product(2 * (c + u), w[0][0], w[1][0], w[0][1], w[1][1]);
+                            product(2 * (c + u) + 1, w[0][2], w[1][2], w[0][3], w[1][3]);
                         } else {
-                            // A lane's eight values are one block's: its half of the 32, or all of them.
-                            const uint32_t f = D == 128 ? twice(kpow[n + x], c)
-                                                        : prmt(c ? kpow[n + x].y : kpow[n + x].x, 0u, lane & 2 ? 0x3232u : 0x1010u);
-                            uint32_t w[4];
-                            e2m1_pairs(w, r[x]);
-                            mma16816<true>(sc[n + x], qf[2 * c], mul_half2(w[0], f), mul_half2(w[1], f));
-                            mma16816<true>(sc[n + x], qf[2 * c + 1], mul_half2(w[2], f), mul_half2(w[3], f));
+                            product(c + u, w[0][0], w[1][0], w[0][1], w[1][1]);
                         }
                     }
                 }
+            }
         }
-        uint32_t pr[PS][4];
-        {
-            float top[2] = {m[0] + kLift<kHalf>, m[1] + kLift<kHalf>};
+        bool more = false;  // a row's maximum grows
+        float top[NB][2];
 #pragma unroll
-            for (int n = 0; n < NT; n++)
+        for (int y = 0; y < NB; y++)
+#pragma unroll
+            for (int x = 0; x < 2; x++) top[y][x] = m[y][x] + kLift<kHalf>;
+#pragma unroll
+        for (int y = 0; y < NB; y++) {
+#pragma unroll
+            for (int i = 0; i < PS; i++)
 #pragma unroll
                 for (int x = 0; x < 4; x++) {
-                    float v = sc[n][x] * scale[x >> 1];
-                    if (!whole && !mask.sees(pos[x >> 1], s0 + 8 * n + 2 * (int32_t)(lane & 3) + (x & 1))) v = -INFINITY;
-                    sc[n][x] = v;
-                    top[x >> 1] = fmaxf(top[x >> 1], v);
+                    float v = sc[i][y][x] * scale[y][x & 1];
+                    if (!whole && !mask.sees(pos[y][x & 1], s0 + 16 * i + 8 * (x >> 1) + (int32_t)(lane / 4))) v = -INFINITY;
+                    sc[i][y][x] = v;
+                    top[y][x & 1] = fmaxf(top[y][x & 1], v);
                 }
 #pragma unroll
             for (int x = 0; x < 2; x++) {
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 1));
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xFFFFFFFFu, top[x], 2));
+                top[y][x] -= kLift<kHalf>;
+                more |= top[y][x] != m[y][x];
             }
-            top[0] -= kLift<kHalf>, top[1] -= kLift<kHalf>;
-            const bool same = top[0] == m[0] && top[1] == m[1];
-            const float use[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
-            if (!__all_sync(0xFFFFFFFFu, same)) {
+        }
+        if (__any_sync(0xFFFFFFFFu, more)) {  // more and more rarely
+#pragma unroll
+            for (int y = 0; y < NB; y++)
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
-                    const float f = exp2_approx(m[x] - use[x]);
-                    l[x] *= f;
+                    float now = top[y][x];
 #pragma unroll
-                    for (int n = 0; n < OT; n++) {
-                        o[n][2 * x] *= f;
-                        o[n][2 * x + 1] *= f;
+                    for (int i = 4; i < 32; i *= 2) now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, i));
+                    const float f = exp2_approx(m[y][x] - (now == -INFINITY ? 0.0f : now));
+                    l[y][x] *= f;
+#pragma unroll
+                    for (int k = 0; k < KS; k++) {
+                        o[k][y][x] *= f;
+                        o[k][y][2 + x] *= f;
                     }
-                    m[x] = top[x];
+                    m[y][x] = now;
                 }
-            }
+        }
+        uint32_t pr[PS][NB][2];  // P^T's fragments
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
+        for (int y = 0; y < NB; y++) {
+            const float use[2] = {m[y][0] == -INFINITY ? 0.0f : m[y][0], m[y][1] == -INFINITY ? 0.0f : m[y][1]};
+#pragma unroll
+            for (int i = 0; i < PS; i++) {
                 float e[4];
 #pragma unroll
                 for (int x = 0; x < 4; x++) {
-                    e[x] = exp2_approx(sc[n][x] - use[x >> 1]);
-                    l[x >> 1] += e[x];
+                    e[x] = exp2_approx(sc[i][y][x] - use[x & 1]);
+                    l[y][x & 1] += e[x];
                 }
                 // p in 16 bits for the product: a relative error of up to 2^-8 (BF16) or
                 // 2^-11 (FP16, down to 2^-29 of the row's largest) of each term,
                 // independent from term to term.
-                pr[n >> 1][2 * (n & 1)] = pack2<kHalf>(e[0], e[1]);
-                pr[n >> 1][2 * (n & 1) + 1] = pack2<kHalf>(e[2], e[3]);
+                pr[i][y][0] = transpose8(pack2<kHalf>(e[0], e[1]));
+                pr[i][y][1] = transpose8(pack2<kHalf>(e[2], e[3]));
             }
         }
-        constexpr int kFrom = kFmt == kBf16 ? 2 : kFmt == kE2m1 ? 8 : 4;  // n-tiles out of two 16-byte chunks of a row
 #pragma unroll
-        for (int k = 0; k < PS; k++) {
-#pragma unroll
-            for (int n = 0; n < OT; n += kFrom) {
-                const int chunk = 2 * (n / kFrom);
-                uint32_t r[4];
-                ldmatrix4_trans(r, vs + chunk_at<S::kRow>(16 * k + 8 * ((lane >> 3) & 1) + (lane & 7), chunk + (lane >> 4)));
-                uint32_t v[2 * kFrom];  // of each n-tile: slots 0-7 and 8-15 of the step
-                if constexpr (kFmt == kBf16) {
-#pragma unroll
-                    for (int x = 0; x < 4; x++) v[x] = r[x];
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; x++) {  // chunk x >> 1, slots 8 (x & 1) ..
-                        uint32_t f = 0;
-                        if constexpr (kQuantised<kFmt>) {
-                            const uint32_t block = kFmt == kInt8 ? (chunk + (x >> 1)) * 16 / (D / 4)
-                                                                 : D == 128 ? chunk + (x >> 1) : 2 * (chunk + (x >> 1)) + (lane >> 4);
-                            f = *reinterpret_cast<const uint32_t*>(scales + 8 * S::kSlots + 2 * (block * S::kSlots + 16 * k + 8 * (x & 1) + 2 * (lane & 3)));
-                        }
-                        if constexpr (kFmt == kE5m2) {
-                            v[4 * (x >> 1) + (x & 1)] = e5m2_02(r[x]);
-                            v[4 * (x >> 1) + 2 + (x & 1)] = e5m2_13(r[x]);
-                        } else if constexpr (kFmt == kInt8) {
-                            const uint32_t w = int8_bias(r[x]);
-                            v[4 * (x >> 1) + (x & 1)] = mul_half2(int8_pair<kInt8_02>(w), f);
-                            v[4 * (x >> 1) + 2 + (x & 1)] = mul_half2(int8_pair<kInt8_13>(w), f);
-                        } else {
-                            // Bytes of the same value of both slots: values 0 and 2, then 1 and 3.
-                            uint32_t even = (r[x] & 0x0F0Fu) | (r[x] >> 12 & 0xF0F0u), w[4];
-                            even |= ((r[x] >> 4 & 0x0F0Fu) | (r[x] >> 16 & 0xF0F0u)) << 16;
-                            e2m1_pairs(w, even);
-                            v[8 * (x >> 1) + (x & 1)] = mul_half2(w[0], f);
-                            v[8 * (x >> 1) + 4 + (x & 1)] = mul_half2(w[1], f);
-                            v[8 * (x >> 1) + 2 + (x & 1)] = mul_half2(w[2], f);
-                            v[8 * (x >> 1) + 6 + (x & 1)] = mul_half2(w[3], f);
-                        }
-                    }
-                }
+        for (int i = 0; i < PS; i++) {
+            // Values of slots 2 (lane & 3) and the next, and of those + 8, as rows of V^T.
+            const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                uint32_t f[4] = {a0, a1, a2, a3};
                 if (!whole) {  // 0 x infinity is not 0: keep such values out of the product
 #pragma unroll
-                    for (int x = 0; x < 2 * kFrom; x++) {
-                        const uint32_t f = finite_or_zero<kHalf>(v[x]);
-                        odd |= f != v[x];
-                        v[x] = f;
+                    for (int x = 0; x < 4; x++) {
+                        const uint32_t v = finite_or_zero<kHalf>(f[x]);
+                        odd |= v != f[x];
+                        f[x] = v;
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < kFrom; x++) mma16816<kHalf>(o[n + x], pr[k], v[2 * x], v[2 * x + 1]);
+                for (int y = 0; y < NB; y++) mma16816<kHalf>(o[k][y], f, pr[i][y][0], pr[i][y][1]);
+            };
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block, transposed
+                ldmatrix4_trans(r, vs + chunk_at<S::kRow>(16 * i + (lane & 15), c + (lane >> 4)));
+                if constexpr (kFmt == kBf16) {
+                    product(c / 2, r[0], r[2], r[1], r[3]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        uint32_t w[2][4];
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            const uint32_t v = r[2 * u + x];
+                            uint32_t f = 0;
+                            if constexpr (kQuantised<kFmt>) {
+                                const uint32_t block = kFmt == kInt8 ? (c + u) * 16 / (D / 4) : D == 128 ? c + u : 2 * (c + u) + (lane >> 4);
+                                f = *reinterpret_cast<const uint32_t*>(scales + 8 * S::kSlots + 2 * (block * S::kSlots + 16 * i + 8 * x + 2 * (lane & 3)));
+                            }
+                            if constexpr (kFmt == kE5m2) {
+                                w[x][0] = e5m2_02(v), w[x][1] = e5m2_13(v);
+                            } else if constexpr (kFmt == kInt8) {
+                                const uint32_t z = int8_bias(v);
+                                w[x][0] = mul_half2(int8_pair<kInt8_02>(z), f), w[x][1] = mul_half2(int8_pair<kInt8_13>(z), f);
+                            } else {
+                                // Bytes of the same value of both slots: values 0 and 2, then 1 and 3.
+                                uint32_t z = (v & 0x0F0Fu) | (v >> 12 & 0xF0F0u);
+                                z |= ((v >> 4 & 0x0F0Fu) | (v >> 16 & 0xF0F0u)) << 16;
+                                e2m1_pairs(w[x], z);
+#pragma unroll
+                                for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
+                            }
+                        }
+                        if constexpr (kFmt == kE2m1) {
+                            product(2 * (c + u), w[0][0], w[0][2], w[1][0], w[1][2]);
+                            product(2 * (c + u) + 1, w[0][1], w[0][3], w[1][1], w[1][3]);
+                        } else {
+                            product(c + u, w[0][0], w[0][1], w[1][0], w[1][1]);
+                        }
+                    }
+                }
             }
         }
         if constexpr (kQuantised<kFmt>) __syncwarp();  // the powers have been read
     }
     cp_async_wait<0>();
-    // Column of o[n][x] in the head: of the lane's accumulator columns i = 2 (lane & 3) + (x & 1).
-    auto column = [&](int n, int x) {
-        const int i = 2 * (int)(lane & 3) + (x & 1);
-        return kFmt == kBf16 ? 8 * n + i : kFmt == kE2m1 ? 32 * (n / 4) + 4 * i + (n & 3) : 16 * (n / 2) + 2 * i + (n & 1);
+    // The head's value of o[k][..][x].
+    auto column = [&](int k, int x) {
+        const int i = (int)(lane / 4), u = x >> 1;
+        return kFmt == kBf16 ? 16 * k + 8 * u + i : kFmt == kE2m1 ? 32 * (k / 2) + 4 * i + 2 * (k & 1) + u : 16 * k + 2 * i + u;
     };
     if (__any_sync(0xFFFFFFFFu, odd)) {
         // The infinite and NaN values of partly visible tiles go to the rows that
@@ -403,21 +468,25 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
             if (p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kSlots - 1)) continue;
             for (int32_t s = s0; s < min(s0 + S::kSlots, mask.n); s++) {
-                if (!mask.sees(pos[0], s) && !mask.sees(pos[1], s)) continue;
+                if (s > p1) break;
+                const bool sinks = s < mask.sinks;
+                if (!sinks && (int64_t)s <= (int64_t)p0 - (int64_t)mask.window) continue;
                 const uint32_t page = (uint32_t)table[s >> p.page_shift];
                 if (page >= pool.pages) continue;
                 const int64_t at = (uint32_t)s & in_page;
                 const uint8_t* row = vbase + page * pool.v.stride_p * kElem + at * vst;
                 const uint8_t* exps = vexps + page * pool.v.exp_stride_p + at * pool.v.exp_stride_t;
 #pragma unroll
-                for (int n = 0; n < OT; n++)
+                for (int k = 0; k < KS; k++)
 #pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        const float v = page_value<D, kFmt>(row, exps, column(n, x));
+                    for (int x = 0; x < 4; x += 2) {
+                        const float v = page_value<D, kFmt>(row, exps, column(k, x));
                         if (isfinite(v)) continue;
 #pragma unroll
-                        for (int y = 0; y < 2; y++)
-                            if (mask.sees(pos[y], s)) o[n][2 * y + x] += v;
+                        for (int y = 0; y < NB; y++) {
+                            if (mask.sees(pos[y][0], s)) o[k][y][x] += v;
+                            if (mask.sees(pos[y][1], s)) o[k][y][x + 1] += v;
+                        }
                     }
             }
         }
@@ -426,20 +495,24 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
 
     // Join the warps: everything into shared memory (over the ring).
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-        l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 2);
-        if ((lane & 3) == 0) {
-            sh.m[warp][8 * x + lane / 4] = m[x];
-            sh.l[warp][8 * x + lane / 4] = lost ? __int_as_float(0x7FC00000) : l[x];
+    for (int y = 0; y < NB; y++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+#pragma unroll
+            for (int i = 4; i < 32; i *= 2) l[y][x] += __shfl_xor_sync(0xFFFFFFFFu, l[y][x], i);
+            if (lane < 4) {
+                sh.m[warp][8 * y + 2 * lane + x] = m[y][x];
+                sh.l[warp][8 * y + 2 * lane + x] = lost ? __int_as_float(0x7FC00000) : l[y][x];
+            }
         }
-    }
     __syncthreads();  // every warp is done with its ring
     float* os = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int n = 0; n < OT; n++)
+    for (int k = 0; k < KS; k++)
 #pragma unroll
-        for (int x = 0; x < 4; x++) os[(warp * kTileRows + 8 * (x >> 1) + lane / 4) * D + column(n, x)] = o[n][x];
+        for (int y = 0; y < NB; y++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) os[(warp * kTileRows + 8 * y + 2 * (lane & 3) + (x & 1)) * D + column(k, x)] = o[k][y][x];
     __syncthreads();
 
     auto store = [&](uint32_t r, uint32_t c, float4 v, float mm, float ll) {
@@ -454,11 +527,11 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
     join_rows<D, kTileRows>(os, sh, unit, split, p.splits, p.cluster, r1 - r0, p.counters, p.partials, store);
 }
 
-template <int D, int kFmt>
+template <int D, int kFmt, int NB>
 cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, cudaStream_t s) {
-    using S = PagedShape<D, kFmt>;
+    constexpr int kSmem = PagedShape<D, kFmt>::kRing + 8 * NB * D * 2;
     Wave w;
-    const cudaError_t e = launch_wave<paged_rows_kernel<D, kFmt>>(32 * kWarpsRows, S::kSmem, w);
+    const cudaError_t e = launch_wave<paged_rows_kernel<D, kFmt, NB>>(32 * kWarpsRows, kSmem, w);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -467,34 +540,44 @@ cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * kWarpsRows);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D, kFmt>, p);
+    return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D, kFmt, NB>, p);
+}
+
+template <int D, int kFmt>
+cudaError_t launch_rows(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, cudaStream_t s) {
+    return tile_rows == 8 ? launch<D, kFmt, 1>(p, ctas, s) : launch<D, kFmt, 2>(p, ctas, s);
 }
 
 template <int D>
-cudaError_t launch_format(const PagedRowsParams& p, uint32_t ctas, cudaStream_t s) {
+cudaError_t launch_format(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, cudaStream_t s) {
     switch (p.a.pool.format) {
-        case kBf16: return launch<D, kBf16>(p, ctas, s);
-        case kE5m2: return launch<D, kE5m2>(p, ctas, s);
-        case kInt8: return launch<D, kInt8>(p, ctas, s);
-        default: return launch<D, kE2m1>(p, ctas, s);
+        case kBf16: return launch_rows<D, kBf16>(p, tile_rows, ctas, s);
+        case kE5m2: return launch_rows<D, kE5m2>(p, tile_rows, ctas, s);
+        case kInt8: return launch_rows<D, kInt8>(p, tile_rows, ctas, s);
+        default: return launch_rows<D, kE2m1>(p, tile_rows, ctas, s);
     }
 }
 
 }  // namespace
 
+// Rows of a tile: 8 where a sequence has no more.
+inline uint32_t tile_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto) {
+    return std::min<uint64_t>((uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads), rows_upto) <= 8 ? 8 : 16;
+}
+
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p) {
-    const uint32_t group = a.q_heads / a.pool.kv_heads, d = a.pool.head_dim;
-    p.row_tiles = (uint32_t)((std::min<uint64_t>((uint64_t)a.max_q_tokens * group, rows_upto) + 15) / 16);
+    const uint32_t group = a.q_heads / a.pool.kv_heads, d = a.pool.head_dim, tile = tile_rows(a, rows_upto);
+    p.row_tiles = (uint32_t)((std::min<uint64_t>((uint64_t)a.max_q_tokens * group, rows_upto) + tile - 1) / tile);
     const uint64_t units = (uint64_t)a.batch * a.pool.kv_heads * p.row_tiles;
     const uint32_t slots = (a.pool.format == kBf16 ? 2048 : 4096) / d;
     uint64_t most = a.kv_tokens;
-    if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (16 + group - 1) / group + 2 * slots);
+    if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (tile + group - 1) / group + 2 * slots);
     p.splits = attention_rows_splits(units, most, slots, 16, d);
-    p.bytes = attention_rows_bytes(units, p.splits, 16, d);
+    p.bytes = attention_rows_bytes(units, p.splits, tile, d);
     return units * p.splits <= 0x7FFFFFFFull;
 }
 
@@ -512,7 +595,8 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.counters = reinterpret_cast<uint32_t*>(workspace);
     p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
     const uint32_t ctas = a.batch * a.pool.kv_heads * plan.row_tiles * plan.splits;
-    return a.pool.head_dim == 64 ? launch_format<64>(p, ctas, s) : launch_format<128>(p, ctas, s);
+    return a.pool.head_dim == 64 ? launch_format<64>(p, tile_rows(a, rows_upto), ctas, s)
+                                    : launch_format<128>(p, tile_rows(a, rows_upto), ctas, s);
 }
 
 }  // namespace splitzip
