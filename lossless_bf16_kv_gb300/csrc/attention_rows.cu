@@ -399,7 +399,7 @@ cudaError_t launch_tile(const RowsParams& p, uint32_t tile_rows, uint32_t ctas, 
 
 }  // namespace
 
-uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, uint32_t tile_rows, uint32_t head_dim) {
+uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, uint32_t tile_rows, uint32_t head_dim, uint32_t ctas) {
     // As many splits as run at once, of which each warp has a tile of slots (512 slots of
     // 8 units: 5.8 us with 8 splits, 6.6 with 4).  Three 16-row CTAs fit an SM, but a
     // cluster lies within one of the GPU's groups of SMs, and fewer of the large ones run
@@ -410,7 +410,7 @@ uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, ui
     static constexpr uint64_t kAtOnce[9] = {0, 3 * kSms, 228, 148, 110, 87, 74, 59, 51};
     const uint64_t tiles = (most + kWarpsRows * slots - 1) / (kWarpsRows * slots);
     uint64_t splits = 8;
-    while (splits > 1 && (splits > tiles || units > (tile_rows == 16 ? kAtOnce[splits] : 256 / splits))) splits--;
+    while (splits > 1 && (splits > tiles || units > (tile_rows == 16 ? kAtOnce[splits] * ctas / kCtasPerSm : 256 / splits))) splits--;
     // Up to eight splits are one cluster.  More are clusters of eight, of which the last
     // one joins all: that costs as much as a few tiles, more with more to join.  8 units,
     // 16-row tiles: 4096 slots of 64 take 7.5 us with 8 splits and 8.6 with 32, 8192 of

@@ -145,8 +145,9 @@ __device__ __forceinline__ void join_rows(float* os, RowsShared<kTileRows>& sh, 
     }
 }
 
-// Splits of each row tile, of `units` row tiles that see up to `most` slots each.
-uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, uint32_t tile_rows, uint32_t head_dim);
+// Splits of each row tile, of `units` row tiles that see up to `most` slots each; `ctas`
+// of the kernel's fit an SM.
+uint32_t attention_rows_splits(uint64_t units, uint64_t most, uint32_t slots, uint32_t tile_rows, uint32_t head_dim, uint32_t ctas = kCtasPerSm);
 // Bytes of workspace that they need.
 size_t attention_rows_bytes(uint64_t units, uint32_t splits, uint32_t tile_rows, uint32_t head_dim);
 

@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
                 sh.row[t][half][r] = __uint_as_float(top);
                 named_sync(pair_bar, 64);
                 const float power = row_power(max(top, __float_as_uint(sh.row[t][half ^ 1][r])));
-                scale /= power;
+                scale = fmaxf(scale / power, 0x1p-126f);  // never 0, which -infinity is multiplied by
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {
                     uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};

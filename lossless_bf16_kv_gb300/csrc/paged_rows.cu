@@ -12,47 +12,73 @@
 // exponentials and registers that 16 rows take.  P^T comes out of S^T by a
 // transposition of 8 x 8 blocks between registers (movmatrix).
 //
-// Pages hold at least 16 slots, and a warp's tiles 32 or 64 (16 of BF16 at head_dim
-// 128), so a tile is a few runs of 16 slots of one page each.  The lanes hold the
-// page numbers of a tile's runs from one tile ahead, so that no copy waits for the
-// table.  A run that no query sees is not looked up (its page may have been given
-// away) and is copied from the pool's first page, masked.
+// A CTA's warps share a ring of slot tiles (64 slots, 128 at head_dim 64, a quarter of
+// them each warp's), which TMA fills page by page, swizzled as ldmatrix reads them.
+// The warps take turns at loading the next tile, so the cost of that is shared, and
+// each has the page numbers of its next turn four tiles ahead.  What no query sees is
+// not looked up (its page may have been given away): it is loaded from behind the
+// pool's last page, as zeros.
 //
 // Quantised codes become FP16 in registers on their way from shared memory to the
-// products: codes by a byte permute and a subtraction (INT8) or a conversion
-// (E2M1), then a multiplication by the block's power of two, all exact.  The powers
-// are made FP16 once per tile and slot by one lane, and laid out as the fragments
-// need them: a key's four side by side, the values' of neighbouring slots side by
-// side.
+// products, exactly: codes by a byte permute and a subtraction (INT8) or a conversion
+// (E2M1).  The keys' powers multiply the scores' sums over a block, in 32 bits.  The
+// values' multiply the codes, as their slots are what is summed over: they are made
+// FP16 once per tile and slot by one lane, those of neighbouring slots side by side.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "attention_rows.cuh"
 #include "pages.cuh"
+#include "tcgen.cuh"
+#include "tensor_map.h"
 
 namespace splitzip {
 namespace {
 
 struct PagedRowsParams {
     splitzip_paged_attention_args a;
+    CUtensorMap kmap, vmap;
     uint32_t group, page_shift, row_tiles, splits, cluster;
-    uint32_t rows_upto;  // only sequences with no more query rows than this
+    uint32_t rows_upto;   // only sequences with no more query rows than this
+    uint32_t box, boxes;  // slots to a copy, and copies to a tile
+    uint32_t bulk_exps;   // a page's exponent bytes of a head are contiguous, in multiples of 16 bytes
     uint32_t* counters;
     float* partials;
+    uint32_t* status;
+    uint32_t wait_limit;
+    uint32_t test_cta, test_tile;  // a copy that a test has left out
 };
 
 template <int D, int kFmt>
 struct PagedShape {
     static constexpr int kRow = kRowBytes<D, kFmt>;
-    static constexpr int kSlots = kFmt == kBf16 ? 2048 / D : 4096 / D;  // slots per warp tile
-    static constexpr int kTile = kSlots * kRow;                         // bytes of its keys, and of its values
-    static constexpr int kStages = kFmt == kE2m1 ? 4 : 2;
-    static constexpr int kExps = kQuantised<kFmt> ? 4 * kSlots : 0;     // bytes of its keys' exponents, and of its values'
-    static constexpr int kStage = 2 * (kTile + kExps);
-    static constexpr int kScales = kQuantised<kFmt> ? 16 * kSlots : 0;  // of the powers as FP16, keys' and values'
-    static constexpr int kRing = kWarpsRows * (kStages * kStage + kScales);
-    static_assert(kRing >= kWarpsRows * 16 * D * 4, "partial results take the place of the ring");
+    static constexpr int kPart = 2048 / D;                   // slots of a tile that a warp takes
+    static constexpr int kSlots = kWarpsRows * kPart;        // slots per tile
+    static constexpr int kTile = kSlots * kRow;              // bytes of its keys, and of its values
+    static constexpr int kStages = kFmt == kBf16 ? 2 : kFmt == kE2m1 ? 4 : 3;
+    static constexpr int kExps = kQuantised<kFmt> ? 4 * kSlots : 0;  // bytes of its keys' exponents, and of its values'
+    // Shared memory: the rings of tiles and of exponents, the values' powers, queries.
+    static constexpr int kAtExps = kStages * 2 * kTile, kAtPowers = kAtExps + kStages * 2 * kExps;
+    static constexpr int kAtQueries = kAtPowers + 2 * kExps;
+    static_assert(kTile % 1024 == 0, "swizzled tiles");
 };
+template <int kStages, int kTileRows>
+struct PagedRowsShared {
+    uint64_t full[kStages], empty[kStages];
+    WaitLimit wait;
+    uint32_t issued;  // tiles whose copies have been issued
+    float scale[kTileRows];
+    RowsShared<kTileRows> join;
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile as TMA writes it: rows of 256
+// bytes as two blocks of 128.
+template <int kRow, int kSlots>
+__device__ __forceinline__ uint32_t tile_at(uint32_t r, uint32_t c) {
+    if (kRow == 256) return (c >> 3) * (kSlots * 128) + chunk_at<128>(r, c & 7u);
+    return chunk_at<kRow>(r, c);
+}
 
 // Position of a head's value d in the products' contraction index, such that the four
 // consecutive bytes of a fragment's row that a lane holds are the indices that the
@@ -65,6 +91,9 @@ __device__ __forceinline__ uint32_t place(uint32_t d) {
     return (d & ~15u) + e5m2_place(d & 15u);
 }
 
+// Whether one of four exponent bytes is 255.
+__device__ __forceinline__ bool has_nan(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x01010101u) & x & 0x80808080u) != 0; }
+
 // The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
@@ -72,18 +101,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
+// CTAs to an SM, by registers and shared memory.
+template <int kFmt, int NB>
+constexpr int kPagedCtas = kWide<kFmt> && NB == 1 ? 4 : 3;
+
 // NB: blocks of 8 query rows.
 template <int D, int kFmt, int NB>
-__global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
+__global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
     using S = PagedShape<D, kFmt>;
     constexpr bool kHalf = kWide<kFmt>;  // operands FP16, else BF16
     constexpr int kTileRows = 8 * NB;
+    constexpr bool kBlockSums = kQuantised<kFmt> && !(kFmt == kE2m1 && D == 64);  // a step's 16 values are of one block
     constexpr int KS = D / 16;           // steps of the scores, and 16-value blocks of the output
-    constexpr int PS = S::kSlots / 16;   // 16-slot blocks of the scores, steps of the output, runs of one page each
+    constexpr int PS = S::kPart / 16;    // 16-slot blocks of a warp's scores, steps of its output
     constexpr int kChunks = S::kRow / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_scale[kTileRows];
-    __shared__ RowsShared<kTileRows> sh;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* qs = smem + S::kAtQueries;
+    auto& sh = *reinterpret_cast<PagedRowsShared<S::kStages, kTileRows>*>(qs + kTileRows * D * 2);
     const splitzip_paged_attention_args& a = p.a;
     const splitzip_pool& pool = a.pool;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -100,89 +134,81 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
     const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
     const uint32_t j1 = (uint32_t)((uint64_t)tiles.count * (split + 1) / p.splits);
 
-    uint8_t* ring = smem + warp * (S::kStages * S::kStage + S::kScales);
-    uint8_t* scales = ring + S::kStages * S::kStage;  // keys' [slot][block], then values' [block][slot]
-    uint8_t* qs = smem + S::kRing;
-    constexpr int kElem = kFmt == kBf16 ? 2 : 1;
-    const uint8_t* kbase = static_cast<const uint8_t*>(pool.k.data) + h * pool.k.stride_h * kElem;
-    const uint8_t* vbase = static_cast<const uint8_t*>(pool.v.data) + h * pool.v.stride_h * kElem;
-    const uint8_t* kexps = pool.k.exponents + h * pool.k.exp_stride_h;
-    const uint8_t* vexps = pool.v.exponents + h * pool.v.exp_stride_h;
+    uint8_t* powers = smem + S::kAtPowers + warp * (8 * S::kPart);  // of this warp's values, [block][slot]
+    volatile WaitLimit* wait = &sh.wait;
     const int32_t* table = a.table + (uint64_t)b * a.table_width;
-    const uint32_t in_page = pool.page_tokens - 1;
+    const uint32_t in_page = pool.page_tokens - 1, count = j1 - j0;
 
-    // Lane i < PS: the page of the tile's run i.  Slots past the last one in use are
-    // taken as copies of it.
+    // Lane i < boxes: the page of copy i of the CTA's n-th tile; `pages` where no query sees it.
     bool lost = false;  // a page that a query sees is outside the pool
-    auto look_up = [&](uint32_t j) -> uint32_t {
-        if (lane >= PS || j >= j1) return 0;
-        const int32_t s = (int32_t)(tiles.tile(j) * S::kSlots + 16 * lane);
-        // The run's last slot is behind the start of the first query's window, or a sink.
-        if (s > p1 || !((int64_t)s + 15 > (int64_t)p0 - (int64_t)mask.window || s < mask.sinks)) return 0;
+    auto look_up = [&](uint32_t n) -> uint32_t {
+        if (lane >= p.boxes || n >= count) return pool.pages;
+        const int32_t s = (int32_t)(tiles.tile(j0 + n) * S::kSlots + p.box * lane);
+        // The last slot is behind the start of the first query's window, or a sink.
+        if (s > p1 || !((int64_t)s + p.box > (int64_t)p0 - (int64_t)mask.window + 1 || s < mask.sinks)) return pool.pages;
         const uint32_t page = (uint32_t)table[s >> p.page_shift];
         if (page < pool.pages) return page;
         lost = true;
-        return 0;
+        return pool.pages;
     };
-    // A lane copies one 16-byte chunk of every kStep-th row of a tile.
-    constexpr int kStep = 32 / kChunks;
-    const uint32_t lr = lane / kChunks, lc = lane % kChunks;
-    const int64_t kst = pool.k.stride_t * kElem, vst = pool.v.stride_t * kElem;
-    auto load = [&](uint32_t j, uint32_t stage, uint32_t pages) {
-        if (j < j1) {
-            const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
-            uint8_t* dk = ring + stage * S::kStage;
-            const bool full = s0 + S::kSlots <= mask.n;
+    // The whole warp: the n-th tile into its stage, which is free.
+    auto load = [&](uint32_t n, uint32_t page) {
+        const uint32_t stage = n % S::kStages, s0 = tiles.tile(j0 + n) * S::kSlots;
+        const bool bulk = kQuantised<kFmt> && p.bulk_exps;
+        uint64_t* full = &sh.full[stage];
+        uint8_t* dk = smem + stage * (2 * S::kTile);
+        uint8_t* de = smem + S::kAtExps + stage * (2 * S::kExps);
+        const uint8_t* kexps = pool.k.exponents + h * pool.k.exp_stride_h;
+        const uint8_t* vexps = pool.v.exponents + h * pool.v.exp_stride_h;
+        if (lane == 0) {
+            sh.issued = n + 1;
+            mbar_arrive_expect_tx(full, 2 * S::kTile + (bulk ? 2 * S::kExps : 0));
+        }
+        __syncwarp();
+        if (lane < p.boxes && !(blockIdx.x == p.test_cta && n == p.test_tile)) {
+            const uint32_t first = p.box * lane;
+            const int32_t at = (int32_t)((s0 + first) & in_page);
+            constexpr int kBlocks = S::kRow == 256 ? 2 : 1, kBlockRow = S::kRow / kBlocks;
 #pragma unroll
-            for (int i = 0; i < PS; i++) {
-                const int64_t page = __shfl_sync(0xFFFFFFFFu, pages, i);
-                const uint8_t* k = kbase + page * pool.k.stride_p * kElem + 16 * lc;
-                const uint8_t* v = vbase + page * pool.v.stride_p * kElem + 16 * lc;
-                const int32_t first = s0 + 16 * i;
-                if (full) {
-                    const uint32_t at = ((uint32_t)first & in_page) + lr;
-                    k += at * kst;
-                    v += at * vst;
-#pragma unroll
-                    for (int x = 0; x < 16 / kStep; x++) {
-                        cp_async16(dk + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), k);
-                        cp_async16(dk + S::kTile + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), v);
-                        k += kStep * kst;
-                        v += kStep * vst;
-                    }
-                } else {
-#pragma unroll 1
-                    for (int x = 0; x < 16 / kStep; x++) {
-                        const uint32_t at = (uint32_t)min(first + x * kStep + (int32_t)lr, mask.n - 1) & in_page;
-                        cp_async16(dk + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), k + at * kst);
-                        cp_async16(dk + S::kTile + chunk_at<S::kRow>(16 * i + x * kStep + lr, lc), v + at * vst);
-                    }
-                }
+            for (int x = 0; x < kBlocks; x++) {
+                tma_load4(dk + x * (S::kTile / 2) + first * kBlockRow, &p.kmap, 64 * x, at, (int32_t)h, (int32_t)page, full);
+                tma_load4(dk + S::kTile + x * (S::kTile / 2) + first * kBlockRow, &p.vmap, 64 * x, at, (int32_t)h, (int32_t)page, full);
             }
-            if constexpr (kQuantised<kFmt>) {
-                uint8_t* de = dk + 2 * S::kTile;
-#pragma unroll
-                for (int i = 0; i < S::kSlots / 32; i++) {
-                    const int32_t s = s0 + 32 * i + (int32_t)lane;
-                    const int64_t page = __shfl_sync(0xFFFFFFFFu, pages, 2 * i + (lane >> 4));
-                    const uint32_t at = (uint32_t)(full ? s : min(s, mask.n - 1)) & in_page;
-                    cp_async4(de + 4 * (32 * i + lane), kexps + page * pool.k.exp_stride_p + at * pool.k.exp_stride_t);
-                    cp_async4(de + S::kExps + 4 * (32 * i + lane), vexps + page * pool.v.exp_stride_p + at * pool.v.exp_stride_t);
-                }
+            if (bulk) {  // where no query sees them, any page's: they multiply zeros
+                const int64_t from = page < pool.pages ? page : 0;
+                bulk_load(de + 4 * first, kexps + from * pool.k.exp_stride_p + 4 * at, 4 * p.box, full);
+                bulk_load(de + S::kExps + 4 * first, vexps + from * pool.v.exp_stride_p + 4 * at, 4 * p.box, full);
             }
         }
-        cp_async_commit();
+        if (kQuantised<kFmt> && !bulk) {  // part of the phase, as the copies' bytes are
+#pragma unroll 1
+            for (uint32_t r = lane; r < S::kSlots; r += 32) {
+                const uint32_t at = (s0 + r) & in_page, from = __shfl_sync(0xFFFFFFFFu, page, r / p.box);
+                const int64_t some = from < pool.pages ? from : 0;
+                cp_async4(de + 4 * r, kexps + some * pool.k.exp_stride_p + at * pool.k.exp_stride_t);
+                cp_async4(de + S::kExps + 4 * r, vexps + some * pool.v.exp_stride_p + at * pool.v.exp_stride_t);
+            }
+            cp_async_arrive(full);
+        }
     };
-    uint32_t ahead = j0 + warp;  // the next tile to be copied, and its pages
-    uint32_t pages = look_up(ahead);
-    auto advance = [&](uint32_t stage) {
-        const uint32_t now = pages, j = ahead;
-        ahead += kWarpsRows;
-        pages = look_up(ahead);
-        load(j, stage, now);
-    };
+    uint32_t mine = S::kStages - 1 + warp;  // the next tile that this warp loads, and its pages
+    uint32_t pages = look_up(mine);
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t arrivals = kQuantised<kFmt> && !p.bulk_exps ? 33 : 1;
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; i++) advance(i);
+            for (int i = 0; i < S::kStages; i++) {
+                mbar_init(&sh.full[i], arrivals);
+                mbar_init(&sh.empty[i], kWarpsRows);
+            }
+            sh.wait.given_up = sh.issued = 0;
+            sh.wait.limit = p.wait_limit;
+            fence_mbar_init();
+            fence_async_proxy();
+        }
+        __syncwarp();
+        for (uint32_t n = 0; n < min(count, (uint32_t)S::kStages - 1); n++) load(n, look_up(n));
+    }
 
     // Queries: one warp per row, as FP16 of the scaled row where the cache is not BF16.
     for (uint32_t r = warp; r < kTileRows; r += kWarpsRows) {
@@ -211,7 +237,9 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             if (kHalf) w = pack2<true>(__uint_as_float(v[i] << 16) * power, __uint_as_float(v[i] & 0xFFFF0000u) * power);
             *reinterpret_cast<uint32_t*>(qs + chunk_at<2 * D>(r, d / 8) + 2 * (d % 8)) = w;
         }
-        if (lane == 0) s_scale[r] = a.scale * kLog2e / power;
+        // Never 0, which -infinity is multiplied by: such queries' scores are all 0 (the products
+        // are below 2^25).
+        if (lane == 0) sh.scale[r] = kHalf ? fmaxf(a.scale * kLog2e / power, 0x1p-126f) : a.scale * kLog2e;
     }
     __syncthreads();
 
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
         for (int x = 0; x < 2; x++) {
             const uint32_t r = 8 * y + 2 * (lane & 3) + x;
             pos[y][x] = r0 + r < r1 ? mask.pos((r0 + r) / p.group) : -1;
-            scale[y][x] = s_scale[r];
+            scale[y][x] = sh.scale[r];
             m[y][x] = -INFINITY;
             l[y][x] = 0.0f;
         }
@@ -246,34 +274,25 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             qf[k][y][0] = r[0], qf[k][y][1] = r[1], qf[k + 1][y][0] = r[2], qf[k + 1][y][1] = r[3];
         }
     bool odd = false;  // a value of a partly visible tile was infinite or NaN
-    uint32_t stage = 0;
-    for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();
-        advance(stage == 0 ? S::kStages - 1 : stage - 1);
-        const uint8_t* tile = ring + stage * S::kStage;
-        const uint32_t ks = smem_addr(tile), vs = ks + S::kTile;
-        stage = stage == S::kStages - 1 ? 0 : stage + 1;
-        const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
-        const bool whole = p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kSlots - 1);
-
+    // A warp's part of a tile: keys at ks, values at vs, exponent bytes at e, the part's first row and slot.
+    // kWhole: every query sees all of it.
+    const auto walk = [&](auto is_whole, uint32_t ks, uint32_t vs, const uint32_t* e, uint32_t part, int32_t s0) {
+        constexpr bool kWhole = decltype(is_whole)::value;
+        bool nan = false;  // a key's block is NaN
         if constexpr (kQuantised<kFmt>) {
-            const uint32_t* e = reinterpret_cast<const uint32_t*>(tile + 2 * S::kTile);
 #pragma unroll
-            for (int i = 0; i < S::kSlots / 32; i++) {
-                const uint32_t s = 32 * i + lane;
-                uint32_t w[2][2];
-#pragma unroll
-                for (int x = 0; x < 2; x++) {
-                    const uint32_t v = e[x * S::kSlots + s];
-                    w[x][0] = pack2<true>(block_scale(v & 255u), block_scale(v >> 8 & 255u));
-                    w[x][1] = pack2<true>(block_scale(v >> 16 & 255u), block_scale(v >> 24));
+            for (uint32_t r = lane; r < 2 * S::kPart; r += 32) {  // the keys', then the values'
+                const uint32_t s = r & (S::kPart - 1), x = e[r < S::kPart ? s : S::kSlots + s];
+                nan |= r < S::kPart && has_nan(x);
+                const uint32_t lo = pack2<true>(block_scale(x & 255u), block_scale(x >> 8 & 255u));
+                const uint32_t hi = pack2<true>(block_scale(x >> 16 & 255u), block_scale(x >> 24));
+                if (r >= S::kPart) {
+                    uint16_t* to = reinterpret_cast<uint16_t*>(powers) + s;
+                    to[0] = (uint16_t)lo, to[S::kPart] = (uint16_t)(lo >> 16);
+                    to[2 * S::kPart] = (uint16_t)hi, to[3 * S::kPart] = (uint16_t)(hi >> 16);
                 }
-                *reinterpret_cast<uint2*>(scales + 8 * s) = make_uint2(w[0][0], w[0][1]);
-                uint16_t* to = reinterpret_cast<uint16_t*>(scales + 8 * S::kSlots) + s;
-                to[0] = (uint16_t)w[1][0], to[S::kSlots] = (uint16_t)(w[1][0] >> 16);
-                to[2 * S::kSlots] = (uint16_t)w[1][1], to[3 * S::kSlots] = (uint16_t)(w[1][1] >> 16);
             }
+            nan = __any_sync(0xFFFFFFFFu, nan);
             __syncwarp();
         }
         // Scores of slots 16 i + lane / 4 and that + 8 (x >> 1) for this thread's rows (x & 1).
@@ -284,29 +303,27 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             for (int y = 0; y < NB; y++)
 #pragma unroll
                 for (int x = 0; x < 4; x++) sc[i][y][x] = 0.0f;
-            const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                const uint32_t f[4] = {a0, a1, a2, a3};
-#pragma unroll
-                for (int y = 0; y < NB; y++) mma16816<kHalf>(sc[i][y], f, qf[k][y][0], qf[k][y][1]);
-            };
             if constexpr (kFmt == kBf16) {
 #pragma unroll
                 for (int k = 0; k < KS; k++) {
                     uint32_t r[4];
-                    ldmatrix4(r, ks + chunk_at<S::kRow>(16 * i + (lane & 15), 2 * k + (lane >> 4)));
-                    product(k, r[0], r[1], r[2], r[3]);
+                    ldmatrix4(r, ks + tile_at<S::kRow, S::kSlots>(part + 16 * i + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int y = 0; y < NB; y++) mma16816<kHalf>(sc[i][y], r, qf[k][y][0], qf[k][y][1]);
                 }
             } else {
-                uint2 power[2];  // of the two slots
-                if constexpr (kQuantised<kFmt>)
-#pragma unroll
-                    for (int x = 0; x < 2; x++) power[x] = *reinterpret_cast<const uint2*>(scales + 8 * (16 * i + 8 * x + lane / 4));
+                uint32_t power[2] = {0, 0};  // the two slots' exponent bytes
+                if constexpr (kQuantised<kFmt>) power[0] = e[16 * i + lane / 4], power[1] = e[16 * i + 8 + lane / 4];
+                float sum[NB][4];  // over a block
 #pragma unroll
                 for (int c = 0; c < kChunks; c += 2) {
-                    uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block
-                    ldmatrix4(r, ks + chunk_at<S::kRow>(16 * i + (lane & 15), c + (lane >> 4)));
+                    uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block of slots
+                    ldmatrix4(r, ks + chunk_at<S::kRow>(part + 16 * i + (lane & 15), c + (lane >> 4)));
 #pragma unroll
                     for (int u = 0; u < 2; u++) {
+                        const int block = kBlockSums ? (c + u) * (D / kChunks) / (D / 4) : 0;
+                        const bool first = kBlockSums && (c + u) * (D / kChunks) % (D / 4) == 0;
+                        const bool last = kBlockSums && (c + u + 1) * (D / kChunks) % (D / 4) == 0;
                         uint32_t w[2][4];
 #pragma unroll
                         for (int x = 0; x < 2; x++) {
@@ -314,24 +331,47 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
                             if constexpr (kFmt == kE5m2) {
                                 w[x][0] = e5m2_01(v), w[x][1] = e5m2_23(v);
                             } else if constexpr (kFmt == kInt8) {
-                                const uint32_t f = twice(power[x], (c + u) * 16 / (D / 4)), z = int8_bias(v);
-                                w[x][0] = mul_half2(int8_pair<kInt8_01>(z), f), w[x][1] = mul_half2(int8_pair<kInt8_23>(z), f);
+                                const uint32_t z = int8_bias(v);
+                                w[x][0] = int8_pair<kInt8_01>(z), w[x][1] = int8_pair<kInt8_23>(z);
                             } else {
-                                // A lane's eight values are one block's: its half of the 32, or all of them.
-                                const uint32_t f = D == 128 ? twice(power[x], c + u)
-                                                            : prmt(u ? power[x].y : power[x].x, 0u, lane & 2 ? 0x3232u : 0x1010u);
                                 e2m1_pairs(w[x], v);
+                                if constexpr (!kBlockSums) {
+                                    // The 16 values of a step are of two blocks, a lane's eight of one.
+                                    const float f = block_scale(power[x] >> (16 * u + ((lane & 2) << 2)) & 255u);
 #pragma unroll
-                                for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
+                                    for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], pack2<true>(f, f));
+                                }
                             }
                         }
-                        if constexpr (kFmt == kE2m1) {
-                            product(2 * (c + u), w[0][0], w[1][0], w[0][1], w[1][1]);
-                            product(2 * (c + u) + 1, w[0][2], w[1][2], w[0][3], w[1][3]);
-                        } else {
-                            product(c + u, w[0][0], w[1][0], w[0][1], w[1][1]);
+#pragma unroll
+                        for (int n = 0; n < (kFmt == kE2m1 ? 2 : 1); n++) {
+                            const int k = kFmt == kE2m1 ? 2 * (c + u) + n : c + u;
+                            const uint32_t f[4] = {w[0][2 * n], w[1][2 * n], w[0][2 * n + 1], w[1][2 * n + 1]};
+#pragma unroll
+                            for (int y = 0; y < NB; y++) {
+                                if (!kBlockSums) mma16816<true>(sc[i][y], f, qf[k][y][0], qf[k][y][1]);
+                                else if (first && n == 0) mma16816_zero(sum[y], f, qf[k][y][0], qf[k][y][1]);
+                                else mma16816<true>(sum[y], f, qf[k][y][0], qf[k][y][1]);
+                            }
+                        }
+                        if (last) {
+                            float s[2];
+#pragma unroll
+                            for (int x = 0; x < 2; x++)
+                                s[x] = __uint_as_float((block < 3 ? power[x] << (23 - 8 * block) : power[x] >> 1) & 0x7F800000u);
+#pragma unroll
+                            for (int y = 0; y < NB; y++)
+#pragma unroll
+                                for (int x = 0; x < 4; x++) sc[i][y][x] = block ? fmaf(s[x >> 1], sum[y][x], sc[i][y][x]) : s[x >> 1] * sum[y][x];
                         }
                     }
+                }
+                if (kQuantised<kFmt> && nan) {  // a block of NaN makes its key's scores NaN
+#pragma unroll
+                    for (int y = 0; y < NB; y++)
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+                            if (has_nan(power[x >> 1])) sc[i][y][x] = __int_as_float(0x7FC00000);
                 }
             }
         }
@@ -340,24 +380,19 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
 #pragma unroll
         for (int y = 0; y < NB; y++)
 #pragma unroll
-            for (int x = 0; x < 2; x++) top[y][x] = m[y][x] + kLift<kHalf>;
-#pragma unroll
-        for (int y = 0; y < NB; y++) {
-#pragma unroll
-            for (int i = 0; i < PS; i++)
-#pragma unroll
-                for (int x = 0; x < 4; x++) {
-                    float v = sc[i][y][x] * scale[y][x & 1];
-                    if (!whole && !mask.sees(pos[y][x & 1], s0 + 16 * i + 8 * (x >> 1) + (int32_t)(lane / 4))) v = -INFINITY;
-                    sc[i][y][x] = v;
-                    top[y][x & 1] = fmaxf(top[y][x & 1], v);
-                }
-#pragma unroll
             for (int x = 0; x < 2; x++) {
-                top[y][x] -= kLift<kHalf>;
+                float now = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < PS; i++)
+#pragma unroll
+                    for (int z = 0; z < 4; z += 2) {
+                        float& v = sc[i][y][x + z];
+                        if (!kWhole && !mask.sees(pos[y][x], s0 + 16 * i + 4 * z + (int32_t)(lane / 4))) v = -INFINITY;
+                        now = fmaxf(now, v);
+                    }
+                top[y][x] = fmaxf(now * scale[y][x] - kLift<kHalf>, m[y][x]);
                 more |= top[y][x] != m[y][x];
             }
-        }
         if (__any_sync(0xFFFFFFFFu, more)) {  // more and more rarely
 #pragma unroll
             for (int y = 0; y < NB; y++)
@@ -385,7 +420,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
                 float e[4];
 #pragma unroll
                 for (int x = 0; x < 4; x++) {
-                    e[x] = exp2_approx(sc[i][y][x] - use[x & 1]);
+                    e[x] = exp2_approx(fmaf(sc[i][y][x], scale[y][x & 1], -use[x & 1]));
                     l[y][x & 1] += e[x];
                 }
                 // p in 16 bits for the product: a relative error of up to 2^-8 (BF16) or
@@ -400,7 +435,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             // Values of slots 2 (lane & 3) and the next, and of those + 8, as rows of V^T.
             const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                 uint32_t f[4] = {a0, a1, a2, a3};
-                if (!whole) {  // 0 x infinity is not 0: keep such values out of the product
+                if constexpr (!kWhole) {  // 0 x infinity is not 0: keep such values out of the product
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
                         const uint32_t v = finite_or_zero<kHalf>(f[x]);
@@ -414,7 +449,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
                 uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block, transposed
-                ldmatrix4_trans(r, vs + chunk_at<S::kRow>(16 * i + (lane & 15), c + (lane >> 4)));
+                ldmatrix4_trans(r, vs + tile_at<S::kRow, S::kSlots>(part + 16 * i + (lane & 15), c + (lane >> 4)));
                 if constexpr (kFmt == kBf16) {
                     product(c / 2, r[0], r[2], r[1], r[3]);
                 } else {
@@ -427,7 +462,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
                             uint32_t f = 0;
                             if constexpr (kQuantised<kFmt>) {
                                 const uint32_t block = kFmt == kInt8 ? (c + u) * 16 / (D / 4) : D == 128 ? c + u : 2 * (c + u) + (lane >> 4);
-                                f = *reinterpret_cast<const uint32_t*>(scales + 8 * S::kSlots + 2 * (block * S::kSlots + 16 * i + 8 * x + 2 * (lane & 3)));
+                                f = *reinterpret_cast<const uint32_t*>(powers + 2 * (block * S::kPart + 16 * i + 8 * x + 2 * (lane & 3)));
                             }
                             if constexpr (kFmt == kE5m2) {
                                 w[x][0] = e5m2_02(v), w[x][1] = e5m2_13(v);
@@ -453,9 +488,36 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
                 }
             }
         }
-        if constexpr (kQuantised<kFmt>) __syncwarp();  // the powers have been read
+    };
+    bool ready = true;
+    uint32_t stage = 0, turn = 0;
+    for (uint32_t n = 0; n < count; n++) {
+        ready = mbar_wait_bounded(&sh.full[stage], turn, wait);
+        if (!ready) break;
+        const uint32_t ks = smem_addr(smem + stage * (2 * S::kTile)), vs = ks + S::kTile;
+        // This warp's part of the tile: from its row `part` on.
+        const uint32_t part = warp * S::kPart;
+        const int32_t s0 = (int32_t)(tiles.tile(j0 + n) * S::kSlots + part);
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(smem + S::kAtExps + stage * (2 * S::kExps)) + part;
+        // Nothing to do for slots behind the last query, or between sinks and windows.
+        const bool seen = s0 <= p1 && ((int64_t)s0 + S::kPart > (int64_t)p0 - (int64_t)mask.window + 1 || s0 < mask.sinks);
+        if (p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kPart - 1)) walk(std::true_type(), ks, vs, e, part, s0);
+        else if (seen) walk(std::false_type(), ks, vs, e, part, s0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (++stage == S::kStages) stage = 0, turn ^= 1;
+        // The tile that takes the place of the one before this.
+        const uint32_t next = n + S::kStages - 1;
+        if (next == mine) {
+            if (next < count) {
+                if (n) ready = mbar_wait_bounded(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1, wait);
+                if (!ready) break;
+                load(next, pages);
+            }
+            mine += kWarpsRows;
+            pages = look_up(mine);
+        }
     }
-    cp_async_wait<0>();
     // The head's value of o[k][..][x].
     auto column = [&](int k, int x) {
         const int i = (int)(lane / 4), u = x >> 1;
@@ -464,23 +526,25 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
     if (__any_sync(0xFFFFFFFFu, odd)) {
         // The infinite and NaN values of partly visible tiles go to the rows that
         // see them: whatever their (positive) weight, the sum takes their value.
-        for (uint32_t j = j0 + warp; j < j1; j += kWarpsRows) {
-            const int32_t s0 = (int32_t)(tiles.tile(j) * S::kSlots);
-            if (p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kSlots - 1)) continue;
-            for (int32_t s = s0; s < min(s0 + S::kSlots, mask.n); s++) {
+        for (uint32_t n = 0; n < count; n++) {
+            const int32_t s0 = (int32_t)(tiles.tile(j0 + n) * S::kSlots + warp * S::kPart);
+            if (p0 >= 0 && mask.all(p0, p1, s0, s0 + S::kPart - 1)) continue;
+            for (int32_t s = s0; s < min(s0 + S::kPart, mask.n); s++) {
                 if (s > p1) break;
                 const bool sinks = s < mask.sinks;
                 if (!sinks && (int64_t)s <= (int64_t)p0 - (int64_t)mask.window) continue;
                 const uint32_t page = (uint32_t)table[s >> p.page_shift];
                 if (page >= pool.pages) continue;
                 const int64_t at = (uint32_t)s & in_page;
-                const uint8_t* row = vbase + page * pool.v.stride_p * kElem + at * vst;
-                const uint8_t* exps = vexps + page * pool.v.exp_stride_p + at * pool.v.exp_stride_t;
+                constexpr int kElem = kFmt == kBf16 ? 2 : 1;
+                const uint8_t* row = static_cast<const uint8_t*>(pool.v.data) +
+                                     (h * pool.v.stride_h + page * pool.v.stride_p + at * pool.v.stride_t) * kElem;
+                const uint8_t* bytes = pool.v.exponents + h * pool.v.exp_stride_h + page * pool.v.exp_stride_p + at * pool.v.exp_stride_t;
 #pragma unroll
                 for (int k = 0; k < KS; k++)
 #pragma unroll
                     for (int x = 0; x < 4; x += 2) {
-                        const float v = page_value<D, kFmt>(row, exps, column(k, x));
+                        const float v = page_value<D, kFmt>(row, bytes, column(k, x));
                         if (isfinite(v)) continue;
 #pragma unroll
                         for (int y = 0; y < NB; y++) {
@@ -491,7 +555,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             }
         }
     }
-    lost = __any_sync(0xFFFFFFFFu, lost);
+    if (!ready && lane == 0) atomicOr(p.status, kStatusTimeout);
+    lost = __any_sync(0xFFFFFFFFu, lost) || !ready;
 
     // Join the warps: everything into shared memory (over the ring).
 #pragma unroll
@@ -501,11 +566,16 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
 #pragma unroll
             for (int i = 4; i < 32; i *= 2) l[y][x] += __shfl_xor_sync(0xFFFFFFFFu, l[y][x], i);
             if (lane < 4) {
-                sh.m[warp][8 * y + 2 * lane + x] = m[y][x];
-                sh.l[warp][8 * y + 2 * lane + x] = lost ? __int_as_float(0x7FC00000) : l[y][x];
+                sh.join.m[warp][8 * y + 2 * lane + x] = m[y][x];
+                sh.join.l[warp][8 * y + 2 * lane + x] = lost ? __int_as_float(0x7FC00000) : l[y][x];
             }
         }
-    __syncthreads();  // every warp is done with its ring
+    __syncthreads();  // every warp is done with the ring
+    if (*const_cast<volatile uint32_t*>(&sh.wait.given_up)) {  // nothing may land after this
+        for (uint32_t n = sh.issued > S::kStages ? sh.issued - S::kStages : 0; n < sh.issued; n++)
+            mbar_wait_bounded<true>(&sh.full[n % S::kStages], (n / S::kStages) & 1, wait);
+        __syncthreads();
+    }
     float* os = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int k = 0; k < KS; k++)
@@ -524,12 +594,14 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kCtasPerSm) paged_rows_kernel
             none ? make_uint2(0, 0) : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
         if (c == 0 && a.lse) a.lse[(uint64_t)hq * a.tokens + seq.row + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
-    join_rows<D, kTileRows>(os, sh, unit, split, p.splits, p.cluster, r1 - r0, p.counters, p.partials, store);
+    join_rows<D, kTileRows>(os, sh.join, unit, split, p.splits, p.cluster, r1 - r0, p.counters, p.partials, store);
 }
 
 template <int D, int kFmt, int NB>
 cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, cudaStream_t s) {
-    constexpr int kSmem = PagedShape<D, kFmt>::kRing + 8 * NB * D * 2;
+    using S = PagedShape<D, kFmt>;
+    static_assert(S::kAtExps >= kWarpsRows * 8 * NB * D * 4, "partial results take the place of the ring");
+    constexpr int kSmem = S::kAtQueries + 8 * NB * D * 2 + (int)sizeof(PagedRowsShared<S::kStages, 8 * NB>);
     Wave w;
     const cudaError_t e = launch_wave<paged_rows_kernel<D, kFmt, NB>>(32 * kWarpsRows, kSmem, w);
     if (e != cudaSuccess) return e;
@@ -573,16 +645,16 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
     const uint32_t group = a.q_heads / a.pool.kv_heads, d = a.pool.head_dim, tile = tile_rows(a, rows_upto);
     p.row_tiles = (uint32_t)((std::min<uint64_t>((uint64_t)a.max_q_tokens * group, rows_upto) + tile - 1) / tile);
     const uint64_t units = (uint64_t)a.batch * a.pool.kv_heads * p.row_tiles;
-    const uint32_t slots = (a.pool.format == kBf16 ? 2048 : 4096) / d;
+    const uint32_t slots = 2048 / d;  // of a tile that a warp takes
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (tile + group - 1) / group + 2 * slots);
-    p.splits = attention_rows_splits(units, most, slots, 16, d);
+    p.splits = attention_rows_splits(units, most, slots, 16, d, a.pool.format != kBf16 && tile == 8 ? 4 : 3);
     p.bytes = attention_rows_bytes(units, p.splits, tile, d);
     return units * p.splits <= 0x7FFFFFFFull;
 }
 
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
-                              cudaStream_t s) {
+                              const WaitTest& test, cudaStream_t s) {
     PagedRowsParams p;
     p.a = a;
     p.group = a.q_heads / a.pool.kv_heads;
@@ -592,6 +664,20 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
     p.cluster = std::min(plan.splits, 8u);
+    const splitzip_pool& pool = a.pool;
+    const uint32_t slots = kWarpsRows * 2048 / pool.head_dim;  // of a tile
+    p.box = std::min(pool.page_tokens, slots);
+    p.boxes = slots / p.box;
+    const auto bulk = [&](const splitzip_page_rows& r) {
+        return r.exp_stride_t == 4 && (uintptr_t)r.exponents % 16 == 0 && (pool.pages == 1 || r.exp_stride_p % 16 == 0) &&
+               (pool.kv_heads == 1 || r.exp_stride_h % 16 == 0);
+    };
+    p.bulk_exps = (pool.format == kInt8 || pool.format == kE2m1) && bulk(pool.k) && bulk(pool.v);
+    if (!page_map(p.kmap, pool, pool.k, p.box, true) || !page_map(p.vmap, pool, pool.v, p.box, true)) return cudaErrorInvalidValue;
+    p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
+    p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a copy's time
+    p.test_cta = test.cta;
+    p.test_tile = test.tile;
     p.counters = reinterpret_cast<uint32_t*>(workspace);
     p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
     const uint32_t ctas = a.batch * a.pool.kv_heads * plan.row_tiles * plan.splits;

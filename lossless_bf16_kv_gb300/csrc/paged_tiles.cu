@@ -49,12 +49,9 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     p.wait_limit = wait_limit(0);  // a wait lasts a few steps at most
     const splitzip_pool& pool = a.pool;
     const bool wide = pool.format != kBf16;
-    const uint32_t row = pool.format == kE2m1 ? pool.head_dim / 2 : pool.head_dim;
-    const auto rows = [&](const splitzip_page_rows& r) { return splitzip_view{r.data, r.stride_p, r.stride_t, r.stride_h}; };
     uint32_t one;
     if ((!wide && !make_map(p.qmap, a.q, 2, pool.head_dim, a.q_heads, a.tokens, 1, p.group, p.tokens, true, &one)) ||
-        !make_map(p.kmap, rows(pool.k), wide ? 1 : 2, row, pool.kv_heads, pool.page_tokens, pool.pages, 1, p.box, false, &one) ||
-        !make_map(p.vmap, rows(pool.v), wide ? 1 : 2, row, pool.kv_heads, pool.page_tokens, pool.pages, 1, p.box, false, &one))
+        !page_map(p.kmap, pool, pool.k, p.box, false) || !page_map(p.vmap, pool, pool.v, p.box, false))
         return cudaErrorInvalidValue;
     const uint32_t ctas = plan.row_tiles * pool.kv_heads * plan.splits;
     if (pool.head_dim == 64) return is_twin(a) ? launch_paged_64_twin(p, ctas, s) : launch_paged_64(p, ctas, s);

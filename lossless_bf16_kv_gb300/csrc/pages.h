@@ -25,7 +25,7 @@ struct PagedPlan {
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p);
 bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from, PagedPlan& p);
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& p, void* workspace,
-                              cudaStream_t s);
+                              const WaitTest& test, cudaStream_t s);
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, const PagedPlan& p, void* workspace,
                                cudaStream_t s);
 
