@@ -91,8 +91,16 @@ __device__ __forceinline__ uint32_t place(uint32_t d) {
     return (d & ~15u) + e5m2_place(d & 15u);
 }
 
+// 2^(e - 127) for exponent byte kByte of four; infinity for 255.
+template <int kByte>
+__device__ __forceinline__ float power_of(uint32_t x) {
+    return __uint_as_float((kByte < 3 ? x << (23 - 8 * kByte) : x >> 1) & 0x7F800000u);
+}
 // Whether one of four exponent bytes is 255.
 __device__ __forceinline__ bool has_nan(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x01010101u) & x & 0x80808080u) != 0; }
+
+// Whether one of them stands for more than 2^5.
+__device__ __forceinline__ bool above_5(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x7B7B7B7Bu) & x & 0x80808080u) != 0; }
 
 // The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -278,22 +286,28 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
     // kWhole: every query sees all of it.
     const auto walk = [&](auto is_whole, uint32_t ks, uint32_t vs, const uint32_t* e, uint32_t part, int32_t s0) {
         constexpr bool kWhole = decltype(is_whole)::value;
-        bool nan = false;  // a key's block is NaN
+        bool rare = false;  // a block is NaN, or (INT8) its power above 2^5
         if constexpr (kQuantised<kFmt>) {
 #pragma unroll
             for (uint32_t r = lane; r < 2 * S::kPart; r += 32) {  // the keys', then the values'
                 const uint32_t s = r & (S::kPart - 1), x = e[r < S::kPart ? s : S::kSlots + s];
-                nan |= r < S::kPart && has_nan(x);
-                const uint32_t lo = pack2<true>(block_scale(x & 255u), block_scale(x >> 8 & 255u));
-                const uint32_t hi = pack2<true>(block_scale(x >> 16 & 255u), block_scale(x >> 24));
+                rare |= kFmt == kInt8 ? above_5(x) : has_nan(x);
+                const uint32_t lo = pack2<true>(power_of<0>(x), power_of<1>(x)), hi = pack2<true>(power_of<2>(x), power_of<3>(x));
                 if (r >= S::kPart) {
                     uint16_t* to = reinterpret_cast<uint16_t*>(powers) + s;
                     to[0] = (uint16_t)lo, to[S::kPart] = (uint16_t)(lo >> 16);
                     to[2 * S::kPart] = (uint16_t)hi, to[3 * S::kPart] = (uint16_t)(hi >> 16);
                 }
             }
-            nan = __any_sync(0xFFFFFFFFu, nan);
+            rare = __any_sync(0xFFFFFFFFu, rare);
             __syncwarp();
+            if (rare) {  // infinity times 0 is NaN already, as the store leaves such blocks
+                for (uint32_t r = lane; r < 4 * S::kPart; r += 32) {
+                    uint16_t* at = reinterpret_cast<uint16_t*>(powers) + r;
+                    if (*at == 0x7C00u) *at = 0x7E00u;
+                }
+                __syncwarp();
+            }
         }
         // Scores of slots 16 i + lane / 4 and that + 8 (x >> 1) for this thread's rows (x & 1).
         float sc[PS][NB][4];
@@ -358,7 +372,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
                             float s[2];
 #pragma unroll
                             for (int x = 0; x < 2; x++)
-                                s[x] = __uint_as_float((block < 3 ? power[x] << (23 - 8 * block) : power[x] >> 1) & 0x7F800000u);
+                                s[x] = block == 0 ? power_of<0>(power[x]) : block == 1 ? power_of<1>(power[x]) : block == 2 ? power_of<2>(power[x]) : power_of<3>(power[x]);
 #pragma unroll
                             for (int y = 0; y < NB; y++)
 #pragma unroll
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
                         }
                     }
                 }
-                if (kQuantised<kFmt> && nan) {  // a block of NaN makes its key's scores NaN
+                if (kQuantised<kFmt> && rare) {  // a block of NaN makes its key's scores NaN
 #pragma unroll
                     for (int y = 0; y < NB; y++)
 #pragma unroll
@@ -430,68 +444,93 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
                 pr[i][y][1] = transpose8(pack2<kHalf>(e[2], e[3]));
             }
         }
+        const auto values = [&](auto is_rare) {
 #pragma unroll
-        for (int i = 0; i < PS; i++) {
-            // Values of slots 2 (lane & 3) and the next, and of those + 8, as rows of V^T.
-            const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-                uint32_t f[4] = {a0, a1, a2, a3};
-                if constexpr (!kWhole) {  // 0 x infinity is not 0: keep such values out of the product
+            for (int i = 0; i < PS; i++) {
+                // Values of slots 2 (lane & 3) and the next, and of those + 8, as rows of V^T.
+                const auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    uint32_t f[4] = {a0, a1, a2, a3};
+                    if constexpr (!kWhole) {  // 0 x infinity is not 0: keep such values out of the product
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                        const uint32_t v = finite_or_zero<kHalf>(f[x]);
-                        odd |= v != f[x];
-                        f[x] = v;
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < NB; y++) mma16816<kHalf>(o[k][y], f, pr[i][y][0], pr[i][y][1]);
-            };
-#pragma unroll
-            for (int c = 0; c < kChunks; c += 2) {
-                uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block, transposed
-                ldmatrix4_trans(r, vs + tile_at<S::kRow, S::kSlots>(part + 16 * i + (lane & 15), c + (lane >> 4)));
-                if constexpr (kFmt == kBf16) {
-                    product(c / 2, r[0], r[2], r[1], r[3]);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        uint32_t w[2][4];
-#pragma unroll
-                        for (int x = 0; x < 2; x++) {
-                            const uint32_t v = r[2 * u + x];
-                            uint32_t f = 0;
-                            if constexpr (kQuantised<kFmt>) {
-                                const uint32_t block = kFmt == kInt8 ? (c + u) * 16 / (D / 4) : D == 128 ? c + u : 2 * (c + u) + (lane >> 4);
-                                f = *reinterpret_cast<const uint32_t*>(powers + 2 * (block * S::kPart + 16 * i + 8 * x + 2 * (lane & 3)));
-                            }
-                            if constexpr (kFmt == kE5m2) {
-                                w[x][0] = e5m2_02(v), w[x][1] = e5m2_13(v);
-                            } else if constexpr (kFmt == kInt8) {
-                                const uint32_t z = int8_bias(v);
-                                w[x][0] = mul_half2(int8_pair<kInt8_02>(z), f), w[x][1] = mul_half2(int8_pair<kInt8_13>(z), f);
-                            } else {
-                                // Bytes of the same value of both slots: values 0 and 2, then 1 and 3.
-                                uint32_t z = (v & 0x0F0Fu) | (v >> 12 & 0xF0F0u);
-                                z |= ((v >> 4 & 0x0F0Fu) | (v >> 16 & 0xF0F0u)) << 16;
-                                e2m1_pairs(w[x], z);
-#pragma unroll
-                                for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
-                            }
+                        for (int x = 0; x < 4; x++) {
+                            const uint32_t v = finite_or_zero<kHalf>(f[x]);
+                            odd |= v != f[x];
+                            f[x] = v;
                         }
-                        if constexpr (kFmt == kE2m1) {
-                            product(2 * (c + u), w[0][0], w[0][2], w[1][0], w[1][2]);
-                            product(2 * (c + u) + 1, w[0][1], w[0][3], w[1][1], w[1][3]);
-                        } else {
-                            product(c + u, w[0][0], w[0][1], w[1][0], w[1][1]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < NB; y++) mma16816<kHalf>(o[k][y], f, pr[i][y][0], pr[i][y][1]);
+                };
+#pragma unroll
+                for (int c = 0; c < kChunks; c += 2) {
+                    uint32_t r[4];  // chunks c and c + 1 (x >> 1) of slots 0-7 and 8-15 (x & 1) of the block, transposed
+                    ldmatrix4_trans(r, vs + tile_at<S::kRow, S::kSlots>(part + 16 * i + (lane & 15), c + (lane >> 4)));
+                    if constexpr (kFmt == kBf16) {
+                        product(c / 2, r[0], r[2], r[1], r[3]);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            uint32_t w[2][4];
+#pragma unroll
+                            for (int x = 0; x < 2; x++) {
+                                const uint32_t v = r[2 * u + x];
+                                uint32_t f = 0;
+                                if constexpr (kQuantised<kFmt>) {
+                                    const uint32_t block = kFmt == kInt8 ? (c + u) * 16 / (D / 4) : D == 128 ? c + u : 2 * (c + u) + (lane >> 4);
+                                    f = *reinterpret_cast<const uint32_t*>(powers + 2 * (block * S::kPart + 16 * i + 8 * x + 2 * (lane & 3)));
+                                }
+                                if constexpr (kFmt == kE5m2) {
+                                    w[x][0] = e5m2_02(v), w[x][1] = e5m2_13(v);
+                                } else if constexpr (kFmt == kInt8) {
+                                    const uint32_t z = int8_bias(v);
+                                    if constexpr (decltype(is_rare)::value) {
+                                        w[x][0] = mul_half2(int8_pair<kInt8_02>(z), f), w[x][1] = mul_half2(int8_pair<kInt8_13>(z), f);
+                                    } else {
+                                        w[x][0] = int8_scaled<kInt8_02>(z, f), w[x][1] = int8_scaled<kInt8_13>(z, f);
+                                    }
+                                } else {
+                                    // Bytes of the same value of both slots: values 0 and 2, then 1 and 3.
+                                    uint32_t z = (v & 0x0F0Fu) | (v >> 12 & 0xF0F0u);
+                                    z |= ((v >> 4 & 0x0F0Fu) | (v >> 16 & 0xF0F0u)) << 16;
+                                    e2m1_pairs(w[x], z);
+#pragma unroll
+                                    for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
+                                }
+                            }
+                            if constexpr (kFmt == kE2m1) {
+                                product(2 * (c + u), w[0][0], w[0][2], w[1][0], w[1][2]);
+                                product(2 * (c + u) + 1, w[0][1], w[0][3], w[1][1], w[1][3]);
+                            } else {
+                                product(c + u, w[0][0], w[0][1], w[1][0], w[1][1]);
+                            }
                         }
                     }
                 }
             }
-        }
+        };
+        if (kFmt == kInt8 && !rare) values(std::false_type());
+        else values(std::true_type());
     };
     bool ready = true;
     uint32_t stage = 0, turn = 0;
+    // The tile that takes the place of the one before the n-th; false where a wait gave up.
+    const auto refill = [&](uint32_t n) {
+        const uint32_t next = n + S::kStages - 1;
+        if (next != mine) return true;
+        if (next < count) {
+            if (n) ready = mbar_wait_bounded(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1, wait);
+            if (!ready) return false;
+            load(next, pages);
+        }
+        mine += kWarpsRows;
+        pages = look_up(mine);
+        return true;
+    };
     for (uint32_t n = 0; n < count; n++) {
+        // With two stages the next tile is asked for before this one's work, to be on its way
+        // meanwhile.  With more there are others on their way, and after it no warp waits
+        // for the slowest (16k caches: BF16 162 us after, 153 before; INT8 97 and 102).
+        if (S::kStages == 2 && !refill(n)) break;
         ready = mbar_wait_bounded(&sh.full[stage], turn, wait);
         if (!ready) break;
         const uint32_t ks = smem_addr(smem + stage * (2 * S::kTile)), vs = ks + S::kTile;
@@ -506,17 +545,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
         if (++stage == S::kStages) stage = 0, turn ^= 1;
-        // The tile that takes the place of the one before this.
-        const uint32_t next = n + S::kStages - 1;
-        if (next == mine) {
-            if (next < count) {
-                if (n) ready = mbar_wait_bounded(&sh.empty[next % S::kStages], (next / S::kStages - 1) & 1, wait);
-                if (!ready) break;
-                load(next, pages);
-            }
-            mine += kWarpsRows;
-            pages = look_up(mine);
-        }
+        if (S::kStages > 2 && !refill(n)) break;
     }
     // The head's value of o[k][..][x].
     auto column = [&](int k, int x) {

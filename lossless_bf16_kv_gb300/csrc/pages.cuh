@@ -50,6 +50,15 @@ __device__ __forceinline__ uint32_t int8_pair(uint32_t biased) {
     const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+// The same times a pair of powers of up to 2^5, in one step: 1152 times those is still
+// an FP16 number, and the sum of the exact products is rounded once, to what it is.
+template <int kSelect>
+__device__ __forceinline__ uint32_t int8_scaled(uint32_t biased, uint32_t powers) {
+    const uint32_t w = prmt(biased, 0x64646464u, kSelect);
+    const __half2 f = *reinterpret_cast<const __half2*>(&powers);
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&w), f, __hmul2(f, __half2half2(__ushort_as_half(0xE480))));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ uint32_t int8_bias(uint32_t r) { return r ^ 0x80808080u; }
 constexpr int kInt8_01 = 0x4140, kInt8_23 = 0x4342, kInt8_02 = 0x4240, kInt8_13 = 0x4341;
 // E2M1: the two halves of each byte of r (the lower half first).
