@@ -20,6 +20,7 @@ struct TilesParams {
     uint32_t test_cta, test_tile;  // a copy that a test has left out
 
     static constexpr bool kPaged = false;
+    __device__ __forceinline__ uint32_t raw_arrivals() const { return 1; }
     // This CTA's part of the work: one thread.  The last row tiles see the most slots: they go first.
     template <bool kTwin>
     __device__ __forceinline__ void place(TilesShared& sh) const {

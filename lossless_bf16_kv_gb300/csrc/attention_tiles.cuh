@@ -83,13 +83,14 @@ constexpr float kTilesLift = kF8 ? 9.0f : 0.0f;
 template <bool kF8>
 constexpr float kTilesLazy = kF8 ? 6.9f : 8.0f;
 
-template <int D, int kFmt>
+template <int D, int kFmt, bool kPaged>
 struct TilesShape {
     static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
     static constexpr int kRaw = kBN * kRowBytes<D, kFmt>;  // bytes of one as it lies in the cache, where it is widened
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
     static constexpr int kStages = D == 128 ? (kWide<kFmt> ? 4 : 5) : (kWide<kFmt> ? 6 : 8);
-    static constexpr int kRaws = !kWide<kFmt> ? 0 : kFmt == kE2m1 ? 4 : 2;
+    static constexpr int kRaws = !kWide<kFmt> ? 0 : kPaged && D == 64 ? 4 : kFmt == kE2m1 ? 3 : 2;
+    static constexpr int kExps = kQuantised<kFmt> ? kBN * 4 : 0;  // bytes of the exponents of one
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
     static constexpr int kTend = kWide<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
@@ -101,7 +102,9 @@ struct TilesShape {
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColO = 2 * kBN, kColP = kApart ? kColO + 2 * D : 0, kStepP = kApart ? kBN / 2 : kBN;
     static constexpr uint32_t kHalfP = kApart ? kBN / 4 : kBN / 2;  // over S, each half of P over its own scores
-    static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * kRaw;
+    static constexpr int kUsed = 2 * kQ + kStages * kKV + kRaws * (kRaw + kExps);
+    // Where exponents take the room, the two threads of a row exchange through one place.
+    static constexpr bool kOneRow = kQuantised<kFmt>;
     static_assert(kUsed >= 2 * kTileM * kRowFloats * 4, "partial results take the place of the tiles");
 };
 
@@ -122,7 +125,7 @@ struct TilesShared {
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
     int32_t upto[2], after[2], whole_sinks;  // WholeTiles of the query tiles
-    float row[2][2][kTileM];  // exchanged by the two threads of a row
+    float row[2][2][kTileM];  // [half][tile]: exchanged by the two threads of a row, the second half where there is room
 };
 
 // The first slot of each step in turn.
@@ -148,6 +151,25 @@ struct WholeTiles {
     }
     __device__ __forceinline__ bool operator()(int32_t s0) const { return s0 <= upto && (s0 > after || s0 <= sinks); }
 };
+
+// The other thread's value of the two of a row, both of which call it; `there`: this
+// thread's has been left already (where it leaves it first), and a barrier passed.
+template <bool kOneRow>
+__device__ __forceinline__ float exchange(TilesShared& sh, uint32_t t, uint32_t half, uint32_t r, uint32_t bar, float v, bool there = false) {
+    if (!there) {
+        if (!kOneRow || !half) sh.row[half][t][r] = v;
+        named_sync(bar, 64);
+    }
+    if (!kOneRow) return sh.row[half ^ 1][t][r];
+    float other = 0.0f;
+    if (half) {
+        other = sh.row[0][t][r];
+        sh.row[0][t][r] = v;
+    }
+    named_sync(bar, 64);
+    if (!half) other = sh.row[0][t][r];
+    return other;
+}
 
 // What a CTA's `per` query tokens from t0 on, of `count`, walk: its part of the slot
 // tiles that they see.
@@ -192,7 +214,7 @@ __device__ __forceinline__ uint32_t seen_bits(int32_t pos, int32_t lo, int32_t s
 // The query tiles, from token `first` of the tensor on.
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void load_queries(const Params& p, TilesShared& sh, uint8_t* qs, uint32_t first, int32_t b) {
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     mbar_arrive_expect_tx(&sh.q_full, 2 * p.tokens * p.group * D * 2);
 #pragma unroll
     for (int t = 0; t < 2; t++)
@@ -204,7 +226,7 @@ __device__ __forceinline__ void load_queries(const Params& p, TilesShared& sh, u
 
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void load_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw) {
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     volatile WaitLimit* wait = &sh.wait;
     const int32_t b = (int32_t)sh.b, h = (int32_t)sh.h;
     const uint32_t steps = sh.steps;
@@ -241,7 +263,7 @@ __device__ __forceinline__ void load_tiles(const Params& p, TilesShared& sh, uin
 // sees, or lies outside the pool, is loaded from behind its last page: as zeros.
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw, uint32_t lane) {
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     constexpr int kRow = kWide<kFmt> ? kRowBytes<D, kFmt> : 128;  // bytes of a row of a box
     volatile WaitLimit* wait = &sh.wait;
     const uint32_t steps = sh.steps;
@@ -257,12 +279,32 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
     constexpr int kN = kWide<kFmt> ? S::kRaws : S::kStages;
     uint64_t* full = kWide<kFmt> ? sh.raw_full : sh.full;
     uint64_t* empty = kWide<kFmt> ? sh.raw_empty : sh.empty;
+    uint8_t* exps = raw + S::kRaws * S::kRaw;  // of each raw stage, by slot
+    const bool bulk = kQuantised<kFmt> && p.bulk_exps;
     uint32_t now = look_up(0), ahead = look_up(1), i = 0;
     for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
         if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
         const bool v = i & 1;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw : S::kKV);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
         __syncwarp();
+        if (kQuantised<kFmt>) {  // where no query sees them, any page's: they multiply zeros
+            const splitzip_page_rows& rows = v ? p.a.pool.v : p.a.pool.k;
+            const uint8_t* from = rows.exponents + (int64_t)sh.h * rows.exp_stride_h;
+            uint8_t* to = exps + st * S::kExps;
+            const uint32_t some = now < p.a.pool.pages ? now : 0, s0 = (uint32_t)step_slot(sh, (int32_t)(i >> 1));
+            if (bulk) {
+                if (lane < p.boxes)
+                    bulk_load(to + 4 * lane * p.box, from + some * rows.exp_stride_p + 4 * ((s0 + lane * p.box) & (p.a.pool.page_tokens - 1)),
+                              4 * p.box, &full[st]);
+            } else {
+#pragma unroll
+                for (uint32_t r = lane; r < kBN; r += 32) {
+                    const int64_t page = __shfl_sync(0xFFFFFFFFu, some, r / p.box);
+                    cp_async4(to + 4 * r, from + page * rows.exp_stride_p + ((s0 + r) & (p.a.pool.page_tokens - 1)) * rows.exp_stride_t);
+                }
+                cp_async_arrive(&full[st]);
+            }
+        }
         if (lane < p.boxes) {
             const int32_t at = (int32_t)((uint32_t)step_slot(sh, (int32_t)(i >> 1)) & (p.a.pool.page_tokens - 1) & ~(p.box - 1));
             if (kWide<kFmt>) {
@@ -284,9 +326,9 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
     for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded<true>(&full[x % kN], (x / kN) & 1, wait);
 }
 
-template <int D, int kFmt, bool kTwin>
+template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, const uint8_t* qs, const uint8_t* ring) {
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     constexpr uint32_t kShapeS = mma_shape(kWide<kFmt>, kBN, false), kShapeO = mma_shape(kWide<kFmt>, D, true);
     volatile WaitLimit* wait = &sh.wait;
     const bool leader = elect_one();
@@ -426,111 +468,82 @@ __device__ __forceinline__ void issue_products(TilesShared& sh, uint32_t tmem, c
 // to the rows that see them at the end.  E5M2 tiles are widened on the way.
 template <int D, int kFmt, class Params>
 __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, uint8_t* ring, const uint8_t* raw, uint32_t thread) {
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     volatile WaitLimit* wait = &sh.wait;
     const uint32_t lane = thread & 31, steps = sh.steps;
     StepSlots slots(sh);
     const WholeTiles whole(sh, sh.p0, sh.p1);
     if constexpr (kQuantised<kFmt>) {
-        // Half of the warps widen the keys, half the values, 16 bytes of codes a lane: a
-        // warp 32 / kCh rows at a time.  The exponent bytes of a warp's rows lie with its
-        // lanes, fetched a step ahead (and their pages two), as FP16 powers; each row's
-        // go to its lanes by shuffles.
-        constexpr uint32_t kWarps = S::kTend / 2, kCh = kRowBytes<D, kFmt> / 16, kAtOnce = 32 / kCh;
-        constexpr uint32_t kIters = (kBN + kWarps * kAtOnce - 1) / (kWarps * kAtOnce);
-        static_assert(kIters <= 2 * kCh, "two words of exponent bytes to a lane");
-        const uint32_t mine = thread >= 16 * S::kTend, warp = (thread - mine * 16 * S::kTend) >> 5;
-        const splitzip_page_rows& rows = mine ? p.a.pool.v : p.a.pool.k;
-        const uint8_t* exps = rows.exponents + (int64_t)sh.h * rows.exp_stride_h;
-        const uint32_t pages = p.a.pool.pages;
-        // This lane's row of word w.
-        const auto row_of = [&](uint32_t w) { return ((w * kCh + lane / kAtOnce) * kWarps + warp) * kAtOnce + lane % kAtOnce; };
-        const auto page_of = [&](uint32_t j, uint32_t w) {
-            const uint32_t r = row_of(w);
-            if (j >= steps || r >= kBN) return pages;
-            const int32_t s = step_slot(sh, (int32_t)j) + (int32_t)r;
-            return p.run_seen(sh, s, 1) ? min(p.page(sh, s), pages) : pages;
-        };
-        const auto exps_of = [&](uint32_t j, uint32_t w, uint32_t page) {
-            if (page == pages) return 0u;
-            const uint32_t at = ((uint32_t)step_slot(sh, (int32_t)j) + row_of(w)) & (p.a.pool.page_tokens - 1);
-            return *reinterpret_cast<const uint32_t*>(exps + page * rows.exp_stride_p + at * rows.exp_stride_t);
-        };
-        uint32_t page[2], e[2];
-#pragma unroll
-        for (uint32_t w = 0; w < 2; w++) e[w] = exps_of(0, w, page_of(0, w));
-#pragma unroll
-        for (uint32_t w = 0; w < 2; w++) page[w] = page_of(1, w);
-        for (uint32_t n = mine; n < 2 * steps; n += 2) {
-            const uint32_t rs = n % S::kRaws, st = n % S::kStages, j = n >> 1;
-            uint32_t power[2][2];
-#pragma unroll
-            for (uint32_t w = 0; w < 2; w++) {
-                power[w][0] = pack2<true>(block_scale(e[w] & 255u), block_scale(e[w] >> 8 & 255u));
-                power[w][1] = pack2<true>(block_scale(e[w] >> 16 & 255u), block_scale(e[w] >> 24));
-                e[w] = exps_of(j + 1, w, page[w]);
-                page[w] = page_of(j + 2, w);
-            }
+        // Half of the warps widen the keys, half the values, 16 bytes of codes a lane.
+        constexpr uint32_t kCh = kRowBytes<D, kFmt> / 16;
+        const uint32_t mine = thread >= 16 * S::kTend, in_half = thread - mine * 16 * S::kTend;
+        const uint8_t* exps = raw + S::kRaws * S::kRaw;
+        for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
+            const uint32_t rs = n % S::kRaws, st = n % S::kStages;
             if (!mbar_wait_bounded(&sh.raw_full[rs], (n / S::kRaws) & 1, wait)) break;
             if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, wait)) break;
-            const bool part = mine && (sh.p0 < 0 || !whole(step_slot(sh, (int32_t)j)));
+            const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
             bool found = false;
-            const uint8_t* from = raw + rs * S::kRaw + 16 * lane;
-#pragma unroll
-            for (uint32_t w = 0; w < 2; w++)
 #pragma unroll 2
-                for (uint32_t k = 0; k < kCh; k++) {
-                    const uint32_t first = ((w * kCh + k) * kWarps + warp) * kAtOnce;  // the same for the warp
-                    if (first >= kBN) break;
-                    const uint32_t r = first + lane / kCh, c = lane % kCh, holder = k * kAtOnce + lane / kCh;
-                    const uint2 f = make_uint2(__shfl_sync(0xFFFFFFFFu, power[w][0], holder), __shfl_sync(0xFFFFFFFFu, power[w][1], holder));
-                    const uint4 v = *reinterpret_cast<const uint4*>(from + first * kRowBytes<D, kFmt>);
-                    uint8_t* row = ring + st * S::kKV + r * 128;
-                    // A 16-byte chunk of FP16 values, out of infinities and NaN where the tile is partly visible.
-                    const auto put = [&](uint32_t chunk, const uint32_t* h) {
-                        uint4 x = make_uint4(h[0], h[1], h[2], h[3]);
-                        if (part) {
-                            const uint4 y = x;
-                            x = make_uint4(finite_or_zero<true>(y.x), finite_or_zero<true>(y.y), finite_or_zero<true>(y.z), finite_or_zero<true>(y.w));
-                            found |= x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w;
-                        }
-                        *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk & 7) ^ (r & 7)) << 4)) = x;
-                    };
-                    if constexpr (kFmt == kInt8) {
-                        const uint32_t block = D == 128 ? c >> 1 : c;
-                        const uint32_t s = twice(f, block);
-                        const uint32_t b[4] = {int8_bias(v.x), int8_bias(v.y), int8_bias(v.z), int8_bias(v.w)};
-                        // Rows of the second block of 64 values store their upper half first, so that the
-                        // lanes of a row hit different banks.
-                        const uint32_t second = c >> 2;
+            for (uint32_t x = in_half; x < kBN * kCh; x += 16 * S::kTend) {
+                const uint32_t r = x / kCh, c = x % kCh;
+                const uint4 v = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + 16 * x);
+                const uint8_t* e = exps + rs * S::kExps + 4 * r;
+                uint8_t* row = ring + st * S::kKV + r * 128;
+                // A 16-byte chunk of FP16 values, out of infinities and NaN where the tile is partly visible.
+                const auto put = [&](uint32_t chunk, const uint32_t* h) {
+                    uint4 y = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (part) {
+                        const uint4 z = y;
+                        y = make_uint4(finite_or_zero<true>(z.x), finite_or_zero<true>(z.y), finite_or_zero<true>(z.z), finite_or_zero<true>(z.w));
+                        found |= y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w;
+                    }
+                    *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk & 7) ^ (r & 7)) << 4)) = y;
+                };
+                if constexpr (kFmt == kInt8) {
+                    const uint32_t power = e[D == 128 ? c >> 1 : c];
+                    const float f = block_scale(power);
+                    const uint32_t s = pack2<true>(f, f);
+                    const uint32_t b[4] = {int8_bias(v.x), int8_bias(v.y), int8_bias(v.z), int8_bias(v.w)};
+                    // Rows of the second block of 64 values store their upper half first, so that the
+                    // lanes of a row hit different banks.
+                    const uint32_t second = c >> 2;
+                    const bool rare = __any_sync(__activemask(), power > kInt8OneStep);
 #pragma unroll
-                        for (uint32_t y = 0; y < 2; y++) {
-                            const uint32_t half = y ^ second, lo = half ? b[2] : b[0], hi = half ? b[3] : b[1];
-                            const uint32_t h[4] = {mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
-                                                   mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s)};
-                            put(2 * c + half, h);
+                    for (uint32_t y = 0; y < 2; y++) {
+                        const uint32_t half = y ^ second, lo = half ? b[2] : b[0], hi = half ? b[3] : b[1];
+                        uint32_t h[4];
+                        if (rare) {
+                            h[0] = mul_half2(int8_pair<kInt8_01>(lo), s), h[1] = mul_half2(int8_pair<kInt8_23>(lo), s);
+                            h[2] = mul_half2(int8_pair<kInt8_01>(hi), s), h[3] = mul_half2(int8_pair<kInt8_23>(hi), s);
+                        } else {
+                            h[0] = int8_scaled<kInt8_01>(lo, s), h[1] = int8_scaled<kInt8_23>(lo, s);
+                            h[2] = int8_scaled<kInt8_01>(hi, s), h[3] = int8_scaled<kInt8_23>(hi, s);
                         }
-                    } else {
-                        const uint32_t second = (c >> 1) << 1;  // as above, by two chunks
+                        put(2 * c + half, h);
+                    }
+                } else {
+                    const float f0 = block_scale(e[D == 128 ? c : 2 * c]), f1 = D == 128 ? f0 : block_scale(e[2 * c + 1]);
+                    const uint32_t s0 = pack2<true>(f0, f0), s1 = D == 128 ? s0 : pack2<true>(f1, f1);
+                    const uint32_t second = (c >> 1) << 1;  // as above, by two chunks
 #pragma unroll
-                        for (uint32_t y = 0; y < 4; y++) {
-                            const uint32_t part_of = y ^ second, word = part_of & 2 ? (part_of & 1 ? v.w : v.z) : part_of & 1 ? v.y : v.x;
-                            const uint32_t s = twice(f, D == 128 ? c : 2 * c + (part_of >> 1));
-                            uint32_t h[4];
-                            e2m1_pairs(h, word);
+                    for (uint32_t y = 0; y < 4; y++) {
+                        const uint32_t at = y ^ second, word = at & 2 ? (at & 1 ? v.w : v.z) : at & 1 ? v.y : v.x;
+                        uint32_t h[4];
+                        e2m1_pairs(h, word);
 #pragma unroll
-                            for (int x = 0; x < 4; x++) h[x] = mul_half2(h[x], s);
-                            put(4 * c + part_of, h);
-                        }
+                        for (int z = 0; z < 4; z++) h[z] = mul_half2(h[z], at & 2 ? s1 : s0);
+                        put(4 * c + at, h);
                     }
                 }
+            }
             if (found) sh.odd = 1;
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh.raw_empty[rs]);
                 mbar_arrive(&sh.full[st]);
-                if (mine) mbar_arrive(&sh.ok[j & 7]);
+                if (mine) mbar_arrive(&sh.ok[(n >> 1) & 7]);
             }
         }
     } else if constexpr (kWide<kFmt>) {
@@ -605,7 +618,7 @@ template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ bool softmax_rows(const Params& p, TilesShared& sh, uint32_t tmem, uint32_t t, uint32_t half,
                                              uint32_t r, uint32_t pair_bar, int32_t pos, float scale, float& m, float& l) {
     volatile WaitLimit* wait = &sh.wait;
-    using S = TilesShape<D, kFmt>;
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     const uint32_t sa = tmem + t * kBN, oa = tmem + S::kColO + t * D + half * (D / 2), pa = tmem + S::kColP + t * S::kStepP + half * S::kHalfP;
     // What a step needs only a moment is read again from shared memory, as volatile.
     const volatile TilesShared& now_sh = sh;
@@ -688,9 +701,9 @@ __device__ __forceinline__ bool softmax_rows(const Params& p, TilesShared& sh, u
         // In the first step and rarely after it one of the rows of these two warps has a
         // new maximum, and they settle on one.  Where one's wait gave up, both return.
         if (named_any(pair_bar, 64, mine != m || !ready)) {
-            sh.row[t][half][r] = mine;
+            if (!S::kOneRow || !half) sh.row[half][t][r] = mine;
             if (named_any(pair_bar, 64, !ready)) return false;
-            const float now = fmaxf(mine, sh.row[t][half ^ 1][r]);
+            const float now = fmaxf(mine, exchange<S::kOneRow>(sh, t, half, r, pair_bar, mine, true));
             const float f = m == now ? 1.0f : exp2_approx(m - now), g = mine == now ? 1.0f : exp2_approx(mine - now);
             m = now;
             l *= f;
@@ -782,8 +795,8 @@ __device__ __forceinline__ void read_output(const Params& p, const TilesShared& 
 }
 
 template <int D, int kFmt, bool kTwin, class Params>
-__global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
-    using S = TilesShape<D, kFmt>;
+__global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
+    using S = TilesShape<D, kFmt, Params::kPaged>;
     extern __shared__ __align__(1024) uint8_t qs[];
     TilesShared& sh = *reinterpret_cast<TilesShared*>(qs + S::kUsed);
     uint8_t* ring = qs + 2 * S::kQ;             // tiles of D / 64 blocks of 128 rows of 128 bytes, as qs
@@ -804,7 +817,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
             mbar_init(&sh.ok[i], kWide<kFmt> ? S::kTend / 2 : S::kTend);
         }
         for (int i = 0; i < 4; i++) {
-            mbar_init(&sh.raw_full[i], 1);
+            mbar_init(&sh.raw_full[i], p.raw_arrivals());
             mbar_init(&sh.raw_empty[i], S::kTend / 2);
         }
         mbar_init(&sh.q_full, kWide<kFmt> ? kSoftmax : 1);
@@ -839,7 +852,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
     if (warp >= 16) {
         regs_dec<S::kOtherRegs>();
         if (sh.steps) {
-            if (warp == 16) issue_products<D, kFmt, kTwin>(sh, tmem, qs, ring);
+            if (warp == 16) issue_products<D, kFmt, kTwin, Params>(sh, tmem, qs, ring);
             else if (warp > 17) tend_values<D, kFmt>(p, sh, ring, raw, threadIdx.x - (kSoftmax + 64));
             else if constexpr (Params::kPaged) load_page_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw, threadIdx.x & 31);
             else if ((threadIdx.x & 31) == 0) load_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw);
@@ -874,9 +887,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
 #pragma unroll
                     for (int x = 0; x < 4; x++) top = max(top, max(w[x] & 0x7FFFu, w[x] >> 16 & 0x7FFFu));
                 }
-                sh.row[t][half][r] = __uint_as_float(top);
-                named_sync(pair_bar, 64);
-                const float power = row_power(max(top, __float_as_uint(sh.row[t][half ^ 1][r])));
+                const float power = row_power(max(top, __float_as_uint(exchange<S::kOneRow>(sh, t, half, r, pair_bar, __uint_as_float(top)))));
                 scale = fmaxf(scale / power, 0x1p-126f);  // never 0, which -infinity is multiplied by
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) {
@@ -895,9 +906,8 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
         }
         // The row's sum, of both halves in the same order.
         __syncwarp();
-        sh.row[t][half][r] = l;
-        named_sync(pair_bar, 64);
-        l = sh.row[t][0][r] + sh.row[t][1][r];
+        const float other = exchange<S::kOneRow>(sh, t, half, r, pair_bar, l);
+        l = half ? other + l : l + other;
         if ((threadIdx.x & 31) == 0 && !go) atomicOr(p.status, kStatusTimeout);
         if (!go || *reinterpret_cast<const volatile uint32_t*>(&sh.lost)) l = __int_as_float(0x7FC00000);  // a wait that gave up, a lost page: NaN
 
@@ -982,10 +992,11 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt>::kThreads, 1) tiles_kernel
 
 template <int D, int kFmt, bool kTwin, class Params>
 cudaError_t launch_tiles(const Params& p, uint32_t ctas, cudaStream_t s) {
-    constexpr int kSmem = TilesShape<D, kFmt>::kUsed + (int)sizeof(TilesShared);
+    using S = TilesShape<D, kFmt, Params::kPaged>;
+    constexpr int kSmem = S::kUsed + (int)sizeof(TilesShared) - (S::kOneRow ? (int)sizeof(TilesShared::row) / 2 : 0);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     Wave w;
-    const cudaError_t e = launch_wave<tiles_kernel<D, kFmt, kTwin, Params>>(TilesShape<D, kFmt>::kThreads, kSmem, w);
+    const cudaError_t e = launch_wave<tiles_kernel<D, kFmt, kTwin, Params>>(TilesShape<D, kFmt, Params::kPaged>::kThreads, kSmem, w);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -993,7 +1004,7 @@ cudaError_t launch_tiles(const Params& p, uint32_t ctas, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(TilesShape<D, kFmt>::kThreads);
+    cfg.blockDim = dim3(TilesShape<D, kFmt, Params::kPaged>::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = &attr;

@@ -697,11 +697,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     const uint32_t slots = kWarpsRows * 2048 / pool.head_dim;  // of a tile
     p.box = std::min(pool.page_tokens, slots);
     p.boxes = slots / p.box;
-    const auto bulk = [&](const splitzip_page_rows& r) {
-        return r.exp_stride_t == 4 && (uintptr_t)r.exponents % 16 == 0 && (pool.pages == 1 || r.exp_stride_p % 16 == 0) &&
-               (pool.kv_heads == 1 || r.exp_stride_h % 16 == 0);
-    };
-    p.bulk_exps = (pool.format == kInt8 || pool.format == kE2m1) && bulk(pool.k) && bulk(pool.v);
+    p.bulk_exps = bulk_exponents(pool);
     if (!page_map(p.kmap, pool, pool.k, p.box, true) || !page_map(p.vmap, pool, pool.v, p.box, true)) return cudaErrorInvalidValue;
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
     p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a copy's time

@@ -44,6 +44,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     p.boxes = kBN / p.box;
     p.page_shift = 0;
     while ((1u << p.page_shift) < a.pool.page_tokens) p.page_shift++;
+    p.bulk_exps = bulk_exponents(a.pool);
     p.rows_from = rows_from;
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
     p.wait_limit = wait_limit(0);  // a wait lasts a few steps at most

@@ -22,11 +22,14 @@ struct PagedTilesParams {
     uint32_t splits;
     uint32_t box, boxes;       // slots to a TMA box, and boxes to a tile
     uint32_t page_shift;
+    uint32_t bulk_exps;        // a page's exponent bytes of a head are contiguous, in multiples of 16 bytes
     uint32_t rows_from;        // only sequences with more query rows than this
     uint32_t* status;
     uint32_t wait_limit;
 
     static constexpr bool kPaged = true;
+    // On a raw tile's barrier: its copies', and the lanes' whose own copies bring the exponents.
+    __device__ __forceinline__ uint32_t raw_arrivals() const { return a.pool.format >= SPLITZIP_FORMAT_INT8 && !bulk_exps ? 33 : 1; }
     // Row-tile CTAs of a sequence.
     template <bool kTwin>
     __device__ __forceinline__ uint32_t ctas_of(uint32_t b) const {

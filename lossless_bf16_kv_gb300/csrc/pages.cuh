@@ -50,8 +50,9 @@ __device__ __forceinline__ uint32_t int8_pair(uint32_t biased) {
     const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-// The same times a pair of powers of up to 2^5, in one step: 1152 times those is still
+// The same times a pair of powers of up to 2^5 (exponent byte kInt8OneStep), in one step: 1152 times those is still
 // an FP16 number, and the sum of the exact products is rounded once, to what it is.
+constexpr uint32_t kInt8OneStep = 127 + 5;
 template <int kSelect>
 __device__ __forceinline__ uint32_t int8_scaled(uint32_t biased, uint32_t powers) {
     const uint32_t w = prmt(biased, 0x64646464u, kSelect);

@@ -29,4 +29,14 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, const PagedPlan& p, void* workspace,
                                cudaStream_t s);
 
+// Whether a page's exponent bytes of a head are contiguous and may be copied in
+// multiples of 16 bytes.
+inline bool bulk_exponents(const splitzip_pool& p) {
+    const auto ok = [&](const splitzip_page_rows& r) {
+        return r.exp_stride_t == 4 && (uintptr_t)r.exponents % 16 == 0 && (p.pages == 1 || r.exp_stride_p % 16 == 0) &&
+               (p.kv_heads == 1 || r.exp_stride_h % 16 == 0);
+    };
+    return (p.format == SPLITZIP_FORMAT_INT8 || p.format == SPLITZIP_FORMAT_E2M1) && ok(p.k) && ok(p.v);
+}
+
 }  // namespace splitzip
