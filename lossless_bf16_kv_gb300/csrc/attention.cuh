@@ -142,6 +142,16 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Byte offset of 16-byte chunk c of row r in a tile of rows of kRow bytes; the
+// chunks of eight consecutive rows at one c fall into eight different banks
+// groups, as ldmatrix reads them.
+template <int kRow>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
+    if (kRow >= 128) return r * kRow + ((c ^ (r & 7u)) << 4);
+    if (kRow == 64) return r * kRow + ((c ^ ((r >> 1) & 3u)) << 4);  // two rows to 128 bytes
+    return r * kRow + ((c ^ ((r >> 2) & 1u)) << 4);                  // four
+}
+
 // --------------------------------------------------------- E5M2 operands
 //
 // An E5M2 value is the upper byte of the FP16 value it stands for, so E5M2

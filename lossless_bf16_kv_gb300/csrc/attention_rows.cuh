@@ -20,16 +20,6 @@ constexpr int kTileBytes = 4096;  // of keys, and of values, per warp and stage
 template <bool kF8>
 constexpr float kLift = kF8 ? 15.0f : 0.0f;
 
-// Byte offset of 16-byte chunk c of row r in a tile of rows of kRow bytes; the
-// chunks of eight consecutive rows at one c fall into eight different banks
-// groups, as ldmatrix reads them.
-template <int kRow>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t r, uint32_t c) {
-    if (kRow >= 128) return r * kRow + ((c ^ (r & 7u)) << 4);
-    if (kRow == 64) return r * kRow + ((c ^ ((r >> 1) & 3u)) << 4);  // two rows to 128 bytes
-    return r * kRow + ((c ^ ((r >> 2) & 1u)) << 4);                  // four
-}
-
 __device__ __forceinline__ void add_scaled(float4& v, float f, float4 x) {
     v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
 }

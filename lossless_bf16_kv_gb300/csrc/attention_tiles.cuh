@@ -93,8 +93,11 @@ struct TilesShape {
     static constexpr int kExps = kQuantised<kFmt> ? kBN * 4 : 0;  // bytes of the exponents of one
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
-    static constexpr int kTend = kWide<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
-    static constexpr int kRegs = kWide<kFmt> ? 96 : 104, kOtherRegs = kWide<kFmt> ? 48 : 64;
+    static constexpr bool kManyTend = kWide<kFmt> && kPaged;
+    static constexpr int kTend = kManyTend ? 10 : kWide<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
+    static constexpr int kRegs = kWide<kFmt> ? 96 : 104, kOtherRegs = kManyTend ? 40 : kWide<kFmt> ? 48 : 64;
+    // Warps that widen a tile, and those that say that its values are fit.
+    static constexpr int kWiden = kManyTend ? 4 : kTend / 2, kFit = kWide<kFmt> ? kWiden : kTend;
     static_assert(kThreads % 128 == 0 && kSoftmax * kRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8),
                   "register shares add up to what the CTA is launched with");
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
@@ -473,10 +476,16 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
     const uint32_t lane = thread & 31, steps = sh.steps;
     StepSlots slots(sh);
     const WholeTiles whole(sh, sh.p0, sh.p1);
-    if constexpr (kQuantised<kFmt>) {
-        // Half of the warps widen the keys, half the values, 16 bytes of codes a lane.
-        constexpr uint32_t kCh = kRowBytes<D, kFmt> / 16;
-        const uint32_t mine = thread >= 16 * S::kTend, in_half = thread - mine * 16 * S::kTend;
+    if constexpr (kWide<kFmt> && Params::kPaged) {
+        // Half of the warps widen the keys, half the values, 16 bytes of the cache a lane:
+        // the lanes of a quarter warp take rows of their own, which the swizzles of both
+        // tiles spread over the banks, so a lane's places in them stay.
+        constexpr uint32_t kWarps = S::kWiden, kCh = kRowBytes<D, kFmt> / 16;
+        constexpr uint32_t kRows = kCh == 2 ? 16 : 8, kEach = kCh == 8 ? 2 : 1;  // rows of a warp at once, chunks of a lane
+        constexpr uint32_t kOut = 8 * D / kRowBytes<D, kFmt> / 4;                // 16-byte chunks of FP16 out of one
+        if (thread >= 64 * kWarps) return;
+        const uint32_t mine = thread / (32 * kWarps), warp = (thread >> 5) % kWarps;
+        const uint32_t r0 = warp * kRows + (lane & 7) + (kCh == 2 ? lane >> 4 << 3 : 0), c0 = kCh == 2 ? lane >> 3 & 1 : lane >> 3;
         const uint8_t* exps = raw + S::kRaws * S::kRaw;
         for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
             const uint32_t rs = n % S::kRaws, st = n % S::kStages;
@@ -484,56 +493,55 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
             if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, wait)) break;
             const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
             bool found = false;
-#pragma unroll 2
-            for (uint32_t x = in_half; x < kBN * kCh; x += 16 * S::kTend) {
-                const uint32_t r = x / kCh, c = x % kCh;
-                const uint4 v = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + 16 * x);
-                const uint8_t* e = exps + rs * S::kExps + 4 * r;
+#pragma unroll 1
+            for (uint32_t r = r0; r < kBN; r += kWarps * kRows) {
+                uint4 v[kEach];
+#pragma unroll
+                for (uint32_t x = 0; x < kEach; x++) v[x] = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + chunk_at<kRowBytes<D, kFmt>>(r, c0 + 4 * x));
+                uint32_t e = 0;
+                if constexpr (kQuantised<kFmt>) e = *reinterpret_cast<const uint32_t*>(exps + rs * S::kExps + 4 * r);
                 uint8_t* row = ring + st * S::kKV + r * 128;
-                // A 16-byte chunk of FP16 values, out of infinities and NaN where the tile is partly visible.
-                const auto put = [&](uint32_t chunk, const uint32_t* h) {
-                    uint4 y = make_uint4(h[0], h[1], h[2], h[3]);
-                    if (part) {
-                        const uint4 z = y;
-                        y = make_uint4(finite_or_zero<true>(z.x), finite_or_zero<true>(z.y), finite_or_zero<true>(z.z), finite_or_zero<true>(z.w));
-                        found |= y.x != z.x || y.y != z.y || y.z != z.z || y.w != z.w;
-                    }
-                    *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk & 7) ^ (r & 7)) << 4)) = y;
-                };
-                if constexpr (kFmt == kInt8) {
-                    const uint32_t power = e[D == 128 ? c >> 1 : c];
-                    const float f = block_scale(power);
-                    const uint32_t s = pack2<true>(f, f);
-                    const uint32_t b[4] = {int8_bias(v.x), int8_bias(v.y), int8_bias(v.z), int8_bias(v.w)};
-                    // Rows of the second block of 64 values store their upper half first, so that the
-                    // lanes of a row hit different banks.
-                    const uint32_t second = c >> 2;
-                    const bool rare = __any_sync(__activemask(), power > kInt8OneStep);
 #pragma unroll
-                    for (uint32_t y = 0; y < 2; y++) {
-                        const uint32_t half = y ^ second, lo = half ? b[2] : b[0], hi = half ? b[3] : b[1];
-                        uint32_t h[4];
-                        if (rare) {
-                            h[0] = mul_half2(int8_pair<kInt8_01>(lo), s), h[1] = mul_half2(int8_pair<kInt8_23>(lo), s);
-                            h[2] = mul_half2(int8_pair<kInt8_01>(hi), s), h[3] = mul_half2(int8_pair<kInt8_23>(hi), s);
-                        } else {
-                            h[0] = int8_scaled<kInt8_01>(lo, s), h[1] = int8_scaled<kInt8_23>(lo, s);
-                            h[2] = int8_scaled<kInt8_01>(hi, s), h[3] = int8_scaled<kInt8_23>(hi, s);
+                for (uint32_t x = 0; x < kEach; x++) {
+                    const uint32_t c = c0 + 4 * x, w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                    // Chunk y of this one's FP16 values, out of infinities and NaN where the tile is partly visible.
+                    const auto put = [&](uint32_t y, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
+                        if (part) {
+                            const uint32_t z0 = finite_or_zero<true>(h0), z1 = finite_or_zero<true>(h1), z2 = finite_or_zero<true>(h2),
+                                           z3 = finite_or_zero<true>(h3);
+                            found |= z0 != h0 || z1 != h1 || z2 != h2 || z3 != h3;
+                            h0 = z0, h1 = z1, h2 = z2, h3 = z3;
                         }
-                        put(2 * c + half, h);
-                    }
-                } else {
-                    const float f0 = block_scale(e[D == 128 ? c : 2 * c]), f1 = D == 128 ? f0 : block_scale(e[2 * c + 1]);
-                    const uint32_t s0 = pack2<true>(f0, f0), s1 = D == 128 ? s0 : pack2<true>(f1, f1);
-                    const uint32_t second = (c >> 1) << 1;  // as above, by two chunks
+                        const uint32_t chunk = kOut * c + y;
+                        *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk ^ r) & 7) << 4)) = make_uint4(h0, h1, h2, h3);
+                    };
+                    if constexpr (kFmt == kE5m2) {
+                        put(0, e5m2_01(w[0]), e5m2_23(w[0]), e5m2_01(w[1]), e5m2_23(w[1]));
+                        put(1, e5m2_01(w[2]), e5m2_23(w[2]), e5m2_01(w[3]), e5m2_23(w[3]));
+                    } else if constexpr (kFmt == kInt8) {
+                        const uint32_t power = e >> 8 * (D == 128 ? c >> 1 : c) & 255u;
+                        const float f = block_scale(power);
+                        const uint32_t s = pack2<true>(f, f);
+                        const bool rare = __any_sync(0xFFFFFFFFu, power > kInt8OneStep);
 #pragma unroll
-                    for (uint32_t y = 0; y < 4; y++) {
-                        const uint32_t at = y ^ second, word = at & 2 ? (at & 1 ? v.w : v.z) : at & 1 ? v.y : v.x;
-                        uint32_t h[4];
-                        e2m1_pairs(h, word);
+                        for (int y = 0; y < 2; y++) {
+                            const uint32_t lo = int8_bias(w[2 * y]), hi = int8_bias(w[2 * y + 1]);
+                            if (rare)
+                                put(y, mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
+                                    mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s));
+                            else
+                                put(y, int8_scaled<kInt8_01>(lo, s), int8_scaled<kInt8_23>(lo, s), int8_scaled<kInt8_01>(hi, s),
+                                    int8_scaled<kInt8_23>(hi, s));
+                        }
+                    } else {
 #pragma unroll
-                        for (int z = 0; z < 4; z++) h[z] = mul_half2(h[z], at & 2 ? s1 : s0);
-                        put(4 * c + at, h);
+                        for (int y = 0; y < 4; y++) {
+                            const float f = block_scale(e >> 8 * (D == 128 ? c : 2 * c + (y >> 1)) & 255u);
+                            const uint32_t s = pack2<true>(f, f);
+                            uint32_t z[4];
+                            e2m1_pairs(z, w[y]);
+                            put(y, mul_half2(z[0], s), mul_half2(z[1], s), mul_half2(z[2], s), mul_half2(z[3], s));
+                        }
                     }
                 }
             }
@@ -812,13 +820,13 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
     if (threadIdx.x == 0) {
         if constexpr (!Params::kPaged) p.template place<kTwin>(sh);
         for (int i = 0; i < 8; i++) {
-            mbar_init(&sh.full[i], kWide<kFmt> ? S::kTend / 2 : 1);
+            mbar_init(&sh.full[i], kWide<kFmt> ? S::kWiden : 1);
             mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.ok[i], kWide<kFmt> ? S::kTend / 2 : S::kTend);
+            mbar_init(&sh.ok[i], S::kFit);
         }
         for (int i = 0; i < 4; i++) {
             mbar_init(&sh.raw_full[i], p.raw_arrivals());
-            mbar_init(&sh.raw_empty[i], S::kTend / 2);
+            mbar_init(&sh.raw_empty[i], S::kWiden);
         }
         mbar_init(&sh.q_full, kWide<kFmt> ? kSoftmax : 1);
         for (int i = 0; i < 2; i++) {

@@ -698,7 +698,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.box = std::min(pool.page_tokens, slots);
     p.boxes = slots / p.box;
     p.bulk_exps = bulk_exponents(pool);
-    if (!page_map(p.kmap, pool, pool.k, p.box, true) || !page_map(p.vmap, pool, pool.v, p.box, true)) return cudaErrorInvalidValue;
+    if (!page_map(p.kmap, pool, pool.k, p.box) || !page_map(p.vmap, pool, pool.v, p.box)) return cudaErrorInvalidValue;
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
     p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a copy's time
     p.test_cta = test.cta;

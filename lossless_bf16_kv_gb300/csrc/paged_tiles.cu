@@ -52,7 +52,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     const bool wide = pool.format != kBf16;
     uint32_t one;
     if ((!wide && !make_map(p.qmap, a.q, 2, pool.head_dim, a.q_heads, a.tokens, 1, p.group, p.tokens, true, &one)) ||
-        !page_map(p.kmap, pool, pool.k, p.box, false) || !page_map(p.vmap, pool, pool.v, p.box, false))
+        !page_map(p.kmap, pool, pool.k, p.box) || !page_map(p.vmap, pool, pool.v, p.box))
         return cudaErrorInvalidValue;
     const uint32_t ctas = plan.row_tiles * pool.kv_heads * plan.splits;
     if (pool.head_dim == 64) return is_twin(a) ? launch_paged_64_twin(p, ctas, s) : launch_paged_64(p, ctas, s);

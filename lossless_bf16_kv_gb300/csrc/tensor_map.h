@@ -48,12 +48,12 @@ inline bool make_map(CUtensorMap& map, const splitzip_view& v, uint32_t elem, ui
 }
 
 // A pool's keys or values as a map of boxes of `box` slots of a page and head, at
-// (value or byte, slot, head, page); swizzle8: rows of bytes swizzled by their length.
-inline bool page_map(CUtensorMap& map, const splitzip_pool& pool, const splitzip_page_rows& rows, uint32_t box, bool swizzle8) {
+// (value or byte, slot, head, page); rows of bytes are swizzled by their length.
+inline bool page_map(CUtensorMap& map, const splitzip_pool& pool, const splitzip_page_rows& rows, uint32_t box) {
     uint32_t one;
     const uint32_t elem = pool.format == SPLITZIP_FORMAT_BF16 ? 2 : 1, dim = pool.format == SPLITZIP_FORMAT_E2M1 ? pool.head_dim / 2 : pool.head_dim;
     return make_map(map, {rows.data, rows.stride_p, rows.stride_t, rows.stride_h}, elem, dim, pool.kv_heads, pool.page_tokens, pool.pages, 1, box,
-                    false, &one, swizzle8);
+                    false, &one, true);
 }
 
 }  // namespace splitzip
