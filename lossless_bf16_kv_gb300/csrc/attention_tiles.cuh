@@ -86,11 +86,13 @@ constexpr float kTilesLazy = kF8 ? 6.9f : 8.0f;
 template <int D, int kFmt, bool kPaged>
 struct TilesShape {
     static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
-    static constexpr int kRaw = kBN * kRowBytes<D, kFmt>;  // bytes of one as it lies in the cache, where it is widened
+    // Where it is widened, a tile comes as it lies in the cache, in one part or two, of kRaw bytes and kExps of exponents.
+    static constexpr int kParts = kPaged && kWide<kFmt> && kRowBytes<D, kFmt> == 128 ? 2 : 1, kPartSlots = kBN / kParts;
+    static constexpr int kRaw = kPartSlots * kRowBytes<D, kFmt>;
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
     static constexpr int kStages = D == 128 ? (kWide<kFmt> ? 4 : 5) : (kWide<kFmt> ? 6 : 8);
-    static constexpr int kRaws = !kWide<kFmt> ? 0 : kPaged && D == 64 ? 4 : kFmt == kE2m1 ? 3 : 2;
-    static constexpr int kExps = kQuantised<kFmt> ? kBN * 4 : 0;  // bytes of the exponents of one
+    static constexpr int kRaws = !kWide<kFmt> ? 0 : kParts == 2 || (kPaged && D == 64) ? 4 : kFmt == kE2m1 ? 3 : 2;
+    static constexpr int kExps = kQuantised<kFmt> ? kPartSlots * 4 : 0;
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
     static constexpr bool kManyTend = kWide<kFmt> && kPaged;
@@ -284,44 +286,48 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
     uint64_t* empty = kWide<kFmt> ? sh.raw_empty : sh.empty;
     uint8_t* exps = raw + S::kRaws * S::kRaw;  // of each raw stage, by slot
     const bool bulk = kQuantised<kFmt> && p.bulk_exps;
-    uint32_t now = look_up(0), ahead = look_up(1), i = 0;
-    for (uint32_t st = 0, ph = 0; i < 2 * steps; i++) {
+    constexpr uint32_t kParts = S::kParts;
+    const uint32_t part_boxes = p.boxes / kParts, slots_mask = p.a.pool.page_tokens - 1;
+    uint32_t now = look_up(0), ahead = look_up(1), i = 0;  // i: of the parts of the keys', values', next keys' .. tiles
+    for (uint32_t st = 0, ph = 0; i < 2 * kParts * steps; i++) {
         if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
-        const bool v = i & 1;
+        const uint32_t step = i / (2 * kParts), part = i % kParts;
+        const bool v = i / kParts & 1;
+        const uint32_t s0 = (uint32_t)step_slot(sh, (int32_t)step) + part * S::kPartSlots;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
         __syncwarp();
+        const uint32_t mine = lane - part * part_boxes;  // this lane's box of the part
         if (kQuantised<kFmt>) {  // where no query sees them, any page's: they multiply zeros
             const splitzip_page_rows& rows = v ? p.a.pool.v : p.a.pool.k;
             const uint8_t* from = rows.exponents + (int64_t)sh.h * rows.exp_stride_h;
             uint8_t* to = exps + st * S::kExps;
-            const uint32_t some = now < p.a.pool.pages ? now : 0, s0 = (uint32_t)step_slot(sh, (int32_t)(i >> 1));
+            const uint32_t some = now < p.a.pool.pages ? now : 0;
             if (bulk) {
-                if (lane < p.boxes)
-                    bulk_load(to + 4 * lane * p.box, from + some * rows.exp_stride_p + 4 * ((s0 + lane * p.box) & (p.a.pool.page_tokens - 1)),
-                              4 * p.box, &full[st]);
+                if (mine < part_boxes)
+                    bulk_load(to + 4 * mine * p.box, from + some * rows.exp_stride_p + 4 * ((s0 + mine * p.box) & slots_mask), 4 * p.box, &full[st]);
             } else {
 #pragma unroll
-                for (uint32_t r = lane; r < kBN; r += 32) {
-                    const int64_t page = __shfl_sync(0xFFFFFFFFu, some, r / p.box);
-                    cp_async4(to + 4 * r, from + page * rows.exp_stride_p + ((s0 + r) & (p.a.pool.page_tokens - 1)) * rows.exp_stride_t);
+                for (uint32_t r = lane; r < S::kPartSlots; r += 32) {
+                    const int64_t page = __shfl_sync(0xFFFFFFFFu, some, part * part_boxes + r / p.box);
+                    cp_async4(to + 4 * r, from + page * rows.exp_stride_p + ((s0 + r) & slots_mask) * rows.exp_stride_t);
                 }
                 cp_async_arrive(&full[st]);
             }
         }
-        if (lane < p.boxes) {
-            const int32_t at = (int32_t)((uint32_t)step_slot(sh, (int32_t)(i >> 1)) & (p.a.pool.page_tokens - 1) & ~(p.box - 1));
+        if (mine < part_boxes) {
+            const int32_t at = (int32_t)((s0 + mine * p.box) & slots_mask);
             if (kWide<kFmt>) {
-                tma_load4(raw + st * S::kRaw + lane * p.box * kRow, v ? &p.vmap : &p.kmap, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);
+                tma_load4(raw + st * S::kRaw + mine * p.box * kRow, v ? &p.vmap : &p.kmap, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);
             } else {
 #pragma unroll
                 for (int x = 0; x < D / 64; x++)
-                    tma_load4(ring + st * S::kKV + x * (kBN * 128) + lane * p.box * kRow, v ? &p.vmap : &p.kmap, 64 * x, at, (int32_t)sh.h,
+                    tma_load4(ring + st * S::kKV + x * (kBN * 128) + mine * p.box * kRow, v ? &p.vmap : &p.kmap, 64 * x, at, (int32_t)sh.h,
                               (int32_t)now, &full[st]);
             }
         }
-        if (v) {
+        if (v && part == kParts - 1) {
             now = ahead;
-            ahead = look_up((i >> 1) + 2);
+            ahead = look_up(step + 2);
         }
         if (++st == kN) st = 0, ph ^= 1;
     }
@@ -488,68 +494,76 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
         const uint32_t r0 = warp * kRows + (lane & 7) + (kCh == 2 ? lane >> 4 << 3 : 0), c0 = kCh == 2 ? lane >> 3 & 1 : lane >> 3;
         const uint8_t* exps = raw + S::kRaws * S::kRaw;
         for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
-            const uint32_t rs = n % S::kRaws, st = n % S::kStages;
-            if (!mbar_wait_bounded(&sh.raw_full[rs], (n / S::kRaws) & 1, wait)) break;
+            const uint32_t st = n % S::kStages;
             if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, wait)) break;
             const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
             bool found = false;
+            bool there = true;
 #pragma unroll 1
-            for (uint32_t r = r0; r < kBN; r += kWarps * kRows) {
-                uint4 v[kEach];
+            for (uint32_t u = 0; u < S::kParts; u++) {
+                const uint32_t m = n * S::kParts + u, rs = m % S::kRaws;
+                there = mbar_wait_bounded(&sh.raw_full[rs], (m / S::kRaws) & 1, wait);
+                if (!there) break;
+#pragma unroll 1
+                for (uint32_t r = r0; r < S::kPartSlots; r += kWarps * kRows) {
+                    uint4 v[kEach];
 #pragma unroll
-                for (uint32_t x = 0; x < kEach; x++) v[x] = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + chunk_at<kRowBytes<D, kFmt>>(r, c0 + 4 * x));
-                uint32_t e = 0;
-                if constexpr (kQuantised<kFmt>) e = *reinterpret_cast<const uint32_t*>(exps + rs * S::kExps + 4 * r);
-                uint8_t* row = ring + st * S::kKV + r * 128;
+                    for (uint32_t x = 0; x < kEach; x++) v[x] = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + chunk_at<kRowBytes<D, kFmt>>(r, c0 + 4 * x));
+                    uint32_t e = 0;
+                    if constexpr (kQuantised<kFmt>) e = *reinterpret_cast<const uint32_t*>(exps + rs * S::kExps + 4 * r);
+                    uint8_t* row = ring + st * S::kKV + (u * S::kPartSlots + r) * 128;
 #pragma unroll
-                for (uint32_t x = 0; x < kEach; x++) {
-                    const uint32_t c = c0 + 4 * x, w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-                    // Chunk y of this one's FP16 values, out of infinities and NaN where the tile is partly visible.
-                    const auto put = [&](uint32_t y, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
-                        if (part) {
-                            const uint32_t z0 = finite_or_zero<true>(h0), z1 = finite_or_zero<true>(h1), z2 = finite_or_zero<true>(h2),
-                                           z3 = finite_or_zero<true>(h3);
-                            found |= z0 != h0 || z1 != h1 || z2 != h2 || z3 != h3;
-                            h0 = z0, h1 = z1, h2 = z2, h3 = z3;
-                        }
-                        const uint32_t chunk = kOut * c + y;
-                        *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk ^ r) & 7) << 4)) = make_uint4(h0, h1, h2, h3);
-                    };
-                    if constexpr (kFmt == kE5m2) {
-                        put(0, e5m2_01(w[0]), e5m2_23(w[0]), e5m2_01(w[1]), e5m2_23(w[1]));
-                        put(1, e5m2_01(w[2]), e5m2_23(w[2]), e5m2_01(w[3]), e5m2_23(w[3]));
-                    } else if constexpr (kFmt == kInt8) {
-                        const uint32_t power = e >> 8 * (D == 128 ? c >> 1 : c) & 255u;
-                        const float f = block_scale(power);
-                        const uint32_t s = pack2<true>(f, f);
-                        const bool rare = __any_sync(0xFFFFFFFFu, power > kInt8OneStep);
-#pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            const uint32_t lo = int8_bias(w[2 * y]), hi = int8_bias(w[2 * y + 1]);
-                            if (rare)
-                                put(y, mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
-                                    mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s));
-                            else
-                                put(y, int8_scaled<kInt8_01>(lo, s), int8_scaled<kInt8_23>(lo, s), int8_scaled<kInt8_01>(hi, s),
-                                    int8_scaled<kInt8_23>(hi, s));
-                        }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            const float f = block_scale(e >> 8 * (D == 128 ? c : 2 * c + (y >> 1)) & 255u);
+                    for (uint32_t x = 0; x < kEach; x++) {
+                        const uint32_t c = c0 + 4 * x, w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                        // Chunk y of this one's FP16 values, out of infinities and NaN where the tile is partly visible.
+                        const auto put = [&](uint32_t y, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
+                            if (part) {
+                                const uint32_t z0 = finite_or_zero<true>(h0), z1 = finite_or_zero<true>(h1), z2 = finite_or_zero<true>(h2),
+                                               z3 = finite_or_zero<true>(h3);
+                                found |= z0 != h0 || z1 != h1 || z2 != h2 || z3 != h3;
+                                h0 = z0, h1 = z1, h2 = z2, h3 = z3;
+                            }
+                            const uint32_t chunk = kOut * c + y;
+                            *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk ^ r) & 7) << 4)) = make_uint4(h0, h1, h2, h3);
+                        };
+                        if constexpr (kFmt == kE5m2) {
+                            put(0, e5m2_01(w[0]), e5m2_23(w[0]), e5m2_01(w[1]), e5m2_23(w[1]));
+                            put(1, e5m2_01(w[2]), e5m2_23(w[2]), e5m2_01(w[3]), e5m2_23(w[3]));
+                        } else if constexpr (kFmt == kInt8) {
+                            const uint32_t power = e >> 8 * (D == 128 ? c >> 1 : c) & 255u;
+                            const float f = block_scale(power);
                             const uint32_t s = pack2<true>(f, f);
-                            uint32_t z[4];
-                            e2m1_pairs(z, w[y]);
-                            put(y, mul_half2(z[0], s), mul_half2(z[1], s), mul_half2(z[2], s), mul_half2(z[3], s));
+                            const bool rare = __any_sync(0xFFFFFFFFu, power > kInt8OneStep);
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                const uint32_t lo = int8_bias(w[2 * y]), hi = int8_bias(w[2 * y + 1]);
+                                if (rare)
+                                    put(y, mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
+                                        mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s));
+                                else
+                                    put(y, int8_scaled<kInt8_01>(lo, s), int8_scaled<kInt8_23>(lo, s), int8_scaled<kInt8_01>(hi, s),
+                                        int8_scaled<kInt8_23>(hi, s));
+                            }
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 4; y++) {
+                                const float f = block_scale(e >> 8 * (D == 128 ? c : 2 * c + (y >> 1)) & 255u);
+                                const uint32_t s = pack2<true>(f, f);
+                                uint32_t z[4];
+                                e2m1_pairs(z, w[y]);
+                                put(y, mul_half2(z[0], s), mul_half2(z[1], s), mul_half2(z[2], s), mul_half2(z[3], s));
+                            }
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
             }
+            if (!there) break;
             if (found) sh.odd = 1;
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.raw_empty[rs]);
                 mbar_arrive(&sh.full[st]);
                 if (mine) mbar_arrive(&sh.ok[(n >> 1) & 7]);
             }

@@ -40,7 +40,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     p.group = a.q_heads / a.pool.kv_heads;
     p.tokens = kTileM / p.group;
     p.splits = plan.splits;
-    p.box = std::min<uint32_t>(a.pool.page_tokens, kBN);
+    p.box = std::min<uint32_t>(a.pool.page_tokens, tile_part(a.pool));
     p.boxes = kBN / p.box;
     p.page_shift = 0;
     while ((1u << p.page_shift) < a.pool.page_tokens) p.page_shift++;

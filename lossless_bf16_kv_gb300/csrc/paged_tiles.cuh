@@ -108,6 +108,16 @@ struct PagedTilesParams {
     }
 };
 
+// Slots of a part that a tile is loaded in.
+template <int D>
+uint32_t tile_part_of(uint32_t format) {
+    return format == kBf16   ? TilesShape<D, kBf16, true>::kPartSlots
+           : format == kE5m2 ? TilesShape<D, kE5m2, true>::kPartSlots
+           : format == kInt8 ? TilesShape<D, kInt8, true>::kPartSlots
+                             : TilesShape<D, kE2m1, true>::kPartSlots;
+}
+inline uint32_t tile_part(const splitzip_pool& p) { return p.head_dim == 64 ? tile_part_of<64>(p.format) : tile_part_of<128>(p.format); }
+
 template <int D, bool kTwin>
 cudaError_t launch_paged_format(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s) {
     switch (p.a.pool.format) {
