@@ -488,74 +488,95 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
         // tiles spread over the banks, so a lane's places in them stay.
         constexpr uint32_t kWarps = S::kWiden, kCh = kRowBytes<D, kFmt> / 16;
         constexpr uint32_t kRows = kCh == 2 ? 16 : 8, kEach = kCh == 8 ? 2 : 1;  // rows of a warp at once, chunks of a lane
-        constexpr uint32_t kOut = 8 * D / kRowBytes<D, kFmt> / 4;                // 16-byte chunks of FP16 out of one
+        constexpr uint32_t kOut = 2 * D / kRowBytes<D, kFmt>;                    // 16-byte chunks of FP16 out of one
         if (thread >= 64 * kWarps) return;
         const uint32_t mine = thread / (32 * kWarps), warp = (thread >> 5) % kWarps;
-        const uint32_t r0 = warp * kRows + (lane & 7) + (kCh == 2 ? lane >> 4 << 3 : 0), c0 = kCh == 2 ? lane >> 3 & 1 : lane >> 3;
+        const uint32_t r0 = warp * kRows + (lane & 7) + (kCh == 2 ? lane >> 4 << 3 : 0);  // its first row, the others a multiple of 8 on
+        const uint32_t c0 = kCh == 2 ? lane >> 3 & 1 : kEach * (lane >> 3);               // its first chunk, in a row and ..
+        const uint32_t shift = kCh == 2 ? lane << 1 & 16 : lane & 24;                     // .. of its block's exponent byte
         const uint8_t* exps = raw + S::kRaws * S::kRaw;
+        uint32_t from[kEach], to[kEach * kOut];  // where its chunks lie
+#pragma unroll
+        for (uint32_t x = 0; x < kEach; x++) from[x] = chunk_at<kRowBytes<D, kFmt>>(r0, c0 + x);
+#pragma unroll
+        for (uint32_t y = 0; y < kEach * kOut; y++) {
+            const uint32_t chunk = kOut * c0 + y;
+            to[y] = (chunk >> 3) * (kBN * 128) + r0 * 128 + (((chunk ^ r0) & 7) << 4);
+        }
+        bool found = false;
+        // One part of a tile; kPart: it may hold infinities and NaN that some query does not see.
+        const auto widen = [&](auto is_part, const uint8_t* src, const uint8_t* e, uint8_t* dst) {
+            constexpr bool kPart = decltype(is_part)::value;
+#pragma unroll 2
+            for (uint32_t r = 0; r < S::kPartSlots; r += kWarps * kRows) {
+                uint4 v[kEach];
+#pragma unroll
+                for (uint32_t x = 0; x < kEach; x++) v[x] = *reinterpret_cast<const uint4*>(src + r * kRowBytes<D, kFmt> + from[x]);
+                uint32_t bytes = 0;
+                if constexpr (kQuantised<kFmt>) bytes = *reinterpret_cast<const uint32_t*>(e + 4 * (r + r0));
+                const auto put = [&](uint32_t y, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
+                    if constexpr (kPart) {
+                        const uint32_t z0 = finite_or_zero<true>(h0), z1 = finite_or_zero<true>(h1), z2 = finite_or_zero<true>(h2),
+                                       z3 = finite_or_zero<true>(h3);
+                        found |= z0 != h0 || z1 != h1 || z2 != h2 || z3 != h3;
+                        h0 = z0, h1 = z1, h2 = z2, h3 = z3;
+                    }
+                    *reinterpret_cast<uint4*>(dst + r * 128 + to[y]) = make_uint4(h0, h1, h2, h3);
+                };
+                // This lane's power, twice.
+                const auto power = [&](uint32_t by) {
+                    const float f = block_scale(bytes >> by & 255u);
+                    return pack2<true>(f, f);
+                };
+                if constexpr (kFmt == kE5m2) {
+#pragma unroll
+                    for (uint32_t x = 0; x < kEach; x++) {
+                        put(2 * x, e5m2_01(v[x].x), e5m2_23(v[x].x), e5m2_01(v[x].y), e5m2_23(v[x].y));
+                        put(2 * x + 1, e5m2_01(v[x].z), e5m2_23(v[x].z), e5m2_01(v[x].w), e5m2_23(v[x].w));
+                    }
+                } else if constexpr (kFmt == kInt8) {
+                    const uint32_t s = power(shift);
+                    const auto all = [&](auto one_step) {
+#pragma unroll
+                        for (uint32_t x = 0; x < 2 * kEach; x++) {
+                            const uint32_t lo = int8_bias(x & 1 ? v[x >> 1].z : v[x >> 1].x), hi = int8_bias(x & 1 ? v[x >> 1].w : v[x >> 1].y);
+                            if constexpr (decltype(one_step)::value)
+                                put(x, int8_scaled<kInt8_01>(lo, s), int8_scaled<kInt8_23>(lo, s), int8_scaled<kInt8_01>(hi, s),
+                                    int8_scaled<kInt8_23>(hi, s));
+                            else
+                                put(x, mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
+                                    mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s));
+                        }
+                    };
+                    if (__any_sync(0xFFFFFFFFu, above_5(bytes))) all(std::false_type());
+                    else all(std::true_type());
+                } else {
+                    const uint32_t s0 = power(shift), s1 = D == 128 ? s0 : power(shift + 8);
+                    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const uint32_t s = y < 2 ? s0 : s1;
+                        uint32_t z[4];
+                        e2m1_pairs(z, w[y]);
+                        put(y, mul_half2(z[0], s), mul_half2(z[1], s), mul_half2(z[2], s), mul_half2(z[3], s));
+                    }
+                }
+            }
+        };
         for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
             const uint32_t st = n % S::kStages;
             if (n >= S::kStages && !mbar_wait_bounded(&sh.empty[st], (n / S::kStages - 1) & 1, wait)) break;
             const bool part = mine && (sh.p0 < 0 || !whole(slots.s0));
-            bool found = false;
             bool there = true;
 #pragma unroll 1
             for (uint32_t u = 0; u < S::kParts; u++) {
                 const uint32_t m = n * S::kParts + u, rs = m % S::kRaws;
                 there = mbar_wait_bounded(&sh.raw_full[rs], (m / S::kRaws) & 1, wait);
                 if (!there) break;
-#pragma unroll 1
-                for (uint32_t r = r0; r < S::kPartSlots; r += kWarps * kRows) {
-                    uint4 v[kEach];
-#pragma unroll
-                    for (uint32_t x = 0; x < kEach; x++) v[x] = *reinterpret_cast<const uint4*>(raw + rs * S::kRaw + chunk_at<kRowBytes<D, kFmt>>(r, c0 + 4 * x));
-                    uint32_t e = 0;
-                    if constexpr (kQuantised<kFmt>) e = *reinterpret_cast<const uint32_t*>(exps + rs * S::kExps + 4 * r);
-                    uint8_t* row = ring + st * S::kKV + (u * S::kPartSlots + r) * 128;
-#pragma unroll
-                    for (uint32_t x = 0; x < kEach; x++) {
-                        const uint32_t c = c0 + 4 * x, w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-                        // Chunk y of this one's FP16 values, out of infinities and NaN where the tile is partly visible.
-                        const auto put = [&](uint32_t y, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
-                            if (part) {
-                                const uint32_t z0 = finite_or_zero<true>(h0), z1 = finite_or_zero<true>(h1), z2 = finite_or_zero<true>(h2),
-                                               z3 = finite_or_zero<true>(h3);
-                                found |= z0 != h0 || z1 != h1 || z2 != h2 || z3 != h3;
-                                h0 = z0, h1 = z1, h2 = z2, h3 = z3;
-                            }
-                            const uint32_t chunk = kOut * c + y;
-                            *reinterpret_cast<uint4*>(row + (chunk >> 3) * (kBN * 128) + (((chunk ^ r) & 7) << 4)) = make_uint4(h0, h1, h2, h3);
-                        };
-                        if constexpr (kFmt == kE5m2) {
-                            put(0, e5m2_01(w[0]), e5m2_23(w[0]), e5m2_01(w[1]), e5m2_23(w[1]));
-                            put(1, e5m2_01(w[2]), e5m2_23(w[2]), e5m2_01(w[3]), e5m2_23(w[3]));
-                        } else if constexpr (kFmt == kInt8) {
-                            const uint32_t power = e >> 8 * (D == 128 ? c >> 1 : c) & 255u;
-                            const float f = block_scale(power);
-                            const uint32_t s = pack2<true>(f, f);
-                            const bool rare = __any_sync(0xFFFFFFFFu, power > kInt8OneStep);
-#pragma unroll
-                            for (int y = 0; y < 2; y++) {
-                                const uint32_t lo = int8_bias(w[2 * y]), hi = int8_bias(w[2 * y + 1]);
-                                if (rare)
-                                    put(y, mul_half2(int8_pair<kInt8_01>(lo), s), mul_half2(int8_pair<kInt8_23>(lo), s),
-                                        mul_half2(int8_pair<kInt8_01>(hi), s), mul_half2(int8_pair<kInt8_23>(hi), s));
-                                else
-                                    put(y, int8_scaled<kInt8_01>(lo, s), int8_scaled<kInt8_23>(lo, s), int8_scaled<kInt8_01>(hi, s),
-                                        int8_scaled<kInt8_23>(hi, s));
-                            }
-                        } else {
-#pragma unroll
-                            for (int y = 0; y < 4; y++) {
-                                const float f = block_scale(e >> 8 * (D == 128 ? c : 2 * c + (y >> 1)) & 255u);
-                                const uint32_t s = pack2<true>(f, f);
-                                uint32_t z[4];
-                                e2m1_pairs(z, w[y]);
-                                put(y, mul_half2(z[0], s), mul_half2(z[1], s), mul_half2(z[2], s), mul_half2(z[3], s));
-                            }
-                        }
-                    }
-                }
+                const uint8_t *src = raw + rs * S::kRaw, *e = exps + rs * S::kExps;
+                uint8_t* dst = ring + st * S::kKV + u * (S::kPartSlots * 128);
+                if (part) widen(std::true_type(), src, e, dst);
+                else widen(std::false_type(), src, e, dst);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.raw_empty[rs]);
             }

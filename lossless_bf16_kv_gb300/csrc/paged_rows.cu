@@ -99,9 +99,6 @@ __device__ __forceinline__ float power_of(uint32_t x) {
 // Whether one of four exponent bytes is 255.
 __device__ __forceinline__ bool has_nan(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x01010101u) & x & 0x80808080u) != 0; }
 
-// Whether one of them stands for more than 2^5.
-__device__ __forceinline__ bool above_5(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x7B7B7B7Bu) & x & 0x80808080u) != 0; }
-
 // The transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;

@@ -71,6 +71,8 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t (&h)[4], uint32_t r) {
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(r));
 }
+// Whether one of four exponent bytes stands for more than 2^5.
+__device__ __forceinline__ bool above_5(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x7B7B7B7Bu) & x & 0x80808080u) != 0; }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&v);
