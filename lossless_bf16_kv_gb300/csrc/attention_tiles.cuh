@@ -850,6 +850,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
         if (warp == 0) p.template place<kTwin>(sh, threadIdx.x);
         __syncthreads();
         if (!sh.count) return;
+        launch_dependents();  // the few-row kernel of the same call, which touches nothing of this one's
     }
     if (warp == 16) tmem_alloc<512>(&sh.tmem);
     if (threadIdx.x == 0) {

@@ -132,6 +132,13 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
     const Sequence seq(a, b);
     const uint32_t rows = (uint32_t)seq.count * p.group;
     const uint32_t r0 = rt * kTileRows, r1 = min(r0 + kTileRows, rows);
+    // A grid that was let start before the one ahead of it has ended ends after that: the
+    // last CTA waits for it, and the others leave their SMs to those that are to come.
+    struct AtEnd {
+        __device__ ~AtEnd() {
+            if (blockIdx.x == gridDim.x - 1) wait_prerequisite_grid();
+        }
+    } at_end;
     if (r0 >= rows || rows > p.rows_upto) return;  // with all of its cluster
     const Mask mask(seq.n, seq.count, a.window, a.sinks);
     const int32_t p0 = mask.first + (int32_t)(r0 / p.group), p1 = mask.first + (int32_t)((r1 - 1) / p.group);
@@ -624,63 +631,73 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
 }
 
 template <int D, int kFmt, int NB>
-cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, cudaStream_t s) {
+cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, bool after_tiles, cudaStream_t s) {
     using S = PagedShape<D, kFmt>;
     static_assert(S::kAtExps >= kWarpsRows * 8 * NB * D * 4, "partial results take the place of the ring");
     constexpr int kSmem = S::kAtQueries + 8 * NB * D * 2 + (int)sizeof(PagedRowsShared<S::kStages, 8 * NB>);
     Wave w;
     const cudaError_t e = launch_wave<paged_rows_kernel<D, kFmt, NB>>(32 * kWarpsRows, kSmem, w);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * kWarpsRows);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_tiles ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D, kFmt, NB>, p);
 }
 
 template <int D, int kFmt>
-cudaError_t launch_rows(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, cudaStream_t s) {
-    return tile_rows == 8 ? launch<D, kFmt, 1>(p, ctas, s) : launch<D, kFmt, 2>(p, ctas, s);
+cudaError_t launch_rows(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, bool after_tiles, cudaStream_t s) {
+    return tile_rows == 8 ? launch<D, kFmt, 1>(p, ctas, after_tiles, s) : launch<D, kFmt, 2>(p, ctas, after_tiles, s);
 }
 
 template <int D>
-cudaError_t launch_format(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, cudaStream_t s) {
+cudaError_t launch_format(const PagedRowsParams& p, uint32_t tile_rows, uint32_t ctas, bool after_tiles, cudaStream_t s) {
     switch (p.a.pool.format) {
-        case kBf16: return launch_rows<D, kBf16>(p, tile_rows, ctas, s);
-        case kE5m2: return launch_rows<D, kE5m2>(p, tile_rows, ctas, s);
-        case kInt8: return launch_rows<D, kInt8>(p, tile_rows, ctas, s);
-        default: return launch_rows<D, kE2m1>(p, tile_rows, ctas, s);
+        case kBf16: return launch_rows<D, kBf16>(p, tile_rows, ctas, after_tiles, s);
+        case kE5m2: return launch_rows<D, kE5m2>(p, tile_rows, ctas, after_tiles, s);
+        case kInt8: return launch_rows<D, kInt8>(p, tile_rows, ctas, after_tiles, s);
+        default: return launch_rows<D, kE2m1>(p, tile_rows, ctas, after_tiles, s);
     }
 }
 
 }  // namespace
 
-// Rows of a tile: 8 where a sequence has no more.
+// Rows of a tile: 8 where a sequence has no more, and in a batch with longer chunks,
+// whose other sequences are taken to bring a token each, where those have no more
+// (24 of them and a chunk of 1024 over 8k caches in 8 bits: the tokens take 62 us in
+// tiles of 8 rows and 96 in tiles of 16).
 inline uint32_t tile_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto) {
-    return std::min<uint64_t>((uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads), rows_upto) <= 8 ? 8 : 16;
+    const uint64_t group = a.q_heads / a.pool.kv_heads, most = a.max_q_tokens * group;
+    return std::min<uint64_t>(most, rows_upto) <= 8 || (most > rows_upto && group <= 8) ? 8 : 16;
 }
 
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p) {
     const uint32_t group = a.q_heads / a.pool.kv_heads, d = a.pool.head_dim, tile = tile_rows(a, rows_upto);
-    p.row_tiles = (uint32_t)((std::min<uint64_t>((uint64_t)a.max_q_tokens * group, rows_upto) + tile - 1) / tile);
+    const uint64_t most_rows = (uint64_t)a.max_q_tokens * group;
+    p.row_tiles = (uint32_t)((std::min<uint64_t>(most_rows, rows_upto) + tile - 1) / tile);
     const uint64_t units = (uint64_t)a.batch * a.pool.kv_heads * p.row_tiles;
     const uint32_t slots = 2048 / d;  // of a tile that a warp takes
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (tile + group - 1) / group + 2 * slots);
-    p.splits = attention_rows_splits(units, most, slots, 16, d, a.pool.format != kBf16 && tile == 8 ? 4 : 3);
+    p.splits = attention_rows_splits(most_rows > rows_upto ? units / p.row_tiles : units, most, slots, 16, d,
+                                     a.pool.format != kBf16 && tile == 8 ? 4 : 3);
+    // Splits in several clusters are counted by row tile, in a header of limited size.
+    if (p.splits > 8 && units > kSms) p.splits = 8;
     p.bytes = attention_rows_bytes(units, p.splits, tile, d);
     return units * p.splits <= 0x7FFFFFFFull;
 }
 
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
-                              const WaitTest& test, cudaStream_t s) {
+                              bool after_tiles, const WaitTest& test, cudaStream_t s) {
     PagedRowsParams p;
     p.a = a;
     p.group = a.q_heads / a.pool.kv_heads;
@@ -703,8 +720,8 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.counters = reinterpret_cast<uint32_t*>(workspace);
     p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
     const uint32_t ctas = a.batch * a.pool.kv_heads * plan.row_tiles * plan.splits;
-    return a.pool.head_dim == 64 ? launch_format<64>(p, tile_rows(a, rows_upto), ctas, s)
-                                    : launch_format<128>(p, tile_rows(a, rows_upto), ctas, s);
+    return a.pool.head_dim == 64 ? launch_format<64>(p, tile_rows(a, rows_upto), ctas, after_tiles, s)
+                                    : launch_format<128>(p, tile_rows(a, rows_upto), ctas, after_tiles, s);
 }
 
 }  // namespace splitzip

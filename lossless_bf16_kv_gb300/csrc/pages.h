@@ -24,8 +24,10 @@ struct PagedPlan {
 // Sequences of up to rows_upto query rows, and of more than rows_from.
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p);
 bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from, PagedPlan& p);
+// after_tiles: the launch ahead of it is launch_paged_tiles of the same call, whose end it
+// need not wait for to start.
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& p, void* workspace,
-                              const WaitTest& test, cudaStream_t s);
+                              bool after_tiles, const WaitTest& test, cudaStream_t s);
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, const PagedPlan& p, void* workspace,
                                cudaStream_t s);
 

@@ -108,7 +108,7 @@ splitzip_status splitzip_paged_attention(const splitzip_paged_attention_args* a,
         const cudaError_t e = launch_paged_tiles(*a, p.border, p.many, workspace, (cudaStream_t)s);
         if (e != cudaSuccess || !p.rows) return from_cuda(e);
     }
-    return from_cuda(launch_paged_rows(*a, p.border, p.few, workspace, WaitTest(), (cudaStream_t)s));
+    return from_cuda(launch_paged_rows(*a, p.border, p.few, workspace, p.tiles, WaitTest(), (cudaStream_t)s));
 }
 
 }  // extern "C"
