@@ -11,13 +11,16 @@
 // Both move each byte once, so HBM bounds them.  A row is shared by head_dim / 8
 // lanes of eight values (16 bytes of BF16); a group of lanes takes kRows tokens of one
 // head, and the groups of a CTA neighbouring tokens, whose rows are neighbours in
-// a page that lies head by head (E2M1 rows of head_dim 64 are 32 bytes).
+// a page that lies head by head (E2M1 rows of head_dim 64 are 32 bytes).  A group of
+// the load takes tokens that lie side by side in one page, so the page, the address
+// and (where they are contiguous) the exponent bytes are found once for them.
 #include <cstdint>
 
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "pages.cuh"
+#include "tcgen.cuh"
 
 namespace splitzip {
 namespace {
@@ -39,12 +42,13 @@ __device__ __forceinline__ Part part_of(uint32_t block, uint32_t heads, uint32_t
     return {y >> 1, x - y * heads, (block - x * token_ctas) * kTokens<D>, (y & 1) != 0};
 }
 
-// The largest magnitude's BF16 bits over the lanes of a block (`lanes` neighbours).
+// The largest magnitude's BF16 bits over the lanes of a block (`lanes` neighbours), of
+// pairs of them.
 template <int kLanes>
 __device__ __forceinline__ uint32_t block_max(uint32_t m) {
 #pragma unroll
-    for (int i = 1; i < kLanes; i *= 2) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
-    return m;
+    for (int i = 1; i < kLanes; i *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
+    return max(m & 0xFFFFu, m >> 16);
 }
 
 // The block's power from its largest magnitude's BF16 bits, and its exponent byte.
@@ -52,17 +56,22 @@ template <int kFmt>
 __device__ __forceinline__ int block_power(uint32_t top, uint32_t& e) {
     constexpr int kAway = kFmt == kInt8 ? 6 : 2, kLow = kFmt == kInt8 ? -24 : -23, kHigh = kFmt == kInt8 ? 9 : 13;
     constexpr uint32_t kNext = kFmt == kInt8 ? 127 : 96;  // fraction bits from where the next power is taken
-    const int k = min(max((int)(top >> 7) - 127 - kAway + ((top & 127u) >= kNext ? 1 : 0), kLow), kHigh);
+    const int k = min(max((int)((top + (128 - kNext)) >> 7) - 127 - kAway, kLow), kHigh);
     e = top >= 0x7F80u ? 255u : top == 0u ? 0u : (uint32_t)(k + 127);
     return k;
 }
-__device__ __forceinline__ uint32_t to_int8x4(const float* z) {
+// Four codes of values x times the power's inverse: added to 1.5 2^23, whose step is 1,
+// they are rounded to nearest even into the sum's lower byte.
+__device__ __forceinline__ uint32_t to_int8x4(const float* x, float inv) {
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) r[i] = (uint32_t)__float2int_rn(fminf(fmaxf(z[i], -127.0f), 127.0f));
+    for (int i = 0; i < 4; i++) r[i] = __float_as_uint(fmaf(x[i], inv, 12582912.0f));
     return prmt(prmt(r[0], r[1], 0x0040), prmt(r[2], r[3], 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint32_t to_e2m1x8(const float* z) {
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* x, float inv) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) z[i] = x[i] * inv;
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -119,22 +128,24 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
             if constexpr (kFmt == kE5m2) {
                 if (there) *reinterpret_cast<uint2*>(to + row + 8 * lane) = make_uint2(pack4_e5m2(f), pack4_e5m2(f + 4));
             } else {
-                uint32_t top = 0, e;
-#pragma unroll
-                for (int i = 0; i < 4; i++) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
-                top = block_max<kLanes / 4>(top);
+                uint32_t e;
+                const uint32_t top = block_max<kLanes / 4>(__vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                                                    __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu)));
                 const int k = block_power<kFmt>(top, e);
-                // A block that holds an infinity or a NaN gets codes 0.
+                // 0 for a block that holds an infinity or a NaN: its codes are 0 below.
                 const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
+                if (kFmt == kInt8 && top >= 0x477Fu) {  // from 65280 on, 127.5 times the largest power
 #pragma unroll
-                for (int i = 0; i < 8; i++) f[i] = e == 255u ? 0.0f : f[i] * inv;
+                    for (int i = 0; i < 8; i++) f[i] = fminf(fmaxf(f[i], -65024.0f), 65024.0f);
+                }
+                const bool odd = top >= 0x7F80u;
                 // The four exponent bytes, gathered over the row's lanes.
                 e <<= 8 * (lane / (kLanes / 4));
 #pragma unroll
                 for (uint32_t i = kLanes / 4; i < kLanes; i *= 2) e |= __shfl_xor_sync(0xFFFFFFFFu, e, i);
                 if (there) {
-                    if constexpr (kFmt == kInt8) *reinterpret_cast<uint2*>(to + row + 8 * lane) = make_uint2(to_int8x4(f), to_int8x4(f + 4));
-                    else *reinterpret_cast<uint32_t*>(to + row + 4 * lane) = to_e2m1x8(f);
+                    if constexpr (kFmt == kInt8) *reinterpret_cast<uint2*>(to + row + 8 * lane) = odd ? make_uint2(0, 0) : make_uint2(to_int8x4(f, inv), to_int8x4(f + 4, inv));
+                    else *reinterpret_cast<uint32_t*>(to + row + 4 * lane) = odd ? 0u : to_e2m1x8(f, inv);
                     if (lane == 0)
                         *reinterpret_cast<uint32_t*>(out.exponents + page * out.exp_stride_p + at * out.exp_stride_t +
                                                      part.h * out.exp_stride_h) = e;
@@ -144,87 +155,114 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
     }
 }
 
+// Eight values of a row, as they lie in a page, in BF16; bytes: the row's exponents.
+template <int D, int kFmt>
+__device__ __forceinline__ uint4 to_bf16(uint4 x, uint32_t bytes, uint32_t lane) {
+    if constexpr (kFmt == kBf16) return x;
+    uint32_t h[4];
+    if constexpr (kFmt == kE5m2) {
+        const uint32_t w[4] = {e5m2_01(x.x), e5m2_23(x.x), e5m2_01(x.y), e5m2_23(x.y)};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float2 f = unpack2<true>(w[i]);
+            h[i] = pack2<false>(f.x, f.y);
+        }
+    } else {
+        const float f = block_scale(bytes >> 8 * (lane / (D / 32)) & 255u);
+        const uint64_t scale = pair(f, f);
+        if constexpr (kFmt == kInt8) {
+            // A byte b as 2^23 + (b + 128), less what is too much: exact in 32 bits.
+            const uint64_t less = pair(-8388736.0f, -8388736.0f);
+            const uint32_t w[2] = {int8_bias(x.x), int8_bias(x.y)};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t s = 0x7440u + 2 * (i & 1);
+                float a, b;
+                unpair(mul2(add2(pair(__uint_as_float(prmt(w[i >> 1], 0x4B000000u, s)), __uint_as_float(prmt(w[i >> 1], 0x4B000000u, s + 1))), less), scale), a, b);
+                h[i] = pack2<false>(a, b);
+            }
+        } else {
+            uint32_t w[4];
+            e2m1_pairs(w, x.x);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 g = unpack2<true>(w[i]);
+                float a, b;
+                unpair(mul2(pair(g.x, g.y), scale), a, b);
+                h[i] = pack2<false>(a, b);
+            }
+        }
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// A group's kRows tokens from t on (all of one page), of one head of keys or values, up
+// to token n: put(row, x) takes eight values in BF16, or (kCopy) E5M2 rows as they are.
+template <int D, int kFmt, bool kCopy, class Put>
+__device__ __forceinline__ void load_rows(const splitzip_pool& pool, const splitzip_page_rows& in, uint32_t page, uint32_t h, uint32_t t, uint32_t n,
+                                          bool bulk_exps, uint32_t lane, const Put& put) {
+    const bool bad = page >= pool.pages;
+    const int64_t at = t & (pool.page_tokens - 1), from = bad ? 0 : page;
+    const uint8_t* src = static_cast<const uint8_t*>(in.data) + (kFmt == kBf16 ? 2 : 1) * (from * in.stride_p + at * in.stride_t + h * in.stride_h) +
+                         kRowBytes<D, kFmt> / (D / 8) * lane;
+    const int64_t step = (kFmt == kBf16 ? 2 : 1) * in.stride_t;
+    uint4 x[kRows];
+    uint32_t e[kRows] = {};
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        x[r] = make_uint4(0, 0, 0, 0);
+        if constexpr (kFmt == kBf16) {
+            x[r] = ld_stream16(src + r * step);
+        } else if constexpr (kFmt == kE2m1) {
+            x[r].x = ld_stream4(src + r * step);
+        } else {
+            const uint2 y = ld_stream8(src + r * step);
+            x[r].x = y.x, x[r].y = y.y;
+        }
+    }
+    if constexpr (kQuantised<kFmt>) {
+        const uint8_t* bytes = in.exponents + from * in.exp_stride_p + at * in.exp_stride_t + h * in.exp_stride_h;
+        if (bulk_exps) {
+            const uint4 y = *reinterpret_cast<const uint4*>(bytes);
+            e[0] = y.x, e[1] = y.y, e[2] = y.z, e[3] = y.w;
+        } else {
+#pragma unroll
+            for (int r = 0; r < kRows; r++) e[r] = *reinterpret_cast<const uint32_t*>(bytes + r * in.exp_stride_t);
+        }
+    }
+    static_assert(kRows == 4, "four rows' exponents in 16 bytes");
+#pragma unroll
+    for (int r = 0; r < kRows; r++) {
+        if (t + r >= n) break;
+        if constexpr (kCopy) put(t + r, bad ? make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0, 0) : x[r]);
+        else put(t + r, bad ? make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u) : to_bf16<D, kFmt>(x[r], e[r], lane));
+    }
+}
+
 struct LoadParams {
     splitzip_pages_load_args a;
-    uint32_t token_ctas, page_shift;
+    uint32_t token_ctas, page_shift, bulk_exps;
 };
 
 // kCopy: E5M2 rows as they are.
 template <int D, int kFmt, bool kCopy>
 __global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_constant__ LoadParams p) {
-    constexpr uint32_t kLanes = D / 8, kGroups = kThreadsPages / kLanes;
+    constexpr uint32_t kLanes = D / 8;
     const splitzip_pages_load_args& a = p.a;
     const Part part = part_of<D>(blockIdx.x, a.pool.kv_heads, p.token_ctas);
     const int32_t len = a.lens ? a.lens[part.b] : (int32_t)a.tokens;
     const uint32_t n = len < 0 ? 0u : min((uint32_t)len, a.tokens);
-    if (part.first >= n) return;
-    const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const splitzip_page_rows& in = part.v ? a.pool.v : a.pool.k;
+    const uint32_t lane = threadIdx.x % kLanes, t = part.first + threadIdx.x / kLanes * kRows;
+    if (t >= n) return;
     const splitzip_view& out = part.v ? a.v_out : a.k_out;
-    const int32_t* table = a.table + (uint64_t)part.b * a.table_width;
-    const uint8_t* src = static_cast<const uint8_t*>(in.data) + kRowBytes<D, kFmt> / kLanes * lane;
-    uint32_t page[kRows], e[kRows];
-    uint4 x[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-        const uint32_t t = part.first + r * kGroups + group;
-        page[r] = t < n ? (uint32_t)table[t >> p.page_shift] : 0xFFFFFFFFu;
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-        const uint32_t at = (part.first + r * kGroups + group) & (a.pool.page_tokens - 1);
-        x[r] = make_uint4(0, 0, 0, 0);
-        e[r] = 0;
-        if (page[r] < a.pool.pages) {
-            const int64_t row = page[r] * in.stride_p + at * in.stride_t + part.h * in.stride_h;
-            if constexpr (kFmt == kBf16) {
-                x[r] = ld_stream16(src + 2 * row);
-            } else if constexpr (kFmt == kE2m1) {
-                x[r].x = ld_stream4(src + row);
-            } else {
-                const uint2 y = ld_stream8(src + row);
-                x[r].x = y.x, x[r].y = y.y;
-            }
-            if constexpr (kQuantised<kFmt>)
-                e[r] = in.exponents[page[r] * in.exp_stride_p + at * in.exp_stride_t + part.h * in.exp_stride_h + lane / (kLanes / 4)];
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; r++) {
-        const uint32_t t = part.first + r * kGroups + group;
-        if (t >= n) continue;
-        const bool bad = page[r] >= a.pool.pages;
-        const int64_t row = part.b * out.stride_b + (int64_t)t * out.stride_t + part.h * out.stride_h;
-        if constexpr (kCopy) {
-            st_stream8(static_cast<uint8_t*>(out.data) + row + 8 * lane, bad ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : make_uint2(x[r].x, x[r].y));
-            continue;
-        }
-        uint32_t h[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-        if constexpr (kFmt == kE5m2) {
-            const uint32_t w[4] = {e5m2_01(x[r].x), e5m2_23(x[r].x), e5m2_01(x[r].y), e5m2_23(x[r].y)};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 f = unpack2<true>(w[i]);
-                h[i] = pack2<false>(f.x, f.y);
-            }
-        } else if constexpr (kQuantised<kFmt>) {
-            uint32_t w[4];
-            if constexpr (kFmt == kInt8) {
-                const uint32_t lo = int8_bias(x[r].x), hi = int8_bias(x[r].y);
-                w[0] = int8_pair<kInt8_01>(lo), w[1] = int8_pair<kInt8_23>(lo), w[2] = int8_pair<kInt8_01>(hi), w[3] = int8_pair<kInt8_23>(hi);
-            } else {
-                e2m1_pairs(w, x[r].x);
-            }
-            const float scale = block_scale(e[r]);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 f = unpack2<true>(w[i]);
-                h[i] = pack2<false>(f.x * scale, f.y * scale);
-            }
-        }
-        if (bad) h[0] = h[1] = h[2] = h[3] = 0x7FC07FC0u;
-        st_stream16(static_cast<uint8_t*>(out.data) + 2 * row + 16 * lane, make_uint4(h[0], h[1], h[2], h[3]));
-    }
+    constexpr int kElem = kCopy ? 1 : 2;
+    uint8_t* to = static_cast<uint8_t*>(out.data) + kElem * (part.b * out.stride_b + part.h * out.stride_h + 8 * lane);
+    const uint32_t page = (uint32_t)a.table[(uint64_t)part.b * a.table_width + (t >> p.page_shift)];
+    load_rows<D, kFmt, kCopy>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane, [&](uint32_t row, uint4 x) {
+        uint8_t* at = to + kElem * ((int64_t)row * out.stride_t);
+        if constexpr (kCopy) st_stream8(at, make_uint2(x.x, x.y));
+        else st_stream16(at, x);
+    });
 }
 
 inline uint32_t log2_of(uint32_t x) {
@@ -250,7 +288,7 @@ cudaError_t store(const splitzip_pages_store_args& a, cudaStream_t s) {
 template <int D>
 cudaError_t load(const splitzip_pages_load_args& a, cudaStream_t s) {
     const uint32_t token_ctas = (a.tokens + kTokens<D> - 1) / kTokens<D>;
-    const LoadParams p{a, token_ctas, log2_of(a.pool.page_tokens)};
+    const LoadParams p{a, token_ctas, log2_of(a.pool.page_tokens), bulk_exponents(a.pool)};
     const uint32_t ctas = token_ctas * a.pool.kv_heads * 2 * a.batch;
     switch (a.pool.format) {
         case kBf16: load_kernel<D, kBf16, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
