@@ -126,6 +126,7 @@ struct TilesShared {
     // 0, the step that jumps from the sinks to the window and to where.
     uint32_t b, h, t0, steps;
     int32_t first_row, count;  // a packed sequence's first query token, and their number
+    uint32_t rank;             // its number among those of the launch
     int32_t s0, jump_at, jump_to;
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
@@ -287,7 +288,7 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
     uint8_t* exps = raw + S::kRaws * S::kRaw;  // of each raw stage, by slot
     const bool bulk = kQuantised<kFmt> && p.bulk_exps;
     constexpr uint32_t kParts = S::kParts;
-    const uint32_t part_boxes = p.boxes / kParts, slots_mask = p.a.pool.page_tokens - 1;
+    const uint32_t part_boxes = p.boxes / kParts, slots_mask = p.slot_mask;
     uint32_t now = look_up(0), ahead = look_up(1), i = 0;  // i: of the parts of the keys', values', next keys' .. tiles
     for (uint32_t st = 0, ph = 0; i < 2 * kParts * steps; i++) {
         if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
@@ -849,8 +850,11 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
     if constexpr (Params::kPaged) {  // more CTAs than the sequences' row tiles need: the others leave, with their clusters
         if (warp == 0) p.template place<kTwin>(sh, threadIdx.x);
         __syncthreads();
-        if (!sh.count) return;
-        launch_dependents();  // the few-row kernel of the same call, which touches nothing of this one's
+        launch_dependents();  // another launch of the same call, which touches nothing of this one's
+        if (!sh.count) {
+            if (blockIdx.x == gridDim.x - 1) wait_prerequisite_grid();
+            return;
+        }
     }
     if (warp == 16) tmem_alloc<512>(&sh.tmem);
     if (threadIdx.x == 0) {
@@ -1032,27 +1036,31 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
     __syncthreads();
     tcgen_fence_after();
     if (warp == 16) tmem_free<512>(tmem);
+    // As such another launch, this one ends after the one ahead of it.
+    if (Params::kPaged && blockIdx.x == gridDim.x - 1) wait_prerequisite_grid();
 }
 
 template <int D, int kFmt, bool kTwin, class Params>
-cudaError_t launch_tiles(const Params& p, uint32_t ctas, cudaStream_t s) {
+cudaError_t launch_tiles(const Params& p, uint32_t ctas, cudaStream_t s, bool beside = false) {
     using S = TilesShape<D, kFmt, Params::kPaged>;
     constexpr int kSmem = S::kUsed + (int)sizeof(TilesShared) - (S::kOneRow ? (int)sizeof(TilesShared::row) / 2 : 0);
     static_assert(kSmem <= 232448, "shared memory of a CTA");
     Wave w;
     const cudaError_t e = launch_wave<tiles_kernel<D, kFmt, kTwin, Params>>(TilesShape<D, kFmt, Params::kPaged>::kThreads, kSmem, w);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = p.splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(TilesShape<D, kFmt, Params::kPaged>::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = beside ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kFmt, kTwin, Params>, p);
 }
 

@@ -23,7 +23,9 @@ struct PagedTilesParams {
     uint32_t box, boxes;       // slots to a TMA box, and boxes to a tile
     uint32_t page_shift;
     uint32_t bulk_exps;        // a page's exponent bytes of a head are contiguous, in multiples of 16 bytes
-    uint32_t rows_from;        // only sequences with more query rows than this
+    uint32_t slot_mask;        // of a slot within its page
+    uint32_t rows_from, rows_upto;  // only sequences with more query rows than the one, up to the other
+    uint32_t widened;          // the pool holds one page for each of these sequences, in their order
     uint32_t* status;
     uint32_t wait_limit;
 
@@ -35,7 +37,7 @@ struct PagedTilesParams {
     __device__ __forceinline__ uint32_t ctas_of(uint32_t b) const {
         if (b >= a.batch) return 0;
         const uint32_t count = (uint32_t)sequence_count(a, a.q_start[b], a.q_start[b + 1]), per = kTwin ? tokens : 2 * tokens;
-        return count * group > rows_from ? (count + per - 1) / per : 0;
+        return count * group > rows_from && count * group <= rows_upto ? (count + per - 1) / per : 0;
     }
     // This CTA's part of the work: one warp.  count stays 0 where there is none.  The last
     // sequence's last tiles, which see the most of its slots, go first.
@@ -47,9 +49,9 @@ struct PagedTilesParams {
         for (uint32_t b = 0; b < a.batch; b += 32) total += __reduce_add_sync(0xFFFFFFFFu, ctas_of<kTwin>(b + lane));
         if (lane == 0) sh.count = 0;
         if (at >= total) return;
-        uint32_t left = total - 1 - at;  // row tiles before this one
+        uint32_t left = total - 1 - at, before = 0;  // row tiles, and sequences, before this one
         for (uint32_t b = 0; b < a.batch; b += 32) {
-            const uint32_t mine = ctas_of<kTwin>(b + lane);
+            const uint32_t mine = ctas_of<kTwin>(b + lane), some = __ballot_sync(0xFFFFFFFFu, mine != 0);
             uint32_t upto = mine;
 #pragma unroll
             for (int i = 1; i < 32; i *= 2) {
@@ -59,6 +61,7 @@ struct PagedTilesParams {
             const uint32_t found = __ballot_sync(0xFFFFFFFFu, left < upto);
             if (!found) {
                 left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+                before += __popc(some);
                 continue;
             }
             if (lane == (uint32_t)__ffs(found) - 1) {
@@ -67,6 +70,7 @@ struct PagedTilesParams {
                 sh.h = h;
                 sh.first_row = seq.row;
                 sh.count = seq.count;
+                sh.rank = before + __popc(some & ((1u << lane) - 1u));
                 set_work<kTwin>(sh, Mask(seq.n, seq.count, a.window, a.sinks), (left - (upto - mine)) * (kTwin ? tokens : 2 * tokens),
                                 (uint32_t)seq.count, tokens, split, splits);
             }
@@ -89,7 +93,7 @@ struct PagedTilesParams {
         return s <= sh.p1 && ((int64_t)s + run > (int64_t)sh.p0 - (int64_t)sh.window + 1 || s < sh.sinks);
     }
     __device__ __forceinline__ uint32_t page(const volatile TilesShared& sh, int32_t s) const {
-        return (uint32_t)a.table[(uint64_t)sh.b * a.table_width + ((uint32_t)s >> page_shift)];
+        return widened ? sh.rank : (uint32_t)a.table[(uint64_t)sh.b * a.table_width + ((uint32_t)s >> page_shift)];
     }
     // The rows of this CTA's values by slot; none where the page is outside the pool.
     struct Row {
@@ -101,7 +105,7 @@ struct PagedTilesParams {
             const splitzip_page_rows& v = a.pool.v;
             const uint32_t x = page(sh, s);
             if (x >= a.pool.pages) return Row{nullptr, nullptr};
-            const int64_t at = (uint32_t)s & (a.pool.page_tokens - 1);
+            const int64_t at = (uint32_t)s & slot_mask;
             return Row{static_cast<const uint8_t*>(v.data) + (x * v.stride_p + at * v.stride_t + (int64_t)sh.h * v.stride_h) * kElem,
                        v.exponents + x * v.exp_stride_p + at * v.exp_stride_t + (int64_t)sh.h * v.exp_stride_h};
         };
@@ -119,18 +123,18 @@ uint32_t tile_part_of(uint32_t format) {
 inline uint32_t tile_part(const splitzip_pool& p) { return p.head_dim == 64 ? tile_part_of<64>(p.format) : tile_part_of<128>(p.format); }
 
 template <int D, bool kTwin>
-cudaError_t launch_paged_format(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s) {
+cudaError_t launch_paged_format(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s) {
     switch (p.a.pool.format) {
-        case kBf16: return launch_tiles<D, kBf16, kTwin>(p, ctas, s);
-        case kE5m2: return launch_tiles<D, kE5m2, kTwin>(p, ctas, s);
-        case kInt8: return launch_tiles<D, kInt8, kTwin>(p, ctas, s);
-        default: return launch_tiles<D, kE2m1, kTwin>(p, ctas, s);
+        case kBf16: return launch_tiles<D, kBf16, kTwin>(p, ctas, s, beside);
+        case kE5m2: return launch_tiles<D, kE5m2, kTwin>(p, ctas, s, beside);
+        case kInt8: return launch_tiles<D, kInt8, kTwin>(p, ctas, s, beside);
+        default: return launch_tiles<D, kE2m1, kTwin>(p, ctas, s, beside);
     }
 }
 // One for each head_dim and kind of tile, compiled side by side.
-cudaError_t launch_paged_64(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
-cudaError_t launch_paged_64_twin(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
-cudaError_t launch_paged_128(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
-cudaError_t launch_paged_128_twin(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s);
+cudaError_t launch_paged_64(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s);
+cudaError_t launch_paged_64_twin(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s);
+cudaError_t launch_paged_128(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s);
+cudaError_t launch_paged_128_twin(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s);
 
 }  // namespace splitzip

@@ -3,6 +3,8 @@
 
 namespace splitzip {
 
-cudaError_t launch_paged_128(const PagedTilesParams& p, uint32_t ctas, cudaStream_t s) { return launch_paged_format<128, false>(p, ctas, s); }
+cudaError_t launch_paged_128(const PagedTilesParams& p, uint32_t ctas, bool beside, cudaStream_t s) {
+    return launch_paged_format<128, false>(p, ctas, beside, s);
+}
 
 }  // namespace splitzip

@@ -265,6 +265,42 @@ __global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_consta
     });
 }
 
+struct WidenParams {
+    splitzip_paged_attention_args a;
+    uint32_t token_ctas, page_shift, bulk_exps;
+    uint32_t group, rows_from, sequences, tokens;  // tokens of a widened cache
+    uint8_t* to;
+};
+
+template <int D, int kFmt>
+__global__ void __launch_bounds__(kThreadsPages) widen_kernel(const __grid_constant__ WidenParams p) {
+    constexpr uint32_t kLanes = D / 8;
+    const splitzip_paged_attention_args& a = p.a;
+    __shared__ int32_t found, from, count, len;
+    const Part part = part_of<D>(blockIdx.x, a.pool.kv_heads, p.token_ctas);
+    if (threadIdx.x < 32) {  // the part.b-th long sequence
+        const uint32_t b = nth_long(a, part.b, p.group, p.rows_from, threadIdx.x);
+        if (threadIdx.x == 0) {
+            found = (int32_t)b;
+            if (b < a.batch) {
+                const Sequence s(a, b);
+                from = s.row, count = s.count, len = s.n;
+            }
+        }
+    }
+    __syncthreads();
+    if (found >= (int32_t)a.batch) return;
+    const uint32_t lane = threadIdx.x % kLanes, t = part.first + threadIdx.x / kLanes * kRows, n = (uint32_t)len;
+    if (t >= n) return;
+    // What no query sees need not be there, and its page may have been given away.
+    const Mask mask(len, count, a.window, a.sinks);
+    if ((int64_t)t + kRows <= (int64_t)mask.first - (int64_t)mask.window + 1 && (int32_t)t >= mask.sinks) return;
+    uint8_t* to = p.to + 2 * ((((uint64_t)part.b * 2 + part.v) * a.pool.kv_heads + part.h) * p.tokens * D + 8 * lane);
+    const uint32_t page = (uint32_t)a.table[(uint64_t)found * a.table_width + (t >> p.page_shift)];
+    load_rows<D, kFmt, false>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane,
+                              [&](uint32_t row, uint4 x) { *reinterpret_cast<uint4*>(to + 2 * (uint64_t)row * D) = x; });
+}
+
 inline uint32_t log2_of(uint32_t x) {
     uint32_t n = 0;
     while (x >>= 1) n++;
@@ -304,6 +340,29 @@ cudaError_t load(const splitzip_pages_load_args& a, cudaStream_t s) {
 
 }  // namespace
 
+template <int D>
+static cudaError_t widen(const WidenParams& p, cudaStream_t s) {
+    const uint32_t ctas = p.token_ctas * p.a.pool.kv_heads * 2 * p.sequences;
+    switch (p.a.pool.format) {
+        case kE5m2: widen_kernel<D, kE5m2><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kInt8: widen_kernel<D, kInt8><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        default: widen_kernel<D, kE2m1><<<ctas, kThreadsPages, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+cudaError_t launch_paged_widen(const splitzip_paged_attention_args& a, uint32_t rows_from, void* widened, cudaStream_t s) {
+    const uint32_t tokens = a.pool.head_dim == 64 ? kTokens<64> : kTokens<128>;
+    WidenParams p{a};
+    p.token_ctas = (a.kv_tokens + tokens - 1) / tokens;
+    p.page_shift = log2_of(a.pool.page_tokens);
+    p.bulk_exps = bulk_exponents(a.pool);
+    p.group = a.q_heads / a.pool.kv_heads;
+    p.rows_from = rows_from;
+    p.sequences = (uint32_t)widened_sequences(a, rows_from);
+    p.tokens = (uint32_t)widened_tokens(a);
+    p.to = static_cast<uint8_t*>(widened);
+    return a.pool.head_dim == 64 ? widen<64>(p, s) : widen<128>(p, s);
+}
 cudaError_t launch_pages_store(const splitzip_pages_store_args& a, cudaStream_t s) {
     return a.pool.head_dim == 64 ? store<64>(a, s) : store<128>(a, s);
 }

@@ -36,6 +36,19 @@ struct Sequence {
     }
 };
 
+// The n-th (from 0) sequence with more than rows_from query rows; a.batch where there is
+// none.  A whole warp.
+__device__ __forceinline__ uint32_t nth_long(const splitzip_paged_attention_args& a, uint32_t n, uint32_t group, uint32_t rows_from, uint32_t lane) {
+    for (uint32_t b = 0; b < a.batch; b += 32) {
+        const bool is = b + lane < a.batch && (uint32_t)sequence_count(a, a.q_start[b + lane], a.q_start[b + lane + 1]) * group > rows_from;
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, is), before = __popc(found & ((1u << lane) - 1u));
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, is && before == n);
+        if (hit) return b + (uint32_t)__ffs(hit) - 1;
+        n -= __popc(found);
+    }
+    return a.batch;
+}
+
 // 2^(e - 127) for an exponent byte: 0 for 0, NaN for 255.
 __device__ __forceinline__ float block_scale(uint32_t e) {
     const uint32_t bits = e << 23;

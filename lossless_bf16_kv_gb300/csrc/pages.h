@@ -21,15 +21,31 @@ struct PagedPlan {
     uint32_t splits;
     size_t bytes;        // of workspace
 };
-// Sequences of up to rows_upto query rows, and of more than rows_from.
+// Sequences of up to rows_upto query rows, and of more than rows_from, up to rows_upto.
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p);
-bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from, PagedPlan& p);
+bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, PagedPlan& p);
 // after_tiles: the launch ahead of it is launch_paged_tiles of the same call, whose end it
 // need not wait for to start.
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& p, void* workspace,
                               bool after_tiles, const WaitTest& test, cudaStream_t s);
-cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, const PagedPlan& p, void* workspace,
-                               cudaStream_t s);
+// beside: the launch ahead of it is another of the same call, whose end it need not wait
+// for.  widened: the sequences' caches in BF16, as launch_paged_widen leaves them (or
+// NULL: they are read from the pool).
+cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& p, void* workspace,
+                               const void* widened, bool beside, cudaStream_t s);
+
+// The caches of a batch's long sequences (more than rows_from query rows) in BF16, one
+// after the other in the batch's order: keys, then values, head by head, of
+// widened_tokens tokens each.
+inline uint64_t widened_sequences(const splitzip_paged_attention_args& a, uint32_t rows_from) {
+    const uint64_t rows = (uint64_t)a.tokens * (a.q_heads / a.pool.kv_heads);
+    return rows / (rows_from + 1) < a.batch ? rows / (rows_from + 1) : a.batch;
+}
+inline uint64_t widened_tokens(const splitzip_paged_attention_args& a) { return ((uint64_t)a.kv_tokens + 127) / 128 * 128; }
+inline uint64_t widened_bytes(const splitzip_paged_attention_args& a, uint32_t rows_from) {
+    return widened_sequences(a, rows_from) * widened_tokens(a) * a.pool.kv_heads * a.pool.head_dim * 4;
+}
+cudaError_t launch_paged_widen(const splitzip_paged_attention_args& a, uint32_t rows_from, void* widened, cudaStream_t s);
 
 // Whether a page's exponent bytes of a head are contiguous and may be copied in
 // multiples of 16 bytes.

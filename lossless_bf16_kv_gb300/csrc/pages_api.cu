@@ -38,25 +38,37 @@ bool sizes_ok(const splitzip_paged_attention_args& a) {
            (uint64_t)a.batch * hk * a.tokens <= kMax31;
 }
 
-// Which kernel takes a sequence: tiles of 128 query rows on the tensor cores from 17
-// rows of a key/value head on.  With one sequence that may have as many, they take it
-// whatever it has.
+// Which kernels take a call's sequences, by their query rows (new tokens times the heads
+// of a group).
 struct Plans {
-    bool rows, tiles;
-    uint32_t border;  // the most rows of the few-row kernel
-    PagedPlan few, many;
-    size_t bytes;
+    bool few, some, many;   // which of them may have sequences
+    uint32_t upto, from;    // the most rows of the few-row kernel; more than that many: over caches widened first
+    PagedPlan rows, tiles, wide;
+    size_t at_wide, bytes;  // of the workspace: where the widened caches lie, and in all
 };
 bool plan(const splitzip_paged_attention_args& a, Plans& p) {
-    constexpr uint32_t kFewRows = 16;
-    p.tiles = (uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads) > kFewRows;
-    p.rows = !p.tiles || a.batch > 1;
-    p.border = p.rows ? kFewRows : 0;
-    p.bytes = 0;
-    if (p.rows && !paged_rows_plan(a, p.border, p.few)) return false;
-    if (p.tiles && !paged_tiles_plan(a, p.border, p.many)) return false;
-    if (p.rows) p.bytes = p.few.bytes;
-    if (p.tiles && p.many.bytes > p.bytes) p.bytes = p.many.bytes;
+    constexpr uint32_t kFewRows = 16, kManyRows = 512;
+    constexpr uint64_t kMostWidened = 4ull << 30;
+    const uint64_t most = (uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads);
+    // Tiles of 128 query rows on the tensor cores from 17 rows on.  One sequence that may
+    // have as many goes to them whatever it has.
+    p.few = most <= kFewRows || a.batch > 1;
+    p.upto = p.few ? kFewRows : 0;
+    // With two pairs of such tiles to a sequence and head, widening its cache to BF16 first
+    // costs less than widening each tile of slots for each pair.
+    p.from = a.batch > 1 ? kManyRows : 0;
+    p.many = a.pool.format != SPLITZIP_FORMAT_BF16 && most > kManyRows && widened_bytes(a, p.from) <= kMostWidened;
+    p.some = most > kFewRows && !(p.many && a.batch == 1);
+    if (!p.many) p.from = 0xFFFFFFFFu;
+    p.bytes = kAttentionHeader;
+    const auto also = [&](const PagedPlan& x) { p.bytes = x.bytes > p.bytes ? x.bytes : p.bytes; };
+    if (p.few && !paged_rows_plan(a, p.upto, p.rows)) return false;
+    if (p.few) also(p.rows);
+    if (p.some && !paged_tiles_plan(a, p.upto, p.from, p.tiles)) return false;
+    if (p.some) also(p.tiles);
+    if (p.many && !paged_tiles_plan(a, p.from, 0xFFFFFFFFu, p.wide)) return false;
+    p.at_wide = (p.bytes + 127) / 128 * 128;
+    if (p.many) p.bytes = p.at_wide + widened_bytes(a, p.from);
     return true;
 }
 
@@ -104,11 +116,16 @@ splitzip_status splitzip_paged_attention(const splitzip_paged_attention_args* a,
         !aligned(a->lse, 4) || !std::isfinite(a->scale) || !(a->scale > 0.0f))
         return SPLITZIP_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
-    if (p.tiles) {
-        const cudaError_t e = launch_paged_tiles(*a, p.border, p.many, workspace, (cudaStream_t)s);
-        if (e != cudaSuccess || !p.rows) return from_cuda(e);
+    const cudaStream_t stream = (cudaStream_t)s;
+    cudaError_t e = cudaSuccess;
+    if (p.many) {
+        void* wide = static_cast<uint8_t*>(workspace) + p.at_wide;
+        e = launch_paged_widen(*a, p.from, wide, stream);
+        if (e == cudaSuccess) e = launch_paged_tiles(*a, p.from, 0xFFFFFFFFu, p.wide, workspace, wide, false, stream);
     }
-    return from_cuda(launch_paged_rows(*a, p.border, p.few, workspace, p.tiles, WaitTest(), (cudaStream_t)s));
+    if (e == cudaSuccess && p.some) e = launch_paged_tiles(*a, p.upto, p.from, p.tiles, workspace, nullptr, p.many, stream);
+    if (e == cudaSuccess && p.few) e = launch_paged_rows(*a, p.upto, p.rows, workspace, p.many || p.some, WaitTest(), stream);
+    return from_cuda(e);
 }
 
 }  // extern "C"
