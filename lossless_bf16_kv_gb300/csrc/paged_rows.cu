@@ -688,7 +688,10 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
     const uint32_t slots = 2048 / d;  // of a tile that a warp takes
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (tile + group - 1) / group + 2 * slots);
-    p.splits = attention_rows_splits(most_rows > rows_upto ? units / p.row_tiles : units, most, slots, 16, d,
+    // In a batch with longer chunks one of the sequences is such a one, and of the others'
+    // row tiles the first has the rows.
+    const uint64_t likely = most_rows > rows_upto ? (uint64_t)std::max(1u, a.batch - 1) * a.pool.kv_heads : units;
+    p.splits = attention_rows_splits(likely, most, slots, 16, d,
                                      a.pool.format != kBf16 && tile == 8 ? 4 : 3);
     // Splits in several clusters are counted by row tile, in a header of limited size.
     if (p.splits > 8 && units > kSms) p.splits = 8;
