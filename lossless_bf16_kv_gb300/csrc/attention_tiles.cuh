@@ -87,11 +87,11 @@ template <int D, int kFmt, bool kPaged>
 struct TilesShape {
     static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
     // Where it is widened, a tile comes as it lies in the cache, in one part or two, of kRaw bytes and kExps of exponents.
-    static constexpr int kParts = kPaged && kWide<kFmt> && kRowBytes<D, kFmt> == 128 ? 2 : 1, kPartSlots = kBN / kParts;
+    static constexpr int kParts = kPaged && kWide<kFmt> && D == 128 ? 2 : 1, kPartSlots = kBN / kParts;
     static constexpr int kRaw = kPartSlots * kRowBytes<D, kFmt>;
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
-    static constexpr int kStages = D == 128 ? (kWide<kFmt> ? 4 : 5) : (kWide<kFmt> ? 6 : 8);
-    static constexpr int kRaws = !kWide<kFmt> ? 0 : kParts == 2 || (kPaged && D == 64) ? 4 : kFmt == kE2m1 ? 3 : 2;
+    static constexpr int kStages = D == 128 ? (kWide<kFmt> || kPaged ? 4 : 5) : (kWide<kFmt> ? 6 : 8);
+    static constexpr int kRaws = !kWide<kFmt> ? 0 : kPaged ? 4 : 2;
     static constexpr int kExps = kQuantised<kFmt> ? kPartSlots * 4 : 0;
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
@@ -99,7 +99,8 @@ struct TilesShape {
     static constexpr int kTend = kManyTend ? 10 : kWide<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
     static constexpr int kRegs = kWide<kFmt> ? 96 : 104, kOtherRegs = kManyTend ? 40 : kWide<kFmt> ? 48 : 64;
     // Warps that widen a tile, and those that say that its values are fit.
-    static constexpr int kWiden = kManyTend ? 4 : kTend / 2, kFit = kWide<kFmt> ? kWiden : kTend;
+    static constexpr int kTenders = kManyTend ? 8 : kPaged ? 1 : kTend;  // the next one loads the values' pages
+    static constexpr int kWiden = kTenders > 1 ? kTenders / 2 : 1, kFit = kWide<kFmt> ? kWiden : kTenders;
     static_assert(kThreads % 128 == 0 && kSoftmax * kRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8),
                   "register shares add up to what the CTA is launched with");
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
@@ -264,16 +265,18 @@ __device__ __forceinline__ void load_tiles(const Params& p, TilesShared& sh, uin
     for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded<true>(&full[x % kN], (x / kN) & 1, wait);
 }
 
-// The same from pages, a tile being one or more boxes of slots of one page each: lane i
-// of the warp looks up and loads box i, the page from one step ahead.  What no query
-// sees, or lies outside the pool, is loaded from behind its last page: as zeros.
+// The keys' tiles, or the values', from pages, a tile being one or more boxes of
+// slots of one page each: lane i of the warp looks up and loads box i, the page from one
+// step ahead.  What no query sees, or lies outside the pool, is loaded from behind its
+// last page: as zeros.  A warp issues a copy in about 80 cycles, so pages of 16 slots
+// want one for the keys and one for the values.
 template <int D, int kFmt, bool kTwin, class Params>
-__device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw, uint32_t lane) {
+__device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw, bool values, uint32_t lane) {
     using S = TilesShape<D, kFmt, Params::kPaged>;
     constexpr int kRow = kWide<kFmt> ? kRowBytes<D, kFmt> : 128;  // bytes of a row of a box
     volatile WaitLimit* wait = &sh.wait;
     const uint32_t steps = sh.steps;
-    if (!kWide<kFmt> && lane == 0) load_queries<D, kFmt, kTwin>(p, sh, qs, (uint32_t)sh.first_row + sh.t0, 0);
+    if (!kWide<kFmt> && !values && lane == 0) load_queries<D, kFmt, kTwin>(p, sh, qs, (uint32_t)sh.first_row + sh.t0, 0);
     const auto look_up = [&](uint32_t j) {
         if (lane >= p.boxes || j >= steps) return p.a.pool.pages;
         const int32_t s = step_slot(sh, (int32_t)j) + (int32_t)(lane * p.box);
@@ -282,24 +285,41 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
         if (page >= p.a.pool.pages) *const_cast<volatile uint32_t*>(&sh.lost) = 1;
         return min(page, p.a.pool.pages);
     };
-    constexpr int kN = kWide<kFmt> ? S::kRaws : S::kStages;
+    constexpr uint32_t kN = kWide<kFmt> ? S::kRaws : S::kStages, kParts = S::kParts;
     uint64_t* full = kWide<kFmt> ? sh.raw_full : sh.full;
     uint64_t* empty = kWide<kFmt> ? sh.raw_empty : sh.empty;
     uint8_t* exps = raw + S::kRaws * S::kRaw;  // of each raw stage, by slot
     const bool bulk = kQuantised<kFmt> && p.bulk_exps;
-    constexpr uint32_t kParts = S::kParts;
+    const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+    const splitzip_page_rows& rows = values ? p.a.pool.v : p.a.pool.k;
     const uint32_t part_boxes = p.boxes / kParts, slots_mask = p.slot_mask;
-    uint32_t now = look_up(0), ahead = look_up(1), i = 0;  // i: of the parts of the keys', values', next keys' .. tiles
-    for (uint32_t st = 0, ph = 0; i < 2 * kParts * steps; i++) {
-        if (i >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
-        const uint32_t step = i / (2 * kParts), part = i % kParts;
-        const bool v = i / kParts & 1;
+    uint32_t now = look_up(0), ahead = look_up(1);
+    // Parts of the keys', values', next keys' .. tiles are numbered in turn.
+    const uint32_t first = values ? kParts : 0;
+    uint32_t i = 0;  // parts issued
+    uint32_t st = first % kN, ph = 0;
+    // No stage takes both keys and values: each warp then waits for every turn of its stages,
+    // and no turn of another's passes unseen, after which a parity would say the opposite.
+    static_assert(kN % (2 * kParts) == 0, "stages of keys and of values are apart");
+    uint32_t m = first;
+    for (; i < kParts * steps; i++) {
+        const uint32_t step = i / kParts, part = i % kParts;
+        if (m >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
         const uint32_t s0 = (uint32_t)step_slot(sh, (int32_t)step) + part * S::kPartSlots;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
         __syncwarp();
         const uint32_t mine = lane - part * part_boxes;  // this lane's box of the part
+        if (mine < part_boxes) {
+            const int32_t at = (int32_t)((s0 + mine * p.box) & slots_mask);
+            if (kWide<kFmt>) {
+                tma_load4(raw + st * S::kRaw + mine * p.box * kRow, map, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < D / 64; x++)
+                    tma_load4(ring + st * S::kKV + x * (kBN * 128) + mine * p.box * kRow, map, 64 * x, at, (int32_t)sh.h, (int32_t)now, &full[st]);
+            }
+        }
         if (kQuantised<kFmt>) {  // where no query sees them, any page's: they multiply zeros
-            const splitzip_page_rows& rows = v ? p.a.pool.v : p.a.pool.k;
             const uint8_t* from = rows.exponents + (int64_t)sh.h * rows.exp_stride_h;
             uint8_t* to = exps + st * S::kExps;
             const uint32_t some = now < p.a.pool.pages ? now : 0;
@@ -315,25 +335,26 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
                 cp_async_arrive(&full[st]);
             }
         }
-        if (mine < part_boxes) {
-            const int32_t at = (int32_t)((s0 + mine * p.box) & slots_mask);
-            if (kWide<kFmt>) {
-                tma_load4(raw + st * S::kRaw + mine * p.box * kRow, v ? &p.vmap : &p.kmap, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);
-            } else {
-#pragma unroll
-                for (int x = 0; x < D / 64; x++)
-                    tma_load4(ring + st * S::kKV + x * (kBN * 128) + mine * p.box * kRow, v ? &p.vmap : &p.kmap, 64 * x, at, (int32_t)sh.h,
-                              (int32_t)now, &full[st]);
-            }
-        }
-        if (v && part == kParts - 1) {
+        uint32_t on = 1;
+        if (part == kParts - 1) {
             now = ahead;
             ahead = look_up(step + 2);
+            on += kParts;
         }
-        if (++st == kN) st = 0, ph ^= 1;
+        m += on;
+        st += on;
+        if (st >= kN) st -= kN, ph ^= 1;
     }
-    if (!kWide<kFmt>) mbar_wait_bounded<true>(&sh.q_full, 0, wait);
-    for (uint32_t x = i > kN ? i - kN : 0; x < i; x++) mbar_wait_bounded<true>(&full[x % kN], (x / kN) & 1, wait);
+    // Every load has landed before this CTA may end, also where a wait gave up.
+    if (!kWide<kFmt> && !values) mbar_wait_bounded<true>(&sh.q_full, 0, wait);
+    // Of a stage the last turn: those of the last kN parts of both warps, where all have been
+    // issued, else of this one's (a turn that is past already costs the failing CTA the limit).
+    const uint32_t end = i == kParts * steps ? 2 * i : m;
+    while (i--) {
+        const uint32_t x = 2 * kParts * (i / kParts) + first + i % kParts;
+        if (x + kN < end) break;
+        mbar_wait_bounded<true>(&full[x % kN], (x / kN) & 1, wait);
+    }
 }
 
 template <int D, int kFmt, bool kTwin, class Params>
@@ -490,7 +511,6 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
         constexpr uint32_t kWarps = S::kWiden, kCh = kRowBytes<D, kFmt> / 16;
         constexpr uint32_t kRows = kCh == 2 ? 16 : 8, kEach = kCh == 8 ? 2 : 1;  // rows of a warp at once, chunks of a lane
         constexpr uint32_t kOut = 2 * D / kRowBytes<D, kFmt>;                    // 16-byte chunks of FP16 out of one
-        if (thread >= 64 * kWarps) return;
         const uint32_t mine = thread / (32 * kWarps), warp = (thread >> 5) % kWarps;
         const uint32_t r0 = warp * kRows + (lane & 7) + (kCh == 2 ? lane >> 4 << 3 : 0);  // its first row, the others a multiple of 8 on
         const uint32_t c0 = kCh == 2 ? lane >> 3 & 1 : kEach * (lane >> 3);               // its first chunk, in a row and ..
@@ -631,12 +651,15 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
     } else {
         for (uint32_t i = 0; i < steps; i++, slots.next()) {
             const uint32_t n = 2 * i + 1, st = n % S::kStages, ph = (n / S::kStages) & 1;
+            // Stages that keys and values share (an odd number): every turn is waited for, as a
+            // parity says the opposite while a turn before it has not come.
+            if (S::kStages % 2 && !mbar_wait_bounded(&sh.full[(n - 1) % S::kStages], ((n - 1) / S::kStages) & 1, wait)) break;
             if (!mbar_wait_bounded(&sh.full[st], ph, wait)) break;
             if (sh.p0 < 0 || !whole(slots.s0)) {
                 bool found = false;
                 uint4* tile = reinterpret_cast<uint4*>(ring + st * S::kKV);
 #pragma unroll 4
-                for (uint32_t x = thread; x < S::kKV / 16; x += 32 * S::kTend) {
+                for (uint32_t x = thread; x < S::kKV / 16; x += 32 * S::kTenders) {
                     const uint4 v = tile[x];
                     const uint4 f = make_uint4(finite_or_zero<false>(v.x), finite_or_zero<false>(v.y), finite_or_zero<false>(v.z),
                                                finite_or_zero<false>(v.w));
@@ -901,9 +924,10 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
         regs_dec<S::kOtherRegs>();
         if (sh.steps) {
             if (warp == 16) issue_products<D, kFmt, kTwin, Params>(sh, tmem, qs, ring);
-            else if (warp > 17) tend_values<D, kFmt>(p, sh, ring, raw, threadIdx.x - (kSoftmax + 64));
-            else if constexpr (Params::kPaged) load_page_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw, threadIdx.x & 31);
-            else if ((threadIdx.x & 31) == 0) load_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw);
+            else if (warp > 17 && warp < 18 + S::kTenders) tend_values<D, kFmt>(p, sh, ring, raw, threadIdx.x - (kSoftmax + 64));
+            else if constexpr (Params::kPaged) {
+                if (warp == 17 || warp == 18 + S::kTenders) load_page_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw, warp != 17, threadIdx.x & 31);
+            } else if ((threadIdx.x & 31) == 0) load_tiles<D, kFmt, kTwin>(p, sh, qs, ring, raw);
         }
         __syncwarp();
         if (kTwin || p.splits > 1) {  // with the softmax warps below

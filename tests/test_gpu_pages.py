@@ -354,6 +354,19 @@ def test_attention_splits_long_caches(fmt):
     check(q, p, table, start, lens)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("counts", [[8, 8, 5], [130], [3, 300, 1]], ids=["tile", "tiles", "mixed"])
+def test_attention_walks_many_tiles_of_slots(counts, dim, fmt):
+    """Enough slots that every ring of tiles turns many times; several calls on one workspace, all alike."""
+    q, p, table, start, lens = batch_of(counts, [5003, 4800, 4999][: len(counts)], 8, 1, dim, 16, fmt, seed=dim)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, max(counts))
+    first, _ = check(q, p, table, start, lens)
+    for _ in range(10):
+        again, _ = attend(q, p, table, start, lens, ws=ws)
+        assert torch.equal(first, again)
+
+
 def test_attention_of_pages_past_32_bits():
     """A pool of over 4 GiB, the sequence's pages at its end."""
     pages, heads, dim = (1 << 32) // (16 * 8 * 128 * 2) + 40, 8, 128
