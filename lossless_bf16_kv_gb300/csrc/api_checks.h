@@ -4,7 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "../../include/splitzip_serving.h"
+#include "../../include/splitzip_serving_testing.h"
+#include "serving.h"
 
 namespace splitzip {
 
@@ -26,5 +27,14 @@ constexpr uint64_t kMax31 = 0x7FFFFFFFull;
 // Slots and query rows of the attention calls: their kernels look up to two tiles
 // of 128 past the last one in signed 32-bit numbers.
 constexpr uint64_t kMostTokens = (1ull << 31) - 256;
+
+// What a test leaves out, and how long waits last in it.
+inline bool wait_test(const splitzip_wait_test_opts* opts, WaitTest& test) {
+    if (!opts || opts->wait_ms > 2000) return false;
+    test.limit = opts->wait_ms * 1000000u >> 10;
+    test.cta = opts->cta;
+    test.tile = opts->tile;
+    return true;
+}
 
 }  // namespace splitzip

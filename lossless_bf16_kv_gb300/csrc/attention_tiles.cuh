@@ -309,7 +309,7 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
         if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
         __syncwarp();
         const uint32_t mine = lane - part * part_boxes;  // this lane's box of the part
-        if (mine < part_boxes) {
+        if (mine < part_boxes && !(blockIdx.x == p.test_cta && m == p.test_tile)) {
             const int32_t at = (int32_t)((s0 + mine * p.box) & slots_mask);
             if (kWide<kFmt>) {
                 tma_load4(raw + st * S::kRaw + mine * p.box * kRow, map, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);

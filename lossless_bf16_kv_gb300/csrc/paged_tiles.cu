@@ -39,7 +39,7 @@ bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from
 }
 
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
-                               const void* widened, bool beside, cudaStream_t s) {
+                               const void* widened, bool beside, const WaitTest& test, cudaStream_t s) {
     PagedTilesParams p;
     p.a = a;
     p.group = a.q_heads / a.pool.kv_heads;
@@ -67,7 +67,9 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     while ((1u << p.page_shift) < a.pool.page_tokens) p.page_shift++;
     p.bulk_exps = bulk_exponents(pool);
     p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
-    p.wait_limit = wait_limit(0);  // a wait lasts a few steps at most
+    p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a few steps at most
+    p.test_cta = test.cta;
+    p.test_tile = test.tile;
     const bool wide = pool.format != kBf16;
     uint32_t one;
     if ((!wide && !make_map(p.qmap, a.q, 2, pool.head_dim, a.q_heads, a.tokens, 1, p.group, p.tokens, true, &one)) ||

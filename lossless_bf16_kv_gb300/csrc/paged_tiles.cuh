@@ -28,6 +28,7 @@ struct PagedTilesParams {
     uint32_t widened;          // the pool holds one page for each of these sequences, in their order
     uint32_t* status;
     uint32_t wait_limit;
+    uint32_t test_cta, test_tile;  // a copy that a test has left out
 
     static constexpr bool kPaged = true;
     // On a raw tile's barrier: its copies', and the lanes' whose own copies bring the exponents.

@@ -32,7 +32,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
 // for.  widened: the sequences' caches in BF16, as launch_paged_widen leaves them (or
 // NULL: they are read from the pool).
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& p, void* workspace,
-                               const void* widened, bool beside, cudaStream_t s);
+                               const void* widened, bool beside, const WaitTest& test, cudaStream_t s);
 
 // The caches of a batch's long sequences (more than rows_from query rows) in BF16, one
 // after the other in the batch's order: keys, then values, head by head, of

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "../../include/splitzip_pages_testing.h"
 #include "api_checks.h"
 #include "pages.h"
 #include "trace.h"
@@ -72,6 +73,27 @@ bool plan(const splitzip_paged_attention_args& a, Plans& p) {
     return true;
 }
 
+// The call as users make it and (test) with a copy left out.
+splitzip_status attention(const splitzip_paged_attention_args* a, void* workspace, size_t workspace_bytes, splitzip_stream_t s, const WaitTest& test) {
+    Plans p;
+    if (!a || !sizes_ok(*a) || !plan(*a, p) || !pool_ok(a->pool)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!view_ok(a->q, 2, 1, a->tokens, a->q_heads) || !view_ok(a->out, 2, 1, a->tokens, a->q_heads, true)) return SPLITZIP_ERR_INVALID_ARG;
+    if (!a->table || !a->q_start || !a->lens || !aligned(a->table, 4) || !aligned(a->q_start, 4) || !aligned(a->lens, 4) ||
+        !aligned(a->lse, 4) || !std::isfinite(a->scale) || !(a->scale > 0.0f))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
+    const cudaStream_t stream = (cudaStream_t)s;
+    cudaError_t e = cudaSuccess;
+    if (p.many) {
+        void* wide = static_cast<uint8_t*>(workspace) + p.at_wide;
+        e = launch_paged_widen(*a, p.from, wide, stream);
+        if (e == cudaSuccess) e = launch_paged_tiles(*a, p.from, 0xFFFFFFFFu, p.wide, workspace, wide, false, test, stream);
+    }
+    if (e == cudaSuccess && p.some) e = launch_paged_tiles(*a, p.upto, p.from, p.tiles, workspace, nullptr, p.many, test, stream);
+    if (e == cudaSuccess && p.few) e = launch_paged_rows(*a, p.upto, p.rows, workspace, p.many || p.some, test, stream);
+    return from_cuda(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -109,23 +131,13 @@ size_t splitzip_paged_attention_workspace_bytes(const splitzip_paged_attention_a
 splitzip_status splitzip_paged_attention(const splitzip_paged_attention_args* a, void* workspace, size_t workspace_bytes,
                                          splitzip_stream_t s) {
     TraceRange trace("splitzip_paged_attention");
-    Plans p;
-    if (!a || !sizes_ok(*a) || !plan(*a, p) || !pool_ok(a->pool)) return SPLITZIP_ERR_INVALID_ARG;
-    if (!view_ok(a->q, 2, 1, a->tokens, a->q_heads) || !view_ok(a->out, 2, 1, a->tokens, a->q_heads, true)) return SPLITZIP_ERR_INVALID_ARG;
-    if (!a->table || !a->q_start || !a->lens || !aligned(a->table, 4) || !aligned(a->q_start, 4) || !aligned(a->lens, 4) ||
-        !aligned(a->lse, 4) || !std::isfinite(a->scale) || !(a->scale > 0.0f))
-        return SPLITZIP_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes) return SPLITZIP_ERR_INVALID_ARG;
-    const cudaStream_t stream = (cudaStream_t)s;
-    cudaError_t e = cudaSuccess;
-    if (p.many) {
-        void* wide = static_cast<uint8_t*>(workspace) + p.at_wide;
-        e = launch_paged_widen(*a, p.from, wide, stream);
-        if (e == cudaSuccess) e = launch_paged_tiles(*a, p.from, 0xFFFFFFFFu, p.wide, workspace, wide, false, stream);
-    }
-    if (e == cudaSuccess && p.some) e = launch_paged_tiles(*a, p.upto, p.from, p.tiles, workspace, nullptr, p.many, stream);
-    if (e == cudaSuccess && p.few) e = launch_paged_rows(*a, p.upto, p.rows, workspace, p.many || p.some, WaitTest(), stream);
-    return from_cuda(e);
+    return attention(a, workspace, workspace_bytes, s, WaitTest());
+}
+
+splitzip_status splitzip_paged_attention_test(const splitzip_paged_attention_args* a, void* workspace, size_t workspace_bytes,
+                                              splitzip_stream_t s, const splitzip_wait_test_opts* opts) {
+    WaitTest test;
+    return wait_test(opts, test) ? attention(a, workspace, workspace_bytes, s, test) : SPLITZIP_ERR_INVALID_ARG;
 }
 
 }  // extern "C"

@@ -3,7 +3,6 @@
 #include <cmath>
 #include <cstdint>
 
-#include "../../include/splitzip_serving_testing.h"
 #include "api_checks.h"
 #include "serving.h"
 #include "trace.h"
@@ -79,14 +78,6 @@ splitzip_status attention_weights(const splitzip_attention_args* a, const float*
         !std::isfinite(a->scale))
         return SPLITZIP_ERR_INVALID_ARG;
     return from_cuda(launch_attention_weights(*a, weights_in, weights_out, test, (cudaStream_t)s));
-}
-
-bool wait_test(const splitzip_wait_test_opts* opts, WaitTest& test) {
-    if (!opts || opts->wait_ms > 2000) return false;
-    test.limit = opts->wait_ms * 1000000u >> 10;
-    test.cta = opts->cta;
-    test.tile = opts->tile;
-    return true;
 }
 
 }  // namespace

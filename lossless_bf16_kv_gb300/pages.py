@@ -77,6 +77,7 @@ def library() -> ctypes.CDLL:
             "splitzip_pages_load": (ctypes.c_int, [_vp, _vp]),
             "splitzip_paged_attention_workspace_bytes": (ctypes.c_size_t, [_vp]),
             "splitzip_paged_attention": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp]),
+            "splitzip_paged_attention_test": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
