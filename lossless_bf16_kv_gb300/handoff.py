@@ -1,6 +1,7 @@
 """A prompt's KV cache from prefill to decode, with every operator of this package.
 
-    python -m lossless_bf16_kv_gb300.handoff [--layers 4] [--tokens 2048] [--budget 512] [--fmt bf16|e5m2] ...
+    python -m lossless_bf16_kv_gb300.handoff [--layers 4] [--tokens 2048] [--budget 512] [--fmt bf16|e5m2]
+        [--pages bf16|e5m2|int8|e2m1] ...
 
 The prefill worker takes a prompt through the attention part of each layer
 (``splitzip_qk_norm_rope`` writes the cache, ``splitzip_attention`` reads it
@@ -8,7 +9,9 @@ with a sliding window and sinks, ``splitzip_attention_weights`` weighs its
 tokens by the last queries), thins all layers at once (``splitzip_evict``) and
 packs what is left for the host link with the lossless codec
 (``encode_to_host``, a codebook per layer).  The decode worker unpacks it
-(``splitzip_decode_from_host``), appends its own tokens and attends over them.
+(``splitzip_decode_from_host``), appends its own tokens and attends over them, or
+(``--pages``) keeps the cache in pages of another format (``splitzip_pages_store``,
+``splitzip_paged_attention``).
 
 Projections are random matrices and the prompt random vectors: nothing here is
 a trained model.  The cache that arrives is bit for bit the one that was sent.
@@ -21,6 +24,7 @@ from dataclasses import dataclass
 
 import torch
 
+from . import pages as paged
 from . import serving
 from . import splitzip as sz
 
@@ -39,6 +43,8 @@ class Shape:
     steps: int = 8         # tokens decoded
     fmt: str = "bf16"
     seed: int = 0
+    pages: str = ""        # the decode worker's pages: bf16, e5m2, int8 or e2m1; "": it keeps the cache as it came
+    page_tokens: int = 16
 
     @property
     def dtype(self) -> torch.dtype:
@@ -151,15 +157,52 @@ def decode(m: Layers, thinned: torch.Tensor):
     return outs, queries, kv
 
 
+def decode_paged(m: Layers, thinned: torch.Tensor):
+    """As ``decode``, over pages: outputs and queries of the new tokens, the pool and its table [layers, pages]."""
+    s, dev = m.s, m.device
+    width = -(-(s.kept + s.steps) // s.page_tokens)
+    pool = paged.alloc_pages(s.layers * width, s.page_tokens, s.kv_heads, s.dim, s.pages, dev)
+    table = torch.arange(s.layers * width, dtype=torch.int32, device=dev).view(s.layers, width)
+
+    def slots(layer: int, t: torch.Tensor) -> torch.Tensor:
+        return table[layer, t // s.page_tokens].long() * s.page_tokens + t % s.page_tokens
+    here = torch.arange(s.kept, device=dev)
+    for layer in range(s.layers):
+        k, v = thinned[layer].bfloat16()
+        paged.splitzip_pages_store(k, v, slots(layer, here), pool)
+    queries = torch.empty((s.steps, s.layers, s.q_heads, s.dim), dtype=torch.bfloat16, device=dev)
+    outs = torch.empty_like(queries)
+    new = torch.empty((2, 1, s.kv_heads, s.dim), dtype=torch.bfloat16, device=dev)     # a token's keys and values
+    first = torch.zeros(1, dtype=torch.int64, device=dev)
+    start = torch.arange(2, dtype=torch.int32, device=dev)
+    lens = torch.full((1,), s.kept, dtype=torch.int32, device=dev)
+    workspace = paged.alloc_paged_attention_workspace(queries[0, :1], pool, table[:1], 1)
+    for step in range(s.steps):
+        position = torch.full((1,), s.tokens + step, dtype=torch.int32, device=dev)
+        lens += 1
+        x = m.new[step:step + 1]
+        for layer in range(s.layers):
+            qr, kr, vr = m.project(layer, x)
+            q, out = queries[step, layer:layer + 1], outs[step, layer:layer + 1]     # [1, q_heads, dim]
+            serving.splitzip_qk_norm_rope(qr, kr, vr, m.norm[layer][0], m.norm[layer][1], position, m.table, first, q, new[0], new[1])
+            paged.splitzip_pages_store(new[0], new[1], slots(layer, first + s.kept + step), pool)
+            paged.splitzip_paged_attention(q, pool, table[layer:layer + 1], start, lens, out, workspace, 1)
+            x = m.mix(layer, x, out)
+    return outs, queries, pool, table
+
+
 def run(s: Shape, device="cuda") -> dict:
     m = Layers(s, device)
     kv, weights = prefill(m)
     small, index = thin(s, kv, weights)
     payload, nbytes, there = send(s, small)
-    outs, queries, decoded = decode(m, there)
+    if s.pages:
+        outs, queries, decoded, table = decode_paged(m, there)
+    else:
+        (outs, queries, decoded), table = decode(m, there), None
     torch.cuda.synchronize()
     return {"kv": kv, "weights": weights, "small": small, "index": index, "there": there, "outs": outs,
-            "queries": queries, "decoded": decoded, "payload_bytes": nbytes, "layers": m}
+            "queries": queries, "decoded": decoded, "table": table, "payload_bytes": nbytes, "layers": m}
 
 
 def main(argv=None) -> int:
