@@ -369,7 +369,13 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
         if (c == 0 && a.lse)
             a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
-    join_rows<D, S::kTileRows>(os, sh, unit, split, p.splits, p.cluster, nrows, p.counters, p.partials, store);
+    const auto is_last = [&] {
+        const bool last = atomicAdd(p.counters + unit, 1u) == p.splits - 1;
+        if (last) p.counters[unit] = 0;  // ready for the next call
+        return last;
+    };
+    float* all = p.partials + (uint64_t)unit * (p.splits / p.cluster) * kPartFloats<D, S::kTileRows>;
+    join_rows<D, S::kTileRows>(os, sh, split, p.splits, p.cluster, nrows, all, is_last, store);
 }
 
 template <int D, bool kF8, int MT>

@@ -31,15 +31,19 @@ struct RowsShared {
     uint32_t last;
 };
 
+// Floats of a partial result in memory: rows of o, m and l.
+template <int D, int kTileRows>
+constexpr uint32_t kPartFloats = kTileRows * (D + 4);
+
 // Joins the partial results of one row tile: of this CTA's warps (rows of D values
 // in `os`, warp by warp, with their m and l in sh), then of the splits of its
-// cluster, then, where there are more clusters (splits / cluster), through
-// `partials` and `counters`, both by `unit`.  store(r, c, o, m, l) takes four
-// columns of a row of the tile once they are complete.  All threads of the CTA,
-// and of the cluster, call it.
-template <int D, int kTileRows, class Store>
-__device__ __forceinline__ void join_rows(float* os, RowsShared<kTileRows>& sh, uint32_t unit, uint32_t split, uint32_t splits,
-                                          uint32_t cluster, uint32_t nrows, uint32_t* counters, float* partials, const Store& store) {
+// cluster, then, where there are more clusters (splits / cluster), through the row
+// tile's `partials`: is_last() counts this CTA (one thread calls it) and says whether
+// it is the last one.  store(r, c, o, m, l) takes four columns of a row of the tile
+// once they are complete.  All threads of the CTA, and of the cluster, call it.
+template <int D, int kTileRows, class Last, class Store>
+__device__ __forceinline__ void join_rows(float* os, RowsShared<kTileRows>& sh, uint32_t split, uint32_t splits, uint32_t cluster,
+                                          uint32_t nrows, float* all, const Last& is_last, const Store& store) {
     const uint32_t tid = threadIdx.x;
     for (uint32_t at = tid; at < nrows * (D / 4); at += 32 * kWarpsRows) {
         const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
@@ -66,9 +70,8 @@ __device__ __forceinline__ void join_rows(float* os, RowsShared<kTileRows>& sh, 
     const uint32_t rank = split % cluster, groups = splits / cluster;
     if (cluster > 1) cluster_sync();
     else __syncthreads();
-    constexpr uint32_t kPart = kTileRows * (D + 4);  // floats of a partial result: rows of o, m, l
+    constexpr uint32_t kPart = kPartFloats<D, kTileRows>;
     const uint32_t group = split / cluster;
-    float* all = partials + (uint64_t)unit * groups * kPart;
     for (uint32_t at = rank * 32 * kWarpsRows + tid; at < nrows * (D / 4); at += cluster * 32 * kWarpsRows) {
         const uint32_t r = at / (D / 4), c = 4 * (at % (D / 4));
         float m8[8], l8[8];
@@ -108,10 +111,7 @@ __device__ __forceinline__ void join_rows(float* os, RowsShared<kTileRows>& sh, 
     if (groups == 1) return;
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        sh.last = atomicAdd(counters + unit, 1u) == splits - 1;
-        if (sh.last) counters[unit] = 0;  // ready for the next call
-    }
+    if (tid == 0) sh.last = is_last();
     __syncthreads();
     if (!sh.last) return;
     __threadfence();

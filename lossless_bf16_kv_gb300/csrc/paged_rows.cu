@@ -39,7 +39,8 @@ namespace {
 struct PagedRowsParams {
     splitzip_paged_attention_args a;
     CUtensorMap kmap, vmap;
-    uint32_t group, page_shift, row_tiles, splits, cluster;
+    uint32_t group, page_shift, row_tiles;
+    uint32_t splits, cluster;  // of each row tile; splits 0: shared out by the sequences' lengths
     uint32_t rows_upto;   // only sequences with no more query rows than this
     uint32_t box, boxes;  // slots to a copy, and copies to a tile
     uint32_t bulk_exps;   // a page's exponent bytes of a head are contiguous, in multiples of 16 bytes
@@ -63,8 +64,87 @@ struct PagedShape {
     static constexpr int kAtQueries = kAtPowers + 2 * kExps;
     static_assert(kTile % 1024 == 0, "swizzled tiles");
 };
+// A CTA's part of the work: row tile rt of sequence b and head h, and which of its
+// splits; the CTA with the first of those.
+struct PagedPart {
+    uint32_t b, h, rt, split, splits, first;
+};
+
+// Sequences whose work is shared out in one launch, by tables of their slot tiles.
+constexpr uint32_t kMostShared = 1024;
+// Row tiles whose splits are counted so, a byte each in the workspace's header.
+constexpr uint32_t kMostCounted = 1016;
+// The least slot tiles of a split, and the most that a CTA may have where work is shared out.
+constexpr uint32_t kLeastTiles = 4, kSharedTiles = 32;
+
+// Shares the work out by the sequences' lengths: splits of at most T slot tiles, with the
+// smallest T for which they are no more than the grid's CTAs.  `part` comes back with
+// splits = 0 where this CTA has none.  All threads; `table` holds a word for each
+// sequence.  T is found by bisection, by one warp: about a microsecond in all, with
+// the loads of the sequences' ranges.
+template <int kTileRows, int kSlots, class Params>
+__device__ __forceinline__ void share_out(const Params& p, uint32_t* table, PagedPart& part) {
+    const splitzip_paged_attention_args& a = p.a;
+    constexpr uint32_t kTiles = 0x3FFFFFFFu;  // of a word; above, how many row tiles the sequence has
+    for (uint32_t b = threadIdx.x; b < a.batch; b += 32 * kWarpsRows) {
+        const Sequence seq(a, b);
+        const uint32_t rows = (uint32_t)seq.count * p.group;
+        uint32_t word = 0;
+        if (rows && rows <= p.rows_upto) {
+            const Mask mask(seq.n, seq.count, a.window, a.sinks);
+            word = SlotTiles(mask, mask.first, seq.n - 1, kSlots).count | (rows + kTileRows - 1) / kTileRows << 30;
+        }
+        table[b] = word;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const uint32_t lane = threadIdx.x, heads = a.pool.kv_heads;
+        uint32_t most = 1;
+        for (uint32_t b = lane; b < a.batch; b += 32) most = max(most, table[b] & kTiles);
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        const auto ctas_of = [&](uint32_t word, uint32_t t) { return (word >> 30) * heads * max(1u, ((word & kTiles) + t - 1) / t); };
+        uint32_t lo = max(kLeastTiles, (most + 254) / 255), hi = max(lo, most);  // a counter of 8 bits counts up to 255
+        while (lo < hi) {
+            const uint32_t t = (lo + hi) / 2;
+            uint32_t sum = 0;
+            for (uint32_t b = lane; b < a.batch; b += 32) sum += ctas_of(table[b], t);
+            if (__reduce_add_sync(0xFFFFFFFFu, sum) <= gridDim.x) hi = t;
+            else lo = t + 1;
+        }
+        uint32_t left = blockIdx.x;
+        if (lane == 0) part.splits = 0;
+        for (uint32_t b = 0; b < a.batch; b += 32) {
+            const uint32_t word = b + lane < a.batch ? table[b + lane] : 0, here = ctas_of(word, lo);
+            uint32_t upto = here;
+#pragma unroll
+            for (int i = 1; i < 32; i *= 2) {
+                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, i);
+                if (lane >= (uint32_t)i) upto += x;
+            }
+            const uint32_t found = __ballot_sync(0xFFFFFFFFu, left < upto);
+            if (found) {
+                if (lane == (uint32_t)__ffs(found) - 1) {
+                    const uint32_t at = left - (upto - here), splits = max(1u, ((word & kTiles) + lo - 1) / lo);
+                    const uint32_t unit = at / splits;
+                    part.b = b + lane;
+                    part.h = unit % heads;
+                    part.rt = unit / heads;
+                    part.split = at - unit * splits;
+                    part.first = blockIdx.x - part.split;
+                    part.splits = splits;
+                }
+                break;
+            }
+            left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+    }
+    __syncthreads();
+    fence_async_proxy();  // the tables' place is the tiles', which TMA writes
+}
+
 template <int kStages, int kTileRows>
 struct PagedRowsShared {
+    PagedPart part;
     uint64_t full[kStages], empty[kStages];
     WaitLimit wait;
     uint32_t issued;  // tiles whose copies have been issued
@@ -126,12 +206,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
     const splitzip_paged_attention_args& a = p.a;
     const splitzip_pool& pool = a.pool;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t unit = blockIdx.x / p.splits, split = blockIdx.x - unit * p.splits;
-    const uint32_t bh = unit / p.row_tiles, rt = unit - bh * p.row_tiles;
-    const uint32_t b = bh / pool.kv_heads, h = bh - b * pool.kv_heads;
-    const Sequence seq(a, b);
-    const uint32_t rows = (uint32_t)seq.count * p.group;
-    const uint32_t r0 = rt * kTileRows, r1 = min(r0 + kTileRows, rows);
+    const bool shared = p.splits == 0;
+    if (shared) share_out<kTileRows, S::kSlots>(p, reinterpret_cast<uint32_t*>(smem), sh.part);
     // A grid that was let start before the one ahead of it has ended ends after that: the
     // last CTA waits for it, and the others leave their SMs to those that are to come.
     struct AtEnd {
@@ -139,12 +215,26 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
             if (blockIdx.x == gridDim.x - 1) wait_prerequisite_grid();
         }
     } at_end;
+    uint32_t b, h, rt, split, splits, first_cta;
+    if (shared) {
+        const PagedPart& part = sh.part;
+        if (!part.splits) return;
+        b = part.b, h = part.h, rt = part.rt, split = part.split, splits = part.splits, first_cta = part.first;
+    } else {
+        splits = p.splits;
+        const uint32_t unit = blockIdx.x / splits, bh = unit / p.row_tiles;
+        split = blockIdx.x - unit * splits, rt = unit - bh * p.row_tiles, b = bh / pool.kv_heads, h = bh - b * pool.kv_heads;
+        first_cta = blockIdx.x - split;
+    }
+    const Sequence seq(a, b);
+    const uint32_t rows = (uint32_t)seq.count * p.group;
+    const uint32_t r0 = rt * kTileRows, r1 = min(r0 + kTileRows, rows);
     if (r0 >= rows || rows > p.rows_upto) return;  // with all of its cluster
     const Mask mask(seq.n, seq.count, a.window, a.sinks);
     const int32_t p0 = mask.first + (int32_t)(r0 / p.group), p1 = mask.first + (int32_t)((r1 - 1) / p.group);
     const SlotTiles tiles(mask, p0, p1, S::kSlots);
-    const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
-    const uint32_t j1 = (uint32_t)((uint64_t)tiles.count * (split + 1) / p.splits);
+    const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / splits);
+    const uint32_t j1 = (uint32_t)((uint64_t)tiles.count * (split + 1) / splits);
 
     uint8_t* powers = smem + S::kAtPowers + warp * (8 * S::kPart);  // of this warp's values, [block][slot]
     volatile WaitLimit* wait = &sh.wait;
@@ -627,7 +717,22 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
             none ? make_uint2(0, 0) : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
         if (c == 0 && a.lse) a.lse[(uint64_t)hq * a.tokens + seq.row + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
-    join_rows<D, kTileRows>(os, sh.join, unit, split, p.splits, p.cluster, r1 - r0, p.counters, p.partials, store);
+    const uint32_t cluster = shared ? 1 : p.cluster, unit = (b * pool.kv_heads + h) * p.row_tiles + rt;
+    // Counters are ready for the next call when the last one has counted: words, or where
+    // there may be many row tiles bytes of them.
+    const auto is_last = [&] {
+        if (!shared) {
+            const bool last = atomicAdd(p.counters + unit, 1u) == splits - 1;
+            if (last) p.counters[unit] = 0;
+            return last;
+        }
+        const uint32_t by = 8 * (unit & 3);
+        const bool last = (atomicAdd(p.counters + unit / 4, 1u << by) >> by & 255u) == splits - 1;
+        if (last) atomicSub(p.counters + unit / 4, splits << by);
+        return last;
+    };
+    float* all = p.partials + (uint64_t)(first_cta / cluster) * kPartFloats<D, kTileRows>;
+    join_rows<D, kTileRows>(os, sh.join, split, splits, cluster, r1 - r0, all, is_last, store);
 }
 
 template <int D, int kFmt, int NB>
@@ -695,8 +800,23 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
                                      a.pool.format != kBf16 && tile == 8 ? 4 : 3);
     // Splits in several clusters are counted by row tile, in a header of limited size.
     if (p.splits > 8 && units > kSms) p.splits = 8;
+    p.ctas = units * p.splits;
     p.bytes = attention_rows_bytes(units, p.splits, tile, d);
-    return units * p.splits <= 0x7FFFFFFFull;
+    // Sequences of a batch differ in length, and a number of splits that is the same for all
+    // does not fill the GPU evenly.  Sharing the work out by length costs 5 us (the tables,
+    // and joining through memory), so it is for caches whose widening keeps the GPU busy
+    // for long: 16 sequences of 8k to 16k, 8 heads of 128, in 8 bits 76 us (86 with splits
+    // alike), in 4 67 (79), in BF16 126 (124); 5 of up to 9000 in 8 bits 28 (26), all 16
+    // of 16k 100 (95).
+    const uint64_t at_once = (uint64_t)kSms * (tile == 8 ? 4 : 3);
+    static_assert(kMostCounted <= kAttentionStatus, "a byte counts the splits of a row tile");
+    if (a.pool.format != kBf16 && a.batch > 1 && a.batch <= kMostShared && units <= kMostCounted && units < at_once &&
+        likely * (most / (kWarpsRows * slots)) >= kSharedTiles * at_once) {
+        p.splits = 0;
+        p.ctas = at_once;
+        p.bytes = kAttentionHeader + at_once * tile * (d + 4) * 4;
+    }
+    return p.ctas <= 0x7FFFFFFFull;
 }
 
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
@@ -709,7 +829,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.rows_upto = rows_upto;
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
-    p.cluster = std::min(plan.splits, 8u);
+    p.cluster = plan.splits ? std::min(plan.splits, 8u) : 1;
     const splitzip_pool& pool = a.pool;
     const uint32_t slots = kWarpsRows * 2048 / pool.head_dim;  // of a tile
     p.box = std::min(pool.page_tokens, slots);
@@ -722,7 +842,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.test_tile = test.tile;
     p.counters = reinterpret_cast<uint32_t*>(workspace);
     p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttentionHeader);
-    const uint32_t ctas = a.batch * a.pool.kv_heads * plan.row_tiles * plan.splits;
+    const uint32_t ctas = (uint32_t)plan.ctas;
     return a.pool.head_dim == 64 ? launch_format<64>(p, tile_rows(a, rows_upto), ctas, after_tiles, s)
                                     : launch_format<128>(p, tile_rows(a, rows_upto), ctas, after_tiles, s);
 }

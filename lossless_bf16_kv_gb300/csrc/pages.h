@@ -18,7 +18,8 @@ cudaError_t launch_pages_load(const splitzip_pages_load_args& a, cudaStream_t s)
 // they do not fit a launch.
 struct PagedPlan {
     uint32_t row_tiles;  // of a sequence (few rows), or at most of the batch (many)
-    uint32_t splits;
+    uint32_t splits;     // 0 (few rows): by the sequences' lengths
+    uint64_t ctas;       // of the launch (few rows)
     size_t bytes;        // of workspace
 };
 // Sequences of up to rows_upto query rows, and of more than rows_from, up to rows_upto.

@@ -367,6 +367,31 @@ def test_attention_walks_many_tiles_of_slots(counts, dim, fmt):
         assert torch.equal(first, again)
 
 
+@pytest.mark.parametrize("fmt", ["e5m2", "int8", "e2m1"])
+@pytest.mark.parametrize("dim,heads,kv_heads", [(128, 8, 4), (64, 16, 8), (128, 24, 2)])
+def test_attention_shares_work_out_by_length(dim, heads, kv_heads, fmt):
+    """A bound on the lengths that is so large that the work is shared out on the GPU: lengths far apart, of zero, a
+    sequence left out; several calls on one workspace, all alike."""
+    lens = [3000, 1, 17, 0, 2900, 64, 1500, 700]
+    q, p, table, start, lens = batch_of([1, 1, 1, 1, 0, 1, 1, 1], lens, heads, kv_heads, dim, 16, fmt, seed=heads)
+    wide = torch.full((8, 1 << 14), -1, dtype=torch.int32, device=DEV)       # 262144 tokens
+    wide[:, : table.shape[1]] = table
+    ws = pg.alloc_paged_attention_workspace(q, p, wide, 1)
+    out, lse = attend(q, p, wide, start, lens, ws=ws)
+    found = ref.attention(q, p, table, start, lens, table.shape[1] * 16, 0, 0, dim ** -0.5)
+    for rows, o, l, tol, ltol in found:
+        close(out[rows], o, tol, "out")
+        close(lse[:, rows], l, ltol, "lse")
+    for _ in range(5):
+        assert torch.equal(attend(q, p, wide, start, lens, ws=ws)[0], out)
+    lens[0], lens[2] = 20, 2999                 # the same workspace, other lengths
+    table[2] = table[0]
+    wide[:, : table.shape[1]] = table
+    out, lse = attend(q, p, wide, start, lens, ws=ws)
+    for rows, o, l, tol, ltol in ref.attention(q, p, table, start, lens, table.shape[1] * 16, 0, 0, dim ** -0.5):
+        close(out[rows], o, tol, "out")
+
+
 def test_attention_of_pages_past_32_bits():
     """A pool of over 4 GiB, the sequence's pages at its end."""
     pages, heads, dim = (1 << 32) // (16 * 8 * 128 * 2) + 40, 8, 128
