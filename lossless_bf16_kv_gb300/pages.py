@@ -141,7 +141,7 @@ def alloc_pages(pages: int, page_tokens: int, kv_heads: int, head_dim: int, fmt:
 def _check_device(pages: Pages, *tensors):
     """The pool, the rows that go with it and the call are on one device: a stream reaches no other."""
     for t in (pages.k, *tensors):
-        if t.get_device() != _current_device():
+        if t is not None and t.get_device() != _current_device():
             _bad(f"a tensor on {t.device}, the current device is cuda:{_current_device()}")
 
 
@@ -154,7 +154,7 @@ def splitzip_pages_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
     kst, vst = k.stride(), v.stride()
     ok = (len(ks) == 3 and ks[1] == pages.kv_heads and ks[2] == pages.head_dim and v.shape == ks
           and k.dtype is _B16 and v.dtype is _B16 and kst[2] == 1 and vst[2] == 1 and k.get_device() == v.get_device() == pages.index == _current_device()
-          and slots.dtype is _I64 and slots.shape == ks[:1] and slots.is_contiguous() and slots.is_cuda)
+          and slots.dtype is _I64 and slots.shape == ks[:1] and slots.is_contiguous() and slots.get_device() == pages.index)
     if not ok:
         _bf16(k, "k")
         _bf16(v, "v")
@@ -162,7 +162,7 @@ def splitzip_pages_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
         _check_view(k, shape, "k")
         _check_view(v, shape, "v")
         _check_array(slots, _I64, shape[:1], "slots")
-        _check_device(pages, k, v)
+        _check_device(pages, k, v, slots)
         _bad("these arguments are not accepted")
     a = _STORE.pack(k.data_ptr(), 0, kst[0], kst[1], v.data_ptr(), 0, vst[0], vst[1], slots.data_ptr(), pages.packed, ks[0])
     if _fn_store is None:
@@ -184,8 +184,8 @@ def splitzip_pages_load(pages: Pages, table: torch.Tensor, lens: torch.Tensor | 
     ok = (len(ks) == 4 and ks[2] == pages.kv_heads and ks[3] == pages.head_dim and v_out.shape == ks and v_out.dtype is kind
           and (kind is _B16 or (kind is _F8 and pages.format == E5M2)) and kst[3] == 1 and vst[3] == 1
           and k_out.get_device() == v_out.get_device() == pages.index == _current_device() and len(ts) == 2 and ts[0] == ks[0] and table.dtype is _I32
-          and table.is_contiguous() and table.is_cuda and ks[1] <= ts[1] * pages.page_tokens
-          and (lens is None or (lens.dtype is _I32 and lens.shape == ks[:1] and lens.is_contiguous() and lens.is_cuda)))
+          and table.is_contiguous() and table.get_device() == pages.index and ks[1] <= ts[1] * pages.page_tokens
+          and (lens is None or (lens.dtype is _I32 and lens.shape == ks[:1] and lens.is_contiguous() and lens.get_device() == pages.index)))
     if not ok:
         _check_load(pages, table, lens, k_out, v_out)
     a = _LOAD.pack(pages.packed, table.data_ptr(), 0 if lens is None else lens.data_ptr(), k_out.data_ptr(), *kst[:3],
@@ -207,7 +207,7 @@ def _check_load(pages, table, lens, k_out, v_out):
     _check_view(k_out, shape, "k_out")
     _check_view(v_out, shape, "v_out")
     _check_table(table, lens, shape[0], shape[1], pages)
-    _check_device(pages, k_out, v_out)
+    _check_device(pages, k_out, v_out, table, lens)
     _bad("these arguments are not accepted")
 
 
@@ -261,12 +261,12 @@ def splitzip_paged_attention(q: torch.Tensor, pages: Pages, table: torch.Tensor,
     ok = (len(qs) == 3 and qs[2] == pages.head_dim and out.shape == qs and q.dtype is _B16 and out.dtype is _B16
           and qst[2] == 1 and ost[2] == 1 and q.get_device() == out.get_device() == pages.index == _current_device()
           and window >= 0 and sinks >= 0
-          and len(ts) == 2 and table.dtype is _I32 and table.is_contiguous() and table.is_cuda
-          and lens.dtype is _I32 and lens.shape == ts[:1] and lens.is_contiguous() and lens.is_cuda
-          and q_start.dtype is _I32 and q_start.shape == (ts[0] + 1,) and q_start.is_contiguous() and q_start.is_cuda
-          and workspace.dtype is _U8 and workspace.is_contiguous() and workspace.is_cuda
+          and len(ts) == 2 and table.dtype is _I32 and table.is_contiguous() and table.get_device() == pages.index
+          and lens.dtype is _I32 and lens.shape == ts[:1] and lens.is_contiguous() and lens.get_device() == pages.index
+          and q_start.dtype is _I32 and q_start.shape == (ts[0] + 1,) and q_start.is_contiguous() and q_start.get_device() == pages.index
+          and workspace.dtype is _U8 and workspace.is_contiguous() and workspace.get_device() == pages.index
           and 0 < max_q_tokens <= qs[0] and (kv_tokens is None or 0 < kv_tokens <= ts[1] * pages.page_tokens)
-          and (lse is None or (lse.dtype is _F32 and lse.shape == (qs[1], qs[0]) and lse.is_contiguous() and lse.is_cuda)))
+          and (lse is None or (lse.dtype is _F32 and lse.shape == (qs[1], qs[0]) and lse.is_contiguous() and lse.get_device() == pages.index)))
     if not ok:
         _check_attention(q, pages, table, q_start, lens, out, workspace, max_q_tokens, kv_tokens, lse, window, sinks)
     if kv_tokens is None:
@@ -303,5 +303,5 @@ def _check_attention(q, pages, table, q_start, lens, out, workspace, max_q_token
         _bad(f"max_q_tokens is {max_q_tokens}, of {shape[0]} tokens")
     if kv_tokens is not None and kv_tokens <= 0:
         _bad(f"kv_tokens is {kv_tokens}")
-    _check_device(pages, q, out)
+    _check_device(pages, q, out, table, q_start, lens, workspace, lse)
     _bad("these arguments are not accepted")

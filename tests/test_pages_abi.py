@@ -186,3 +186,49 @@ def test_the_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
                dict(lse=torch.zeros((5, 4)))):
         refused(pg.splitzip_paged_attention, **{**good, **kw})
     assert pg.splitzip_paged_attention_workspace_bytes(q, p, table, 0) == 0
+
+
+class Here(torch.Tensor):
+    """A tensor that says that it lies on GPU 0."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+class There(Here):
+    def get_device(self):
+        return 1
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    """Every tensor of a call in turn on the other GPU; with all of them on the current one the call is made."""
+    def zeros(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Here)
+    calls = []
+    for module in (pg, pg._sz):
+        monkeypatch.setattr(module, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(pg, "_stream_of", lambda s: 0)
+    for name in ("_fn_store", "_fn_load", "_fn_attention"):
+        monkeypatch.setattr(pg, name, lambda *a: calls.append(a) or 0)
+    bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    rows = {"k": zeros(torch.int8, 4, 16, 2, 64), "v": zeros(torch.int8, 4, 16, 2, 64),
+            "k_exp": zeros(u8, 4, 16, 2, 4), "v_exp": zeros(u8, 4, 16, 2, 4)}
+    p = pg.Pages(**rows)
+    for name in ("v", "k_exp", "v_exp"):
+        monkeypatch.setattr(There, "device", torch.device("cuda:1"), raising=False)
+        with pytest.raises(sz.SplitZipError):
+            pg.Pages(**{**rows, name: rows[name].as_subclass(There)})
+    store = {"k": zeros(bf16, 5, 2, 64), "v": zeros(bf16, 5, 2, 64), "slots": zeros(torch.int64, 5)}
+    load = {"table": zeros(i32, 3, 2), "lens": zeros(i32, 3), "k_out": zeros(bf16, 3, 30, 2, 64), "v_out": zeros(bf16, 3, 30, 2, 64)}
+    attend = {"q": zeros(bf16, 5, 4, 64), "table": zeros(i32, 3, 2), "q_start": zeros(i32, 4), "lens": zeros(i32, 3),
+              "out": zeros(bf16, 5, 4, 64), "workspace": zeros(u8, 1 << 16), "lse": zeros(torch.float32, 4, 5)}
+    for fn, args, more in ((pg.splitzip_pages_store, store, {}), (pg.splitzip_pages_load, load, {}),
+                           (pg.splitzip_paged_attention, attend, {"max_q_tokens": 3})):
+        calls.clear()
+        fn(pages=p, **args, **more)
+        assert len(calls) == 1
+        for name in args:
+            with pytest.raises(sz.SplitZipError):
+                fn(pages=p, **{**args, name: args[name].as_subclass(There)}, **more)
+        assert len(calls) == 1, fn.__name__
