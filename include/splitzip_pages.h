@@ -70,8 +70,9 @@ typedef struct splitzip_pool {
 
 /* The keys and values of n tokens into their slots.
  *   k, v   BF16 [n, kv_heads, head_dim], e.g. slices of a fused projection
- *   slots  int64[n], page * page_tokens + slot, each used once; a token whose
- *          slot is outside the pool is dropped
+ *   slots  int64[n], page * page_tokens + slot, each used once (a slot named twice
+ *          holds a mixture of both tokens); a token whose slot is outside the pool
+ *          is dropped
  * BF16 rows are copied, E5M2 values rounded to nearest even (infinite past the
  * largest finite one).  n * kv_heads < 2^31.  One launch; n = 0 enqueues nothing. */
 typedef struct splitzip_pages_store_args {
@@ -124,7 +125,9 @@ splitzip_status splitzip_pages_load(const splitzip_pages_load_args *args, splitz
  *   lens     int32[batch], with the new tokens counted
  * Scores, the softmax statistics and sums are held in 32 bits; a query that sees
  * nothing, or scores of -infinity alone, gets out = 0 and lse = -inf.  Tokens
- * that a query does not see contribute nothing to it, whatever their slots hold.
+ * that a query does not see contribute nothing to it, whatever their slots hold;
+ * where it sees a quantised token whose exponent bytes are not ones that the store
+ * writes, its out and lse are unspecified.
  * q_heads a multiple of kv_heads, at most SPLITZIP_MAX_GROUP times it; scale
  * positive and finite; kv_tokens <= table_width * page_tokens; max_q_tokens <=
  * tokens; tokens * (q_heads / kv_heads) and kv_tokens at most 2^31 - 256; batch *

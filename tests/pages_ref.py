@@ -20,6 +20,8 @@ def two_to(k):
 
 def quantise(x, fmt):
     """(signed code numbers' magnitudes index, sign, exponent bytes [..., 4]) of BF16 rows [..., dim]."""
+    if x.numel() > 1 << 22 and len(x) > 1:      # half at a time: the table of distances is large
+        return tuple(map(torch.cat, zip(*(quantise(half, fmt) for half in x.tensor_split(2)))))
     grid, beyond, low, high = GRID[fmt]
     grid = torch.tensor(grid, dtype=torch.float64, device=x.device)
     v = x.double().unflatten(-1, (4, -1))
