@@ -48,17 +48,29 @@ struct Plans {
     size_t at_wide, bytes;  // of the workspace: where the widened caches lie, and in all
 };
 bool plan(const splitzip_paged_attention_args& a, Plans& p) {
-    constexpr uint32_t kFewRows = 16, kManyRows = 512;
+    constexpr uint32_t kFewRows = 16;
     constexpr uint64_t kMostWidened = 4ull << 30;
+    const uint32_t many_rows = a.pool.format == SPLITZIP_FORMAT_E5M2 && a.pool.head_dim == 128 ? 2048 : 1024;
     const uint64_t most = (uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads);
-    // Tiles of 128 query rows on the tensor cores from 17 rows on.  One sequence that may
-    // have as many goes to them whatever it has.
+    // Tiles of 128 query rows on the tensor cores from 17 rows on: where the other kernel
+    // would read each key a third time (8 heads of 128, 20 rows of each of 16 sequences of
+    // 16k: BF16 159 us, 248 there, E5M2 172 and 190, INT8 202 and 300, E2M1 190 and 273; of
+    // 2 of 8k 25 to 30 in both).  One sequence that may have as many goes to them whatever
+    // it has.
     p.few = most <= kFewRows || a.batch > 1;
     p.upto = p.few ? kFewRows : 0;
-    // With two pairs of such tiles to a sequence and head, widening its cache to BF16 first
-    // costs less than widening each tile of slots for each pair.
-    p.from = a.batch > 1 ? kManyRows : 0;
-    p.many = a.pool.format != SPLITZIP_FORMAT_BF16 && most > kManyRows && widened_bytes(a, p.from) <= kMostWidened;
+    // Each pair of such tiles widens the slots that it reads.  With more than four pairs to
+    // a sequence and head, widening its cache to BF16 ahead of them costs less; E5M2's bytes
+    // are widened by a permute alone, in half the time, and at head_dim 128 the products
+    // cover that up to eight pairs.  8 heads, 2 sequences of 16k, widened ahead and not, us:
+    //   rows           512         1024        1536        2048        4096
+    //   INT8  128    96   77    139  130    213  218    219  230
+    //   INT8   64    68   59    101  102    154  170    162  184    293  353
+    //   E2M1  128    93   73    135  124    208  210    215  222
+    //   E5M2   64    67   55    100   94    153  157    161  168    291  323
+    //   E5M2  128    94   70    137  119    210  203    217  210    392  406
+    p.from = a.batch > 1 ? many_rows : 0;
+    p.many = a.pool.format != SPLITZIP_FORMAT_BF16 && most > many_rows && widened_bytes(a, p.from) <= kMostWidened;
     p.some = most > kFewRows && !(p.many && a.batch == 1);
     if (!p.many) p.from = 0xFFFFFFFFu;
     p.bytes = kAttentionHeader;

@@ -15,9 +15,9 @@ from tests.test_gpu_pages import DEV, FORMATS, attend, batch_of, check, close, f
 
 pytestmark = pytest.mark.gpu
 QUANTISED = ["int8", "e2m1"]
-#: (new tokens, q_heads, kv_heads, head_dim): single tokens, tiles of rows, more than 512 rows to a head
+#: (new tokens, q_heads, kv_heads, head_dim): single tokens, tiles of rows, more than 1024 and 2048 rows to a head
 COUNTS = [([1, 1, 1], 8, 2, 128), ([1, 2, 1], 8, 2, 64), ([30, 1, 90], 8, 2, 128), ([140, 20, 3], 6, 2, 64),
-          ([200, 1, 140], 8, 2, 128), ([300, 64, 1], 8, 2, 64), ([0, 0, 260], 8, 2, 128)]
+          ([200, 1, 140], 8, 2, 128), ([300, 64, 1], 8, 2, 64), ([0, 0, 260], 8, 2, 128), ([530, 1, 270], 8, 2, 128)]
 ids = [f"{'_'.join(map(str, c))}x{h}x{k}x{d}" for c, h, k, d in COUNTS]
 
 
