@@ -12,8 +12,8 @@
 // exponentials and registers that 16 rows take.  P^T comes out of S^T by a
 // transposition of 8 x 8 blocks between registers (movmatrix).
 //
-// A CTA's warps share a ring of slot tiles (64 slots, 128 at head_dim 64, a quarter of
-// them each warp's), which TMA fills page by page, swizzled as ldmatrix reads them.
+// A CTA's warps share a ring of slot tiles (64 or 128 slots, a quarter of them each
+// warp's), which TMA fills page by page, swizzled as ldmatrix reads them.
 // The warps take turns at loading the next tile, so the cost of that is shared, and
 // each has the page numbers of its next turn four tiles ahead.  What no query sees is
 // not looked up (its page may have been given away): it is loaded from behind the
@@ -51,13 +51,27 @@ struct PagedRowsParams {
     uint32_t test_cta, test_tile;  // a copy that a test has left out
 };
 
-template <int D, int kFmt>
+// Slots of a tile that a warp takes.  32 give it two independent blocks of work, and half
+// the waits of 16: 16 single tokens over 16k caches of 8 heads of 128, 4 query heads to
+// each, E2M1 76 us (91 with 16), of 16 query heads 114 (140), E5M2 100 (108), INT8 126
+// (146).  They do not fit in BF16, and in 8 bits only three CTAs of them fit an SM: in
+// E5M2 that costs nothing (88 us in both), but INT8's widening wants the fourth one in
+// tiles of 8 rows (24 windows of 4096 42 us, with 32 slots 46).
+constexpr uint32_t warp_slots(uint32_t format, uint32_t d, uint32_t tile_rows) {
+    return format == kBf16 || (format == kInt8 && tile_rows == 8) ? 2048 / d : 32;
+}
+// CTAs to an SM, by registers and shared memory.
+constexpr uint32_t ctas_per_sm(uint32_t format, uint32_t d, uint32_t tile_rows) {
+    return format != kBf16 && tile_rows == 8 && (d == 64 || format != kE5m2) ? 4 : 3;
+}
+
+template <int D, int kFmt, int kTileRows>
 struct PagedShape {
     static constexpr int kRow = kRowBytes<D, kFmt>;
-    static constexpr int kPart = 2048 / D;                   // slots of a tile that a warp takes
+    static constexpr int kPart = warp_slots(kFmt, D, kTileRows);
     static constexpr int kSlots = kWarpsRows * kPart;        // slots per tile
     static constexpr int kTile = kSlots * kRow;              // bytes of its keys, and of its values
-    static constexpr int kStages = kFmt == kBf16 ? 2 : kFmt == kE2m1 ? 4 : 3;
+    static constexpr int kStages = kTile >= 16384 ? 2 : kTile >= 8192 ? 3 : 4;
     static constexpr int kExps = kQuantised<kFmt> ? 4 * kSlots : 0;  // bytes of its keys' exponents, and of its values'
     // Shared memory: the rings of tiles and of exponents, the values' powers, queries.
     static constexpr int kAtExps = kStages * 2 * kTile, kAtPowers = kAtExps + kStages * 2 * kExps;
@@ -186,14 +200,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// CTAs to an SM, by registers and shared memory.
-template <int kFmt, int NB>
-constexpr int kPagedCtas = kWide<kFmt> && NB == 1 ? 4 : 3;
-
 // NB: blocks of 8 query rows.
 template <int D, int kFmt, int NB>
-__global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
-    using S = PagedShape<D, kFmt>;
+__global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB)) paged_rows_kernel(const __grid_constant__ PagedRowsParams p) {
+    using S = PagedShape<D, kFmt, 8 * NB>;
     constexpr bool kHalf = kWide<kFmt>;  // operands FP16, else BF16
     constexpr int kTileRows = 8 * NB;
     constexpr bool kBlockSums = kQuantised<kFmt> && !(kFmt == kE2m1 && D == 64);  // a step's 16 values are of one block
@@ -737,7 +747,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, kPagedCtas<kFmt, NB>) paged_r
 
 template <int D, int kFmt, int NB>
 cudaError_t launch(const PagedRowsParams& p, uint32_t ctas, bool after_tiles, cudaStream_t s) {
-    using S = PagedShape<D, kFmt>;
+    using S = PagedShape<D, kFmt, 8 * NB>;
     static_assert(S::kAtExps >= kWarpsRows * 8 * NB * D * 4, "partial results take the place of the ring");
     constexpr int kSmem = S::kAtQueries + 8 * NB * D * 2 + (int)sizeof(PagedRowsShared<S::kStages, 8 * NB>);
     Wave w;
@@ -790,14 +800,13 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
     const uint64_t most_rows = (uint64_t)a.max_q_tokens * group;
     p.row_tiles = (uint32_t)((std::min<uint64_t>(most_rows, rows_upto) + tile - 1) / tile);
     const uint64_t units = (uint64_t)a.batch * a.pool.kv_heads * p.row_tiles;
-    const uint32_t slots = 2048 / d;  // of a tile that a warp takes
+    const uint32_t slots = warp_slots(a.pool.format, d, tile), ctas = ctas_per_sm(a.pool.format, d, tile);
     uint64_t most = a.kv_tokens;
     if (a.window) most = std::min(most, (uint64_t)a.window + a.sinks + (tile + group - 1) / group + 2 * slots);
     // In a batch with longer chunks one of the sequences is such a one, and of the others'
     // row tiles the first has the rows.
     const uint64_t likely = most_rows > rows_upto ? (uint64_t)std::max(1u, a.batch - 1) * a.pool.kv_heads : units;
-    p.splits = attention_rows_splits(likely, most, slots, 16, d,
-                                     a.pool.format != kBf16 && tile == 8 ? 4 : 3);
+    p.splits = attention_rows_splits(likely, most, slots, 16, d, ctas);
     // Splits in several clusters are counted by row tile, in a header of limited size.
     if (p.splits > 8 && units > kSms) p.splits = 8;
     p.ctas = units * p.splits;
@@ -808,10 +817,10 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
     // for long: 16 sequences of 8k to 16k, 8 heads of 128, in 8 bits 76 us (86 with splits
     // alike), in 4 67 (79), in BF16 126 (124); 5 of up to 9000 in 8 bits 28 (26), all 16
     // of 16k 100 (95).
-    const uint64_t at_once = (uint64_t)kSms * (tile == 8 ? 4 : 3);
+    const uint64_t at_once = (uint64_t)kSms * ctas;
     static_assert(kMostCounted <= kAttentionStatus, "a byte counts the splits of a row tile");
     if (a.pool.format != kBf16 && a.batch > 1 && a.batch <= kMostShared && units <= kMostCounted && units < at_once &&
-        likely * (most / (kWarpsRows * slots)) >= kSharedTiles * at_once) {
+        likely * (most / (kWarpsRows * (2048 / d))) >= kSharedTiles * at_once) {
         p.splits = 0;
         p.ctas = at_once;
         p.bytes = kAttentionHeader + at_once * tile * (d + 4) * 4;
@@ -831,7 +840,7 @@ cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t r
     p.splits = plan.splits;
     p.cluster = plan.splits ? std::min(plan.splits, 8u) : 1;
     const splitzip_pool& pool = a.pool;
-    const uint32_t slots = kWarpsRows * 2048 / pool.head_dim;  // of a tile
+    const uint32_t slots = kWarpsRows * warp_slots(pool.format, pool.head_dim, tile_rows(a, rows_upto));  // of a tile
     p.box = std::min(pool.page_tokens, slots);
     p.boxes = slots / p.box;
     p.bulk_exps = bulk_exponents(pool);
