@@ -86,10 +86,8 @@ struct PagedPart {
 
 // Sequences whose work is shared out in one launch, by tables of their slot tiles.
 constexpr uint32_t kMostShared = 1024;
-// Row tiles whose splits are counted so, a byte each in the workspace's header.
-constexpr uint32_t kMostCounted = 1016;
-// The least slot tiles of a split, and the most that a CTA may have where work is shared out.
-constexpr uint32_t kLeastTiles = 4, kSharedTiles = 32;
+// The least slot tiles of a split where work is shared out.
+constexpr uint32_t kLeastTiles = 4;
 
 // Shares the work out by the sequences' lengths: splits of at most T slot tiles, with the
 // smallest T for which they are no more than the grid's CTAs.  `part` comes back with
@@ -812,15 +810,22 @@ bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto,
     p.ctas = units * p.splits;
     p.bytes = attention_rows_bytes(units, p.splits, tile, d);
     // Sequences of a batch differ in length, and a number of splits that is the same for all
-    // does not fill the GPU evenly.  Sharing the work out by length costs 5 us (the tables,
-    // and joining through memory), so it is for caches whose widening keeps the GPU busy
-    // for long: 16 sequences of 8k to 16k, 8 heads of 128, in 8 bits 76 us (86 with splits
-    // alike), in 4 67 (79), in BF16 126 (124); 5 of up to 9000 in 8 bits 28 (26), all 16
-    // of 16k 100 (95).
+    // does not fill the GPU evenly, or (eight to a cluster) not at all.  Sharing the work out
+    // by length costs 5 us (the tables, and joining through memory), so it is for splits of
+    // 3000 slots and more, and quantised caches, whose widening keeps the GPU busy for long
+    // enough.  8 heads of 128, 32 query heads, splits alike and shared out, us:
+    //   sequences of    half to full length      one length
+    //   INT8   3 x 30k        57    42             59    46
+    //         16 x 16k        86    76             94   100
+    //         24 x 16k       111   109            128   135
+    //         40 x  4k        70    59             76    78
+    //   E2M1  16 x 16k        67    58             72    76
+    // and not taken: INT8 4 x 16k 35 33, 36 38; 16 x 8k 46 45, 52 57; 75 x 4k (600 units for
+    // 608 CTAs) 90 92, 101 104; E5M2 16 x 16k 67 70, 81 86; BF16 124 126.
     const uint64_t at_once = (uint64_t)kSms * ctas;
-    static_assert(kMostCounted <= kAttentionStatus, "a byte counts the splits of a row tile");
-    if (a.pool.format != kBf16 && a.batch > 1 && a.batch <= kMostShared && units <= kMostCounted && units < at_once &&
-        likely * (most / (kWarpsRows * (2048 / d))) >= kSharedTiles * at_once) {
+    static_assert(3 * kSms <= kAttentionStatus, "a byte of the workspace's header counts the splits of a row tile");
+    if ((a.pool.format == kInt8 || a.pool.format == kE2m1) && a.batch > 1 && a.batch <= kMostShared &&
+        units <= at_once * 3 / 4 && most / p.splits >= 3000) {
         p.splits = 0;
         p.ctas = at_once;
         p.bytes = kAttentionHeader + at_once * tile * (d + 4) * 4;
