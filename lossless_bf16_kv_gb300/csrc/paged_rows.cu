@@ -4,7 +4,10 @@
 // query heads) in tiles of 8 or 16, a tile's slots in splits, one CTA each, each of
 // its four warps with its own slot tiles, running maximum, sum and output as in
 // attention_rows.cu, joined at the end in a fixed order.  Every key and value is
-// read once: HBM bounds it, next to the widening of quantised codes.
+// read once: HBM bounds BF16 (16 single tokens over 16k caches of 8 heads of 128, 32 query
+// heads: 150 us, 7.1 TB/s) and E5M2 (80, 6.7); of quantised codes the instructions that
+// widen them and their latencies (99 us in 8 bits, 76 in 4; 5.6 and 3.7 TB/s, issue slots
+// half used).
 //
 // The products are transposed: S^T = K Q^T and O^T += V^T P^T, with slots, then a
 // head's values as the 16 rows of an m16n8k16 product and the query rows as its 8

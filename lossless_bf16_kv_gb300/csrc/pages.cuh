@@ -91,11 +91,6 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The FP16 power of block b, twice, of a slot's four.
-__device__ __forceinline__ uint32_t twice(uint2 powers, uint32_t b) {
-    return prmt(b & 2 ? powers.y : powers.x, 0u, b & 1 ? 0x3232u : 0x1010u);
-}
-
 // One value of a row as the products have it, for the rare ones that are not finite.
 template <int D, int kFmt>
 __device__ __forceinline__ float page_value(const uint8_t* row, const uint8_t* exps, uint32_t d) {
