@@ -329,3 +329,79 @@ def test_load_of_tables_with_a_page_many_times(fmt):
     for b in range(2):
         for i, x in enumerate("kv"):
             assert torch.equal(out[i, b].double(), ref.sequence(p, table[b], 50, x))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("most", [17, 257, 600, 1500])
+def test_attention_of_small_sequences_under_large_bounds(most, fmt):
+    """max_q_tokens and the rows of q far above what the sequences bring: every kernel that may run has little or nothing."""
+    q, p, table, start, lens = batch_of([1, 3, 0, 2], [300, 411, 290, 5], 8, 2, 128, 16, fmt, seed=most, pad=1500)
+    out, lse = check(q, p, table, start, lens, most=most)
+    near, near_lse = attend(q[:6], p, table, start, lens)
+    close(out[:6].float(), near.double(), 2.0 ** -7 * near.abs().double() + 2.0 ** -6 * near.abs().max().item(), "out")
+    assert bool((out[6:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_one_graph_takes_batches_of_any_make_up(fmt):
+    """Captured once for 1000 rows; then other ranges, lengths and tables, sequences moving between the kernels."""
+    q, p, table, start, lens = batch_of([600, 1, 100, 1], [900, 850, 411, 17], 8, 2, 128, 16, fmt, seed=23, pad=298)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 700)
+    out, lse = torch.zeros_like(q), torch.zeros((8, 1000), device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pg.splitzip_paged_attention(q, p, table, start, lens, out, ws, 700, lse=lse)
+    full = torch.randperm(p.pages, generator=gen(24), device=DEV)[: table.numel()].view(table.shape).int()
+    for starts, n in (([0, 600, 601, 701, 702], [900, 850, 411, 17]), ([0, 1, 2, 3, 4], [912, 1, 0, 500]),
+                      ([100, 101, 701, 701, 800], [300, 912, 4, 700]), ([0, 0, 0, 0, 0], [1, 2, 3, 4]),
+                      ([3, 260, 517, 774, 1000], [257, 900, 100, 226]), ([0, 800, 1000, 1000, 1000], [900, 900, 900, 900])):
+        start.copy_(ints(starts))
+        lens.copy_(ints(n))
+        table.copy_(full)
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        kept = start.clone()
+        if starts[1] - starts[0] > 700:                 # left out
+            kept[0] = kept[1]
+        mine = torch.zeros(1000, dtype=torch.bool, device=DEV)
+        for rows, o, l, tol, ltol in ref.attention(q, p, table, kept, lens, table.shape[1] * 16, 0, 0, 128 ** -0.5):
+            close(out[rows], o, tol, "out")
+            close(lse[:, rows], l, ltol, "lse")
+            mine[rows] = True
+        assert bool((out[~mine] == 7.0).all()) and bool((lse[:, ~mine] == 7.0).all())
+    assert serving.splitzip_attention_status(ws) == sz.OK
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_at_the_far_end_of_the_lengths(fmt):
+    """Positions up to 2^31: a table that names one page again and again.  With a window and sinks, in both kernels;
+    and in 8 bits every slot, whose weights are those of the page's, lse more by the log of how often."""
+    size, width = 65536, 1 << 15
+    n = width * size - 256
+    q, p, table, start, _ = batch_of([1], [size], 4, 1, 64, size, fmt, seed=25, spare=0)
+    far = torch.zeros((1, width), dtype=torch.int32, device=DEV)
+    g = gen(26)
+    for count in (1, 3, 40):
+        x = randn(g, count, 4, 64).bfloat16()
+        window, sinks = 500, 5
+        out, lse = attend(x, p, far, ints([0, count]), ints([n]), window=window, sinks=sinks, kv_tokens=n)
+        # The same slots in a short cache: the sinks' page in front, the window's end where the far one has it.
+        near = torch.zeros((1, 2), dtype=torch.int32, device=DEV)
+        for rows, o, l, tol, ltol in ref.attention(x, p, near, ints([0, count]), ints([2 * size - 256]), 2 * size, window,
+                                                   sinks, 64 ** -0.5):
+            close(out[rows], o, tol, "out")
+            close(lse[:, rows], l, ltol, "lse")
+    if fmt == "int8":
+        n = width * size // 2
+        out, lse = attend(q, p, far, ints([0, 1]), ints([n]), kv_tokens=n)
+        (rows, o, l, tol, ltol), = ref.attention(q, p, ints([[0]]), ints([0, 1]), ints([size]), size, 0, 0, 64 ** -0.5)
+        # A split's sum has up to 2^30 terms in 32 bits, of which a lane's chain has at most 2^30 / 2^13.
+        close(out, o, tol + 2.0 ** -7 * o.abs().amax(), "out")
+        close(lse, l + math.log(n // size), ltol + 2.0 ** -7, "lse")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_keys_and_values_in_one_tensor(fmt):
+    q, p, table, start, lens = batch_of([1, 30], [300, 411], 8, 2, 128, 16, fmt, seed=27)
+    check(q, pg.Pages(p.k, p.k, p.k_exp, p.k_exp), table, start, lens)
