@@ -594,10 +594,12 @@ __global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB))
                                         w[x][0] = int8_scaled<kInt8_02>(z, f), w[x][1] = int8_scaled<kInt8_13>(z, f);
                                     }
                                 } else {
-                                    // Bytes of the same value of both slots: values 0 and 2, then 1 and 3.
-                                    uint32_t z = (v & 0x0F0Fu) | (v >> 12 & 0xF0F0u);
-                                    z |= ((v >> 4 & 0x0F0Fu) | (v >> 16 & 0xF0F0u)) << 16;
-                                    e2m1_pairs(w[x], z);
+                                    // Values 0 and 1, then 2 and 3 of the one slot and of the other, to each value
+                                    // of both slots: 0 and 2, then 1 and 3.
+                                    uint32_t z[4];
+                                    e2m1_pairs(z, v);
+                                    w[x][0] = prmt(z[0], z[2], 0x5410), w[x][1] = prmt(z[1], z[3], 0x5410);
+                                    w[x][2] = prmt(z[0], z[2], 0x7632), w[x][3] = prmt(z[1], z[3], 0x7632);
 #pragma unroll
                                     for (int n = 0; n < 4; n++) w[x][n] = mul_half2(w[x][n], f);
                                 }
