@@ -199,11 +199,12 @@ __device__ __forceinline__ void set_work(TilesShared& sh, const Mask& mask, uint
     sh.sinks = mask.sinks;
     sh.window = mask.window;
     for (int t = 0; t < 2; t++) {
-        // No tile of slots is whole for a tile without queries.
+        // All tiles of slots are whole for a tile without queries: its rows go nowhere, and
+        // masking every step would make it the CTA's slower one.
         const uint32_t ta = t0 + (kTwin ? 0 : t * tokens), tb = min(ta + tokens, count);
         const WholeTiles whole(sh, mask.first + (int32_t)ta, mask.first + (int32_t)tb - 1);
-        sh.upto[t] = ta < count ? whole.upto : -1;
-        sh.after[t] = whole.after;
+        sh.upto[t] = ta < count ? whole.upto : 0x7FFFFFFF;
+        sh.after[t] = ta < count ? whole.after : -1;
         sh.whole_sinks = whole.sinks;
     }
 }
