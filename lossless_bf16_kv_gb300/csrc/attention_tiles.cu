@@ -28,7 +28,10 @@ struct TilesParams {
         const uint32_t heads = a.batch * a.kv_heads, rc = row_ctas - 1 - unit / heads, bh = unit % heads;
         sh.b = bh / a.kv_heads;
         sh.h = bh - sh.b * a.kv_heads;
-        set_work<kTwin>(sh, Mask(a, sh.b), rc * 2 * tokens, a.q_tokens, tokens, split, splits);
+        set_work<kTwin>(sh, Mask(a, sh.b), rc * 2 * tokens, a.q_tokens, tokens, [&](uint32_t n, uint32_t& j0, uint32_t& j1) {
+            j0 = (uint32_t)((uint64_t)n * split / splits);
+            j1 = (uint32_t)((uint64_t)n * (split + 1) / splits);
+        });
     }
     // Where query token tok and query head hq of this CTA's sequence lie.
     __device__ __forceinline__ uint32_t queries(const TilesShared&) const { return a.q_tokens; }
@@ -60,13 +63,13 @@ inline bool is_twin(const splitzip_attention_args& a) {
     return a.q_tokens <= kTileM / (a.q_heads / a.kv_heads) && a.kv_tokens > kBN;
 }
 
-uint32_t attention_tiles_splits(uint64_t units, uint64_t most, uint64_t at_once) {
+uint32_t attention_tiles_splits(uint64_t units, uint64_t most, uint64_t at_once, uint64_t* steps) {
     // The splits (one cluster) with the least time, as waves of clusters times the steps
     // of a split plus kSplitCost steps for a CTA's start, join and end.  A cluster lies
     // within one of the GPU's groups of SMs, so fewer of the large ones run at once (as
     // cudaOccupancyMaxActiveClusters has it): 16 units of 2048 slots of 64 take 20.6 us
     // in 8 splits, two waves, and 11.7 in 6.
-    constexpr uint64_t kSplitCost = 4, kAtOnce[9] = {0, kSms, 76, 46, 36, 28, 23, 15, 15};
+    constexpr uint64_t kAtOnce[9] = {0, kSms, 76, 46, 36, 28, 23, 15, 15};
     uint64_t best = ~0ull;
     uint32_t splits = 1;
     for (uint64_t n = 1; n <= 8 && (n == 1 || 2 * n <= most); n++) {
@@ -76,6 +79,7 @@ uint32_t attention_tiles_splits(uint64_t units, uint64_t most, uint64_t at_once)
             splits = (uint32_t)n;
         }
     }
+    if (steps) *steps = best;
     return splits;
 }
 

@@ -72,8 +72,10 @@
 
 namespace splitzip {
 
-// Splits of `units` row tiles that see up to `most` tiles of slots and take `at_once` of them a step.
-uint32_t attention_tiles_splits(uint64_t units, uint64_t most, uint64_t at_once);
+// Splits of `units` row tiles that see up to `most` tiles of slots and take `at_once` of them a
+// step, and the steps that this takes in all.
+constexpr uint64_t kSplitCost = 4;  // of a CTA, in steps
+uint32_t attention_tiles_splits(uint64_t units, uint64_t most, uint64_t at_once, uint64_t* steps = nullptr);
 
 constexpr int kBN = 128;       // slots per step
 constexpr int kTileM = 128;    // query rows per tile
@@ -130,6 +132,9 @@ struct TilesShared {
     uint32_t b, h, t0, steps;
     int32_t first_row, count;  // a packed sequence's first query token, and their number
     uint32_t rank;             // its number among those of the launch
+    // Pieces of this CTA's work, joined through memory: which one, of how many; the first
+    // one's place there, and the counter.
+    uint32_t piece, pieces, first_piece, counter, last;
     int32_t s0, jump_at, jump_to;
     int32_t n, first, sinks, p0, p1;
     uint32_t window;
@@ -180,17 +185,18 @@ __device__ __forceinline__ float exchange(TilesShared& sh, uint32_t t, uint32_t 
     return other;
 }
 
-// What a CTA's `per` query tokens from t0 on, of `count`, walk: its part of the slot
-// tiles that they see.
-template <bool kTwin>
-__device__ __forceinline__ void set_work(TilesShared& sh, const Mask& mask, uint32_t t0, uint32_t count, uint32_t tokens, uint32_t split, uint32_t splits) {
+// What a CTA's query tokens from t0 on, of `count`, walk: of the slot tiles that they see
+// those from j0 to j1 - 1, as cut(their number, j0, j1) has it.
+template <bool kTwin, class Cut>
+__device__ __forceinline__ void set_work(TilesShared& sh, const Mask& mask, uint32_t t0, uint32_t count, uint32_t tokens, const Cut& cut) {
     const uint32_t t1 = min(t0 + 2 * tokens, count);
     sh.p0 = mask.first + (int32_t)t0;
     sh.p1 = mask.first + (int32_t)t1 - 1;
     const SlotTiles tiles(mask, sh.p0, sh.p1, kBN);
-    const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / splits);
+    uint32_t j0, j1;
+    cut(tiles.count, j0, j1);
     sh.t0 = t0;
-    sh.steps = (uint32_t)((uint64_t)tiles.count * (split + 1) / splits) - j0;
+    sh.steps = j1 - j0;
     sh.s0 = (int32_t)(tiles.tile(j0) * kBN);
     sh.jump_at = j0 < tiles.head ? (int32_t)(tiles.head - j0) : -1;
     sh.jump_to = (int32_t)(tiles.from * kBN);
@@ -864,6 +870,74 @@ __device__ __forceinline__ void read_output(const Params& p, const TilesShared& 
     }
 }
 
+// Rows [columns in fours, then m and l][row] of a piece's partial result.
+template <int D>
+constexpr uint32_t kPieceFloat4s = (D / 4 + 1) * 2 * kTileM;
+
+// Leaves this piece's rows in memory, and joins all pieces', in their order, in the CTA that
+// comes last.  Lanes hold neighbouring rows, so both ways run in whole lines.  All softmax
+// threads.
+template <int D, int kFmt, class Params>
+__device__ __forceinline__ void join_pieces(const Params& p, TilesShared& sh, uint32_t oa, uint32_t t, uint32_t half, uint32_t r, bool valid,
+                                            int32_t pos, float m, float l, __nv_bfloat16* out, float* lse) {
+    constexpr uint32_t kBar = 9, kStep = 2 * kTileM;  // a barrier that no pair of warps has
+    const uint32_t row = t * kTileM + r, pieces = sh.pieces;
+    float4* all = p.partials + (uint64_t)sh.first_piece * kPieceFloat4s<D> + row;
+    float4* mine = all + sh.piece * kPieceFloat4s<D>;
+#pragma unroll 1
+    for (int c = half * (D / 64); c < (int)(half + 1) * (D / 64); c++) {  // this half's columns
+        float o[32];
+        read_output<D, kFmt, false>(p, sh, oa, t, pos, c, o);
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) __stcg(mine + (8 * c + x / 4) * kStep, make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]));
+    }
+    if (half == 0) __stcg(mine + D / 4 * kStep, make_float4(m, l, 0.0f, 0.0f));
+    __threadfence();
+    named_sync(kBar, kSoftmax);
+    if (threadIdx.x == 0) {  // a byte counts, and is 0 again for the next call when the last one has counted
+        const uint32_t by = 8 * (sh.counter & 3);
+        sh.last = (atomicAdd(p.counters + sh.counter / 4, 1u << by) >> by & 255u) == pieces - 1;
+        if (sh.last) atomicSub(p.counters + sh.counter / 4, pieces << by);
+        __threadfence();
+    }
+    named_sync(kBar, kSoftmax);
+    if (!*reinterpret_cast<const volatile uint32_t*>(&sh.last)) return;
+    float top = -INFINITY, sum = 0.0f;
+    for (uint32_t i = 0; i < pieces; i++) top = fmaxf(top, __ldcg(all + i * kPieceFloat4s<D> + D / 4 * kStep).x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    for (uint32_t i = 0; i < pieces; i++) {
+        const float4 ml = __ldcg(all + i * kPieceFloat4s<D> + D / 4 * kStep);
+        sum = fmaf(ml.y, exp2_approx(ml.x - base), sum);
+    }
+    const bool none = sum == 0.0f;  // nothing seen, or scores of -infinity alone
+    const float inv = 1.0f / sum;
+#pragma unroll 1
+    for (int c = half * (D / 32); c < (int)(half + 1) * (D / 32); c++) {
+        float4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; x++) v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (uint32_t i = 0; i < pieces; i++) {
+            const float4* from = all + i * kPieceFloat4s<D>;
+            const float f = exp2_approx(__ldcg(from + D / 4 * kStep).x - base);
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const float4 y = __ldcg(from + (4 * c + x) * kStep);
+                v[x] = make_float4(fmaf(y.x, f, v[x].x), fmaf(y.y, f, v[x].y), fmaf(y.z, f, v[x].z), fmaf(y.w, f, v[x].w));
+            }
+        }
+        if (valid) {
+#pragma unroll
+            for (int x = 0; x < 4; x += 2)
+                *reinterpret_cast<uint4*>(out + 16 * c + 4 * x) =
+                    none ? make_uint4(0, 0, 0, 0)
+                         : make_uint4(pack2<false>(v[x].x * inv, v[x].y * inv), pack2<false>(v[x].z * inv, v[x].w * inv),
+                                      pack2<false>(v[x + 1].x * inv, v[x + 1].y * inv), pack2<false>(v[x + 1].z * inv, v[x + 1].w * inv));
+        }
+    }
+    if (valid && lse && half == 0) *lse = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
 template <int D, int kFmt, bool kTwin, class Params>
 __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
     using S = TilesShape<D, kFmt, Params::kPaged>;
@@ -994,7 +1068,13 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
         const uint32_t oa = tmem + (((warp & 3) * 32) << 16) + S::kColO + t * D;
         __nv_bfloat16* out = p.out(sh, tok, hq);
         float* lse = p.a.lse ? p.lse(sh, tok, hq) : nullptr;
-        if (!kTwin && p.splits == 1) {
+        bool done = false;
+        if constexpr (Params::kPaged && !kTwin) {
+            done = p.splits == 1 && sh.pieces > 1;
+            if (done) join_pieces<D, kFmt>(p, sh, oa, t, half, rr, valid, pos, m, l, out, lse);
+        }
+        if (done) {
+        } else if (!kTwin && p.splits == 1) {
             const float inv = 1.0f / l;
             const bool none = l == 0.0f;  // nothing seen, or scores of -infinity alone
 #pragma unroll 1

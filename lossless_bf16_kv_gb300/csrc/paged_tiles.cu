@@ -33,18 +33,41 @@ bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from
     uint64_t most = ((uint64_t)a.kv_tokens + kBN - 1) / kBN;
     if (a.window)
         most = std::min(most, ((uint64_t)a.window + 2 * tokens + kBN - 1) / kBN + 1 + ((uint64_t)a.sinks + kBN - 1) / kBN);
-    p.splits = attention_tiles_splits(units, most, twin ? 2 : 1);
-    p.bytes = kAttentionHeader;
-    return (uint64_t)p.row_tiles * a.pool.kv_heads * p.splits <= 0x7FFFFFFFull;
+    uint64_t steps;
+    p.splits = attention_tiles_splits(units, most, twin ? 2 : 1, &steps);
+    // Or no splits, and the row tiles behind the last whole wave cut (as many as there are on
+    // the device) into pieces, as PagedTilesParams::part_of has it: where that takes fewer
+    // steps.  Joining through memory costs 4 and another for each piece.
+    const uint64_t waves = units / kSms, rest = units % kSms;
+    bool cut = !twin && rest && rest <= kSms * 2 / 3 && most >= PagedTilesParams::kLeastCut;
+    if (cut) {
+        uint64_t n = std::min<uint64_t>(kSms / rest, PagedTilesParams::kMostPieces);
+        while (n > 1 && n * n > most) n--;
+        const uint64_t longest = rest <= kSms / 2 ? (most + n - 1) / n : most - most / 3;
+        cut = waves * (most + kSplitCost) + longest + kSplitCost + 4 + std::max<uint64_t>(n, 2) < steps;
+    }
+    if (cut) p.splits = 1;
+    p.ctas = (uint64_t)p.row_tiles * a.pool.kv_heads * p.splits;
+    p.bytes = 0;
+    if (cut) {
+        p.ctas += kSms;
+        const uint64_t pieces = std::min<uint64_t>(p.row_tiles * (uint64_t)a.pool.kv_heads * PagedTilesParams::kMostPieces, 2 * kSms);
+        p.bytes = pieces * (a.pool.head_dim == 64 ? kPieceFloat4s<64> : kPieceFloat4s<128>) * sizeof(float4);
+    }
+    return p.ctas <= 0x7FFFFFFFull;
 }
 
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& plan, void* workspace,
-                               const void* widened, bool beside, const WaitTest& test, cudaStream_t s) {
+                               size_t at_partials, const void* widened, bool beside, const WaitTest& test, cudaStream_t s) {
     PagedTilesParams p;
     p.a = a;
     p.group = a.q_heads / a.pool.kv_heads;
     p.tokens = kTileM / p.group;
     p.splits = plan.splits;
+    uint8_t* space = static_cast<uint8_t*>(workspace);
+    p.partials = plan.bytes ? reinterpret_cast<float4*>(space + at_partials) : nullptr;
+    p.counters = reinterpret_cast<uint32_t*>(space + kTilesCounters + (widened ? kSms : 0));
+    static_assert(kTilesCounters + 2 * kSms <= kAttentionStatus && kSms % 4 == 0, "a byte for each row tile that is cut");
     p.rows_from = rows_from;
     p.rows_upto = rows_upto;
     p.widened = widened != nullptr;
@@ -66,7 +89,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     p.page_shift = 0;
     while ((1u << p.page_shift) < a.pool.page_tokens) p.page_shift++;
     p.bulk_exps = bulk_exponents(pool);
-    p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kAttentionStatus);
+    p.status = reinterpret_cast<uint32_t*>(space + kAttentionStatus);
     p.wait_limit = test.limit ? test.limit : wait_limit(0);  // a wait lasts a few steps at most
     p.test_cta = test.cta;
     p.test_tile = test.tile;
@@ -75,7 +98,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     if ((!wide && !make_map(p.qmap, a.q, 2, pool.head_dim, a.q_heads, a.tokens, 1, p.group, p.tokens, true, &one)) ||
         !page_map(p.kmap, pool, pool.k, p.box) || !page_map(p.vmap, pool, pool.v, p.box))
         return cudaErrorInvalidValue;
-    const uint32_t ctas = plan.row_tiles * pool.kv_heads * plan.splits;
+    const uint32_t ctas = (uint32_t)plan.ctas;
     const bool twin = is_twin(a, rows_upto);
     if (pool.head_dim == 64) return twin ? launch_paged_64_twin(p, ctas, beside, s) : launch_paged_64(p, ctas, beside, s);
     return twin ? launch_paged_128_twin(p, ctas, beside, s) : launch_paged_128(p, ctas, beside, s);

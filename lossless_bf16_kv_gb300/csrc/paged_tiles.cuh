@@ -27,7 +27,9 @@ struct PagedTilesParams {
     splitzip_paged_attention_args a;
     CUtensorMap qmap, kmap, vmap;
     uint32_t group, tokens;    // query tokens per tile: 128 / group
-    uint32_t splits;
+    uint32_t splits;           // a cluster's
+    float4* partials;          // of pieces of work, or NULL: no CTA's is cut
+    uint32_t* counters;        // a byte for each row tile that is cut
     uint32_t box, boxes;       // slots to a TMA box, and boxes to a tile
     uint32_t page_shift;
     uint32_t bulk_exps;        // a page's exponent bytes of a head are contiguous, in multiples of 16 bytes
@@ -39,6 +41,8 @@ struct PagedTilesParams {
     uint32_t test_cta, test_tile;  // a copy that a test has left out
 
     static constexpr bool kPaged = true;
+    // The most pieces of a row tile, and the least slot tiles of one that is cut.
+    static constexpr uint32_t kMostPieces = 16, kLeastCut = 24;
     // On a raw tile's barrier: its copies', and the lanes' whose own copies bring the exponents.
     __device__ __forceinline__ uint32_t raw_arrivals() const { return a.pool.format >= SPLITZIP_FORMAT_INT8 && !bulk_exps ? 33 : 1; }
     // Row-tile CTAs of a sequence.
@@ -48,14 +52,41 @@ struct PagedTilesParams {
         const uint32_t count = (uint32_t)sequence_count(a, a.q_start[b], a.q_start[b + 1]), per = kTwin ? tokens : 2 * tokens;
         return count * group > rows_from && count * group <= rows_upto ? (count + per - 1) / per : 0;
     }
+    // Which of `units` row tiles a CTA takes, and which piece of it.
+    struct Part {
+        uint32_t unit, piece, pieces, first_piece, counter;
+        bool thirds;  // two pieces, the first of two thirds
+    };
+    // A CTA fills an SM, so `units` of about the same work take whole waves of kSms and one
+    // that is not full, whose row tiles are cut: into equal pieces where there are two or more
+    // SMs to each, else, up to two thirds of a wave, into a piece of two thirds and one of the
+    // rest, two of which an SM without a large one takes in turn.  Pieces are joined through
+    // memory, which costs 10 us (a cluster's splits half of that, but few clusters run at
+    // once): worth it from 24 slot tiles on, 48 where it saves a third, in at most as many
+    // pieces as those have steps.  A chunk in 16k of BF16, 32 heads over 8 of 128, cut and not:
+    // 80 row tiles 149 us and 187, 160 237 and 291, 192 269 and 300, 232 338 and 356; 256, as
+    // pieces of three and one quarter, 371 and 362, so those are not.
+    __device__ __forceinline__ Part part_of(uint32_t units) const {
+        const uint32_t i = blockIdx.x, whole = partials ? units - units % kSms : units, rest = units - whole;
+        if (i < whole || !rest || rest > kSms * 2 / 3) return {i, 0, 1, 0, 0, false};
+        const uint32_t j = i - whole;
+        if (rest <= kSms / 2) {
+            const uint32_t n = min(kSms / rest, kMostPieces), r = j / n;
+            return {r < rest ? whole + r : units, j - r * n, n, r * n, r, false};
+        }
+        const uint32_t r = j < rest ? j : j - rest;
+        return {r < rest ? whole + r : units, j < rest ? 0u : 1u, 2, 2 * r, r, true};
+    }
     // This CTA's part of the work: one warp.  count stays 0 where there is none.  The last
     // sequence's last tiles, which see the most of its slots, go first.
     template <bool kTwin>
     __device__ __forceinline__ void place(TilesShared& sh, uint32_t lane) const {
-        const uint32_t unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
-        const uint32_t h = unit % a.pool.kv_heads, at = unit / a.pool.kv_heads;
         uint32_t total = 0;
         for (uint32_t b = 0; b < a.batch; b += 32) total += __reduce_add_sync(0xFFFFFFFFu, ctas_of<kTwin>(b + lane));
+        Part part;
+        if (kTwin || splits > 1) part = {blockIdx.x / splits, blockIdx.x % splits, splits, 0, 0, false};
+        else part = part_of(total * a.pool.kv_heads);
+        const uint32_t h = part.unit % a.pool.kv_heads, at = part.unit / a.pool.kv_heads;
         if (lane == 0) sh.count = 0;
         if (at >= total) return;
         uint32_t left = total - 1 - at, before = 0;  // row tiles, and sequences, before this one
@@ -81,7 +112,19 @@ struct PagedTilesParams {
                 sh.count = seq.count;
                 sh.rank = before + __popc(some & ((1u << lane) - 1u));
                 set_work<kTwin>(sh, Mask(seq.n, seq.count, a.window, a.sinks), (left - (upto - mine)) * (kTwin ? tokens : 2 * tokens),
-                                (uint32_t)seq.count, tokens, split, splits);
+                                (uint32_t)seq.count, tokens, [&](uint32_t n, uint32_t& j0, uint32_t& j1) {
+                    uint32_t pieces = part.pieces;
+                    if (!kTwin && splits == 1) {
+                        if (n < (part.thirds ? 2 : 1) * kLeastCut) pieces = 1;
+                        while (pieces * pieces > n && pieces > 1) pieces--;
+                        sh.piece = part.piece, sh.pieces = pieces, sh.first_piece = part.first_piece, sh.counter = part.counter;
+                        if (part.piece >= pieces) sh.count = 0;  // another one has it all
+                    }
+                    const auto upto = [&](uint32_t x) {
+                        return part.thirds && pieces > 1 ? x == 1 ? n - n / 3 : x * n / 2 : (uint32_t)((uint64_t)n * x / pieces);
+                    };
+                    j0 = upto(part.piece), j1 = upto(part.piece + 1);
+                });
             }
             return;
         }

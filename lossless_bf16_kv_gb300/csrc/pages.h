@@ -19,8 +19,8 @@ cudaError_t launch_pages_load(const splitzip_pages_load_args& a, cudaStream_t s)
 struct PagedPlan {
     uint32_t row_tiles;  // of a sequence (few rows), or at most of the batch (many)
     uint32_t splits;     // 0 (few rows): by the sequences' lengths
-    uint64_t ctas;       // of the launch (few rows)
-    size_t bytes;        // of workspace
+    uint64_t ctas;       // of the launch
+    size_t bytes;        // of workspace: from its start (few rows), or of partial results (many)
 };
 // Sequences of up to rows_upto query rows, and of more than rows_from, up to rows_upto.
 bool paged_rows_plan(const splitzip_paged_attention_args& a, uint32_t rows_upto, PagedPlan& p);
@@ -29,11 +29,16 @@ bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from
 // need not wait for to start.
 cudaError_t launch_paged_rows(const splitzip_paged_attention_args& a, uint32_t rows_upto, const PagedPlan& p, void* workspace,
                               bool after_tiles, const WaitTest& test, cudaStream_t s);
+// The bytes of the workspace's header that count the pieces of row tiles, behind those
+// that count the splits of few rows.
+constexpr size_t kTilesCounters = 640;
+// at_partials: where the plan's partial results lie in the workspace, apart from those of
+// the call's other launches, which may run at the same time.
 // beside: the launch ahead of it is another of the same call, whose end it need not wait
 // for.  widened: the sequences' caches in BF16, as launch_paged_widen leaves them (or
 // NULL: they are read from the pool).
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& p, void* workspace,
-                               const void* widened, bool beside, const WaitTest& test, cudaStream_t s);
+                               size_t at_partials, const void* widened, bool beside, const WaitTest& test, cudaStream_t s);
 
 // The caches of a batch's long sequences (more than rows_from query rows) in BF16, one
 // after the other in the batch's order: keys, then values, head by head, of

@@ -45,7 +45,8 @@ struct Plans {
     bool few, some, many;   // which of them may have sequences
     uint32_t upto, from;    // the most rows of the few-row kernel; more than that many: over caches widened first
     PagedPlan rows, tiles, wide;
-    size_t at_wide, bytes;  // of the workspace: where the widened caches lie, and in all
+    // Of the workspace: where partial results and the widened caches lie, and in all.
+    size_t at_tiles, at_wide, at_widened, bytes;
 };
 bool plan(const splitzip_paged_attention_args& a, Plans& p) {
     constexpr uint32_t kFewRows = 16;
@@ -73,15 +74,14 @@ bool plan(const splitzip_paged_attention_args& a, Plans& p) {
     p.many = a.pool.format != SPLITZIP_FORMAT_BF16 && most > many_rows && widened_bytes(a, p.from) <= kMostWidened;
     p.some = most > kFewRows && !(p.many && a.batch == 1);
     if (!p.many) p.from = 0xFFFFFFFFu;
-    p.bytes = kAttentionHeader;
-    const auto also = [&](const PagedPlan& x) { p.bytes = x.bytes > p.bytes ? x.bytes : p.bytes; };
     if (p.few && !paged_rows_plan(a, p.upto, p.rows)) return false;
-    if (p.few) also(p.rows);
     if (p.some && !paged_tiles_plan(a, p.upto, p.from, p.tiles)) return false;
-    if (p.some) also(p.tiles);
     if (p.many && !paged_tiles_plan(a, p.from, 0xFFFFFFFFu, p.wide)) return false;
-    p.at_wide = (p.bytes + 127) / 128 * 128;
-    if (p.many) p.bytes = p.at_wide + widened_bytes(a, p.from);
+    const auto after = [](size_t at, size_t bytes) { return (at + bytes + 127) / 128 * 128; };
+    p.at_tiles = after(p.few ? p.rows.bytes : kAttentionHeader, 0);
+    p.at_wide = after(p.at_tiles, p.some ? p.tiles.bytes : 0);
+    p.at_widened = after(p.at_wide, p.many ? p.wide.bytes : 0);
+    p.bytes = p.at_widened + (p.many ? widened_bytes(a, p.from) : 0);
     return true;
 }
 
@@ -97,11 +97,11 @@ splitzip_status attention(const splitzip_paged_attention_args* a, void* workspac
     const cudaStream_t stream = (cudaStream_t)s;
     cudaError_t e = cudaSuccess;
     if (p.many) {
-        void* wide = static_cast<uint8_t*>(workspace) + p.at_wide;
+        void* wide = static_cast<uint8_t*>(workspace) + p.at_widened;
         e = launch_paged_widen(*a, p.from, wide, stream);
-        if (e == cudaSuccess) e = launch_paged_tiles(*a, p.from, 0xFFFFFFFFu, p.wide, workspace, wide, false, test, stream);
+        if (e == cudaSuccess) e = launch_paged_tiles(*a, p.from, 0xFFFFFFFFu, p.wide, workspace, p.at_wide, wide, false, test, stream);
     }
-    if (e == cudaSuccess && p.some) e = launch_paged_tiles(*a, p.upto, p.from, p.tiles, workspace, nullptr, p.many, test, stream);
+    if (e == cudaSuccess && p.some) e = launch_paged_tiles(*a, p.upto, p.from, p.tiles, workspace, p.at_tiles, nullptr, p.many, test, stream);
     if (e == cudaSuccess && p.few) e = launch_paged_rows(*a, p.upto, p.rows, workspace, p.many || p.some, test, stream);
     return from_cuda(e);
 }

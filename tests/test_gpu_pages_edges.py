@@ -405,3 +405,36 @@ def test_attention_at_the_far_end_of_the_lengths(fmt):
 def test_keys_and_values_in_one_tensor(fmt):
     q, p, table, start, lens = batch_of([1, 30], [300, 411], 8, 2, 128, 16, fmt, seed=27)
     check(q, pg.Pages(p.k, p.k, p.k_exp, p.k_exp), table, start, lens)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("batch,tokens", [(10, 4000), (15, 6500)], ids=["pieces", "thirds"])
+def test_attention_cuts_the_last_wave(batch, tokens, dim, fmt):
+    """Row tiles for a wave of CTAs and some more, which are cut into pieces: full batches, ones that bring fewer row
+    tiles than planned, short caches, a window; several calls on one workspace, all alike."""
+    q, p, table, start, lens = batch_of([300] * batch, [tokens] * batch, 8, 8, dim, 64, fmt, seed=batch + dim)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 300)
+    scale = dim ** -0.5
+
+    def calls(start, lens, window=0, sinks=0):
+        out, lse = attend(q, p, table, start, lens, most=300, window=window, sinks=sinks, ws=ws)
+        compare(ref.attention(q, p, table, start, lens, table.shape[1] * 64, window, sinks, scale), out, lse)
+        for _ in range(3):
+            assert torch.equal(attend(q, p, table, start, lens, most=300, window=window, sinks=sinks, ws=ws)[0], out)
+
+    calls(start, lens)
+    few = start.clone()
+    few[2:] = few[2]                                                # two sequences with new tokens
+    calls(few, lens)
+    some = start.clone()
+    some[4:7] = some[4]                                             # two sequences without, one with too many
+    calls_lens = lens.clone()
+    calls_lens[0], calls_lens[1], calls_lens[9] = 0, 290, tokens // 2
+    out, lse = attend(q, p, table, some, calls_lens, most=300, ws=ws)
+    kept = some.clone()
+    found = [x for x in ref.attention(q, p, table, kept, calls_lens, table.shape[1] * 64, 0, 0, scale)
+             if x[0].stop - x[0].start <= 300]
+    compare(found, out, lse)
+    assert bool((out[4 * 300: 7 * 300] == 7.0).all())
+    calls(start, lens, window=3500, sinks=2)
