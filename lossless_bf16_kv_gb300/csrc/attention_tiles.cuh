@@ -278,7 +278,7 @@ __device__ __forceinline__ void load_tiles(const Params& p, TilesShared& sh, uin
 // slots of one page each: lane i of the warp looks up and loads box i, the page from one
 // step ahead.  What no query sees, or lies outside the pool, is loaded from behind its
 // last page: as zeros.  The keys have one warp and the values another, as a tile of pages
-// of 16 slots is 16 copies of each (a chunk of 4096 over 16k: 684 us, with one 837).
+// of 16 slots is 16 copies of each (a chunk of 4096 over 16k, not cut: 684 us, with one 837).
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw, bool values, uint32_t lane) {
     using S = TilesShape<D, kFmt, Params::kPaged>;

@@ -4,7 +4,8 @@
 //
 // A CTA's row tiles belong to one sequence.  How many a batch has is on the device,
 // so the grid is as large as it can be, each CTA counts the sequences' row tiles up
-// to its own, and those past the last one leave.
+// to its own, and those past the last one leave.  Row tiles that do not fill a last wave
+// of CTAs are cut into pieces.
 //
 // A tile of 128 slots is loaded page by page, one TMA box of up to 128 rows each, by as
 // many lanes of a loading warp, one for the keys and one for the values; where tiles of
@@ -14,7 +15,7 @@
 // copy a page where they are contiguous, else 4 bytes a lane.
 //
 // BF16 caches run as strided ones do (a chunk of 4096 after 12k tokens, 32 heads over 8 of
-// 128: 683 us, 1.4 PFLOP/s, with pages of 16 and of 128 slots alike).  The widening warps
+// 128: 632 us, 1.5 PFLOP/s, with pages of 16 and of 128 slots alike).  The widening warps
 // bound the others: a chunk of 2048 in 8k tokens of 8 bits takes 215 us, where one over a
 // BF16 cache takes 177, and 186 with the cache widened to BF16 ahead of the products.
 #pragma once

@@ -28,7 +28,8 @@ def lib():
 CASES = {  # new tokens, lengths, q_heads, kv_heads: few rows in a cluster of splits, in several clusters, both tiles
     # of a CTA the same rows, two tiles, so many rows that caches are widened first
     "few": ([1, 1], [1500, 1400], 8, 2), "long": ([1], [30000], 4, 1), "tile": ([40, 30], [1200, 1300], 4, 2),
-    "tiles": ([120], [900], 8, 2), "many": ([400], [1000], 4, 2)}
+    "tiles": ([120], [900], 8, 2), "many": ([400], [1000], 4, 2),
+    "wide": ([1100], [1300], 4, 2)}
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -80,3 +81,41 @@ def test_the_test_call_refuses(lib):
     long_wait = serving.WaitTestOpts(2001, 0, 0)
     for o in (None, ctypes.byref(long_wait)):
         assert lib.splitzip_paged_attention_test(ctypes.byref(a), ws.data_ptr(), ws.numel(), None, o) == sz.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_piece_of_a_row_tile_gives_up(lib, dim, fmt):
+    """160 row tiles, the eight behind a wave of 152 cut into pieces: one that gives up makes its rows NaN, whichever
+    piece joins them, and leaves the workspace fit for the next call."""
+    q, p, table, start, lens = batch_of([300] * 10, [4000] * 10, 8, 8, dim, 64, fmt, seed=dim)
+    good, good_lse = attend(q, p, table, start, lens)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 300)
+    out, lse = torch.zeros_like(q), torch.zeros((8, q.shape[0]), device=DEV)
+    pool = pg.Pool.from_buffer_copy(p.packed)
+    a = pg.PagedAttentionArgs((q.data_ptr(), 0, *q.stride()[:2]), (out.data_ptr(), 0, *out.stride()[:2]), pool, lse.data_ptr(),
+                              table.data_ptr(), start.data_ptr(), lens.data_ptr(), 10, q.shape[0], 300,
+                              table.shape[1] * 64, table.shape[1], 8, 0, 0, dim ** -0.5)
+
+    def call(cta, tile):
+        torch.cuda.synchronize()
+        o = serving.WaitTestOpts(LIMIT_MS, cta, tile)
+        assert lib.splitzip_paged_attention_test(ctypes.byref(a), ws.data_ptr(), ws.numel(), None, ctypes.byref(o)) == sz.OK
+        return serving.splitzip_attention_status(ws)
+
+    some = 0
+    for cta in (152, 156, 171):
+        out.zero_()
+        lse.zero_()
+        status = call(cta, 1)
+        lost = torch.isnan(lse)
+        assert status == (sz.ERR_TIMEOUT if bool(lost.any()) else sz.OK)
+        some += bool(lost.any())
+        assert torch.equal(torch.isnan(out), lost.T[..., None].expand_as(out))
+        assert len(lost.any(1).nonzero()) <= 1, "rows of one head"
+        assert int(lost.sum()) <= 256, "rows of one row tile"
+        assert torch.equal(lse[~lost], good_lse[~lost])
+        assert torch.equal(out[~lost.T], good[~lost.T])
+    assert some == 3, "no copy was left out"
+    assert call(NONE, NONE) == sz.OK
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
