@@ -17,8 +17,9 @@
 //
 // 16 sequences of 16k tokens, 8 heads of 128, read back: BF16 309 us (6.9 TB/s read and
 // written), E5M2 235, 8 bits 240, 4 bits 202, all within 2% of a copy's rate.  One layer
-// of a 16k prompt stored and read back: 35, 29, 34 and 32 us; the store's part in 8 bits
-// (23 us) is half instructions, its arithmetic unit 60% busy.
+// of a 16k prompt stored and read back: 35, 29, 33 and 31 us, where the store of quantised
+// rows is bound by its instructions as much (in 8 bits 1.4 us of it were addresses in 64
+// bits of what fits 32).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -102,6 +103,9 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
     const splitzip_page_rows& out = part.v ? a.pool.v : a.pool.k;
     const uint64_t slots = (uint64_t)a.pool.pages << p.page_shift;
     const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * (part.h * in.stride_h) + 16 * lane;
+    constexpr uint32_t kElem = kFmt == kBf16 ? 2 : 1, kPiece = kRowBytes<D, kFmt> / kLanes;
+    uint8_t* to = static_cast<uint8_t*>(out.data) + kElem * (part.h * out.stride_h) + kPiece * lane;
+    uint8_t* to_exp = kQuantised<kFmt> ? out.exponents + part.h * out.exp_stride_h : nullptr;
     uint4 x[kRows];
     int64_t slot[kRows];
 #pragma unroll
@@ -117,12 +121,11 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
 #pragma unroll
     for (int r = 0; r < kRows; r++) {
         const bool there = slot[r] >= 0 && (uint64_t)slot[r] < slots;
-        const int64_t page = slot[r] >> p.page_shift, at = slot[r] & (a.pool.page_tokens - 1);
-        const int64_t row = page * out.stride_p + at * out.stride_t + part.h * out.stride_h;
-        uint8_t* to = static_cast<uint8_t*>(out.data);
+        const uint32_t page = (uint32_t)(slot[r] >> p.page_shift), at = (uint32_t)slot[r] & (a.pool.page_tokens - 1);
+        uint8_t* row = to + kElem * ((int64_t)page * out.stride_p + (int64_t)at * out.stride_t);
         const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
         if constexpr (kFmt == kBf16) {
-            if (there) *reinterpret_cast<uint4*>(to + 2 * row + 16 * lane) = x[r];
+            if (there) *reinterpret_cast<uint4*>(row) = x[r];
         } else {
             float f[8];
 #pragma unroll
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
                 f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             }
             if constexpr (kFmt == kE5m2) {
-                if (there) *reinterpret_cast<uint2*>(to + row + 8 * lane) = make_uint2(pack4_e5m2(f), pack4_e5m2(f + 4));
+                if (there) *reinterpret_cast<uint2*>(row) = make_uint2(pack4_e5m2(f), pack4_e5m2(f + 4));
             } else {
                 uint32_t e;
                 const uint32_t top = block_max<kLanes / 4>(__vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
@@ -149,11 +152,10 @@ __global__ void __launch_bounds__(kThreadsPages) store_kernel(const __grid_const
 #pragma unroll
                 for (uint32_t i = kLanes / 4; i < kLanes; i *= 2) e |= __shfl_xor_sync(0xFFFFFFFFu, e, i);
                 if (there) {
-                    if constexpr (kFmt == kInt8) *reinterpret_cast<uint2*>(to + row + 8 * lane) = odd ? make_uint2(0, 0) : make_uint2(to_int8x4(f, inv), to_int8x4(f + 4, inv));
-                    else *reinterpret_cast<uint32_t*>(to + row + 4 * lane) = odd ? 0u : to_e2m1x8(f, inv);
+                    if constexpr (kFmt == kInt8) *reinterpret_cast<uint2*>(row) = odd ? make_uint2(0, 0) : make_uint2(to_int8x4(f, inv), to_int8x4(f + 4, inv));
+                    else *reinterpret_cast<uint32_t*>(row) = odd ? 0u : to_e2m1x8(f, inv);
                     if (lane == 0)
-                        *reinterpret_cast<uint32_t*>(out.exponents + page * out.exp_stride_p + at * out.exp_stride_t +
-                                                     part.h * out.exp_stride_h) = e;
+                        *reinterpret_cast<uint32_t*>(to_exp + (int64_t)page * out.exp_stride_p + (int64_t)at * out.exp_stride_t) = e;
                 }
             }
         }
