@@ -121,7 +121,8 @@ splitzip_status splitzip_pages_load(const splitzip_pages_load_args *args, splitz
  *            a query sees a token whose page is outside the pool, its out and lse,
  *            and those of queries near it, are NaN
  *   q_start  int32[batch + 1]; a sequence whose range does not lie in [0, tokens]
- *            or holds more than max_q_tokens is left out
+ *            or holds more than max_q_tokens is left out; where starts that go back
+ *            make ranges overlap, out and lse are unspecified
  *   lens     int32[batch], with the new tokens counted
  * Scores, the softmax statistics and sums are held in 32 bits; a query that sees
  * nothing, or scores of -infinity alone, gets out = 0 and lse = -inf.  Tokens

@@ -51,8 +51,9 @@ bool paged_tiles_plan(const splitzip_paged_attention_args& a, uint32_t rows_from
     p.bytes = 0;
     if (cut) {
         p.ctas += kSms;
-        const uint64_t pieces = std::min<uint64_t>(p.row_tiles * (uint64_t)a.pool.kv_heads * PagedTilesParams::kMostPieces, 2 * kSms);
-        p.bytes = pieces * (a.pool.head_dim == 64 ? kPieceFloat4s<64> : kPieceFloat4s<128>) * sizeof(float4);
+        // Whatever the ranges on the device are: thirds make the most pieces.
+        p.bytes = 2 * (kSms * 2 / 3) * sizeof(float4) * (a.pool.head_dim == 64 ? kPieceFloat4s<64> : kPieceFloat4s<128>);
+        static_assert(2 * (kSms * 2 / 3) >= kSms, "equal pieces are kSms at most");
     }
     return p.ctas <= 0x7FFFFFFFull;
 }

@@ -68,7 +68,10 @@ struct PagedTilesParams {
     // 80 row tiles 149 us and 187, 160 237 and 291, 192 269 and 300, 232 338 and 356; 256, as
     // pieces of three and one quarter, 371 and 362, so those are not.
     __device__ __forceinline__ Part part_of(uint32_t units) const {
-        const uint32_t i = blockIdx.x, whole = partials ? units - units % kSms : units, rest = units - whole;
+        // Where ranges that overlap make more of them than the grid is for, none is cut: a piece
+        // that no CTA takes would leave its counter behind.
+        const bool cut = partials && units + kSms <= gridDim.x;
+        const uint32_t i = blockIdx.x, whole = cut ? units - units % kSms : units, rest = units - whole;
         if (i < whole || !rest || rest > kSms * 2 / 3) return {i, 0, 1, 0, 0, false};
         const uint32_t j = i - whole;
         if (rest <= kSms / 2) {

@@ -438,3 +438,28 @@ def test_attention_cuts_the_last_wave(batch, tokens, dim, fmt):
     compare(found, out, lse)
     assert bool((out[4 * 300: 7 * 300] == 7.0).all())
     calls(start, lens, window=3500, sinks=2)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("batch,count,heads", [(9, 1024, 1), (17, 700, 2), (5, 300, 8), (40, 20, 2), (40, 3, 8)])
+def test_ranges_that_overlap_stay_inside_the_buffers(batch, count, heads, fmt):
+    """Starts that go back and forth bring more rows than q has, under a bound that has long caches cut."""
+    q, p, table, _, lens = batch_of([count] + [0] * (batch - 1), [4000] * batch, heads, heads, 64, 16, fmt, seed=batch)
+    start = ints([0, count] * (batch // 2 + 1))[: batch + 1]
+    wide = torch.full((batch, 1 << 14), -1, dtype=torch.int32, device=DEV)       # 262144 tokens
+    wide[:, : table.shape[1]] = table
+    size = pg.splitzip_paged_attention_workspace_bytes(q, p, wide, count)
+    assert size
+    room = torch.zeros(size + (64 << 20), dtype=torch.uint8, device=DEV)
+    room[size:] = 0x5A
+    lse = torch.zeros((heads + 1, count), device=DEV)
+    out = torch.zeros((count + 1, heads, 64), dtype=torch.bfloat16, device=DEV)
+    for _ in range(2):
+        pg.splitzip_paged_attention(q, p, wide, start, lens, out[:count], room[:size], count, lse=lse[:heads])
+        assert serving.splitzip_attention_status(room[:size]) == sz.OK
+    assert bool((room[size:] == 0x5A).all()) and not out[count].any() and not lse[heads].any()
+    # The same workspace, ranges in order again.
+    start[2:] = count
+    check_out, check_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    pg.splitzip_paged_attention(q, p, wide, start, lens, check_out[:count], room[:size], count, lse=check_lse[:heads])
+    compare(ref.attention(q, p, table, start, lens, table.shape[1] * 16, 0, 0, 0.125), check_out, check_lse[:heads])
