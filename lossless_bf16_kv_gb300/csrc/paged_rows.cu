@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB))
 #pragma unroll
                             for (int x = 0; x < 2; x++) {
                                 const uint32_t v = r[2 * u + x];
-                                uint32_t f = 0;
+                                [[maybe_unused]] uint32_t f = 0;
                                 if constexpr (kQuantised<kFmt>) {
                                     const uint32_t block = kFmt == kInt8 ? (c + u) * 16 / (D / 4) : D == 128 ? c + u : 2 * (c + u) + (lane >> 4);
                                     f = *reinterpret_cast<const uint32_t*>(powers + 2 * (block * S::kPart + 16 * i + 8 * x + 2 * (lane & 3)));
