@@ -91,20 +91,20 @@ template <int D, int kFmt, bool kPaged>
 struct TilesShape {
     static constexpr int kKV = kBN * D * 2;      // bytes of a key or value tile in 16 bits
     // Where it is widened, a tile comes as it lies in the cache, in one part or two, of kRaw bytes and kExps of exponents.
-    static constexpr int kParts = kPaged && kWide<kFmt> && D == 128 ? 2 : 1, kPartSlots = kBN / kParts;
+    static constexpr int kParts = kPaged && kWidens<kFmt> && D == 128 ? 2 : 1, kPartSlots = kBN / kParts;
     static constexpr int kRaw = kPartSlots * kRowBytes<D, kFmt>;
     static constexpr int kQ = kTileM * D * 2;    // bytes of a query tile
-    static constexpr int kStages = D == 128 ? (kWide<kFmt> || kPaged ? 4 : 5) : (kWide<kFmt> ? 6 : 8);
-    static constexpr int kRaws = !kWide<kFmt> ? 0 : kPaged ? 4 : 2;
+    static constexpr int kStages = D == 128 ? (kWidens<kFmt> || kPaged ? 4 : 5) : (kWidens<kFmt> ? 6 : 8);
+    static constexpr int kRaws = !kWidens<kFmt> ? 0 : kPaged ? 4 : 2;
     static constexpr int kExps = kQuantised<kFmt> ? kPartSlots * 4 : 0;
     // Threads: softmax, a warp for the products, one for the loads, and those that
     // tend the values; registers of a softmax thread and of another.
-    static constexpr bool kManyTend = kWide<kFmt> && kPaged;
-    static constexpr int kTend = kManyTend ? 10 : kWide<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
-    static constexpr int kRegs = kWide<kFmt> ? 96 : 104, kOtherRegs = kManyTend ? 40 : kWide<kFmt> ? 48 : 64;
+    static constexpr bool kManyTend = kWidens<kFmt> && kPaged;
+    static constexpr int kTend = kManyTend ? 10 : kWidens<kFmt> ? 6 : 2, kThreads = kSoftmax + 32 * (2 + kTend);
+    static constexpr int kRegs = kWidens<kFmt> ? 96 : 104, kOtherRegs = kManyTend ? 40 : kWidens<kFmt> ? 48 : 64;
     // Warps that widen a tile, and those that say that its values are fit.
     static constexpr int kTenders = kManyTend ? 8 : kPaged ? 1 : kTend;  // the next one loads the values' pages
-    static constexpr int kWiden = kTenders > 1 ? kTenders / 2 : 1, kFit = kWide<kFmt> ? kWiden : kTenders;
+    static constexpr int kWiden = kTenders > 1 ? kTenders / 2 : 1, kFit = kWidens<kFmt> ? kWiden : kTenders;
     static_assert(kThreads % 128 == 0 && kSoftmax * kRegs + (kThreads - kSoftmax) * kOtherRegs <= kThreads * (65536 / kThreads / 8 * 8),
                   "register shares add up to what the CTA is launched with");
     static constexpr int kRowFloats = D + 4;     // of a row's partial result: o, m, l
@@ -282,7 +282,7 @@ __device__ __forceinline__ void load_tiles(const Params& p, TilesShared& sh, uin
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh, uint8_t* qs, uint8_t* ring, uint8_t* raw, bool values, uint32_t lane) {
     using S = TilesShape<D, kFmt, Params::kPaged>;
-    constexpr int kRow = kWide<kFmt> ? kRowBytes<D, kFmt> : 128;  // bytes of a row of a box
+    constexpr int kRow = kWidens<kFmt> ? kRowBytes<D, kFmt> : 128;  // bytes of a row of a box
     volatile WaitLimit* wait = &sh.wait;
     const uint32_t steps = sh.steps;
     if (!kWide<kFmt> && !values && lane == 0) load_queries<D, kFmt, kTwin>(p, sh, qs, (uint32_t)sh.first_row + sh.t0, 0);
@@ -294,9 +294,9 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
         if (page >= p.a.pool.pages) *const_cast<volatile uint32_t*>(&sh.lost) = 1;
         return min(page, p.a.pool.pages);
     };
-    constexpr uint32_t kN = kWide<kFmt> ? S::kRaws : S::kStages, kParts = S::kParts;
-    uint64_t* full = kWide<kFmt> ? sh.raw_full : sh.full;
-    uint64_t* empty = kWide<kFmt> ? sh.raw_empty : sh.empty;
+    constexpr uint32_t kN = kWidens<kFmt> ? S::kRaws : S::kStages, kParts = S::kParts;
+    uint64_t* full = kWidens<kFmt> ? sh.raw_full : sh.full;
+    uint64_t* empty = kWidens<kFmt> ? sh.raw_empty : sh.empty;
     uint8_t* exps = raw + S::kRaws * S::kRaw;  // of each raw stage, by slot
     const bool bulk = kQuantised<kFmt> && p.bulk_exps;
     const CUtensorMap* map = values ? &p.vmap : &p.kmap;
@@ -315,12 +315,12 @@ __device__ __forceinline__ void load_page_tiles(const Params& p, TilesShared& sh
         const uint32_t step = i / kParts, part = i % kParts;
         if (m >= kN && !mbar_wait_bounded(&empty[st], ph ^ 1, wait)) break;
         const uint32_t s0 = (uint32_t)step_slot(sh, (int32_t)step) + part * S::kPartSlots;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kWide<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kWidens<kFmt> ? S::kRaw + (bulk ? S::kExps : 0) : S::kKV);
         __syncwarp();
         const uint32_t mine = lane - part * part_boxes;  // this lane's box of the part
         if (mine < part_boxes && !(blockIdx.x == p.test_cta && m == p.test_tile)) {
             const int32_t at = (int32_t)((s0 + mine * p.box) & slots_mask);
-            if (kWide<kFmt>) {
+            if (kWidens<kFmt>) {
                 tma_load4(raw + st * S::kRaw + mine * p.box * kRow, map, 0, at, (int32_t)sh.h, (int32_t)now, &full[st]);
             } else {
 #pragma unroll
@@ -513,7 +513,7 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
     const uint32_t lane = thread & 31, steps = sh.steps;
     StepSlots slots(sh);
     const WholeTiles whole(sh, sh.p0, sh.p1);
-    if constexpr (kWide<kFmt> && Params::kPaged) {
+    if constexpr (kWidens<kFmt> && Params::kPaged) {
         // Half of the warps widen the keys, half the values, 16 bytes of the cache a lane:
         // the lanes of a quarter warp take rows of their own, which the swizzles of both
         // tiles spread over the banks, so a lane's places in them stay.
@@ -619,7 +619,7 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
                 if (mine) mbar_arrive(&sh.ok[(n >> 1) & 7]);
             }
         }
-    } else if constexpr (kWide<kFmt>) {
+    } else if constexpr (kWidens<kFmt>) {
         // Half of the warps widen the keys, half the values.
         const uint32_t mine = thread >= 16 * S::kTend, in_half = thread - mine * 16 * S::kTend;
         for (uint32_t n = mine; n < 2 * steps; n += 2, slots.next()) {
@@ -670,8 +670,8 @@ __device__ __forceinline__ void tend_values(const Params& p, TilesShared& sh, ui
 #pragma unroll 4
                 for (uint32_t x = thread; x < S::kKV / 16; x += 32 * S::kTenders) {
                     const uint4 v = tile[x];
-                    const uint4 f = make_uint4(finite_or_zero<false>(v.x), finite_or_zero<false>(v.y), finite_or_zero<false>(v.z),
-                                               finite_or_zero<false>(v.w));
+                    const uint4 f = make_uint4(finite_or_zero<kWide<kFmt>>(v.x), finite_or_zero<kWide<kFmt>>(v.y), finite_or_zero<kWide<kFmt>>(v.z),
+                                               finite_or_zero<kWide<kFmt>>(v.w));
                     if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
                         tile[x] = f;
                         found = true;
@@ -834,7 +834,7 @@ __device__ __forceinline__ bool softmax_rows(const Params& p, TilesShared& sh, u
 template <int D, int kFmt, bool kTwin, class Params>
 __device__ __forceinline__ void read_output(const Params& p, const TilesShared& sh, uint32_t oa, uint32_t t, int32_t pos, int c,
                                             float (&o)[32]) {
-    constexpr int kElem = kWide<kFmt> ? 1 : 2;
+    constexpr int kElem = kWidens<kFmt> ? 1 : 2;
     const uint32_t steps = sh.steps;
     const bool any = kTwin ? steps > t : steps != 0;
     uint32_t w[32];
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(TilesShape<D, kFmt, Params::kPaged>::kThreads,
     if (threadIdx.x == 0) {
         if constexpr (!Params::kPaged) p.template place<kTwin>(sh);
         for (int i = 0; i < 8; i++) {
-            mbar_init(&sh.full[i], kWide<kFmt> ? S::kWiden : 1);
+            mbar_init(&sh.full[i], kWidens<kFmt> ? S::kWiden : 1);
             mbar_init(&sh.empty[i], 1);
             mbar_init(&sh.ok[i], S::kFit);
         }

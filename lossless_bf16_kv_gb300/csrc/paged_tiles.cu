@@ -75,7 +75,7 @@ cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t 
     splitzip_pool& pool = p.a.pool;
     if (widened) {
         const int64_t t = (int64_t)widened_tokens(a), d = pool.head_dim;
-        pool.format = kBf16;
+        pool.format = kF16;
         pool.pages = (uint32_t)widened_sequences(a, rows_from);
         pool.page_tokens = (uint32_t)t;
         pool.k = {const_cast<void*>(widened), 2 * t * d * pool.kv_heads, d, t * d, nullptr, 0, 0, 0};

@@ -17,7 +17,7 @@
 // BF16 caches run as strided ones do (a chunk of 4096 after 12k tokens, 32 heads over 8 of
 // 128: 632 us, 1.5 PFLOP/s, with pages of 16 and of 128 slots alike).  The widening warps
 // bound the others: a chunk of 2048 in 8k tokens of 8 bits takes 215 us, where one over a
-// BF16 cache takes 177, and 186 with the cache widened to BF16 ahead of the products.
+// BF16 cache takes 177, and 188 with the cache widened to FP16 ahead of the products.
 #pragma once
 
 #include "attention_tiles.cuh"
@@ -45,7 +45,7 @@ struct PagedTilesParams {
     // The most pieces of a row tile, and the least slot tiles of one that is cut.
     static constexpr uint32_t kMostPieces = 16, kLeastCut = 24;
     // On a raw tile's barrier: its copies', and the lanes' whose own copies bring the exponents.
-    __device__ __forceinline__ uint32_t raw_arrivals() const { return a.pool.format >= SPLITZIP_FORMAT_INT8 && !bulk_exps ? 33 : 1; }
+    __device__ __forceinline__ uint32_t raw_arrivals() const { return (a.pool.format == kInt8 || a.pool.format == kE2m1) && !bulk_exps ? 33 : 1; }
     // Row-tile CTAs of a sequence.
     template <bool kTwin>
     __device__ __forceinline__ uint32_t ctas_of(uint32_t b) const {
@@ -171,7 +171,7 @@ struct PagedTilesParams {
 // Slots of a part that a tile is loaded in.
 template <int D>
 uint32_t tile_part_of(uint32_t format) {
-    return format == kBf16   ? TilesShape<D, kBf16, true>::kPartSlots
+    return format == kBf16 || format == kF16 ? TilesShape<D, kBf16, true>::kPartSlots
            : format == kE5m2 ? TilesShape<D, kE5m2, true>::kPartSlots
            : format == kInt8 ? TilesShape<D, kInt8, true>::kPartSlots
                              : TilesShape<D, kE2m1, true>::kPartSlots;
@@ -184,6 +184,9 @@ cudaError_t launch_paged_format(const PagedTilesParams& p, uint32_t ctas, bool b
         case kBf16: return launch_tiles<D, kBf16, kTwin>(p, ctas, s, beside);
         case kE5m2: return launch_tiles<D, kE5m2, kTwin>(p, ctas, s, beside);
         case kInt8: return launch_tiles<D, kInt8, kTwin>(p, ctas, s, beside);
+        case kF16:  // of many rows, never twins
+            if constexpr (kTwin) return cudaErrorInvalidValue;
+            else return launch_tiles<D, kF16, kTwin>(p, ctas, s, beside);
         default: return launch_tiles<D, kE2m1, kTwin>(p, ctas, s, beside);
     }
 }

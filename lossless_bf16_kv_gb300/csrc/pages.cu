@@ -203,9 +203,25 @@ __device__ __forceinline__ uint4 to_bf16(uint4 x, uint32_t bytes, uint32_t lane)
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// The same in FP16, which holds every value that the store leaves (infinities and NaN too).
+template <int D, int kFmt>
+__device__ __forceinline__ uint4 to_f16(uint4 x, uint32_t bytes, uint32_t lane) {
+    if constexpr (kFmt == kE5m2) return make_uint4(e5m2_01(x.x), e5m2_23(x.x), e5m2_01(x.y), e5m2_23(x.y));
+    const float f = block_scale(bytes >> 8 * (lane / (D / 32)) & 255u);
+    const uint32_t s = pack2<true>(f, f);
+    uint32_t h[4];
+    if constexpr (kFmt == kInt8) {
+        const uint32_t lo = int8_bias(x.x), hi = int8_bias(x.y);
+        h[0] = int8_pair<kInt8_01>(lo), h[1] = int8_pair<kInt8_23>(lo), h[2] = int8_pair<kInt8_01>(hi), h[3] = int8_pair<kInt8_23>(hi);
+    } else {
+        e2m1_pairs(h, x.x);
+    }
+    return make_uint4(mul_half2(h[0], s), mul_half2(h[1], s), mul_half2(h[2], s), mul_half2(h[3], s));
+}
+
 // A group's kRows tokens from t on (all of one page), of one head of keys or values, up
-// to token n: put(row, x) takes eight values in BF16, or (kCopy) E5M2 rows as they are.
-template <int D, int kFmt, bool kCopy, class Put>
+// to token n: put(row, x) takes eight values in kOut: BF16, FP16, or E5M2 rows as they are.
+template <int D, int kFmt, int kOut, class Put>
 __device__ __forceinline__ void load_rows(const splitzip_pool& pool, const splitzip_page_rows& in, uint32_t page, uint32_t h, uint32_t t, uint32_t n,
                                           bool bulk_exps, uint32_t lane, const Put& put) {
     const bool bad = page >= pool.pages;
@@ -241,7 +257,8 @@ __device__ __forceinline__ void load_rows(const splitzip_pool& pool, const split
 #pragma unroll
     for (int r = 0; r < kRows; r++) {
         if (t + r >= n) break;
-        if constexpr (kCopy) put(t + r, bad ? make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0, 0) : x[r]);
+        if constexpr (kOut == kE5m2) put(t + r, bad ? make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0, 0) : x[r]);
+        else if constexpr (kOut == kF16) put(t + r, bad ? make_uint4(0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u) : to_f16<D, kFmt>(x[r], e[r], lane));
         else put(t + r, bad ? make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u) : to_bf16<D, kFmt>(x[r], e[r], lane));
     }
 }
@@ -251,8 +268,7 @@ struct LoadParams {
     uint32_t token_ctas, page_shift, bulk_exps;
 };
 
-// kCopy: E5M2 rows as they are.
-template <int D, int kFmt, bool kCopy>
+template <int D, int kFmt, int kOut>
 __global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_constant__ LoadParams p) {
     constexpr uint32_t kLanes = D / 8;
     const splitzip_pages_load_args& a = p.a;
@@ -262,19 +278,20 @@ __global__ void __launch_bounds__(kThreadsPages) load_kernel(const __grid_consta
     const uint32_t lane = threadIdx.x % kLanes, t = part.first + threadIdx.x / kLanes * kRows;
     if (t >= n) return;
     const splitzip_view& out = part.v ? a.v_out : a.k_out;
-    constexpr int kElem = kCopy ? 1 : 2;
+    constexpr int kElem = kOut == kE5m2 ? 1 : 2;
     uint8_t* to = static_cast<uint8_t*>(out.data) + kElem * (part.b * out.stride_b + part.h * out.stride_h + 8 * lane);
     const uint32_t page = (uint32_t)a.table[(uint64_t)part.b * a.table_width + (t >> p.page_shift)];
-    load_rows<D, kFmt, kCopy>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane, [&](uint32_t row, uint4 x) {
+    load_rows<D, kFmt, kOut>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane, [&](uint32_t row, uint4 x) {
         uint8_t* at = to + kElem * ((int64_t)row * out.stride_t);
-        if constexpr (kCopy) st_stream8(at, make_uint2(x.x, x.y));
+        if constexpr (kOut == kE5m2) st_stream8(at, make_uint2(x.x, x.y));
         else st_stream16(at, x);
     });
 }
 
-// The caches of long sequences, widened for launch_paged_tiles: the load's work, to
+// The caches of long sequences, widened to FP16 for launch_paged_tiles: the load's work, to
 // contiguous rows, which the products then find in L2 where they fit (8k tokens of 8 heads
-// of 128 in 8 bits: 11 us).
+// of 128 in 8 bits: 11 us).  FP16 and not BF16, as the softmax weights take their values'
+// type: 11 bits of each, as where tiles are widened one by one, and not 8.
 struct WidenParams {
     splitzip_paged_attention_args a;
     uint32_t token_ctas, page_shift, bulk_exps;
@@ -307,7 +324,7 @@ __global__ void __launch_bounds__(kThreadsPages) widen_kernel(const __grid_const
     if ((int64_t)t + kRows <= (int64_t)mask.first - (int64_t)mask.window + 1 && (int32_t)t >= mask.sinks) return;
     uint8_t* to = p.to + 2 * ((((uint64_t)part.b * 2 + part.v) * a.pool.kv_heads + part.h) * p.tokens * D + 8 * lane);
     const uint32_t page = (uint32_t)a.table[(uint64_t)found * a.table_width + (t >> p.page_shift)];
-    load_rows<D, kFmt, false>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane,
+    load_rows<D, kFmt, kF16>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane,
                               [&](uint32_t row, uint4 x) { *reinterpret_cast<uint4*>(to + 2 * (uint64_t)row * D) = x; });
 }
 
@@ -337,13 +354,13 @@ cudaError_t load(const splitzip_pages_load_args& a, cudaStream_t s) {
     const LoadParams p{a, token_ctas, log2_of(a.pool.page_tokens), bulk_exponents(a.pool)};
     const uint32_t ctas = token_ctas * a.pool.kv_heads * 2 * a.batch;
     switch (a.pool.format) {
-        case kBf16: load_kernel<D, kBf16, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kBf16: load_kernel<D, kBf16, kBf16><<<ctas, kThreadsPages, 0, s>>>(p); break;
         case kE5m2:
-            if (a.out_format == kE5m2) load_kernel<D, kE5m2, true><<<ctas, kThreadsPages, 0, s>>>(p);
-            else load_kernel<D, kE5m2, false><<<ctas, kThreadsPages, 0, s>>>(p);
+            if (a.out_format == kE5m2) load_kernel<D, kE5m2, kE5m2><<<ctas, kThreadsPages, 0, s>>>(p);
+            else load_kernel<D, kE5m2, kBf16><<<ctas, kThreadsPages, 0, s>>>(p);
             break;
-        case kInt8: load_kernel<D, kInt8, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
-        default: load_kernel<D, kE2m1, false><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        case kInt8: load_kernel<D, kInt8, kBf16><<<ctas, kThreadsPages, 0, s>>>(p); break;
+        default: load_kernel<D, kE2m1, kBf16><<<ctas, kThreadsPages, 0, s>>>(p); break;
     }
     return cudaGetLastError();
 }

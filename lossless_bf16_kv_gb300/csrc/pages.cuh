@@ -9,15 +9,20 @@
 
 namespace splitzip {
 
-enum Format : int { kBf16 = SPLITZIP_FORMAT_BF16, kE5m2 = SPLITZIP_FORMAT_E5M2, kInt8 = SPLITZIP_FORMAT_INT8, kE2m1 = SPLITZIP_FORMAT_E2M1 };
+enum Format : int {
+    kBf16 = SPLITZIP_FORMAT_BF16, kE5m2 = SPLITZIP_FORMAT_E5M2, kInt8 = SPLITZIP_FORMAT_INT8, kE2m1 = SPLITZIP_FORMAT_E2M1,
+    kF16  // no pool's: caches widened ahead of the products
+};
 
 template <int kFmt>
-constexpr bool kWide = kFmt != kBf16;  // operands are FP16, widened from the cache's bytes
+constexpr bool kWide = kFmt != kBf16;  // operands are FP16 ..
+template <int kFmt>
+constexpr bool kWidens = kWide<kFmt> && kFmt != kF16;  // .. and widened from the cache's bytes by the attention kernel
 template <int kFmt>
 constexpr bool kQuantised = kFmt == kInt8 || kFmt == kE2m1;
 // Bytes of a row's codes.
 template <int D, int kFmt>
-constexpr int kRowBytes = kFmt == kBf16 ? 2 * D : kFmt == kE2m1 ? D / 2 : D;
+constexpr int kRowBytes = !kWidens<kFmt> ? 2 * D : kFmt == kE2m1 ? D / 2 : D;
 
 // New tokens of a sequence whose rows are from .. to - 1; 0 where that is no range to be taken.
 __device__ __forceinline__ int32_t sequence_count(const splitzip_paged_attention_args& a, int32_t from, int32_t to) {
@@ -95,6 +100,7 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 template <int D, int kFmt>
 __device__ __forceinline__ float page_value(const uint8_t* row, const uint8_t* exps, uint32_t d) {
     if (kFmt == kBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
+    if (kFmt == kF16) return __half2float(reinterpret_cast<const __half*>(row)[d]);
     if (kFmt == kE5m2) return __half2float(__ushort_as_half((unsigned short)(row[d] << 8)));
     uint32_t w[4];
     if (kFmt == kInt8) w[0] = int8_pair<kInt8_01>(int8_bias(row[d]));

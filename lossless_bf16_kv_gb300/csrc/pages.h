@@ -35,12 +35,12 @@ constexpr size_t kTilesCounters = 640;
 // at_partials: where the plan's partial results lie in the workspace, apart from those of
 // the call's other launches, which may run at the same time.
 // beside: the launch ahead of it is another of the same call, whose end it need not wait
-// for.  widened: the sequences' caches in BF16, as launch_paged_widen leaves them (or
+// for.  widened: the sequences' caches in FP16, as launch_paged_widen leaves them (or
 // NULL: they are read from the pool).
 cudaError_t launch_paged_tiles(const splitzip_paged_attention_args& a, uint32_t rows_from, uint32_t rows_upto, const PagedPlan& p, void* workspace,
                                size_t at_partials, const void* widened, bool beside, const WaitTest& test, cudaStream_t s);
 
-// The caches of a batch's long sequences (more than rows_from query rows) in BF16, one
+// The caches of a batch's long sequences (more than rows_from query rows) in FP16, one
 // after the other in the batch's order: keys, then values, head by head, of
 // widened_tokens tokens each.
 inline uint64_t widened_sequences(const splitzip_paged_attention_args& a, uint32_t rows_from) {

@@ -61,15 +61,15 @@ bool plan(const splitzip_paged_attention_args& a, Plans& p) {
     p.few = most <= kFewRows || a.batch > 1;
     p.upto = p.few ? kFewRows : 0;
     // Each pair of such tiles widens the slots that it reads.  With more than four pairs to
-    // a sequence and head, widening its cache to BF16 ahead of them costs less; E5M2's bytes
+    // a sequence and head, widening its cache to FP16 ahead of them costs less; E5M2's bytes
     // are widened by a permute alone, in half the time, and at head_dim 128 the products
     // cover that up to eight pairs.  8 heads, 2 sequences of 16k, widened ahead and not, us:
     //   rows           512         1024        1536        2048        4096
-    //   INT8  128    96   77    139  130    213  218    219  230
-    //   INT8   64    68   59    101  102    154  170    162  184    293  353
-    //   E2M1  128    93   73    135  124    208  210    215  222
-    //   E5M2   64    67   55    100   94    153  157    161  168    291  323
-    //   E5M2  128    94   70    137  119    210  203    217  210    392  406
+    //   INT8  128    98   77    141  130    185  179    219  230
+    //   INT8   64    69   59    102  101    131  139    163  182    293  350
+    //   E2M1  128    94   75    136  129    181  181    215  231
+    //   E5M2   64    68   55    101   94    131  129    162  168    292  323
+    //   E5M2  128    97   71    139  119    184  167    219  210    392  405
     p.from = a.batch > 1 ? many_rows : 0;
     p.many = a.pool.format != SPLITZIP_FORMAT_BF16 && most > many_rows && widened_bytes(a, p.from) <= kMostWidened;
     p.some = most > kFewRows && !(p.many && a.batch == 1);

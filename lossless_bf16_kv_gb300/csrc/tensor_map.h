@@ -51,7 +51,8 @@ inline bool make_map(CUtensorMap& map, const splitzip_view& v, uint32_t elem, ui
 // (value or byte, slot, head, page); rows of bytes are swizzled by their length.
 inline bool page_map(CUtensorMap& map, const splitzip_pool& pool, const splitzip_page_rows& rows, uint32_t box) {
     uint32_t one;
-    const uint32_t elem = pool.format == SPLITZIP_FORMAT_BF16 ? 2 : 1, dim = pool.format == SPLITZIP_FORMAT_E2M1 ? pool.head_dim / 2 : pool.head_dim;
+    const bool bytes = pool.format >= SPLITZIP_FORMAT_E5M2 && pool.format <= SPLITZIP_FORMAT_E2M1;  // else 16 bits, of which a copy takes no notice
+    const uint32_t elem = bytes ? 1 : 2, dim = pool.format == SPLITZIP_FORMAT_E2M1 ? pool.head_dim / 2 : pool.head_dim;
     return make_map(map, {rows.data, rows.stride_p, rows.stride_t, rows.stride_h}, elem, dim, pool.kv_heads, pool.page_tokens, pool.pages, 1, box,
                     false, &one, true);
 }
