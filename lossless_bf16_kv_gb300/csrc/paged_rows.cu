@@ -33,6 +33,7 @@
 
 #include "attention_rows.cuh"
 #include "pages.cuh"
+#include "ring_turns.h"
 #include "tcgen.cuh"
 #include "tensor_map.h"
 
@@ -162,7 +163,7 @@ struct PagedRowsShared {
     PagedPart part;
     uint64_t full[kStages], empty[kStages];
     WaitLimit wait;
-    uint32_t issued;  // tiles whose copies have been issued
+    RingTurns<kStages> turns;  // tiles whose copies have been issued
     float scale[kTileRows];
     RowsShared<kTileRows> join;
 };
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB))
         const uint8_t* kexps = pool.k.exponents + h * pool.k.exp_stride_h;
         const uint8_t* vexps = pool.v.exponents + h * pool.v.exp_stride_h;
         if (lane == 0) {
-            sh.issued = n + 1;
+            sh.turns.put(n);
             mbar_arrive_expect_tx(full, 2 * S::kTile + (bulk ? 2 * S::kExps : 0));
         }
         __syncwarp();
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB))
                 mbar_init(&sh.full[i], arrivals);
                 mbar_init(&sh.empty[i], kWarpsRows);
             }
-            sh.wait.given_up = sh.issued = 0;
+            sh.wait.given_up = 0;
+            sh.turns.clear();
             sh.wait.limit = p.wait_limit;
             fence_mbar_init();
             fence_async_proxy();
@@ -708,8 +710,8 @@ __global__ void __launch_bounds__(32 * kWarpsRows, ctas_per_sm(kFmt, D, 8 * NB))
         }
     __syncthreads();  // every warp is done with the ring
     if (*const_cast<volatile uint32_t*>(&sh.wait.given_up)) {  // nothing may land after this
-        for (uint32_t n = sh.issued > S::kStages ? sh.issued - S::kStages : 0; n < sh.issued; n++)
-            mbar_wait_bounded<true>(&sh.full[n % S::kStages], (n / S::kStages) & 1, wait);
+        for (uint32_t i = 0; i < S::kStages; i++)
+            if (sh.turns.used(i)) mbar_wait_bounded<true>(&sh.full[i], sh.turns.parity(i), wait);
         __syncthreads();
     }
     float* os = reinterpret_cast<float*>(smem);
