@@ -90,7 +90,8 @@ def library() -> ctypes.CDLL:
 class Pages:
     """A pool of pages: k, v [pages, page_tokens, kv_heads, row] of torch.bfloat16, torch.float8_e5m2, torch.int8
     (row = head_dim) or torch.uint8 (two E2M1 codes to a byte, row = head_dim / 2); k_exp, v_exp uint8
-    [pages, page_tokens, kv_heads, 4] for the last two."""
+    [pages, page_tokens, kv_heads, 4] for the last two.  The handle keeps views of them, and addresses: a call whose
+    pool's memory has been resized since is refused."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor | None = None,
                  v_exp: torch.Tensor | None = None):
@@ -116,14 +117,30 @@ class Pages:
         for t in (v, k_exp, v_exp):
             if t is not None and t.device != k.device:
                 _bad("a pool lies on one device")
-        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        # Views of its own, which a caller's k.resize_() or k.set_() does not change.
+        self._tensors = tuple(None if t is None else t.detach() for t in (k, v, k_exp, v_exp))
+        self._now = tuple(t.data_ptr for t in self._tensors if t is not None)     # where they are, asked with each call
+        self._then = tuple(f() for f in self._now)
         self.format, self.pages, self.page_tokens, self.kv_heads = fmt, *shape[:3]
         self.head_dim = 2 * shape[3] if fmt == E2M1 else shape[3]
         self.device, self.index = k.device, k.get_device()
         rows = []
         for t, e in ((k, k_exp), (v, v_exp)):
             rows += [t.data_ptr(), *t.stride()[:3], *((0, 0, 0, 0) if e is None else (e.data_ptr(), *e.stride()[:3]))]
-        self.packed = _POOL.pack(*rows, *shape[:3], self.head_dim, fmt)
+        self._packed = _POOL.pack(*rows, *shape[:3], self.head_dim, fmt)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_exp = property(lambda self: self._tensors[2])
+    v_exp = property(lambda self: self._tensors[3])
+
+    @property
+    def packed(self) -> bytes:
+        """The pool as the library takes it."""
+        now, then = self._now, self._then
+        if now[0]() != then[0] or now[1]() != then[1] or (len(now) > 2 and (now[2]() != then[2] or now[3]() != then[3])):
+            _bad("the pool's memory has moved since its handle was made")
+        return self._packed
 
 
 def alloc_pages(pages: int, page_tokens: int, kv_heads: int, head_dim: int, fmt: str = "bf16", device="cuda") -> Pages:

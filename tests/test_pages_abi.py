@@ -232,3 +232,43 @@ def test_tensors_of_another_device_are_refused(lib, monkeypatch):
             with pytest.raises(sz.SplitZipError):
                 fn(pages=p, **{**args, name: args[name].as_subclass(There)}, **more)
         assert len(calls) == 1, fn.__name__
+
+
+def test_a_pool_whose_memory_has_moved_is_refused(lib, monkeypatch):
+    """A handle holds addresses: of tensors resized since, memory that is no longer theirs."""
+    def zeros(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Here)
+    made = []
+    monkeypatch.setattr(pg, "_current_device", lambda: 0)
+    monkeypatch.setattr(pg, "_stream_of", lambda s: 0)
+    for name in ("_fn_store", "_fn_load", "_fn_attention"):
+        monkeypatch.setattr(pg, name, lambda *a: made.append(a) or 0)
+    bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    new, table, ints = zeros(bf16, 5, 2, 64), zeros(i32, 3, 2), zeros(i32, 3)
+
+    def every_call(p):
+        yield lambda: pg.splitzip_pages_store(new, new, zeros(torch.int64, 5), p)
+        yield lambda: pg.splitzip_pages_load(p, table, ints, zeros(bf16, 3, 30, 2, 64), zeros(bf16, 3, 30, 2, 64))
+        yield lambda: pg.splitzip_paged_attention(zeros(bf16, 5, 4, 64), p, table, zeros(i32, 4), ints, zeros(bf16, 5, 4, 64),
+                                                  zeros(u8, 1 << 16), 3)
+
+    def fresh():
+        return {"k": zeros(torch.int8, 4, 16, 2, 64), "v": zeros(torch.int8, 4, 16, 2, 64), "k_exp": zeros(u8, 4, 16, 2, 4),
+                "v_exp": zeros(u8, 4, 16, 2, 4)}
+    for name in ("k", "v", "k_exp", "v_exp"):
+        rows = fresh()
+        p = pg.Pages(**rows)
+        with pytest.raises(AttributeError):
+            setattr(p, name, rows[name].clone())
+        # What changes the caller's tensor alone leaves the pool as it is.
+        rows[name].transpose_(0, 1)
+        made.clear()
+        for call in every_call(p):
+            call()
+        assert len(made) == 3 and getattr(p, name).shape[:3] == (4, 16, 2)
+        rows[name].untyped_storage().resize_(1 << 20)
+        for call in every_call(p):
+            with pytest.raises(sz.SplitZipError) as e:
+                call()
+            assert e.value.status == INV
+        assert len(made) == 3
