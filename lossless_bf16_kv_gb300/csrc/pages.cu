@@ -318,14 +318,24 @@ __global__ void __launch_bounds__(kThreadsPages) widen_kernel(const __grid_const
     __syncthreads();
     if (found >= (int32_t)a.batch) return;
     const uint32_t lane = threadIdx.x % kLanes, t = part.first + threadIdx.x / kLanes * kRows, n = (uint32_t)len;
-    if (t >= n) return;
     // What no query sees need not be there, and its page may have been given away.
     const Mask mask(len, count, a.window, a.sinks);
-    if ((int64_t)t + kRows <= (int64_t)mask.first - (int64_t)mask.window + 1 && (int32_t)t >= mask.sinks) return;
+    const auto seen = [&](uint32_t s, uint32_t run) {
+        return s < n && ((int64_t)s + run > (int64_t)mask.first - (int64_t)mask.window + 1 || s < (uint32_t)mask.sinks);
+    };
+    if (!seen(t & ~127u, 128)) return;  // a tile of the products
     uint8_t* to = p.to + 2 * ((((uint64_t)part.b * 2 + part.v) * a.pool.kv_heads + part.h) * p.tokens * D + 8 * lane);
-    const uint32_t page = (uint32_t)a.table[(uint64_t)found * a.table_width + (t >> p.page_shift)];
-    load_rows<D, kFmt, kF16>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane,
-                              [&](uint32_t row, uint4 x) { *reinterpret_cast<uint4*>(to + 2 * (uint64_t)row * D) = x; });
+    const auto put = [&](uint32_t row, uint4 x) { *reinterpret_cast<uint4*>(to + 2 * (uint64_t)row * D) = x; };
+    const bool here = seen(t, kRows);
+    if (here) {
+        const uint32_t page = (uint32_t)a.table[(uint64_t)found * a.table_width + (t >> p.page_shift)];
+        load_rows<D, kFmt, kF16>(a.pool, part.v ? a.pool.v : a.pool.k, page, part.h, t, n, p.bulk_exps, lane, put);
+    }
+    // The rest of a tile is zeros and not what the workspace held: infinities and NaN among
+    // that would be kept out of the products one by one.
+#pragma unroll
+    for (uint32_t r = 0; r < kRows; r++)
+        if (!here || t + r >= n) put(t + r, make_uint4(0, 0, 0, 0));
 }
 
 inline uint32_t log2_of(uint32_t x) {
@@ -380,13 +390,13 @@ static cudaError_t widen(const WidenParams& p, cudaStream_t s) {
 cudaError_t launch_paged_widen(const splitzip_paged_attention_args& a, uint32_t rows_from, void* widened, cudaStream_t s) {
     const uint32_t tokens = a.pool.head_dim == 64 ? kTokens<64> : kTokens<128>;
     WidenParams p{a};
-    p.token_ctas = (a.kv_tokens + tokens - 1) / tokens;
     p.page_shift = log2_of(a.pool.page_tokens);
     p.bulk_exps = bulk_exponents(a.pool);
     p.group = a.q_heads / a.pool.kv_heads;
     p.rows_from = rows_from;
     p.sequences = (uint32_t)widened_sequences(a, rows_from);
     p.tokens = (uint32_t)widened_tokens(a);
+    p.token_ctas = p.tokens / tokens;  // which divides 128
     p.to = static_cast<uint8_t*>(widened);
     return a.pool.head_dim == 64 ? widen<64>(p, s) : widen<128>(p, s);
 }

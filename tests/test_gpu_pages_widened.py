@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from lossless_bf16_kv_gb300 import pages as pg
 from tests import pages_ref, serving_ref
 from tests.gpu_helpers import ensure_library
 from tests.test_gpu_pages import DEV, attend, batch_of, close, ints
@@ -45,3 +46,45 @@ def test_weights_keep_eleven_bits(counts, dim, fmt):
         close(out[i:j], o[0], tol, "out")
         close(lse[:, i:j], l[0], ltol[0], "lse")
     assert near > 1000
+
+
+def widened_caches(ws, kv_tokens, p, fmt, batch, rows):
+    """[sequences, k and v, heads, tokens, dim] in FP16, which lie at the workspace's end: of as many sequences as `rows`
+    query rows may be widened for (from 1025 on, or 2049)."""
+    border = 2048 if fmt == "e5m2" and p.head_dim == 128 else 1024
+    sequences = 1 if batch == 1 else min(batch, rows // (border + 1))
+    shape = (sequences, 2, p.kv_heads, -(-kv_tokens // 128) * 128, p.head_dim)
+    count = torch.Size(shape).numel()
+    return ws[ws.numel() - 2 * count:].view(torch.float16).view(shape)
+
+
+@pytest.mark.parametrize("fmt", WIDENED)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3), (300, 200)])
+@pytest.mark.parametrize("lens", [[777], [1290, 5, 601, 700], [1281, 610, 640, 0]], ids=["one", "three", "ends"])
+def test_widened_caches_hold_nothing_of_the_workspace(lens, window, sinks, dim, fmt):
+    """Where queries look at tiles of 128 slots, those are the pool's rows and zeros, whatever lay there before: NaN of
+    another call would be kept out of the products value by value."""
+    counts = [600 if n > 600 else 0 for n in lens]
+    q, p, table, start, lens = batch_of(counts, lens, 8, 2, dim, 16, fmt, seed=dim)
+    kv_tokens = table.shape[1] * 16
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 600, None, window, sinks)
+    wide = widened_caches(ws, kv_tokens, p, fmt, len(counts), 4 * len(q))
+    wide.fill_(float("nan"))
+    out, lse = attend(q, p, table, start, lens, most=600, window=window, sinks=sinks, ws=ws)
+    for rows, o, l, tol, ltol in pages_ref.attention(q, p, table, start, lens, kv_tokens, window, sinks, dim ** -0.5):
+        close(out[rows], o, tol, "out")
+        close(lse[:, rows], l, ltol, "lse")
+    for rank, b in enumerate(b for b, n in enumerate(counts) if n):
+        n = lens[b].item()
+        t = torch.arange(wide.shape[3], device=DEV)
+        first = n - counts[b] - window + 1 if window else 0                  # of the first query's window
+        looked_at = (t // 128 * 128 < n) & ((t // 128 * 128 + 128 > first) | (t // 128 * 128 < sinks))
+        seen = (t < n) & ((t >= first) | (t < sinks))
+        for i, x in enumerate("kv"):
+            rows = pages_ref.sequence(p, table[b], n, x)
+            got = wide[rank, i].transpose(0, 1).double()
+            assert torch.equal(got[:n][seen[:n]], rows[seen[:n]])
+            others = got[looked_at & ~seen]
+            assert not others.isnan().any()
+            assert not got[looked_at & (t >= n)].any()
