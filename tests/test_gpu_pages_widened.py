@@ -1,8 +1,12 @@
 """Attention of so many new tokens that quantised and E5M2 caches are widened ahead of the products."""
+import ctypes
+
 import pytest
 import torch
 
 from lossless_bf16_kv_gb300 import pages as pg
+from lossless_bf16_kv_gb300 import serving
+from lossless_bf16_kv_gb300 import splitzip as sz
 from tests import pages_ref, serving_ref
 from tests.gpu_helpers import ensure_library
 from tests.test_gpu_pages import DEV, attend, batch_of, close, ints
@@ -88,3 +92,64 @@ def test_widened_caches_hold_nothing_of_the_workspace(lens, window, sinks, dim, 
             others = got[looked_at & ~seen]
             assert not others.isnan().any()
             assert not got[looked_at & (t >= n)].any()
+
+
+#: new tokens of three sequences, whose row tiles (eight heads of four query heads) are waves of 152 and some more that
+#: are cut: of the widened sequences, of the others, of both, which run at the same time
+CUT = [[600, 600, 600], [600, 250, 250], [320, 256, 250], [600, 200, 1], [250, 250, 250], [0, 600, 30]]
+
+
+@pytest.mark.parametrize("fmt", WIDENED)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pieces_of_widened_and_other_row_tiles_at_once(dim, fmt):
+    """Both tile launches of a call cut their last waves, each with counters and partial results of its own."""
+    q, p, table, _, lens = batch_of([600] * 3, [8000, 7900, 7000], 32, 8, dim, 64, fmt, seed=dim)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 600)
+    sequences = min(3, 4 * len(q) // (2049 if fmt == "e5m2" and dim == 128 else 1025))
+    pieces = 202 * (dim // 4 + 1) * 256 * 16                                 # bytes, of a launch that is cut
+    rest = ws.numel() - sequences * 8064 * 8 * dim * 4 - 2 * pieces
+    assert 0 < rest < pieces, "partial results of two launches"
+    scale = dim ** -0.5
+    for counts in CUT:
+        start = ints([0, *torch.tensor(counts).cumsum(0).tolist()])
+        out, lse = attend(q, p, table, start, lens, most=600, ws=ws)
+        for rows, o, l, tol, ltol in pages_ref.attention(q, p, table, start, lens, table.shape[1] * 64, 0, 0, scale):
+            close(out[rows], o, tol, "out")
+            close(lse[:, rows], l, ltol, "lse")
+        assert bool((out[sum(counts):] == 7.0).all()) and bool((lse[:, sum(counts):] == 7.0).all())
+        for _ in range(3):
+            again = attend(q, p, table, start, lens, most=600, ws=ws)
+            assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("fmt", WIDENED)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_piece_of_a_widened_row_tile_gives_up(dim, fmt):
+    """240 row tiles of widened sequences, the 88 behind a wave of 152 cut: a copy that is left out of a piece makes the
+    row tile's rows NaN, whichever piece joins them, and leaves the workspace fit for the next call."""
+    q, p, table, start, lens = batch_of([600] * 3, [8000, 7900, 7000], 32, 8, dim, 64, fmt, seed=dim + 1)
+    good, good_lse = attend(q, p, table, start, lens)
+    ws = pg.alloc_paged_attention_workspace(q, p, table, 600)
+    out, lse = torch.zeros_like(q), torch.zeros((32, q.shape[0]), device=DEV)
+    a = pg.PagedAttentionArgs((q.data_ptr(), 0, *q.stride()[:2]), (out.data_ptr(), 0, *out.stride()[:2]),
+                              pg.Pool.from_buffer_copy(p.packed), lse.data_ptr(), table.data_ptr(), start.data_ptr(), lens.data_ptr(),
+                              3, q.shape[0], 600, table.shape[1] * 64, table.shape[1], 32, 0, 0, dim ** -0.5)
+
+    def call(cta, tile):
+        torch.cuda.synchronize()
+        o = serving.WaitTestOpts(30, cta, tile)
+        assert pg.library().splitzip_paged_attention_test(ctypes.byref(a), ws.data_ptr(), ws.numel(), None, ctypes.byref(o)) == sz.OK
+        return serving.splitzip_attention_status(ws)
+
+    for cta in (152, 170, 241, 300):
+        out.zero_()
+        lse.zero_()
+        assert call(cta, 1) == sz.ERR_TIMEOUT
+        lost = torch.isnan(lse)
+        assert 0 < int(lost.sum()) <= 256, "rows of one row tile"
+        heads = lost.any(1).nonzero().flatten() // 4
+        assert len(heads.unique()) == 1, "rows of one key/value head"
+        assert torch.equal(torch.isnan(out), lost.T[..., None].expand_as(out))
+        assert torch.equal(lse[~lost], good_lse[~lost]) and torch.equal(out[~lost.T], good[~lost.T])
+    assert call(0xFFFFFFFF, 0xFFFFFFFF) == sz.OK
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
