@@ -52,13 +52,14 @@ bool plan(const splitzip_paged_attention_args& a, Plans& p) {
     constexpr uint32_t kFewRows = 16;
     constexpr uint64_t kMostWidened = 4ull << 30;
     const uint32_t many_rows = a.pool.format == SPLITZIP_FORMAT_E5M2 && a.pool.head_dim == 128 ? 2048 : 1024;
-    const uint64_t most = (uint64_t)a.max_q_tokens * (a.q_heads / a.pool.kv_heads);
+    const uint32_t group = a.q_heads / a.pool.kv_heads;
+    const uint64_t most = (uint64_t)a.max_q_tokens * group;
     // Tiles of 128 query rows on the tensor cores from 17 rows on: where the other kernel
     // would read each key a third time (8 heads of 128, 20 rows of each of 16 sequences of
     // 16k: BF16 159 us, 248 there, E5M2 172 and 190, INT8 202 and 300, E2M1 190 and 273; of
     // 2 of 8k 25 to 30 in both).  One sequence that may have as many goes to them whatever
-    // it has.
-    p.few = most <= kFewRows || a.batch > 1;
+    // it has, and so does a batch whose single tokens have as many.
+    p.few = most <= kFewRows || (a.batch > 1 && group <= kFewRows);
     p.upto = p.few ? kFewRows : 0;
     // Each pair of such tiles widens the slots that it reads.  With more than four pairs to
     // a sequence and head, widening its cache to FP16 ahead of them costs less; E5M2's bytes

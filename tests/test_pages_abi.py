@@ -272,3 +272,14 @@ def test_a_pool_whose_memory_has_moved_is_refused(lib, monkeypatch):
                 call()
             assert e.value.status == INV
         assert len(made) == 3
+
+
+@pytest.mark.parametrize("heads,few", [(8, True), (16 * 8, True), (17 * 8, False), (64 * 8, False)])
+@pytest.mark.parametrize("tokens", [16, 40])
+def test_no_few_row_kernel_where_a_token_has_too_many_rows(lib, heads, few, tokens):
+    """16 sequences of 16k in 8 bits: where a single token has up to 16 query rows the few-row kernel may have to share
+    their work out, whose partial results take megabytes; where it has more, that kernel has no sequence."""
+    pool = pool_of(pages=1 << 20)
+    a = pg.PagedAttentionArgs(VIEW, VIEW, pool, 0, 0, 0, 0, 16, tokens, 1, 16384, 1024, heads, 0, 0, 1.0)
+    size = lib.splitzip_paged_attention_workspace_bytes(ctypes.byref(a))
+    assert size > 1 << 20 if few else size == 1024
