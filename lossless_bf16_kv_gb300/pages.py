@@ -27,6 +27,7 @@ from .splitzip import SplitZipError  # noqa: F401  (raised by the checks)
 BF16, E5M2, INT8, E2M1 = 0, 1, 2, 3
 _FORMAT = {torch.bfloat16: BF16, torch.float8_e5m2: E5M2, torch.int8: INT8, torch.uint8: E2M1}
 _DTYPE = {"bf16": torch.bfloat16, "e5m2": torch.float8_e5m2, "int8": torch.int8, "e2m1": torch.uint8}
+_MOST_TOKENS = (1 << 31) - 256     # of a sequence that attention takes
 _u32, _i64, _f32, _vp = ctypes.c_uint32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
 
@@ -260,7 +261,7 @@ def alloc_paged_attention_workspace(q: torch.Tensor, pages: Pages, table: torch.
 
 def _kv_tokens(kv_tokens, table, pages):
     width = table.shape[1]
-    return (min(width * pages.page_tokens, _MOST) if kv_tokens is None else min(kv_tokens, _MOST)), width
+    return (min(width * pages.page_tokens, _MOST_TOKENS) if kv_tokens is None else min(kv_tokens, _MOST)), width
 
 
 def splitzip_paged_attention(q: torch.Tensor, pages: Pages, table: torch.Tensor, q_start: torch.Tensor, lens: torch.Tensor,
@@ -270,8 +271,8 @@ def splitzip_paged_attention(q: torch.Tensor, pages: Pages, table: torch.Tensor,
     """out = attention of the new tokens q [tokens, q_heads, head_dim] of a batch, packed, sequence b's being rows
     q_start[b] .. q_start[b + 1] - 1 (int32 [batch + 1]) and the last of its lens[b] (int32 [batch]) tokens, over
     the pages that table (int32 [batch, width]) names; asynchronous.  max_q_tokens: the most new tokens of a
-    sequence; kv_tokens: the longest sequence (None: what the table holds).  lse: float32 [q_heads, tokens] or
-    None.  scale: None for head_dim ** -0.5.  Rows that are no sequence's stay as they were.
+    sequence; kv_tokens: the longest sequence (None: what the table holds, 2^31 - 256 at most).  lse: float32
+    [q_heads, tokens] or None.  scale: None for head_dim ** -0.5.  Rows that are no sequence's stay as they were.
     ``serving.splitzip_attention_status`` reports on the workspace."""
     qs, ts = q.shape, table.shape
     qst, ost = q.stride(), out.stride()
@@ -287,7 +288,7 @@ def splitzip_paged_attention(q: torch.Tensor, pages: Pages, table: torch.Tensor,
     if not ok:
         _check_attention(q, pages, table, q_start, lens, out, workspace, max_q_tokens, kv_tokens, lse, window, sinks)
     if kv_tokens is None:
-        kv_tokens = ts[1] * pages.page_tokens
+        kv_tokens = min(ts[1] * pages.page_tokens, _MOST_TOKENS)
     a = _ATTENTION.pack(q.data_ptr(), 0, qst[0], qst[1], out.data_ptr(), 0, ost[0], ost[1], pages.packed,
                         0 if lse is None else lse.data_ptr(), table.data_ptr(), q_start.data_ptr(), lens.data_ptr(),
                         ts[0], qs[0], max_q_tokens, kv_tokens if kv_tokens < _MOST else _MOST, ts[1], qs[1], window if window < _MOST else _MOST,

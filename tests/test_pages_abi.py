@@ -283,3 +283,24 @@ def test_no_few_row_kernel_where_a_token_has_too_many_rows(lib, heads, few, toke
     a = pg.PagedAttentionArgs(VIEW, VIEW, pool, 0, 0, 0, 0, 16, tokens, 1, 16384, 1024, heads, 0, 0, 1.0)
     size = lib.splitzip_paged_attention_workspace_bytes(ctypes.byref(a))
     assert size > 1 << 20 if few else size == 1024
+
+
+def test_a_table_of_more_slots_than_a_sequence_may_have(lib, monkeypatch):
+    """Without kv_tokens the bound is what the table holds, or the most that a call takes."""
+    def zeros(dtype, *shape):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Here)
+    made = []
+    monkeypatch.setattr(pg, "_current_device", lambda: 0)
+    monkeypatch.setattr(pg, "_stream_of", lambda s: 0)
+    monkeypatch.setattr(pg, "_fn_attention", lambda a, *more: made.append(pg.PagedAttentionArgs.from_buffer_copy(a)) or 0)
+    i32 = torch.int32
+    rows, exps = zeros(torch.int8, 1, 65536, 1, 64), zeros(torch.uint8, 1, 65536, 1, 4)
+    p = pg.Pages(rows, rows, exps, exps)
+    q, ws = zeros(torch.bfloat16, 3, 4, 64), zeros(torch.uint8, 1 << 16)
+    for width, most in ((1, 65536), ((1 << 15) - 1, 65536 * ((1 << 15) - 1)), (1 << 15, (1 << 31) - 256), (1 << 17, (1 << 31) - 256)):
+        table = zeros(i32, 1, width)
+        size = pg.splitzip_paged_attention_workspace_bytes(q, p, table, 3)
+        assert size and size == pg.splitzip_paged_attention_workspace_bytes(q, p, table, 3, most)
+        pg.splitzip_paged_attention(q, p, table, zeros(i32, 2), zeros(i32, 1), q.clone(), ws, 3)
+        assert made[-1].kv_tokens == most
+    assert pg.splitzip_paged_attention_workspace_bytes(q, p, table, 3, (1 << 31) - 255) == 0
