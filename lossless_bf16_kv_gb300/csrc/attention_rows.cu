@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "attention_rows.cuh"
+#include "tcgen.cuh"
 
 namespace splitzip {
 namespace {
@@ -47,6 +48,20 @@ struct RowsShape {
     static constexpr int kSmem = kRing + kQ;
 };
 
+// A CTA's row tile and which of its splits, its sequence, head and rows.
+struct RowsPlace {
+    uint32_t unit, split, b, h, r0, r1;
+    __device__ __forceinline__ RowsPlace(const RowsParams& p, uint32_t block, uint32_t tile_rows) {
+        unit = block / p.splits;
+        split = block - unit * p.splits;
+        const uint32_t bh = unit / p.row_tiles, rt = unit - bh * p.row_tiles;
+        b = bh / p.a.kv_heads;
+        h = bh - b * p.a.kv_heads;
+        r0 = rt * tile_rows;
+        r1 = min(r0 + tile_rows, p.rows);
+    }
+};
+
 template <int D, bool kF8, int MT>
 __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) rows_kernel(const __grid_constant__ RowsParams p) {
     using S = RowsShape<D, kF8, MT>;
@@ -60,12 +75,9 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
     __shared__ RowsShared<S::kTileRows> sh;
     const splitzip_attention_args& a = p.a;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t unit = blockIdx.x / p.splits;
-    const uint32_t split = blockIdx.x - unit * p.splits;
-    const uint32_t bh = unit / p.row_tiles, rt = unit - bh * p.row_tiles;
-    const uint32_t b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+    const RowsPlace place(p, blockIdx.x, S::kTileRows);
+    const uint32_t split = place.split, b = place.b, h = place.h, r0 = place.r0, r1 = place.r1;
     const Mask mask(a, b);
-    const uint32_t r0 = rt * S::kTileRows, r1 = min(r0 + S::kTileRows, p.rows);
     const int32_t p0 = mask.first + (int32_t)(r0 / p.group), p1 = mask.first + (int32_t)((r1 - 1) / p.group);
     const SlotTiles tiles(mask, p0, p1, S::kSlots);
     const uint32_t j0 = (uint32_t)((uint64_t)tiles.count * split / p.splits);
@@ -356,26 +368,30 @@ __global__ void __launch_bounds__(32 * kWarpsRows, MT == 1 ? kCtasPerSm : 1) row
                 os[(warp * S::kTileRows + 16 * i + 8 * (x >> 1) + lane / 4) * D + column(n, x)] = o[i][n][x];
     __syncthreads();
 
-    const uint32_t nrows = r1 - r0;
+    // The place is found again by the kernel that has no registers to keep it in: kept, its loop
+    // spills (16 tokens over 16k caches 79.0 us, found again 75.9).  The divisions cost the others'
+    // shortest calls 0.1 of 6.8 us, so they keep it.
+    constexpr bool kAgain = kF8 && D == 128 && MT == 1;
+    const RowsPlace end = kAgain ? RowsPlace(p, opaque(blockIdx.x), S::kTileRows) : place;
     auto store = [&](uint32_t r, uint32_t c, float4 v, float mm, float ll) {
-        const uint32_t row = r0 + r, t = row / p.group, g = row - t * p.group;
-        const uint32_t hq = h * p.group + g;
+        const uint32_t row = end.r0 + r, t = row / p.group, g = row - t * p.group;
+        const uint32_t hq = end.h * p.group + g;
         const bool none = ll == 0.0f;  // nothing seen, or scores of -infinity alone
         const float inv = 1.0f / ll;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.stride_b + (int64_t)t * a.out.stride_t +
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + end.b * a.out.stride_b + (int64_t)t * a.out.stride_t +
                              hq * a.out.stride_h;
         *reinterpret_cast<uint2*>(out + c) =
             none ? make_uint2(0, 0) : make_uint2(pack2<false>(v.x * inv, v.y * inv), pack2<false>(v.z * inv, v.w * inv));
         if (c == 0 && a.lse)
-            a.lse[((uint64_t)b * a.q_heads + hq) * a.q_tokens + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            a.lse[((uint64_t)end.b * a.q_heads + hq) * a.q_tokens + t] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     };
     const auto is_last = [&] {
-        const bool last = atomicAdd(p.counters + unit, 1u) == p.splits - 1;
-        if (last) p.counters[unit] = 0;  // ready for the next call
+        const bool last = atomicAdd(p.counters + end.unit, 1u) == p.splits - 1;
+        if (last) p.counters[end.unit] = 0;  // ready for the next call
         return last;
     };
-    float* all = p.partials + (uint64_t)unit * (p.splits / p.cluster) * kPartFloats<D, S::kTileRows>;
-    join_rows<D, S::kTileRows>(os, sh, split, p.splits, p.cluster, nrows, all, is_last, store);
+    float* all = p.partials + (uint64_t)end.unit * (p.splits / p.cluster) * kPartFloats<D, S::kTileRows>;
+    join_rows<D, S::kTileRows>(os, sh, end.split, p.splits, p.cluster, end.r1 - end.r0, all, is_last, store);
 }
 
 template <int D, bool kF8, int MT>
