@@ -149,8 +149,18 @@ typedef struct splitzip_paged_attention_args {
 
 /* Bytes of workspace for these sizes (pointers, strides and scale are not looked
  * at), as splitzip_attention_workspace_bytes: zero-filled once, shared by calls
- * that are ordered on one stream, also with those of splitzip_attention.  0 for
- * sizes that are refused. */
+ * that are ordered on one stream and need no more than it holds, also with those
+ * of splitzip_attention.  Smaller sizes may need more: fewer sequences are split
+ * into more parts.  0 for sizes that are refused.
+ *
+ * Over pages other than BF16 a sequence of more than 1024 query rows (new tokens
+ * times the heads of a group; 2048 in E5M2 at head_dim 128) has its cache widened
+ * to 16 bits in the workspace first, so there is room for as many sequences as may
+ * have more: each 4 bytes a value of kv_tokens (rounded up to 128) * kv_heads *
+ * head_dim.  If that is above 4 GiB none is, and the pages are widened again for
+ * every 256 rows, which takes longer (2048 tokens of 32 heads over 8k tokens of 8
+ * heads of 128 in 8 bits: 215 us in place of 188).  It goes by max_q_tokens for a
+ * batch of one: a token under a bound of 2048 has its whole cache widened. */
 size_t splitzip_paged_attention_workspace_bytes(const splitzip_paged_attention_args *args);
 
 /* splitzip_attention_status reports on the workspace. */

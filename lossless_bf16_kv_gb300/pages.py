@@ -252,7 +252,7 @@ def splitzip_paged_attention_workspace_bytes(q: torch.Tensor, pages: Pages, tabl
 
 def alloc_paged_attention_workspace(q: torch.Tensor, pages: Pages, table: torch.Tensor, max_q_tokens: int,
                                     kv_tokens: int | None = None, window: int = 0, sinks: int = 0) -> torch.Tensor:
-    """Zero-filled workspace for these sizes (zeroed once; reusable after)."""
+    """Zero-filled workspace for these sizes (zeroed once; reusable after).  Others, smaller ones too, may need more."""
     nbytes = splitzip_paged_attention_workspace_bytes(q, pages, table, max_q_tokens, kv_tokens, window, sinks)
     if not nbytes:
         _bad("no attention for these sizes")
