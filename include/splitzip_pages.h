@@ -125,11 +125,12 @@ splitzip_status splitzip_pages_load(const splitzip_pages_load_args *args, splitz
  *            make ranges overlap, out and lse are unspecified
  *   lens     int32[batch], with the new tokens counted
  * Scores, the softmax statistics and sums are held in 32 bits.  A weight enters its
- * product with the values in their 16 bits: BF16 over BF16 pages (off by up to 2^-8
- * of itself), FP16 over all others (2^-11).  Over those a query too is FP16, of its
- * row scaled by a power of two: values down to 2^-17 of the row's largest keep all
- * their bits.  A query that sees nothing, or scores of -infinity alone, gets out = 0
- * and lse = -inf.  Tokens
+ * product with the values in 16 bits, and so counts for out, but not for lse: BF16
+ * over BF16 pages (off by up to 2^-8 of itself), FP16 over all others (2^-11, below
+ * 2^-22 of the row's largest by up to 2^-33 of that).  Over those a query too is
+ * FP16, of its row scaled by a power of two: values down to 2^-17 of the row's
+ * largest keep all their bits.  A query that sees nothing, or scores of -infinity
+ * alone, gets out = 0 and lse = -inf.  Tokens
  * that a query does not see contribute nothing to it, whatever their slots hold;
  * where it sees a quantised token whose exponent bytes are not ones that the store
  * writes, its out and lse are unspecified.

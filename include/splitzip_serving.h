@@ -134,7 +134,11 @@ size_t splitzip_attention_workspace_bytes(const splitzip_attention_args *args);
 /* out = softmax(scale q k^T over the visible slots) v, and lse = log(sum
  * exp(scale q k^T)) (natural logarithm).  A query that sees nothing, or scores
  * of -infinity alone, gets out = 0 and lse = -inf, and gives no weight below.
- * Scores, the softmax statistics and sums are held in 32 bits.  workspace:
+ * Scores, the softmax statistics and sums are held in 32 bits.  A weight counts
+ * for out in 16 bits, as its product with the values takes it: BF16 over BF16
+ * caches (off by up to 2^-8 of itself), FP16 over E5M2 (2^-11, below 2^-22 of the
+ * row's largest by up to 2^-33 of that), where queries too are FP16, of their row
+ * scaled by a power of two.  workspace:
  * 16-byte aligned, workspace_bytes of it. */
 splitzip_status splitzip_attention(const splitzip_attention_args *args, void *workspace,
                                    size_t workspace_bytes, splitzip_stream_t s);
