@@ -153,3 +153,25 @@ def test_a_piece_of_a_widened_row_tile_gives_up(dim, fmt):
         assert torch.equal(lse[~lost], good_lse[~lost]) and torch.equal(out[~lost.T], good[~lost.T])
     assert call(0xFFFFFFFF, 0xFFFFFFFF) == sz.OK
     assert torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("fmt", WIDENED)
+@pytest.mark.parametrize("batch,count,tokens", [(9, 600, 4000), (5, 800, 700), (12, 560, 8000)])
+def test_ranges_that_overlap_under_widened_caches(batch, count, tokens, fmt):
+    """Starts that go back bring more long sequences than the workspace has room for widened: those that it has none for
+    are NaN or left out, nothing is written behind the buffers, and ranges in order are right again after it."""
+    q, p, table, _, lens = batch_of([count] + [0] * (batch - 1), [tokens] * batch, 8, 2, 64, 16, fmt, seed=batch)
+    start = ints([0, count] * (batch // 2 + 1))[: batch + 1]
+    size = pg.splitzip_paged_attention_workspace_bytes(q, p, table, count)
+    room = torch.zeros(size + (64 << 20), dtype=torch.uint8, device=DEV)
+    room[size:] = 0x5A
+    out, lse = torch.zeros((count + 1, 8, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((9, count), device=DEV)
+    for _ in range(2):
+        pg.splitzip_paged_attention(q, p, table, start, lens, out[:count], room[:size], count, lse=lse[:8])
+        assert serving.splitzip_attention_status(room[:size]) == sz.OK
+    assert bool((room[size:] == 0x5A).all()) and not out[count].any() and not lse[8].any()
+    start[2:] = count
+    pg.splitzip_paged_attention(q, p, table, start, lens, out[:count], room[:size], count, lse=lse[:8])
+    for rows, o, l, tol, ltol in pages_ref.attention(q, p, table, start, lens, table.shape[1] * 16, 0, 0, 0.125):
+        close(out[rows], o, tol, "out")
+        close(lse[:8][:, rows], l, ltol, "lse")
